@@ -11,4 +11,7 @@ def __getattr__(name):
     if name in ("EagleTree", "row_topk", "expand", "build_tree", "verify_walk", "linear_bf16"):
         from . import engine
         return getattr(engine, name)
+    if name == "KV4Cache":
+        from . import kv4
+        return kv4.KV4Cache
     raise AttributeError(name)

@@ -53,6 +53,11 @@ class DecoderLayerWeights(ctypes.Structure):
                [(n, c_void_p) for n in ("w_qkv", "w_o", "w_norm", "w_gu", "w_d")]
 
 
+class KV4CacheStruct(ctypes.Structure):
+    _fields_ = [(n, c_int32) for n in ("kv_heads", "head_dim", "page_size", "num_pages", "max_pages")] + \
+               [(n, c_void_p) for n in ("pages", "table", "lengths")]
+
+
 _SIGS = {
     "eagle_tree_workspace_bytes": (c_size_t, [POINTER(TreeConfig)]),
     "eagle_tree_init": (c_int, [POINTER(TreeConfig), c_void_p, c_size_t, POINTER(c_void_p)]),
@@ -95,6 +100,19 @@ _SIGS = {
     "eagle_decoder_layer_workspace_bytes": (c_size_t, [POINTER(DecoderLayerWeights), c_int32, c_int32]),
     "eagle_decoder_layer": (c_int, [POINTER(DecoderLayerWeights), c_int32, c_int32, c_int32]
                             + [c_void_p] * 9 + [c_size_t, c_void_p]),
+    "eagle_kv4_pages_bytes": (c_size_t, [POINTER(KV4CacheStruct)]),
+    "eagle_kv4_append": (c_int, [POINTER(KV4CacheStruct), c_int32, c_int32, c_int32, c_void_p, c_void_p, c_int64]
+                         + [c_void_p] * 5),
+    "eagle_kv4_read": (c_int, [POINTER(KV4CacheStruct), c_int32, c_int32, c_void_p, c_void_p, c_void_p, c_int,
+                               c_void_p, c_void_p]),
+    "eagle_kv4_attention_workspace_bytes": (c_size_t, [POINTER(KV4CacheStruct), c_int32, c_int32]),
+    "eagle_kv4_attention": (c_int, [POINTER(KV4CacheStruct), c_int32, c_int32, c_int32, c_void_p, c_int64,
+                                    c_void_p, c_void_p, c_int64, c_void_p, c_void_p, c_void_p, c_size_t,
+                                    c_void_p, c_void_p]),
+    "eagle_decoder_layer_kv4_workspace_bytes": (c_size_t, [POINTER(DecoderLayerWeights), POINTER(KV4CacheStruct),
+                                                           c_int32, c_int32]),
+    "eagle_decoder_layer_kv4": (c_int, [POINTER(DecoderLayerWeights), POINTER(KV4CacheStruct), c_int32, c_int32]
+                                + [c_void_p] * 7 + [c_size_t, c_void_p, c_void_p]),
     "eagle_linear_noalloc_scratch_bytes": (c_size_t, []),
     "eagle_linear_bf16_noalloc": (c_int, [c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int32,
                                           c_int32, c_int32, c_void_p, c_int64, c_int32, c_void_p]),

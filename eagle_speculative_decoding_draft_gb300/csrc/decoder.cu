@@ -19,6 +19,7 @@
 #include "../../include/eagle_tree.h"
 #include "common.cuh"
 #include "kernels.cuh"
+#include "kv4.cuh"
 #include "select.cuh"
 
 namespace eagle {
@@ -1213,7 +1214,7 @@ namespace {
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 struct DecoderLayout {
-    size_t qkv, o, y, h1, r, gu, act, counters, partials, part_o, part_ml, total;
+    size_t qkv, o, y, h1, r, gu, act, counters, partials, part_o, part_ml, kv4, total;
 };
 
 constexpr int32_t kAttnMaxSplits = 32;
@@ -1263,7 +1264,9 @@ bool decoder_dims_ok(const eagle_decoder_layer_weights *w) {
     return true;
 }
 
-DecoderLayout decoder_layout(const eagle_decoder_layer_weights *w, int32_t batch, int32_t nodes, int32_t sms) {
+// kv4_bytes: the 4-bit cache's attention works in its own region instead of the key splits'.
+DecoderLayout decoder_layout(const eagle_decoder_layer_weights *w, int32_t batch, int32_t nodes, int32_t sms,
+                             size_t kv4_bytes = 0) {
     const int64_t rows = static_cast<int64_t>(batch) * nodes;
     const int64_t h = w->hidden, nq = static_cast<int64_t>(w->heads) * w->head_dim;
     const int64_t nk = static_cast<int64_t>(w->kv_heads) * w->head_dim, I = w->inter;
@@ -1287,9 +1290,10 @@ DecoderLayout decoder_layout(const eagle_decoder_layer_weights *w, int32_t batch
     L.gu = take(static_cast<size_t>(rows) * 2 * I * 2);
     L.act = take(static_cast<size_t>(rows) * I * 2);
     const AttnPlan ap = attn_plan(w, batch, nodes, sms);
-    const size_t prows = ap.splits_max > 1 ? static_cast<size_t>(ap.splits_max) * batch * w->kv_heads * ap.Mq : 0;
+    const size_t prows = kv4_bytes == 0 && ap.splits_max > 1 ? static_cast<size_t>(ap.splits_max) * batch * w->kv_heads * ap.Mq : 0;
     L.part_o = take(prows * w->head_dim * 4);
     L.part_ml = take(prows * 8);
+    if (kv4_bytes) L.kv4 = take(kv4_bytes);
     L.total = o;
     return L;
 }
@@ -1361,29 +1365,16 @@ cudaError_t prepare_once(int dev) {
     return e;
 }
 
-}  // namespace
-}  // namespace eagle
-
-extern "C" {
-
-size_t eagle_decoder_layer_workspace_bytes(const eagle_decoder_layer_weights *w, int32_t batch, int32_t nodes) {
-    if (!eagle::decoder_dims_ok(w) || batch < 1 || nodes < 1) return 0;
-    const int32_t sms = eagle::sms_now();
-    if (sms < 1) return 0;
-    return eagle::decoder_layout(w, batch, nodes, sms).total;
-}
-
-eagle_status eagle_decoder_layer(const eagle_decoder_layer_weights *w, int32_t batch, int32_t nodes, int32_t prefix,
-                                 const void *d_x, const void *d_k_cache, const void *d_v_cache,
-                                 const int32_t *d_positions, const uint32_t *d_mask, void *d_out, void *d_k_new,
-                                 void *d_v_new, void *d_ws, size_t ws_bytes, eagle_stream_t stream) {
-    using namespace eagle;
-    NvtxRange nvtx_range("eagle_decoder_layer");
+// Both layers: over the bf16 cache (kv4 null) or over a 4-bit one (prefix 0, no cache pointers).
+eagle_status run_layer(const eagle_decoder_layer_weights *w, int32_t batch, int32_t nodes, int32_t prefix,
+                       const void *d_x, const void *d_k_cache, const void *d_v_cache, const int32_t *d_positions,
+                       const uint32_t *d_mask, void *d_out, void *d_k_new, void *d_v_new, void *d_ws, size_t ws_bytes,
+                       eagle_stream_t stream, const Kv4View *kv4, int32_t *d_status) {
     if (!decoder_dims_ok(w) || batch < 0 || nodes < 1 || nodes > kMaxCandidates + 1 || prefix < 0)
         return EAGLE_ERR_INVALID_ARG;
     if (batch == 0) return EAGLE_OK;
-    if (!w->w_qkv || !w->w_o || !w->w_norm || !w->w_gu || !w->w_d || !d_x || !d_positions || !d_mask || !d_out ||
-        !d_ws)
+    if (!w->w_qkv || !w->w_o || !w->w_norm || !w->w_gu || !w->w_d || !d_x || !d_positions || (!d_mask && !kv4) ||
+        !d_out || !d_ws)
         return EAGLE_ERR_INVALID_ARG;
     if (prefix > 0 && (!d_k_cache || !d_v_cache)) return EAGLE_ERR_INVALID_ARG;
     if ((d_k_new == nullptr) != (d_v_new == nullptr)) return EAGLE_ERR_INVALID_ARG;
@@ -1397,7 +1388,9 @@ eagle_status eagle_decoder_layer(const eagle_decoder_layer_weights *w, int32_t b
     if (sms < 1 || cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return EAGLE_ERR_CUDA;
     if (prepare_once(dev) != cudaSuccess) return EAGLE_ERR_CUDA;
     const int32_t rows = batch * nodes;
-    const DecoderLayout L = decoder_layout(w, batch, nodes, sms);
+    const size_t kv4_bytes = kv4 ? kv4_attention_workspace(w->kv_heads, w->head_dim / kKv4Group, w->heads, nodes) : 0;
+    if (kv4 && kv4_bytes == 0) return EAGLE_ERR_CUDA;
+    const DecoderLayout L = decoder_layout(w, batch, nodes, sms, kv4_bytes);
     if (ws_bytes < L.total) return EAGLE_ERR_INVALID_ARG;
     uint8_t *ws = reinterpret_cast<uint8_t *>(d_ws);
     auto at = [&](size_t off) { return ws + off; };
@@ -1431,32 +1424,49 @@ eagle_status eagle_decoder_layer(const eagle_decoder_layer_weights *w, int32_t b
                         d_positions, static_cast<double>(w->rope_theta), reinterpret_cast<__nv_bfloat16 *>(d_k_new),
                         reinterpret_cast<__nv_bfloat16 *>(d_v_new)));
     // tree attention over the cache and the tree
-    const AttnPlan ap = attn_plan(w, batch, nodes, sms);
-    int32_t splits = 1, tps = 1;
-    attn_splits(ap, prefix, nodes, &splits, &tps);
-    AttnArgs aa{batch, nodes, prefix, H, Hk, nqkv, ap.group, ap.Mq, ap.rows_cta, ap.q_tiles, splits, tps,
-                (nodes + 31) / 32, qkv, reinterpret_cast<const __nv_bfloat16 *>(d_k_cache),
-                reinterpret_cast<const __nv_bfloat16 *>(d_v_cache), d_mask, o,
-                reinterpret_cast<float *>(at(L.part_o)), reinterpret_cast<float2 *>(at(L.part_ml))};
-    const dim3 agrid(batch * Hk * ap.q_tiles, splits);
-    // the tensor-core kernel reads whole tiles of cached keys by tensor copies
-    CUtensorMap tk{}, tv{}, tq{};
-    if (ap.tc && prefix > 0 &&
-        (!encode_kv_cache_map(&tk, d_k_cache, batch, prefix, Hk, D) ||
-         !encode_kv_cache_map(&tv, d_v_cache, batch, prefix, Hk, D)))
-        return EAGLE_ERR_CUDA;
-    if (ap.tc && !encode_bf16_rows_map(&tq, qkv, static_cast<uint64_t>(nqkv), static_cast<uint64_t>(rows),
-                                       static_cast<uint64_t>(nqkv), 64, kTcKeys))
-        return EAGLE_ERR_CUDA;
-    switch (D) {
-        case 32: DEC_CUDA(launch_attention<32>(ap, agrid, aa, tk, tv, tq, st)); break;
-        case 64: DEC_CUDA(launch_attention<64>(ap, agrid, aa, tk, tv, tq, st)); break;
-        case 96: DEC_CUDA(launch_attention<96>(ap, agrid, aa, tk, tv, tq, st)); break;
-        default: DEC_CUDA(launch_attention<128>(ap, agrid, aa, tk, tv, tq, st)); break;
+    if (kv4) {
+        Kv4Attention ka{};
+        ka.cache = *kv4;
+        ka.B = batch;
+        ka.n = nodes;
+        ka.H = H;
+        ka.q = qkv;
+        ka.kn = qkv + nq;
+        ka.vn = qkv + nq + nk;
+        ka.ldq = ka.ldkv = nqkv;
+        ka.mask = d_mask;
+        ka.o = o;
+        ka.ws = at(L.kv4);
+        ka.status = d_status;
+        DEC_CUDA(launch_kv4_attention(ka, st));
+    } else {
+        const AttnPlan ap = attn_plan(w, batch, nodes, sms);
+        int32_t splits = 1, tps = 1;
+        attn_splits(ap, prefix, nodes, &splits, &tps);
+        AttnArgs aa{batch, nodes, prefix, H, Hk, nqkv, ap.group, ap.Mq, ap.rows_cta, ap.q_tiles, splits, tps,
+                    (nodes + 31) / 32, qkv, reinterpret_cast<const __nv_bfloat16 *>(d_k_cache),
+                    reinterpret_cast<const __nv_bfloat16 *>(d_v_cache), d_mask, o,
+                    reinterpret_cast<float *>(at(L.part_o)), reinterpret_cast<float2 *>(at(L.part_ml))};
+        const dim3 agrid(batch * Hk * ap.q_tiles, splits);
+        // the tensor-core kernel reads whole tiles of cached keys by tensor copies
+        CUtensorMap tk{}, tv{}, tq{};
+        if (ap.tc && prefix > 0 &&
+            (!encode_kv_cache_map(&tk, d_k_cache, batch, prefix, Hk, D) ||
+             !encode_kv_cache_map(&tv, d_v_cache, batch, prefix, Hk, D)))
+            return EAGLE_ERR_CUDA;
+        if (ap.tc && !encode_bf16_rows_map(&tq, qkv, static_cast<uint64_t>(nqkv), static_cast<uint64_t>(rows),
+                                           static_cast<uint64_t>(nqkv), 64, kTcKeys))
+            return EAGLE_ERR_CUDA;
+        switch (D) {
+            case 32: DEC_CUDA(launch_attention<32>(ap, agrid, aa, tk, tv, tq, st)); break;
+            case 64: DEC_CUDA(launch_attention<64>(ap, agrid, aa, tk, tv, tq, st)); break;
+            case 96: DEC_CUDA(launch_attention<96>(ap, agrid, aa, tk, tv, tq, st)); break;
+            default: DEC_CUDA(launch_attention<128>(ap, agrid, aa, tk, tv, tq, st)); break;
+        }
+        if (splits > 1)
+            DEC_CUDA(launch_pdl(attention_combine_kernel, dim3((batch * Hk * ap.Mq + kCombineRows - 1) / kCombineRows),
+                                dim3(kCombineRows * 32), 0, st, aa, D));
     }
-    if (splits > 1)
-        DEC_CUDA(launch_pdl(attention_combine_kernel, dim3((batch * Hk * ap.Mq + kCombineRows - 1) / kCombineRows),
-                            dim3(kCombineRows * 32), 0, st, aa, D));
     // output projection, residual and post-attention RMSNorm
     DEC_CUDA(gemm_rows(w->w_o, h, nq, o, rows, y, 0, partials, counters, sms, st));
     DEC_CUDA(launch_pdl(add_rmsnorm_kernel, dim3(rows), dim3(256), 0, st, reinterpret_cast<const __nv_bfloat16 *>(d_x),
@@ -1472,6 +1482,54 @@ eagle_status eagle_decoder_layer(const eagle_decoder_layer_weights *w, int32_t b
                         static_cast<const float *>(y), reinterpret_cast<__nv_bfloat16 *>(d_out), hcount));
 #undef DEC_CUDA
     return EAGLE_OK;
+}
+
+}  // namespace
+}  // namespace eagle
+
+extern "C" {
+
+size_t eagle_decoder_layer_workspace_bytes(const eagle_decoder_layer_weights *w, int32_t batch, int32_t nodes) {
+    if (!eagle::decoder_dims_ok(w) || batch < 1 || nodes < 1) return 0;
+    const int32_t sms = eagle::sms_now();
+    if (sms < 1) return 0;
+    return eagle::decoder_layout(w, batch, nodes, sms).total;
+}
+
+eagle_status eagle_decoder_layer(const eagle_decoder_layer_weights *w, int32_t batch, int32_t nodes, int32_t prefix,
+                                 const void *d_x, const void *d_k_cache, const void *d_v_cache,
+                                 const int32_t *d_positions, const uint32_t *d_mask, void *d_out, void *d_k_new,
+                                 void *d_v_new, void *d_ws, size_t ws_bytes, eagle_stream_t stream) {
+    eagle::NvtxRange nvtx_range("eagle_decoder_layer");
+    return eagle::run_layer(w, batch, nodes, prefix, d_x, d_k_cache, d_v_cache, d_positions, d_mask, d_out, d_k_new,
+                            d_v_new, d_ws, ws_bytes, stream, nullptr, nullptr);
+}
+
+size_t eagle_decoder_layer_kv4_workspace_bytes(const eagle_decoder_layer_weights *w, const eagle_kv4_cache *cache,
+                                               int32_t batch, int32_t nodes) {
+    eagle::Kv4View v;
+    if (!eagle::decoder_dims_ok(w) || !eagle::kv4_view(cache, &v) || batch < 1 || nodes < 1 ||
+        nodes > eagle::kMaxCandidates + 1)
+        return 0;
+    if (v.Hk != w->kv_heads || v.G * eagle::kKv4Group != w->head_dim) return 0;
+    const int32_t sms = eagle::sms_now();
+    if (sms < 1) return 0;
+    const size_t kv4 = eagle::kv4_attention_workspace(v.Hk, v.G, w->heads, nodes);
+    return kv4 ? eagle::decoder_layout(w, batch, nodes, sms, kv4).total : 0;
+}
+
+eagle_status eagle_decoder_layer_kv4(const eagle_decoder_layer_weights *w, const eagle_kv4_cache *cache, int32_t batch,
+                                     int32_t nodes, const void *d_x, const int32_t *d_positions,
+                                     const uint32_t *d_mask, void *d_out, void *d_k_new, void *d_v_new, void *d_ws,
+                                     size_t ws_bytes, int32_t *d_status, eagle_stream_t stream) {
+    eagle::NvtxRange nvtx_range("eagle_decoder_layer_kv4");
+    eagle::Kv4View v;
+    if (!eagle::decoder_dims_ok(w) || !eagle::kv4_view(cache, &v)) return EAGLE_ERR_INVALID_ARG;
+    if (v.Hk != w->kv_heads || v.G * eagle::kKv4Group != w->head_dim || w->heads > 65536) return EAGLE_ERR_INVALID_ARG;
+    if (nodes > 0 && static_cast<int64_t>(nodes) * (w->heads / w->kv_heads) > (1 << 24)) return EAGLE_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(d_status) & 3u) return EAGLE_ERR_INVALID_ARG;
+    return eagle::run_layer(w, batch, nodes, 0, d_x, nullptr, nullptr, d_positions, d_mask, d_out, d_k_new, d_v_new,
+                            d_ws, ws_bytes, stream, &v, d_status);
 }
 
 }  // extern "C"

@@ -1,0 +1,1006 @@
+// kv4_attn.cu - attention over the 4-bit key/value cache and the new keys of each request's nodes.
+//
+// For node i of request b and query head h (kv head hk = h / (H / Hk)):
+//     o = sum_j p_j v_j / sum_j p_j,  p_j = exp(q . k_j / sqrt(D) - max)
+// over the lengths[b] cached positions, whose keys and values are m + s c (kv4.cuh), and the new
+// keys that the node sees, which are bf16.  A row that sees nothing gives 0.
+//
+// What bounds it: reading the cache, 2 (D / 2 + D / 8) bytes a token and kv head.  At 6.8 TB/s that
+// is 11 T values a second on 152 SMs x 128 lanes x 1.9 GHz, so a value may cost at most 3.4
+// lane-instructions, the softmax and everything else included: unpacking codes to bf16 and scaling
+// them one by one would take most of that.  Hence the cached tiles are multiplied as codes:
+//   * an fp16 whose bits are a code (0..15) in its lowest bits is the subnormal c 2^-24, exactly, and
+//     with the code four bits higher 16 c 2^-24.  Masking a 32-bit word of eight codes twice before
+//     and twice after a shift by 8 gives four fp16 pairs: 5 instructions for 8 values.  The factor
+//     16 is taken out of the query (a power of two, exact) or of the output rows.
+//   * scores: q . k = sum_g s_g (q . c)_g + sum_g m_g (sum of q over the group).  The MMAs of a group
+//     (32 dims, two k-steps) start from zero and the sum over groups is fp32 with the key's s_g; the
+//     second sum is one more MMA with the m_g of a key against fp16 hi + lo of the query's sums.
+//     Queries are scaled by a power of two to fp16 (bf16 has 8 significand bits: exact but for
+//     elements 2^-19 below the row's largest).
+//   * output: o_d = sum_j (p_j s_gj) c_jd + sum_j p_j m_gj.  For each group p s_g is the B operand
+//     (two fp16 products a key pair), the codes again the A operand; the second sum is one MMA whose
+//     rows are the groups.  p and p s are rounded to fp16 (half a step is 2^-11 relative, against
+//     2^-8 of the bf16 output); sums, the running maximum and p's sum are fp32.
+// Scores are formed transposed (16 keys on the MMA's M side, 8 query rows on N), so few query rows
+// waste no MMA rows, and the accumulators turn into the value product's operand by movmatrix.
+//
+// Work split.  A unit is (request, kv head, tile of query rows); its keys come in tiles of 64: new
+// keys first, then cached ones.  All units' tiles, in order, form one line that the CTAs cut evenly,
+// whatever the requests' lengths; the line is laid out on the device from the lengths, so the host
+// needs none of them.  A unit that more than one CTA works on is merged by a second kernel from
+// partial sums in the workspace: each CTA leaves at most two.
+#include <algorithm>
+#include <mutex>
+
+#include "kernels.cuh"
+#include "kv4.cuh"
+
+namespace eagle {
+namespace {
+
+constexpr int kTile = 64;       // keys of a tile: a chunk of 16 for each of the 4 warps
+constexpr int kWarps = 4;       // warps that multiply
+constexpr int kThreads = kWarps * 32 + 32;  // and one that copies
+constexpr int kStages = 4;
+constexpr int kMinTiles = 2;    // tiles a CTA takes at least
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr uint32_t kFull = 0xffffffffu;
+
+// What each CTA of the attention kernel leaves for the merge: the unit that it continues (begun by
+// an earlier CTA) if it is the first to do so, and the CTAs first..last that share it.
+struct Kv4Share {
+    int32_t b, hk, qt;       // b < 0: nothing to merge here
+    int32_t first, last, first_slot;
+};
+
+struct Kv4Args {
+    Kv4Attention a;
+    int32_t group, Mq, rows, QT, W;
+    float scale2;            // log2(e) / sqrt(D)
+    Kv4Share *share;         // [grid]
+    float2 *part_ml;         // [grid * 2][rows]: running maximum (base 2) and sum
+    float *part_o;           // [grid * 2][rows][D]
+};
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// Transpose of an 8 x 8 matrix of 16-bit elements spread over the warp.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ uint32_t pack_b16(float lo, float hi) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t x, uint32_t y) {
+    const __half2 r = __hmul2(*reinterpret_cast<const __half2 *>(&x), *reinterpret_cast<const __half2 *>(&y));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+__device__ __forceinline__ float low_f16(uint32_t x) { return __half2float(__ushort_as_half(static_cast<uint16_t>(x))); }
+__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// N 32-bit words at p, whose address is a multiple of 4 N bytes (N 1, 2 or 4) or of 4 (N 3).
+template <int N>
+__device__ __forceinline__ void load_words(const uint8_t *p, uint32_t (&w)[N]) {
+    if constexpr (N == 4) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(p);
+        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+    } else if constexpr (N == 2) {
+        const uint2 v = *reinterpret_cast<const uint2 *>(p);
+        w[0] = v.x, w[1] = v.y;
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) w[i] = reinterpret_cast<const uint32_t *>(p)[i];
+    }
+}
+
+// ---------------------------------------------------------------------------------------------
+// The line of tiles
+// ---------------------------------------------------------------------------------------------
+// Tiles of new keys that the rows of query tile qt need.
+__device__ __forceinline__ int32_t new_tiles(const Kv4Args &k, int32_t qt) {
+    if (!k.a.kn) return 0;
+    if (k.a.mask) return (k.a.n + kTile - 1) / kTile;
+    const int32_t last = min(k.a.n - 1, ((qt + 1) * k.rows - 1) / k.group);
+    return last / kTile + 1;
+}
+// Tiles of cached keys of request b; at least one where a unit would have none.
+__device__ __forceinline__ int64_t cached_tiles(const Kv4Args &k, int32_t b) {
+    const int64_t t = (kv4_length(k.a.cache, b) + kTile - 1) / kTile;
+    return t < 1 && !k.a.kn ? 1 : t;
+}
+
+// Where a CTA begins and ends, and the unit that its first tile belongs to.
+struct Place {
+    int64_t total, begin, end;  // tiles of the line
+    int64_t ctas;               // CTAs that share it
+    int32_t b, hk, qt;
+    int64_t off;                // the first tile's place in its unit
+};
+
+// Sum over the block; every thread gets it.  `red`: one slot a warp.
+__device__ int64_t block_sum64(int64_t v, int64_t *red) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(kFull, v, off);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    int64_t t = 0;
+    for (int w = 0; w < static_cast<int>(blockDim.x) / 32; ++w) t += red[w];
+    return t;
+}
+
+// All threads of the block; the result is in *out after the last barrier.  Returns false when this
+// CTA has nothing to do.
+__device__ bool find_place(const Kv4Args &k, Place *out, int64_t *red) {
+    const int32_t tid = threadIdx.x, nt = blockDim.x, B = k.a.B;
+    const int64_t Hk = k.a.cache.Hk;
+    int64_t per = 0;  // tiles of new keys of one (request, kv head)
+    if (k.a.mask || !k.a.kn) {
+        per = static_cast<int64_t>(k.QT) * new_tiles(k, 0);
+    } else {
+        for (int32_t q = tid; q < k.QT; q += nt) per += new_tiles(k, q);
+        per = block_sum64(per, red);
+    }
+    int64_t mine = 0;
+    for (int32_t b = tid; b < B; b += nt) mine += Hk * (k.QT * cached_tiles(k, b) + per);
+    const int64_t total = block_sum64(mine, red);
+    const int64_t want = (total + kMinTiles - 1) / kMinTiles;
+    const int64_t ctas = want < gridDim.x ? (want < 1 ? 1 : want) : gridDim.x;
+    const int64_t c = blockIdx.x;
+    if (c >= ctas) return false;
+    const int64_t begin = c * total / ctas, end = (c + 1) * total / ctas;
+    // the request that holds tile `begin`
+    int64_t base = 0;
+    for (int32_t b0 = 0; b0 < B; b0 += nt) {
+        const int32_t b = b0 + tid;
+        const int64_t w = b < B ? Hk * (k.QT * cached_tiles(k, b) + per) : 0;
+        int64_t inc = w;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int64_t o = __shfl_up_sync(kFull, inc, off);
+            if ((tid & 31) >= off) inc += o;
+        }
+        __syncthreads();
+        if ((tid & 31) == 31) red[tid >> 5] = inc;
+        __syncthreads();
+        int64_t before = base, all = base;
+        for (int w2 = 0; w2 < nt / 32; ++w2) {
+            if (w2 < (tid >> 5)) before += red[w2];
+            all += red[w2];
+        }
+        const int64_t lo = before + inc - w;
+        if (b < B && begin >= lo && begin < lo + w) {
+            int64_t off = begin - lo;
+            const int64_t ct = cached_tiles(k, b), block = k.QT * ct + per;
+            Place p;
+            p.total = total;
+            p.begin = begin;
+            p.end = end;
+            p.ctas = ctas;
+            p.b = b;
+            p.hk = static_cast<int32_t>(off / block);
+            off -= p.hk * block;
+            if (k.a.mask || !k.a.kn) {
+                const int64_t u = ct + new_tiles(k, 0);
+                p.qt = static_cast<int32_t>(off / u);
+                off -= p.qt * u;
+            } else {
+                p.qt = 0;
+                for (int64_t u; off >= (u = ct + new_tiles(k, p.qt)); ++p.qt) off -= u;
+            }
+            p.off = off;
+            *out = p;
+        }
+        base = all;
+        if (begin < base) break;
+    }
+    __syncthreads();
+    return true;
+}
+
+// A CTA's run through the line, unit by unit: [s0, s1) of the unit's tiles.
+struct Walk {
+    int32_t b, hk, qt;
+    int64_t t, s0, s1, unit;
+    int32_t nt;  // tiles of new keys (the unit's first)
+    int64_t len;
+
+    __device__ __forceinline__ void start(const Kv4Args &k, const Place &p) {
+        b = p.b;
+        hk = p.hk;
+        qt = p.qt;
+        t = p.begin;
+        s0 = p.off;
+        fill(k, p);
+    }
+    __device__ __forceinline__ void fill(const Kv4Args &k, const Place &p) {
+        nt = new_tiles(k, qt);
+        len = kv4_length(k.a.cache, b);
+        unit = cached_tiles(k, b) + nt;
+        s1 = min(unit, s0 + (p.end - t));
+    }
+    __device__ __forceinline__ bool next(const Kv4Args &k, const Place &p) {
+        t += s1 - s0;
+        if (t >= p.end) return false;
+        s0 = 0;
+        if (++qt == k.QT) {
+            qt = 0;
+            if (++hk == k.a.cache.Hk) {
+                hk = 0;
+                if (++b == k.a.B) return false;  // lengths changed under the call
+            }
+        }
+        fill(k, p);
+        return true;
+    }
+};
+
+// ---------------------------------------------------------------------------------------------
+// The kernel
+// ---------------------------------------------------------------------------------------------
+template <int G, int NQ>
+struct Shape {
+    static constexpr int D = G * kKv4Group;
+    static constexpr int kRows = 8 * NQ;
+    static constexpr uint32_t kStageBytes = 4u * kv4_chunk_bytes(G);
+    static constexpr uint32_t kMergeStride = D + 4;  // floats a row: no bank conflicts
+    static constexpr uint32_t kRing = 0;
+    static constexpr uint32_t kMerge = kRing + kStages * kStageBytes;
+    static constexpr uint32_t kMl = kMerge + kWarps * kRows * kMergeStride * 4;
+    static constexpr uint32_t kTotal = kMl + kWarps * kRows * 8;
+    static constexpr int kBlocks = NQ == 1 ? 3 : (NQ == 2 ? 2 : 1);
+};
+
+template <int G, int NQ>
+__global__ void __launch_bounds__(kThreads, Shape<G, NQ>::kBlocks) kv4_attention_kernel(const Kv4Args k) {
+    using S = Shape<G, NQ>;
+    constexpr int D = S::D, kRows = S::kRows;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ uint64_t full[kStages], empty[kStages];
+    __shared__ int32_t valid[kStages][4];  // keys of each chunk of the stage (0..16)
+    __shared__ int32_t abort_mark;
+    __shared__ Place place;
+    __shared__ int64_t red[kThreads / 32];
+    const int32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], kWarps);
+        }
+        abort_mark = 0;
+        fence_barrier_init();
+    }
+    pdl_launch_dependents();
+    pdl_wait();
+    const Kv4Attention &a = k.a;
+    const bool busy = find_place(k, &place, red);  // its barriers also publish the mbarriers
+    if (!busy) {
+        if (threadIdx.x == 0) k.share[blockIdx.x].b = -1;
+        return;
+    }
+    const Place p = place;
+    volatile int32_t *abort_flag = &abort_mark;
+    Walk w;
+    w.start(k, p);
+    if (threadIdx.x == 0) {
+        Kv4Share sh{-1, 0, 0, 0, 0, 0};
+        if (w.s0 > 0) {
+            const int64_t u0 = p.begin - w.s0;  // the unit's first tile
+            const int64_t c0 = ((u0 + 1) * p.ctas - 1) / p.total, c1 = ((u0 + w.unit) * p.ctas - 1) / p.total;
+            if (c0 == static_cast<int64_t>(blockIdx.x) - 1)
+                sh = Kv4Share{w.b, w.hk, w.qt, static_cast<int32_t>(c0), static_cast<int32_t>(c1),
+                              c0 * p.total / p.ctas == u0 ? 0 : 1};
+        }
+        k.share[blockIdx.x] = sh;
+    }
+
+    if (warp == kWarps) {
+        // ---------------- copies: a stage is up to four chunks of cached keys and values ----------
+        int32_t issued = 0;
+        bool dead = false;
+        do {
+            if (lane == 0 && w.len != a.cache.lengths[w.b]) latch(a.status, kDevBounds);  // clamped
+            const int64_t k0 = max(w.s0 - w.nt, int64_t{0}), k1 = w.s1 - w.nt;
+            for (int64_t kt = k0; kt < k1 && !dead; kt += 8) {
+                // the chunks of 8 tiles, one a lane
+                const int64_t key = kt * kTile + lane * kKv4Chunk;
+                int32_t nv = static_cast<int32_t>(min(max(w.len - key, int64_t{0}), int64_t{kKv4Chunk}));
+                const uint8_t *src = nullptr;
+                if (nv > 0 && kt + (lane >> 2) < k1) {
+                    src = kv4_chunk(a.cache, w.b, w.hk, key);
+                    if (!src) latch(a.status, kDevBounds);  // its keys count as absent
+                }
+                if (!src) nv = 0;
+                const int32_t tiles = static_cast<int32_t>(min(k1 - kt, int64_t{8}));
+                for (int32_t j = 0; j < tiles; ++j, ++issued) {
+                    const int32_t st = issued % kStages;
+                    if (issued >= kStages && lane == 0 &&
+                        !mbar_wait(&empty[st], static_cast<uint32_t>(issued / kStages - 1) & 1u, abort_flag)) {
+                        *abort_flag = 1;
+                        latch(a.status, kDevTimeout);
+                    }
+                    dead = __shfl_sync(kFull, static_cast<int>(*abort_flag), 0) != 0;
+                    if (dead) break;
+                    const bool my = (lane >> 2) == j;
+                    const uint32_t have = __ballot_sync(kFull, my && src);
+                    if (my) valid[st][lane & 3] = nv;
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive_expect_tx(&full[st], static_cast<uint32_t>(__popc(have)) * kv4_chunk_bytes(G));
+                    __syncwarp();
+                    if (my && src)
+                        bulk_load(smem + S::kRing + st * S::kStageBytes + (lane & 3) * kv4_chunk_bytes(G), src,
+                                  kv4_chunk_bytes(G), &full[st]);
+                }
+            }
+        } while (!dead && w.next(k, p));
+        // every copy has landed before the block's memory is handed on
+        if (lane == 0)
+            for (int32_t i = max(issued - kStages, 0); i < issued; ++i)
+                mbar_wait(&full[i % kStages], static_cast<uint32_t>(i / kStages) & 1u, nullptr);
+        return;
+    }
+
+    // ---------------- multiplication: warp `warp` takes chunk `warp` of each tile ----------------
+    const int32_t gq = lane >> 2, qd = lane & 3;
+    float *merge = reinterpret_cast<float *>(smem + S::kMerge);
+    float2 *merge_ml = reinterpret_cast<float2 *>(smem + S::kMl);
+    int32_t taken = 0;  // stages
+    do {
+        uint32_t qf[2 * G][NQ][2];  // fp16 queries, the score MMAs' B operand
+        uint32_t qs[NQ];            // fp16 hi + lo of the sum of group qd's elements
+        float qk[NQ][2];            // what turns a column's accumulated score into base 2
+        float o[2 * G][NQ][4];      // dims (rows) x queries
+        float om[NQ][4];            // groups (rows gq < G) x queries: sum of p m
+        float ref[NQ][2], l[NQ][2];
+        // p = 2^(score - ref), at most 2^top; a new ref puts the largest at 2^aim
+        float aim = 9.0f, top = 12.0f;
+#pragma unroll
+        for (int nq = 0; nq < NQ; ++nq) {
+            const int32_t row = w.qt * kRows + nq * 8 + gq;
+            const bool live = row < k.Mq;
+            const int32_t node = live ? row / k.group : 0, head = w.hk * k.group + (live ? row - node * k.group : 0);
+            const __nv_bfloat16 *src = a.q + (static_cast<int64_t>(w.b) * a.n + node) * a.ldq + static_cast<int64_t>(head) * D + 8 * qd;
+            float x[G][8];
+            float big = 0.0f;
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                const uint4 v = live ? *reinterpret_cast<const uint4 *>(src + 32 * g) : make_uint4(0, 0, 0, 0);
+                const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    x[g][2 * i] = bf_lo(vw[i]);
+                    x[g][2 * i + 1] = bf_hi(vw[i]);
+                    big = fmaxf(big, fmaxf(fabsf(x[g][2 * i]), fabsf(x[g][2 * i + 1])));
+                }
+            }
+            big = fmaxf(big, __shfl_xor_sync(kFull, big, 1));
+            big = fmaxf(big, __shfl_xor_sync(kFull, big, 2));
+            // 2^(9 - floor(log2 big)): the row's largest element becomes 2^9 .. 2^10
+            const int32_t e = max(static_cast<int32_t>(__float_as_uint(big) >> 23), 10);
+            const float f = __uint_as_float(static_cast<uint32_t>(263 - e) << 23);
+            const float inv = __uint_as_float(static_cast<uint32_t>(e - 9) << 23);
+            float sum = 0.0f;
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                float t = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    x[g][i] *= f;
+                    t += x[g][i];
+                }
+                t += __shfl_xor_sync(kFull, t, 1);
+                t += __shfl_xor_sync(kFull, t, 2);
+                if (g == qd) sum = t;
+                // pairs (0, 4), (1, 5), (2, 6), (3, 7) of the word's codes; 1, 3, 5, 7 come as 16 c
+                qf[2 * g][nq][0] = pack_f16(x[g][0], x[g][4]);
+                qf[2 * g][nq][1] = pack_f16(x[g][1] * 0.0625f, x[g][5] * 0.0625f);
+                qf[2 * g + 1][nq][0] = pack_f16(x[g][2], x[g][6]);
+                qf[2 * g + 1][nq][1] = pack_f16(x[g][3] * 0.0625f, x[g][7] * 0.0625f);
+            }
+            const float hi = __half2float(__float2half_rn(sum));
+            qs[nq] = pack_f16(hi, sum - hi);
+            const float mul = inv * k.scale2 * 16777216.0f;
+            qk[nq][0] = __shfl_sync(kFull, mul, 8 * qd);
+            qk[nq][1] = __shfl_sync(kFull, mul, 8 * qd + 4);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                ref[nq][c] = -INFINITY;
+                l[nq][c] = 0.0f;
+            }
+#pragma unroll
+            for (int e2 = 0; e2 < 4; ++e2) om[nq][e2] = 0.0f;
+#pragma unroll
+            for (int t = 0; t < 2 * G; ++t)
+#pragma unroll
+                for (int e2 = 0; e2 < 4; ++e2) o[t][nq][e2] = 0.0f;
+        }
+
+        // scores in base 2 (t: keys gq, gq + 8 x queries 2 qd, 2 qd + 1) to p, with the running
+        // maximum, the sum and what was accumulated so far brought to the same reference
+        auto softmax = [&](float (&t)[NQ][4]) {
+            bool raise = false;
+            float corr[NQ][2];
+#pragma unroll
+            for (int nq = 0; nq < NQ; ++nq)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    float mx = fmaxf(t[nq][c], t[nq][c + 2]);
+#pragma unroll
+                    for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, off));
+                    corr[nq][c] = 1.0f;
+                    if (mx - ref[nq][c] > top) {
+                        const float nr = mx - aim;
+                        corr[nq][c] = ref[nq][c] == -INFINITY ? 0.0f : ex2_approx(ref[nq][c] - nr);
+                        ref[nq][c] = nr;
+                        raise = true;
+                    }
+                }
+            if (__any_sync(kFull, raise)) {
+#pragma unroll
+                for (int nq = 0; nq < NQ; ++nq) {
+                    l[nq][0] *= corr[nq][0];
+                    l[nq][1] *= corr[nq][1];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) om[nq][e] *= corr[nq][e & 1];
+#pragma unroll
+                    for (int i = 0; i < 2 * G; ++i)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[i][nq][e] *= corr[nq][e & 1];
+                }
+            }
+#pragma unroll
+            for (int nq = 0; nq < NQ; ++nq)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float r = ref[nq][e & 1];
+                    const float pv = ex2_approx(t[nq][e] - (r == -INFINITY ? 0.0f : r));
+                    t[nq][e] = pv;
+                    l[nq][e & 1] += pv;
+                }
+        };
+
+        int64_t s = w.s0;
+        // ---------------- new keys: bf16, straight from memory ----------------
+        for (; s < w.s1 && s < w.nt; ++s) {
+            const int32_t key0 = static_cast<int32_t>(s) * kTile + warp * 16;
+            if (key0 >= a.n) continue;
+            const int64_t krow = static_cast<int64_t>(w.b) * a.n;
+            float sc[NQ][4];
+#pragma unroll
+            for (int nq = 0; nq < NQ; ++nq)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sc[nq][e] = 0.0f;
+            const int32_t ka = key0 + gq, kb = ka + 8;
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                const uint4 z = make_uint4(0, 0, 0, 0);
+                const __nv_bfloat16 *src = a.kn + krow * a.ldkv + static_cast<int64_t>(w.hk) * D + 32 * g + 8 * qd;
+                const uint4 va = ka < a.n ? *reinterpret_cast<const uint4 *>(src + ka * a.ldkv) : z;
+                const uint4 vb = kb < a.n ? *reinterpret_cast<const uint4 *>(src + kb * a.ldkv) : z;
+#pragma unroll
+                for (int nq = 0; nq < NQ; ++nq) {
+                    const int32_t row = w.qt * kRows + nq * 8 + gq;
+                    const bool live = row < k.Mq;
+                    const int32_t node = live ? row / k.group : 0, head = w.hk * k.group + (live ? row - node * k.group : 0);
+                    const uint4 vq = live ? *reinterpret_cast<const uint4 *>(a.q + (krow + node) * a.ldq + static_cast<int64_t>(head) * D + 32 * g + 8 * qd) : z;
+                    mma_bf16(sc[nq], va.x, vb.x, va.y, vb.y, vq.x, vq.y);
+                    mma_bf16(sc[nq], va.z, vb.z, va.w, vb.w, vq.z, vq.w);
+                }
+            }
+            // which of the two keys each of the two queries sees
+            bool see[NQ][4];
+#pragma unroll
+            for (int nq = 0; nq < NQ; ++nq)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int32_t row = w.qt * kRows + nq * 8 + 2 * qd + (e & 1), key = e < 2 ? ka : kb;
+                    bool vis = row < k.Mq && key < a.n;
+                    if (vis) {
+                        const int32_t node = row / k.group;
+                        vis = a.mask ? (a.mask[(krow + node) * k.W + (key >> 5)] >> (key & 31)) & 1u : key <= node;
+                    }
+                    see[nq][e] = vis;
+                    sc[nq][e] = vis ? sc[nq][e] * k.scale2 : -INFINITY;
+                }
+            softmax(sc);
+            // values: dims 32 g + 4 gq .. + 3 of keys 2 qd, 2 qd + 1, 2 qd + 8, 2 qd + 9
+            uint2 v[G][4];
+            bool odd = false;  // a NaN or an infinity among them
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int32_t key = key0 + 2 * qd + (u & 1) + 8 * (u >> 1);
+                const __nv_bfloat16 *src = a.vn + (krow + key) * a.ldkv + static_cast<int64_t>(w.hk) * D + 4 * gq;
+#pragma unroll
+                for (int g = 0; g < G; ++g) {
+                    v[g][u] = key < a.n ? *reinterpret_cast<const uint2 *>(src + 32 * g) : make_uint2(0, 0);
+                    const uint32_t x = v[g][u].x, y = v[g][u].y;
+                    odd = odd || (x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u ||
+                          (y & 0x7f80u) == 0x7f80u || (y & 0x7f800000u) == 0x7f800000u;
+                }
+            }
+            if (__any_sync(kFull, odd)) {
+                // A hidden key's NaN or infinity must not reach the rows that do not see it (0 x NaN
+                // is NaN): such elements join the rows that see them one by one, and count as 0 below.
+                for (int kk = 0; kk < 16 && key0 + kk < a.n; ++kk) {
+                    const __nv_bfloat16 *src = a.vn + (krow + key0 + kk) * a.ldkv + static_cast<int64_t>(w.hk) * D + 4 * gq;
+#pragma unroll
+                    for (int nq = 0; nq < NQ; ++nq)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            const int from = (kk & 7) * 4 + qd;
+                            const float p0 = __shfl_sync(kFull, sc[nq][c], from), p1 = __shfl_sync(kFull, sc[nq][2 + c], from);
+                            const int s0 = __shfl_sync(kFull, static_cast<int>(see[nq][c]), from);
+                            const int s1 = __shfl_sync(kFull, static_cast<int>(see[nq][2 + c]), from);
+                            const float pk = kk < 8 ? p0 : p1;
+                            if (!(kk < 8 ? s0 : s1)) continue;
+#pragma unroll
+                            for (int g = 0; g < G; ++g)
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    const float x = __bfloat162float(src[32 * g + i]);
+                                    if (!isfinite(x)) o[2 * g + (i >> 1)][nq][2 * (i & 1) + c] += pk * x;
+                                }
+                        }
+                }
+#pragma unroll
+                for (int g = 0; g < G; ++g)
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        uint32_t &x = v[g][u].x, &y = v[g][u].y;
+                        if ((x & 0x7f80u) == 0x7f80u) x &= 0xffff0000u;
+                        if ((x & 0x7f800000u) == 0x7f800000u) x &= 0xffffu;
+                        if ((y & 0x7f80u) == 0x7f80u) y &= 0xffff0000u;
+                        if ((y & 0x7f800000u) == 0x7f800000u) y &= 0xffffu;
+                    }
+            }
+#pragma unroll
+            for (int nq = 0; nq < NQ; ++nq) {
+                // p as bf16 hi + lo: 2^-16 relative
+                float hi[4], lo[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    hi[e] = __bfloat162float(__float2bfloat16_rn(sc[nq][e]));
+                    lo[e] = sc[nq][e] - hi[e];
+                }
+                const uint32_t h0 = transpose8(pack_b16(hi[0], hi[1])), h1 = transpose8(pack_b16(hi[2], hi[3]));
+                const uint32_t l0 = transpose8(pack_b16(lo[0], lo[1])), l1 = transpose8(pack_b16(lo[2], lo[3]));
+#pragma unroll
+                for (int g = 0; g < G; ++g) {
+                    const uint32_t a0 = __byte_perm(v[g][0].x, v[g][1].x, 0x5410), a1 = __byte_perm(v[g][0].x, v[g][1].x, 0x7632);
+                    const uint32_t a2 = __byte_perm(v[g][2].x, v[g][3].x, 0x5410), a3 = __byte_perm(v[g][2].x, v[g][3].x, 0x7632);
+                    mma_bf16(o[2 * g][nq], a0, a1, a2, a3, h0, h1);
+                    mma_bf16(o[2 * g][nq], a0, a1, a2, a3, l0, l1);
+                    const uint32_t c0 = __byte_perm(v[g][0].y, v[g][1].y, 0x5410), c1 = __byte_perm(v[g][0].y, v[g][1].y, 0x7632);
+                    const uint32_t c2 = __byte_perm(v[g][2].y, v[g][3].y, 0x5410), c3 = __byte_perm(v[g][2].y, v[g][3].y, 0x7632);
+                    mma_bf16(o[2 * g + 1][nq], c0, c1, c2, c3, h0, h1);
+                    mma_bf16(o[2 * g + 1][nq], c0, c1, c2, c3, l0, l1);
+                }
+            }
+        }
+        // the cached tiles accumulate c 2^-24 (rows 0-7: even dims) and 16 c 2^-24 (rows 8-15: odd dims)
+#pragma unroll
+        for (int i = 0; i < 2 * G; ++i)
+#pragma unroll
+            for (int nq = 0; nq < NQ; ++nq)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[i][nq][e] *= e < 2 ? 0x1p-24f : 0x1p-20f;
+
+        // ---------------- cached keys ----------------
+        for (; s < w.s1; ++s, ++taken) {
+            const int32_t st = taken % kStages;
+            if (!mbar_wait(&full[st], static_cast<uint32_t>(taken / kStages) & 1u, abort_flag)) {
+                *abort_flag = 1;
+                latch(a.status, kDevTimeout);
+            }
+            const int32_t nv = __shfl_sync(kFull, *abort_flag ? 0 : valid[st][warp], 0);
+            if (nv > 0) {
+                const uint8_t *ch = smem + S::kRing + st * S::kStageBytes + warp * kv4_chunk_bytes(G);
+                // scores of keys kv4 rows gq, gq + 8
+                float sc[NQ][4];
+                {
+                    const uint8_t *kp = ch + kv4_key_params(G);
+                    const uint32_t ma = qd < G ? *reinterpret_cast<const uint32_t *>(kp + gq * 4 * G + 4 * qd) : 0u;
+                    const uint32_t mb = qd < G ? *reinterpret_cast<const uint32_t *>(kp + (gq + 8) * 4 * G + 4 * qd) : 0u;
+                    const uint32_t a0 = __byte_perm(ma, ma, 0x3232), a1 = __byte_perm(mb, mb, 0x3232);
+#pragma unroll
+                    for (int nq = 0; nq < NQ; ++nq) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) sc[nq][e] = 0.0f;
+                        mma_f16(sc[nq], a0, a1, 0u, 0u, qs[nq], 0u);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) sc[nq][e] *= 0x1p-24f;
+                    }
+                    uint32_t wa[G], wb[G], pa[G], pb[G];
+                    load_words<G>(ch + gq * 16 * G + qd * 4 * G, wa);
+                    load_words<G>(ch + (gq + 8) * 16 * G + qd * 4 * G, wb);
+                    load_words<G>(kp + gq * 4 * G, pa);
+                    load_words<G>(kp + (gq + 8) * 4 * G, pb);
+#pragma unroll
+                    for (int g = 0; g < G; ++g) {
+                        const uint32_t xa = wa[g] >> 8, xb = wb[g] >> 8;
+                        const float sa = low_f16(pa[g]), sb = low_f16(pb[g]);
+#pragma unroll
+                        for (int nq = 0; nq < NQ; ++nq) {
+                            float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                            mma_f16(acc, wa[g] & 0x000f000fu, wb[g] & 0x000f000fu, wa[g] & 0x00f000f0u,
+                                    wb[g] & 0x00f000f0u, qf[2 * g][nq][0], qf[2 * g][nq][1]);
+                            mma_f16(acc, xa & 0x000f000fu, xb & 0x000f000fu, xa & 0x00f000f0u, xb & 0x00f000f0u,
+                                    qf[2 * g + 1][nq][0], qf[2 * g + 1][nq][1]);
+                            sc[nq][0] = fmaf(sa, acc[0], sc[nq][0]);
+                            sc[nq][1] = fmaf(sa, acc[1], sc[nq][1]);
+                            sc[nq][2] = fmaf(sb, acc[2], sc[nq][2]);
+                            sc[nq][3] = fmaf(sb, acc[3], sc[nq][3]);
+                        }
+                    }
+                }
+                // MMA row i is key t with kv4_key_slot(t) = i
+                const int32_t ta = (gq >> 1) | ((gq & 1) << 2);
+#pragma unroll
+                for (int nq = 0; nq < NQ; ++nq)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sc[nq][e] *= qk[nq][e & 1];
+                if (nv < 16) {
+#pragma unroll
+                    for (int nq = 0; nq < NQ; ++nq)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (ta + (e < 2 ? 0 : 8) >= nv) sc[nq][e] = -INFINITY;
+                }
+                // values: keys qd, qd + 4, qd + 8, qd + 12
+                const uint8_t *vp = ch + kv4_value_params(G);
+                uint32_t par[4][G];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) load_words<G>(vp + (qd + 4 * u) * 4 * G, par[u]);
+                uint32_t mm[4] = {0u, 0u, 0u, 0u};
+                if (gq < G) {
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) mm[u] = *reinterpret_cast<const uint32_t *>(vp + (qd + 4 * u) * 4 * G + 4 * gq);
+                }
+                if (nv < 16) {  // what lies behind the last key is not a number that may be used
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        if (qd + 4 * u >= nv) {
+                            mm[u] = 0u;
+#pragma unroll
+                            for (int g = 0; g < G; ++g) par[u][g] = 0u;
+                        }
+                }
+                // p s must stay below fp16's largest: with p up to 2^12, s below 16.  Steeper
+                // values (s up to 2^12.1) take p up to 2^3 from here on.
+                if (aim != 0.0f) {
+                    bool steep = false;
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+#pragma unroll
+                        for (int g = 0; g < G; ++g) steep = steep || (par[u][g] & 0xffffu) >= 0x4c00u;  // s >= 16, or NaN
+                    if (__any_sync(kFull, steep)) {
+                        aim = 0.0f;
+                        top = 3.0f;
+#pragma unroll
+                        for (int nq = 0; nq < NQ; ++nq) {
+                            ref[nq][0] += 9.0f;
+                            ref[nq][1] += 9.0f;
+                            l[nq][0] *= 0x1p-9f;
+                            l[nq][1] *= 0x1p-9f;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                om[nq][e] *= 0x1p-9f;
+#pragma unroll
+                                for (int i = 0; i < 2 * G; ++i) o[i][nq][e] *= 0x1p-9f;
+                            }
+                        }
+                    }
+                }
+                softmax(sc);
+                uint32_t b0[NQ], b1[NQ];
+#pragma unroll
+                for (int nq = 0; nq < NQ; ++nq) {
+                    b0[nq] = transpose8(pack_f16(sc[nq][0], sc[nq][1]));
+                    b1[nq] = transpose8(pack_f16(sc[nq][2], sc[nq][3]));
+                    mma_f16(om[nq], __byte_perm(mm[0], mm[1], 0x7632), 0u, __byte_perm(mm[2], mm[3], 0x7632), 0u, b0[nq], b1[nq]);
+                }
+                const uint8_t *vc = ch + kv4_value_codes(G);
+                uint32_t vw[4][(G + 1) / 2];  // two groups a word
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int32_t t = qd + 4 * u;
+                    const uint8_t *src = vc + t * 16 * G + kv4_value_word(t, gq, 0, G);
+                    if constexpr (G == 4 || G == 2) {
+                        load_words<G / 2>(src, vw[u]);
+                    } else {
+#pragma unroll
+                        for (int g = 0; g < G; ++g) {
+                            const uint32_t x = reinterpret_cast<const uint16_t *>(src)[g];
+                            vw[u][g / 2] = g & 1 ? vw[u][g / 2] | (x << 16) : x;
+                        }
+                    }
+                }
+#pragma unroll
+                for (int g = 0; g < G; ++g) {
+                    const uint32_t sel = g & 1 ? 0x7632 : 0x5410;
+                    const uint32_t x = __byte_perm(vw[0][g / 2], vw[1][g / 2], sel), y = __byte_perm(vw[2][g / 2], vw[3][g / 2], sel);
+                    const uint32_t x8 = x >> 8, y8 = y >> 8;
+                    const uint32_t s01 = __byte_perm(par[0][g], par[1][g], 0x5410), s23 = __byte_perm(par[2][g], par[3][g], 0x5410);
+#pragma unroll
+                    for (int nq = 0; nq < NQ; ++nq) {
+                        const uint32_t p0 = mul_f16x2(b0[nq], s01), p1 = mul_f16x2(b1[nq], s23);
+                        mma_f16(o[2 * g][nq], x & 0x000f000fu, x & 0x00f000f0u, y & 0x000f000fu, y & 0x00f000f0u, p0, p1);
+                        mma_f16(o[2 * g + 1][nq], x8 & 0x000f000fu, x8 & 0x00f000f0u, y8 & 0x000f000fu, y8 & 0x00f000f0u, p0, p1);
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&empty[st]);
+        }
+
+        // ---------------- the warps' shares of the segment meet ----------------
+        named_barrier_sync(1, kWarps * 32);  // the previous segment's sums have been read
+#pragma unroll
+        for (int nq = 0; nq < NQ; ++nq) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int off = 4; off < 32; off <<= 1) l[nq][c] += __shfl_xor_sync(kFull, l[nq][c], off);
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const float add = __shfl_sync(kFull, om[nq][c], g * 4 + qd);
+                    float4 v;  // dims 32 g + 4 gq .. + 3
+                    v.x = fmaf(o[2 * g][nq][c], 0x1p24f, add);
+                    v.y = fmaf(o[2 * g][nq][2 + c], 0x1p20f, add);
+                    v.z = fmaf(o[2 * g + 1][nq][c], 0x1p24f, add);
+                    v.w = fmaf(o[2 * g + 1][nq][2 + c], 0x1p20f, add);
+                    *reinterpret_cast<float4 *>(merge + (warp * kRows + nq * 8 + 2 * qd + c) * S::kMergeStride + 32 * g + 4 * gq) = v;
+                }
+            if (gq < 2) merge_ml[warp * kRows + nq * 8 + 2 * qd + gq] = gq ? make_float2(ref[nq][1], l[nq][1]) : make_float2(ref[nq][0], l[nq][0]);
+        }
+        named_barrier_sync(1, kWarps * 32);
+        if (!*abort_flag) {
+            const bool whole = w.s0 == 0 && w.s1 == w.unit;
+            const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (w.t == p.begin ? 0 : 1);
+            for (int32_t it = threadIdx.x; it < kRows * (D / 4); it += kWarps * 32) {
+                const int32_t r = it / (D / 4), c4 = it - r * (D / 4), row = w.qt * kRows + r;
+                if (row >= k.Mq) break;
+                float M = -INFINITY, L = 0.0f, wt[kWarps];
+#pragma unroll
+                for (int i = 0; i < kWarps; ++i) M = fmaxf(M, merge_ml[i * kRows + r].x);
+                float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+                for (int i = 0; i < kWarps; ++i) {
+                    const float2 ml = merge_ml[i * kRows + r];
+                    if (ml.x == -INFINITY) {
+                        // a warp whose keys are all hidden, or whose scores are all NaN (sum NaN)
+                        wt[i] = ml.y == 0.0f ? 0.0f : ml.y;
+                    } else {
+                        wt[i] = ex2_approx(ml.x - M);
+                    }
+                    L += wt[i] * ml.y;
+                    if (wt[i] == 0.0f) continue;
+                    const float4 x = *reinterpret_cast<const float4 *>(merge + (i * kRows + r) * S::kMergeStride + 4 * c4);
+                    v.x = fmaf(wt[i], x.x, v.x);
+                    v.y = fmaf(wt[i], x.y, v.y);
+                    v.z = fmaf(wt[i], x.z, v.z);
+                    v.w = fmaf(wt[i], x.w, v.w);
+                }
+                if (whole) {
+                    const int32_t node = row / k.group, head = w.hk * k.group + row - node * k.group;
+                    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+                    *reinterpret_cast<uint2 *>(a.o + ((static_cast<int64_t>(w.b) * a.n + node) * a.H + head) * D + 4 * c4) =
+                        make_uint2(pack_b16(v.x * inv, v.y * inv), pack_b16(v.z * inv, v.w * inv));
+                } else {
+                    *reinterpret_cast<float4 *>(k.part_o + (slot * kRows + r) * D + 4 * c4) = v;
+                    if (c4 == 0) k.part_ml[slot * kRows + r] = make_float2(M, L);
+                }
+            }
+        }
+    } while (w.next(k, p));
+}
+
+// Units that several CTAs worked on: block c merges the unit that CTA c is the first to continue.
+// o = sum_i w_i O_i / sum_i w_i l_i, w_i = 2^(m_i - max m), over CTAs first..last in order.
+__global__ void __launch_bounds__(128) kv4_merge_kernel(const Kv4Args k) {
+    pdl_launch_dependents();
+    pdl_wait();
+    const Kv4Share sh = k.share[blockIdx.x];
+    if (sh.b < 0) return;
+    const int32_t D = k.a.cache.G * kKv4Group, quads = D / 4;
+    const int32_t rows = min(k.rows, k.Mq - sh.qt * k.rows);
+    for (int32_t it = threadIdx.x + blockIdx.y * 128; it < rows * quads; it += 128 * gridDim.y) {
+        const int32_t r = it / quads, c4 = it - r * quads;
+        auto slot = [&](int32_t c) { return 2 * static_cast<int64_t>(c) + (c == sh.first ? sh.first_slot : 0); };
+        float M = -INFINITY;
+        for (int32_t c = sh.first; c <= sh.last; ++c) M = fmaxf(M, k.part_ml[slot(c) * k.rows + r].x);
+        float L = 0.0f;
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+        for (int32_t c = sh.first; c <= sh.last; ++c) {
+            const float2 ml = k.part_ml[slot(c) * k.rows + r];
+            const float4 x = *reinterpret_cast<const float4 *>(k.part_o + (slot(c) * k.rows + r) * D + 4 * c4);
+            const float wt = ml.x == -INFINITY ? (ml.y == 0.0f ? 0.0f : ml.y) : ex2_approx(ml.x - M);
+            if (wt == 0.0f) continue;
+            L += wt * ml.y;
+            v.x = fmaf(wt, x.x, v.x);
+            v.y = fmaf(wt, x.y, v.y);
+            v.z = fmaf(wt, x.z, v.z);
+            v.w = fmaf(wt, x.w, v.w);
+        }
+        const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+        const int32_t row = sh.qt * k.rows + r, node = row / k.group, head = sh.hk * k.group + row - node * k.group;
+        *reinterpret_cast<uint2 *>(k.a.o + ((static_cast<int64_t>(sh.b) * k.a.n + node) * k.a.H + head) * D + 4 * c4) =
+            make_uint2(pack_b16(v.x * inv, v.y * inv), pack_b16(v.z * inv, v.w * inv));
+    }
+}
+
+// ---------------------------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------------------------
+struct Variant {
+    int32_t rows, threads;
+    size_t smem;
+    void (*kernel)(const Kv4Args);
+};
+
+template <int G>
+Variant variant_of(int32_t mq) {
+    // query rows a unit takes: 8, 16 or 32
+    if (mq <= 8) return Variant{8, kThreads, Shape<G, 1>::kTotal, kv4_attention_kernel<G, 1>};
+    if (mq <= 16) return Variant{16, kThreads, Shape<G, 2>::kTotal, kv4_attention_kernel<G, 2>};
+    return Variant{32, kThreads, Shape<G, 4>::kTotal, kv4_attention_kernel<G, 4>};
+}
+Variant variant(int32_t G, int32_t mq) {
+    switch (G) {
+        case 1: return variant_of<1>(mq);
+        case 2: return variant_of<2>(mq);
+        case 3: return variant_of<3>(mq);
+        default: return variant_of<4>(mq);
+    }
+}
+
+struct Device {
+    int32_t sms = 0;
+    int32_t blocks[5][3] = {};  // CTAs an SM holds, by groups and rows
+};
+std::mutex g_mu;
+Device g_dev[64];
+
+// The device's SM count and each variant's CTAs an SM (attributes set once).
+const Device *device_now() {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return nullptr;
+    std::lock_guard<std::mutex> lock(g_mu);
+    Device &d = g_dev[dev];
+    if (d.sms) return &d;
+    int sms = 0;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1) return nullptr;
+    for (int g = 1; g <= 4; ++g)
+        for (int i = 0; i < 3; ++i) {
+            const Variant v = variant(g, 8 << i);
+            int n = 0;
+            if (cudaFuncSetAttribute(v.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(v.smem)) != cudaSuccess ||
+                cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, v.kernel, v.threads, v.smem) != cudaSuccess || n < 1)
+                return nullptr;
+            d.blocks[g][i] = n;
+        }
+    d.sms = sms;
+    return &d;
+}
+
+int32_t grid_of(const Device &d, int32_t G, const Variant &v) { return d.sms * d.blocks[G][v.rows == 8 ? 0 : (v.rows == 16 ? 1 : 2)]; }
+
+size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+
+}  // namespace
+
+size_t kv4_attention_workspace(int32_t Hk, int32_t G, int32_t H, int32_t n) {
+    const Device *d = device_now();
+    if (!d) return 0;
+    const Variant v = variant(G, static_cast<int32_t>(std::min<int64_t>(static_cast<int64_t>(n) * (H / Hk), 1 << 20)));
+    const size_t grid = grid_of(*d, G, v);
+    return align256(grid * sizeof(Kv4Share)) + align256(grid * 2 * v.rows * sizeof(float2)) + grid * 2 * v.rows * G * kKv4Group * 4;
+}
+
+cudaError_t launch_kv4_attention(const Kv4Attention &a, cudaStream_t st) {
+    const Device *d = device_now();
+    if (!d) return cudaErrorInvalidDevice;
+    const int32_t G = a.cache.G;
+    Kv4Args k;
+    k.a = a;
+    k.group = a.H / a.cache.Hk;
+    k.Mq = a.n * k.group;
+    const Variant v = variant(G, k.Mq);
+    k.rows = v.rows;
+    k.QT = (k.Mq + v.rows - 1) / v.rows;
+    k.W = (a.n + 31) / 32;
+    k.scale2 = kLog2e / sqrtf(static_cast<float>(G * kKv4Group));
+    const int32_t full = grid_of(*d, G, v);
+    uint8_t *ws = static_cast<uint8_t *>(a.ws);
+    k.share = reinterpret_cast<Kv4Share *>(ws);
+    ws += align256(full * sizeof(Kv4Share));
+    k.part_ml = reinterpret_cast<float2 *>(ws);
+    ws += align256(static_cast<size_t>(full) * 2 * v.rows * sizeof(float2));
+    k.part_o = reinterpret_cast<float *>(ws);
+    // no more CTAs than the longest possible line gives work to
+    const int64_t units = static_cast<int64_t>(a.B) * a.cache.Hk * k.QT;
+    const int64_t tiles = (a.cache.cap + kTile - 1) / kTile + (a.kn ? (a.n + kTile - 1) / kTile : 0);
+    const int64_t most = (units > (int64_t{1} << 40) / tiles) ? full : (units * tiles + kMinTiles - 1) / kMinTiles;
+    const unsigned grid = static_cast<unsigned>(std::min<int64_t>(full, std::max<int64_t>(most, 1)));
+    const cudaError_t e = launch_pdl(v.kernel, dim3(grid), dim3(v.threads), v.smem, st, k);
+    if (e != cudaSuccess || grid == 1) return e;
+    return launch_pdl(kv4_merge_kernel, dim3(grid, v.rows / 8 * 2), dim3(128), 0, st, k);
+}
+
+}  // namespace eagle
+
+extern "C" {
+
+size_t eagle_kv4_attention_workspace_bytes(const eagle_kv4_cache *cache, int32_t nodes, int32_t heads) {
+    eagle::Kv4View v;
+    if (!eagle::kv4_view(cache, &v) || nodes < 1 || nodes > eagle::kMaxCandidates + 1) return 0;
+    if (heads < 1 || heads > 65536 || heads % v.Hk) return 0;
+    return eagle::kv4_attention_workspace(v.Hk, v.G, heads, nodes);
+}
+
+eagle_status eagle_kv4_attention(const eagle_kv4_cache *cache, int32_t batch, int32_t nodes, int32_t heads,
+                                 const void *d_q, int64_t ldq, const void *d_k, const void *d_v, int64_t ldkv,
+                                 const uint32_t *d_mask, void *d_out, void *d_ws, size_t ws_bytes, int32_t *d_status,
+                                 eagle_stream_t stream) {
+    using namespace eagle;
+    NvtxRange nvtx_range("eagle_kv4_attention");
+    Kv4Attention a{};
+    if (!kv4_view(cache, &a.cache) || batch < 0 || nodes < 1 || nodes > kMaxCandidates + 1) return EAGLE_ERR_INVALID_ARG;
+    if (heads < 1 || heads > 65536 || heads % a.cache.Hk) return EAGLE_ERR_INVALID_ARG;
+    if (batch == 0) return EAGLE_OK;
+    const int64_t D = a.cache.G * kKv4Group;
+    if (!d_q || !d_out || !d_ws || (d_k == nullptr) != (d_v == nullptr)) return EAGLE_ERR_INVALID_ARG;
+    if (d_mask && !d_k) return EAGLE_ERR_INVALID_ARG;
+    if (ldq < heads * D || ldq % 8 || (d_k && (ldkv < a.cache.Hk * D || ldkv % 8))) return EAGLE_ERR_INVALID_ARG;
+    const void *p16[] = {d_q, d_k, d_v, d_out};
+    for (const void *p : p16)
+        if (reinterpret_cast<uintptr_t>(p) & 15u) return EAGLE_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(d_ws) & 255u) return EAGLE_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(d_mask) | reinterpret_cast<uintptr_t>(d_status)) & 3u) return EAGLE_ERR_INVALID_ARG;
+    if (static_cast<int64_t>(nodes) * (heads / a.cache.Hk) > (1 << 24)) return EAGLE_ERR_INVALID_ARG;
+    const size_t need = kv4_attention_workspace(a.cache.Hk, a.cache.G, heads, nodes);
+    if (need == 0) return EAGLE_ERR_CUDA;
+    if (ws_bytes < need) return EAGLE_ERR_INVALID_ARG;
+    a.B = batch;
+    a.n = nodes;
+    a.H = heads;
+    a.q = static_cast<const __nv_bfloat16 *>(d_q);
+    a.kn = static_cast<const __nv_bfloat16 *>(d_k);
+    a.vn = static_cast<const __nv_bfloat16 *>(d_v);
+    a.ldq = ldq;
+    a.ldkv = ldkv;
+    a.mask = d_mask;
+    a.o = static_cast<__nv_bfloat16 *>(d_out);
+    a.ws = d_ws;
+    a.status = d_status;
+    return launch_kv4_attention(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? EAGLE_OK : EAGLE_ERR_CUDA;
+}
+
+}  // extern "C"

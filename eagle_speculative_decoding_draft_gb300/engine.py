@@ -437,6 +437,7 @@ class DecoderLayer:
         self.hidden, self.heads, self.kv_heads, self.head_dim, self.inter = h, heads, kv_heads, D, inter
         self.device = w_qkv.device
         self._ws = None
+        self._ws4 = {}
 
     def workspace(self, batch: int, nodes: int):
         nbytes = self._lib.eagle_decoder_layer_workspace_bytes(ctypes.byref(self.w), batch, nodes)
@@ -476,4 +477,47 @@ class DecoderLayer:
                                             _ptr(positions), _ptr(mask), _ptr(out), _ptr(kn), _ptr(vn),
                                             _ptr(ws), nbytes, _stream(x.device, stream)),
               "eagle_decoder_layer")
+        return (out, kn, vn) if new_kv else out
+
+    def kv4(self, x, cache, positions, mask=None, out=None, new_kv: bool = False, workspace=None, stream=None):
+        """The layer over a 4-bit cache (a ``KV4Cache`` of the layer's kv heads and head_dim; each
+        request at its own length).  x, positions, mask and the results are those of the call above
+        (mask None: node i sees nodes 0..i); ``cache.append`` takes k_new and v_new.  workspace: a
+        zero-filled uint8 tensor, used for these sizes alone, instead of the layer's own (one for each
+        batch and n); calls that may overlap need one each."""
+        _need(x, "x", torch.bfloat16)
+        B, n, h = x.shape
+        if h != self.hidden or B != cache.batch:
+            raise ValueError("x does not match the weights or the cache")
+        if cache.device != x.device or self.device != x.device:
+            raise ValueError("the weights, the cache and x must be on one device")
+        _need(positions, "positions", torch.int32)
+        if positions.shape != (B, n):
+            raise ValueError("positions shape does not match")
+        if mask is not None and _need(mask, "mask", torch.int32).shape != (B, n, (n + 31) // 32):
+            raise ValueError("mask shape does not match")
+        with cache._on(stream):
+            if out is None:
+                out = torch.empty_like(x)
+            elif _need(out, "out", torch.bfloat16).shape != x.shape:
+                raise ValueError("out shape does not match")
+            kn = vn = None
+            if new_kv:
+                kn = torch.empty(B, n, self.kv_heads, self.head_dim, dtype=torch.bfloat16, device=x.device)
+                vn = torch.empty_like(kn)
+            nbytes = self._lib.eagle_decoder_layer_kv4_workspace_bytes(ctypes.byref(self.w), cache._ref, max(B, 1), n)
+            if nbytes == 0:
+                raise ValueError(f"unusable decoder layer sizes (batch={B}, nodes={n}) or a cache of other heads")
+            if workspace is None:
+                # one a shape, kept: regions lie elsewhere at other sizes, and the tile tickets
+                # must find the zeros that the last call of the same sizes left
+                workspace = self._ws4.get((B, n))
+                if workspace is None or workspace.numel() < nbytes:
+                    workspace = self._ws4[(B, n)] = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
+            elif _need(workspace, "workspace", torch.uint8).numel() < nbytes:
+                raise ValueError(f"workspace must hold at least {nbytes} bytes")
+            check(self._lib.eagle_decoder_layer_kv4(
+                ctypes.byref(self.w), cache._ref, B, n, _ptr(x), _ptr(positions), _ptr(mask), _ptr(out), _ptr(kn),
+                _ptr(vn), _ptr(workspace), nbytes, cache._status.data_ptr(), _stream(x.device, stream)),
+                "eagle_decoder_layer_kv4")
         return (out, kn, vn) if new_kv else out

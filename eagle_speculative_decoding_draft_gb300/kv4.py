@@ -1,0 +1,215 @@
+"""A key/value cache in 4 bits: argument marshalling over the eagle_kv4_* entry points of the C ABI.
+
+One round of drafting with it: the decoder layer attends over the cache (``DecoderLayer.kv4``, or
+``KV4Cache.attention`` alone) and hands out the keys and values of the tree's nodes; the verify names
+the accepted nodes; ``KV4Cache.append`` quantises those nodes' rows into the cache.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+
+import torch
+
+from . import _lib
+from ._lib import check
+from .engine import _dtype_code, _need, _ptr, _stream
+
+
+def _here(t, name, device, dtype=None):
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the cache on {device}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    return t
+
+
+def _ints(t, name, device, shape):
+    """A contiguous int32 tensor of this shape, or None."""
+    if t is None:
+        return None
+    _need(_here(t, name, device, torch.int32), name)
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    return t
+
+
+def _row_step(t, name):
+    """Elements between the rows of a [B][n][heads][D] tensor whose rows are packed (a contiguous
+    tensor, or a slice of wider rows such as a projection's output)."""
+    B, n, h, D = t.shape
+    row = h * D
+    if t.stride(3) != 1 or (h > 1 and t.stride(2) != D):
+        raise ValueError(f"{name}: a row's heads must be packed")
+    step = t.stride(1) if n > 1 else (t.stride(0) if B > 1 else row)
+    if n > 1 and B > 1 and t.stride(0) != n * step:
+        raise ValueError(f"{name}: rows of all requests must be evenly spaced")
+    if step < row or step % 8:
+        raise ValueError(f"{name}: rows must be a multiple of 8 elements apart and not overlap")
+    return step
+
+
+class KV4Cache:
+    """A paged 4-bit cache of `batch` requests (see eagle_kv4_cache in include/eagle_tree.h).
+
+    table [batch][max_pages] int32 and lengths [batch] int32 are the cache's own tensors: a scheduler
+    writes page numbers into `table` (it starts as pages 0, 1, 2, ... dealt out request by request
+    where the pool is large enough, else as -1) and may set `lengths` (they start as 0).  page_size is
+    a power of two of at least 16; head_dim 32, 64, 96 or 128."""
+
+    def __init__(self, batch: int, kv_heads: int, head_dim: int, num_pages: int, max_pages: int,
+                 page_size: int = 64, device=None, pages=None):
+        self._lib = _lib.load()
+        self.device = torch.device("cuda" if device is None else device)
+        if self.device.type != "cuda":
+            raise ValueError("a KV4Cache lives on a CUDA device")
+        if self.device.index is None:
+            self.device = torch.device("cuda", torch.cuda.current_device())
+        self.batch, self.kv_heads, self.head_dim = batch, kv_heads, head_dim
+        self.page_size, self.num_pages, self.max_pages = page_size, num_pages, max_pages
+        self._c = _lib.KV4CacheStruct(kv_heads, head_dim, page_size, num_pages, max_pages, None, None, None)
+        self._ref = ctypes.byref(self._c)
+        nbytes = self._lib.eagle_kv4_pages_bytes(self._ref)
+        if nbytes == 0 or batch < 0:
+            raise ValueError("unusable 4-bit cache sizes")
+        if pages is None:
+            pages = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+        elif _need(_here(pages, "pages", self.device, torch.uint8), "pages").numel() < nbytes:
+            raise ValueError(f"pages must hold at least {nbytes} bytes")
+        self._pages = pages
+        if num_pages >= batch * max_pages:
+            self._table = torch.arange(batch * max_pages, dtype=torch.int32, device=self.device).view(batch, max_pages)
+        else:
+            self._table = torch.full((batch, max_pages), -1, dtype=torch.int32, device=self.device)
+        self._lengths = torch.zeros(batch, dtype=torch.int32, device=self.device)
+        self._status = torch.zeros(1, dtype=torch.int32, device=self.device)
+        self._c.pages, self._c.table, self._c.lengths = pages.data_ptr(), self._table.data_ptr(), self._lengths.data_ptr()
+        self._ws_bytes = {}
+
+    pages = property(lambda self: self._pages, doc="The page pool, uint8.")
+    table = property(lambda self: self._table, doc="Pages of each request, [batch][max_pages] int32.")
+    lengths = property(lambda self: self._lengths, doc="Positions held, [batch] int32.")
+    capacity = property(lambda self: self.max_pages * self.page_size, doc="Positions a request can hold.")
+
+    def _on(self, stream):
+        """Makes the cache's device current, and `stream` where one is given, so that what is
+        allocated belongs to the stream that uses it."""
+        if stream is not None:
+            return torch.cuda.stream(stream)
+        if torch.cuda.current_device() != self.device.index:
+            return torch.cuda.device(self.device)
+        return contextlib.nullcontext()
+
+    def _kv(self, k, v):
+        for t, name in ((k, "k"), (v, "v")):
+            _here(t, name, self.device, torch.bfloat16)
+            if t.dim() != 4 or t.shape[0] != self.batch or tuple(t.shape[2:]) != (self.kv_heads, self.head_dim):
+                raise ValueError(f"{name} must be [{self.batch}][rows][{self.kv_heads}][{self.head_dim}]")
+        if k.shape != v.shape:
+            raise ValueError("k and v must have the same shape")
+        if k.shape[1] == 0:
+            return k.shape[2] * k.shape[3]
+        ld = _row_step(k, "k")
+        if _row_step(v, "v") != ld:
+            raise ValueError("k and v must have the same row spacing")
+        return ld
+
+    def append(self, k, v, select=None, count=None, start=None, stream=None):
+        """Quantises rows of k and v ([batch][rows][kv_heads][head_dim] bf16) into the cache, behind
+        each request's length or from start [batch] int32 on, and sets the lengths to the end of
+        what was written.  select [batch][slots] int32 names the row of each slot (negative: the slot
+        is not written), e.g. a verify's accept_nodes; count [batch] int32 is each request's number of
+        slots."""
+        ld = self._kv(k, v)
+        rows = k.shape[1]
+        slots = rows
+        if select is not None:
+            if select.dim() != 2:
+                raise ValueError("select must be [batch][slots]")
+            slots = select.shape[1]
+            _ints(select, "select", self.device, (self.batch, slots))
+        _ints(count, "count", self.device, (self.batch,))
+        _ints(start, "start", self.device, (self.batch,))
+        with self._on(stream):
+            check(self._lib.eagle_kv4_append(self._ref, self.batch, rows, slots, _ptr(k), _ptr(v), ld, _ptr(select),
+                                             _ptr(count), _ptr(start), self._status.data_ptr(),
+                                             _stream(self.device, stream)), "eagle_kv4_append")
+
+    def read(self, start=None, rows=None, dtype=torch.bfloat16, out=None, stream=None):
+        """The values that positions start[b] (default 0) .. + rows - 1 stand for: (k, v), each
+        [batch][rows][kv_heads][head_dim] of `dtype` (bf16 or fp32).  out = (k, v) receives them (its
+        shape gives rows); rows behind a request's length are left as they are (0 in fresh
+        tensors).  rows defaults to the capacity."""
+        _ints(start, "start", self.device, (self.batch,))
+        with self._on(stream):
+            if out is None:
+                rows = self.capacity if rows is None else rows
+                shape = (self.batch, rows, self.kv_heads, self.head_dim)
+                out = (torch.zeros(shape, dtype=dtype, device=self.device), torch.zeros(shape, dtype=dtype, device=self.device))
+            k, v = out
+            for t, name in ((k, "out[0]"), (v, "out[1]")):
+                _need(_here(t, name, self.device), name)
+                if t.dim() != 4 or t.shape[0] != self.batch or tuple(t.shape[2:]) != (self.kv_heads, self.head_dim):
+                    raise ValueError(f"{name} must be [{self.batch}][rows][{self.kv_heads}][{self.head_dim}]")
+            if k.shape != v.shape or k.dtype != v.dtype or (rows is not None and k.shape[1] != rows):
+                raise ValueError("the outputs must agree in shape and dtype")
+            check(self._lib.eagle_kv4_read(self._ref, self.batch, k.shape[1], _ptr(start), _ptr(k), _ptr(v),
+                                           _dtype_code(k.dtype), self._status.data_ptr(), _stream(self.device, stream)),
+                  "eagle_kv4_read")
+        return k, v
+
+    def attention_workspace_bytes(self, nodes: int, heads: int) -> int:
+        """Bytes of scratch that an attention call with these sizes needs."""
+        n = self._ws_bytes.get((nodes, heads))
+        if n is None:
+            with self._on(None):
+                n = self._lib.eagle_kv4_attention_workspace_bytes(self._ref, nodes, heads)
+            if n == 0:
+                raise ValueError(f"unusable attention sizes (nodes={nodes}, heads={heads})")
+            self._ws_bytes[(nodes, heads)] = n
+        return n
+
+    def attention(self, q, k=None, v=None, mask=None, out=None, workspace=None, stream=None):
+        """Attention of the nodes' queries q [batch][n][heads][head_dim] bf16 over each request's
+        cached positions and the nodes' new keys and values k, v [batch][n][kv_heads][head_dim]:
+        those that mask [batch][n][ceil(n / 32)] int32 marks, or without a mask the node's own and
+        the earlier ones.  Returns out [batch][n][heads][head_dim] bf16.  workspace: a uint8 tensor to
+        use instead of a fresh one; calls that may overlap need one each."""
+        _here(q, "q", self.device, torch.bfloat16)
+        if q.dim() != 4 or q.shape[0] != self.batch or q.shape[3] != self.head_dim or q.shape[1] < 1:
+            raise ValueError(f"q must be [{self.batch}][n][heads][{self.head_dim}]")
+        n, heads = q.shape[1], q.shape[2]
+        ldq, ldkv = _row_step(q, "q"), 0
+        if (k is None) != (v is None):
+            raise ValueError("k and v go together")
+        if k is not None:
+            ldkv = self._kv(k, v)
+            if k.shape[1] != n:
+                raise ValueError("k and v must have a row for each node")
+        elif mask is not None:
+            raise ValueError("a mask needs k and v")
+        _ints(mask, "mask", self.device, (self.batch, n, (n + 31) // 32))
+        nbytes = self.attention_workspace_bytes(n, heads)
+        with self._on(stream):
+            if out is None:
+                out = torch.empty(self.batch, n, heads, self.head_dim, dtype=torch.bfloat16, device=self.device)
+            elif _need(_here(out, "out", self.device, torch.bfloat16), "out").shape != q.shape:
+                raise ValueError("out must have the shape of q")
+            if workspace is None:
+                workspace = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+            elif _need(_here(workspace, "workspace", self.device, torch.uint8), "workspace").numel() < nbytes:
+                raise ValueError(f"workspace must hold at least {nbytes} bytes")
+            check(self._lib.eagle_kv4_attention(self._ref, self.batch, n, heads, _ptr(q), ldq, _ptr(k), _ptr(v), ldkv,
+                                                _ptr(mask), _ptr(out), _ptr(workspace), nbytes,
+                                                self._status.data_ptr(), _stream(self.device, stream)),
+                  "eagle_kv4_attention")
+        return out
+
+    def status(self, stream=None):
+        """Waits for `stream` (default: the current one), raises the first device error latched since
+        the last call (an index out of range, a wait that ran out) and clears it."""
+        with self._on(stream):
+            bits = int(self._status.item())
+            if bits:
+                self._status.zero_()
+        check(5 if bits & 1 else (6 if bits else 0), "KV4Cache.status")

@@ -501,6 +501,130 @@ EAGLE_API eagle_status eagle_decoder_layer(const eagle_decoder_layer_weights *w,
                                            size_t ws_bytes, eagle_stream_t stream);
 
 /*
+ * A key/value cache in 4 bits (no counterpart on the pages: they name the draft model's KV cache and
+ * give no layout or format).  Keys and values are quantised as they are written, per token, kv head
+ * and group of 32 neighbouring head dimensions.  With lo and hi the least and largest value of a
+ * group:  m = lo rounded down to fp16,  s = (hi - m) / 15 rounded up to fp16,
+ *   c = (x - m) / s rounded to the nearest whole number (ties to even) in 0..15 (0 where s = 0),
+ * and the group stands for m + s c, at most s / 2 from x: 4 bits a value and 32 bits a group, 0.31 of
+ * bf16.  A group that holds a NaN, an infinity or a magnitude above 32768 reads back as NaN.
+ *   kv_heads    1 .. 1024
+ *   head_dim    32, 64, 96 or 128
+ *   page_size   tokens of a page: a power of two, 16 .. 1024
+ *   num_pages   pages of the pool
+ *   max_pages   pages a request can have; max_pages * page_size <= 2^30 positions
+ *   pages       the pool, eagle_kv4_pages_bytes bytes, 16-byte aligned; a page holds page_size tokens
+ *               of all kv heads.  Its bytes are read and written only by the calls below (codes and
+ *               parameters lie in the order in which the attention takes them); whole pages may be
+ *               copied.  It needs no initial content.
+ *   table       [batch][max_pages] int32: the page of positions i * page_size .. of the request.
+ *               Entries of positions behind a request's length are not read.  An entry outside
+ *               [0, num_pages) where a position is needed latches EAGLE_ERR_DEVICE_BOUNDS: a write
+ *               skips the row, a read leaves it, the attention takes its keys as absent.  Requests
+ *               may share pages that none of them writes; a page that is written belongs to one
+ *               place of one request's table.
+ *   lengths     [batch] int32: positions held, written by eagle_kv4_append.  Values outside
+ *               [0, max_pages * page_size] are clamped and latch EAGLE_ERR_DEVICE_BOUNDS in the
+ *               attention.
+ * The calls take the arrays by device pointer and read table and lengths on the device, so captured
+ * graphs follow the lengths.  d_status is an int32 of the caller's that latches device errors (bit 0:
+ * a bounded wait ran out, bit 1: an index out of range), or NULL.
+ */
+typedef struct {
+    int32_t kv_heads, head_dim, page_size, num_pages, max_pages;
+    void *pages;
+    const int32_t *table;
+    int32_t *lengths;
+} eagle_kv4_cache;
+
+/* Bytes of the page pool (the pointers of `cache` are not looked at); 0 for sizes out of range. */
+EAGLE_API size_t eagle_kv4_pages_bytes(const eagle_kv4_cache *cache);
+
+/*
+ * Quantises rows of keys and values into the cache: slot j of request b goes to position start[b] + j.
+ *   d_k, d_v   [batch][src_rows] rows of kv_heads * head_dim bf16, ld elements apart (a multiple of
+ *              8); 16-byte aligned.  eagle_decoder_layer's k_new and v_new are such rows.
+ *   d_select   NULL: slot j is row j (slots <= src_rows); else [batch][slots], the row of each slot,
+ *              e.g. the accepted nodes of a verified tree.  A slot whose entry is negative is not
+ *              written (its position keeps what it holds), one whose entry is src_rows or more
+ *              neither, and latches EAGLE_ERR_DEVICE_BOUNDS.  A row may be selected more than once.
+ *   d_count    NULL: every request has `slots` slots; else [batch], clamped to [0, slots].
+ *   d_start    NULL: the request's length; else [batch] (may be cache->lengths), for rows that
+ *              replace what was drafted behind an earlier position.  A negative start latches
+ *              EAGLE_ERR_DEVICE_BOUNDS and leaves the request as it is.
+ * lengths[b] becomes start[b] plus the last written slot's number plus one (start[b] if there is
+ * none), at most the capacity; slots beyond the capacity latch EAGLE_ERR_DEVICE_BOUNDS.  Positions
+ * other than those written keep what they hold.  A request's slots are written by one launch; a
+ * second, small one sets the lengths when they are also the starts and a request needs several
+ * blocks.  d_start must not overlap cache->lengths other than being it.
+ * Errors: INVALID_ARG, CUDA.
+ */
+EAGLE_API eagle_status eagle_kv4_append(const eagle_kv4_cache *cache, int32_t batch, int32_t src_rows,
+                                        int32_t slots, const void *d_k, const void *d_v, int64_t ld,
+                                        const int32_t *d_select, const int32_t *d_count,
+                                        const int32_t *d_start, int32_t *d_status,
+                                        eagle_stream_t stream);
+
+/*
+ * Reads the cache back: row j of request b is position start[b] + j (d_start NULL: 0), as the values
+ * its codes stand for, rounded to `dtype` (EAGLE_F32 or EAGLE_BF16) from fp32.
+ *   d_k, d_v   [batch][rows][kv_heads][head_dim], 16-byte aligned.  Rows at or behind the request's
+ *              length are left as they are.
+ * Errors: INVALID_ARG, CUDA; a negative start latches EAGLE_ERR_DEVICE_BOUNDS and reads nothing.
+ */
+EAGLE_API eagle_status eagle_kv4_read(const eagle_kv4_cache *cache, int32_t batch, int32_t rows,
+                                      const int32_t *d_start, void *d_k, void *d_v, eagle_dtype dtype,
+                                      int32_t *d_status, eagle_stream_t stream);
+
+/*
+ * Attention of each request's nodes over its cached positions and the nodes' own new keys, the form
+ * of eagle_decoder_layer's tree attention for this cache (EAGLE notes ch. 04 §12.5: a node sees the
+ * cached context and its own ancestors):
+ *   o[b][i][h] = softmax_j(q . k_j / sqrt(head_dim)) v_j, query head h reading kv head
+ *   h / (heads / kv_heads), over all lengths[b] cached positions and the new keys that node i sees.
+ *   d_q     [batch][nodes] rows of heads * head_dim bf16, ldq elements apart (a multiple of 8)
+ *   d_k, d_v  [batch][nodes] rows of kv_heads * head_dim bf16, ldkv elements apart (a multiple of 8);
+ *             both NULL: the cached positions alone
+ *   d_mask  [batch][nodes][ceil(nodes / 32)]: bit t of row i set where node i sees node t (the tree
+ *           mask of eagle_rerank_build_tree); NULL: node i sees nodes 0..i (the next piece of a
+ *           prompt; nodes = 1 is a single token).  Without new keys it must be NULL.
+ *   d_out   [batch][nodes][heads][head_dim] bf16, rounded once from fp32
+ * A row that sees nothing gives 0.  What a masked key or value holds (NaN and infinities included)
+ * has no influence on the rows that do not see it.  nodes in [1, 4097]; heads a multiple of
+ * kv_heads, at most 65536, with nodes * heads / kv_heads <= 2^24.  Pointers are 16-byte aligned.
+ * d_ws: eagle_kv4_attention_workspace_bytes bytes, 256-byte aligned, of any content; calls that may
+ * run at the same time (other streams, graphs replayed side by side) need workspaces of their own.
+ * The size depends on the current device, not on the batch or the lengths.  Results do not depend on
+ * what else runs, and are the same in every call with the same lengths.
+ * Errors: INVALID_ARG, CUDA.
+ */
+EAGLE_API size_t eagle_kv4_attention_workspace_bytes(const eagle_kv4_cache *cache, int32_t nodes,
+                                                     int32_t heads);
+EAGLE_API eagle_status eagle_kv4_attention(const eagle_kv4_cache *cache, int32_t batch, int32_t nodes,
+                                           int32_t heads, const void *d_q, int64_t ldq,
+                                           const void *d_k, const void *d_v, int64_t ldkv,
+                                           const uint32_t *d_mask, void *d_out, void *d_ws,
+                                           size_t ws_bytes, int32_t *d_status, eagle_stream_t stream);
+
+/*
+ * The draft decoder layer over a 4-bit cache: eagle_decoder_layer with the cached keys and values
+ * read by eagle_kv4_attention, each request with its own length.  cache->kv_heads and head_dim must be
+ * the layer's; the other arguments, limits and rounding points are those of eagle_decoder_layer
+ * (d_mask NULL: node i sees nodes 0..i).  d_k_new / d_v_new are what eagle_kv4_append takes after the
+ * verify.  The layer does not write to the cache.
+ */
+EAGLE_API size_t eagle_decoder_layer_kv4_workspace_bytes(const eagle_decoder_layer_weights *w,
+                                                         const eagle_kv4_cache *cache, int32_t batch,
+                                                         int32_t nodes);
+EAGLE_API eagle_status eagle_decoder_layer_kv4(const eagle_decoder_layer_weights *w,
+                                               const eagle_kv4_cache *cache, int32_t batch,
+                                               int32_t nodes, const void *d_x,
+                                               const int32_t *d_positions, const uint32_t *d_mask,
+                                               void *d_out, void *d_k_new, void *d_v_new, void *d_ws,
+                                               size_t ws_bytes, int32_t *d_status,
+                                               eagle_stream_t stream);
+
+/*
  * The streamed-weight GEMM of eagle_linear_bf16 without caller-provided scratch.  The pages have
  * no counterpart: this is an engineering variant for callers that cannot allocate device memory
  * (code where cudaMalloc is not allowed or not wanted because it synchronises the device and can

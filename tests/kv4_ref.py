@@ -1,0 +1,91 @@
+"""The 4-bit cache's definition in 64 bits, written apart from the library: the values a bf16 row
+stands for once cached, attention over them, and how far the library's arithmetic may be off."""
+import math
+
+import torch
+
+
+def half_grid(x, up):
+    """x (fp64) to a multiple of its fp16 step, down or up (normal and subnormal)."""
+    e = torch.frexp(x).exponent.clamp(min=-13).long()  # |x| in [2^(e-1), 2^e)
+    step = ((e - 11 + 1023) << 52).view(torch.float64)
+    return (torch.ceil(x / step) if up else torch.floor(x / step)) * step
+
+
+def parts(x):
+    """(m, s, c) of bf16 rows [..., D]: m and s [..., D/32, 1], c [..., D/32, 32], all fp64."""
+    g = x.double().unflatten(-1, (-1, 32))
+    bad = ~((g.abs() <= 32768).all(-1, keepdim=True))
+    z = torch.where(bad, 0.0, g)
+    m = half_grid(z.amin(-1, keepdim=True), up=False)
+    s = half_grid((z.amax(-1, keepdim=True) - m) / 15, up=True)
+    c = torch.where(s > 0, torch.round((z - m) / torch.where(s > 0, s, 1.0)), 0.0).clamp(0, 15)
+    nan = torch.full_like(m, math.nan)
+    return torch.where(bad, nan, m), torch.where(bad, nan, s), c
+
+
+def stands_for(x):
+    m, s, c = parts(x)
+    return (m + s * c).flatten(-2)
+
+
+def size_of(x):
+    """|m| + s c: the terms whose roundings the value sums carry."""
+    m, s, c = parts(x)
+    return (m.abs() + s * c).flatten(-2)
+
+
+def sees(n, t, mask_row_bits, device):
+    """[n][t + n]: cached positions, then the new keys that mask bits mark (None: causal)."""
+    new = torch.ones(n, n, dtype=torch.bool, device=device).tril()
+    if mask_row_bits is not None:
+        j = torch.arange(n, device=device)
+        new = ((mask_row_bits[:, j // 32].long() >> (j % 32)) & 1).bool()
+    return torch.cat([torch.ones(n, t, dtype=torch.bool, device=device), new], 1)
+
+
+def attend(q, kc, vc, kn, vn, see):
+    """One request.  q [n][H][D]; kc, vc the bf16 rows that were cached [t][Hk][D]; kn, vn the new
+    rows [n][Hk][D] or None; see [n][t (+ n)].  Returns (o, tol) in fp64.
+
+    tol, from the library's arithmetic:
+      output rounding            2^-8 |o|                       (half a bf16 step)
+      p and p s to fp16          2 x 2^-11 of the sum of p (|m| + s c)   (half fp16 steps)
+      scores in fp32             a sum of D products and D / 32 + 2 more terms, each step at most
+                                 2^-22 (accumulation that truncates) of the sum of magnitudes A: the
+                                 exponent is off by delta = (D + 16) 2^-22 A at most, p relatively by
+                                 as much, numerator and denominator: 2 delta
+      exponentials               2^-21 relative each
+      fp16 range                 products below 2^-14 lose at most 2^-25 of a scale where the largest
+                                 p is 2^9 or more (2^0 where some s is 16 or more): 15 N 2^-34 or 2^-25
+    """
+    n, H, D = q.shape
+    Hk = kc.shape[1]
+    k, v, size, ksize = stands_for(kc), stands_for(vc), size_of(vc), size_of(kc)
+    steep = bool((parts(vc)[1] >= 16).any()) if vc.numel() else False
+    if kn is not None:
+        k, v = torch.cat([k, kn.double()]), torch.cat([v, vn.double()])
+        size, ksize = torch.cat([size, vn.double().abs()]), torch.cat([ksize, kn.double().abs()])
+    if k.shape[0] == 0:
+        return torch.zeros_like(q, dtype=torch.float64), torch.zeros_like(q, dtype=torch.float64)
+    rep = H // Hk
+    kh, vh = k.repeat_interleave(rep, 1), v.repeat_interleave(rep, 1)
+    z = torch.einsum("nhd,thd->hnt", q.double(), kh) / math.sqrt(D)
+    z = torch.nan_to_num(z, nan=0.0).masked_fill(~see, -math.inf)
+    m = z.amax(-1, keepdim=True)
+    p = torch.exp(z - torch.where(m == -math.inf, 0.0, m))
+    p = torch.where(see, p, 0.0)
+    total = p.sum(-1, keepdim=True)
+    p = torch.where(total == 0, 0.0, p / total)
+    seen_v = torch.where(see.any(0)[:, None, None], vh, 0.0)
+    o = torch.einsum("hnt,thd->nhd", p, torch.nan_to_num(seen_v, nan=0.0, posinf=0.0, neginf=0.0))
+    # a cached group that is NaN: its dims of every row that sees it (a key's: the whole row)
+    see_f = see.double()
+    o[torch.einsum("nt,thd->nhd", see_f, torch.isnan(vh).double()) > 0] = math.nan
+    o[torch.einsum("nt,th->nh", see_f, torch.isnan(kh).any(-1).double()) > 0] = math.nan
+    A = torch.einsum("nhd,thd->hnt", q.double().abs(), torch.nan_to_num(ksize.repeat_interleave(rep, 1))) / math.sqrt(D)
+    delta = (D + 16) * 2.0 ** -22 * torch.where(see, A, 0.0).amax(-1, keepdim=True)
+    mag = torch.einsum("hnt,thd->nhd", p * (2.0 ** -10 + 2.0 ** -19 + 2 * delta),
+                       torch.nan_to_num(size.repeat_interleave(rep, 1), posinf=0.0))
+    tol = 2.0 ** -8 * torch.nan_to_num(o).abs() * 1.001 + mag + 15 * k.shape[0] * (2.0 ** -25 if steep else 2.0 ** -34)
+    return o, tol

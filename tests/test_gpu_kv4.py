@@ -1,0 +1,541 @@
+"""The 4-bit key/value cache on the GPU: writing, reading back and attention, against the definition
+in 64 bits (kv4_ref.py, which also derives the tolerances)."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import kv4_ref as ref
+from decoder_ref import layer, random_tree, reference_layer, tolerance, tree_mask
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def dev():
+    assert torch.cuda.is_available()
+    return torch.device("cuda", 0)
+
+
+def rows(g, *shape, scale=0.8):
+    """Keys or values: normal, with an offset of each channel."""
+    x = torch.randn(*shape, generator=g, device="cuda") + torch.randn(shape[-2:], generator=g, device="cuda")
+    return (scale * x).to(torch.bfloat16)
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def make_cache(B, Hk, D, cap, page, seed=0, spare=2, fill=0xFF):
+    """A cache whose pages lie in random order in a pool full of 0xFF (NaN parameters: nothing may
+    depend on what no row was written to)."""
+    from eagle_speculative_decoding_draft_gb300 import KV4Cache
+    mp = max(1, -(-cap // page))
+    c = KV4Cache(B, Hk, D, num_pages=B * mp + spare, max_pages=mp, page_size=page)
+    c.pages.fill_(fill)
+    perm = torch.randperm(B * mp + spare, generator=gen(seed), device="cuda")[:B * mp]
+    c.table.copy_(perm.view(B, mp))
+    return c
+
+
+def i32(x):
+    return torch.as_tensor(x, dtype=torch.int32, device="cuda")
+
+
+# ------------------------------------------------------------------------------------------------
+# writing and reading back
+# ------------------------------------------------------------------------------------------------
+WRITES = [
+    # B, Hk, D, page, rows, starts
+    (1, 1, 32, 16, 1, [0]),
+    (2, 3, 64, 16, 5, [0, 13]),
+    (3, 2, 96, 32, 77, [0, 31, 100]),
+    (2, 8, 128, 64, 200, [63, 1]),
+    (5, 32, 128, 128, 9, [0, 5, 127, 128, 300]),
+    (1, 1, 128, 1024, 1500, [1]),
+]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("case", WRITES, ids=lambda c: "B%d_Hk%d_D%d_page%d_rows%d" % c[:5])
+def test_rows_written_read_back_as_their_values(dev, case, dtype):
+    B, Hk, D, page, n, starts = case
+    g = gen(1)
+    c = make_cache(B, Hk, D, max(starts) + n, page)
+    k, v = rows(g, B, n, Hk, D), rows(g, B, n, Hk, D, scale=0.01)
+    c.append(k, v, start=i32(starts))
+    assert c.lengths.tolist() == [s + n for s in starts]
+    gk, gv = c.read(start=i32(starts), rows=n, dtype=dtype)
+    c.status()
+    half = 2.0 ** -24 if dtype == torch.float32 else 2.0 ** -8 + 2.0 ** -24
+    for got, x in ((gk, k), (gv, v)):
+        want = ref.stands_for(x)
+        assert torch.all((got.double() - want).abs() <= half * want.abs())
+        step = ref.parts(x)[1].expand(-1, -1, -1, -1, 32).flatten(-2)
+        assert torch.all((want - x.double()).abs() <= step / 2 * (1 + 1e-12))  # at most half a step from x
+
+
+def test_writes_touch_their_positions_only_and_follow_the_lengths(dev):
+    """Three writes one behind the other (the second of them empty for one request), then a rewrite
+    from an earlier position: earlier rows keep their values, the lengths follow."""
+    g = gen(2)
+    B, Hk, D = 3, 2, 64
+    c = make_cache(B, Hk, D, 200, 16)
+    want = [torch.zeros(0, Hk, D, dtype=torch.bfloat16, device="cuda") for _ in range(B)]
+    for counts in ([37, 1, 20], [5, 0, 64], [50, 3, 16]):
+        k = rows(g, B, 64, Hk, D)
+        c.append(k, k, count=i32(counts))
+        want = [torch.cat([w, k[b, :m]]) for b, (w, m) in enumerate(zip(want, counts))]
+    k = rows(g, B, 7, Hk, D)
+    back = [30, 2, 99]
+    c.append(k, k, start=i32(back))
+    want = [torch.cat([w[:s], k[b]]) for b, (w, s) in enumerate(zip(want, back))]
+    assert c.lengths.tolist() == [len(w) for w in want]
+    got, _ = c.read(rows=200, dtype=torch.float32)
+    c.status()
+    for b in range(B):
+        m = len(want[b])
+        assert torch.equal(got[b, :m], ref.stands_for(want[b]).float())
+        assert torch.all(got[b, m:] == 0)
+
+
+def test_long_write_without_starts_sets_the_lengths_behind_all_blocks(dev):
+    """Many blocks a request that all read their start from the lengths they end up changing."""
+    g = gen(3)
+    B, Hk, D, n = 2, 8, 128, 1000
+    c = make_cache(B, Hk, D, 2100, 64)
+    k, v = rows(g, B, n, Hk, D), rows(g, B, n, Hk, D)
+    c.append(k, v)
+    c.append(v, k, count=i32([1000, 17]))
+    assert c.lengths.tolist() == [2000, 1017]
+    gk, gv = c.read(rows=2100, dtype=torch.float32)
+    for b, m in ((0, 1000), (1, 17)):
+        assert torch.equal(gk[b, :1000 + m], ref.stands_for(torch.cat([k[b], v[b, :m]])).float())
+        assert torch.equal(gv[b, :1000 + m], ref.stands_for(torch.cat([v[b], k[b, :m]])).float())
+
+
+def test_selected_rows(dev):
+    """Slots name their rows: padding is skipped, a row may come twice, a row that is not there
+    latches an error and leaves its position."""
+    from eagle_speculative_decoding_draft_gb300._lib import EagleError
+    g = gen(4)
+    B, n, Hk, D = 4, 9, 2, 128
+    c = make_cache(B, Hk, D, 64, 16)
+    first = rows(g, B, 20, Hk, D)
+    c.append(first, first)
+    k = rows(g, B, n, Hk, D)
+    sel = [[0, 3, 7, -1, -1], [0, 0, 8, 1, 2], [-1, -1, -1, -1, -1], [4, -1, 5, -1, 6]]
+    c.append(k, k, select=i32(sel), count=i32([5, 4, 5, 3]))
+    c.status()
+    assert c.lengths.tolist() == [23, 24, 20, 23]
+    got, _ = c.read(rows=30, dtype=torch.float32)
+    for b, take in enumerate([[0, 3, 7], [0, 0, 8, 1], [], [4, None, 5]]):
+        assert torch.equal(got[b, :20], ref.stands_for(first[b]).float())
+        for j, r in enumerate(take):
+            if r is not None:
+                assert torch.equal(got[b, 20 + j], ref.stands_for(k[b, r]).float())
+    c.lengths.fill_(20)
+    c.append(k, k, select=i32([[0, 9, 1]] + [[0, 1, 2]] * 3))
+    with pytest.raises(EagleError, match="BOUNDS"):
+        c.status()
+    c.status()  # cleared
+
+
+def test_groups_that_hold_no_numbers_or_only_one(dev):
+    """NaN, infinities and magnitudes above 32768 make their own group NaN; constants, zeros, tiny and
+    subnormal values, and wide ranges keep the error bound."""
+    D = 128
+    x = torch.zeros(12, 1, D, dtype=torch.float32, device="cuda")
+    x[0, 0, 5] = math.nan
+    x[1, 0, 40] = math.inf
+    x[2, 0, 70] = -math.inf
+    x[3, 0, 100] = 33000.0
+    x[4] = 3.25
+    x[5] = -1e-30
+    x[6, 0] = torch.linspace(-32768, 32768, D)
+    x[7, 0] = torch.linspace(0, 1e-6, D)
+    x[8, 0] = torch.linspace(-1e-38, 1e-38, D)
+    x[9, 0] = 1000 + torch.linspace(0, 8, D)
+    x[10, 0, ::2] = -0.0
+    x[11, 0] = torch.linspace(-2.0 ** -14, 2.0 ** -15, D)
+    x = x.to(torch.bfloat16)[None]
+    c = make_cache(1, 1, D, 12, 16)
+    c.append(x, x)
+    for got in c.read(rows=12, dtype=torch.float32):
+        want = ref.stands_for(x)
+        bad = torch.isnan(want)
+        assert torch.equal(torch.isnan(got), bad) and int(bad.sum()) == 4 * 32
+        assert torch.all((got.double() - want).abs()[~bad] <= 2.0 ** -24 * want.abs()[~bad])
+        # each within half a step of x, and a step no larger than the range asks for
+        step = ref.parts(x)[1].expand(-1, -1, -1, -1, 32).flatten(-2)
+        assert torch.all(((got.double() - x.double()).abs() <= step / 2 * (1 + 1e-6) + 2.0 ** -24 * want.abs())[~bad])
+
+
+def test_bad_pages_and_positions_are_skipped_and_reported(dev):
+    from eagle_speculative_decoding_draft_gb300._lib import EagleError
+    g = gen(5)
+    c = make_cache(3, 1, 32, 64, 16)
+    k = rows(g, 3, 40, 1, 32)
+    c.table[1, 1] = -1
+    c.table[2, 0] = c.num_pages
+    c.append(k, k, start=i32([40, 0, 0]))  # request 0: 40 .. 79 of 64
+    with pytest.raises(EagleError, match="BOUNDS"):
+        c.status()
+    assert c.lengths.tolist() == [64, 40, 40]
+    out = torch.full((3, 64, 1, 32), 7.0, device="cuda")
+    got, _ = c.read(out=(out, out.clone()))
+    with pytest.raises(EagleError, match="BOUNDS"):
+        c.status()
+    assert torch.equal(got[0, 40:], ref.stands_for(k[0, :24]).float())
+    assert torch.equal(got[1, :16], ref.stands_for(k[1, :16]).float())
+    assert torch.all(got[1, 16:32] == 7.0) and torch.all(got[1, 40:] == 7.0) and torch.all(got[2, :16] == 7.0)
+    assert torch.equal(got[2, 16:40], ref.stands_for(k[2, 16:40]).float())
+    before = c.lengths.clone()
+    c.append(k, k, start=i32([-1, -5, -1]))
+    with pytest.raises(EagleError, match="BOUNDS"):
+        c.status()
+    assert torch.equal(c.lengths, before)
+
+
+def test_pool_beyond_32_bits(dev):
+    """Pages whose byte offsets pass 2^32, written, read and attended to."""
+    from eagle_speculative_decoding_draft_gb300 import KV4Cache
+    Hk, D, page = 8, 128, 64
+    num = (1 << 32) // (Hk * 4 * 640 * 4) + 40
+    c = KV4Cache(1, Hk, D, num_pages=num, max_pages=4, page_size=page)
+    assert c.pages.numel() > 1 << 32
+    c.table.copy_(i32([[num - 1, num - 3, 0, num - 2]]))
+    g = gen(6)
+    k, v = rows(g, 1, 250, Hk, D), rows(g, 1, 250, Hk, D)
+    c.append(k, v)
+    gk, gv = c.read(rows=250, dtype=torch.float32)
+    assert torch.equal(gk, ref.stands_for(k).float()) and torch.equal(gv, ref.stands_for(v).float())
+    q = rows(g, 1, 1, 16, D)
+    o = c.attention(q)
+    c.status()
+    want, tol = ref.attend(q[0], k[0], v[0], None, None, torch.ones(1, 250, dtype=torch.bool, device="cuda"))
+    assert torch.all((o[0].double() - want).abs() <= tol)
+
+
+# ------------------------------------------------------------------------------------------------
+# attention
+# ------------------------------------------------------------------------------------------------
+def build(case, seed=0, kscale=0.8, vscale=0.8, qscale=1.5):
+    B, n, H, Hk, D, page, lens, kind = case
+    g = gen(seed)
+    cap = max(max(lens), 1)
+    c = make_cache(B, Hk, D, cap, page, seed)
+    kc, vc = rows(g, B, cap, Hk, D, scale=kscale), rows(g, B, cap, Hk, D, scale=vscale)
+    c.append(kc, vc, count=i32(lens))  # nothing behind the lengths is ever written
+    q = (qscale * torch.randn(B, n, H, D, generator=g, device="cuda")).to(torch.bfloat16)
+    kn, vn = (rows(g, B, n, Hk, D, scale=kscale), rows(g, B, n, Hk, D, scale=vscale)) if kind != "cache" else (None, None)
+    mask = None
+    if kind == "tree":
+        rng = np.random.default_rng(seed)
+        mask = np.stack([tree_mask(random_tree(n, 8, rng)[0]) for _ in range(B)])
+        mask = torch.from_numpy(mask.view(np.int32)).cuda()
+    return c, kc, vc, q, kn, vn, mask
+
+
+def check_attention(case, made, o):
+    B, n, H, Hk, D, page, lens, kind = case
+    c, kc, vc, q, kn, vn, mask = made
+    assert o.shape == q.shape and o.dtype == torch.bfloat16
+    for b in range(B):
+        t = lens[b]
+        see = ref.sees(n, t, None if mask is None else mask[b], "cuda")
+        if kn is None:
+            see = see[:, :t]
+        want, tol = ref.attend(q[b], kc[b, :t], vc[b, :t], None if kn is None else kn[b], None if vn is None else vn[b], see)
+        assert torch.equal(torch.isnan(o[b]), torch.isnan(want))
+        err = torch.nan_to_num(o[b].double() - want).abs()
+        assert torch.all(err <= tol), (b, float((err - tol).max()), float(err.max()))
+
+
+ATTENTION = [
+    # B, n, H, Hk, D, page, lengths, new keys
+    (1, 1, 1, 1, 32, 16, [0], "causal"),            # a lone token and nothing cached
+    (1, 1, 1, 1, 128, 16, [1], "cache"),            # one cached key and no new ones
+    (2, 1, 4, 4, 128, 64, [0, 5], "cache"),         # a request that sees nothing
+    (3, 1, 32, 32, 128, 64, [1024, 1, 63], "causal"),
+    (2, 5, 8, 8, 64, 16, [64, 129], "tree"),
+    (4, 8, 8, 8, 128, 32, [0, 15, 16, 700], "tree"),
+    (2, 7, 12, 4, 64, 32, [3001, 0], "tree"),        # groups of 3: 21 rows
+    (2, 16, 2, 2, 128, 128, [250, 1], "tree"),       # 16 rows
+    (3, 11, 6, 2, 96, 16, [100, 33, 1], "tree"),     # head_dim 96, 33 rows
+    (2, 40, 3, 1, 32, 64, [70, 200], "tree"),        # head_dim 32, 120 rows, two mask words
+    (1, 61, 4, 4, 128, 64, [1024], "tree"),
+    (2, 65, 8, 2, 128, 64, [1024, 77], "tree"),      # 260 rows: two full tiles and 4 rows
+    (2, 65, 8, 2, 64, 16, [130, 600], "tree"),
+    (1, 130, 8, 8, 128, 64, [511], "causal"),        # more new keys than a tile
+    (2, 200, 16, 2, 128, 256, [0, 1000], "causal"),
+    (2, 129, 4, 4, 96, 16, [50, 0], "causal"),
+    (1, 33, 8, 1, 64, 32, [64], "cache"),            # MQA, 264 rows, no new keys
+    (9, 1, 64, 8, 128, 16, [1, 20000, 3, 0, 511, 4097, 9000, 64, 65], "causal"),  # ragged: split units
+    (1, 1, 8, 8, 128, 64, [50000], "causal"),
+    (1, 70, 32, 4, 128, 64, [9000], "tree"),         # 560 rows, split units of many rows
+    (300, 1, 2, 1, 64, 16, [i % 37 for i in range(300)], "causal"),  # more requests than threads
+]
+
+
+@pytest.mark.parametrize("case", ATTENTION, ids=lambda c: "B%d_n%d_H%d_Hk%d_D%d_page%d_%s" % (*c[:6], c[7]))
+def test_attention_matches_the_definition(dev, case):
+    made = build(case)
+    c, _, _, q, kn, vn, mask = made
+    o = c.attention(q, kn, vn, mask=mask)
+    c.status()
+    check_attention(case, made, o)
+    again = c.attention(q, kn, vn, mask=mask)
+    assert torch.equal(o, again)  # bit for bit
+
+
+@pytest.mark.parametrize("kscale,vscale,qscale", [(0.8, 60.0, 1.5), (4.0, 1e-3, 4.0), (0.8, 8000.0, 1.5), (1e-3, 1e-5, 1e3),
+                                                  (0.8, 0.8, 1e-30), (0.02, 0.8, 1e30)])
+@pytest.mark.parametrize("case", [(2, 8, 4, 4, 128, 32, [700, 33], "tree"), (2, 65, 8, 2, 128, 64, [300, 1], "tree"),
+                                  (1, 20, 3, 3, 64, 64, [1000], "causal")], ids=["8rows", "260rows", "20rows"])
+def test_attention_over_values_of_other_sizes(dev, case, kscale, vscale, qscale):
+    made = build(case, 3, kscale, vscale, qscale)
+    c, _, _, q, kn, vn, mask = made
+    if qscale == 1e30:  # scores near 1e28: one key takes all; the definition is the arg-max's value
+        q.zero_()
+        q[..., 0] = 1e30
+        q[..., 3] = 1e29
+    o = c.attention(q, kn, vn, mask=mask)
+    check_attention(case, made, o)
+
+
+@pytest.mark.parametrize("case", [(2, 9, 4, 4, 128, 32, [70, 0], "tree"), (1, 65, 8, 2, 64, 64, [100], "tree"),
+                                  (2, 40, 8, 1, 128, 16, [0, 257], "tree")], ids=["9rows", "260rows", "320rows"])
+@pytest.mark.parametrize("what", [math.nan, math.inf, -math.inf, 3e38])
+def test_what_hidden_keys_hold_has_no_influence(dev, case, what):
+    """A leaf that no other node sees: its key and value may hold anything."""
+    made = build(case, 4)
+    c, kc, vc, q, kn, vn, mask = made
+    B, n = q.shape[:2]
+    hidden = n - 1  # the last node is no one's ancestor
+    clean = c.attention(q, kn, vn, mask=mask)
+    kn[:, hidden] = what
+    vn[:, hidden, :, 3::5] = what
+    dirty = c.attention(q, kn, vn, mask=mask)
+    assert torch.equal(clean[:, :hidden], dirty[:, :hidden])
+    if not math.isfinite(what):
+        assert torch.all(~torch.isfinite(dirty[:, hidden, :, 3]))
+
+
+@pytest.mark.parametrize("n,H", [(5, 2), (5, 64)], ids=["5rows", "160rows"])
+def test_infinite_values_reach_the_rows_that_see_them(dev, n, H):
+    case = (1, n, H, 2, 128, 16, [40], "causal")
+    made = build(case, 5)
+    c, kc, vc, q, kn, vn, mask = made
+    clean = c.attention(q, kn, vn)
+    vn[0, 2, :, 7] = math.inf
+    vn[0, 3, :, 9] = math.nan
+    vn[0, 4, :, 7] = -math.inf
+    o = c.attention(q, kn, vn)[0]
+    assert torch.equal(o[:2], clean[0, :2])
+    assert torch.all(o[2:4, :, 7] == math.inf) and torch.all(torch.isnan(o[4, :, 7]))
+    assert torch.all(torch.isnan(o[3:, :, 9])) and torch.all(torch.isfinite(o[2, :, 9]))
+    rest = [d for d in range(128) if d not in (7, 9)]
+    assert torch.equal(o[:, :, rest], clean[0][:, :, rest])
+
+
+@pytest.mark.parametrize("n,H", [(1, 2), (40, 8)], ids=["1row", "160rows"])
+def test_cached_groups_without_numbers_reach_their_dims_only(dev, n, H):
+    """A cached value group that is NaN makes its 32 dims NaN for every row, a key group every dim."""
+    case = (1, n, H, 2, 128, 16, [200], "causal")
+    c, kc, vc, q, kn, vn, mask = made = build(case, 6)
+    vc[0, 150, 0, 70] = math.nan  # kv head 0, dims 64 .. 95
+    c.append(kc, vc, start=i32([0]))
+    o = c.attention(q, kn, vn)[0]
+    per = H // 2
+    assert torch.all(torch.isnan(o[:, :per, 64:96]))
+    assert torch.all(torch.isfinite(o[:, :per, :64])) and torch.all(torch.isfinite(o[:, :per, 96:]))
+    assert torch.all(torch.isfinite(o[:, per:]))
+    kc[0, 199, 1, 0] = math.inf
+    c.append(kc, vc, start=i32([0]))
+    o = c.attention(q, kn, vn)[0]
+    assert torch.all(torch.isnan(o[:, per:]))
+
+
+@pytest.mark.parametrize("n,Hq", [(4, 1), (30, 2), (50, 4)])
+def test_rows_that_see_nothing_are_zero(dev, n, Hq):
+    """Empty mask rows over an empty cache; rows with a key beside them keep their values."""
+    case = (2, n, Hq, 1, 128, 16, [0, 9], "tree")
+    c, kc, vc, q, kn, vn, mask = made = build(case, 7)
+    mask[:, 1::2] = 0
+    o = c.attention(q, kn, vn, mask=mask)
+    assert torch.all(o[0, 1::2] == 0)
+    check_attention(case, made, o)
+
+
+@pytest.mark.parametrize("n,H,Hk", [(1, 4, 2), (9, 4, 2), (70, 8, 2)])
+def test_attention_on_slices_of_wider_rows(dev, n, H, Hk):
+    """q, k and v as parts of one projection's rows, as the decoder layer passes them."""
+    D = 64
+    case = (2, n, H, Hk, D, 32, [100, 41], "causal")
+    c, kc, vc, q, kn, vn, mask = build(case, 8)
+    want = c.attention(q, kn, vn)
+    wide = torch.full((2, n, (H + 2 * Hk) * D + 24), math.nan, dtype=torch.bfloat16, device="cuda")
+    wide[..., :H * D] = q.flatten(2)
+    wide[..., H * D:(H + Hk) * D] = kn.flatten(2)
+    wide[..., (H + Hk) * D:(H + 2 * Hk) * D] = vn.flatten(2)
+    view = lambda lo, h: wide[..., lo:lo + h * D].unflatten(2, (h, D))
+    got = c.attention(view(0, H), view(H * D, Hk), view((H + Hk) * D, Hk))
+    assert torch.equal(got, want)
+    c2 = make_cache(2, Hk, D, n, 16)
+    c2.append(view(H * D, Hk), view((H + Hk) * D, Hk))
+    assert torch.equal(c2.read(rows=n, dtype=torch.float32)[1], ref.stands_for(vn).float())
+
+
+def test_bad_pages_count_as_absent(dev):
+    from eagle_speculative_decoding_draft_gb300._lib import EagleError
+    case = (1, 3, 4, 2, 128, 16, [100], "causal")
+    c, kc, vc, q, kn, vn, mask = build(case, 9)
+    c.table[0, 2] = 1 << 20
+    o = c.attention(q, kn, vn)
+    with pytest.raises(EagleError, match="BOUNDS"):
+        c.status()
+    keep = [i for i in range(100) if not 32 <= i < 48]
+    see = ref.sees(3, len(keep), None, "cuda")
+    want, tol = ref.attend(q[0], kc[0, keep], vc[0, keep], kn[0], vn[0], see)
+    assert torch.all((o[0].double() - want).abs() <= tol)
+
+
+@pytest.mark.parametrize("n,H", [(1, 8), (50, 8)], ids=["8rows", "400rows"])
+def test_captured_calls_follow_the_lengths_and_streams(dev, n, H):
+    """One graph of a write and the attention after it, replayed over growing lengths; and calls on a
+    side stream whose outputs and workspaces belong to it."""
+    B, Hk, D = 2, 1, 128
+    case = (B, n, H, Hk, D, 16, [600, 600], "causal")
+    c, kc, vc, q, kn, vn, _ = build(case, 10)
+    lens = [5, 90]
+    c.lengths.copy_(i32(lens))
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    c.append(kn, vn)  # warm up
+    c.attention(q, kn, vn)
+    c.lengths.copy_(i32(lens))
+    c.append(kc, vc, start=i32([0, 0]))
+    c.lengths.copy_(i32(lens))
+    with torch.cuda.graph(graph):
+        c.append(kn, vn)
+        o = c.attention(q)
+    have = [kc[b, :lens[b]] for b in range(B)]
+    have_v = [vc[b, :lens[b]] for b in range(B)]
+    for _ in range(3):
+        graph.replay()
+        for b in range(B):
+            have[b], have_v[b] = torch.cat([have[b], kn[b]]), torch.cat([have_v[b], vn[b]])
+            want, tol = ref.attend(q[b], have[b], have_v[b], None, None,
+                                   torch.ones(n, len(have[b]), dtype=torch.bool, device="cuda"))
+            assert torch.all((o[b].double() - want).abs() <= tol)
+    want = c.attention(q)
+    side.wait_stream(torch.cuda.current_stream())
+    got = [c.attention(q, stream=side) for _ in range(4)]
+    torch.cuda.current_stream().wait_stream(side)
+    assert all(torch.equal(g, want) for g in got)
+
+
+def test_two_graphs_side_by_side(dev):
+    """Two captured calls over one cache, replayed on two streams: each graph holds its own
+    workspace."""
+    case = (4, 6, 16, 4, 128, 32, [3000, 1, 700, 50], "tree")
+    c, kc, vc, q, kn, vn, mask = build(case, 11)
+    want = c.attention(q, kn, vn, mask=mask), c.attention(kn, vn, kn)
+    graphs, outs, streams = [], [], [torch.cuda.Stream(), torch.cuda.Stream()]
+    for args, kw in (((q, kn, vn), dict(mask=mask)), ((kn, vn, kn), {})):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(c.attention(*args, **kw))
+        graphs.append(g)
+    for _ in range(20):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1])
+
+
+# ------------------------------------------------------------------------------------------------
+# the decoder layer and a round of drafting
+# ------------------------------------------------------------------------------------------------
+LAYERS = [
+    # B, n, P, h, H, Hk, D, I
+    (2, 9, 37, 256, 4, 2, 64, 512),
+    (1, 1, 0, 128, 2, 2, 128, 256),
+    (3, 40, 70, 192, 3, 1, 32, 320),
+    (2, 33, 150, 256, 8, 2, 128, 512),
+]
+
+
+@pytest.mark.parametrize("case", LAYERS, ids=lambda c: "B%d_n%d_P%d_h%d_H%d_Hk%d_D%d" % c[:7])
+def test_decoder_layer_over_the_cache(dev, case):
+    """Against the layer's 64-bit restatement over the values that the cache stands for, within the
+    bound of the layer over bf16 caches; the new keys and values are that layer's, bit for bit."""
+    from eagle_speculative_decoding_draft_gb300.engine import DecoderLayer
+    B, n, P, h, H, Hk, D, I = case
+    w, d = layer(B=B, n=n, P=P, h=h, H=H, Hk=Hk, D=D, I=I, seed=1)
+    rng = np.random.default_rng(1)
+    parents, depths = random_tree(n, 5, rng)
+    mask = np.broadcast_to(tree_mask(parents), (B, n, (n + 31) // 32)).copy()
+    pos = np.broadcast_to(np.asarray(depths) + P, (B, n)).astype(np.int32).copy()
+    g = lambda t: t.to(dev).contiguous()
+    lay = DecoderLayer(g(w["w_qkv"]), g(w["w_o"]), g(w["w_norm"]), g(w["w_gu"]), g(w["w_d"]), H, Hk)
+    c = make_cache(B, Hk, D, max(P, 1), 16)
+    if P:
+        c.append(g(w["k_cache"]), g(w["v_cache"]))
+    mask_d, pos_d = torch.from_numpy(mask.view(np.int32)).to(dev), torch.from_numpy(pos).to(dev)
+    out, kn, vn = lay.kv4(g(w["x"]), c, pos_d, mask_d, new_kv=True)
+    c.status()
+    held = dict(w, k_cache=ref.stands_for(w["k_cache"]), v_cache=ref.stands_for(w["v_cache"])) if P else w
+    want, h1, absterms = reference_layer(held, d, parents, pos)
+    assert np.all(np.abs(out.double().cpu().numpy() - want) <= tolerance(h1, want, absterms))
+    _, kb, vb = lay(g(w["x"]), g(w["k_cache"]) if P else None, g(w["v_cache"]) if P else None, pos_d, mask_d, new_kv=True)
+    assert torch.equal(kn, kb) and torch.equal(vn, vb)
+    assert torch.equal(lay.kv4(g(w["x"]), c, pos_d, mask_d), out)
+
+
+def test_rounds_of_drafting_over_the_cache(dev):
+    """Three rounds as an engine makes them: the layer over the cache and a tree, a verify of that
+    tree, and the accepted nodes' rows into the cache.  After each round the cache holds the accepted
+    rows behind the earlier ones, and the layer's output follows the definition over them."""
+    from eagle_speculative_decoding_draft_gb300.engine import DecoderLayer, verify_walk
+    B, n, h, H, Hk, D, I, depth = 3, 12, 256, 8, 2, 64, 512, 4
+    w, d = layer(B=B, n=n, P=20, h=h, H=H, Hk=Hk, D=D, I=I, seed=2)
+    g = lambda t: t.to(dev).contiguous()
+    lay = DecoderLayer(g(w["w_qkv"]), g(w["w_o"]), g(w["w_norm"]), g(w["w_gu"]), g(w["w_d"]), H, Hk)
+    c = make_cache(B, Hk, D, 64, 16)
+    prompt = [20, 3, 11]
+    c.append(g(w["k_cache"]), g(w["v_cache"]), count=i32(prompt))
+    held_k = [w["k_cache"][b, :t] for b, t in enumerate(prompt)]
+    held_v = [w["v_cache"][b, :t] for b, t in enumerate(prompt)]
+    rng = np.random.default_rng(3)
+    for rnd in range(3):
+        parents, depths = random_tree(n, depth, rng)
+        tokens = np.tile(np.arange(n, dtype=np.int32), (B, 1))
+        par = np.tile(np.asarray(parents, np.int32), (B, 1))
+        want_child = rng.integers(0, n, size=(B, n)).astype(np.int32)  # the target's token at each node
+        mask = np.broadcast_to(tree_mask(parents), (B, n, 1)).copy()
+        lens = c.lengths.tolist()
+        pos = np.stack([np.asarray(depths) + t for t in lens]).astype(np.int32)
+        x = torch.randn(B, n, h, generator=torch.Generator().manual_seed(rnd)).to(torch.bfloat16)
+        out, kn, vn = lay.kv4(g(x), c, torch.from_numpy(pos).to(dev), torch.from_numpy(mask.view(np.int32)).to(dev), new_kv=True)
+        for b in range(B):
+            one = dict(w, x=x[b:b + 1], k_cache=ref.stands_for(held_k[b])[None], v_cache=ref.stands_for(held_v[b])[None])
+            want, h1, absterms = reference_layer(one, dict(d, B=1, P=lens[b]), parents, pos[b:b + 1])
+            assert np.all(np.abs(out[b].double().cpu().numpy() - want[0]) <= tolerance(h1, want, absterms)[0])
+        ver = verify_walk(i32(tokens), i32(par), i32(want_child), depth)
+        c.append(kn, vn, select=ver["accept_nodes"])
+        c.status()
+        acc = (ver["accept_len"] + 1).tolist()
+        assert c.lengths.tolist() == [t + a for t, a in zip(lens, acc)]
+        got_k, got_v = c.read(rows=64, dtype=torch.float32)
+        for b in range(B):
+            path = ver["accept_nodes"][b, :acc[b]].long().cpu()
+            held_k[b] = torch.cat([held_k[b], kn[b].cpu()[path]])
+            held_v[b] = torch.cat([held_v[b], vn[b].cpu()[path]])
+            m = len(held_k[b])
+            assert torch.equal(got_k[b, :m].cpu(), ref.stands_for(held_k[b]).float())
+            assert torch.equal(got_v[b, :m].cpu(), ref.stands_for(held_v[b]).float())
