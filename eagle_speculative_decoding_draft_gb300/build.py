@@ -21,7 +21,7 @@ LIB = OUT_DIR / "libeagle_tree.so"
 CHECKS_DIR = OUT_DIR / "checks"
 CHECKS_LIB = CHECKS_DIR / "libeagle_tree.so"
 SOURCES = ["api.cu", "gemm.cu", "topk.cu", "tree.cu", "sample.cu", "noalloc.cu", "decoder.cu",
-           "kv4_cache.cu", "kv4_attn.cu"]
+           "kv4_cache.cu", "kv4_attn.cu", "kv4_attn_tc.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -25,16 +25,12 @@
 // Scores are formed transposed (16 keys on the MMA's M side, 8 query rows on N), so few query rows
 // waste no MMA rows, and the accumulators turn into the value product's operand by movmatrix.
 //
-// Work split.  A unit is (request, kv head, tile of query rows); its keys come in tiles of 64: new
-// keys first, then cached ones.  All units' tiles, in order, form one line that the CTAs cut evenly,
-// whatever the requests' lengths; the line is laid out on the device from the lengths, so the host
-// needs none of them.  A unit that more than one CTA works on is merged by a second kernel from
-// partial sums in the workspace: each CTA leaves at most two.
+// kv4_line.cuh: how the work is split.  kv4_attn_tc.cu: the kernel for many query rows.
 #include <algorithm>
 #include <mutex>
 
 #include "kernels.cuh"
-#include "kv4.cuh"
+#include "kv4_line.cuh"
 
 namespace eagle {
 namespace {
@@ -45,23 +41,6 @@ constexpr int kThreads = kWarps * 32 + 32;  // and one that copies
 constexpr int kStages = 4;
 constexpr int kMinTiles = 2;    // tiles a CTA takes at least
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr uint32_t kFull = 0xffffffffu;
-
-// What each CTA of the attention kernel leaves for the merge: the unit that it continues (begun by
-// an earlier CTA) if it is the first to do so, and the CTAs first..last that share it.
-struct Kv4Share {
-    int32_t b, hk, qt;       // b < 0: nothing to merge here
-    int32_t first, last, first_slot;
-};
-
-struct Kv4Args {
-    Kv4Attention a;
-    int32_t group, Mq, rows, QT, W;
-    float scale2;            // log2(e) / sqrt(D)
-    Kv4Share *share;         // [grid]
-    float2 *part_ml;         // [grid * 2][rows]: running maximum (base 2) and sum
-    float *part_o;           // [grid * 2][rows][D]
-};
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
@@ -85,179 +64,11 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-__device__ __forceinline__ uint32_t pack_b16(float lo, float hi) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t x, uint32_t y) {
     const __half2 r = __hmul2(*reinterpret_cast<const __half2 *>(&x), *reinterpret_cast<const __half2 *>(&y));
     return *reinterpret_cast<const uint32_t *>(&r);
 }
 __device__ __forceinline__ float low_f16(uint32_t x) { return __half2float(__ushort_as_half(static_cast<uint16_t>(x))); }
-__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
-
-// N 32-bit words at p, whose address is a multiple of 4 N bytes (N 1, 2 or 4) or of 4 (N 3).
-template <int N>
-__device__ __forceinline__ void load_words(const uint8_t *p, uint32_t (&w)[N]) {
-    if constexpr (N == 4) {
-        const uint4 v = *reinterpret_cast<const uint4 *>(p);
-        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-    } else if constexpr (N == 2) {
-        const uint2 v = *reinterpret_cast<const uint2 *>(p);
-        w[0] = v.x, w[1] = v.y;
-    } else {
-#pragma unroll
-        for (int i = 0; i < N; ++i) w[i] = reinterpret_cast<const uint32_t *>(p)[i];
-    }
-}
-
-// ---------------------------------------------------------------------------------------------
-// The line of tiles
-// ---------------------------------------------------------------------------------------------
-// Tiles of new keys that the rows of query tile qt need.
-__device__ __forceinline__ int32_t new_tiles(const Kv4Args &k, int32_t qt) {
-    if (!k.a.kn) return 0;
-    if (k.a.mask) return (k.a.n + kTile - 1) / kTile;
-    const int32_t last = min(k.a.n - 1, ((qt + 1) * k.rows - 1) / k.group);
-    return last / kTile + 1;
-}
-// Tiles of cached keys of request b; at least one where a unit would have none.
-__device__ __forceinline__ int64_t cached_tiles(const Kv4Args &k, int32_t b) {
-    const int64_t t = (kv4_length(k.a.cache, b) + kTile - 1) / kTile;
-    return t < 1 && !k.a.kn ? 1 : t;
-}
-
-// Where a CTA begins and ends, and the unit that its first tile belongs to.
-struct Place {
-    int64_t total, begin, end;  // tiles of the line
-    int64_t ctas;               // CTAs that share it
-    int32_t b, hk, qt;
-    int64_t off;                // the first tile's place in its unit
-};
-
-// Sum over the block; every thread gets it.  `red`: one slot a warp.
-__device__ int64_t block_sum64(int64_t v, int64_t *red) {
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(kFull, v, off);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-    __syncthreads();
-    int64_t t = 0;
-    for (int w = 0; w < static_cast<int>(blockDim.x) / 32; ++w) t += red[w];
-    return t;
-}
-
-// All threads of the block; the result is in *out after the last barrier.  Returns false when this
-// CTA has nothing to do.
-__device__ bool find_place(const Kv4Args &k, Place *out, int64_t *red) {
-    const int32_t tid = threadIdx.x, nt = blockDim.x, B = k.a.B;
-    const int64_t Hk = k.a.cache.Hk;
-    int64_t per = 0;  // tiles of new keys of one (request, kv head)
-    if (k.a.mask || !k.a.kn) {
-        per = static_cast<int64_t>(k.QT) * new_tiles(k, 0);
-    } else {
-        for (int32_t q = tid; q < k.QT; q += nt) per += new_tiles(k, q);
-        per = block_sum64(per, red);
-    }
-    int64_t mine = 0;
-    for (int32_t b = tid; b < B; b += nt) mine += Hk * (k.QT * cached_tiles(k, b) + per);
-    const int64_t total = block_sum64(mine, red);
-    const int64_t want = (total + kMinTiles - 1) / kMinTiles;
-    const int64_t ctas = want < gridDim.x ? (want < 1 ? 1 : want) : gridDim.x;
-    const int64_t c = blockIdx.x;
-    if (c >= ctas) return false;
-    const int64_t begin = c * total / ctas, end = (c + 1) * total / ctas;
-    // the request that holds tile `begin`
-    int64_t base = 0;
-    for (int32_t b0 = 0; b0 < B; b0 += nt) {
-        const int32_t b = b0 + tid;
-        const int64_t w = b < B ? Hk * (k.QT * cached_tiles(k, b) + per) : 0;
-        int64_t inc = w;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const int64_t o = __shfl_up_sync(kFull, inc, off);
-            if ((tid & 31) >= off) inc += o;
-        }
-        __syncthreads();
-        if ((tid & 31) == 31) red[tid >> 5] = inc;
-        __syncthreads();
-        int64_t before = base, all = base;
-        for (int w2 = 0; w2 < nt / 32; ++w2) {
-            if (w2 < (tid >> 5)) before += red[w2];
-            all += red[w2];
-        }
-        const int64_t lo = before + inc - w;
-        if (b < B && begin >= lo && begin < lo + w) {
-            int64_t off = begin - lo;
-            const int64_t ct = cached_tiles(k, b), block = k.QT * ct + per;
-            Place p;
-            p.total = total;
-            p.begin = begin;
-            p.end = end;
-            p.ctas = ctas;
-            p.b = b;
-            p.hk = static_cast<int32_t>(off / block);
-            off -= p.hk * block;
-            if (k.a.mask || !k.a.kn) {
-                const int64_t u = ct + new_tiles(k, 0);
-                p.qt = static_cast<int32_t>(off / u);
-                off -= p.qt * u;
-            } else {
-                p.qt = 0;
-                for (int64_t u; off >= (u = ct + new_tiles(k, p.qt)); ++p.qt) off -= u;
-            }
-            p.off = off;
-            *out = p;
-        }
-        base = all;
-        if (begin < base) break;
-    }
-    __syncthreads();
-    return true;
-}
-
-// A CTA's run through the line, unit by unit: [s0, s1) of the unit's tiles.
-struct Walk {
-    int32_t b, hk, qt;
-    int64_t t, s0, s1, unit;
-    int32_t nt;  // tiles of new keys (the unit's first)
-    int64_t len;
-
-    __device__ __forceinline__ void start(const Kv4Args &k, const Place &p) {
-        b = p.b;
-        hk = p.hk;
-        qt = p.qt;
-        t = p.begin;
-        s0 = p.off;
-        fill(k, p);
-    }
-    __device__ __forceinline__ void fill(const Kv4Args &k, const Place &p) {
-        nt = new_tiles(k, qt);
-        len = kv4_length(k.a.cache, b);
-        unit = cached_tiles(k, b) + nt;
-        s1 = min(unit, s0 + (p.end - t));
-    }
-    __device__ __forceinline__ bool next(const Kv4Args &k, const Place &p) {
-        t += s1 - s0;
-        if (t >= p.end) return false;
-        s0 = 0;
-        if (++qt == k.QT) {
-            qt = 0;
-            if (++hk == k.a.cache.Hk) {
-                hk = 0;
-                if (++b == k.a.B) return false;  // lengths changed under the call
-            }
-        }
-        fill(k, p);
-        return true;
-    }
-};
-
 // ---------------------------------------------------------------------------------------------
 // The kernel
 // ---------------------------------------------------------------------------------------------
@@ -305,17 +116,7 @@ __global__ void __launch_bounds__(kThreads, Shape<G, NQ>::kBlocks) kv4_attention
     volatile int32_t *abort_flag = &abort_mark;
     Walk w;
     w.start(k, p);
-    if (threadIdx.x == 0) {
-        Kv4Share sh{-1, 0, 0, 0, 0, 0};
-        if (w.s0 > 0) {
-            const int64_t u0 = p.begin - w.s0;  // the unit's first tile
-            const int64_t c0 = ((u0 + 1) * p.ctas - 1) / p.total, c1 = ((u0 + w.unit) * p.ctas - 1) / p.total;
-            if (c0 == static_cast<int64_t>(blockIdx.x) - 1)
-                sh = Kv4Share{w.b, w.hk, w.qt, static_cast<int32_t>(c0), static_cast<int32_t>(c1),
-                              c0 * p.total / p.ctas == u0 ? 0 : 1};
-        }
-        k.share[blockIdx.x] = sh;
-    }
+    if (threadIdx.x == 0) k.share[blockIdx.x] = share_of(k, p, w);
 
     if (warp == kWarps) {
         // ---------------- copies: a stage is up to four chunks of cached keys and values ----------
@@ -862,7 +663,7 @@ __global__ void __launch_bounds__(128) kv4_merge_kernel(const Kv4Args k) {
 struct Variant {
     int32_t rows, threads;
     size_t smem;
-    void (*kernel)(const Kv4Args);
+    void (*kernel)(const Kv4Args);  // null: the tcgen05 kernel
 };
 
 template <int G>
@@ -870,6 +671,7 @@ Variant variant_of(int32_t mq) {
     // query rows a unit takes: 8, 16 or 32
     if (mq <= 8) return Variant{8, kThreads, Shape<G, 1>::kTotal, kv4_attention_kernel<G, 1>};
     if (mq <= 16) return Variant{16, kThreads, Shape<G, 2>::kTotal, kv4_attention_kernel<G, 2>};
+    if (mq > 32 && (G == 2 || G == 4)) return Variant{kKv4TcRows, 0, 0, nullptr};
     return Variant{32, kThreads, Shape<G, 4>::kTotal, kv4_attention_kernel<G, 4>};
 }
 Variant variant(int32_t G, int32_t mq) {
@@ -906,11 +708,15 @@ const Device *device_now() {
                 return nullptr;
             d.blocks[g][i] = n;
         }
+    if (prepare_kv4_attention_tc() != cudaSuccess) return nullptr;
     d.sms = sms;
     return &d;
 }
 
-int32_t grid_of(const Device &d, int32_t G, const Variant &v) { return d.sms * d.blocks[G][v.rows == 8 ? 0 : (v.rows == 16 ? 1 : 2)]; }
+int32_t grid_of(const Device &d, int32_t G, const Variant &v) {
+    if (!v.kernel) return d.sms;
+    return d.sms * d.blocks[G][v.rows == 8 ? 0 : (v.rows == 16 ? 1 : 2)];
+}
 
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
@@ -936,6 +742,8 @@ cudaError_t launch_kv4_attention(const Kv4Attention &a, cudaStream_t st) {
     k.rows = v.rows;
     k.QT = (k.Mq + v.rows - 1) / v.rows;
     k.W = (a.n + 31) / 32;
+    k.tile = v.kernel ? kTile : kKv4TcTile;
+    k.min_tiles = v.kernel ? kMinTiles : 1;
     k.scale2 = kLog2e / sqrtf(static_cast<float>(G * kKv4Group));
     const int32_t full = grid_of(*d, G, v);
     uint8_t *ws = static_cast<uint8_t *>(a.ws);
@@ -946,12 +754,13 @@ cudaError_t launch_kv4_attention(const Kv4Attention &a, cudaStream_t st) {
     k.part_o = reinterpret_cast<float *>(ws);
     // no more CTAs than the longest possible line gives work to
     const int64_t units = static_cast<int64_t>(a.B) * a.cache.Hk * k.QT;
-    const int64_t tiles = (a.cache.cap + kTile - 1) / kTile + (a.kn ? (a.n + kTile - 1) / kTile : 0);
-    const int64_t most = (units > (int64_t{1} << 40) / tiles) ? full : (units * tiles + kMinTiles - 1) / kMinTiles;
+    const int64_t tiles = (a.cache.cap + k.tile - 1) / k.tile + (a.kn ? (a.n + k.tile - 1) / k.tile : 0);
+    const int64_t most = (units > (int64_t{1} << 40) / tiles) ? full : (units * tiles + k.min_tiles - 1) / k.min_tiles;
     const unsigned grid = static_cast<unsigned>(std::min<int64_t>(full, std::max<int64_t>(most, 1)));
-    const cudaError_t e = launch_pdl(v.kernel, dim3(grid), dim3(v.threads), v.smem, st, k);
+    const cudaError_t e = v.kernel ? launch_pdl(v.kernel, dim3(grid), dim3(v.threads), v.smem, st, k)
+                                   : launch_kv4_attention_tc(k, static_cast<int32_t>(grid), st);
     if (e != cudaSuccess || grid == 1) return e;
-    return launch_pdl(kv4_merge_kernel, dim3(grid, v.rows / 8 * 2), dim3(128), 0, st, k);
+    return launch_pdl(kv4_merge_kernel, dim3(grid, v.rows / 8), dim3(128), 0, st, k);
 }
 
 }  // namespace eagle

@@ -58,9 +58,16 @@ def attend(q, kc, vc, kn, vn, see):
       exponentials               2^-21 relative each
       fp16 range                 products below 2^-14 lose at most 2^-25 of a scale where the largest
                                  p is 2^9 or more (2^0 where some s is 16 or more): 15 N 2^-34 or 2^-25
+    More than 32 query rows a kv head of 64 or 128 dims go through tiles of fp16 values instead:
+      cached k, v to fp16        2^-11 of their size and 2^-25: the exponent is off by 2^-11 A +
+                                 2^-25 sum |q| / sqrt(D) more, v by 2^-11 |v| + 2^-25
+      new k, v to fp16           exact but for 2^-25 below 2^-14: the same 2^-25 terms
+      p to fp16                  2^-11 |v|; below 2^-14 at most 2^-25 where the largest is 2^9 or
+                                 more: N 2^-34 of the largest |v|
     """
     n, H, D = q.shape
     Hk = kc.shape[1]
+    tiles = n * H // Hk > 32 and D in (64, 128)
     k, v, size, ksize = stands_for(kc), stands_for(vc), size_of(vc), size_of(kc)
     steep = bool((parts(vc)[1] >= 16).any()) if vc.numel() else False
     if kn is not None:
@@ -85,6 +92,15 @@ def attend(q, kc, vc, kn, vn, see):
     o[torch.einsum("nt,th->nh", see_f, torch.isnan(kh).any(-1).double()) > 0] = math.nan
     A = torch.einsum("nhd,thd->hnt", q.double().abs(), torch.nan_to_num(ksize.repeat_interleave(rep, 1))) / math.sqrt(D)
     delta = (D + 16) * 2.0 ** -22 * torch.where(see, A, 0.0).amax(-1, keepdim=True)
+    if tiles:
+        kabs = torch.nan_to_num(k[:kc.shape[0]].abs().repeat_interleave(rep, 1))
+        Ac = torch.einsum("nhd,thd->hnt", q.double().abs(), kabs) / math.sqrt(D)
+        worst = torch.where(see[:, :kc.shape[0]], Ac, 0.0).amax(-1, keepdim=True) if kc.shape[0] else 0.0
+        delta = delta + 2.0 ** -11 * worst + 2.0 ** -25 * q.double().abs().sum(-1).T[..., None] / math.sqrt(D)
+        vfin = torch.nan_to_num(seen_v, posinf=0.0, neginf=0.0).abs()
+        mag = torch.einsum("hnt,thd->nhd", p * (2.0 ** -10 + 2.0 ** -19 + 2 * delta), vfin)
+        big = vfin.amax(0)[None]
+        return o, 2.0 ** -8 * torch.nan_to_num(o).abs() * 1.001 + mag + 2.0 ** -25 + k.shape[0] * 2.0 ** -34 * big
     mag = torch.einsum("hnt,thd->nhd", p * (2.0 ** -10 + 2.0 ** -19 + 2 * delta),
                        torch.nan_to_num(size.repeat_interleave(rep, 1), posinf=0.0))
     tol = 2.0 ** -8 * torch.nan_to_num(o).abs() * 1.001 + mag + 15 * k.shape[0] * (2.0 ** -25 if steep else 2.0 ** -34)

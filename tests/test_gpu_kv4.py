@@ -287,6 +287,12 @@ def test_attention_matches_the_definition(dev, case):
     o = c.attention(q, kn, vn, mask=mask)
     c.status()
     check_attention(case, made, o)
+    # roundings to bf16 are off by 2^-8 / sqrt(3) in the mean square, everything else by less
+    want = torch.cat([ref.attend(q[b], made[1][b, :t], made[2][b, :t], None if kn is None else kn[b],
+                                 None if vn is None else vn[b],
+                                 ref.sees(q.shape[1], t, None if mask is None else mask[b], "cuda")[:, :t + (0 if kn is None else q.shape[1])])[0]
+                      for b, t in enumerate(case[6])])
+    assert float((o.double().flatten(0, 1) - want).norm()) <= 2.0 ** -8 * float(want.norm())
     again = c.attention(q, kn, vn, mask=mask)
     assert torch.equal(o, again)  # bit for bit
 
