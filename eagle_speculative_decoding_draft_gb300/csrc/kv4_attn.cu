@@ -86,7 +86,7 @@ struct Shape {
 };
 
 template <int G, int NQ>
-__global__ void __launch_bounds__(kThreads, Shape<G, NQ>::kBlocks) kv4_attention_kernel(const Kv4Args k) {
+__global__ void __launch_bounds__(kThreads, Shape<G, NQ>::kBlocks) kv4_attention_kernel(const __grid_constant__ Kv4Args k) {
     using S = Shape<G, NQ>;
     constexpr int D = S::D, kRows = S::kRows;
     extern __shared__ __align__(128) uint8_t smem[];
@@ -138,11 +138,7 @@ __global__ void __launch_bounds__(kThreads, Shape<G, NQ>::kBlocks) kv4_attention
                 const int32_t tiles = static_cast<int32_t>(min(k1 - kt, int64_t{8}));
                 for (int32_t j = 0; j < tiles; ++j, ++issued) {
                     const int32_t st = issued % kStages;
-                    if (issued >= kStages && lane == 0 &&
-                        !mbar_wait(&empty[st], static_cast<uint32_t>(issued / kStages - 1) & 1u, abort_flag)) {
-                        *abort_flag = 1;
-                        latch(a.status, kDevTimeout);
-                    }
+                    if (issued >= kStages && lane == 0) kv4_wait(&empty[st], issued / kStages - 1, abort_flag);
                     dead = __shfl_sync(kFull, static_cast<int>(*abort_flag), 0) != 0;
                     if (dead) break;
                     const bool my = (lane >> 2) == j;
@@ -162,6 +158,7 @@ __global__ void __launch_bounds__(kThreads, Shape<G, NQ>::kBlocks) kv4_attention
         if (lane == 0)
             for (int32_t i = max(issued - kStages, 0); i < issued; ++i)
                 mbar_wait(&full[i % kStages], static_cast<uint32_t>(i / kStages) & 1u, nullptr);
+        if (dead && lane == 0) latch(a.status, kDevTimeout);
         return;
     }
 
@@ -413,10 +410,7 @@ __global__ void __launch_bounds__(kThreads, Shape<G, NQ>::kBlocks) kv4_attention
         // ---------------- cached keys ----------------
         for (; s < w.s1; ++s, ++taken) {
             const int32_t st = taken % kStages;
-            if (!mbar_wait(&full[st], static_cast<uint32_t>(taken / kStages) & 1u, abort_flag)) {
-                *abort_flag = 1;
-                latch(a.status, kDevTimeout);
-            }
+            kv4_wait(&full[st], taken / kStages, abort_flag);
             const int32_t nv = __shfl_sync(kFull, *abort_flag ? 0 : valid[st][warp], 0);
             if (nv > 0) {
                 const uint8_t *ch = smem + S::kRing + st * S::kStageBytes + warp * kv4_chunk_bytes(G);
@@ -581,7 +575,9 @@ __global__ void __launch_bounds__(kThreads, Shape<G, NQ>::kBlocks) kv4_attention
             if (gq < 2) merge_ml[warp * kRows + nq * 8 + 2 * qd + gq] = gq ? make_float2(ref[nq][1], l[nq][1]) : make_float2(ref[nq][0], l[nq][0]);
         }
         named_barrier_sync(1, kWarps * 32);
-        if (!*abort_flag) {
+        if (*abort_flag) {
+            if (threadIdx.x == 0) latch(a.status, kDevTimeout);
+        } else {
             const bool whole = w.s0 == 0 && w.s1 == w.unit;
             const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (w.t == p.begin ? 0 : 1);
             for (int32_t it = threadIdx.x; it < kRows * (D / 4); it += kWarps * 32) {
@@ -624,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, Shape<G, NQ>::kBlocks) kv4_attention
 
 // Units that several CTAs worked on: block c merges the unit that CTA c is the first to continue.
 // o = sum_i w_i O_i / sum_i w_i l_i, w_i = 2^(m_i - max m), over CTAs first..last in order.
-__global__ void __launch_bounds__(128) kv4_merge_kernel(const Kv4Args k) {
+__global__ void __launch_bounds__(128) kv4_merge_kernel(const __grid_constant__ Kv4Args k) {
     pdl_launch_dependents();
     pdl_wait();
     const Kv4Share sh = k.share[blockIdx.x];
@@ -742,7 +738,9 @@ cudaError_t launch_kv4_attention(const Kv4Attention &a, cudaStream_t st) {
     k.rows = v.rows;
     k.QT = (k.Mq + v.rows - 1) / v.rows;
     k.W = (a.n + 31) / 32;
-    k.tile = v.kernel ? kTile : kKv4TcTile;
+    static_assert(kTile == 1 << 6 && kKv4TcTile == 1 << 7, "tile_shift");
+    const int64_t tile = v.kernel ? kTile : kKv4TcTile;
+    k.tile_shift = v.kernel ? 6 : 7;
     k.min_tiles = v.kernel ? kMinTiles : 1;
     k.scale2 = kLog2e / sqrtf(static_cast<float>(G * kKv4Group));
     const int32_t full = grid_of(*d, G, v);
@@ -754,7 +752,7 @@ cudaError_t launch_kv4_attention(const Kv4Attention &a, cudaStream_t st) {
     k.part_o = reinterpret_cast<float *>(ws);
     // no more CTAs than the longest possible line gives work to
     const int64_t units = static_cast<int64_t>(a.B) * a.cache.Hk * k.QT;
-    const int64_t tiles = (a.cache.cap + k.tile - 1) / k.tile + (a.kn ? (a.n + k.tile - 1) / k.tile : 0);
+    const int64_t tiles = (a.cache.cap + tile - 1) / tile + (a.kn ? (a.n + tile - 1) / tile : 0);
     const int64_t most = (units > (int64_t{1} << 40) / tiles) ? full : (units * tiles + k.min_tiles - 1) / k.min_tiles;
     const unsigned grid = static_cast<unsigned>(std::min<int64_t>(full, std::max<int64_t>(most, 1)));
     const cudaError_t e = v.kernel ? launch_pdl(v.kernel, dim3(grid), dim3(v.threads), v.smem, st, k)

@@ -12,7 +12,8 @@
 //                   reference only moved (and O rescaled) when a tile's maximum passes that.
 //   warps 8-11      fill the tiles: codes become fp16 values m + s c (one fused multiply-add: half an
 //                   fp16 step, 2^-11 relative); new keys and values are converted from bf16 (exact
-//                   but for magnitudes below 2^-14).  Loads run one batch ahead of the conversion.
+//                   but for magnitudes below 2^-14).
+//   warp 13         copies the codes of cached tiles into a ring of three halves of tiles
 //   warp 12         one thread issues the MMAs: S = Q K^T (128 x 128 x D, operands in shared memory)
 //                   and O += P V (P from TMEM, V as stored: the MN-major B operand).  The order S0 S1
 //                   [P0] O0 S0' [P1] O1 S1' ... keeps one stream's MMAs under the other's softmax.
@@ -23,6 +24,8 @@
 // New keys or values that fp16 cannot hold (above 65504, infinite, NaN) count as 0 in the tiles, and
 // the rows that see them add their terms one by one: nothing hidden reaches a row, whatever it is.
 // TMEM: S0 S1 O0 O1, 128 columns each (O uses D).  Every wait is bounded.
+#include <type_traits>
+
 #include "kernels.cuh"
 #include "kv4_line.cuh"
 
@@ -30,7 +33,8 @@ namespace eagle {
 namespace {
 
 constexpr int kKeys = kKv4TcTile;
-constexpr int kThreads = 13 * 32;
+constexpr int kThreads = 14 * 32;
+constexpr int kRaw = 3;  // halves of tiles (keys or values) of codes in flight
 constexpr float kTop = 12.0f, kAim = 9.0f;  // p <= 2^12; a new reference puts the largest at 2^9
 constexpr uint32_t kTmemCols = 512;
 
@@ -41,12 +45,15 @@ struct Tc {
     static constexpr uint32_t kQ = 0;                      // two streams
     static constexpr uint32_t kK = kQ + 2 * kTileBytes;    // two stages
     static constexpr uint32_t kV = kK + 2 * kTileBytes;    // two stages
-    static constexpr uint32_t kTotal = kV + 2 * kTileBytes + 1024;  // and alignment
+    static constexpr uint32_t kPart = 320u * G;            // a chunk's keys or values: codes and parameters
+    static constexpr uint32_t kCodes = kV + 2 * kTileBytes;  // kRaw stages of eight such parts
+    static constexpr uint32_t kTotal = kCodes + kRaw * 8 * kPart + 1024;  // and alignment
 };
 
 struct TcBars {
     uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];  // stages
     uint64_t q_full[2], s_full[2], p_full[2], o_done[2];    // streams
+    uint64_t raw_full[kRaw], raw_empty[kRaw];
     uint64_t drain;
 };
 
@@ -106,38 +113,59 @@ __device__ __forceinline__ uint4 dequant8(uint32_t w, uint32_t sm) {
 __device__ __forceinline__ bool is_odd(float x) { return !(fabsf(x) <= 65504.0f); }
 
 // Eight bf16 to fp16 in the same order; what fp16 cannot hold becomes 0 and sets `odd`.
-__device__ __forceinline__ uint4 convert8(const uint4 v, bool &odd) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    float x[8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = bf_lo(w[i]);
-        x[2 * i + 1] = bf_hi(w[i]);
-    }
-    float big = 0.0f;
-    bool nan = false;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        big = fmaxf(big, fabsf(x[i]));
-        nan = nan || x[i] != x[i];
-    }
-    if (nan || big > 65504.0f) {
+__device__ __forceinline__ uint4 convert8(uint4 v, bool &odd) {
+    auto abs2 = [](uint32_t x) { return x & 0x7fff7fffu; };
+    auto b2 = [](uint32_t x) { return *reinterpret_cast<const __nv_bfloat162 *>(&x); };
+    const __nv_bfloat162 big = __hmax2_nan(__hmax2_nan(b2(abs2(v.x)), b2(abs2(v.y))), __hmax2_nan(b2(abs2(v.z)), b2(abs2(v.w))));
+    if (!(__low2float(big) <= 65504.0f && __high2float(big) <= 65504.0f)) {
         odd = true;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (is_odd(x[i])) x[i] = 0.0f;
+        uint32_t *w = reinterpret_cast<uint32_t *>(&v);
+        for (int i = 0; i < 4; ++i) {
+            if (is_odd(bf_lo(w[i]))) w[i] &= 0xffff0000u;
+            if (is_odd(bf_hi(w[i]))) w[i] &= 0x0000ffffu;
+        }
     }
-    return make_uint4(pack_f16(x[0], x[4]), pack_f16(x[1], x[5]), pack_f16(x[2], x[6]), pack_f16(x[3], x[7]));
+    return make_uint4(pack_f16(bf_lo(v.x), bf_lo(v.z)), pack_f16(bf_hi(v.x), bf_hi(v.z)), pack_f16(bf_lo(v.y), bf_lo(v.w)),
+                      pack_f16(bf_hi(v.y), bf_hi(v.w)));
 }
 
-// A batch of a filling thread: 8 pieces of 16 bytes (of new keys), or 4 of codes with parameters.
-template <int G>
-struct Batch {
-    uint32_t r[4][2 * G > 8 ? 2 * G : 8];
-};
+// The terms of elements that fp16 cannot hold, which count as 0 in the tiles: for the keys into the
+// row's scores (f: what the query was scaled by), for the values into its output, where the row sees
+// the key.  Warp-wide; `rows`: keys of the tile.
+template <int D>
+static __device__ __noinline__ void add_odd_keys(const __nv_bfloat16 *kt, int64_t ld, int32_t rows, const __nv_bfloat16 *q,
+                                                 float f, uint32_t t_s) {
+    for (int32_t key = 0; key < rows; ++key) {
+        float add = 0.0f;
+        bool any = false;
+        for (int32_t d = 0; d < D; ++d) {
+            const float x = __bfloat162float(kt[key * ld + d]);
+            if (!is_odd(x)) continue;
+            any = true;
+            add += __bfloat162float(q[d]) * f * x;
+        }
+        if (any) tmem_st_1(t_s + key, tmem_ld_1(t_s + key) + add);
+    }
+}
+template <int D>
+static __device__ __noinline__ void add_odd_values(const __nv_bfloat16 *vt, int64_t ld, int32_t rows, uint4 see, float mul,
+                                                   float sub, uint32_t t_s, uint32_t t_o) {
+    for (int32_t key = 0; key < rows; ++key) {
+        const float pv = ex2_approx(__fadd_rn(__fmul_rn(tmem_ld_1(t_s + key), mul), sub));
+        const uint32_t word = key < 64 ? (key < 32 ? see.x : see.y) : (key < 96 ? see.z : see.w);
+        const bool mine = (word >> (key & 31)) & 1u;
+        for (int32_t d = 0; d < D; ++d) {
+            const float x = __bfloat162float(vt[key * ld + d]);
+            if (!is_odd(x)) continue;
+            const uint32_t col = (d & ~7) + ((d & 3) << 1) + ((d >> 2) & 1);  // the order 0 4 1 5 2 6 3 7
+            const float o = tmem_ld_1(t_o + col);
+            tmem_st_1(t_o + col, mine ? o + pv * x : o);
+        }
+    }
+}
 
 template <int G>
-__global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const Kv4Args k) {
+__global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __grid_constant__ Kv4Args k) {
     using S = Tc<G>;
     constexpr int D = S::D;
     extern __shared__ uint8_t smem_raw[];
@@ -145,8 +173,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const Kv4
     __shared__ TcBars bar;
     __shared__ uint32_t tmem_base;
     __shared__ int32_t abort_mark;
-    __shared__ uint8_t key_bits[4][16];       // by tile & 3: which of its 128 keys are there
-    __shared__ uint8_t odd_tile[4][2][4];     // by tile & 3, key or value, filling warp
+    __shared__ __align__(4) uint8_t key_bits[4][16];  // by tile & 3: which of its 128 keys are there
+    __shared__ uint8_t raw_keys[kRaw][8];             // keys of each chunk that are there
+    __shared__ __align__(4) uint8_t odd_tile[4][2][4];     // by tile & 3, key or value, filling warp
     __shared__ float2 stream_ml[2][128];      // one unit of at most 128 rows: maxima and sums
     __shared__ Place place;
     __shared__ int64_t red[kThreads / 32];
@@ -163,6 +192,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const Kv4
             mbar_init(&bar.s_full[i], 1);
             mbar_init(&bar.p_full[i], 128);
             mbar_init(&bar.o_done[i], 1);
+        }
+        for (int i = 0; i < kRaw; ++i) {
+            mbar_init(&bar.raw_full[i], 1);
+            mbar_init(&bar.raw_empty[i], 4);
         }
         mbar_init(&bar.drain, 1);
         abort_mark = 0;
@@ -187,182 +220,146 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const Kv4
     Walk w;
     w.start(k, p);
     if (threadIdx.x == 0) k.share[blockIdx.x] = share_of(k, p, w);
-    auto wait = [&](uint64_t *b, uint32_t parity) -> bool {
-        if (mbar_wait(b, parity & 1u, abort_flag)) return true;
-        *abort_flag = 1;
-        return false;
-    };
+    auto wait = [&](uint64_t *b, uint32_t parity) -> bool { return kv4_wait(b, parity, abort_flag); };
     auto rows_of = [&]() { return min(kKv4TcRows, k.Mq - w.qt * kKv4TcRows); };  // rows of the unit
 
     if (warp >= 8 && warp < 12) {
         // ---------------- the tiles ----------------
         const int32_t fw = warp - 8;
-        uint32_t gt = 0;  // tiles so far
-        // what the next batch is: tile s of the walk, half 0 (keys) or 1 (values), sub-batch
-        constexpr int kSubs = D / 64;  // batches of a half of a new tile
-        int64_t s = w.s0;
-        int32_t half = 0, sub = 0;
-        const uint8_t *chunk[4];  // of the tile's four row groups that this warp fills
-        auto check_length = [&]() {
-            if (fw == 0 && lane == 0 && w.len != a.cache.lengths[w.b]) latch(a.status, kDevBounds);  // clamped
-        };
-        auto find_chunks = [&]() {
-            if (s < w.nt) return;
+        uint32_t gt = 0, raw = 0;  // tiles and halves of cached tiles so far
+        do {
+            for (int64_t s = w.s0; s < w.s1; ++s, ++gt) {
+                const uint32_t st = gt & 1u;
+#pragma unroll 1
+                for (int32_t half = 0; half < 2; ++half) {
+                    uint8_t *dst = base + (half ? S::kV : S::kK) + st * S::kTileBytes;
+                    bool odd = false;
+                    if (s >= w.nt) {
+                        const uint32_t rs = raw % kRaw;
+                        wait(&bar.raw_full[rs], raw / kRaw);
+                        if (gt >= 2) wait(half ? &bar.v_empty[st] : &bar.k_empty[st], (gt >> 1) - 1);
+                        __syncwarp();
+                        const uint8_t *src = base + S::kCodes + rs * 8 * S::kPart;
+                        // lanes: four pieces of 8 dims of rows t and t + 4: the stores of eight
+                        // lanes touch all banks
+                        const int32_t m = lane >> 2, q = lane & 3;
+                        const int32_t t8 = (m >> 1) | ((m & 1) << 2);          // token among the 8
+                        const int32_t slot8 = half ? t8 : m;                   // its row
+                        const int32_t qq = half && G == 4 ? q ^ (t8 & 2) : q;  // value rows' halves change places
+                        // group i of 8 rows: 1024 bytes on; dims 32 g + 8 q: chunk 4 g + q
+                        uint8_t *to = dst + fw * 1024 + t8 * 128 + ((qq ^ t8) << 4);
+                        const int32_t odd_g = ((((4 + qq) ^ t8) - (qq ^ t8)) << 4);
+#pragma unroll 2
+                        for (int32_t i = 0; i < 4; ++i) {
+                            const int32_t group = 4 * i + fw;
+                            const uint8_t *part = src + (group >> 1) * S::kPart;
+                            const int32_t slot = (group & 1) * 8 + slot8;
+                            const int32_t here = max(0, min(8, static_cast<int32_t>(raw_keys[rs][group >> 1]) - 8 * (group & 1)));
+                            uint32_t c[G], sm[G];
+                            if constexpr (G == 4) {
+                                const uint4 cv = *reinterpret_cast<const uint4 *>(part + slot * 64 + q * 16);
+                                const uint4 mv = *reinterpret_cast<const uint4 *>(part + 1024 + slot * 16);
+                                c[0] = cv.x, c[1] = cv.y, c[2] = cv.z, c[3] = cv.w;
+                                sm[0] = mv.x, sm[1] = mv.y, sm[2] = mv.z, sm[3] = mv.w;
+                            } else {
+                                const uint2 cv = *reinterpret_cast<const uint2 *>(part + slot * 32 + q * 8);
+                                const uint2 mv = *reinterpret_cast<const uint2 *>(part + 512 + slot * 8);
+                                c[0] = cv.x, c[1] = cv.y;
+                                sm[0] = mv.x, sm[1] = mv.y;
+                            }
+                            if (half) {  // two 16-bit words of four dims each to the keys' words of eight
+                                uint32_t x[G];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int64_t key = (s - w.nt) * kKeys + ((4 * i + fw) >> 1) * 16;
-                chunk[i] = nullptr;
-                if (key < w.len) {
-                    chunk[i] = kv4_chunk(a.cache, w.b, w.hk, key);
-                    if (!chunk[i]) latch(a.status, kDevBounds);  // its keys count as absent
-                }
-            }
-        };
-        auto load = [&](Batch<G> &x) {
-            if (s >= w.nt) {
-                const int32_t q = lane >> 3;
+                                for (int g = 0; g < G; ++g) x[g] = __byte_perm(c[g / 2], c[G / 2 + g / 2], g & 1 ? 0x7632 : 0x5410);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int32_t slot = ((4 * i + fw) & 1) * 8 + (lane & 7);
-                    uint32_t c[G], m[G];
+                                for (int g = 0; g < G; ++g) c[g] = x[g];
+                            } else if (lane == 0) {
+                                key_bits[gt & 3][group] = static_cast<uint8_t>((1u << here) - 1u);
+                            }
+                            if (here < 8) {  // rows that are not there hold 0
 #pragma unroll
-                    for (int g = 0; g < G; ++g) c[g] = m[g] = 0u;
-                    if (chunk[i]) {
-                        const uint8_t *codes = chunk[i] + (half ? kv4_value_codes(G) : 0) + slot * 16 * G + q * 4 * G;
-                        const uint8_t *par = chunk[i] + (half ? kv4_value_params(G) : kv4_key_params(G)) + slot * 4 * G;
-                        if constexpr (G == 4) {
-                            const uint4 cv = __ldg(reinterpret_cast<const uint4 *>(codes)), mv = __ldg(reinterpret_cast<const uint4 *>(par));
-                            c[0] = cv.x, c[1] = cv.y, c[2] = cv.z, c[3] = cv.w;
-                            m[0] = mv.x, m[1] = mv.y, m[2] = mv.z, m[3] = mv.w;
-                        } else {
-                            const uint2 cv = __ldg(reinterpret_cast<const uint2 *>(codes)), mv = __ldg(reinterpret_cast<const uint2 *>(par));
-                            c[0] = cv.x, c[1] = cv.y;
-                            m[0] = mv.x, m[1] = mv.y;
+                                for (int g = 0; g < G; ++g)
+                                    if (t8 >= here) c[g] = sm[g] = 0u;
+                            }
+#pragma unroll
+                            for (int g = 0; g < G; ++g)
+                                *reinterpret_cast<uint4 *>(to + i * 4096 + (g >> 1) * (kKeys * 128) + (g & 1 ? odd_g : 0)) = dequant8(c[g], sm[g]);
+                        }
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bar.raw_empty[rs]);
+                        ++raw;
+                    } else {
+                        constexpr int kPer = D / 8, kRowsWarp = 32 / kPer;  // pieces a row; rows a warp takes at once
+                        const int32_t ch = lane % kPer, first = fw * kRowsWarp + lane / kPer;
+                        const __nv_bfloat16 *src = (half ? a.vn : a.kn) + (static_cast<int64_t>(w.b) * a.n + s * kKeys) * a.ldkv +
+                                                   static_cast<int64_t>(w.hk) * D + ch * 8;
+                        const int32_t rows = static_cast<int32_t>(min(a.n - s * kKeys, int64_t{kKeys}));
+#pragma unroll 1
+                        for (int32_t sub = 0; sub < D / 64; ++sub) {
+                            uint4 v[8];
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const int32_t row = (sub * 8 + i) * 4 * kRowsWarp + first;
+                                v[i] = row < rows ? *reinterpret_cast<const uint4 *>(src + row * a.ldkv) : make_uint4(0, 0, 0, 0);
+                            }
+                            if (sub == 0) {
+                                if (gt >= 2) wait(half ? &bar.v_empty[st] : &bar.k_empty[st], (gt >> 1) - 1);
+                                __syncwarp();
+                            }
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const int32_t row = (sub * 8 + i) * 4 * kRowsWarp + first;
+                                *reinterpret_cast<uint4 *>(dst + (ch >> 3) * (kKeys * 128) + sw128(row, ch & 7)) = convert8(v[i], odd);
+                            }
                         }
                     }
-#pragma unroll
-                    for (int g = 0; g < G; ++g) {
-                        x.r[i][g] = c[g];
-                        x.r[i][G + g] = m[g];
-                    }
-                }
-            } else {
-                constexpr int kPer = D / 8, kRowsWarp = 32 / kPer;  // pieces a row; rows a warp takes at once
-                const __nv_bfloat16 *src = (half ? a.vn : a.kn) + static_cast<int64_t>(w.b) * a.n * a.ldkv +
-                                           static_cast<int64_t>(w.hk) * D + (lane % kPer) * 8;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int32_t row = (sub * 8 + i) * 4 * kRowsWarp + fw * kRowsWarp + lane / kPer;
-                    const int64_t key = s * kKeys + row;
-                    const uint4 v = key < a.n ? *reinterpret_cast<const uint4 *>(src + key * a.ldkv) : make_uint4(0, 0, 0, 0);
-                    x.r[i >> 1][(i & 1) * 4] = v.x;
-                    x.r[i >> 1][(i & 1) * 4 + 1] = v.y;
-                    x.r[i >> 1][(i & 1) * 4 + 2] = v.z;
-                    x.r[i >> 1][(i & 1) * 4 + 3] = v.w;
+                    const bool any = __any_sync(kFull, odd);
+                    if (lane == 0) odd_tile[gt & 3][half][fw] = any;
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(half ? &bar.v_full[st] : &bar.k_full[st]);
                 }
             }
-        };
-        bool odd = false;  // of the half that is being filled
-        struct Where {
-            int64_t s, len;
-            int32_t half, sub, nt, n;
-            bool last, there[4];
-        };
-        auto emit = [&](const Batch<G> &x, const Where &at) {
-            const uint32_t st = gt & 1u;
-            uint8_t *dst = base + (at.half ? S::kV : S::kK) + st * S::kTileBytes;
-            if (at.sub == 0) {
-                if (gt >= 2) wait(at.half ? &bar.v_empty[st] : &bar.k_empty[st], (gt >> 1) - 1);
-                odd = false;
-            }
-            if (at.s >= at.nt) {
-                const int32_t q = lane >> 3;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int32_t group = 4 * i + fw, slot = (group & 1) * 8 + (lane & 7);
-                    // a key row's token: the inverse of kv4_key_slot
-                    const int32_t t = at.half ? slot : (((slot & 7) >> 1) | ((slot & 1) << 2) | (slot & 8));
-                    const int32_t row = (group >> 1) * 16 + t;
-                    const bool there = at.there[i] && (at.s - at.nt) * kKeys + row < at.len;
-                    const int32_t qq = at.half && G == 4 ? q ^ (t & 2) : q;  // value rows' halves change places
-#pragma unroll
-                    for (int g = 0; g < G; ++g) {
-                        uint32_t c = x.r[i][g];
-                        if (at.half)  // two 16-bit words of four dims
-                            c = __byte_perm(x.r[i][g / 2], x.r[i][G / 2 + g / 2], g & 1 ? 0x7632 : 0x5410);
-                        uint4 v = dequant8(c, x.r[i][G + g]);
-                        if (!there) v = make_uint4(0, 0, 0, 0);
-                        const int32_t ch = 4 * g + qq;
-                        *reinterpret_cast<uint4 *>(dst + (ch >> 3) * (kKeys * 128) + sw128(row, ch & 7)) = v;
-                    }
-                    if (at.half == 0) {
-                        // bits of the rows in token order: 8 keys of two half-chunks interleave, so
-                        // each lane reports its own token
-                        const uint32_t b = __ballot_sync(kFull, there && q == 0);
-                        if (lane == 0) {
-                            // lanes 0..7 are slots; tokens (slot & 7) >> 1 | (slot & 1) << 2
-                            uint32_t bits = 0;
-#pragma unroll
-                            for (int l = 0; l < 8; ++l) bits |= ((b >> l) & 1u) << ((l >> 1) | ((l & 1) << 2));
-                            key_bits[gt & 3][group] = static_cast<uint8_t>(bits);
-                        }
-                    }
+        } while (w.next(k, p));
+    } else if (warp == 13) {
+        // ---------------- copies of codes: a stage is the keys or the values of a cached tile -------
+        uint32_t raw = 0;
+        bool dead = false;
+        do {
+            if (lane == 0 && w.len != a.cache.lengths[w.b]) latch(a.status, kDevBounds);  // clamped
+            const int64_t k0 = max(w.s0 - w.nt, int64_t{0}), k1 = w.s1 - w.nt;
+            for (int64_t kt = k0; kt < k1 && !dead; kt += 4) {
+                // the chunks of four tiles, one a lane
+                const int64_t key = kt * kKeys + lane * 16;
+                int32_t nv = static_cast<int32_t>(min(max(w.len - key, int64_t{0}), int64_t{16}));
+                const uint8_t *src = nullptr;
+                if (nv > 0 && kt + (lane >> 3) < k1) {
+                    src = kv4_chunk(a.cache, w.b, w.hk, key);
+                    if (!src) latch(a.status, kDevBounds);  // its keys count as absent
                 }
-            } else {
-                constexpr int kPer = D / 8, kRowsWarp = 32 / kPer;
-                const int32_t ch = lane % kPer;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int32_t row = (at.sub * 8 + i) * 4 * kRowsWarp + fw * kRowsWarp + lane / kPer;
-                    const uint32_t *r = &x.r[i >> 1][(i & 1) * 4];
-                    *reinterpret_cast<uint4 *>(dst + (ch >> 3) * (kKeys * 128) + sw128(row, ch & 7)) =
-                        convert8(make_uint4(r[0], r[1], r[2], r[3]), odd);
+                if (!src) nv = 0;
+                const int32_t halves = 2 * static_cast<int32_t>(min(k1 - kt, int64_t{4}));
+                for (int32_t hh = 0; hh < halves; ++hh, ++raw) {
+                    const uint32_t rs = raw % kRaw;
+                    if (raw >= kRaw && lane == 0) wait(&bar.raw_empty[rs], raw / kRaw - 1);
+                    dead = __shfl_sync(kFull, static_cast<int>(*abort_flag), 0) != 0;
+                    if (dead) break;
+                    const bool my = (lane >> 3) == (hh >> 1);
+                    const uint32_t have = __ballot_sync(kFull, my && src);
+                    if (my) raw_keys[rs][lane & 7] = static_cast<uint8_t>(nv);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_expect_tx(&bar.raw_full[rs], __popc(have) * S::kPart);
+                    __syncwarp();
+                    if (my && src)
+                        bulk_load(base + S::kCodes + rs * 8 * S::kPart + (lane & 7) * S::kPart, src + (hh & 1 ? S::kPart : 0u), S::kPart,
+                                  &bar.raw_full[rs]);
                 }
             }
-            if (at.last) {
-                const bool any = __any_sync(kFull, odd);
-                if (lane == 0) odd_tile[gt & 3][at.half][fw] = any;
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(at.half ? &bar.v_full[st] : &bar.k_full[st]);
-                if (at.half) ++gt;
-            }
-        };
-        auto here = [&]() {
-            Where at{s, w.len, half, sub, w.nt, a.n, s >= w.nt || sub == kSubs - 1, {}};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) at.there[i] = s >= w.nt && chunk[i];
-            return at;
-        };
-        // to the next batch; false behind the last
-        auto step = [&]() {
-            if (s < w.nt && ++sub < kSubs) return true;
-            sub = 0;
-            if ((half ^= 1) == 1) return true;
-            if (++s == w.s1) {
-                if (!w.next(k, p)) return false;
-                s = w.s0;
-                check_length();
-            }
-            find_chunks();
-            return true;
-        };
-        check_length();
-        find_chunks();
-        Batch<G> now, ahead;
-        load(now);
-        Where at = here();
-        for (bool more = true; more;) {
-            more = step();
-            Where next_at = at;
-            if (more) {
-                load(ahead);
-                next_at = here();
-            }
-            emit(now, at);
-            now = ahead;
-            at = next_at;
-        }
+        } while (!dead && w.next(k, p));
+        // every copy has landed before the block's memory is handed on
+        if (lane == 0)
+            for (uint32_t i = raw > kRaw ? raw - kRaw : 0; i < raw; ++i) mbar_wait(&bar.raw_full[i % kRaw], (i / kRaw) & 1u, nullptr);
+        __syncwarp();
     } else if (warp == 12) {
         // ---------------- MMA issue (one thread) ----------------
         if (lane == 0) {
@@ -433,11 +430,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const Kv4
             float f, mul;  // what the query was scaled by; what makes its scores base 2
             {
                 float big = 0.0f;
-                uint4 v[D / 8];
-#pragma unroll
+                auto piece = [&](int c) { return live ? *reinterpret_cast<const uint4 *>(q_src + 8 * c) : make_uint4(0, 0, 0, 0); };
+#pragma unroll 4
                 for (int c = 0; c < D / 8; ++c) {
-                    v[c] = live ? *reinterpret_cast<const uint4 *>(q_src + 8 * c) : make_uint4(0, 0, 0, 0);
-                    const uint32_t vw[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+                    const uint4 v = piece(c);
+                    const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                     for (int i = 0; i < 4; ++i) big = fmaxf(big, fmaxf(fabsf(bf_lo(vw[i])), fabsf(bf_hi(vw[i]))));
                 }
@@ -445,17 +442,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const Kv4
                 f = __uint_as_float(static_cast<uint32_t>(263 - e) << 23);
                 mul = __uint_as_float(static_cast<uint32_t>(e - 9) << 23) * k.scale2;
                 uint8_t *dst = base + S::kQ + j * S::kTileBytes;
-#pragma unroll
+#pragma unroll 2
                 for (int c = 0; c < D / 8; ++c) {
-                    const uint32_t vw[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
-                    float x[8];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        x[2 * i] = bf_lo(vw[i]) * f;
-                        x[2 * i + 1] = bf_hi(vw[i]) * f;
-                    }
+                    const uint4 v = piece(c);
                     *reinterpret_cast<uint4 *>(dst + (c >> 3) * (kKeys * 128) + sw128(r, c & 7)) =
-                        make_uint4(pack_f16(x[0], x[4]), pack_f16(x[1], x[5]), pack_f16(x[2], x[6]), pack_f16(x[3], x[7]));
+                        make_uint4(pack_f16(bf_lo(v.x) * f, bf_lo(v.z) * f), pack_f16(bf_hi(v.x) * f, bf_hi(v.z) * f),
+                                   pack_f16(bf_lo(v.y) * f, bf_lo(v.w) * f), pack_f16(bf_hi(v.y) * f, bf_hi(v.w) * f));
                 }
                 fence_proxy_async_smem();
                 mbar_arrive(&bar.q_full[j]);
@@ -505,33 +497,32 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const Kv4
                 if (!live) see[0] = see[1] = see[2] = see[3] = 0u;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) all = all && see[i] == kFull;
-                if (odd_k) {
-                    // products with the key elements that count as 0 in the tile
-                    for (int32_t key = 0; key < kKeys && s * kKeys + key < a.n; ++key) {
-                        const __nv_bfloat16 *kp = a.kn + (static_cast<int64_t>(w.b) * a.n + s * kKeys + key) * a.ldkv + static_cast<int64_t>(w.hk) * D;
-                        float add = 0.0f;
-                        bool any = false;
-                        for (int32_t d = 0; d < D; ++d) {
-                            const float x = __bfloat162float(kp[d]);
-                            if (!is_odd(x)) continue;
-                            any = true;
-                            if (live) add += __bfloat162float(q_src[d]) * f * x;
-                        }
-                        if (any) tmem_st_1(t_s + key, tmem_ld_1(t_s + key) + add);
-                    }
-                }
+                all = __all_sync(kFull, all);
+                const int64_t new_row = (static_cast<int64_t>(w.b) * a.n + s * kKeys) * a.ldkv + static_cast<int64_t>(w.hk) * D;
+                const int32_t new_rows = static_cast<int32_t>(min(a.n - s * kKeys, int64_t{kKeys}));
+                if (odd_k) add_odd_keys<D>(a.kn + new_row, a.ldkv, new_rows, q_src, f, t_s);
                 float mx = -INFINITY;
+                if (all) {
+                    float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t v[32];
+                        tmem_ld_32(t_s + 32 * c, v);
+                        tmem_wait_ld();
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t v[32];
-                    tmem_ld_32(t_s + 32 * c, v);
-                    tmem_wait_ld();
-                    if (all) {
+                        for (int i = 0; i < 32; ++i) m4[i & 3] = fmaxf(m4[i & 3], __uint_as_float(v[i]));
+                    }
+                    mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                } else {
+                    uint32_t bits[4] = {see[0], see[1], see[2], see[3]};
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t v[32];
+                        tmem_ld_32(t_s + 32 * c, v);
+                        tmem_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) mx = fmaxf(mx, __uint_as_float(v[i]));
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) mx = fmaxf(mx, (see[c] >> i) & 1u ? __uint_as_float(v[i]) : -INFINITY);
+                        for (int i = 0; i < 32; ++i) mx = fmaxf(mx, (bits[0] >> i) & 1u ? __uint_as_float(v[i]) : -INFINITY);
+                        bits[0] = bits[1], bits[1] = bits[2], bits[2] = bits[3];
                     }
                 }
                 mx = mx == -INFINITY ? mx : mx * mul;  // mul may underflow to 0
@@ -545,7 +536,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const Kv4
                 const float sub = ref == -INFINITY ? 0.0f : -ref;
                 if (done > 0 && __any_sync(kFull, corr != 1.0f)) {
                     // the scores' arrival says that the stream's earlier products are complete
-#pragma unroll
+#pragma unroll 1
                     for (int c = 0; c < D / 32; ++c) {
                         uint32_t v[32];
                         tmem_ld_32(t_o + 32 * c, v);
@@ -556,25 +547,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const Kv4
                     }
                     tmem_wait_st();
                 }
-                if (odd_v) {
-                    for (int32_t key = 0; key < kKeys && s * kKeys + key < a.n; ++key) {
-                        const __nv_bfloat16 *vp = a.vn + (static_cast<int64_t>(w.b) * a.n + s * kKeys + key) * a.ldkv + static_cast<int64_t>(w.hk) * D;
-                        const float pv = ex2_approx(__fadd_rn(__fmul_rn(tmem_ld_1(t_s + key), mul), sub));
-                        const bool mine = (see[key >> 5] >> (key & 31)) & 1u;
-                        for (int32_t d = 0; d < D; ++d) {
-                            const float x = __bfloat162float(vp[d]);
-                            if (!is_odd(x)) continue;
-                            const uint32_t col = (d & ~7) + ((d & 3) << 1) + ((d >> 2) & 1);  // the order 0 4 1 5 2 6 3 7
-                            const float o = tmem_ld_1(t_o + col);
-                            tmem_st_1(t_o + col, mine ? o + pv * x : o);
-                        }
-                    }
-                }
-// One product and difference; scores so large that the product's rounding matters next
+                if (odd_v)
+                    add_odd_values<D>(a.vn + new_row, a.ldkv, new_rows, make_uint4(see[0], see[1], see[2], see[3]), mul, sub, t_s, t_o);
+                // One product and difference; scores so large that the product's rounding matters next
                 // to their differences (and could pass for a score above the maximum) in two steps,
                 // as the maximum was formed.
-                auto exponentials = [&](auto exponent) {
-#pragma unroll
+                auto exponentials = [&](auto exponent, auto masked) {
+                    uint32_t bits[4] = {see[0], see[1], see[2], see[3]};
+#pragma unroll 1
                     for (int c = 0; c < 4; ++c) {
                         uint32_t v[32], pk[16];
                         tmem_ld_32(t_s + 32 * c, v);
@@ -584,21 +564,24 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const Kv4
                         for (int i = 0; i < 16; ++i) {
                             float p0 = ex2_approx(exponent(__uint_as_float(v[2 * i])));
                             float p1 = ex2_approx(exponent(__uint_as_float(v[2 * i + 1])));
-                            if (!all) {
-                                p0 = (see[c] >> (2 * i)) & 1u ? p0 : 0.0f;
-                                p1 = (see[c] >> (2 * i + 1)) & 1u ? p1 : 0.0f;
+                            if constexpr (decltype(masked)::value) {
+                                p0 = (bits[0] >> (2 * i)) & 1u ? p0 : 0.0f;
+                                p1 = (bits[0] >> (2 * i + 1)) & 1u ? p1 : 0.0f;
                             }
                             sum[i & 1] += p0 + p1;
                             pk[i] = pack_f16(p0, p1);
                         }
                         l += sum[0] + sum[1];
                         tmem_st_16(t_s + 16 * c, pk);
+                        if constexpr (decltype(masked)::value) bits[0] = bits[1], bits[1] = bits[2], bits[2] = bits[3];
                     }
                 };
                 if (__any_sync(kFull, fabsf(sub) > 1048576.0f))
-                    exponentials([&](float x) { return __fadd_rn(__fmul_rn(x, mul), sub); });
+                    exponentials([&](float x) { return __fadd_rn(__fmul_rn(x, mul), sub); }, std::true_type{});
+                else if (all)
+                    exponentials([&](float x) { return fmaf(x, mul, sub); }, std::false_type{});
                 else
-                    exponentials([&](float x) { return fmaf(x, mul, sub); });
+                    exponentials([&](float x) { return fmaf(x, mul, sub); }, std::true_type{});
                 tmem_wait_st();
                 tc_fence_before();
                 mbar_arrive(&bar.p_full[j]);
@@ -631,6 +614,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const Kv4
             const float inv = L == 0.0f ? 0.0f : 1.0f / L;
             const bool ok = !*abort_flag;
             const int32_t c_begin = both ? 0 : j * (D / 64), c_end = both ? D / 32 : (j + 1) * (D / 64);
+#pragma unroll 1
             for (int32_t c = c_begin; c < c_end; ++c) {
                 float x[32];
                 {

@@ -23,7 +23,8 @@ struct Kv4Share {
 struct Kv4Args {
     Kv4Attention a;
     int32_t group, Mq, rows, QT, W;
-    int32_t tile, min_tiles; // keys of a tile; tiles a CTA takes at least
+    int32_t tile_shift;      // log2 of the keys of a tile
+    int32_t min_tiles;       // tiles a CTA takes at least
     float scale2;            // log2(e) / sqrt(D)
     Kv4Share *share;         // [grid]
     float2 *part_ml;         // [grid * 2][rows]: running maximum (base 2) and sum
@@ -56,19 +57,39 @@ __device__ __forceinline__ void load_words(const uint8_t *p, uint32_t (&w)[N]) {
     }
 }
 
+// Waits for `parity` (its lowest bit) on `bar`.  Gives up when *abort is set, and sets it after
+// kWaitLimitNs.  Small, so that the kernels' loops stay in the instruction cache: the clock is looked
+// at once in a thousand tries.
+__device__ __forceinline__ bool kv4_wait(uint64_t *bar, uint32_t parity, volatile int32_t *abort) {
+    uint64_t since = 0;
+    for (uint32_t i = 1;; ++i) {
+        if (mbar_try_wait(bar, parity & 1u)) return true;
+        if (*abort) return false;
+        if ((i & 1023u) == 0) {
+            const uint64_t now = global_timer_ns();
+            if (since == 0) {
+                since = now;
+            } else if (now - since > kWaitLimitNs) {
+                *abort = 1;
+                return false;
+            }
+        }
+    }
+}
+
 // ---------------------------------------------------------------------------------------------
 // The line of tiles
 // ---------------------------------------------------------------------------------------------
 // Tiles of new keys that the rows of query tile qt need.
 __device__ __forceinline__ int32_t new_tiles(const Kv4Args &k, int32_t qt) {
     if (!k.a.kn) return 0;
-    if (k.a.mask) return (k.a.n + k.tile - 1) / k.tile;
+    if (k.a.mask) return ((k.a.n - 1) >> k.tile_shift) + 1;
     const int32_t last = min(k.a.n - 1, ((qt + 1) * k.rows - 1) / k.group);
-    return last / k.tile + 1;
+    return (last >> k.tile_shift) + 1;
 }
 // Tiles of cached keys of request b; at least one where a unit would have none.
 __device__ __forceinline__ int64_t cached_tiles(const Kv4Args &k, int32_t b) {
-    const int64_t t = (kv4_length(k.a.cache, b) + k.tile - 1) / k.tile;
+    const int64_t t = (kv4_length(k.a.cache, b) + (1 << k.tile_shift) - 1) >> k.tile_shift;
     return t < 1 && !k.a.kn ? 1 : t;
 }
 
@@ -81,7 +102,7 @@ struct Place {
 };
 
 // Sum over the block; every thread gets it.  `red`: one slot a warp.
-__device__ inline int64_t block_sum64(int64_t v, int64_t *red) {
+static __device__ __noinline__ int64_t block_sum64(int64_t v, int64_t *red) {
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(kFull, v, off);
     __syncthreads();
@@ -94,7 +115,7 @@ __device__ inline int64_t block_sum64(int64_t v, int64_t *red) {
 
 // All threads of the block; the result is in *out after the last barrier.  Returns false when this
 // CTA has nothing to do.
-__device__ inline bool find_place(const Kv4Args &k, Place *out, int64_t *red) {
+static __device__ __noinline__ bool find_place(const Kv4Args &k, Place *out, int64_t *red) {
     const int32_t tid = threadIdx.x, nt = blockDim.x, B = k.a.B;
     const int64_t Hk = k.a.cache.Hk;
     int64_t per = 0;  // tiles of new keys of one (request, kv head)
@@ -199,7 +220,7 @@ struct Walk {
 };
 
 // What CTA blockIdx.x leaves for the merge.
-__device__ __forceinline__ Kv4Share share_of(const Kv4Args &k, const Place &p, const Walk &w) {
+static __device__ __noinline__ Kv4Share share_of(const Kv4Args &k, const Place &p, const Walk &w) {
     Kv4Share sh{-1, 0, 0, 0, 0, 0};
     if (w.s0 > 0) {
         const int64_t u0 = p.begin - w.s0;  // the unit's first tile
