@@ -6,17 +6,20 @@
 // 256 query rows of one (request, kv head), as two streams of 128 rows that share every key and
 // value tile; where a unit has at most 128 rows, both streams hold the same rows and take the even
 // and the odd tiles, each with its own maximum, sum and output.  Tiles are 128 keys.
-//   warps 0-3, 4-7  softmax of stream 0 and 1, a row a thread (its TMEM lane): two passes over the
-//                   row of scores (maximum; exponentials), p as fp16 into TMEM over the scores it
-//                   came from, the running maximum and sum in fp32.  p is held below 2^12 and its
-//                   reference only moved (and O rescaled) when a tile's maximum passes that.
-//   warps 8-11      fill the tiles: codes become fp16 values m + s c (one fused multiply-add: half an
-//                   fp16 step, 2^-11 relative); new keys and values are converted from bf16 (exact
-//                   but for magnitudes below 2^-14).
-//   warp 13         copies the codes of cached tiles into a ring of three halves of tiles
-//   warp 12         one thread issues the MMAs: S = Q K^T (128 x 128 x D, operands in shared memory)
-//                   and O += P V (P from TMEM, V as stored: the MN-major B operand).  The order S0 S1
-//                   [P0] O0 S0' [P1] O1 S1' ... keeps one stream's MMAs under the other's softmax.
+//   warps 0-7, 8-15  softmax of stream 0 and 1, two threads a row (its TMEM lane), each on 64 of the
+//                    tile's keys: two passes over the scores (maximum; exponentials), p as fp16 into
+//                    TMEM over the scores it came from, the running maximum and sum in fp32.  p is
+//                    held below 2^15 and its reference only moved (and O rescaled) when a tile's
+//                    maximum passes that; the halves agree on the maximum through shared memory.
+//   warps 16-23      fill the tiles: codes become fp16 values m + s c (one fused multiply-add: half
+//                    an fp16 step, 2^-11 relative); new keys and values are converted from bf16
+//                    (exact but for magnitudes below 2^-14).
+//   warp 24          issues the MMAs: S = Q K^T (128 x 128 x D, operands in shared memory) and
+//                    O += P V (P from TMEM, V as stored: the MN-major B operand).  The order S0 S1
+//                    [P0] O0 S0' [P1] O1 S1' ... keeps one stream's MMAs under the other's softmax.
+//                    The warp stays whole and one lane's instructions count, so that descriptors
+//                    are in uniform registers (moving them there cost 100 cycles an MMA).
+//   warp 25          copies the codes of cached tiles into a ring of two halves of tiles
 // Queries are scaled by a power of two so that a row's largest element is 2^9..2^10 (exact, as in
 // kv4_attn.cu).  Within 8 neighbouring dims the tiles hold them in the order 0 4 1 5 2 6 3 7, in
 // which masking a word of codes leaves them; queries are stored in the same order and the output's
@@ -33,9 +36,10 @@ namespace eagle {
 namespace {
 
 constexpr int kKeys = kKv4TcTile;
-constexpr int kThreads = 14 * 32;
-constexpr int kRaw = 3;  // halves of tiles (keys or values) of codes in flight
-constexpr float kTop = 12.0f, kAim = 9.0f;  // p <= 2^12; a new reference puts the largest at 2^9
+constexpr int kThreads = 26 * 32;
+constexpr int kFillWarps = 8;
+constexpr int kRaw = 2;  // halves of tiles (keys or values) of codes in flight
+constexpr float kTop = 15.0f, kAim = 4.0f;  // p <= 2^15; a new reference puts the largest at 2^4
 constexpr uint32_t kTmemCols = 512;
 
 template <int G>
@@ -61,14 +65,43 @@ __device__ __forceinline__ uint32_t sw128(uint32_t row, uint32_t chunk) {
     return (row >> 3) * 1024u + (row & 7u) * 128u + ((chunk ^ (row & 7u)) << 4);
 }
 
-// D[tmem] (+)= A[tmem] * B[smem]: fp16 in, fp32 accumulation.
-__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+// The MMAs and their commit, issued by the lane whose `leader` is set; the whole warp takes part.
+// D[tmem] (+)= A[smem] * B[smem] and D[tmem] += A[tmem] * B[smem], fp16 in, fp32 accumulation.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate, uint32_t leader) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(leader)
         : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b_desc, uint32_t idesc, uint32_t leader) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.eq.b32 p, 0, 0;\n\t"
+        "setp.ne.b32 q, %4, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b_desc), "r"(idesc), "r"(leader)
+        : "memory");
+}
+__device__ __forceinline__ void commit_to(uint64_t *bar, uint32_t leader) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+        "r"(leader)
+        : "memory");
+}
+__device__ __forceinline__ uint32_t elected() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void tmem_st_8(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
 }
 __device__ __forceinline__ void tmem_st_16(uint32_t taddr, const uint32_t (&r)[16]) {
     asm volatile(
@@ -130,12 +163,12 @@ __device__ __forceinline__ uint4 convert8(uint4 v, bool &odd) {
 }
 
 // The terms of elements that fp16 cannot hold, which count as 0 in the tiles: for the keys into the
-// row's scores (f: what the query was scaled by), for the values into its output, where the row sees
-// the key.  Warp-wide; `rows`: keys of the tile.
+// row's scores (f: what the query was scaled by; keys first .. last of the tile), for the values into
+// dims first .. last of its output, where the row sees the key.  Warp-wide; `rows`: keys of the tile.
 template <int D>
-static __device__ __noinline__ void add_odd_keys(const __nv_bfloat16 *kt, int64_t ld, int32_t rows, const __nv_bfloat16 *q,
-                                                 float f, uint32_t t_s) {
-    for (int32_t key = 0; key < rows; ++key) {
+static __device__ __noinline__ void add_odd_keys(const __nv_bfloat16 *kt, int64_t ld, int32_t first, int32_t last,
+                                                 const __nv_bfloat16 *q, float f, uint32_t t_s) {
+    for (int32_t key = first; key < last; ++key) {
         float add = 0.0f;
         bool any = false;
         for (int32_t d = 0; d < D; ++d) {
@@ -147,14 +180,13 @@ static __device__ __noinline__ void add_odd_keys(const __nv_bfloat16 *kt, int64_
         if (any) tmem_st_1(t_s + key, tmem_ld_1(t_s + key) + add);
     }
 }
-template <int D>
 static __device__ __noinline__ void add_odd_values(const __nv_bfloat16 *vt, int64_t ld, int32_t rows, uint4 see, float mul,
-                                                   float sub, uint32_t t_s, uint32_t t_o) {
+                                                   float sub, uint32_t t_s, uint32_t t_o, int32_t first, int32_t last) {
     for (int32_t key = 0; key < rows; ++key) {
         const float pv = ex2_approx(__fadd_rn(__fmul_rn(tmem_ld_1(t_s + key), mul), sub));
         const uint32_t word = key < 64 ? (key < 32 ? see.x : see.y) : (key < 96 ? see.z : see.w);
         const bool mine = (word >> (key & 31)) & 1u;
-        for (int32_t d = 0; d < D; ++d) {
+        for (int32_t d = first; d < last; ++d) {
             const float x = __bfloat162float(vt[key * ld + d]);
             if (!is_odd(x)) continue;
             const uint32_t col = (d & ~7) + ((d & 3) << 1) + ((d >> 2) & 1);  // the order 0 4 1 5 2 6 3 7
@@ -173,10 +205,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
     __shared__ TcBars bar;
     __shared__ uint32_t tmem_base;
     __shared__ int32_t abort_mark;
-    __shared__ __align__(4) uint8_t key_bits[4][16];  // by tile & 3: which of its 128 keys are there
+    __shared__ __align__(8) uint8_t key_bits[4][16];  // by tile & 3: which of its 128 keys are there
     __shared__ uint8_t raw_keys[kRaw][8];             // keys of each chunk that are there
-    __shared__ __align__(4) uint8_t odd_tile[4][2][4];     // by tile & 3, key or value, filling warp
-    __shared__ float2 stream_ml[2][128];      // one unit of at most 128 rows: maxima and sums
+    __shared__ __align__(8) uint8_t odd_tile[4][2][kFillWarps];  // by tile & 3, key or value, filling warp
+    __shared__ float half_max[2][2][2][128];  // stream, tile & 1, half of the keys, row
+    __shared__ float2 half_ml[2][2][128];     // stream, half, row: references and sums of a segment
     __shared__ Place place;
     __shared__ int64_t red[kThreads / 32];
     const int32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -184,18 +217,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
     const Kv4Attention &a = k.a;
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&bar.k_full[i], 4);
-            mbar_init(&bar.v_full[i], 4);
+            mbar_init(&bar.k_full[i], kFillWarps);
+            mbar_init(&bar.v_full[i], kFillWarps);
             mbar_init(&bar.k_empty[i], 1);
             mbar_init(&bar.v_empty[i], 1);
-            mbar_init(&bar.q_full[i], 128);
+            mbar_init(&bar.q_full[i], 256);
             mbar_init(&bar.s_full[i], 1);
-            mbar_init(&bar.p_full[i], 128);
+            mbar_init(&bar.p_full[i], 256);
             mbar_init(&bar.o_done[i], 1);
         }
         for (int i = 0; i < kRaw; ++i) {
             mbar_init(&bar.raw_full[i], 1);
-            mbar_init(&bar.raw_empty[i], 4);
+            mbar_init(&bar.raw_empty[i], kFillWarps);
         }
         mbar_init(&bar.drain, 1);
         abort_mark = 0;
@@ -208,14 +241,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
         if (threadIdx.x == 0) k.share[blockIdx.x].b = -1;
         return;
     }
-    if (warp == 12) {
+    if (warp == 24) {
         tmem_alloc(&tmem_base, kTmemCols);
         tmem_relinquish();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = tmem_base;
+    const uint32_t tmem = __shfl_sync(kFull, tmem_base, 0);
     const Place p = place;
     Walk w;
     w.start(k, p);
@@ -223,9 +256,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
     auto wait = [&](uint64_t *b, uint32_t parity) -> bool { return kv4_wait(b, parity, abort_flag); };
     auto rows_of = [&]() { return min(kKv4TcRows, k.Mq - w.qt * kKv4TcRows); };  // rows of the unit
 
-    if (warp >= 8 && warp < 12) {
+    if (warp >= 16 && warp < 24) {
         // ---------------- the tiles ----------------
-        const int32_t fw = warp - 8;
+        const int32_t fw = warp - 16;
         uint32_t gt = 0, raw = 0;  // tiles and halves of cached tiles so far
         do {
             for (int64_t s = w.s0; s < w.s1; ++s, ++gt) {
@@ -250,8 +283,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
                         uint8_t *to = dst + fw * 1024 + t8 * 128 + ((qq ^ t8) << 4);
                         const int32_t odd_g = ((((4 + qq) ^ t8) - (qq ^ t8)) << 4);
 #pragma unroll 2
-                        for (int32_t i = 0; i < 4; ++i) {
-                            const int32_t group = 4 * i + fw;
+                        for (int32_t i = 0; i < 2; ++i) {
+                            const int32_t group = kFillWarps * i + fw;
                             const uint8_t *part = src + (group >> 1) * S::kPart;
                             const int32_t slot = (group & 1) * 8 + slot8;
                             const int32_t here = max(0, min(8, static_cast<int32_t>(raw_keys[rs][group >> 1]) - 8 * (group & 1)));
@@ -283,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
                             }
 #pragma unroll
                             for (int g = 0; g < G; ++g)
-                                *reinterpret_cast<uint4 *>(to + i * 4096 + (g >> 1) * (kKeys * 128) + (g & 1 ? odd_g : 0)) = dequant8(c[g], sm[g]);
+                                *reinterpret_cast<uint4 *>(to + i * (kFillWarps * 1024) + (g >> 1) * (kKeys * 128) + (g & 1 ? odd_g : 0)) = dequant8(c[g], sm[g]);
                         }
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&bar.raw_empty[rs]);
@@ -296,10 +329,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
                         const int32_t rows = static_cast<int32_t>(min(a.n - s * kKeys, int64_t{kKeys}));
 #pragma unroll 1
                         for (int32_t sub = 0; sub < D / 64; ++sub) {
-                            uint4 v[8];
+                            uint4 v[4];
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const int32_t row = (sub * 8 + i) * 4 * kRowsWarp + first;
+                            for (int i = 0; i < 4; ++i) {
+                                const int32_t row = (sub * 4 + i) * kFillWarps * kRowsWarp + first;
                                 v[i] = row < rows ? *reinterpret_cast<const uint4 *>(src + row * a.ldkv) : make_uint4(0, 0, 0, 0);
                             }
                             if (sub == 0) {
@@ -307,8 +340,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
                                 __syncwarp();
                             }
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const int32_t row = (sub * 8 + i) * 4 * kRowsWarp + first;
+                            for (int i = 0; i < 4; ++i) {
+                                const int32_t row = (sub * 4 + i) * kFillWarps * kRowsWarp + first;
                                 *reinterpret_cast<uint4 *>(dst + (ch >> 3) * (kKeys * 128) + sw128(row, ch & 7)) = convert8(v[i], odd);
                             }
                         }
@@ -321,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
                 }
             }
         } while (w.next(k, p));
-    } else if (warp == 13) {
+    } else if (warp == 25) {
         // ---------------- copies of codes: a stage is the keys or the values of a cached tile -------
         uint32_t raw = 0;
         bool dead = false;
@@ -360,65 +393,65 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
         if (lane == 0)
             for (uint32_t i = raw > kRaw ? raw - kRaw : 0; i < raw; ++i) mbar_wait(&bar.raw_full[i % kRaw], (i / kRaw) & 1u, nullptr);
         __syncwarp();
-    } else if (warp == 12) {
-        // ---------------- MMA issue (one thread) ----------------
-        if (lane == 0) {
-            constexpr uint32_t idesc_s = idesc_f16(128, kKeys), idesc_o = idesc_f16_bmn(128, D);
-            uint32_t gt = 0, seg = 0, jobs[2] = {0, 0};  // tiles, segments, P's of each stream so far
-            bool ok = true;
-            do {
-                const int32_t tiles = static_cast<int32_t>(w.s1 - w.s0);
-                const bool both = rows_of() > 128;
-                const int32_t n = both ? 2 * tiles : tiles;
-                auto tile_of = [&](int32_t q) { return both ? q >> 1 : q; };
-                // the last job that reads a tile's keys or values
-                auto last_of_tile = [&](int32_t q) { return !both || (q & 1); };
-                auto issue_s = [&](int32_t q) -> bool {
-                    const uint32_t t = gt + tile_of(q), st = t & 1u, j = q & 1;
-                    if (!wait(&bar.k_full[st], t >> 1)) return false;
-                    tc_fence_after();
-                    const uint32_t q0 = smem_u32(base + S::kQ + j * S::kTileBytes), k0 = smem_u32(base + S::kK + st * S::kTileBytes);
+    } else if (warp == 24) {
+        // ---------------- MMA issue ----------------
+        constexpr uint32_t idesc_s = idesc_f16(128, kKeys), idesc_o = idesc_f16_bmn(128, D);
+        constexpr uint32_t kStep = S::kTileBytes >> 4;  // descriptors count in 16 bytes
+        const uint32_t leader = elected();
+        uint32_t gt = 0, seg = 0, jobs0 = 0, jobs1 = 0;  // tiles, segments, P's of each stream so far
+        const uint64_t q_desc = sw128_kmajor_desc(smem_u32(base + S::kQ)), k_desc = sw128_kmajor_desc(smem_u32(base + S::kK));
+        const uint64_t v_desc = sw128_desc(smem_u32(base + S::kV), kKeys * 128u, 1024u);
+        bool ok = true;
+        do {
+            const int32_t tiles = __shfl_sync(kFull, static_cast<int32_t>(w.s1 - w.s0), 0);
+            const uint32_t both = __shfl_sync(kFull, rows_of() > 128 ? 1 : 0, 0);
+            const int32_t n = tiles << both;
+            auto issue_s = [&](int32_t q) -> bool {
+                const uint32_t t = gt + (q >> both), st = t & 1u, j = q & 1;
+                if (!wait(&bar.k_full[st], t >> 1)) return false;
+                tc_fence_after();
+                const uint64_t qd = q_desc + j * kStep, kd = k_desc + st * kStep;
+                const uint32_t d = tmem + j * 128u;
 #pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint32_t off = (kk >> 2) * (kKeys * 128u) + (kk & 3) * 32u;
-                        mma_bf16_ss(tmem + j * 128u, sw128_kmajor_desc(q0 + off), sw128_kmajor_desc(k0 + off), idesc_s, kk > 0);
-                    }
-                    mma_commit(&bar.s_full[j]);
-                    if (last_of_tile(q)) mma_commit(&bar.k_empty[st]);
-                    return true;
-                };
-                for (int32_t j = 0; j < 2 && ok; ++j) {
-                    ok = wait(&bar.q_full[j], seg);
-                    if (ok && j < n) ok = issue_s(j);
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t off = ((kk >> 2) * (kKeys * 128u) + (kk & 3) * 32u) >> 4;
+                    mma_ss(d, qd + off, kd + off, idesc_s, kk > 0, leader);
                 }
-                for (int32_t q = 0; q < n && ok; ++q) {
-                    const uint32_t t = gt + tile_of(q), st = t & 1u, j = q & 1;
-                    ok = wait(&bar.v_full[st], t >> 1) && wait(&bar.p_full[j], jobs[j]);
-                    if (!ok) break;
-                    ++jobs[j];
-                    tc_fence_after();
-                    const uint32_t v0 = smem_u32(base + S::kV + st * S::kTileBytes);
+                commit_to(&bar.s_full[j], leader);
+                if (!both || j) commit_to(&bar.k_empty[st], leader);  // the tile's last reader
+                return true;
+            };
+            ok = wait(&bar.q_full[0], seg) && issue_s(0);
+            ok = ok && wait(&bar.q_full[1], seg) && (n < 2 || issue_s(1));
+            for (int32_t q = 0; q < n && ok; ++q) {
+                const uint32_t t = gt + (q >> both), st = t & 1u, j = q & 1;
+                ok = wait(&bar.v_full[st], t >> 1) && wait(&bar.p_full[j], j ? jobs1 : jobs0);
+                if (!ok) break;
+                if (j) ++jobs1;
+                else ++jobs0;
+                tc_fence_after();
+                const uint64_t vd = v_desc + st * kStep;
+                const uint32_t d = tmem + 256u + j * 128u, pa = tmem + j * 128u;
 #pragma unroll
-                    for (int kk = 0; kk < kKeys / 16; ++kk)
-                        mma_f16_ts(tmem + 256u + j * 128u, tmem + j * 128u + kk * 8u, sw128_desc(v0 + kk * 2048u, kKeys * 128u, 1024u),
-                                   idesc_o, 1u);
-                    if (q + 2 >= n) mma_commit(&bar.o_done[j]);
-                    if (last_of_tile(q)) mma_commit(&bar.v_empty[st]);
-                    if (q + 2 < n) ok = issue_s(q + 2);
-                }
-                gt += tiles;
-                ++seg;
-            } while (ok && w.next(k, p));
-            // what was issued lands before the block's memory is handed on
-            mma_commit(&bar.drain);
-            mbar_wait(&bar.drain, 0, nullptr);
-        }
+                for (int kk = 0; kk < kKeys / 16; ++kk)  // keys 64 .. 127 lie 64 columns on
+                    mma_ts(d, pa + (kk & 3) * 8u + (kk >> 2) * 64u, vd + kk * 128u, idesc_o, leader);
+                if (q + 2 >= n) commit_to(&bar.o_done[j], leader);
+                if (!both || j) commit_to(&bar.v_empty[st], leader);
+                if (q + 2 < n) ok = issue_s(q + 2);
+            }
+            gt += tiles;
+            ++seg;
+        } while (ok && w.next(k, p));
+        // what was issued lands before the block's memory is handed on
+        commit_to(&bar.drain, leader);
+        mbar_wait(&bar.drain, 0, nullptr);
         __syncwarp();
-    } else if (warp < 8) {
+    } else if (warp < 16) {
         // ---------------- softmax and output ----------------
-        const int32_t j = warp >> 2, r = threadIdx.x & 127;  // stream, row of the stream
+        // stream, half of a tile's keys (and of the output's columns), row of the stream
+        const int32_t j = warp >> 3, h = (warp >> 2) & 1, r = (warp & 3) * 32 + lane;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        const uint32_t t_s = tmem + lanes + j * 128u, t_o = tmem + lanes + 256u + j * 128u;
+        const uint32_t t_s = tmem + lanes + j * 128u, t_h = t_s + 64 * h, t_o = tmem + lanes + 256u + j * 128u;
         uint32_t gt = 0, n_s = 0, n_o = 0;  // tiles, scores and outputs of this stream so far
         do {
             const int32_t unit_rows = rows_of();
@@ -443,7 +476,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
                 mul = __uint_as_float(static_cast<uint32_t>(e - 9) << 23) * k.scale2;
                 uint8_t *dst = base + S::kQ + j * S::kTileBytes;
 #pragma unroll 2
-                for (int c = 0; c < D / 8; ++c) {
+                for (int i = 0; i < D / 16; ++i) {
+                    const int32_t c = h * (D / 16) + i;
                     const uint4 v = piece(c);
                     *reinterpret_cast<uint4 *>(dst + (c >> 3) * (kKeys * 128) + sw128(r, c & 7)) =
                         make_uint4(pack_f16(bf_lo(v.x) * f, bf_lo(v.z) * f), pack_f16(bf_hi(v.x) * f, bf_hi(v.z) * f),
@@ -452,15 +486,22 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
                 fence_proxy_async_smem();
                 mbar_arrive(&bar.q_full[j]);
             }
-            const uint32_t *mrow = a.mask ? a.mask + (static_cast<int64_t>(w.b) * a.n + node) * k.W : nullptr;
             {
-                uint32_t z[32];
+                uint32_t z[16];
 #pragma unroll
-                for (int i = 0; i < 32; ++i) z[i] = 0u;
+                for (int i = 0; i < 16; ++i) z[i] = 0u;
 #pragma unroll
-                for (int c = 0; c < D / 32; ++c) tmem_st_32(t_o + 32 * c, z);
+                for (int c = 0; c < D / 32; ++c) tmem_st_16(t_o + h * (D / 2) + 16 * c, z);
                 tmem_wait_st();
             }
+            const uint32_t *mrow = a.mask ? a.mask + (static_cast<int64_t>(w.b) * a.n + node) * k.W : nullptr;
+            // which of new keys k0 .. k0 + 31 the row sees
+            auto new_seen = [&](int32_t k0) {
+                const int32_t left = a.n - k0, own = node - k0;  // causal: nodes 0..node
+                uint32_t v = own >= 31 ? kFull : (own >= 0 ? (2u << own) - 1u : 0u);
+                if (mrow) v = left > 0 ? mrow[k0 >> 5] : 0u;
+                return v & (left >= 32 ? kFull : (left > 0 ? (1u << left) - 1u : 0u));
+            };
             float ref = -INFINITY, l = 0.0f;
             const int32_t tiles = static_cast<int32_t>(w.s1 - w.s0);
             int32_t done = 0;  // tiles of this segment that this stream took
@@ -468,63 +509,53 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
                 const int64_t s = w.s0 + ti;
                 const uint32_t t = gt + ti;
                 wait(&bar.s_full[j], n_s);
-                ++n_s;
                 __syncwarp();
                 tc_fence_after();
-                // which keys of the tile the row sees
-                uint32_t see[4];
-                bool all = true, odd_k = false, odd_v = false;
+                // which of this half's keys the row sees
+                uint32_t see0, see1;
+                bool odd_k = false, odd_v = false;
                 if (s >= w.nt) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) see[i] = reinterpret_cast<const volatile uint32_t *>(key_bits[t & 3])[i];
+                    const uint2 b = *reinterpret_cast<const uint2 *>(key_bits[t & 3] + 8 * h);
+                    see0 = b.x;
+                    see1 = b.y;
                 } else {
-                    const int32_t key0 = static_cast<int32_t>(s) * kKeys;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int32_t k0 = key0 + 32 * i, left = a.n - k0;
-                        const uint32_t in = left >= 32 ? kFull : (left > 0 ? (1u << left) - 1u : 0u);
-                        const int32_t own = node - k0;  // causal: nodes 0..node
-                        uint32_t v = own >= 31 ? kFull : (own >= 0 ? (2u << own) - 1u : 0u);
-                        if (mrow) v = left > 0 ? mrow[k0 >> 5] : 0u;
-                        see[i] = v & in;
-                    }
+                    const int32_t key0 = static_cast<int32_t>(s) * kKeys + 64 * h;
+                    see0 = new_seen(key0);
+                    see1 = new_seen(key0 + 32);
                     // the tile's values have come too: whether it holds what fp16 does not
                     wait(&bar.v_full[t & 1], t >> 1);
                     __syncwarp();
-                    odd_k = *reinterpret_cast<const volatile uint32_t *>(odd_tile[t & 3][0]) != 0;
-                    odd_v = *reinterpret_cast<const volatile uint32_t *>(odd_tile[t & 3][1]) != 0;
+                    odd_k = *reinterpret_cast<const volatile unsigned long long *>(odd_tile[t & 3][0]) != 0;
+                    odd_v = *reinterpret_cast<const volatile unsigned long long *>(odd_tile[t & 3][1]) != 0;
                 }
-                if (!live) see[0] = see[1] = see[2] = see[3] = 0u;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) all = all && see[i] == kFull;
-                all = __all_sync(kFull, all);
+                if (!live) see0 = see1 = 0u;
+                const bool all = __all_sync(kFull, (see0 & see1) == kFull);
                 const int64_t new_row = (static_cast<int64_t>(w.b) * a.n + s * kKeys) * a.ldkv + static_cast<int64_t>(w.hk) * D;
                 const int32_t new_rows = static_cast<int32_t>(min(a.n - s * kKeys, int64_t{kKeys}));
-                if (odd_k) add_odd_keys<D>(a.kn + new_row, a.ldkv, new_rows, q_src, f, t_s);
-                float mx = -INFINITY;
-                if (all) {
+                if (odd_k) add_odd_keys<D>(a.kn + new_row, a.ldkv, 64 * h, min(new_rows, 64 * h + 64), q_src, f, t_s);
+                float mx;
+                {
                     float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
+                    for (int c = 0; c < 2; ++c) {
                         uint32_t v[32];
-                        tmem_ld_32(t_s + 32 * c, v);
+                        tmem_ld_32(t_h + 32 * c, v);
                         tmem_wait_ld();
+                        if (!all) {
+                            const uint32_t bits = c ? see1 : see0;
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) m4[i & 3] = fmaxf(m4[i & 3], __uint_as_float(v[i]));
+                            for (int i = 0; i < 32; ++i) v[i] = (bits >> i) & 1u ? v[i] : __float_as_uint(-INFINITY);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) m4[(i >> 1) & 3] = fmaxf(fmaxf(m4[(i >> 1) & 3], __uint_as_float(v[i])), __uint_as_float(v[i + 1]));
                     }
                     mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-                } else {
-                    uint32_t bits[4] = {see[0], see[1], see[2], see[3]};
-#pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t v[32];
-                        tmem_ld_32(t_s + 32 * c, v);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) mx = fmaxf(mx, (bits[0] >> i) & 1u ? __uint_as_float(v[i]) : -INFINITY);
-                        bits[0] = bits[1], bits[1] = bits[2], bits[2] = bits[3];
-                    }
                 }
+                // the row's maximum over both halves
+                half_max[j][n_s & 1][h][r] = mx;
+                named_barrier_sync(1 + j, 256);
+                mx = fmaxf(mx, half_max[j][n_s & 1][h ^ 1][r]);
+                ++n_s;
                 mx = mx == -INFINITY ? mx : mx * mul;  // mul may underflow to 0
                 float corr = 1.0f;
                 if (mx - ref > kTop) {
@@ -538,50 +569,52 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
                     // the scores' arrival says that the stream's earlier products are complete
 #pragma unroll 1
                     for (int c = 0; c < D / 32; ++c) {
-                        uint32_t v[32];
-                        tmem_ld_32(t_o + 32 * c, v);
+                        uint32_t v[16];
+                        tmem_ld_16(t_o + h * (D / 2) + 16 * c, v);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * corr);
-                        tmem_st_32(t_o + 32 * c, v);
+                        for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * corr);
+                        tmem_st_16(t_o + h * (D / 2) + 16 * c, v);
                     }
                     tmem_wait_st();
                 }
-                if (odd_v)
-                    add_odd_values<D>(a.vn + new_row, a.ldkv, new_rows, make_uint4(see[0], see[1], see[2], see[3]), mul, sub, t_s, t_o);
+                if (odd_v) {
+                    const int32_t key0 = static_cast<int32_t>(s) * kKeys;
+                    uint4 see = make_uint4(0u, 0u, 0u, 0u);
+                    if (live) see = make_uint4(new_seen(key0), new_seen(key0 + 32), new_seen(key0 + 64), new_seen(key0 + 96));
+                    add_odd_values(a.vn + new_row, a.ldkv, new_rows, see, mul, sub, t_s, t_o, h * (D / 2), (h + 1) * (D / 2));
+                    named_barrier_sync(1 + j, 256);  // both halves have read the scores that p overwrites
+                }
                 // One product and difference; scores so large that the product's rounding matters next
                 // to their differences (and could pass for a score above the maximum) in two steps,
                 // as the maximum was formed.
                 auto exponentials = [&](auto exponent, auto masked) {
-                    uint32_t bits[4] = {see[0], see[1], see[2], see[3]};
 #pragma unroll 1
                     for (int c = 0; c < 4; ++c) {
-                        uint32_t v[32], pk[16];
-                        tmem_ld_32(t_s + 32 * c, v);
+                        uint32_t v[16], pk[8];
+                        tmem_ld_16(t_h + 16 * c, v);
                         tmem_wait_ld();
+                        const uint32_t bits = (c < 2 ? see0 : see1) >> (16 * (c & 1));
                         float sum[2] = {0.0f, 0.0f};
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
+                        for (int i = 0; i < 8; ++i) {
                             float p0 = ex2_approx(exponent(__uint_as_float(v[2 * i])));
                             float p1 = ex2_approx(exponent(__uint_as_float(v[2 * i + 1])));
                             if constexpr (decltype(masked)::value) {
-                                p0 = (bits[0] >> (2 * i)) & 1u ? p0 : 0.0f;
-                                p1 = (bits[0] >> (2 * i + 1)) & 1u ? p1 : 0.0f;
+                                p0 = (bits >> (2 * i)) & 1u ? p0 : 0.0f;
+                                p1 = (bits >> (2 * i + 1)) & 1u ? p1 : 0.0f;
                             }
                             sum[i & 1] += p0 + p1;
                             pk[i] = pack_f16(p0, p1);
                         }
                         l += sum[0] + sum[1];
-                        tmem_st_16(t_s + 16 * c, pk);
-                        if constexpr (decltype(masked)::value) bits[0] = bits[1], bits[1] = bits[2], bits[2] = bits[3];
+                        tmem_st_8(t_h + 8 * c, pk);
                     }
                 };
-                if (__any_sync(kFull, fabsf(sub) > 1048576.0f))
-                    exponentials([&](float x) { return __fadd_rn(__fmul_rn(x, mul), sub); }, std::true_type{});
-                else if (all)
+                if (all && !__any_sync(kFull, fabsf(sub) > 1048576.0f))
                     exponentials([&](float x) { return fmaf(x, mul, sub); }, std::false_type{});
                 else
-                    exponentials([&](float x) { return fmaf(x, mul, sub); }, std::true_type{});
+                    exponentials([&](float x) { return __fadd_rn(__fmul_rn(x, mul), sub); }, std::true_type{});
                 tmem_wait_st();
                 tc_fence_before();
                 mbar_arrive(&bar.p_full[j]);
@@ -593,74 +626,75 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
                 ++n_o;
             }
             __syncwarp();
+            // the halves' sums, and of a unit of at most 128 rows both streams' shares
+            half_ml[j][h][r] = make_float2(ref, l);
+            tc_fence_before();
+            if (both) named_barrier_sync(1 + j, 256);
+            else named_barrier_sync(3, 512);
             tc_fence_after();
             const bool whole = w.s0 == 0 && w.s1 == w.unit;
             const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (w.t == p.begin ? 0 : 1);
-            float M = ref, L = l, w0 = 1.0f, w1 = 0.0f;
             const uint32_t o_first = tmem + lanes + 256u;
-            if (!both) {
-                // the two streams' shares: each thread sees both and writes half of the columns
-                stream_ml[j][r] = make_float2(ref, l);
-                tc_fence_before();
-                named_barrier_sync(1, 256);
-                tc_fence_after();
-                const float2 m0 = stream_ml[0][r], m1 = stream_ml[1][r];
-                M = fmaxf(m0.x, m1.x);
+            float M, L, w0 = 1.0f, w1 = 0.0f;
+            if (both) {
+                M = ref;
+                L = half_ml[j][0][r].y + half_ml[j][1][r].y;
+            } else {
+                const float m0 = half_ml[0][0][r].x, m1 = half_ml[1][0][r].x;
+                const float l0 = half_ml[0][0][r].y + half_ml[0][1][r].y, l1 = half_ml[1][0][r].y + half_ml[1][1][r].y;
+                M = fmaxf(m0, m1);
                 // a stream whose scores are all NaN has no maximum and a sum of NaN
-                w0 = m0.x == -INFINITY ? (m0.y == 0.0f ? 0.0f : m0.y) : ex2_approx(m0.x - M);
-                w1 = m1.x == -INFINITY ? (m1.y == 0.0f ? 0.0f : m1.y) : ex2_approx(m1.x - M);
-                L = w0 * m0.y + w1 * m1.y;
+                w0 = m0 == -INFINITY ? (l0 == 0.0f ? 0.0f : l0) : ex2_approx(m0 - M);
+                w1 = m1 == -INFINITY ? (l1 == 0.0f ? 0.0f : l1) : ex2_approx(m1 - M);
+                L = w0 * l0 + w1 * l1;
             }
             const float inv = L == 0.0f ? 0.0f : 1.0f / L;
             const bool ok = !*abort_flag;
-            const int32_t c_begin = both ? 0 : j * (D / 64), c_end = both ? D / 32 : (j + 1) * (D / 64);
+            // 16 columns at a time: a half of the stream's, or a quarter of both streams' sum
+            const int32_t first = both ? h * (D / 2) : (2 * j + h) * (D / 4), cols = both ? D / 2 : D / 4;
 #pragma unroll 1
-            for (int32_t c = c_begin; c < c_end; ++c) {
-                float x[32];
+            for (int32_t c = first; c < first + cols; c += 16) {
+                float x[16];
                 {
-                    uint32_t v[32];
-                    if (both) {
-                        tmem_ld_32(t_o + 32 * c, v);
+                    uint32_t v[16];
+                    tmem_ld_16((both ? t_o : o_first) + c, v);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) x[i] = w0 == 0.0f ? 0.0f : w0 * __uint_as_float(v[i]);
+                    if (!both) {
+                        tmem_ld_16(o_first + 128u + c, v);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(v[i]);
-                    } else {
-                        tmem_ld_32(o_first + 32 * c, v);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) x[i] = w0 == 0.0f ? 0.0f : w0 * __uint_as_float(v[i]);
-                        tmem_ld_32(o_first + 128u + 32 * c, v);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) x[i] = w1 == 0.0f ? x[i] : fmaf(w1, __uint_as_float(v[i]), x[i]);
+                        for (int i = 0; i < 16; ++i) x[i] = w1 == 0.0f ? x[i] : fmaf(w1, __uint_as_float(v[i]), x[i]);
                     }
                 }
                 if (L == 0.0f) {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) x[i] = 0.0f;
+                    for (int i = 0; i < 16; ++i) x[i] = 0.0f;
                 }
                 if (!live || !ok) continue;
                 // columns 8 i + (0 .. 7) are dims 8 i + (0 4 1 5 2 6 3 7)
                 if (whole) {
-                    __nv_bfloat16 *dst = a.o + ((static_cast<int64_t>(w.b) * a.n + node) * a.H + head) * D + 32 * c;
+                    __nv_bfloat16 *dst = a.o + ((static_cast<int64_t>(w.b) * a.n + node) * a.H + head) * D + c;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
+                    for (int i = 0; i < 2; ++i)
                         *reinterpret_cast<uint4 *>(dst + 8 * i) =
                             make_uint4(pack_b16(x[8 * i] * inv, x[8 * i + 2] * inv), pack_b16(x[8 * i + 4] * inv, x[8 * i + 6] * inv),
                                        pack_b16(x[8 * i + 1] * inv, x[8 * i + 3] * inv), pack_b16(x[8 * i + 5] * inv, x[8 * i + 7] * inv));
                 } else {
-                    float *dst = k.part_o + (slot * k.rows + ur) * D + 32 * c;
+                    float *dst = k.part_o + (slot * k.rows + ur) * D + c;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
+                    for (int i = 0; i < 2; ++i) {
                         *reinterpret_cast<float4 *>(dst + 8 * i) = make_float4(x[8 * i], x[8 * i + 2], x[8 * i + 4], x[8 * i + 6]);
                         *reinterpret_cast<float4 *>(dst + 8 * i + 4) = make_float4(x[8 * i + 1], x[8 * i + 3], x[8 * i + 5], x[8 * i + 7]);
                     }
                 }
             }
-            if (!whole && live && ok && (both || j == 0)) k.part_ml[slot * k.rows + ur] = make_float2(M, L);
+            if (!whole && live && ok && h == 0 && (both || j == 0)) k.part_ml[slot * k.rows + ur] = make_float2(M, L);
             tc_fence_before();
-            // neither stream's outputs are overwritten before both have been read
-            if (!both) named_barrier_sync(1, 256);
+            // no output column or sum is overwritten before all of its readers have it
+            if (both) named_barrier_sync(1 + j, 256);
+            else named_barrier_sync(3, 512);
         } while (w.next(k, p));
     }
 
@@ -669,7 +703,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 12) {
+    if (warp == 24) {
         __syncwarp();
         tmem_dealloc(tmem, kTmemCols);
     }

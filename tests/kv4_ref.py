@@ -62,8 +62,9 @@ def attend(q, kc, vc, kn, vn, see):
       cached k, v to fp16        2^-11 of their size and 2^-25: the exponent is off by 2^-11 A +
                                  2^-25 sum |q| / sqrt(D) more, v by 2^-11 |v| + 2^-25
       new k, v to fp16           exact but for 2^-25 below 2^-14: the same 2^-25 terms
-      p to fp16                  2^-11 |v|; below 2^-14 at most 2^-25 where the largest is 2^9 or
-                                 more: N 2^-34 of the largest |v|
+      p to fp16                  2^-11 |v|; below 2^-14 at most 2^-25 where the largest is 2^4 or
+                                 more (a reference puts a row's largest p at 2^4, later ones pass
+                                 it): N 2^-29 of the largest |v|
     """
     n, H, D = q.shape
     Hk = kc.shape[1]
@@ -100,7 +101,7 @@ def attend(q, kc, vc, kn, vn, see):
         vfin = torch.nan_to_num(seen_v, posinf=0.0, neginf=0.0).abs()
         mag = torch.einsum("hnt,thd->nhd", p * (2.0 ** -10 + 2.0 ** -19 + 2 * delta), vfin)
         big = vfin.amax(0)[None]
-        return o, 2.0 ** -8 * torch.nan_to_num(o).abs() * 1.001 + mag + 2.0 ** -25 + k.shape[0] * 2.0 ** -34 * big
+        return o, 2.0 ** -8 * torch.nan_to_num(o).abs() * 1.001 + mag + 2.0 ** -25 + k.shape[0] * 2.0 ** -29 * big
     mag = torch.einsum("hnt,thd->nhd", p * (2.0 ** -10 + 2.0 ** -19 + 2 * delta),
                        torch.nan_to_num(size.repeat_interleave(rep, 1), posinf=0.0))
     tol = 2.0 ** -8 * torch.nan_to_num(o).abs() * 1.001 + mag + 15 * k.shape[0] * (2.0 ** -25 if steep else 2.0 ** -34)
