@@ -93,8 +93,8 @@ __global__ void __launch_bounds__(kThreads, Shape<G, NQ>::kBlocks) kv4_attention
     __shared__ uint64_t full[kStages], empty[kStages];
     __shared__ int32_t valid[kStages][4];  // keys of each chunk of the stage (0..16)
     __shared__ int32_t abort_mark;
-    __shared__ Place place;
     __shared__ int64_t red[kThreads / 32];
+    __shared__ Spot spots[2];
     const int32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
@@ -107,12 +107,13 @@ __global__ void __launch_bounds__(kThreads, Shape<G, NQ>::kBlocks) kv4_attention
     pdl_launch_dependents();
     pdl_wait();
     const Kv4Attention &a = k.a;
-    const bool busy = find_place(k, &place, red);  // its barriers also publish the mbarriers
+    Place p;
+    const bool busy = find_place(k, &p, red, spots);
+    __syncthreads();  // the mbarriers too
     if (!busy) {
         if (threadIdx.x == 0) k.share[blockIdx.x].b = -1;
         return;
     }
-    const Place p = place;
     volatile int32_t *abort_flag = &abort_mark;
     Walk w;
     w.start(k, p);
@@ -579,7 +580,7 @@ __global__ void __launch_bounds__(kThreads, Shape<G, NQ>::kBlocks) kv4_attention
             if (threadIdx.x == 0) latch(a.status, kDevTimeout);
         } else {
             const bool whole = w.s0 == 0 && w.s1 == w.unit;
-            const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (w.t == p.begin ? 0 : 1);
+            const int64_t slot = slot_of(w);
             for (int32_t it = threadIdx.x; it < kRows * (D / 4); it += kWarps * 32) {
                 const int32_t r = it / (D / 4), c4 = it - r * (D / 4), row = w.qt * kRows + r;
                 if (row >= k.Mq) break;
@@ -629,7 +630,7 @@ __global__ void __launch_bounds__(128) kv4_merge_kernel(const __grid_constant__ 
     const int32_t rows = min(k.rows, k.Mq - sh.qt * k.rows);
     for (int32_t it = threadIdx.x + blockIdx.y * 128; it < rows * quads; it += 128 * gridDim.y) {
         const int32_t r = it / quads, c4 = it - r * quads;
-        auto slot = [&](int32_t c) { return 2 * static_cast<int64_t>(c) + (c == sh.first ? sh.first_slot : 0); };
+        auto slot = [&](int32_t c) { return 2 * static_cast<int64_t>(c) + (c == sh.first ? 1 : 0); };
         float M = -INFINITY;
         for (int32_t c = sh.first; c <= sh.last; ++c) M = fmaxf(M, k.part_ml[slot(c) * k.rows + r].x);
         float L = 0.0f;
@@ -742,6 +743,7 @@ cudaError_t launch_kv4_attention(const Kv4Attention &a, cudaStream_t st) {
     const int64_t tile = v.kernel ? kTile : kKv4TcTile;
     k.tile_shift = v.kernel ? 6 : 7;
     k.min_tiles = v.kernel ? kMinTiles : 1;
+    k.snap = v.kernel ? 1 : 5;
     k.scale2 = kLog2e / sqrtf(static_cast<float>(G * kKv4Group));
     const int32_t full = grid_of(*d, G, v);
     uint8_t *ws = static_cast<uint8_t *>(a.ws);

@@ -208,10 +208,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
     __shared__ __align__(8) uint8_t key_bits[4][16];  // by tile & 3: which of its 128 keys are there
     __shared__ uint8_t raw_keys[kRaw][8];             // keys of each chunk that are there
     __shared__ __align__(8) uint8_t odd_tile[4][2][kFillWarps];  // by tile & 3, key or value, filling warp
-    __shared__ float half_max[2][2][2][128];  // stream, tile & 1, half of the keys, row
+    __shared__ float half_max[2][2][2][128];  // stream, exchange & 1, half, row
     __shared__ float2 half_ml[2][2][128];     // stream, half, row: references and sums of a segment
-    __shared__ Place place;
     __shared__ int64_t red[kThreads / 32];
+    __shared__ Spot spots[2];
     const int32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     volatile int32_t *abort_flag = &abort_mark;
     const Kv4Attention &a = k.a;
@@ -236,7 +236,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
     }
     pdl_launch_dependents();
     pdl_wait();
-    const bool busy = find_place(k, &place, red);
+    Place p;
+    const bool busy = find_place(k, &p, red, spots);
     if (!busy) {
         if (threadIdx.x == 0) k.share[blockIdx.x].b = -1;
         return;
@@ -249,7 +250,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(kFull, tmem_base, 0);
-    const Place p = place;
     Walk w;
     w.start(k, p);
     if (threadIdx.x == 0) k.share[blockIdx.x] = share_of(k, p, w);
@@ -453,6 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t t_s = tmem + lanes + j * 128u, t_h = t_s + 64 * h, t_o = tmem + lanes + 256u + j * 128u;
         uint32_t gt = 0, n_s = 0, n_o = 0;  // tiles, scores and outputs of this stream so far
+        uint32_t buf = 0;                   // of half_max: another one at every exchange
         do {
             const int32_t unit_rows = rows_of();
             const bool both = unit_rows > 128;
@@ -462,26 +463,31 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
             const __nv_bfloat16 *q_src = a.q + (static_cast<int64_t>(w.b) * a.n + node) * a.ldq + static_cast<int64_t>(head) * D;
             float f, mul;  // what the query was scaled by; what makes its scores base 2
             {
-                float big = 0.0f;
-                auto piece = [&](int c) { return live ? *reinterpret_cast<const uint4 *>(q_src + 8 * c) : make_uint4(0, 0, 0, 0); };
-#pragma unroll 4
-                for (int c = 0; c < D / 8; ++c) {
-                    const uint4 v = piece(c);
-                    const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
+                uint4 v[D / 16];  // this half of the row
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) big = fmaxf(big, fmaxf(fabsf(bf_lo(vw[i])), fabsf(bf_hi(vw[i]))));
+                for (int i = 0; i < D / 16; ++i)
+                    v[i] = live ? *reinterpret_cast<const uint4 *>(q_src + h * (D / 2) + 8 * i) : make_uint4(0, 0, 0, 0);
+                float big = 0.0f;
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) {
+                    const uint32_t vw[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) big = fmaxf(big, fmaxf(fabsf(bf_lo(vw[u])), fabsf(bf_hi(vw[u]))));
                 }
+                half_max[j][buf][h][r] = big;
+                named_barrier_sync(1 + j, 256);
+                big = fmaxf(big, half_max[j][buf][h ^ 1][r]);
+                buf ^= 1;
                 const int32_t e = max(static_cast<int32_t>(__float_as_uint(big) >> 23), 10);
                 f = __uint_as_float(static_cast<uint32_t>(263 - e) << 23);
                 mul = __uint_as_float(static_cast<uint32_t>(e - 9) << 23) * k.scale2;
                 uint8_t *dst = base + S::kQ + j * S::kTileBytes;
-#pragma unroll 2
+#pragma unroll
                 for (int i = 0; i < D / 16; ++i) {
                     const int32_t c = h * (D / 16) + i;
-                    const uint4 v = piece(c);
                     *reinterpret_cast<uint4 *>(dst + (c >> 3) * (kKeys * 128) + sw128(r, c & 7)) =
-                        make_uint4(pack_f16(bf_lo(v.x) * f, bf_lo(v.z) * f), pack_f16(bf_hi(v.x) * f, bf_hi(v.z) * f),
-                                   pack_f16(bf_lo(v.y) * f, bf_lo(v.w) * f), pack_f16(bf_hi(v.y) * f, bf_hi(v.w) * f));
+                        make_uint4(pack_f16(bf_lo(v[i].x) * f, bf_lo(v[i].z) * f), pack_f16(bf_hi(v[i].x) * f, bf_hi(v[i].z) * f),
+                                   pack_f16(bf_lo(v[i].y) * f, bf_lo(v[i].w) * f), pack_f16(bf_hi(v[i].y) * f, bf_hi(v[i].w) * f));
                 }
                 fence_proxy_async_smem();
                 mbar_arrive(&bar.q_full[j]);
@@ -508,20 +514,22 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
             for (int32_t ti = both ? 0 : j; ti < tiles; ti += both ? 1 : 2, ++done) {
                 const int64_t s = w.s0 + ti;
                 const uint32_t t = gt + ti;
+                // which of this half's keys the row sees
+                uint32_t see0 = 0u, see1 = 0u;
+                bool odd_k = false, odd_v = false;
+                if (s < w.nt) {
+                    const int32_t key0 = static_cast<int32_t>(s) * kKeys + 64 * h;
+                    see0 = new_seen(key0);
+                    see1 = new_seen(key0 + 32);
+                }
                 wait(&bar.s_full[j], n_s);
                 __syncwarp();
                 tc_fence_after();
-                // which of this half's keys the row sees
-                uint32_t see0, see1;
-                bool odd_k = false, odd_v = false;
                 if (s >= w.nt) {
                     const uint2 b = *reinterpret_cast<const uint2 *>(key_bits[t & 3] + 8 * h);
                     see0 = b.x;
                     see1 = b.y;
                 } else {
-                    const int32_t key0 = static_cast<int32_t>(s) * kKeys + 64 * h;
-                    see0 = new_seen(key0);
-                    see1 = new_seen(key0 + 32);
                     // the tile's values have come too: whether it holds what fp16 does not
                     wait(&bar.v_full[t & 1], t >> 1);
                     __syncwarp();
@@ -552,9 +560,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
                     mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
                 }
                 // the row's maximum over both halves
-                half_max[j][n_s & 1][h][r] = mx;
+                half_max[j][buf][h][r] = mx;
                 named_barrier_sync(1 + j, 256);
-                mx = fmaxf(mx, half_max[j][n_s & 1][h ^ 1][r]);
+                mx = fmaxf(mx, half_max[j][buf][h ^ 1][r]);
+                buf ^= 1;
                 ++n_s;
                 mx = mx == -INFINITY ? mx : mx * mul;  // mul may underflow to 0
                 float corr = 1.0f;
@@ -633,7 +642,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
             else named_barrier_sync(3, 512);
             tc_fence_after();
             const bool whole = w.s0 == 0 && w.s1 == w.unit;
-            const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (w.t == p.begin ? 0 : 1);
+            const int64_t slot = slot_of(w);
             const uint32_t o_first = tmem + lanes + 256u;
             float M, L, w0 = 1.0f, w1 = 0.0f;
             if (both) {

@@ -17,7 +17,7 @@ constexpr uint32_t kFull = 0xffffffffu;
 // an earlier CTA) if it is the first to do so, and the CTAs first..last that share it.
 struct Kv4Share {
     int32_t b, hk, qt;       // b < 0: nothing to merge here
-    int32_t first, last, first_slot;
+    int32_t first, last;
 };
 
 struct Kv4Args {
@@ -25,6 +25,7 @@ struct Kv4Args {
     int32_t group, Mq, rows, QT, W;
     int32_t tile_shift;      // log2 of the keys of a tile
     int32_t min_tiles;       // tiles a CTA takes at least
+    int32_t snap;            // how far a cut may move to a unit's end
     float scale2;            // log2(e) / sqrt(D)
     Kv4Share *share;         // [grid]
     float2 *part_ml;         // [grid * 2][rows]: running maximum (base 2) and sum
@@ -97,9 +98,19 @@ __device__ __forceinline__ int64_t cached_tiles(const Kv4Args &k, int32_t b) {
 struct Place {
     int64_t total, begin, end;  // tiles of the line
     int64_t ctas;               // CTAs that share it
-    int32_t b, hk, qt;
+    int64_t snap;               // how far cuts were moved at most
     int64_t off;                // the first tile's place in its unit
+    int32_t b, hk, qt;
 };
+struct Spot {
+    int32_t b, hk, qt;
+    int64_t off, unit;  // place in the unit, and its tiles
+};
+
+__device__ __forceinline__ int64_t quotient(int64_t x, int64_t y) {  // x >= 0, y > 0
+    if (((x | y) >> 32) == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
+    return x / y;
+}
 
 // Sum over the block; every thread gets it.  `red`: one slot a warp.
 static __device__ __noinline__ int64_t block_sum64(int64_t v, int64_t *red) {
@@ -113,12 +124,104 @@ static __device__ __noinline__ int64_t block_sum64(int64_t v, int64_t *red) {
     return t;
 }
 
-// All threads of the block; the result is in *out after the last barrier.  Returns false when this
-// CTA has nothing to do.
-static __device__ __noinline__ bool find_place(const Kv4Args &k, Place *out, int64_t *red) {
+// The unit `off` tiles into request b, which has ct tiles of cached keys and `per` of new keys for each
+// kv head.
+static __device__ __noinline__ Spot spot_of(const Kv4Args &k, int32_t b, int64_t ct, int64_t off, int64_t per) {
+    const int64_t block = k.QT * ct + per;
+    Spot s;
+    s.b = b;
+    s.hk = static_cast<int32_t>(quotient(off, block));
+    off -= s.hk * block;
+    if (k.a.mask || !k.a.kn) {
+        s.unit = ct + new_tiles(k, 0);
+        s.qt = static_cast<int32_t>(quotient(off, s.unit));
+        off -= s.qt * s.unit;
+    } else {
+        s.qt = 0;
+        for (; off >= (s.unit = ct + new_tiles(k, s.qt)); ++s.qt) off -= s.unit;
+    }
+    s.off = off;
+    return s;
+}
+
+// Moves a cut that falls within `snap` tiles of a unit's end to the nearer end: a unit cut in two costs
+// partial sums of all its rows, written and read again.  True: to the unit's own end.
+__device__ __forceinline__ bool move_cut(int64_t &cut, const Spot &s, int64_t snap) {
+    const int64_t left = s.unit - s.off;
+    if (s.off <= left) {
+        if (s.off <= snap) cut -= s.off;
+        return false;
+    }
+    if (left > snap) return false;
+    cut += left;
+    return true;
+}
+// The place of the CTA whose share runs from cut[0] to cut[1], which lie at the given spots.  False:
+// nothing to do.
+__device__ __forceinline__ bool place_at(const Kv4Args &k, Place *p, int64_t total, int64_t ctas, int64_t cut0, int64_t cut1,
+                                         Spot s0, const Spot &s1) {
+    // at most a third of a CTA's share, so that few tiles still spread over all CTAs
+    const int64_t snap = min(static_cast<int64_t>(k.snap), quotient(total, 3 * ctas));
+    const int64_t was = cut0;
+    if (move_cut(cut0, s0, snap)) {  // the next unit's first tile
+        s0.off = 0;
+        if (++s0.qt == k.QT) {
+            s0.qt = 0;
+            if (++s0.hk == k.a.cache.Hk) {
+                s0.hk = 0;
+                ++s0.b;
+            }
+        }
+    } else {
+        s0.off -= was - cut0;
+    }
+    if (cut1 < total) move_cut(cut1, s1, snap);
+    *p = Place{total, cut0, cut1, ctas, snap, s0.off, s0.b, s0.hk, s0.qt};
+    return cut0 < cut1;
+}
+__device__ __forceinline__ int64_t ctas_of(const Kv4Args &k, int64_t total) {
+    const int64_t want = quotient(total + k.min_tiles - 1, k.min_tiles);
+    return want < gridDim.x ? (want < 1 ? 1 : want) : gridDim.x;
+}
+
+// At most 32 requests: every warp finds the place by itself (one request a lane), with no barrier.
+static __device__ __noinline__ bool find_place_warp(const Kv4Args &k, Place *p) {
+    const int32_t lane = threadIdx.x & 31;
+    const int64_t ct = lane < k.a.B ? cached_tiles(k, lane) : 0;
+    int64_t per = 0;
+    if (k.a.mask || !k.a.kn) {
+        per = static_cast<int64_t>(k.QT) * new_tiles(k, 0);
+    } else {
+        for (int32_t q = lane; q < k.QT; q += 32) per += new_tiles(k, q);
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) per += __shfl_xor_sync(kFull, per, off);
+    }
+    const int64_t w = lane < k.a.B ? k.a.cache.Hk * (k.QT * ct + per) : 0;
+    int64_t inc = w;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int64_t o = __shfl_up_sync(kFull, inc, off);
+        if (lane >= off) inc += o;
+    }
+    const int64_t total = __shfl_sync(kFull, inc, 31), ctas = ctas_of(k, total), c = blockIdx.x;
+    if (c >= ctas) return false;
+    const int64_t cut0 = quotient(c * total, ctas), cut1 = quotient((c + 1) * total, ctas);
+    // the lanes' runs are ascending: the first whose end lies behind the cut holds it
+    const int32_t b0 = __ffs(__ballot_sync(kFull, inc > cut0)) - 1;
+    const int32_t b1 = cut1 < total ? __ffs(__ballot_sync(kFull, inc > cut1)) - 1 : b0;
+    const int64_t lo = inc - w;
+    const int64_t lo0 = __shfl_sync(kFull, lo, b0), lo1 = __shfl_sync(kFull, lo, b1);
+    const int64_t ct0 = __shfl_sync(kFull, ct, b0), ct1 = __shfl_sync(kFull, ct, b1);
+    const Spot s0 = spot_of(k, b0, ct0, cut0 - lo0, per);
+    const Spot s1 = cut1 < total ? spot_of(k, b1, ct1, cut1 - lo1, per) : s0;
+    return place_at(k, p, total, ctas, cut0, cut1, s0, s1);
+}
+
+// More: all threads of the block together.  `red`: a slot a warp.
+static __device__ __noinline__ bool find_place_block(const Kv4Args &k, Place *p, int64_t *red, Spot *spots) {
     const int32_t tid = threadIdx.x, nt = blockDim.x, B = k.a.B;
     const int64_t Hk = k.a.cache.Hk;
-    int64_t per = 0;  // tiles of new keys of one (request, kv head)
+    int64_t per = 0;
     if (k.a.mask || !k.a.kn) {
         per = static_cast<int64_t>(k.QT) * new_tiles(k, 0);
     } else {
@@ -127,17 +230,14 @@ static __device__ __noinline__ bool find_place(const Kv4Args &k, Place *out, int
     }
     int64_t mine = 0;
     for (int32_t b = tid; b < B; b += nt) mine += Hk * (k.QT * cached_tiles(k, b) + per);
-    const int64_t total = block_sum64(mine, red);
-    const int64_t want = (total + k.min_tiles - 1) / k.min_tiles;
-    const int64_t ctas = want < gridDim.x ? (want < 1 ? 1 : want) : gridDim.x;
-    const int64_t c = blockIdx.x;
+    const int64_t total = block_sum64(mine, red), ctas = ctas_of(k, total), c = blockIdx.x;
     if (c >= ctas) return false;
-    const int64_t begin = c * total / ctas, end = (c + 1) * total / ctas;
-    // the request that holds tile `begin`
+    const int64_t cut[2] = {quotient(c * total, ctas), quotient((c + 1) * total, ctas)};
+    // the requests that hold the tiles behind the two cuts
     int64_t base = 0;
     for (int32_t b0 = 0; b0 < B; b0 += nt) {
         const int32_t b = b0 + tid;
-        const int64_t w = b < B ? Hk * (k.QT * cached_tiles(k, b) + per) : 0;
+        const int64_t ct = b < B ? cached_tiles(k, b) : 0, w = b < B ? Hk * (k.QT * ct + per) : 0;
         int64_t inc = w;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
@@ -153,33 +253,17 @@ static __device__ __noinline__ bool find_place(const Kv4Args &k, Place *out, int
             all += red[w2];
         }
         const int64_t lo = before + inc - w;
-        if (b < B && begin >= lo && begin < lo + w) {
-            int64_t off = begin - lo;
-            const int64_t ct = cached_tiles(k, b), block = k.QT * ct + per;
-            Place p;
-            p.total = total;
-            p.begin = begin;
-            p.end = end;
-            p.ctas = ctas;
-            p.b = b;
-            p.hk = static_cast<int32_t>(off / block);
-            off -= p.hk * block;
-            if (k.a.mask || !k.a.kn) {
-                const int64_t u = ct + new_tiles(k, 0);
-                p.qt = static_cast<int32_t>(off / u);
-                off -= p.qt * u;
-            } else {
-                p.qt = 0;
-                for (int64_t u; off >= (u = ct + new_tiles(k, p.qt)); ++p.qt) off -= u;
-            }
-            p.off = off;
-            *out = p;
-        }
+#pragma unroll 1
+        for (int i = 0; i < 2; ++i)
+            if (cut[i] >= lo && cut[i] < lo + w) spots[i] = spot_of(k, b, ct, cut[i] - lo, per);
         base = all;
-        if (begin < base) break;
+        if (cut[1] < base) break;
     }
     __syncthreads();
-    return true;
+    return place_at(k, p, total, ctas, cut[0], cut[1], spots[0], spots[cut[1] < total]);
+}
+__device__ __forceinline__ bool find_place(const Kv4Args &k, Place *p, int64_t *red, Spot *spots) {
+    return k.a.B <= 32 ? find_place_warp(k, p) : find_place_block(k, p, red, spots);
 }
 
 // A CTA's run through the line, unit by unit: [s0, s1) of the unit's tiles.
@@ -195,12 +279,13 @@ struct Walk {
         qt = p.qt;
         t = p.begin;
         s0 = p.off;
+        len = kv4_length(k.a.cache, b);
         fill(k, p);
     }
     __device__ __forceinline__ void fill(const Kv4Args &k, const Place &p) {
         nt = new_tiles(k, qt);
-        len = kv4_length(k.a.cache, b);
-        unit = cached_tiles(k, b) + nt;
+        unit = ((len + (1 << k.tile_shift) - 1) >> k.tile_shift) + nt;
+        unit = unit < 1 ? 1 : unit;  // nothing cached and no new keys: a tile with no keys
         s1 = min(unit, s0 + (p.end - t));
     }
     __device__ __forceinline__ bool next(const Kv4Args &k, const Place &p) {
@@ -212,6 +297,7 @@ struct Walk {
             if (++hk == k.a.cache.Hk) {
                 hk = 0;
                 if (++b == k.a.B) return false;  // lengths changed under the call
+                len = kv4_length(k.a.cache, b);
             }
         }
         fill(k, p);
@@ -219,18 +305,21 @@ struct Walk {
     }
 };
 
-// What CTA blockIdx.x leaves for the merge.
+// What CTA blockIdx.x leaves for the merge, given that its first unit was begun by an earlier one.  The
+// cuts left inside a unit [u0, u1) are those of CTAs c with u0 + snap < c total / ctas < u1 - snap; the
+// CTA before the first of them began the unit.
 static __device__ __noinline__ Kv4Share share_of(const Kv4Args &k, const Place &p, const Walk &w) {
-    Kv4Share sh{-1, 0, 0, 0, 0, 0};
+    Kv4Share sh{-1, 0, 0, 0, 0};
     if (w.s0 > 0) {
-        const int64_t u0 = p.begin - w.s0;  // the unit's first tile
-        const int64_t c0 = ((u0 + 1) * p.ctas - 1) / p.total, c1 = ((u0 + w.unit) * p.ctas - 1) / p.total;
-        if (c0 == static_cast<int64_t>(blockIdx.x) - 1)
-            sh = Kv4Share{w.b, w.hk, w.qt, static_cast<int32_t>(c0), static_cast<int32_t>(c1),
-                          c0 * p.total / p.ctas == u0 ? 0 : 1};
+        const int64_t u0 = p.begin - w.s0, c = blockIdx.x;
+        if (quotient((c - 1) * p.total, p.ctas) <= u0 + p.snap)
+            sh = Kv4Share{w.b, w.hk, w.qt, static_cast<int32_t>(c) - 1,
+                          static_cast<int32_t>(quotient((u0 + w.unit - p.snap) * p.ctas - 1, p.total))};
     }
     return sh;
 }
+// Where a segment's partial sums go: slot 0 of its CTA for a unit that an earlier CTA began, else 1.
+__device__ __forceinline__ int64_t slot_of(const Walk &w) { return 2 * static_cast<int64_t>(blockIdx.x) + (w.s0 > 0 ? 0 : 1); }
 
 // The tcgen05 kernel (kv4_attn_tc.cu): head_dim 64 or 128, units of 256 query rows, tiles of 128 keys.
 constexpr int32_t kKv4TcRows = 256;
