@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(kThreads, Shape<G, NQ>::kBlocks) kv4_attention
     __shared__ uint64_t full[kStages], empty[kStages];
     __shared__ int32_t valid[kStages][4];  // keys of each chunk of the stage (0..16)
     __shared__ int32_t abort_mark;
-    __shared__ int64_t red[kThreads / 32];
+    __shared__ int32_t red[kThreads / 32];
     __shared__ Spot spots[2];
     const int32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -111,13 +111,13 @@ __global__ void __launch_bounds__(kThreads, Shape<G, NQ>::kBlocks) kv4_attention
     const bool busy = find_place(k, &p, red, spots);
     __syncthreads();  // the mbarriers too
     if (!busy) {
-        if (threadIdx.x == 0) k.share[blockIdx.x].b = -1;
+        if (threadIdx.x == 0) k.share[blockIdx.x].kind = 0;
         return;
     }
     volatile int32_t *abort_flag = &abort_mark;
     Walk w;
     w.start(k, p);
-    if (threadIdx.x == 0) k.share[blockIdx.x] = share_of(k, p, w);
+    if (threadIdx.x == 0) k.share[blockIdx.x] = share_of(w);
 
     if (warp == kWarps) {
         // ---------------- copies: a stage is up to four chunks of cached keys and values ----------
@@ -125,18 +125,18 @@ __global__ void __launch_bounds__(kThreads, Shape<G, NQ>::kBlocks) kv4_attention
         bool dead = false;
         do {
             if (lane == 0 && w.len != a.cache.lengths[w.b]) latch(a.status, kDevBounds);  // clamped
-            const int64_t k0 = max(w.s0 - w.nt, int64_t{0}), k1 = w.s1 - w.nt;
-            for (int64_t kt = k0; kt < k1 && !dead; kt += 8) {
+            const int32_t k0 = max(w.s0 - w.nt, 0), k1 = w.s1 - w.nt;
+            for (int32_t kt = k0; kt < k1 && !dead; kt += 8) {
                 // the chunks of 8 tiles, one a lane
-                const int64_t key = kt * kTile + lane * kKv4Chunk;
-                int32_t nv = static_cast<int32_t>(min(max(w.len - key, int64_t{0}), int64_t{kKv4Chunk}));
+                const int32_t key = kt * kTile + lane * kKv4Chunk;
+                int32_t nv = min(max(w.len - key, 0), kKv4Chunk);
                 const uint8_t *src = nullptr;
                 if (nv > 0 && kt + (lane >> 2) < k1) {
                     src = kv4_chunk(a.cache, w.b, w.hk, key);
                     if (!src) latch(a.status, kDevBounds);  // its keys count as absent
                 }
                 if (!src) nv = 0;
-                const int32_t tiles = static_cast<int32_t>(min(k1 - kt, int64_t{8}));
+                const int32_t tiles = min(k1 - kt, 8);
                 for (int32_t j = 0; j < tiles; ++j, ++issued) {
                     const int32_t st = issued % kStages;
                     if (issued >= kStages && lane == 0) kv4_wait(&empty[st], issued / kStages - 1, abort_flag);
@@ -282,10 +282,10 @@ __global__ void __launch_bounds__(kThreads, Shape<G, NQ>::kBlocks) kv4_attention
                 }
         };
 
-        int64_t s = w.s0;
+        int32_t s = w.s0;
         // ---------------- new keys: bf16, straight from memory ----------------
         for (; s < w.s1 && s < w.nt; ++s) {
-            const int32_t key0 = static_cast<int32_t>(s) * kTile + warp * 16;
+            const int32_t key0 = s * kTile + warp * 16;
             if (key0 >= a.n) continue;
             const int64_t krow = static_cast<int64_t>(w.b) * a.n;
             float sc[NQ][4];
@@ -619,24 +619,28 @@ __global__ void __launch_bounds__(kThreads, Shape<G, NQ>::kBlocks) kv4_attention
     } while (w.next(k, p));
 }
 
-// Units that several CTAs worked on: block c merges the unit that CTA c is the first to continue.
+// Units that several CTAs worked on: block c merges the unit that CTA c is the second to work on.
 // o = sum_i w_i O_i / sum_i w_i l_i, w_i = 2^(m_i - max m), over CTAs first..last in order.
 __global__ void __launch_bounds__(128) kv4_merge_kernel(const __grid_constant__ Kv4Args k) {
     pdl_launch_dependents();
     pdl_wait();
+    // CTA c continues a unit that CTA c - 1 began, and that goes on to CTA `last`
     const Kv4Share sh = k.share[blockIdx.x];
-    if (sh.b < 0) return;
+    if (sh.kind == 0 || k.share[blockIdx.x - 1].kind == 2) return;
+    const int32_t first = blockIdx.x - 1;
+    int32_t last = blockIdx.x;
+    while (last + 1 < static_cast<int32_t>(gridDim.x) && k.share[last].kind == 2) ++last;
     const int32_t D = k.a.cache.G * kKv4Group, quads = D / 4;
     const int32_t rows = min(k.rows, k.Mq - sh.qt * k.rows);
     for (int32_t it = threadIdx.x + blockIdx.y * 128; it < rows * quads; it += 128 * gridDim.y) {
         const int32_t r = it / quads, c4 = it - r * quads;
-        auto slot = [&](int32_t c) { return 2 * static_cast<int64_t>(c) + (c == sh.first ? 1 : 0); };
+        auto slot = [&](int32_t c) { return 2 * static_cast<int64_t>(c) + (c == first ? 1 : 0); };
         float M = -INFINITY;
-        for (int32_t c = sh.first; c <= sh.last; ++c) M = fmaxf(M, k.part_ml[slot(c) * k.rows + r].x);
+        for (int32_t c = first; c <= last; ++c) M = fmaxf(M, k.part_ml[slot(c) * k.rows + r].x);
         float L = 0.0f;
         float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
-        for (int32_t c = sh.first; c <= sh.last; ++c) {
+        for (int32_t c = first; c <= last; ++c) {
             const float2 ml = k.part_ml[slot(c) * k.rows + r];
             const float4 x = *reinterpret_cast<const float4 *>(k.part_o + (slot(c) * k.rows + r) * D + 4 * c4);
             const float wt = ml.x == -INFINITY ? (ml.y == 0.0f ? 0.0f : ml.y) : ex2_approx(ml.x - M);
@@ -755,7 +759,8 @@ cudaError_t launch_kv4_attention(const Kv4Attention &a, cudaStream_t st) {
     // no more CTAs than the longest possible line gives work to
     const int64_t units = static_cast<int64_t>(a.B) * a.cache.Hk * k.QT;
     const int64_t tiles = (a.cache.cap + tile - 1) / tile + (a.kn ? (a.n + tile - 1) / tile : 0);
-    const int64_t most = (units > (int64_t{1} << 40) / tiles) ? full : (units * tiles + k.min_tiles - 1) / k.min_tiles;
+    if (units >= (int64_t{1} << 31) || units * tiles >= (int64_t{1} << 31)) return cudaErrorNotSupported;
+    const int64_t most = (units * tiles + k.min_tiles - 1) / k.min_tiles;
     const unsigned grid = static_cast<unsigned>(std::min<int64_t>(full, std::max<int64_t>(most, 1)));
     const cudaError_t e = v.kernel ? launch_pdl(v.kernel, dim3(grid), dim3(v.threads), v.smem, st, k)
                                    : launch_kv4_attention_tc(k, static_cast<int32_t>(grid), st);
@@ -809,7 +814,8 @@ eagle_status eagle_kv4_attention(const eagle_kv4_cache *cache, int32_t batch, in
     a.o = static_cast<__nv_bfloat16 *>(d_out);
     a.ws = d_ws;
     a.status = d_status;
-    return launch_kv4_attention(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? EAGLE_OK : EAGLE_ERR_CUDA;
+    const cudaError_t e = launch_kv4_attention(a, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? EAGLE_OK : (e == cudaErrorNotSupported ? EAGLE_ERR_UNSUPPORTED : EAGLE_ERR_CUDA);
 }
 
 }  // extern "C"

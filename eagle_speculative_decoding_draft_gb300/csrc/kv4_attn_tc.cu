@@ -208,9 +208,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
     __shared__ __align__(8) uint8_t key_bits[4][16];  // by tile & 3: which of its 128 keys are there
     __shared__ uint8_t raw_keys[kRaw][8];             // keys of each chunk that are there
     __shared__ __align__(8) uint8_t odd_tile[4][2][kFillWarps];  // by tile & 3, key or value, filling warp
+    __shared__ int32_t row_at[2][128];        // stream, row: node << 16 | head, -1 behind the unit's last row
+    __shared__ float2 q_scale[2][128];        // what a row's query and its scores are multiplied by
     __shared__ float half_max[2][2][2][128];  // stream, exchange & 1, half, row
     __shared__ float2 half_ml[2][2][128];     // stream, half, row: references and sums of a segment
-    __shared__ int64_t red[kThreads / 32];
+    __shared__ int32_t red[kThreads / 32];
     __shared__ Spot spots[2];
     const int32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     volatile int32_t *abort_flag = &abort_mark;
@@ -239,7 +241,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
     Place p;
     const bool busy = find_place(k, &p, red, spots);
     if (!busy) {
-        if (threadIdx.x == 0) k.share[blockIdx.x].b = -1;
+        if (threadIdx.x == 0) k.share[blockIdx.x].kind = 0;
         return;
     }
     if (warp == 24) {
@@ -252,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
     const uint32_t tmem = __shfl_sync(kFull, tmem_base, 0);
     Walk w;
     w.start(k, p);
-    if (threadIdx.x == 0) k.share[blockIdx.x] = share_of(k, p, w);
+    if (threadIdx.x == 0) k.share[blockIdx.x] = share_of(w);
     auto wait = [&](uint64_t *b, uint32_t parity) -> bool { return kv4_wait(b, parity, abort_flag); };
     auto rows_of = [&]() { return min(kKv4TcRows, k.Mq - w.qt * kKv4TcRows); };  // rows of the unit
 
@@ -261,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
         const int32_t fw = warp - 16;
         uint32_t gt = 0, raw = 0;  // tiles and halves of cached tiles so far
         do {
-            for (int64_t s = w.s0; s < w.s1; ++s, ++gt) {
+            for (int32_t s = w.s0; s < w.s1; ++s, ++gt) {
                 const uint32_t st = gt & 1u;
 #pragma unroll 1
                 for (int32_t half = 0; half < 2; ++half) {
@@ -326,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
                         const int32_t ch = lane % kPer, first = fw * kRowsWarp + lane / kPer;
                         const __nv_bfloat16 *src = (half ? a.vn : a.kn) + (static_cast<int64_t>(w.b) * a.n + s * kKeys) * a.ldkv +
                                                    static_cast<int64_t>(w.hk) * D + ch * 8;
-                        const int32_t rows = static_cast<int32_t>(min(a.n - s * kKeys, int64_t{kKeys}));
+                        const int32_t rows = min(a.n - s * kKeys, kKeys);
 #pragma unroll 1
                         for (int32_t sub = 0; sub < D / 64; ++sub) {
                             uint4 v[4];
@@ -360,18 +362,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
         bool dead = false;
         do {
             if (lane == 0 && w.len != a.cache.lengths[w.b]) latch(a.status, kDevBounds);  // clamped
-            const int64_t k0 = max(w.s0 - w.nt, int64_t{0}), k1 = w.s1 - w.nt;
-            for (int64_t kt = k0; kt < k1 && !dead; kt += 4) {
+            const int32_t k0 = max(w.s0 - w.nt, 0), k1 = w.s1 - w.nt;
+            for (int32_t kt = k0; kt < k1 && !dead; kt += 4) {
                 // the chunks of four tiles, one a lane
-                const int64_t key = kt * kKeys + lane * 16;
-                int32_t nv = static_cast<int32_t>(min(max(w.len - key, int64_t{0}), int64_t{16}));
+                const int32_t key = kt * kKeys + lane * 16;
+                int32_t nv = min(max(w.len - key, 0), 16);
                 const uint8_t *src = nullptr;
                 if (nv > 0 && kt + (lane >> 3) < k1) {
                     src = kv4_chunk(a.cache, w.b, w.hk, key);
                     if (!src) latch(a.status, kDevBounds);  // its keys count as absent
                 }
                 if (!src) nv = 0;
-                const int32_t halves = 2 * static_cast<int32_t>(min(k1 - kt, int64_t{4}));
+                const int32_t halves = 2 * min(k1 - kt, 4);
                 for (int32_t hh = 0; hh < halves; ++hh, ++raw) {
                     const uint32_t rs = raw % kRaw;
                     if (raw >= kRaw && lane == 0) wait(&bar.raw_empty[rs], raw / kRaw - 1);
@@ -401,14 +403,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
         uint32_t gt = 0, seg = 0, jobs0 = 0, jobs1 = 0;  // tiles, segments, P's of each stream so far
         const uint64_t q_desc = sw128_kmajor_desc(smem_u32(base + S::kQ)), k_desc = sw128_kmajor_desc(smem_u32(base + S::kK));
         const uint64_t v_desc = sw128_desc(smem_u32(base + S::kV), kKeys * 128u, 1024u);
+        // the warp stays whole when a wait gives up, too
+        auto wait_all = [&](uint64_t *b, uint32_t parity) -> bool { return __all_sync(kFull, wait(b, parity)); };
         bool ok = true;
         do {
-            const int32_t tiles = __shfl_sync(kFull, static_cast<int32_t>(w.s1 - w.s0), 0);
+            const int32_t tiles = __shfl_sync(kFull, w.s1 - w.s0, 0);
             const uint32_t both = __shfl_sync(kFull, rows_of() > 128 ? 1 : 0, 0);
             const int32_t n = tiles << both;
             auto issue_s = [&](int32_t q) -> bool {
                 const uint32_t t = gt + (q >> both), st = t & 1u, j = q & 1;
-                if (!wait(&bar.k_full[st], t >> 1)) return false;
+                if (!wait_all(&bar.k_full[st], t >> 1)) return false;
                 tc_fence_after();
                 const uint64_t qd = q_desc + j * kStep, kd = k_desc + st * kStep;
                 const uint32_t d = tmem + j * 128u;
@@ -421,11 +425,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
                 if (!both || j) commit_to(&bar.k_empty[st], leader);  // the tile's last reader
                 return true;
             };
-            ok = wait(&bar.q_full[0], seg) && issue_s(0);
-            ok = ok && wait(&bar.q_full[1], seg) && (n < 2 || issue_s(1));
+            ok = wait_all(&bar.q_full[0], seg) && issue_s(0);
+            ok = ok && wait_all(&bar.q_full[1], seg) && (n < 2 || issue_s(1));
             for (int32_t q = 0; q < n && ok; ++q) {
                 const uint32_t t = gt + (q >> both), st = t & 1u, j = q & 1;
-                ok = wait(&bar.v_full[st], t >> 1) && wait(&bar.p_full[j], j ? jobs1 : jobs0);
+                ok = wait_all(&bar.v_full[st], t >> 1) && wait_all(&bar.p_full[j], j ? jobs1 : jobs0);
                 if (!ok) break;
                 if (j) ++jobs1;
                 else ++jobs0;
@@ -459,39 +463,43 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
             const bool both = unit_rows > 128;
             const int32_t ur = both ? j * 128 + r : r, row = w.qt * kKv4TcRows + ur;
             const bool live = ur < unit_rows;
-            const int32_t node = live ? row / k.group : 0, head = w.hk * k.group + (live ? row - node * k.group : 0);
-            const __nv_bfloat16 *q_src = a.q + (static_cast<int64_t>(w.b) * a.n + node) * a.ldq + static_cast<int64_t>(head) * D;
-            float f, mul;  // what the query was scaled by; what makes its scores base 2
-            {
-                uint4 v[D / 16];  // this half of the row
+            const int32_t node = live ? row / k.group : 0;
+            if (h == 0) row_at[j][r] = live ? (node << 16) | (w.hk * k.group + row - node * k.group) : -1;
+            named_barrier_sync(1 + j, 256);
+            // the stream's queries, whole rows at a time: scaled, to fp16, and what turns a row's
+            // scores to base 2
+            constexpr int kPer = D / 8, kRowsLoad = 32 / kPer;  // 16-byte pieces a row; rows a warp takes at once
+            const int32_t w8 = warp & 7, piece = lane % kPer;
+#pragma unroll 1
+            for (int32_t i0 = 0; i0 < 16 / kRowsLoad; i0 += 4) {
+                uint4 v[4];
 #pragma unroll
-                for (int i = 0; i < D / 16; ++i)
-                    v[i] = live ? *reinterpret_cast<const uint4 *>(q_src + h * (D / 2) + 8 * i) : make_uint4(0, 0, 0, 0);
-                float big = 0.0f;
-#pragma unroll
-                for (int i = 0; i < D / 16; ++i) {
-                    const uint32_t vw[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) big = fmaxf(big, fmaxf(fabsf(bf_lo(vw[u])), fabsf(bf_hi(vw[u]))));
+                for (int i = 0; i < 4; ++i) {
+                    const int32_t at = row_at[j][(i0 + i) * kRowsLoad + w8 * 16 + lane / kPer];
+                    v[i] = make_uint4(0, 0, 0, 0);
+                    if (at >= 0)
+                        v[i] = *reinterpret_cast<const uint4 *>(a.q + (static_cast<int64_t>(w.b) * a.n + (at >> 16)) * a.ldq +
+                                                                 static_cast<int64_t>(at & 0xffff) * D + 8 * piece);
                 }
-                half_max[j][buf][h][r] = big;
-                named_barrier_sync(1 + j, 256);
-                big = fmaxf(big, half_max[j][buf][h ^ 1][r]);
-                buf ^= 1;
-                const int32_t e = max(static_cast<int32_t>(__float_as_uint(big) >> 23), 10);
-                f = __uint_as_float(static_cast<uint32_t>(263 - e) << 23);
-                mul = __uint_as_float(static_cast<uint32_t>(e - 9) << 23) * k.scale2;
-                uint8_t *dst = base + S::kQ + j * S::kTileBytes;
 #pragma unroll
-                for (int i = 0; i < D / 16; ++i) {
-                    const int32_t c = h * (D / 16) + i;
-                    *reinterpret_cast<uint4 *>(dst + (c >> 3) * (kKeys * 128) + sw128(r, c & 7)) =
+                for (int i = 0; i < 4; ++i) {
+                    const int32_t qr = (i0 + i) * kRowsLoad + w8 * 16 + lane / kPer;
+                    const uint32_t vw[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                    uint32_t big = 0;  // magnitudes compare as whole numbers, NaN above all
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) big = max(big, max((vw[u] << 16) & 0x7fffffffu, vw[u] & 0x7fff0000u));
+#pragma unroll
+                    for (int off = 1; off < kPer; off <<= 1) big = max(big, __shfl_xor_sync(kFull, big, off));
+                    const int32_t e = max(static_cast<int32_t>(big >> 23), 10);
+                    const float f = __uint_as_float(static_cast<uint32_t>(263 - e) << 23);
+                    *reinterpret_cast<uint4 *>(base + S::kQ + j * S::kTileBytes + (piece >> 3) * (kKeys * 128) + sw128(qr, piece & 7)) =
                         make_uint4(pack_f16(bf_lo(v[i].x) * f, bf_lo(v[i].z) * f), pack_f16(bf_hi(v[i].x) * f, bf_hi(v[i].z) * f),
                                    pack_f16(bf_lo(v[i].y) * f, bf_lo(v[i].w) * f), pack_f16(bf_hi(v[i].y) * f, bf_hi(v[i].w) * f));
+                    if (piece == 0) q_scale[j][qr] = make_float2(f, __uint_as_float(static_cast<uint32_t>(e - 9) << 23) * k.scale2);
                 }
-                fence_proxy_async_smem();
-                mbar_arrive(&bar.q_full[j]);
             }
+            fence_proxy_async_smem();
+            mbar_arrive(&bar.q_full[j]);
             {
                 uint32_t z[16];
 #pragma unroll
@@ -500,6 +508,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
                 for (int c = 0; c < D / 32; ++c) tmem_st_16(t_o + h * (D / 2) + 16 * c, z);
                 tmem_wait_st();
             }
+            named_barrier_sync(1 + j, 256);
+            const float f = q_scale[j][r].x, mul = q_scale[j][r].y;
             const uint32_t *mrow = a.mask ? a.mask + (static_cast<int64_t>(w.b) * a.n + node) * k.W : nullptr;
             // which of new keys k0 .. k0 + 31 the row sees
             auto new_seen = [&](int32_t k0) {
@@ -509,16 +519,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
                 return v & (left >= 32 ? kFull : (left > 0 ? (1u << left) - 1u : 0u));
             };
             float ref = -INFINITY, l = 0.0f;
-            const int32_t tiles = static_cast<int32_t>(w.s1 - w.s0);
+            const int32_t tiles = w.s1 - w.s0;
             int32_t done = 0;  // tiles of this segment that this stream took
             for (int32_t ti = both ? 0 : j; ti < tiles; ti += both ? 1 : 2, ++done) {
-                const int64_t s = w.s0 + ti;
+                const int32_t s = w.s0 + ti;
                 const uint32_t t = gt + ti;
                 // which of this half's keys the row sees
                 uint32_t see0 = 0u, see1 = 0u;
                 bool odd_k = false, odd_v = false;
                 if (s < w.nt) {
-                    const int32_t key0 = static_cast<int32_t>(s) * kKeys + 64 * h;
+                    const int32_t key0 = s * kKeys + 64 * h;
                     see0 = new_seen(key0);
                     see1 = new_seen(key0 + 32);
                 }
@@ -539,8 +549,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
                 if (!live) see0 = see1 = 0u;
                 const bool all = __all_sync(kFull, (see0 & see1) == kFull);
                 const int64_t new_row = (static_cast<int64_t>(w.b) * a.n + s * kKeys) * a.ldkv + static_cast<int64_t>(w.hk) * D;
-                const int32_t new_rows = static_cast<int32_t>(min(a.n - s * kKeys, int64_t{kKeys}));
-                if (odd_k) add_odd_keys<D>(a.kn + new_row, a.ldkv, 64 * h, min(new_rows, 64 * h + 64), q_src, f, t_s);
+                const int32_t new_rows = min(a.n - s * kKeys, kKeys);
+                if (odd_k) {
+                    const int32_t head = live ? row_at[j][r] & 0xffff : 0;  // rows that are not there read a query that is
+                    add_odd_keys<D>(a.kn + new_row, a.ldkv, 64 * h, min(new_rows, 64 * h + 64),
+                                    a.q + (static_cast<int64_t>(w.b) * a.n + node) * a.ldq + static_cast<int64_t>(head) * D, f, t_s);
+                }
                 float mx;
                 {
                     float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -588,7 +602,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
                     tmem_wait_st();
                 }
                 if (odd_v) {
-                    const int32_t key0 = static_cast<int32_t>(s) * kKeys;
+                    const int32_t key0 = s * kKeys;
                     uint4 see = make_uint4(0u, 0u, 0u, 0u);
                     if (live) see = make_uint4(new_seen(key0), new_seen(key0 + 32), new_seen(key0 + 64), new_seen(key0 + 96));
                     add_odd_values(a.vn + new_row, a.ldkv, new_rows, see, mul, sub, t_s, t_o, h * (D / 2), (h + 1) * (D / 2));
@@ -684,10 +698,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
                 if (!live || !ok) continue;
                 // columns 8 i + (0 .. 7) are dims 8 i + (0 4 1 5 2 6 3 7)
                 if (whole) {
-                    __nv_bfloat16 *dst = a.o + ((static_cast<int64_t>(w.b) * a.n + node) * a.H + head) * D + c;
+                    // over the stream's queries, which no MMA reads any more; a unit of at most 128
+                    // rows over those of stream 0
+                    uint8_t *dst = base + S::kQ + (both ? j * S::kTileBytes : 0u);
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
-                        *reinterpret_cast<uint4 *>(dst + 8 * i) =
+                        *reinterpret_cast<uint4 *>(dst + (c >> 6) * (kKeys * 128) + sw128(r, ((c >> 3) & 7) + i)) =
                             make_uint4(pack_b16(x[8 * i] * inv, x[8 * i + 2] * inv), pack_b16(x[8 * i + 4] * inv, x[8 * i + 6] * inv),
                                        pack_b16(x[8 * i + 1] * inv, x[8 * i + 3] * inv), pack_b16(x[8 * i + 5] * inv, x[8 * i + 7] * inv));
                 } else {
@@ -701,9 +717,23 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
             }
             if (!whole && live && ok && h == 0 && (both || j == 0)) k.part_ml[slot * k.rows + ur] = make_float2(M, L);
             tc_fence_before();
-            // no output column or sum is overwritten before all of its readers have it
+            // no output column or sum is overwritten before all of its readers have it, and the rows
+            // to be written are all there
             if (both) named_barrier_sync(1 + j, 256);
             else named_barrier_sync(3, 512);
+            if (whole) {
+                const uint8_t *src = base + S::kQ + (both ? j * S::kTileBytes : 0u);
+                const int32_t warps = both ? 8 : 16, wi = both ? w8 : warp;
+#pragma unroll 4
+                for (int32_t r0 = wi * kRowsLoad; r0 < 128; r0 += warps * kRowsLoad) {
+                    const int32_t orow = r0 + lane / kPer, at = row_at[both ? j : 0][orow];
+                    if (at >= 0 && ok)
+                        *reinterpret_cast<uint4 *>(a.o + ((static_cast<int64_t>(w.b) * a.n + (at >> 16)) * a.H + (at & 0xffff)) * D + 8 * piece) =
+                            *reinterpret_cast<const uint4 *>(src + (piece >> 3) * (kKeys * 128) + sw128(orow, piece & 7));
+                }
+                if (both) named_barrier_sync(1 + j, 256);
+                else named_barrier_sync(3, 512);
+            }
         } while (w.next(k, p));
     }
 

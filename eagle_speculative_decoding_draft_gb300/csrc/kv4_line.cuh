@@ -13,11 +13,11 @@ namespace eagle {
 
 constexpr uint32_t kFull = 0xffffffffu;
 
-// What each CTA of the attention kernel leaves for the merge: the unit that it continues (begun by
-// an earlier CTA) if it is the first to do so, and the CTAs first..last that share it.
+// What each CTA leaves for the merge: of the unit that its first segment belongs to, where that one was
+// begun by an earlier CTA.
 struct Kv4Share {
-    int32_t b, hk, qt;       // b < 0: nothing to merge here
-    int32_t first, last;
+    int32_t kind;  // 0: begun here (or nothing to do), 1: begun earlier and ended here, 2: ended later
+    int32_t b, hk, qt;
 };
 
 struct Kv4Args {
@@ -58,15 +58,27 @@ __device__ __forceinline__ void load_words(const uint8_t *p, uint32_t (&w)[N]) {
     }
 }
 
+// True once the phase with the given parity has completed; sleeps on the barrier up to 20 us.
+__device__ __forceinline__ bool try_wait_long(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(20000u)
+        : "memory");
+    return ok != 0;
+}
 // Waits for `parity` (its lowest bit) on `bar`.  Gives up when *abort is set, and sets it after
 // kWaitLimitNs.  Small, so that the kernels' loops stay in the instruction cache: the clock is looked
-// at once in a thousand tries.
+// at once in 64 tries.
 __device__ __forceinline__ bool kv4_wait(uint64_t *bar, uint32_t parity, volatile int32_t *abort) {
     uint64_t since = 0;
     for (uint32_t i = 1;; ++i) {
-        if (mbar_try_wait(bar, parity & 1u)) return true;
+        if (try_wait_long(bar, parity & 1u)) return true;
         if (*abort) return false;
-        if ((i & 1023u) == 0) {
+        if ((i & 63u) == 0) {
             const uint64_t now = global_timer_ns();
             if (since == 0) {
                 since = now;
@@ -81,6 +93,7 @@ __device__ __forceinline__ bool kv4_wait(uint64_t *bar, uint32_t parity, volatil
 // ---------------------------------------------------------------------------------------------
 // The line of tiles
 // ---------------------------------------------------------------------------------------------
+// Everything is counted in 32 bits: the host refuses calls whose line could be longer.
 // Tiles of new keys that the rows of query tile qt need.
 __device__ __forceinline__ int32_t new_tiles(const Kv4Args &k, int32_t qt) {
     if (!k.a.kn) return 0;
@@ -88,53 +101,35 @@ __device__ __forceinline__ int32_t new_tiles(const Kv4Args &k, int32_t qt) {
     const int32_t last = min(k.a.n - 1, ((qt + 1) * k.rows - 1) / k.group);
     return (last >> k.tile_shift) + 1;
 }
-// Tiles of cached keys of request b; at least one where a unit would have none.
-__device__ __forceinline__ int64_t cached_tiles(const Kv4Args &k, int32_t b) {
-    const int64_t t = (kv4_length(k.a.cache, b) + (1 << k.tile_shift) - 1) >> k.tile_shift;
+// Tiles of `len` cached keys; at least one where a unit would have none.
+__device__ __forceinline__ int32_t cached_tiles(const Kv4Args &k, int32_t len) {
+    const int32_t t = (len + (1 << k.tile_shift) - 1) >> k.tile_shift;
     return t < 1 && !k.a.kn ? 1 : t;
 }
+__device__ __forceinline__ int32_t length_of(const Kv4Args &k, int32_t b) { return static_cast<int32_t>(kv4_length(k.a.cache, b)); }
 
-// Where a CTA begins and ends, and the unit that its first tile belongs to.
+// A CTA's tiles [begin, end) of the line, and the unit that the first of them belongs to.
 struct Place {
-    int64_t total, begin, end;  // tiles of the line
-    int64_t ctas;               // CTAs that share it
-    int64_t snap;               // how far cuts were moved at most
-    int64_t off;                // the first tile's place in its unit
+    int32_t begin, end;
     int32_t b, hk, qt;
+    int32_t off;  // the first tile's place in its unit
 };
 struct Spot {
     int32_t b, hk, qt;
-    int64_t off, unit;  // place in the unit, and its tiles
+    int32_t off, unit;  // place in the unit, and its tiles
 };
-
-__device__ __forceinline__ int64_t quotient(int64_t x, int64_t y) {  // x >= 0, y > 0
-    if (((x | y) >> 32) == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
-    return x / y;
-}
-
-// Sum over the block; every thread gets it.  `red`: one slot a warp.
-static __device__ __noinline__ int64_t block_sum64(int64_t v, int64_t *red) {
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(kFull, v, off);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-    __syncthreads();
-    int64_t t = 0;
-    for (int w = 0; w < static_cast<int>(blockDim.x) / 32; ++w) t += red[w];
-    return t;
-}
 
 // The unit `off` tiles into request b, which has ct tiles of cached keys and `per` of new keys for each
 // kv head.
-static __device__ __noinline__ Spot spot_of(const Kv4Args &k, int32_t b, int64_t ct, int64_t off, int64_t per) {
-    const int64_t block = k.QT * ct + per;
+__device__ __forceinline__ Spot spot_of(const Kv4Args &k, int32_t b, int32_t ct, int32_t off, int32_t per) {
     Spot s;
     s.b = b;
-    s.hk = static_cast<int32_t>(quotient(off, block));
+    const uint32_t block = k.QT * ct + per;
+    s.hk = static_cast<uint32_t>(off) / block;
     off -= s.hk * block;
-    if (k.a.mask || !k.a.kn) {
+    if (k.QT == 1 || k.a.mask || !k.a.kn) {
         s.unit = ct + new_tiles(k, 0);
-        s.qt = static_cast<int32_t>(quotient(off, s.unit));
+        s.qt = k.QT == 1 ? 0 : static_cast<uint32_t>(off) / static_cast<uint32_t>(s.unit);
         off -= s.qt * s.unit;
     } else {
         s.qt = 0;
@@ -143,11 +138,10 @@ static __device__ __noinline__ Spot spot_of(const Kv4Args &k, int32_t b, int64_t
     s.off = off;
     return s;
 }
-
 // Moves a cut that falls within `snap` tiles of a unit's end to the nearer end: a unit cut in two costs
 // partial sums of all its rows, written and read again.  True: to the unit's own end.
-__device__ __forceinline__ bool move_cut(int64_t &cut, const Spot &s, int64_t snap) {
-    const int64_t left = s.unit - s.off;
+__device__ __forceinline__ bool move_cut(int32_t &cut, const Spot &s, int32_t snap) {
+    const int32_t left = s.unit - s.off;
     if (s.off <= left) {
         if (s.off <= snap) cut -= s.off;
         return false;
@@ -156,13 +150,20 @@ __device__ __forceinline__ bool move_cut(int64_t &cut, const Spot &s, int64_t sn
     cut += left;
     return true;
 }
-// The place of the CTA whose share runs from cut[0] to cut[1], which lie at the given spots.  False:
-// nothing to do.
-__device__ __forceinline__ bool place_at(const Kv4Args &k, Place *p, int64_t total, int64_t ctas, int64_t cut0, int64_t cut1,
+// CTA c's raw cuts: c total / ctas and the next, rounded down.
+__device__ __forceinline__ void raw_cuts(const Kv4Args &k, uint32_t total, uint32_t &ctas, int32_t &cut0, int32_t &cut1) {
+    const uint32_t want = (total + k.min_tiles - 1) / k.min_tiles, c = blockIdx.x;
+    ctas = min(max(want, 1u), gridDim.x);
+    const uint32_t q = total / ctas, r = total - q * ctas;
+    cut0 = c * q + c * r / ctas;
+    cut1 = (c + 1) * q + (c + 1) * r / ctas;
+}
+// The place of the CTA whose raw cuts lie at the given spots.  False: nothing to do.
+__device__ __forceinline__ bool place_at(const Kv4Args &k, Place *p, uint32_t total, uint32_t ctas, int32_t cut0, int32_t cut1,
                                          Spot s0, const Spot &s1) {
     // at most a third of a CTA's share, so that few tiles still spread over all CTAs
-    const int64_t snap = min(static_cast<int64_t>(k.snap), quotient(total, 3 * ctas));
-    const int64_t was = cut0;
+    const int32_t snap = min(static_cast<uint32_t>(k.snap), total / (3 * ctas));
+    const int32_t was = cut0;
     if (move_cut(cut0, s0, snap)) {  // the next unit's first tile
         s0.off = 0;
         if (++s0.qt == k.QT) {
@@ -175,84 +176,95 @@ __device__ __forceinline__ bool place_at(const Kv4Args &k, Place *p, int64_t tot
     } else {
         s0.off -= was - cut0;
     }
-    if (cut1 < total) move_cut(cut1, s1, snap);
-    *p = Place{total, cut0, cut1, ctas, snap, s0.off, s0.b, s0.hk, s0.qt};
+    if (static_cast<uint32_t>(cut1) < total) move_cut(cut1, s1, snap);
+    *p = Place{cut0, cut1, s0.b, s0.hk, s0.qt, s0.off};
     return cut0 < cut1;
-}
-__device__ __forceinline__ int64_t ctas_of(const Kv4Args &k, int64_t total) {
-    const int64_t want = quotient(total + k.min_tiles - 1, k.min_tiles);
-    return want < gridDim.x ? (want < 1 ? 1 : want) : gridDim.x;
 }
 
 // At most 32 requests: every warp finds the place by itself (one request a lane), with no barrier.
-static __device__ __noinline__ bool find_place_warp(const Kv4Args &k, Place *p) {
+__device__ __forceinline__ bool find_place_warp(const Kv4Args &k, Place *p) {
     const int32_t lane = threadIdx.x & 31;
-    const int64_t ct = lane < k.a.B ? cached_tiles(k, lane) : 0;
-    int64_t per = 0;
-    if (k.a.mask || !k.a.kn) {
-        per = static_cast<int64_t>(k.QT) * new_tiles(k, 0);
+    const int32_t ct = lane < k.a.B ? cached_tiles(k, length_of(k, lane)) : 0;
+    int32_t per;
+    if (k.QT == 1 || k.a.mask || !k.a.kn) {
+        per = k.QT * new_tiles(k, 0);
     } else {
+        per = 0;
         for (int32_t q = lane; q < k.QT; q += 32) per += new_tiles(k, q);
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) per += __shfl_xor_sync(kFull, per, off);
+        per = __reduce_add_sync(kFull, per);
     }
-    const int64_t w = lane < k.a.B ? k.a.cache.Hk * (k.QT * ct + per) : 0;
-    int64_t inc = w;
+    const int32_t w = lane < k.a.B ? k.a.cache.Hk * (k.QT * ct + per) : 0;
+    int32_t inc = w;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-        const int64_t o = __shfl_up_sync(kFull, inc, off);
+        const int32_t o = __shfl_up_sync(kFull, inc, off);
         if (lane >= off) inc += o;
     }
-    const int64_t total = __shfl_sync(kFull, inc, 31), ctas = ctas_of(k, total), c = blockIdx.x;
-    if (c >= ctas) return false;
-    const int64_t cut0 = quotient(c * total, ctas), cut1 = quotient((c + 1) * total, ctas);
-    // the lanes' runs are ascending: the first whose end lies behind the cut holds it
-    const int32_t b0 = __ffs(__ballot_sync(kFull, inc > cut0)) - 1;
-    const int32_t b1 = cut1 < total ? __ffs(__ballot_sync(kFull, inc > cut1)) - 1 : b0;
-    const int64_t lo = inc - w;
-    const int64_t lo0 = __shfl_sync(kFull, lo, b0), lo1 = __shfl_sync(kFull, lo, b1);
-    const int64_t ct0 = __shfl_sync(kFull, ct, b0), ct1 = __shfl_sync(kFull, ct, b1);
-    const Spot s0 = spot_of(k, b0, ct0, cut0 - lo0, per);
-    const Spot s1 = cut1 < total ? spot_of(k, b1, ct1, cut1 - lo1, per) : s0;
-    return place_at(k, p, total, ctas, cut0, cut1, s0, s1);
+    const uint32_t total = __shfl_sync(kFull, inc, 31);
+    uint32_t ctas;
+    int32_t cut0, cut1;
+    raw_cuts(k, total, ctas, cut0, cut1);
+    if (blockIdx.x >= ctas) return false;
+    // the lanes' runs are ascending: the first whose end lies behind a cut holds it
+    Spot s[2];
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i) {
+        const int32_t cut = min(i ? cut1 : cut0, static_cast<int32_t>(total) - 1);
+        const int32_t b = __ffs(__ballot_sync(kFull, inc > cut)) - 1;
+        const Spot x = spot_of(k, b, __shfl_sync(kFull, ct, b), cut - __shfl_sync(kFull, inc - w, b), per);
+        if (i) s[1] = x;
+        else s[0] = x;
+    }
+    return place_at(k, p, total, ctas, cut0, cut1, s[0], s[1]);
 }
 
-// More: all threads of the block together.  `red`: a slot a warp.
-static __device__ __noinline__ bool find_place_block(const Kv4Args &k, Place *p, int64_t *red, Spot *spots) {
-    const int32_t tid = threadIdx.x, nt = blockDim.x, B = k.a.B;
-    const int64_t Hk = k.a.cache.Hk;
-    int64_t per = 0;
+// Sum over the block; every thread gets it.  `red`: one slot a warp.
+static __device__ __noinline__ int32_t block_sum(int32_t v, int32_t *red) {
+    v = __reduce_add_sync(kFull, v);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    int32_t t = 0;
+    for (int w = 0; w < static_cast<int>(blockDim.x) / 32; ++w) t += red[w];
+    return t;
+}
+// More: all threads of the block together.
+static __device__ __noinline__ bool find_place_block(const Kv4Args &k, Place *p, int32_t *red, Spot *spots) {
+    const int32_t tid = threadIdx.x, nt = blockDim.x, B = k.a.B, Hk = k.a.cache.Hk;
+    int32_t per = 0;
     if (k.a.mask || !k.a.kn) {
-        per = static_cast<int64_t>(k.QT) * new_tiles(k, 0);
+        per = k.QT * new_tiles(k, 0);
     } else {
         for (int32_t q = tid; q < k.QT; q += nt) per += new_tiles(k, q);
-        per = block_sum64(per, red);
+        per = block_sum(per, red);
     }
-    int64_t mine = 0;
-    for (int32_t b = tid; b < B; b += nt) mine += Hk * (k.QT * cached_tiles(k, b) + per);
-    const int64_t total = block_sum64(mine, red), ctas = ctas_of(k, total), c = blockIdx.x;
-    if (c >= ctas) return false;
-    const int64_t cut[2] = {quotient(c * total, ctas), quotient((c + 1) * total, ctas)};
+    int32_t mine = 0;
+    for (int32_t b = tid; b < B; b += nt) mine += Hk * (k.QT * cached_tiles(k, length_of(k, b)) + per);
+    const uint32_t total = block_sum(mine, red);
+    uint32_t ctas;
+    int32_t cut[2];
+    raw_cuts(k, total, ctas, cut[0], cut[1]);
+    if (blockIdx.x >= ctas) return false;
     // the requests that hold the tiles behind the two cuts
-    int64_t base = 0;
+    int32_t base = 0;
     for (int32_t b0 = 0; b0 < B; b0 += nt) {
         const int32_t b = b0 + tid;
-        const int64_t ct = b < B ? cached_tiles(k, b) : 0, w = b < B ? Hk * (k.QT * ct + per) : 0;
-        int64_t inc = w;
+        const int32_t ct = b < B ? cached_tiles(k, length_of(k, b)) : 0, w = b < B ? Hk * (k.QT * ct + per) : 0;
+        int32_t inc = w;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
-            const int64_t o = __shfl_up_sync(kFull, inc, off);
+            const int32_t o = __shfl_up_sync(kFull, inc, off);
             if ((tid & 31) >= off) inc += o;
         }
         __syncthreads();
         if ((tid & 31) == 31) red[tid >> 5] = inc;
         __syncthreads();
-        int64_t before = base, all = base;
+        int32_t before = base, all = base;
         for (int w2 = 0; w2 < nt / 32; ++w2) {
             if (w2 < (tid >> 5)) before += red[w2];
             all += red[w2];
         }
-        const int64_t lo = before + inc - w;
+        const int32_t lo = before + inc - w;
 #pragma unroll 1
         for (int i = 0; i < 2; ++i)
             if (cut[i] >= lo && cut[i] < lo + w) spots[i] = spot_of(k, b, ct, cut[i] - lo, per);
@@ -260,18 +272,18 @@ static __device__ __noinline__ bool find_place_block(const Kv4Args &k, Place *p,
         if (cut[1] < base) break;
     }
     __syncthreads();
-    return place_at(k, p, total, ctas, cut[0], cut[1], spots[0], spots[cut[1] < total]);
+    return place_at(k, p, total, ctas, cut[0], cut[1], spots[0], spots[static_cast<uint32_t>(cut[1]) < total]);
 }
-__device__ __forceinline__ bool find_place(const Kv4Args &k, Place *p, int64_t *red, Spot *spots) {
+__device__ __forceinline__ bool find_place(const Kv4Args &k, Place *p, int32_t *red, Spot *spots) {
     return k.a.B <= 32 ? find_place_warp(k, p) : find_place_block(k, p, red, spots);
 }
 
 // A CTA's run through the line, unit by unit: [s0, s1) of the unit's tiles.
 struct Walk {
     int32_t b, hk, qt;
-    int64_t t, s0, s1, unit;
+    int32_t t, s0, s1, unit;
     int32_t nt;  // tiles of new keys (the unit's first)
-    int64_t len;
+    int32_t len;
 
     __device__ __forceinline__ void start(const Kv4Args &k, const Place &p) {
         b = p.b;
@@ -279,13 +291,12 @@ struct Walk {
         qt = p.qt;
         t = p.begin;
         s0 = p.off;
-        len = kv4_length(k.a.cache, b);
+        len = length_of(k, b);
         fill(k, p);
     }
     __device__ __forceinline__ void fill(const Kv4Args &k, const Place &p) {
         nt = new_tiles(k, qt);
-        unit = ((len + (1 << k.tile_shift) - 1) >> k.tile_shift) + nt;
-        unit = unit < 1 ? 1 : unit;  // nothing cached and no new keys: a tile with no keys
+        unit = cached_tiles(k, len) + nt;
         s1 = min(unit, s0 + (p.end - t));
     }
     __device__ __forceinline__ bool next(const Kv4Args &k, const Place &p) {
@@ -297,7 +308,7 @@ struct Walk {
             if (++hk == k.a.cache.Hk) {
                 hk = 0;
                 if (++b == k.a.B) return false;  // lengths changed under the call
-                len = kv4_length(k.a.cache, b);
+                len = length_of(k, b);
             }
         }
         fill(k, p);
@@ -305,18 +316,9 @@ struct Walk {
     }
 };
 
-// What CTA blockIdx.x leaves for the merge, given that its first unit was begun by an earlier one.  The
-// cuts left inside a unit [u0, u1) are those of CTAs c with u0 + snap < c total / ctas < u1 - snap; the
-// CTA before the first of them began the unit.
-static __device__ __noinline__ Kv4Share share_of(const Kv4Args &k, const Place &p, const Walk &w) {
-    Kv4Share sh{-1, 0, 0, 0, 0};
-    if (w.s0 > 0) {
-        const int64_t u0 = p.begin - w.s0, c = blockIdx.x;
-        if (quotient((c - 1) * p.total, p.ctas) <= u0 + p.snap)
-            sh = Kv4Share{w.b, w.hk, w.qt, static_cast<int32_t>(c) - 1,
-                          static_cast<int32_t>(quotient((u0 + w.unit - p.snap) * p.ctas - 1, p.total))};
-    }
-    return sh;
+// What CTA blockIdx.x leaves for the merge.
+__device__ __forceinline__ Kv4Share share_of(const Walk &w) {
+    return Kv4Share{w.s0 == 0 ? 0 : (w.s1 == w.unit ? 1 : 2), w.b, w.hk, w.qt};
 }
 // Where a segment's partial sums go: slot 0 of its CTA for a unit that an earlier CTA began, else 1.
 __device__ __forceinline__ int64_t slot_of(const Walk &w) { return 2 * static_cast<int64_t>(blockIdx.x) + (w.s0 > 0 ? 0 : 1); }
