@@ -38,7 +38,7 @@ namespace {
 constexpr int kTile = 64;       // keys of a tile: a chunk of 16 for each of the 4 warps
 constexpr int kWarps = 4;       // warps that multiply
 constexpr int kThreads = kWarps * 32 + 32;  // and one that copies
-constexpr int kStages = 4;
+constexpr int kStages = 5;
 constexpr int kMinTiles = 2;    // tiles a CTA takes at least
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -175,6 +175,7 @@ __global__ void __launch_bounds__(kThreads, Shape<G, NQ>::kBlocks) kv4_attention
         float o[2 * G][NQ][4];      // dims (rows) x queries
         float om[NQ][4];            // groups (rows gq < G) x queries: sum of p m
         float ref[NQ][2], l[NQ][2];
+        int32_t node_of[NQ][2];     // the columns' nodes, -1 behind the last row
         // p = 2^(score - ref), at most 2^top; a new ref puts the largest at 2^aim
         float aim = 9.0f, top = 12.0f;
 #pragma unroll
@@ -223,6 +224,8 @@ __global__ void __launch_bounds__(kThreads, Shape<G, NQ>::kBlocks) kv4_attention
             const float hi = __half2float(__float2half_rn(sum));
             qs[nq] = pack_f16(hi, sum - hi);
             const float mul = inv * k.scale2 * 16777216.0f;
+            node_of[nq][0] = __shfl_sync(kFull, live ? node : -1, 8 * qd);
+            node_of[nq][1] = __shfl_sync(kFull, live ? node : -1, 8 * qd + 4);
             qk[nq][0] = __shfl_sync(kFull, mul, 8 * qd);
             qk[nq][1] = __shfl_sync(kFull, mul, 8 * qd + 4);
 #pragma unroll
@@ -238,16 +241,19 @@ __global__ void __launch_bounds__(kThreads, Shape<G, NQ>::kBlocks) kv4_attention
                 for (int e2 = 0; e2 < 4; ++e2) o[t][nq][e2] = 0.0f;
         }
 
-        // scores in base 2 (t: keys gq, gq + 8 x queries 2 qd, 2 qd + 1) to p, with the running
+        // scores in base 2 (t: pairs of two keys x queries 2 qd, 2 qd + 1) to p, with the running
         // maximum, the sum and what was accumulated so far brought to the same reference
-        auto softmax = [&](float (&t)[NQ][4]) {
+        auto softmax = [&](auto &t) {
+            constexpr int N = sizeof(t[0]) / sizeof(float);
             bool raise = false;
             float corr[NQ][2];
 #pragma unroll
             for (int nq = 0; nq < NQ; ++nq)
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    float mx = fmaxf(t[nq][c], t[nq][c + 2]);
+                    float mx = t[nq][c];
+#pragma unroll
+                    for (int e = c + 2; e < N; e += 2) mx = fmaxf(mx, t[nq][e]);
 #pragma unroll
                     for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, off));
                     corr[nq][c] = 1.0f;
@@ -272,14 +278,15 @@ __global__ void __launch_bounds__(kThreads, Shape<G, NQ>::kBlocks) kv4_attention
                 }
             }
 #pragma unroll
-            for (int nq = 0; nq < NQ; ++nq)
+            for (int nq = 0; nq < NQ; ++nq) {
+                const float r0 = ref[nq][0] == -INFINITY ? 0.0f : ref[nq][0], r1 = ref[nq][1] == -INFINITY ? 0.0f : ref[nq][1];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float r = ref[nq][e & 1];
-                    const float pv = ex2_approx(t[nq][e] - (r == -INFINITY ? 0.0f : r));
+                for (int e = 0; e < N; ++e) {
+                    const float pv = ex2_approx(t[nq][e] - (e & 1 ? r1 : r0));
                     t[nq][e] = pv;
                     l[nq][e & 1] += pv;
                 }
+            }
         };
 
         int32_t s = w.s0;
@@ -316,10 +323,9 @@ __global__ void __launch_bounds__(kThreads, Shape<G, NQ>::kBlocks) kv4_attention
             for (int nq = 0; nq < NQ; ++nq)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const int32_t row = w.qt * kRows + nq * 8 + 2 * qd + (e & 1), key = e < 2 ? ka : kb;
-                    bool vis = row < k.Mq && key < a.n;
+                    const int32_t node = node_of[nq][e & 1], key = e < 2 ? ka : kb;
+                    bool vis = node >= 0 && key < a.n;
                     if (vis) {
-                        const int32_t node = row / k.group;
                         vis = a.mask ? (a.mask[(krow + node) * k.W + (key >> 5)] >> (key & 31)) & 1u : key <= node;
                     }
                     see[nq][e] = vis;
@@ -408,31 +414,43 @@ __global__ void __launch_bounds__(kThreads, Shape<G, NQ>::kBlocks) kv4_attention
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[i][nq][e] *= e < 2 ? 0x1p-24f : 0x1p-20f;
 
-        // ---------------- cached keys ----------------
-        for (; s < w.s1; ++s, ++taken) {
-            const int32_t st = taken % kStages;
-            kv4_wait(&full[st], taken / kStages, abort_flag);
-            const int32_t nv = __shfl_sync(kFull, *abort_flag ? 0 : valid[st][warp], 0);
-            if (nv > 0) {
-                const uint8_t *ch = smem + S::kRing + st * S::kStageBytes + warp * kv4_chunk_bytes(G);
-                // scores of keys kv4 rows gq, gq + 8
-                float sc[NQ][4];
-                {
-                    const uint8_t *kp = ch + kv4_key_params(G);
-                    const uint32_t ma = qd < G ? *reinterpret_cast<const uint32_t *>(kp + gq * 4 * G + 4 * qd) : 0u;
-                    const uint32_t mb = qd < G ? *reinterpret_cast<const uint32_t *>(kp + (gq + 8) * 4 * G + 4 * qd) : 0u;
-                    const uint32_t a0 = __byte_perm(ma, ma, 0x3232), a1 = __byte_perm(mb, mb, 0x3232);
+        // ---------------- cached keys: two stages, i.e. two chunks of the warp, at a time ----------
+#pragma unroll 1
+        for (; s < w.s1; s += 2) {
+            const int32_t count = min(w.s1 - s, 2);
+            const int32_t st0 = taken % kStages, st1 = (taken + 1) % kStages;
+            kv4_wait(&full[st0], taken / kStages, abort_flag);
+            if (count == 2) kv4_wait(&full[st1], (taken + 1) / kStages, abort_flag);
+            int32_t nv[2];  // keys of the chunks that are there
+            nv[0] = valid[st0][warp];
+            nv[1] = count == 2 ? valid[st1][warp] : 0;
+            nv[0] = __shfl_sync(kFull, *abort_flag ? 0 : nv[0], 0);
+            nv[1] = __shfl_sync(kFull, *abort_flag ? 0 : nv[1], 0);
+            if (nv[0] + nv[1] > 0) {
+                const uint8_t *ch[2] = {smem + S::kRing + st0 * S::kStageBytes + warp * kv4_chunk_bytes(G),
+                                        smem + S::kRing + st1 * S::kStageBytes + warp * kv4_chunk_bytes(G)};
+                // scores of each chunk's key rows gq, gq + 8
+                float sc[NQ][8];
 #pragma unroll
-                    for (int nq = 0; nq < NQ; ++nq) {
+                for (int u = 0; u < 2; ++u) {
+                    const uint8_t *kp = ch[u] + kv4_key_params(G);
+                    float x[NQ][4];
+                    {
+                        const uint32_t ma = qd < G ? *reinterpret_cast<const uint32_t *>(kp + gq * 4 * G + 4 * qd) : 0u;
+                        const uint32_t mb = qd < G ? *reinterpret_cast<const uint32_t *>(kp + (gq + 8) * 4 * G + 4 * qd) : 0u;
+                        const uint32_t a0 = __byte_perm(ma, ma, 0x3232), a1 = __byte_perm(mb, mb, 0x3232);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) sc[nq][e] = 0.0f;
-                        mma_f16(sc[nq], a0, a1, 0u, 0u, qs[nq], 0u);
+                        for (int nq = 0; nq < NQ; ++nq) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) sc[nq][e] *= 0x1p-24f;
+                            for (int e = 0; e < 4; ++e) x[nq][e] = 0.0f;
+                            mma_f16(x[nq], a0, a1, 0u, 0u, qs[nq], 0u);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) x[nq][e] *= 0x1p-24f;
+                        }
                     }
                     uint32_t wa[G], wb[G], pa[G], pb[G];
-                    load_words<G>(ch + gq * 16 * G + qd * 4 * G, wa);
-                    load_words<G>(ch + (gq + 8) * 16 * G + qd * 4 * G, wb);
+                    load_words<G>(ch[u] + gq * 16 * G + qd * 4 * G, wa);
+                    load_words<G>(ch[u] + (gq + 8) * 16 * G + qd * 4 * G, wb);
                     load_words<G>(kp + gq * 4 * G, pa);
                     load_words<G>(kp + (gq + 8) * 4 * G, pb);
 #pragma unroll
@@ -446,53 +464,40 @@ __global__ void __launch_bounds__(kThreads, Shape<G, NQ>::kBlocks) kv4_attention
                                     wb[g] & 0x00f000f0u, qf[2 * g][nq][0], qf[2 * g][nq][1]);
                             mma_f16(acc, xa & 0x000f000fu, xb & 0x000f000fu, xa & 0x00f000f0u, xb & 0x00f000f0u,
                                     qf[2 * g + 1][nq][0], qf[2 * g + 1][nq][1]);
-                            sc[nq][0] = fmaf(sa, acc[0], sc[nq][0]);
-                            sc[nq][1] = fmaf(sa, acc[1], sc[nq][1]);
-                            sc[nq][2] = fmaf(sb, acc[2], sc[nq][2]);
-                            sc[nq][3] = fmaf(sb, acc[3], sc[nq][3]);
+                            x[nq][0] = fmaf(sa, acc[0], x[nq][0]);
+                            x[nq][1] = fmaf(sa, acc[1], x[nq][1]);
+                            x[nq][2] = fmaf(sb, acc[2], x[nq][2]);
+                            x[nq][3] = fmaf(sb, acc[3], x[nq][3]);
                         }
                     }
-                }
-                // MMA row i is key t with kv4_key_slot(t) = i
-                const int32_t ta = (gq >> 1) | ((gq & 1) << 2);
-#pragma unroll
-                for (int nq = 0; nq < NQ; ++nq)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) sc[nq][e] *= qk[nq][e & 1];
-                if (nv < 16) {
 #pragma unroll
                     for (int nq = 0; nq < NQ; ++nq)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (ta + (e < 2 ? 0 : 8) >= nv) sc[nq][e] = -INFINITY;
+                        for (int e = 0; e < 4; ++e) sc[nq][4 * u + e] = x[nq][e] * qk[nq][e & 1];
                 }
-                // values: keys qd, qd + 4, qd + 8, qd + 12
-                const uint8_t *vp = ch + kv4_value_params(G);
-                uint32_t par[4][G];
+                const bool tail = nv[0] + nv[1] < 32;
+                if (tail) {
+                    // MMA row i is key t with kv4_key_slot(t) = i
+                    const int32_t ta = (gq >> 1) | ((gq & 1) << 2);
 #pragma unroll
-                for (int u = 0; u < 4; ++u) load_words<G>(vp + (qd + 4 * u) * 4 * G, par[u]);
-                uint32_t mm[4] = {0u, 0u, 0u, 0u};
-                if (gq < G) {
+                    for (int nq = 0; nq < NQ; ++nq)
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) mm[u] = *reinterpret_cast<const uint32_t *>(vp + (qd + 4 * u) * 4 * G + 4 * gq);
-                }
-                if (nv < 16) {  // what lies behind the last key is not a number that may be used
-#pragma unroll
-                    for (int u = 0; u < 4; ++u)
-                        if (qd + 4 * u >= nv) {
-                            mm[u] = 0u;
-#pragma unroll
-                            for (int g = 0; g < G; ++g) par[u][g] = 0u;
-                        }
+                        for (int e = 0; e < 8; ++e)
+                            if (ta + (e & 2 ? 8 : 0) >= nv[e >> 2]) sc[nq][e] = -INFINITY;
                 }
                 // p s must stay below fp16's largest: with p up to 2^12, s below 16.  Steeper
-                // values (s up to 2^12.1) take p up to 2^3 from here on.
+                // values (s up to 2^12.1) take p up to 2^3 from here on.  Each lane looks at its
+                // share of the chunks' 16 G scales.
                 if (aim != 0.0f) {
                     bool steep = false;
 #pragma unroll
-                    for (int u = 0; u < 4; ++u)
+                    for (int u = 0; u < 2; ++u)
 #pragma unroll
-                        for (int g = 0; g < G; ++g) steep = steep || (par[u][g] & 0xffffu) >= 0x4c00u;  // s >= 16, or NaN
+                        for (int i = 0; i < (G + 1) / 2; ++i) {
+                            const int32_t at = lane + 32 * i;
+                            if (at < 16 * G && at / G < nv[u])  // s >= 16, or NaN
+                                steep = steep || (reinterpret_cast<const uint32_t *>(ch[u] + kv4_value_params(G))[at] & 0xffffu) >= 0x4c00u;
+                        }
                     if (__any_sync(kFull, steep)) {
                         aim = 0.0f;
                         top = 3.0f;
@@ -512,45 +517,71 @@ __global__ void __launch_bounds__(kThreads, Shape<G, NQ>::kBlocks) kv4_attention
                     }
                 }
                 softmax(sc);
-                uint32_t b0[NQ], b1[NQ];
+                // values: keys qd, qd + 4, qd + 8, qd + 12 of each chunk
 #pragma unroll
-                for (int nq = 0; nq < NQ; ++nq) {
-                    b0[nq] = transpose8(pack_f16(sc[nq][0], sc[nq][1]));
-                    b1[nq] = transpose8(pack_f16(sc[nq][2], sc[nq][3]));
-                    mma_f16(om[nq], __byte_perm(mm[0], mm[1], 0x7632), 0u, __byte_perm(mm[2], mm[3], 0x7632), 0u, b0[nq], b1[nq]);
-                }
-                const uint8_t *vc = ch + kv4_value_codes(G);
-                uint32_t vw[4][(G + 1) / 2];  // two groups a word
+                for (int u = 0; u < 2; ++u) {
+                    const uint8_t *vp = ch[u] + kv4_value_params(G);
+                    uint32_t par[4][G];
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const int32_t t = qd + 4 * u;
-                    const uint8_t *src = vc + t * 16 * G + kv4_value_word(t, gq, 0, G);
-                    if constexpr (G == 4 || G == 2) {
-                        load_words<G / 2>(src, vw[u]);
-                    } else {
+                    for (int i = 0; i < 4; ++i) load_words<G>(vp + (qd + 4 * i) * 4 * G, par[i]);
+                    uint32_t mm[4] = {0u, 0u, 0u, 0u};
+                    if (gq < G) {
 #pragma unroll
-                        for (int g = 0; g < G; ++g) {
-                            const uint32_t x = reinterpret_cast<const uint16_t *>(src)[g];
-                            vw[u][g / 2] = g & 1 ? vw[u][g / 2] | (x << 16) : x;
-                        }
+                        for (int i = 0; i < 4; ++i) mm[i] = *reinterpret_cast<const uint32_t *>(vp + (qd + 4 * i) * 4 * G + 4 * gq);
                     }
-                }
+                    if (tail) {  // what lies behind the last key is not a number that may be used
 #pragma unroll
-                for (int g = 0; g < G; ++g) {
-                    const uint32_t sel = g & 1 ? 0x7632 : 0x5410;
-                    const uint32_t x = __byte_perm(vw[0][g / 2], vw[1][g / 2], sel), y = __byte_perm(vw[2][g / 2], vw[3][g / 2], sel);
-                    const uint32_t x8 = x >> 8, y8 = y >> 8;
-                    const uint32_t s01 = __byte_perm(par[0][g], par[1][g], 0x5410), s23 = __byte_perm(par[2][g], par[3][g], 0x5410);
+                        for (int i = 0; i < 4; ++i)
+                            if (qd + 4 * i >= nv[u]) {
+                                mm[i] = 0u;
+#pragma unroll
+                                for (int g = 0; g < G; ++g) par[i][g] = 0u;
+                            }
+                    }
+                    uint32_t b0[NQ], b1[NQ];
 #pragma unroll
                     for (int nq = 0; nq < NQ; ++nq) {
-                        const uint32_t p0 = mul_f16x2(b0[nq], s01), p1 = mul_f16x2(b1[nq], s23);
-                        mma_f16(o[2 * g][nq], x & 0x000f000fu, x & 0x00f000f0u, y & 0x000f000fu, y & 0x00f000f0u, p0, p1);
-                        mma_f16(o[2 * g + 1][nq], x8 & 0x000f000fu, x8 & 0x00f000f0u, y8 & 0x000f000fu, y8 & 0x00f000f0u, p0, p1);
+                        b0[nq] = transpose8(pack_f16(sc[nq][4 * u], sc[nq][4 * u + 1]));
+                        b1[nq] = transpose8(pack_f16(sc[nq][4 * u + 2], sc[nq][4 * u + 3]));
+                        mma_f16(om[nq], __byte_perm(mm[0], mm[1], 0x7632), 0u, __byte_perm(mm[2], mm[3], 0x7632), 0u, b0[nq], b1[nq]);
+                    }
+                    const uint8_t *vc = ch[u] + kv4_value_codes(G);
+                    uint32_t vw[4][(G + 1) / 2];  // two groups a word
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int32_t t = qd + 4 * i;
+                        const uint8_t *src = vc + t * 16 * G + kv4_value_word(t, gq, 0, G);
+                        if constexpr (G == 4 || G == 2) {
+                            load_words<G / 2>(src, vw[i]);
+                        } else {
+#pragma unroll
+                            for (int g = 0; g < G; ++g) {
+                                const uint32_t x = reinterpret_cast<const uint16_t *>(src)[g];
+                                vw[i][g / 2] = g & 1 ? vw[i][g / 2] | (x << 16) : x;
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int g = 0; g < G; ++g) {
+                        const uint32_t sel = g & 1 ? 0x7632 : 0x5410;
+                        const uint32_t x = __byte_perm(vw[0][g / 2], vw[1][g / 2], sel), y = __byte_perm(vw[2][g / 2], vw[3][g / 2], sel);
+                        const uint32_t x8 = x >> 8, y8 = y >> 8;
+                        const uint32_t s01 = __byte_perm(par[0][g], par[1][g], 0x5410), s23 = __byte_perm(par[2][g], par[3][g], 0x5410);
+#pragma unroll
+                        for (int nq = 0; nq < NQ; ++nq) {
+                            const uint32_t p0 = mul_f16x2(b0[nq], s01), p1 = mul_f16x2(b1[nq], s23);
+                            mma_f16(o[2 * g][nq], x & 0x000f000fu, x & 0x00f000f0u, y & 0x000f000fu, y & 0x00f000f0u, p0, p1);
+                            mma_f16(o[2 * g + 1][nq], x8 & 0x000f000fu, x8 & 0x00f000f0u, y8 & 0x000f000fu, y8 & 0x00f000f0u, p0, p1);
+                        }
                     }
                 }
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&empty[st]);
+            if (lane == 0) {
+                mbar_arrive(&empty[st0]);
+                if (count == 2) mbar_arrive(&empty[st1]);
+            }
+            taken += count;
         }
 
         // ---------------- the warps' shares of the segment meet ----------------
@@ -672,8 +703,8 @@ Variant variant_of(int32_t mq) {
     // query rows a unit takes: 8, 16 or 32
     if (mq <= 8) return Variant{8, kThreads, Shape<G, 1>::kTotal, kv4_attention_kernel<G, 1>};
     if (mq <= 16) return Variant{16, kThreads, Shape<G, 2>::kTotal, kv4_attention_kernel<G, 2>};
-    if (mq > 32 && (G == 2 || G == 4)) return Variant{kKv4TcRows, 0, 0, nullptr};
-    return Variant{32, kThreads, Shape<G, 4>::kTotal, kv4_attention_kernel<G, 4>};
+    if constexpr (G == 2 || G == 4) return Variant{kKv4TcRows, 0, 0, nullptr};
+    else return Variant{32, kThreads, Shape<G, 4>::kTotal, kv4_attention_kernel<G, 4>};
 }
 Variant variant(int32_t G, int32_t mq) {
     switch (G) {
@@ -703,6 +734,7 @@ const Device *device_now() {
     for (int g = 1; g <= 4; ++g)
         for (int i = 0; i < 3; ++i) {
             const Variant v = variant(g, 8 << i);
+            if (!v.kernel) continue;
             int n = 0;
             if (cudaFuncSetAttribute(v.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(v.smem)) != cudaSuccess ||
                 cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, v.kernel, v.threads, v.smem) != cudaSuccess || n < 1)
