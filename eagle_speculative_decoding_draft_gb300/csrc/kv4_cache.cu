@@ -26,11 +26,30 @@ bool kv4_view(const eagle_kv4_cache *c, Kv4View *out) {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr uint32_t kFull = 0xffffffffu;
+
+// Both kernels: a warp takes one chunk (16 positions) of one kv head, whose 640 G bytes it assembles or
+// unpacks in shared memory, so that the cache is written and read in whole lines whatever the order
+// of the codes, and rows of the callers' tensors by 16-byte pieces of neighbouring lanes.  Bound by
+// memory: at 26 k tokens of 8 kv heads of 128 the write moves 141 MB and the read as much.
+struct Units {
+    int32_t Hk, per_request;  // per_request: kv heads x chunks that a request may touch
+    int64_t total;            // warps of work
+};
+// Warp `id` of the launch; `start` is the request's first position.
+__device__ __forceinline__ bool unit_request(const Units &u, int64_t id, int32_t &b, int32_t &rest) {
+    if (id >= u.total) return false;
+    b = static_cast<int32_t>(id / u.per_request);
+    rest = static_cast<int32_t>(id - static_cast<int64_t>(b) * u.per_request);
+    return true;
+}
 
 struct AppendArgs {
     Kv4View v;
-    int32_t B, src_rows, slots, blocks, slots_block;
+    Units u;
+    int32_t B, src_rows, slots;
     const __nv_bfloat16 *k, *w;  // keys and values [B][src_rows] rows of ld elements
     int64_t ld;
     const int32_t *select;       // [B][slots] or null
@@ -43,204 +62,295 @@ struct AppendArgs {
 __device__ __forceinline__ int32_t slots_of(const AppendArgs &a, int32_t b) {
     return a.count ? min(max(a.count[b], 0), a.slots) : a.slots;
 }
+// The request's length after the write: behind its last written slot.  Whole warp.
+__device__ __forceinline__ int32_t length_after(const AppendArgs &a, int32_t b, int64_t start, int32_t cnt) {
+    int32_t last = cnt;
+    if (a.select) {
+        last = 0;
+        for (int32_t j = threadIdx.x & 31; j < cnt; j += 32)
+            if (a.select[static_cast<int64_t>(b) * a.slots + j] >= 0) last = j + 1;
+        last = __reduce_max_sync(kFull, last);
+    }
+    return static_cast<int32_t>(min(start + last, a.v.cap));
+}
 
 // Eight values of a group of 32 that four neighbouring lanes hold: their codes (the first in the
-// low bits) and the group's (s, m).
+// low bits) and the group's (s, m).  A code is a s^-1 rounded to the nearest whole number by a sum
+// with 1.5 2^23 (whose low bits it then is); with r a rounded reciprocal that can miss the nearest by
+// one next to a half, so the remainder a - c s, which is exact, is held against s / 2: beyond it, or at
+// it with c odd, the neighbour on its side is the one.
 __device__ __forceinline__ uint32_t quantise8(const uint4 raw, uint32_t *params) {
-    float x[8];
     const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+    float x[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         x[2 * i] = __uint_as_float(w[i] << 16);
         x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
-    float lo = x[0], hi = x[0];
-    bool ok = true;
+    // NaN passes minima and maxima by, so the magnitudes are checked as whole numbers
+    uint32_t big = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        lo = fminf(lo, x[i]);
-        hi = fmaxf(hi, x[i]);
-        ok = ok && fabsf(x[i]) <= kKv4MaxAbs;  // false for NaN
-    }
+    for (int i = 0; i < 4; ++i) big = max(big, max((w[i] << 16) & 0x7fff0000u, w[i] & 0x7fff0000u));
+    float lo = fminf(fminf(fminf(x[0], x[1]), fminf(x[2], x[3])), fminf(fminf(x[4], x[5]), fminf(x[6], x[7])));
+    float hi = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
 #pragma unroll
     for (int off = 1; off < 4; off <<= 1) {
-        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, off));
-        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, off));
-        ok = __shfl_xor_sync(0xffffffffu, static_cast<int>(ok), off) && ok;
-    }
-    if (!ok) {
-        *params = 0x7fff7fffu;
-        return 0;
+        lo = fminf(lo, __shfl_xor_sync(kFull, lo, off));
+        hi = fmaxf(hi, __shfl_xor_sync(kFull, hi, off));
+        big = max(big, __shfl_xor_sync(kFull, big, off));
     }
     const __half m = __float2half_rd(lo);
     const float mf = __half2float(m);
     const __half s = __float2half_ru(__fdiv_rn(hi - mf, 15.0f));
-    const float sf = __half2float(s);
-    *params = static_cast<uint32_t>(__half_as_ushort(s)) | (static_cast<uint32_t>(__half_as_ushort(m)) << 16);
-    if (sf == 0.0f) return 0;
+    const float sf = __half2float(s), half = 0.5f * sf, r = sf > 0.0f ? __frcp_rn(sf) : 0.0f;
     uint32_t codes = 0;
+    constexpr float kMagic = 12582912.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float c = rintf(__fdiv_rn(x[i] - mf, sf));
-        codes |= static_cast<uint32_t>(min(static_cast<int32_t>(c), 15)) << (4 * i);
+    for (int i = 7; i >= 0; --i) {
+        const float a = x[i] - mf, t = fmaf(a, r, kMagic), rem = fmaf(kMagic - t, sf, a);
+        int32_t c = __float_as_int(t);
+        const bool next = __float_as_int(fabsf(rem)) + (c & 1) > __float_as_int(half);
+        c += next ? (rem < 0.0f ? -1 : 1) : 0;
+        codes = codes * 16u + (static_cast<uint32_t>(c) & 15u);
     }
-    return codes;
+    const bool ok = big <= __float_as_uint(kKv4MaxAbs);
+    *params = ok ? static_cast<uint32_t>(__half_as_ushort(s)) | (static_cast<uint32_t>(__half_as_ushort(m)) << 16) : 0x7fff7fffu;
+    return ok ? codes : 0u;
 }
 
-// Block (request, run of slots): a thread takes 8 dims of a key row and the same 8 of the value
-// row (16 bytes each), so four lanes make a group and consecutive lanes read consecutive memory.
-// Bound by memory: 4 bytes a value pair in, 1.25 out.
+template <int G>
 __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const AppendArgs a) {
-    __shared__ int32_t s_last;
+    constexpr int kPer = 4 * G, R = 32 / kPer, kIters = 16 / R;  // lanes a row, rows at once
+    constexpr int kBytes = kv4_chunk_bytes(G);
+    __shared__ __align__(16) uint8_t stage[kWarps][kBytes];
     pdl_launch_dependents();
     pdl_wait();
-    const int32_t b = blockIdx.x / a.blocks, part = blockIdx.x - b * a.blocks;
+    const int32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int32_t b, rest;
+    if (!unit_request(a.u, static_cast<int64_t>(blockIdx.x) * kWarps + warp, b, rest)) return;
+    const int32_t ci = rest / a.u.Hk, hk = rest - ci * a.u.Hk;
     const int64_t start = a.start[b];
     const int32_t cnt = slots_of(a, b);
     if (start < 0) {
-        if (part == 0 && threadIdx.x == 0) latch(a.status, kDevBounds);
+        if (rest == 0 && lane == 0) latch(a.status, kDevBounds);
         return;
     }
-    const int32_t G = a.v.G, D = G * kKv4Group, per_row = a.v.Hk * D / 8;  // a multiple of 4
-    const int32_t j0 = part * a.slots_block, j1 = min(cnt, j0 + a.slots_block);
-    const int64_t items = static_cast<int64_t>(max(j1 - j0, 0)) * per_row;
-    for (int64_t it0 = threadIdx.x & ~31; it0 < items; it0 += kThreads) {
-        const int64_t it = it0 + (threadIdx.x & 31);
-        const int32_t dj = static_cast<int32_t>(it / per_row), piece = static_cast<int32_t>(it - static_cast<int64_t>(dj) * per_row);
-        const int32_t j = j0 + dj;
-        bool live = it < items;
-        int32_t src = j;
-        if (live && a.select) src = a.select[static_cast<int64_t>(b) * a.slots + j];
-        live = live && src >= 0;
-        const int64_t pos = start + j;
-        if (live && (src >= a.src_rows || pos >= a.v.cap)) {
-            latch(a.status, kDevBounds);
-            live = false;
+    if (a.lengths && rest == 0) {
+        const int32_t len = length_after(a, b, start, cnt);
+        if (lane == 0) a.lengths[b] = len;
+    }
+    // lane t: the source row of position chunk0 + t, or -1
+    const int64_t chunk0 = ((start >> 4) + ci) << 4, j0 = chunk0 - start;
+    int32_t src = -1;
+    {
+        const int64_t j = j0 + lane;
+        if (lane < 16 && j >= 0 && j < cnt) {
+            src = a.select ? a.select[static_cast<int64_t>(b) * a.slots + j] : static_cast<int32_t>(j);
+            if (src >= a.src_rows || (src >= 0 && chunk0 + lane >= a.v.cap)) {
+                latch(a.status, kDevBounds);
+                src = -1;
+            }
         }
-        uint4 rk = make_uint4(0, 0, 0, 0), rv = rk;
-        const int32_t hk = piece / (D / 8), in = piece - hk * (D / 8);
-        uint8_t *chunk = nullptr;
-        if (live) {
-            const int64_t off = (static_cast<int64_t>(b) * a.src_rows + src) * a.ld + static_cast<int64_t>(piece) * 8;
-            rk = *reinterpret_cast<const uint4 *>(a.k + off);
-            rv = *reinterpret_cast<const uint4 *>(a.w + off);
-            chunk = kv4_chunk(a.v, b, hk, pos);
-            if (!chunk) latch(a.status, kDevBounds);
+    }
+    const uint32_t rows = __ballot_sync(kFull, src >= 0);
+    if (rows == 0) return;
+    uint8_t *chunk = kv4_chunk(a.v, b, hk, chunk0);
+    if (!chunk) {
+        if (lane == 0) latch(a.status, kDevBounds);
+        return;
+    }
+    const int32_t piece = lane % kPer, g = piece >> 2, qd = piece & 3;
+    const bool idle = lane / kPer >= R;  // head_dim 96: 24 lanes work
+    uint4 kx[kIters], vx[kIters];
+#pragma unroll
+    for (int i = 0; i < kIters; ++i) {
+        const int32_t t = i * R + lane / kPer, from = __shfl_sync(kFull, src, t & 15);
+        kx[i] = vx[i] = make_uint4(0, 0, 0, 0);
+        if (from >= 0 && !idle) {
+            const int64_t off = (static_cast<int64_t>(b) * a.src_rows + from) * a.ld + (static_cast<int64_t>(hk) * kPer + piece) * 8;
+            kx[i] = __ldg(reinterpret_cast<const uint4 *>(a.k + off));
+            vx[i] = __ldg(reinterpret_cast<const uint4 *>(a.w + off));
         }
+    }
+    uint8_t *st = stage[warp];
+#pragma unroll
+    for (int i = 0; i < kIters; ++i) {
+        const int32_t t = i * R + lane / kPer;
+        if (((rows >> (i * R)) & ((1u << R) - 1u)) == 0) continue;  // warp-uniform
+        const int32_t ks = kv4_key_slot(t & 15);
         uint32_t pk, pv;
-        const uint32_t ck = quantise8(rk, &pk), cv = quantise8(rv, &pv);
-        if (!chunk) continue;
-        const int32_t t = static_cast<int32_t>(pos & 15), ks = kv4_key_slot(t), g = in >> 2, qd = in & 3;
-        *reinterpret_cast<uint32_t *>(chunk + ks * 16 * G + (qd * G + g) * 4) = ck;
-        uint8_t *vrow = chunk + kv4_value_codes(G) + t * 16 * G;
+        const uint32_t ck = quantise8(kx[i], &pk), cv = quantise8(vx[i], &pv);
+        if (idle) continue;
+        *reinterpret_cast<uint32_t *>(st + ks * 16 * G + (qd * G + g) * 4) = ck;
+        uint8_t *vrow = st + kv4_value_codes(G) + t * 16 * G;
         *reinterpret_cast<uint16_t *>(vrow + kv4_value_word(t, 2 * qd, g, G)) = static_cast<uint16_t>(cv);
         *reinterpret_cast<uint16_t *>(vrow + kv4_value_word(t, 2 * qd + 1, g, G)) = static_cast<uint16_t>(cv >> 16);
-        if (qd == 0) *reinterpret_cast<uint32_t *>(chunk + kv4_key_params(G) + ks * 4 * G + 4 * g) = pk;
-        if (qd == 1) *reinterpret_cast<uint32_t *>(chunk + kv4_value_params(G) + t * 4 * G + 4 * g) = pv;
+        if (qd == 0) *reinterpret_cast<uint32_t *>(st + kv4_key_params(G) + ks * 4 * G + 4 * g) = pk;
+        if (qd == 1) *reinterpret_cast<uint32_t *>(st + kv4_value_params(G) + t * 4 * G + 4 * g) = pv;
     }
-    if (!a.lengths || part != 0) return;
-    // the length ends behind the last slot written
-    if (threadIdx.x == 0) s_last = a.select ? 0 : cnt;
-    __syncthreads();  // also: every thread has read start, which may be the lengths themselves
-    if (a.select) {
-        for (int32_t j = threadIdx.x; j < cnt; j += kThreads)
-            if (a.select[static_cast<int64_t>(b) * a.slots + j] >= 0) atomicMax(&s_last, j + 1);
-        __syncthreads();
+    __syncwarp();
+    if (rows == 0xffffu) {
+#pragma unroll
+        for (int i = 0; i < (kBytes / 16 + 31) / 32; ++i) {
+            const int32_t at = i * 32 + lane;
+            if (at < kBytes / 16) reinterpret_cast<uint4 *>(chunk)[at] = reinterpret_cast<const uint4 *>(st)[at];
+        }
+    } else {
+        // some rows only: 32-bit words, each of one row
+#pragma unroll 4
+        for (int32_t at = lane; at < kBytes / 4; at += 32) {
+            const bool key = at < kv4_value_codes(G) / 4;
+            const int32_t in = key ? at : at - kv4_value_codes(G) / 4;
+            const int32_t row = in < 64 * G ? in / (4 * G) : (in - 64 * G) / G;
+            const int32_t t = key ? ((row & 7) >> 1) | ((row & 1) << 2) | (row & 8) : row;
+            if ((rows >> t) & 1u) reinterpret_cast<uint32_t *>(chunk)[at] = reinterpret_cast<const uint32_t *>(st)[at];
+        }
     }
-    if (threadIdx.x == 0) a.lengths[b] = static_cast<int32_t>(min(start + s_last, a.v.cap));
 }
 
 // The lengths alone, after a write whose blocks all read their starts from them.
 __global__ void __launch_bounds__(32) kv4_lengths_kernel(const AppendArgs a, int32_t *lengths) {
     pdl_launch_dependents();
     pdl_wait();
-    const int32_t b = blockIdx.x, lane = threadIdx.x;
+    const int32_t b = blockIdx.x;
     const int64_t start = lengths[b];
     if (start < 0) return;
-    const int32_t cnt = slots_of(a, b);
-    int32_t last = a.select ? 0 : cnt;
-    if (a.select)
-        for (int32_t j = lane; j < cnt; j += 32)
-            if (a.select[static_cast<int64_t>(b) * a.slots + j] >= 0) last = j + 1;
-    last = __reduce_max_sync(0xffffffffu, last);
-    if (lane == 0) lengths[b] = static_cast<int32_t>(min(start + last, a.v.cap));
+    const int32_t len = length_after(a, b, start, slots_of(a, b));
+    if (threadIdx.x == 0) lengths[b] = len;
 }
 
 struct ReadArgs {
     Kv4View v;
-    int32_t B, rows, blocks, rows_block;
+    Units u;
+    int32_t B, rows;
     const int32_t *start;  // [B] or null: 0
     void *k, *w;           // [B][rows][Hk * D]
     int32_t *status;
 };
 
-template <typename T>
-__device__ __forceinline__ void store8(T *dst, uint32_t codes, uint32_t params) {
+// N codes from the low bits of `codes` to m + s c, one fused product and sum each.
+template <int N>
+__device__ __forceinline__ void values_of(uint32_t codes, uint32_t params, float (&x)[N]) {
     const __half2 sm = *reinterpret_cast<const __half2 *>(&params);
     const float s = __low2float(sm), m = __high2float(sm);
-    float x[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = fmaf(s, static_cast<float>((codes >> (4 * i)) & 15u), m);
-    if constexpr (sizeof(T) == 4) {
-        reinterpret_cast<float4 *>(dst)[0] = make_float4(x[0], x[1], x[2], x[3]);
-        reinterpret_cast<float4 *>(dst)[1] = make_float4(x[4], x[5], x[6], x[7]);
-    } else {
-        uint4 o;
-        uint32_t *ow = reinterpret_cast<uint32_t *>(&o);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const __nv_bfloat162 p = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-            ow[i] = *reinterpret_cast<const uint32_t *>(&p);
-        }
-        *reinterpret_cast<uint4 *>(dst) = o;
-    }
+    for (int i = 0; i < N; ++i)  // 2^23 + c has c in its low bits
+        x[i] = fmaf(s, __uint_as_float(((codes >> (4 * i)) & 15u) | 0x4b000000u) - 8388608.0f, m);
 }
 
-// Block (request, run of rows): a thread takes 8 dims of a key and of a value.
-template <typename T>
+// T float: a lane takes 4 dims (16 bytes out), T bf16: 8.
+template <int G, typename T>
 __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const ReadArgs a) {
+    constexpr int N = 16 / sizeof(T), kPer = 32 * G / N, R = 32 / kPer;  // dims a lane, lanes a row, rows at once
+    constexpr int kBytes = kv4_chunk_bytes(G);
+    __shared__ __align__(16) uint8_t stage[kWarps][kBytes];
     pdl_launch_dependents();
     pdl_wait();
-    const int32_t b = blockIdx.x / a.blocks, part = blockIdx.x - b * a.blocks;
+    const int32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int32_t b, rest;
+    if (!unit_request(a.u, static_cast<int64_t>(blockIdx.x) * kWarps + warp, b, rest)) return;
+    const int32_t ci = rest / a.u.Hk, hk = rest - ci * a.u.Hk;
     const int64_t start = a.start ? a.start[b] : 0, len = kv4_length(a.v, b);
     if (start < 0) {
-        if (part == 0 && threadIdx.x == 0) latch(a.status, kDevBounds);
+        if (rest == 0 && lane == 0) latch(a.status, kDevBounds);
         return;
     }
-    const int32_t G = a.v.G, D = G * kKv4Group, per_row = a.v.Hk * D / 8;
-    const int32_t j0 = part * a.rows_block;
-    const int32_t j1 = static_cast<int32_t>(min(static_cast<int64_t>(min(a.rows, j0 + a.rows_block)), len - start));
-    const int64_t items = static_cast<int64_t>(max(j1 - j0, 0)) * per_row;
-    for (int64_t it = threadIdx.x; it < items; it += kThreads) {
-        const int32_t dj = static_cast<int32_t>(it / per_row), piece = static_cast<int32_t>(it - static_cast<int64_t>(dj) * per_row);
-        const int64_t pos = start + j0 + dj;
-        const int32_t hk = piece / (D / 8), in = piece - hk * (D / 8);
-        const uint8_t *chunk = kv4_chunk(a.v, b, hk, pos);
-        if (!chunk) {
-            latch(a.status, kDevBounds);
-            continue;
+    const int64_t chunk0 = ((start >> 4) + ci) << 4;
+    // rows t0 .. t1 - 1 of the chunk are asked for and there
+    const int32_t t0 = static_cast<int32_t>(max(start - chunk0, int64_t{0}));
+    const int32_t t1 = static_cast<int32_t>(min(min(start + a.rows, len) - chunk0, int64_t{16}));
+    if (t0 >= t1) return;
+    const uint8_t *chunk = kv4_chunk(a.v, b, hk, chunk0);
+    if (!chunk) {
+        if (lane == 0) latch(a.status, kDevBounds);
+        return;
+    }
+    uint8_t *st = stage[warp];
+    {
+        constexpr int kPieces = kBytes / 16, kLoads = (kPieces + 31) / 32;
+        uint4 x[kLoads];
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i)
+            if (i * 32 + lane < kPieces) x[i] = __ldg(reinterpret_cast<const uint4 *>(chunk) + i * 32 + lane);
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i)
+            if (i * 32 + lane < kPieces) reinterpret_cast<uint4 *>(st)[i * 32 + lane] = x[i];
+    }
+    __syncwarp();
+    const int32_t in = lane % kPer, dim = in * N, g = dim >> 5, qd = (dim >> 3) & 3;
+    if (lane / kPer >= R) return;
+    T *k_out = reinterpret_cast<T *>(a.k), *v_out = reinterpret_cast<T *>(a.w);
+    const int64_t row_len = static_cast<int64_t>(a.u.Hk) * G * kKv4Group;
+    const int64_t out0 = (static_cast<int64_t>(b) * a.rows + (chunk0 - start)) * row_len + static_cast<int64_t>(hk) * G * kKv4Group + dim;
+#pragma unroll 4
+    for (int32_t t = lane / kPer; t < 16; t += R) {
+        if (t < t0 || t >= t1) continue;
+        const int32_t ks = kv4_key_slot(t);
+        uint32_t ck = *reinterpret_cast<const uint32_t *>(st + ks * 16 * G + (qd * G + g) * 4);
+        const uint32_t pk = *reinterpret_cast<const uint32_t *>(st + kv4_key_params(G) + ks * 4 * G + 4 * g);
+        const uint8_t *vrow = st + kv4_value_codes(G) + t * 16 * G;
+        const uint32_t pv = *reinterpret_cast<const uint32_t *>(st + kv4_value_params(G) + t * 4 * G + 4 * g);
+        float x[N], y[N];
+        uint32_t cv;
+        if constexpr (N == 4) {
+            ck >>= (dim & 4) * 4;
+            cv = *reinterpret_cast<const uint16_t *>(vrow + kv4_value_word(t, (dim >> 2) & 7, g, G));
+        } else {
+            cv = *reinterpret_cast<const uint16_t *>(vrow + kv4_value_word(t, 2 * qd, g, G)) |
+                 (static_cast<uint32_t>(*reinterpret_cast<const uint16_t *>(vrow + kv4_value_word(t, 2 * qd + 1, g, G))) << 16);
         }
-        const int32_t t = static_cast<int32_t>(pos & 15), ks = kv4_key_slot(t), g = in >> 2, qd = in & 3;
-        const uint32_t ck = *reinterpret_cast<const uint32_t *>(chunk + ks * 16 * G + (qd * G + g) * 4);
-        const uint32_t pk = *reinterpret_cast<const uint32_t *>(chunk + kv4_key_params(G) + ks * 4 * G + 4 * g);
-        const uint8_t *vrow = chunk + kv4_value_codes(G) + t * 16 * G;
-        const uint32_t cv = *reinterpret_cast<const uint16_t *>(vrow + kv4_value_word(t, 2 * qd, g, G)) |
-                            (static_cast<uint32_t>(*reinterpret_cast<const uint16_t *>(vrow + kv4_value_word(t, 2 * qd + 1, g, G))) << 16);
-        const uint32_t pv = *reinterpret_cast<const uint32_t *>(chunk + kv4_value_params(G) + t * 4 * G + 4 * g);
-        const int64_t off = ((static_cast<int64_t>(b) * a.rows + j0 + dj) * a.v.Hk * D) + static_cast<int64_t>(piece) * 8;
-        store8(reinterpret_cast<T *>(a.k) + off, ck, pk);
-        store8(reinterpret_cast<T *>(a.w) + off, cv, pv);
+        values_of(ck, pk, x);
+        values_of(cv, pv, y);
+        const int64_t out = out0 + t * row_len;
+        if constexpr (N == 4) {
+            *reinterpret_cast<float4 *>(k_out + out) = make_float4(x[0], x[1], x[2], x[3]);
+            *reinterpret_cast<float4 *>(v_out + out) = make_float4(y[0], y[1], y[2], y[3]);
+        } else {
+            uint4 ko, vo;
+            uint32_t *kw = reinterpret_cast<uint32_t *>(&ko), *vw = reinterpret_cast<uint32_t *>(&vo);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const __nv_bfloat162 p = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]), q = __floats2bfloat162_rn(y[2 * i], y[2 * i + 1]);
+                kw[i] = *reinterpret_cast<const uint32_t *>(&p);
+                vw[i] = *reinterpret_cast<const uint32_t *>(&q);
+            }
+            *reinterpret_cast<uint4 *>(k_out + out) = ko;
+            *reinterpret_cast<uint4 *>(v_out + out) = vo;
+        }
     }
 }
 
-// Blocks a request's rows are cut into: about 8 passes of a block's threads each, fewer blocks
-// than the grid can hold.
-int32_t rows_a_block(int64_t rows, int64_t per_row, int32_t batch) {
-    int64_t r = (8 * kThreads + per_row - 1) / per_row;
-    const int64_t most = (int64_t{1} << 30) / batch;  // blocks a request
-    r = r < 1 ? 1 : r;
-    if ((rows + r - 1) / r > most) r = (rows + most - 1) / most;
-    return static_cast<int32_t>(r < rows ? r : rows);
+// A request's `rows` rows touch at most rows / 16 + 2 chunks (one more than they fill), of each kv head.
+Units units_of(int32_t batch, int32_t Hk, int64_t rows) {
+    Units u;
+    u.Hk = Hk;
+    u.per_request = static_cast<int32_t>(Hk * ((rows + 30) / 16));
+    u.total = static_cast<int64_t>(batch) * u.per_request;
+    return u;
+}
+bool launchable(const Units &u, int64_t rows) {
+    return static_cast<int64_t>(u.Hk) * ((rows + 30) / 16) <= INT32_MAX && (u.total + kWarps - 1) / kWarps <= INT32_MAX;
+}
+dim3 grid_of(const Units &u) { return dim3(static_cast<unsigned>((u.total + kWarps - 1) / kWarps)); }
+
+using AppendKernel = void (*)(const AppendArgs);
+AppendKernel append_kernel(int32_t G) {
+    switch (G) {
+        case 1: return kv4_append_kernel<1>;
+        case 2: return kv4_append_kernel<2>;
+        case 3: return kv4_append_kernel<3>;
+        default: return kv4_append_kernel<4>;
+    }
+}
+using ReadKernel = void (*)(const ReadArgs);
+template <typename T>
+ReadKernel read_kernel(int32_t G) {
+    switch (G) {
+        case 1: return kv4_read_kernel<1, T>;
+        case 2: return kv4_read_kernel<2, T>;
+        case 3: return kv4_read_kernel<3, T>;
+        default: return kv4_read_kernel<4, T>;
+    }
 }
 
 bool misaligned(const void *p, uintptr_t by) { return (reinterpret_cast<uintptr_t>(p) & (by - 1)) != 0; }
@@ -287,14 +397,13 @@ eagle_status eagle_kv4_append(const eagle_kv4_cache *cache, int32_t batch, int32
     a.count = d_count;
     a.start = d_start ? d_start : cache->lengths;
     a.status = d_status;
-    a.slots_block = slots > 0 ? rows_a_block(slots, row / 8, batch) : 1;
-    a.blocks = slots > 0 ? (slots + a.slots_block - 1) / a.slots_block : 1;
-    // one block a request, or starts of their own: the lengths are written in the same launch
-    const bool own_lengths = a.blocks == 1 || a.start != cache->lengths;
+    a.u = units_of(batch, a.v.Hk, slots > 0 ? slots : 1);
+    if (!launchable(a.u, slots)) return EAGLE_ERR_UNSUPPORTED;
+    // starts of their own: the lengths are written in the same launch
+    const bool own_lengths = a.start != cache->lengths;
     a.lengths = own_lengths ? cache->lengths : nullptr;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (launch_pdl(kv4_append_kernel, dim3(static_cast<unsigned>(batch) * a.blocks), dim3(kThreads), 0, st, a) != cudaSuccess)
-        return EAGLE_ERR_CUDA;
+    if (launch_pdl(append_kernel(a.v.G), grid_of(a.u), dim3(kThreads), 0, st, a) != cudaSuccess) return EAGLE_ERR_CUDA;
     if (!own_lengths &&
         launch_pdl(kv4_lengths_kernel, dim3(batch), dim3(32), 0, st, a, cache->lengths) != cudaSuccess)
         return EAGLE_ERR_CUDA;
@@ -317,13 +426,11 @@ eagle_status eagle_kv4_read(const eagle_kv4_cache *cache, int32_t batch, int32_t
     a.k = d_k;
     a.w = d_v;
     a.status = d_status;
-    a.rows_block = rows_a_block(rows, static_cast<int64_t>(a.v.Hk) * a.v.G * 4, batch);
-    a.blocks = (rows + a.rows_block - 1) / a.rows_block;
-    const dim3 grid(static_cast<unsigned>(batch) * a.blocks), block(kThreads);
+    a.u = units_of(batch, a.v.Hk, rows);
+    if (!launchable(a.u, rows)) return EAGLE_ERR_UNSUPPORTED;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    const cudaError_t e = dtype == EAGLE_F32 ? launch_pdl(kv4_read_kernel<float>, grid, block, 0, st, a)
-                                             : launch_pdl(kv4_read_kernel<__nv_bfloat16>, grid, block, 0, st, a);
-    return e == cudaSuccess ? EAGLE_OK : EAGLE_ERR_CUDA;
+    const ReadKernel kernel = dtype == EAGLE_F32 ? read_kernel<float>(a.v.G) : read_kernel<__nv_bfloat16>(a.v.G);
+    return launch_pdl(kernel, grid_of(a.u), dim3(kThreads), 0, st, a) == cudaSuccess ? EAGLE_OK : EAGLE_ERR_CUDA;
 }
 
 }  // extern "C"
