@@ -650,42 +650,65 @@ __global__ void __launch_bounds__(kThreads, Shape<G, NQ>::kBlocks) kv4_attention
     } while (w.next(k, p));
 }
 
-// Units that several CTAs worked on: block c merges the unit that CTA c is the second to work on.
-// o = sum_i w_i O_i / sum_i w_i l_i, w_i = 2^(m_i - max m), over CTAs first..last in order.
-__global__ void __launch_bounds__(128) kv4_merge_kernel(const __grid_constant__ Kv4Args k) {
+// Units that several CTAs worked on: block (c, .) merges the unit that CTA c is the second to work on.
+// o = sum_i w_i O_i / sum_i w_i l_i, w_i = 2^(m_i - max m), over its CTAs in order.  A warp a row: a lane
+// a part for the weights, then four dims a lane over all parts.
+constexpr int kMergeRows = 4;
+__global__ void __launch_bounds__(kMergeRows * 32) kv4_merge_kernel(const __grid_constant__ Kv4Args k) {
     pdl_launch_dependents();
     pdl_wait();
-    // CTA c continues a unit that CTA c - 1 began, and that goes on to CTA `last`
+    const int32_t lane = threadIdx.x & 31, grid = gridDim.x;
+    // CTA c continues a unit that CTA c - 1 began, and that goes on while the kind is 2
     const Kv4Share sh = k.share[blockIdx.x];
-    if (sh.kind == 0 || k.share[blockIdx.x - 1].kind == 2) return;
+    const int32_t before = blockIdx.x > 0 ? k.share[blockIdx.x - 1].kind : 2;
+    if (sh.kind == 0 || before == 2) return;
     const int32_t first = blockIdx.x - 1;
     int32_t last = blockIdx.x;
-    while (last + 1 < static_cast<int32_t>(gridDim.x) && k.share[last].kind == 2) ++last;
-    const int32_t D = k.a.cache.G * kKv4Group, quads = D / 4;
-    const int32_t rows = min(k.rows, k.Mq - sh.qt * k.rows);
-    for (int32_t it = threadIdx.x + blockIdx.y * 128; it < rows * quads; it += 128 * gridDim.y) {
-        const int32_t r = it / quads, c4 = it - r * quads;
-        auto slot = [&](int32_t c) { return 2 * static_cast<int64_t>(c) + (c == first ? 1 : 0); };
-        float M = -INFINITY;
-        for (int32_t c = first; c <= last; ++c) M = fmaxf(M, k.part_ml[slot(c) * k.rows + r].x);
-        float L = 0.0f;
+    for (bool more = true; more;) {
+        const int32_t c = last + lane;
+        const uint32_t ends = __ballot_sync(kFull, c >= grid - 1 || k.share[min(c, grid - 1)].kind != 2);
+        more = ends == 0;
+        last += more ? 32 : __ffs(ends) - 1;
+    }
+    const int32_t parts = last - first + 1;
+    const int32_t D = k.a.cache.G * kKv4Group, rows = min(k.rows, k.Mq - sh.qt * k.rows);
+    // part i is slot 0 of CTA first + i, but slot 1 of the first
+    auto slot = [&](int32_t i) { return 2 * static_cast<int64_t>(first + i) + (i == 0 ? 1 : 0); };
+    for (int32_t r = blockIdx.y * kMergeRows + (threadIdx.x >> 5); r < rows; r += kMergeRows * gridDim.y) {
+        float M = -INFINITY, L = 0.0f;
+        for (int32_t i = lane; i < parts; i += 32) M = fmaxf(M, k.part_ml[slot(i) * k.rows + r].x);
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, off));
         float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-        for (int32_t c = first; c <= last; ++c) {
-            const float2 ml = k.part_ml[slot(c) * k.rows + r];
-            const float4 x = *reinterpret_cast<const float4 *>(k.part_o + (slot(c) * k.rows + r) * D + 4 * c4);
-            const float wt = ml.x == -INFINITY ? (ml.y == 0.0f ? 0.0f : ml.y) : ex2_approx(ml.x - M);
-            if (wt == 0.0f) continue;
-            L += wt * ml.y;
-            v.x = fmaf(wt, x.x, v.x);
-            v.y = fmaf(wt, x.y, v.y);
-            v.z = fmaf(wt, x.z, v.z);
-            v.w = fmaf(wt, x.w, v.w);
+        for (int32_t i0 = 0; i0 < parts; i0 += 32) {
+            float wt = 0.0f;
+            if (i0 + lane < parts) {
+                const float2 ml = k.part_ml[slot(i0 + lane) * k.rows + r];
+                // a part whose scores are all NaN has no maximum and a sum of NaN
+                wt = ml.x == -INFINITY ? (ml.y == 0.0f ? 0.0f : ml.y) : ex2_approx(ml.x - M);
+                if (wt != 0.0f) L += wt * ml.y;
+            }
+            const int32_t n = min(parts - i0, 32);
+#pragma unroll 8
+            for (int32_t i = 0; i < n; ++i) {
+                const float x = __shfl_sync(kFull, wt, i);
+                float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (4 * lane < D) o = *reinterpret_cast<const float4 *>(k.part_o + (slot(i0 + i) * k.rows + r) * D + 4 * lane);
+                if (x != 0.0f) {
+                    v.x = fmaf(x, o.x, v.x);
+                    v.y = fmaf(x, o.y, v.y);
+                    v.z = fmaf(x, o.z, v.z);
+                    v.w = fmaf(x, o.w, v.w);
+                }
+            }
         }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(kFull, L, off);
         const float inv = L == 0.0f ? 0.0f : 1.0f / L;
         const int32_t row = sh.qt * k.rows + r, node = row / k.group, head = sh.hk * k.group + row - node * k.group;
-        *reinterpret_cast<uint2 *>(k.a.o + ((static_cast<int64_t>(sh.b) * k.a.n + node) * k.a.H + head) * D + 4 * c4) =
-            make_uint2(pack_b16(v.x * inv, v.y * inv), pack_b16(v.z * inv, v.w * inv));
+        if (4 * lane < D)
+            *reinterpret_cast<uint2 *>(k.a.o + ((static_cast<int64_t>(sh.b) * k.a.n + node) * k.a.H + head) * D + 4 * lane) =
+                make_uint2(pack_b16(v.x * inv, v.y * inv), pack_b16(v.z * inv, v.w * inv));
     }
 }
 
@@ -797,7 +820,7 @@ cudaError_t launch_kv4_attention(const Kv4Attention &a, cudaStream_t st) {
     const cudaError_t e = v.kernel ? launch_pdl(v.kernel, dim3(grid), dim3(v.threads), v.smem, st, k)
                                    : launch_kv4_attention_tc(k, static_cast<int32_t>(grid), st);
     if (e != cudaSuccess || grid == 1) return e;
-    return launch_pdl(kv4_merge_kernel, dim3(grid, v.rows / 8), dim3(128), 0, st, k);
+    return launch_pdl(kv4_merge_kernel, dim3(grid, std::min(k.rows / kMergeRows, 16)), dim3(kMergeRows * 32), 0, st, k);
 }
 
 }  // namespace eagle

@@ -3,6 +3,8 @@
 // The engine's decoder layer hands out the keys and values of a tree's nodes; after the verify the
 // accepted path's rows join the cache, in 4 bits, at the request's next positions (a prompt's rows
 // in order, a path's rows through the list of its nodes).  kv4.cuh has the format.
+#include <type_traits>
+
 #include "kernels.cuh"
 #include "kv4.cuh"
 
@@ -36,13 +38,13 @@ constexpr uint32_t kFull = 0xffffffffu;
 // memory: at 26 k tokens of 8 kv heads of 128 the write moves 141 MB and the read as much.
 struct Units {
     int32_t Hk, per_request;  // per_request: kv heads x chunks that a request may touch
-    int64_t total;            // warps of work
+    int32_t total;            // warps of work
 };
-// Warp `id` of the launch; `start` is the request's first position.
-__device__ __forceinline__ bool unit_request(const Units &u, int64_t id, int32_t &b, int32_t &rest) {
+// The request of warp `id` of the launch, and which of the request's warps it is.
+__device__ __forceinline__ bool unit_request(const Units &u, int32_t id, int32_t &b, int32_t &rest) {
     if (id >= u.total) return false;
-    b = static_cast<int32_t>(id / u.per_request);
-    rest = static_cast<int32_t>(id - static_cast<int64_t>(b) * u.per_request);
+    b = id / u.per_request;
+    rest = id - b * u.per_request;
     return true;
 }
 
@@ -74,46 +76,47 @@ __device__ __forceinline__ int32_t length_after(const AppendArgs &a, int32_t b, 
     return static_cast<int32_t>(min(start + last, a.v.cap));
 }
 
+__device__ __forceinline__ __nv_bfloat162 as_b2(uint32_t x) { return *reinterpret_cast<const __nv_bfloat162 *>(&x); }
+__device__ __forceinline__ uint32_t b2_bits(__nv_bfloat162 x) { return *reinterpret_cast<const uint32_t *>(&x); }
+
 // Eight values of a group of 32 that four neighbouring lanes hold: their codes (the first in the
-// low bits) and the group's (s, m).  A code is a s^-1 rounded to the nearest whole number by a sum
-// with 1.5 2^23 (whose low bits it then is); with r a rounded reciprocal that can miss the nearest by
-// one next to a half, so the remainder a - c s, which is exact, is held against s / 2: beyond it, or at
-// it with c odd, the neighbour on its side is the one.
+// low bits) and the group's (s, m).  A code is (x - m) / s rounded to the nearest whole number, ties to
+// even.  The quotient is a product with a reciprocal that is a few units too large, rounded by a sum
+// with 1.5 2^23 (whose low bits it then is): never too small, and too large by one only for ties and
+// just below them.  The remainder a - c s, which is exact, tells: below -s / 2 the code is one too
+// large, at -s / 2 it is a tie, of which the even neighbour is the one.
 __device__ __forceinline__ uint32_t quantise8(const uint4 raw, uint32_t *params) {
-    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-    float x[8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(w[i] << 16);
-        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-    // NaN passes minima and maxima by, so the magnitudes are checked as whole numbers
-    uint32_t big = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) big = max(big, max((w[i] << 16) & 0x7fff0000u, w[i] & 0x7fff0000u));
-    float lo = fminf(fminf(fminf(x[0], x[1]), fminf(x[2], x[3])), fminf(fminf(x[4], x[5]), fminf(x[6], x[7])));
-    float hi = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+    // both halves of a word at once; NaN passes on
+    __nv_bfloat162 hi2 = __hmax2_nan(__hmax2_nan(as_b2(raw.x), as_b2(raw.y)), __hmax2_nan(as_b2(raw.z), as_b2(raw.w)));
+    __nv_bfloat162 lo2 = __hmin2_nan(__hmin2_nan(as_b2(raw.x), as_b2(raw.y)), __hmin2_nan(as_b2(raw.z), as_b2(raw.w)));
 #pragma unroll
     for (int off = 1; off < 4; off <<= 1) {
-        lo = fminf(lo, __shfl_xor_sync(kFull, lo, off));
-        hi = fmaxf(hi, __shfl_xor_sync(kFull, hi, off));
-        big = max(big, __shfl_xor_sync(kFull, big, off));
+        hi2 = __hmax2_nan(hi2, as_b2(__shfl_xor_sync(kFull, b2_bits(hi2), off)));
+        lo2 = __hmin2_nan(lo2, as_b2(__shfl_xor_sync(kFull, b2_bits(lo2), off)));
     }
+    const float h0 = __low2float(hi2), h1 = __high2float(hi2), l0 = __low2float(lo2), l1 = __high2float(lo2);
+    const float hi = fmaxf(h0, h1), lo = fminf(l0, l1);
+    const bool ok = fabsf(h0) <= kKv4MaxAbs && fabsf(h1) <= kKv4MaxAbs && fabsf(l0) <= kKv4MaxAbs && fabsf(l1) <= kKv4MaxAbs;
     const __half m = __float2half_rd(lo);
     const float mf = __half2float(m);
     const __half s = __float2half_ru(__fdiv_rn(hi - mf, 15.0f));
-    const float sf = __half2float(s), half = 0.5f * sf, r = sf > 0.0f ? __frcp_rn(sf) : 0.0f;
+    const float sf = __half2float(s), below = -0.5f * sf;
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(sf));  // within 2^-23: 3 units more are above 1 / s
+    r = sf > 0.0f ? __int_as_float(__float_as_int(r) + 3) : 0.0f;
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
     uint32_t codes = 0;
-    constexpr float kMagic = 12582912.0f;
+    constexpr float kMagic = 12582912.0f;  // bits 0x4b400000: the code adds to them
 #pragma unroll
     for (int i = 7; i >= 0; --i) {
-        const float a = x[i] - mf, t = fmaf(a, r, kMagic), rem = fmaf(kMagic - t, sf, a);
-        int32_t c = __float_as_int(t);
-        const bool next = __float_as_int(fabsf(rem)) + (c & 1) > __float_as_int(half);
-        c += next ? (rem < 0.0f ? -1 : 1) : 0;
-        codes = codes * 16u + (static_cast<uint32_t>(c) & 15u);
+        const float x = i & 1 ? __uint_as_float(w[i >> 1] & 0xffff0000u) : __uint_as_float(w[i >> 1] << 16);
+        const float a = x - mf, t = fmaf(a, r, kMagic), rem = fmaf(kMagic - t, sf, a);
+        uint32_t c = __float_as_uint(t);
+        if (rem <= below && ((c & 1u) || rem < below)) --c;
+        codes = codes * 16u + c;
     }
-    const bool ok = big <= __float_as_uint(kKv4MaxAbs);
+    // 0x4b400000 (1 + 16 + 256 + ...) without what leaves the word
+    codes -= 0x4b400000u + 0xb4000000u + 0x40000000u;
     *params = ok ? static_cast<uint32_t>(__half_as_ushort(s)) | (static_cast<uint32_t>(__half_as_ushort(m)) << 16) : 0x7fff7fffu;
     return ok ? codes : 0u;
 }
@@ -127,7 +130,7 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const AppendArgs a
     pdl_wait();
     const int32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int32_t b, rest;
-    if (!unit_request(a.u, static_cast<int64_t>(blockIdx.x) * kWarps + warp, b, rest)) return;
+    if (!unit_request(a.u, static_cast<int32_t>(blockIdx.x) * kWarps + warp, b, rest)) return;
     const int32_t ci = rest / a.u.Hk, hk = rest - ci * a.u.Hk;
     const int64_t start = a.start[b];
     const int32_t cnt = slots_of(a, b);
@@ -154,57 +157,70 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const AppendArgs a
     }
     const uint32_t rows = __ballot_sync(kFull, src >= 0);
     if (rows == 0) return;
+    const int32_t piece = lane % kPer, g = piece >> 2, qd = piece & 3;
+    const bool idle = lane / kPer >= R;  // head_dim 96: 24 lanes work
+    // two steps of rows at a time, the next two on their way: few instructions, so that a small write
+    // does not wait for its code
+    auto load = [&](int32_t i, uint4 &kx, uint4 &vx) {
+        const int32_t t = i * R + lane / kPer, from = __shfl_sync(kFull, src, t & 15);
+        kx = vx = make_uint4(0, 0, 0, 0);
+        if (i < kIters && from >= 0 && !idle) {
+            const int64_t off = (static_cast<int64_t>(b) * a.src_rows + from) * a.ld + (static_cast<int64_t>(hk) * kPer + piece) * 8;
+            kx = __ldg(reinterpret_cast<const uint4 *>(a.k + off));
+            vx = __ldg(reinterpret_cast<const uint4 *>(a.w + off));
+        }
+    };
+    constexpr int kStep = kIters < 2 ? 1 : 2;
+    uint4 kx[kStep], vx[kStep];
+#pragma unroll
+    for (int u = 0; u < kStep; ++u) load(u, kx[u], vx[u]);
     uint8_t *chunk = kv4_chunk(a.v, b, hk, chunk0);
     if (!chunk) {
         if (lane == 0) latch(a.status, kDevBounds);
         return;
     }
-    const int32_t piece = lane % kPer, g = piece >> 2, qd = piece & 3;
-    const bool idle = lane / kPer >= R;  // head_dim 96: 24 lanes work
-    uint4 kx[kIters], vx[kIters];
-#pragma unroll
-    for (int i = 0; i < kIters; ++i) {
-        const int32_t t = i * R + lane / kPer, from = __shfl_sync(kFull, src, t & 15);
-        kx[i] = vx[i] = make_uint4(0, 0, 0, 0);
-        if (from >= 0 && !idle) {
-            const int64_t off = (static_cast<int64_t>(b) * a.src_rows + from) * a.ld + (static_cast<int64_t>(hk) * kPer + piece) * 8;
-            kx[i] = __ldg(reinterpret_cast<const uint4 *>(a.k + off));
-            vx[i] = __ldg(reinterpret_cast<const uint4 *>(a.w + off));
-        }
-    }
     uint8_t *st = stage[warp];
+#pragma unroll 1
+    for (int32_t i0 = 0; i0 < kIters; i0 += kStep) {
+        uint4 kn[kStep], vn[kStep];
 #pragma unroll
-    for (int i = 0; i < kIters; ++i) {
-        const int32_t t = i * R + lane / kPer;
-        if (((rows >> (i * R)) & ((1u << R) - 1u)) == 0) continue;  // warp-uniform
-        const int32_t ks = kv4_key_slot(t & 15);
-        uint32_t pk, pv;
-        const uint32_t ck = quantise8(kx[i], &pk), cv = quantise8(vx[i], &pv);
-        if (idle) continue;
-        *reinterpret_cast<uint32_t *>(st + ks * 16 * G + (qd * G + g) * 4) = ck;
-        uint8_t *vrow = st + kv4_value_codes(G) + t * 16 * G;
-        *reinterpret_cast<uint16_t *>(vrow + kv4_value_word(t, 2 * qd, g, G)) = static_cast<uint16_t>(cv);
-        *reinterpret_cast<uint16_t *>(vrow + kv4_value_word(t, 2 * qd + 1, g, G)) = static_cast<uint16_t>(cv >> 16);
-        if (qd == 0) *reinterpret_cast<uint32_t *>(st + kv4_key_params(G) + ks * 4 * G + 4 * g) = pk;
-        if (qd == 1) *reinterpret_cast<uint32_t *>(st + kv4_value_params(G) + t * 4 * G + 4 * g) = pv;
+        for (int u = 0; u < kStep; ++u) load(i0 + kStep + u, kn[u], vn[u]);
+        if (((rows >> (i0 * R)) & ((1u << (R * kStep)) - 1u)) != 0) {  // warp-uniform
+#pragma unroll
+            for (int u = 0; u < kStep; ++u) {
+                const int32_t t = ((i0 + u) * R + lane / kPer) & 15, ks = kv4_key_slot(t);
+                uint32_t pk, pv;
+                const uint32_t ck = quantise8(kx[u], &pk), cv = quantise8(vx[u], &pv);
+                if (!idle) {
+                    *reinterpret_cast<uint32_t *>(st + ks * 16 * G + (qd * G + g) * 4) = ck;
+                    uint8_t *vrow = st + kv4_value_codes(G) + t * 16 * G;
+                    *reinterpret_cast<uint16_t *>(vrow + kv4_value_word(t, 2 * qd, g, G)) = static_cast<uint16_t>(cv);
+                    *reinterpret_cast<uint16_t *>(vrow + kv4_value_word(t, 2 * qd + 1, g, G)) = static_cast<uint16_t>(cv >> 16);
+                    if (qd == 0) *reinterpret_cast<uint32_t *>(st + kv4_key_params(G) + ks * 4 * G + 4 * g) = pk;
+                    if (qd == 1) *reinterpret_cast<uint32_t *>(st + kv4_value_params(G) + t * 4 * G + 4 * g) = pv;
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kStep; ++u) {
+            kx[u] = kn[u];
+            vx[u] = vn[u];
+        }
     }
     __syncwarp();
-    if (rows == 0xffffu) {
+    // out in the widest words that hold one row's bytes each: a row has 16 G bytes of codes and 4 G of
+    // parameters
+    using Word = std::conditional_t<G == 4, uint4, std::conditional_t<G == 2, uint2, uint32_t>>;
+    constexpr int kWord = sizeof(Word), kCodeWords = 16 * G / kWord, kParWords = 4 * G / kWord, kPart = 320 * G / kWord;
 #pragma unroll
-        for (int i = 0; i < (kBytes / 16 + 31) / 32; ++i) {
-            const int32_t at = i * 32 + lane;
-            if (at < kBytes / 16) reinterpret_cast<uint4 *>(chunk)[at] = reinterpret_cast<const uint4 *>(st)[at];
-        }
-    } else {
-        // some rows only: 32-bit words, each of one row
-#pragma unroll 4
-        for (int32_t at = lane; at < kBytes / 4; at += 32) {
-            const bool key = at < kv4_value_codes(G) / 4;
-            const int32_t in = key ? at : at - kv4_value_codes(G) / 4;
-            const int32_t row = in < 64 * G ? in / (4 * G) : (in - 64 * G) / G;
-            const int32_t t = key ? ((row & 7) >> 1) | ((row & 1) << 2) | (row & 8) : row;
-            if ((rows >> t) & 1u) reinterpret_cast<uint32_t *>(chunk)[at] = reinterpret_cast<const uint32_t *>(st)[at];
-        }
+    for (int i = 0; i < (kBytes / kWord + 31) / 32; ++i) {
+        const int32_t at = i * 32 + lane;
+        if (at >= kBytes / kWord) break;
+        const bool key = at < kPart;
+        const int32_t in = key ? at : at - kPart;
+        const int32_t row = in < 16 * kCodeWords ? in / kCodeWords : (in - 16 * kCodeWords) / kParWords;
+        const int32_t t = key ? ((row & 7) >> 1) | ((row & 1) << 2) | (row & 8) : row;
+        if ((rows >> t) & 1u) reinterpret_cast<Word *>(chunk)[at] = reinterpret_cast<const Word *>(st)[at];
     }
 }
 
@@ -248,7 +264,7 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const ReadArgs a) {
     pdl_wait();
     const int32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int32_t b, rest;
-    if (!unit_request(a.u, static_cast<int64_t>(blockIdx.x) * kWarps + warp, b, rest)) return;
+    if (!unit_request(a.u, static_cast<int32_t>(blockIdx.x) * kWarps + warp, b, rest)) return;
     const int32_t ci = rest / a.u.Hk, hk = rest - ci * a.u.Hk;
     const int64_t start = a.start ? a.start[b] : 0, len = kv4_length(a.v, b);
     if (start < 0) {
@@ -320,16 +336,13 @@ __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const ReadArgs a) {
     }
 }
 
-// A request's `rows` rows touch at most rows / 16 + 2 chunks (one more than they fill), of each kv head.
-Units units_of(int32_t batch, int32_t Hk, int64_t rows) {
-    Units u;
-    u.Hk = Hk;
-    u.per_request = static_cast<int32_t>(Hk * ((rows + 30) / 16));
-    u.total = static_cast<int64_t>(batch) * u.per_request;
-    return u;
-}
-bool launchable(const Units &u, int64_t rows) {
-    return static_cast<int64_t>(u.Hk) * ((rows + 30) / 16) <= INT32_MAX && (u.total + kWarps - 1) / kWarps <= INT32_MAX;
+// A request's `rows` rows touch at most (rows + 30) / 16 chunks of each kv head.  False: more warps than
+// 32 bits count (over a terabyte of cache).
+bool units_of(int32_t batch, int32_t Hk, int64_t rows, Units *u) {
+    const int64_t per = Hk * ((rows + 30) / 16);
+    if (per * batch > INT32_MAX - kWarps) return false;
+    *u = Units{Hk, static_cast<int32_t>(per), static_cast<int32_t>(per * batch)};
+    return true;
 }
 dim3 grid_of(const Units &u) { return dim3(static_cast<unsigned>((u.total + kWarps - 1) / kWarps)); }
 
@@ -397,8 +410,7 @@ eagle_status eagle_kv4_append(const eagle_kv4_cache *cache, int32_t batch, int32
     a.count = d_count;
     a.start = d_start ? d_start : cache->lengths;
     a.status = d_status;
-    a.u = units_of(batch, a.v.Hk, slots > 0 ? slots : 1);
-    if (!launchable(a.u, slots)) return EAGLE_ERR_UNSUPPORTED;
+    if (!units_of(batch, a.v.Hk, slots > 0 ? slots : 1, &a.u)) return EAGLE_ERR_UNSUPPORTED;
     // starts of their own: the lengths are written in the same launch
     const bool own_lengths = a.start != cache->lengths;
     a.lengths = own_lengths ? cache->lengths : nullptr;
@@ -426,8 +438,7 @@ eagle_status eagle_kv4_read(const eagle_kv4_cache *cache, int32_t batch, int32_t
     a.k = d_k;
     a.w = d_v;
     a.status = d_status;
-    a.u = units_of(batch, a.v.Hk, rows);
-    if (!launchable(a.u, rows)) return EAGLE_ERR_UNSUPPORTED;
+    if (!units_of(batch, a.v.Hk, rows, &a.u)) return EAGLE_ERR_UNSUPPORTED;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const ReadKernel kernel = dtype == EAGLE_F32 ? read_kernel<float>(a.v.G) : read_kernel<__nv_bfloat16>(a.v.G);
     return launch_pdl(kernel, grid_of(a.u), dim3(kThreads), 0, st, a) == cudaSuccess ? EAGLE_OK : EAGLE_ERR_CUDA;
