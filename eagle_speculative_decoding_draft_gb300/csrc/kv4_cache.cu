@@ -77,22 +77,20 @@ __device__ __forceinline__ int32_t length_after(const AppendArgs &a, int32_t b, 
 }
 
 __device__ __forceinline__ __nv_bfloat162 as_b2(uint32_t x) { return *reinterpret_cast<const __nv_bfloat162 *>(&x); }
-__device__ __forceinline__ uint32_t b2_bits(__nv_bfloat162 x) { return *reinterpret_cast<const uint32_t *>(&x); }
 
-// Eight values of a group of 32 that four neighbouring lanes hold: their codes (the first in the
-// low bits) and the group's (s, m).  A code is (x - m) / s rounded to the nearest whole number, ties to
-// even.  The quotient is a product with a reciprocal that is a few units too large, rounded by a sum
-// with 1.5 2^23 (whose low bits it then is): never too small, and too large by one only for ties and
-// just below them.  The remainder a - c s, which is exact, tells: below -s / 2 the code is one too
-// large, at -s / 2 it is a tie, of which the even neighbour is the one.
-__device__ __forceinline__ uint32_t quantise8(const uint4 raw, uint32_t *params) {
+// A group of 32 values: four words of eight codes (the first in the low bits) and (s, m).  A code is
+// (x - m) / s rounded to the nearest whole number, ties to even.  The quotient is a product with a
+// reciprocal that is a few units too large, rounded by a sum with 1.5 2^23 (whose low bits it then is):
+// never too small, and too large by one only for ties and just below them.  The remainder a - c s, which
+// is exact, tells: below -s / 2 the code is one too large, at -s / 2 it is a tie, of which the even
+// neighbour is the one.
+__device__ __forceinline__ uint32_t quantise(const uint32_t (&w)[16], uint32_t (&codes)[4]) {
     // both halves of a word at once; NaN passes on
-    __nv_bfloat162 hi2 = __hmax2_nan(__hmax2_nan(as_b2(raw.x), as_b2(raw.y)), __hmax2_nan(as_b2(raw.z), as_b2(raw.w)));
-    __nv_bfloat162 lo2 = __hmin2_nan(__hmin2_nan(as_b2(raw.x), as_b2(raw.y)), __hmin2_nan(as_b2(raw.z), as_b2(raw.w)));
+    __nv_bfloat162 hi2 = as_b2(w[0]), lo2 = hi2;
 #pragma unroll
-    for (int off = 1; off < 4; off <<= 1) {
-        hi2 = __hmax2_nan(hi2, as_b2(__shfl_xor_sync(kFull, b2_bits(hi2), off)));
-        lo2 = __hmin2_nan(lo2, as_b2(__shfl_xor_sync(kFull, b2_bits(lo2), off)));
+    for (int i = 1; i < 16; ++i) {
+        hi2 = __hmax2_nan(hi2, as_b2(w[i]));
+        lo2 = __hmin2_nan(lo2, as_b2(w[i]));
     }
     const float h0 = __low2float(hi2), h1 = __high2float(hi2), l0 = __low2float(lo2), l1 = __high2float(lo2);
     const float hi = fmaxf(h0, h1), lo = fminf(l0, l1);
@@ -104,28 +102,33 @@ __device__ __forceinline__ uint32_t quantise8(const uint4 raw, uint32_t *params)
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(sf));  // within 2^-23: 3 units more are above 1 / s
     r = sf > 0.0f ? __int_as_float(__float_as_int(r) + 3) : 0.0f;
-    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-    uint32_t codes = 0;
     constexpr float kMagic = 12582912.0f;  // bits 0x4b400000: the code adds to them
 #pragma unroll
-    for (int i = 7; i >= 0; --i) {
-        const float x = i & 1 ? __uint_as_float(w[i >> 1] & 0xffff0000u) : __uint_as_float(w[i >> 1] << 16);
-        const float a = x - mf, t = fmaf(a, r, kMagic), rem = fmaf(kMagic - t, sf, a);
-        uint32_t c = __float_as_uint(t);
-        if (rem <= below && ((c & 1u) || rem < below)) --c;
-        codes = codes * 16u + c;
+    for (int k = 0; k < 4; ++k) {
+        uint32_t c8 = 0;
+#pragma unroll
+        for (int i = 7; i >= 0; --i) {
+            const uint32_t p = w[4 * k + (i >> 1)];
+            const float a = __uint_as_float(i & 1 ? p & 0xffff0000u : p << 16) - mf;
+            const float t = fmaf(a, r, kMagic), rem = fmaf(kMagic - t, sf, a);
+            uint32_t c = __float_as_uint(t);
+            if (rem <= below && ((c & 1u) || rem < below)) --c;
+            c8 = c8 * 16u + c;
+        }
+        // without 0x4b400000 (1 + 16 + 256 + ...), of which three terms stay in the word
+        codes[k] = ok ? c8 - (0x4b400000u + 0xb4000000u + 0x40000000u) : 0u;
     }
-    // 0x4b400000 (1 + 16 + 256 + ...) without what leaves the word
-    codes -= 0x4b400000u + 0xb4000000u + 0x40000000u;
-    *params = ok ? static_cast<uint32_t>(__half_as_ushort(s)) | (static_cast<uint32_t>(__half_as_ushort(m)) << 16) : 0x7fff7fffu;
-    return ok ? codes : 0u;
+    return ok ? static_cast<uint32_t>(__half_as_ushort(s)) | (static_cast<uint32_t>(__half_as_ushort(m)) << 16) : 0x7fff7fffu;
 }
 
+// A lane takes whole groups (64 bytes): their least and largest value and parameters need no other
+// lane.  The chunk's rows that are written come one behind the other, keys, then values, 32 groups a
+// pass, the next pass on its way.  Bound by instructions: about 13 a value.
 template <int G>
 __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const AppendArgs a) {
-    constexpr int kPer = 4 * G, R = 32 / kPer, kIters = 16 / R;  // lanes a row, rows at once
     constexpr int kBytes = kv4_chunk_bytes(G);
     __shared__ __align__(16) uint8_t stage[kWarps][kBytes];
+    __shared__ uint8_t order[kWarps][16];  // the rows that are written, in order
     pdl_launch_dependents();
     pdl_wait();
     const int32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -157,23 +160,29 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const AppendArgs a
     }
     const uint32_t rows = __ballot_sync(kFull, src >= 0);
     if (rows == 0) return;
-    const int32_t piece = lane % kPer, g = piece >> 2, qd = piece & 3;
-    const bool idle = lane / kPer >= R;  // head_dim 96: 24 lanes work
-    // two steps of rows at a time, the next two on their way: few instructions, so that a small write
-    // does not wait for its code
-    auto load = [&](int32_t i, uint4 &kx, uint4 &vx) {
-        const int32_t t = i * R + lane / kPer, from = __shfl_sync(kFull, src, t & 15);
-        kx = vx = make_uint4(0, 0, 0, 0);
-        if (i < kIters && from >= 0 && !idle) {
-            const int64_t off = (static_cast<int64_t>(b) * a.src_rows + from) * a.ld + (static_cast<int64_t>(hk) * kPer + piece) * 8;
-            kx = __ldg(reinterpret_cast<const uint4 *>(a.k + off));
-            vx = __ldg(reinterpret_cast<const uint4 *>(a.w + off));
+    const int32_t live = __popc(rows), items = 2 * live * G;
+    if (src >= 0) order[warp][__popc(rows & ((1u << lane) - 1u))] = static_cast<uint8_t>(lane);
+    __syncwarp();
+    // group `it` of the pass: row, tensor and place in the row
+    auto load = [&](int32_t it, uint32_t (&w)[16]) {
+        const int32_t n = it / G, g = it - n * G;
+        const bool value = n >= live;
+        const int32_t t = order[warp][min(value ? n - live : n, 15)], from = __shfl_sync(kFull, src, t & 15);
+        if (it < items) {
+            const uint4 *p = reinterpret_cast<const uint4 *>((value ? a.w : a.k) + (static_cast<int64_t>(b) * a.src_rows + from) * a.ld +
+                                                             (static_cast<int64_t>(hk) * G + g) * kKv4Group);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint4 x = __ldg(p + i);
+                w[4 * i] = x.x, w[4 * i + 1] = x.y, w[4 * i + 2] = x.z, w[4 * i + 3] = x.w;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) w[i] = 0u;
         }
     };
-    constexpr int kStep = kIters < 2 ? 1 : 2;
-    uint4 kx[kStep], vx[kStep];
-#pragma unroll
-    for (int u = 0; u < kStep; ++u) load(u, kx[u], vx[u]);
+    uint32_t now[16], ahead[16];
+    load(lane, now);
     uint8_t *chunk = kv4_chunk(a.v, b, hk, chunk0);
     if (!chunk) {
         if (lane == 0) latch(a.status, kDevBounds);
@@ -181,31 +190,29 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const AppendArgs a
     }
     uint8_t *st = stage[warp];
 #pragma unroll 1
-    for (int32_t i0 = 0; i0 < kIters; i0 += kStep) {
-        uint4 kn[kStep], vn[kStep];
+    for (int32_t it0 = 0; it0 < items; it0 += 32) {
+        load(it0 + 32 + lane, ahead);
+        uint32_t codes[4];
+        const uint32_t params = quantise(now, codes);
+        const int32_t it = it0 + lane;
+        if (it < items) {
+            const int32_t n = it / G, g = it - n * G;
+            if (n < live) {
+                const int32_t ks = kv4_key_slot(order[warp][n]);
 #pragma unroll
-        for (int u = 0; u < kStep; ++u) load(i0 + kStep + u, kn[u], vn[u]);
-        if (((rows >> (i0 * R)) & ((1u << (R * kStep)) - 1u)) != 0) {  // warp-uniform
+                for (int qd = 0; qd < 4; ++qd) *reinterpret_cast<uint32_t *>(st + ks * 16 * G + (qd * G + g) * 4) = codes[qd];
+                *reinterpret_cast<uint32_t *>(st + kv4_key_params(G) + ks * 4 * G + 4 * g) = params;
+            } else {
+                const int32_t t = order[warp][n - live];
+                uint8_t *vrow = st + kv4_value_codes(G) + t * 16 * G;
 #pragma unroll
-            for (int u = 0; u < kStep; ++u) {
-                const int32_t t = ((i0 + u) * R + lane / kPer) & 15, ks = kv4_key_slot(t);
-                uint32_t pk, pv;
-                const uint32_t ck = quantise8(kx[u], &pk), cv = quantise8(vx[u], &pv);
-                if (!idle) {
-                    *reinterpret_cast<uint32_t *>(st + ks * 16 * G + (qd * G + g) * 4) = ck;
-                    uint8_t *vrow = st + kv4_value_codes(G) + t * 16 * G;
-                    *reinterpret_cast<uint16_t *>(vrow + kv4_value_word(t, 2 * qd, g, G)) = static_cast<uint16_t>(cv);
-                    *reinterpret_cast<uint16_t *>(vrow + kv4_value_word(t, 2 * qd + 1, g, G)) = static_cast<uint16_t>(cv >> 16);
-                    if (qd == 0) *reinterpret_cast<uint32_t *>(st + kv4_key_params(G) + ks * 4 * G + 4 * g) = pk;
-                    if (qd == 1) *reinterpret_cast<uint32_t *>(st + kv4_value_params(G) + t * 4 * G + 4 * g) = pv;
-                }
+                for (int gq = 0; gq < 8; ++gq)
+                    *reinterpret_cast<uint16_t *>(vrow + kv4_value_word(t, gq, g, G)) = static_cast<uint16_t>(codes[gq >> 1] >> (16 * (gq & 1)));
+                *reinterpret_cast<uint32_t *>(st + kv4_value_params(G) + t * 4 * G + 4 * g) = params;
             }
         }
 #pragma unroll
-        for (int u = 0; u < kStep; ++u) {
-            kx[u] = kn[u];
-            vx[u] = vn[u];
-        }
+        for (int i = 0; i < 16; ++i) now[i] = ahead[i];
     }
     __syncwarp();
     // out in the widest words that hold one row's bytes each: a row has 16 G bytes of codes and 4 G of
