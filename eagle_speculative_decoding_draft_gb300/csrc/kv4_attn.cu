@@ -104,7 +104,8 @@ __global__ void __launch_bounds__(kThreads, Shape<G, NQ>::kBlocks) kv4_attention
         abort_mark = 0;
         fence_barrier_init();
     }
-    pdl_launch_dependents();
+    // no early launch of dependents: their blocks would take the places of the next call's CTAs, of
+    // which all must be resident at once (64 8-node trees back to back: 150 us with it, 115 without)
     pdl_wait();
     const Kv4Attention &a = k.a;
     Place p;
@@ -655,7 +656,6 @@ __global__ void __launch_bounds__(kThreads, Shape<G, NQ>::kBlocks) kv4_attention
 // a part for the weights, then four dims a lane over all parts.
 constexpr int kMergeRows = 4;
 __global__ void __launch_bounds__(kMergeRows * 32) kv4_merge_kernel(const __grid_constant__ Kv4Args k) {
-    pdl_launch_dependents();
     pdl_wait();
     const int32_t lane = threadIdx.x & 31, grid = gridDim.x;
     // CTA c continues a unit that CTA c - 1 began, and that goes on while the kind is 2

@@ -236,8 +236,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
         abort_mark = 0;
         fence_barrier_init();
     }
-    pdl_launch_dependents();
-    pdl_wait();
+    pdl_wait();  // and no early launch of dependents (kv4_attn.cu)
     Place p;
     const bool busy = find_place(k, &p, red, spots);
     if (!busy) {

@@ -12,8 +12,12 @@ import ctypes
 import torch
 
 from . import _lib
-from ._lib import check
-from .engine import _dtype_code, _need, _ptr, _stream
+from ._lib import EAGLE_BF16, EAGLE_F32, check
+from .engine import _need
+
+_BF16, _I32, _U8 = torch.bfloat16, torch.int32, torch.uint8
+_DTYPES = {torch.bfloat16: EAGLE_BF16, torch.float32: EAGLE_F32}
+_AS_IS = contextlib.nullcontext()
 
 
 def _here(t, name, device, dtype=None):
@@ -25,13 +29,14 @@ def _here(t, name, device, dtype=None):
 
 
 def _ints(t, name, device, shape):
-    """A contiguous int32 tensor of this shape, or None."""
+    """The address of a contiguous int32 tensor of this shape, or None."""
     if t is None:
         return None
-    _need(_here(t, name, device, torch.int32), name)
-    if tuple(t.shape) != shape:
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor")
+    if _here(t, name, device, _I32).shape != shape:
         raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-    return t
+    return t.data_ptr()
 
 
 def _row_step(t, name):
@@ -39,6 +44,8 @@ def _row_step(t, name):
     tensor, or a slice of wider rows such as a projection's output)."""
     B, n, h, D = t.shape
     row = h * D
+    if t.is_contiguous():
+        return row
     if t.stride(3) != 1 or (h > 1 and t.stride(2) != D):
         raise ValueError(f"{name}: a row's heads must be packed")
     step = t.stride(1) if n > 1 else (t.stride(0) if B > 1 else row)
@@ -65,7 +72,9 @@ class KV4Cache:
             raise ValueError("a KV4Cache lives on a CUDA device")
         if self.device.index is None:
             self.device = torch.device("cuda", torch.cuda.current_device())
+        self._index = self.device.index
         self.batch, self.kv_heads, self.head_dim = batch, kv_heads, head_dim
+        self._tail = (kv_heads, head_dim)
         self.page_size, self.num_pages, self.max_pages = page_size, num_pages, max_pages
         self._c = _lib.KV4CacheStruct(kv_heads, head_dim, page_size, num_pages, max_pages, None, None, None)
         self._ref = ctypes.byref(self._c)
@@ -74,7 +83,7 @@ class KV4Cache:
             raise ValueError("unusable 4-bit cache sizes")
         if pages is None:
             pages = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
-        elif _need(_here(pages, "pages", self.device, torch.uint8), "pages").numel() < nbytes:
+        elif _need(_here(pages, "pages", self.device, _U8), "pages").numel() < nbytes:
             raise ValueError(f"pages must hold at least {nbytes} bytes")
         self._pages = pages
         if num_pages >= batch * max_pages:
@@ -84,6 +93,7 @@ class KV4Cache:
         self._lengths = torch.zeros(batch, dtype=torch.int32, device=self.device)
         self._status = torch.zeros(1, dtype=torch.int32, device=self.device)
         self._c.pages, self._c.table, self._c.lengths = pages.data_ptr(), self._table.data_ptr(), self._lengths.data_ptr()
+        self._status_ptr = self._status.data_ptr()
         self._ws_bytes = {}
 
     pages = property(lambda self: self._pages, doc="The page pool, uint8.")
@@ -96,19 +106,22 @@ class KV4Cache:
         allocated belongs to the stream that uses it."""
         if stream is not None:
             return torch.cuda.stream(stream)
-        if torch.cuda.current_device() != self.device.index:
+        if torch.cuda.current_device() != self._index:
             return torch.cuda.device(self.device)
-        return contextlib.nullcontext()
+        return _AS_IS
+
+    def _raw_stream(self, stream):
+        return torch._C._cuda_getCurrentRawStream(self._index) if stream is None else stream.cuda_stream
 
     def _kv(self, k, v):
         for t, name in ((k, "k"), (v, "v")):
-            _here(t, name, self.device, torch.bfloat16)
-            if t.dim() != 4 or t.shape[0] != self.batch or tuple(t.shape[2:]) != (self.kv_heads, self.head_dim):
+            _here(t, name, self.device, _BF16)
+            if t.dim() != 4 or t.shape[0] != self.batch or t.shape[2:] != self._tail:
                 raise ValueError(f"{name} must be [{self.batch}][rows][{self.kv_heads}][{self.head_dim}]")
         if k.shape != v.shape:
             raise ValueError("k and v must have the same shape")
         if k.shape[1] == 0:
-            return k.shape[2] * k.shape[3]
+            return self.kv_heads * self.head_dim
         ld = _row_step(k, "k")
         if _row_step(v, "v") != ld:
             raise ValueError("k and v must have the same row spacing")
@@ -121,41 +134,39 @@ class KV4Cache:
         is not written), e.g. a verify's accept_nodes; count [batch] int32 is each request's number of
         slots."""
         ld = self._kv(k, v)
-        rows = k.shape[1]
-        slots = rows
+        slots = rows = k.shape[1]
         if select is not None:
             if select.dim() != 2:
                 raise ValueError("select must be [batch][slots]")
             slots = select.shape[1]
-            _ints(select, "select", self.device, (self.batch, slots))
-        _ints(count, "count", self.device, (self.batch,))
-        _ints(start, "start", self.device, (self.batch,))
+        # addresses beside the tensors, which must live until the call is enqueued
+        p_select = _ints(select, "select", self.device, (self.batch, slots))
+        p_count = _ints(count, "count", self.device, (self.batch,))
+        p_start = _ints(start, "start", self.device, (self.batch,))
         with self._on(stream):
-            check(self._lib.eagle_kv4_append(self._ref, self.batch, rows, slots, _ptr(k), _ptr(v), ld, _ptr(select),
-                                             _ptr(count), _ptr(start), self._status.data_ptr(),
-                                             _stream(self.device, stream)), "eagle_kv4_append")
+            check(self._lib.eagle_kv4_append(self._ref, self.batch, rows, slots, k.data_ptr(), v.data_ptr(), ld, p_select,
+                                             p_count, p_start, self._status_ptr, self._raw_stream(stream)), "eagle_kv4_append")
 
     def read(self, start=None, rows=None, dtype=torch.bfloat16, out=None, stream=None):
         """The values that positions start[b] (default 0) .. + rows - 1 stand for: (k, v), each
         [batch][rows][kv_heads][head_dim] of `dtype` (bf16 or fp32).  out = (k, v) receives them (its
         shape gives rows); rows behind a request's length are left as they are (0 in fresh
         tensors).  rows defaults to the capacity."""
-        _ints(start, "start", self.device, (self.batch,))
+        p_start = _ints(start, "start", self.device, (self.batch,))
         with self._on(stream):
             if out is None:
-                rows = self.capacity if rows is None else rows
-                shape = (self.batch, rows, self.kv_heads, self.head_dim)
+                shape = (self.batch, self.capacity if rows is None else rows, *self._tail)
                 out = (torch.zeros(shape, dtype=dtype, device=self.device), torch.zeros(shape, dtype=dtype, device=self.device))
             k, v = out
             for t, name in ((k, "out[0]"), (v, "out[1]")):
-                _need(_here(t, name, self.device), name)
-                if t.dim() != 4 or t.shape[0] != self.batch or tuple(t.shape[2:]) != (self.kv_heads, self.head_dim):
+                if not _here(t, name, self.device).is_contiguous() or t.dtype not in _DTYPES:
+                    raise ValueError(f"{name} must be a contiguous bf16 or fp32 tensor")
+                if t.dim() != 4 or t.shape[0] != self.batch or t.shape[2:] != self._tail:
                     raise ValueError(f"{name} must be [{self.batch}][rows][{self.kv_heads}][{self.head_dim}]")
             if k.shape != v.shape or k.dtype != v.dtype or (rows is not None and k.shape[1] != rows):
                 raise ValueError("the outputs must agree in shape and dtype")
-            check(self._lib.eagle_kv4_read(self._ref, self.batch, k.shape[1], _ptr(start), _ptr(k), _ptr(v),
-                                           _dtype_code(k.dtype), self._status.data_ptr(), _stream(self.device, stream)),
-                  "eagle_kv4_read")
+            check(self._lib.eagle_kv4_read(self._ref, self.batch, k.shape[1], p_start, k.data_ptr(), v.data_ptr(), _DTYPES[k.dtype],
+                                           self._status_ptr, self._raw_stream(stream)), "eagle_kv4_read")
         return k, v
 
     def attention_workspace_bytes(self, nodes: int, heads: int) -> int:
@@ -175,34 +186,35 @@ class KV4Cache:
         those that mask [batch][n][ceil(n / 32)] int32 marks, or without a mask the node's own and
         the earlier ones.  Returns out [batch][n][heads][head_dim] bf16.  workspace: a uint8 tensor to
         use instead of a fresh one; calls that may overlap need one each."""
-        _here(q, "q", self.device, torch.bfloat16)
+        _here(q, "q", self.device, _BF16)
         if q.dim() != 4 or q.shape[0] != self.batch or q.shape[3] != self.head_dim or q.shape[1] < 1:
             raise ValueError(f"q must be [{self.batch}][n][heads][{self.head_dim}]")
         n, heads = q.shape[1], q.shape[2]
         ldq, ldkv = _row_step(q, "q"), 0
-        if (k is None) != (v is None):
-            raise ValueError("k and v go together")
-        if k is not None:
+        p_k = p_v = None
+        if k is not None and v is not None:
             ldkv = self._kv(k, v)
             if k.shape[1] != n:
                 raise ValueError("k and v must have a row for each node")
+            p_k, p_v = k.data_ptr(), v.data_ptr()
+        elif k is not v:
+            raise ValueError("k and v go together")
         elif mask is not None:
             raise ValueError("a mask needs k and v")
-        _ints(mask, "mask", self.device, (self.batch, n, (n + 31) // 32))
-        nbytes = self.attention_workspace_bytes(n, heads)
+        p_mask = _ints(mask, "mask", self.device, (self.batch, n, (n + 31) // 32))
+        nbytes = self._ws_bytes.get((n, heads)) or self.attention_workspace_bytes(n, heads)
         with self._on(stream):
             if out is None:
-                out = torch.empty(self.batch, n, heads, self.head_dim, dtype=torch.bfloat16, device=self.device)
-            elif _need(_here(out, "out", self.device, torch.bfloat16), "out").shape != q.shape:
-                raise ValueError("out must have the shape of q")
+                out = q.new_empty(q.shape)
+            elif not _here(out, "out", self.device, _BF16).is_contiguous() or out.shape != q.shape:
+                raise ValueError("out must be contiguous and have the shape of q")
             if workspace is None:
-                workspace = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
-            elif _need(_here(workspace, "workspace", self.device, torch.uint8), "workspace").numel() < nbytes:
+                workspace = self._pages.new_empty(nbytes)
+            elif _need(_here(workspace, "workspace", self.device, _U8), "workspace").numel() < nbytes:
                 raise ValueError(f"workspace must hold at least {nbytes} bytes")
-            check(self._lib.eagle_kv4_attention(self._ref, self.batch, n, heads, _ptr(q), ldq, _ptr(k), _ptr(v), ldkv,
-                                                _ptr(mask), _ptr(out), _ptr(workspace), nbytes,
-                                                self._status.data_ptr(), _stream(self.device, stream)),
-                  "eagle_kv4_attention")
+            check(self._lib.eagle_kv4_attention(self._ref, self.batch, n, heads, q.data_ptr(), ldq, p_k, p_v, ldkv, p_mask,
+                                                out.data_ptr(), workspace.data_ptr(), nbytes, self._status_ptr,
+                                                self._raw_stream(stream)), "eagle_kv4_attention")
         return out
 
     def status(self, stream=None):
