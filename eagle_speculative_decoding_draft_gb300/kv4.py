@@ -34,7 +34,9 @@ def _ints(t, name, device, shape):
         return None
     if not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous CUDA tensor")
-    if _here(t, name, device, _I32).shape != shape:
+    if t.dtype is not _I32 or t.get_device() != device.index:
+        _here(t, name, device, _I32)
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
     return t.data_ptr()
 
@@ -45,7 +47,7 @@ def _row_step(t, name):
     B, n, h, D = t.shape
     row = h * D
     if t.is_contiguous():
-        return row
+        return row  # whatever the strides of sizes of 1
     if t.stride(3) != 1 or (h > 1 and t.stride(2) != D):
         raise ValueError(f"{name}: a row's heads must be packed")
     step = t.stride(1) if n > 1 else (t.stride(0) if B > 1 else row)
@@ -94,7 +96,7 @@ class KV4Cache:
         self._status = torch.zeros(1, dtype=torch.int32, device=self.device)
         self._c.pages, self._c.table, self._c.lengths = pages.data_ptr(), self._table.data_ptr(), self._lengths.data_ptr()
         self._status_ptr = self._status.data_ptr()
-        self._ws_bytes = {}
+        self._plans = {}
 
     pages = property(lambda self: self._pages, doc="The page pool, uint8.")
     table = property(lambda self: self._table, doc="Pages of each request, [batch][max_pages] int32.")
@@ -115,7 +117,8 @@ class KV4Cache:
 
     def _kv(self, k, v):
         for t, name in ((k, "k"), (v, "v")):
-            _here(t, name, self.device, _BF16)
+            if t.dtype is not _BF16 or t.get_device() != self._index:
+                _here(t, name, self.device, _BF16)
             if t.dim() != 4 or t.shape[0] != self.batch or t.shape[2:] != self._tail:
                 raise ValueError(f"{name} must be [{self.batch}][rows][{self.kv_heads}][{self.head_dim}]")
         if k.shape != v.shape:
@@ -171,14 +174,21 @@ class KV4Cache:
 
     def attention_workspace_bytes(self, nodes: int, heads: int) -> int:
         """Bytes of scratch that an attention call with these sizes needs."""
-        n = self._ws_bytes.get((nodes, heads))
-        if n is None:
-            with self._on(None):
-                n = self._lib.eagle_kv4_attention_workspace_bytes(self._ref, nodes, heads)
-            if n == 0:
-                raise ValueError(f"unusable attention sizes (nodes={nodes}, heads={heads})")
-            self._ws_bytes[(nodes, heads)] = n
+        with self._on(None):
+            n = self._lib.eagle_kv4_attention_workspace_bytes(self._ref, nodes, heads)
+        if n == 0:
+            raise ValueError(f"unusable attention sizes (nodes={nodes}, heads={heads})")
         return n
+
+    def _plan(self, q):
+        """What an attention call with queries of this shape needs: checked and computed once."""
+        if q.dim() != 4 or q.shape[0] != self.batch or q.shape[3] != self.head_dim or q.shape[1] < 1:
+            raise ValueError(f"q must be [{self.batch}][n][heads][{self.head_dim}]")
+        n, heads = q.shape[1], q.shape[2]
+        plan = (n, heads, self.attention_workspace_bytes(n, heads), (self.batch, n, *self._tail),
+                (self.batch, n, (n + 31) // 32), heads * self.head_dim, self.kv_heads * self.head_dim)
+        self._plans[q.shape] = plan
+        return plan
 
     def attention(self, q, k=None, v=None, mask=None, out=None, workspace=None, stream=None):
         """Attention of the nodes' queries q [batch][n][heads][head_dim] bf16 over each request's
@@ -186,27 +196,30 @@ class KV4Cache:
         those that mask [batch][n][ceil(n / 32)] int32 marks, or without a mask the node's own and
         the earlier ones.  Returns out [batch][n][heads][head_dim] bf16.  workspace: a uint8 tensor to
         use instead of a fresh one; calls that may overlap need one each."""
-        _here(q, "q", self.device, _BF16)
-        if q.dim() != 4 or q.shape[0] != self.batch or q.shape[3] != self.head_dim or q.shape[1] < 1:
-            raise ValueError(f"q must be [{self.batch}][n][heads][{self.head_dim}]")
-        n, heads = q.shape[1], q.shape[2]
-        ldq, ldkv = _row_step(q, "q"), 0
-        p_k = p_v = None
+        shape = q.shape
+        n, heads, nbytes, kv_shape, mask_shape, ldq, ldkv = self._plans.get(shape) or self._plan(q)
+        if q.dtype is not _BF16 or q.get_device() != self._index:
+            _here(q, "q", self.device, _BF16)
+        if not q.is_contiguous():
+            ldq = _row_step(q, "q")
+        p_k = p_v = p_mask = None
         if k is not None and v is not None:
-            ldkv = self._kv(k, v)
-            if k.shape[1] != n:
-                raise ValueError("k and v must have a row for each node")
+            if k.shape != kv_shape or v.shape != kv_shape:
+                raise ValueError(f"k and v must be {list(kv_shape)}")
+            if not (k.dtype is v.dtype is _BF16 and k.get_device() == v.get_device() == self._index and k.is_contiguous()
+                    and v.is_contiguous()):
+                ldkv = self._kv(k, v)
             p_k, p_v = k.data_ptr(), v.data_ptr()
         elif k is not v:
             raise ValueError("k and v go together")
         elif mask is not None:
             raise ValueError("a mask needs k and v")
-        p_mask = _ints(mask, "mask", self.device, (self.batch, n, (n + 31) // 32))
-        nbytes = self._ws_bytes.get((n, heads)) or self.attention_workspace_bytes(n, heads)
+        if mask is not None:
+            p_mask = _ints(mask, "mask", self.device, mask_shape)
         with self._on(stream):
             if out is None:
-                out = q.new_empty(q.shape)
-            elif not _here(out, "out", self.device, _BF16).is_contiguous() or out.shape != q.shape:
+                out = q.new_empty(shape)
+            elif not _here(out, "out", self.device, _BF16).is_contiguous() or out.shape != shape:
                 raise ValueError("out must be contiguous and have the shape of q")
             if workspace is None:
                 workspace = self._pages.new_empty(nbytes)
