@@ -50,6 +50,15 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// The first of a sum: from zero.
+__device__ __forceinline__ void mma_f16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                              uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
 __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
     asm volatile(
@@ -442,9 +451,7 @@ __global__ void __launch_bounds__(kThreads, Shape<G, NQ>::kBlocks) kv4_attention
                         const uint32_t a0 = __byte_perm(ma, ma, 0x3232), a1 = __byte_perm(mb, mb, 0x3232);
 #pragma unroll
                         for (int nq = 0; nq < NQ; ++nq) {
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) x[nq][e] = 0.0f;
-                            mma_f16(x[nq], a0, a1, 0u, 0u, qs[nq], 0u);
+                            mma_f16_first(x[nq], a0, a1, 0u, 0u, qs[nq], 0u);
 #pragma unroll
                             for (int e = 0; e < 4; ++e) x[nq][e] *= 0x1p-24f;
                         }
@@ -460,8 +467,8 @@ __global__ void __launch_bounds__(kThreads, Shape<G, NQ>::kBlocks) kv4_attention
                         const float sa = low_f16(pa[g]), sb = low_f16(pb[g]);
 #pragma unroll
                         for (int nq = 0; nq < NQ; ++nq) {
-                            float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                            mma_f16(acc, wa[g] & 0x000f000fu, wb[g] & 0x000f000fu, wa[g] & 0x00f000f0u,
+                            float acc[4];
+                            mma_f16_first(acc, wa[g] & 0x000f000fu, wb[g] & 0x000f000fu, wa[g] & 0x00f000f0u,
                                     wb[g] & 0x00f000f0u, qf[2 * g][nq][0], qf[2 * g][nq][1]);
                             mma_f16(acc, xa & 0x000f000fu, xb & 0x000f000fu, xa & 0x00f000f0u, xb & 0x00f000f0u,
                                     qf[2 * g + 1][nq][0], qf[2 * g + 1][nq][1]);

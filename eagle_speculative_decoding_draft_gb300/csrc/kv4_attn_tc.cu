@@ -37,8 +37,8 @@ namespace {
 
 constexpr int kKeys = kKv4TcTile;
 constexpr int kThreads = 26 * 32;
-constexpr int kFillWarps = 8;
-constexpr int kRaw = 2;  // halves of tiles (keys or values) of codes in flight
+constexpr int kFillWarps = 4;  // for the keys, and as many for the values
+constexpr int kRaw = 2;        // a tile's codes in flight: the keys', the values'
 constexpr float kTop = 15.0f, kAim = 4.0f;  // p <= 2^15; a new reference puts the largest at 2^4
 constexpr uint32_t kTmemCols = 512;
 
@@ -145,18 +145,24 @@ __device__ __forceinline__ uint4 dequant8(uint32_t w, uint32_t sm) {
 // Whether fp16 cannot hold x.
 __device__ __forceinline__ bool is_odd(float x) { return !(fabsf(x) <= 65504.0f); }
 
-// Eight bf16 to fp16 in the same order; what fp16 cannot hold becomes 0 and sets `odd`.
+// Eight bf16 with 0 in place of what fp16 cannot hold.
+static __device__ __noinline__ uint4 without_odd(uint4 v) {
+    uint32_t *w = reinterpret_cast<uint32_t *>(&v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (is_odd(bf_lo(w[i]))) w[i] &= 0xffff0000u;
+        if (is_odd(bf_hi(w[i]))) w[i] &= 0x0000ffffu;
+    }
+    return v;
+}
+// Eight bf16 to fp16 in the order of the tiles; what fp16 cannot hold becomes 0 and sets `odd`.
 __device__ __forceinline__ uint4 convert8(uint4 v, bool &odd) {
     auto abs2 = [](uint32_t x) { return x & 0x7fff7fffu; };
     auto b2 = [](uint32_t x) { return *reinterpret_cast<const __nv_bfloat162 *>(&x); };
     const __nv_bfloat162 big = __hmax2_nan(__hmax2_nan(b2(abs2(v.x)), b2(abs2(v.y))), __hmax2_nan(b2(abs2(v.z)), b2(abs2(v.w))));
     if (!(__low2float(big) <= 65504.0f && __high2float(big) <= 65504.0f)) {
         odd = true;
-        uint32_t *w = reinterpret_cast<uint32_t *>(&v);
-        for (int i = 0; i < 4; ++i) {
-            if (is_odd(bf_lo(w[i]))) w[i] &= 0xffff0000u;
-            if (is_odd(bf_hi(w[i]))) w[i] &= 0x0000ffffu;
-        }
+        v = without_odd(v);
     }
     return make_uint4(pack_f16(bf_lo(v.x), bf_lo(v.z)), pack_f16(bf_hi(v.x), bf_hi(v.z)), pack_f16(bf_lo(v.y), bf_lo(v.w)),
                       pack_f16(bf_hi(v.y), bf_hi(v.w)));
@@ -196,6 +202,92 @@ static __device__ __noinline__ void add_odd_values(const __nv_bfloat16 *vt, int6
     }
 }
 
+// Two fp32 operations by one instruction, and the largest of three.
+__device__ __forceinline__ uint64_t pack_2(uint32_t lo, uint32_t hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 unpack_2(uint64_t x) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma_2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add_2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float max_3(float a, uint32_t b, uint32_t c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(__uint_as_float(b)), "f"(__uint_as_float(c)));
+    return r;
+}
+
+// Scores of keys that the row does not see become -inf: most tiles have none, and their loops know
+// nothing of masks.  Warp-wide, as all of these.
+static __device__ __noinline__ void hide_keys(uint32_t t, uint32_t see0, uint32_t see1) {
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+        uint32_t v[16];
+        tmem_ld_16(t + 16 * c, v);
+        tmem_wait_ld();
+        const uint32_t bits = (c < 2 ? see0 : see1) >> (16 * (c & 1));
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = (bits >> i) & 1u ? v[i] : __float_as_uint(-INFINITY);
+        tmem_st_16(t + 16 * c, v);
+    }
+    tmem_wait_st();
+}
+
+// p = 2^(score mul + sub) of 64 keys, as fp16 over the first 32 columns of their scores; returns the
+// sum.  One product and difference; `steps`: in two, as the maximum was formed, for scores so large
+// that the product's rounding matters next to their differences (and could pass for a score above
+// the maximum).
+__device__ __forceinline__ float probabilities(uint32_t t, float mul, float sub) {
+    const uint64_t mul2 = pack_2(__float_as_uint(mul), __float_as_uint(mul)), sub2 = pack_2(__float_as_uint(sub), __float_as_uint(sub));
+    uint64_t sum = 0;
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+        uint32_t v[16], pk[8];
+        tmem_ld_16(t + 16 * c, v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float2 x = unpack_2(fma_2(pack_2(v[2 * i], v[2 * i + 1]), mul2, sub2));
+            const float p0 = ex2_approx(x.x), p1 = ex2_approx(x.y);
+            sum = add_2(sum, pack_2(__float_as_uint(p0), __float_as_uint(p1)));
+            pk[i] = pack_f16(p0, p1);
+        }
+        tmem_st_8(t + 8 * c, pk);
+    }
+    const float2 x = unpack_2(sum);
+    return x.x + x.y;
+}
+static __device__ __noinline__ float probabilities_in_steps(uint32_t t, float mul, float sub) {
+    float sum = 0.0f;
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+        uint32_t v[16], pk[8];
+        tmem_ld_16(t + 16 * c, v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float p0 = ex2_approx(__fadd_rn(__fmul_rn(__uint_as_float(v[2 * i]), mul), sub));
+            const float p1 = ex2_approx(__fadd_rn(__fmul_rn(__uint_as_float(v[2 * i + 1]), mul), sub));
+            sum += p0 + p1;
+            pk[i] = pack_f16(p0, p1);
+        }
+        tmem_st_8(t + 8 * c, pk);
+    }
+    return sum;
+}
+
 template <int G>
 __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __grid_constant__ Kv4Args k) {
     using S = Tc<G>;
@@ -207,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
     __shared__ int32_t abort_mark;
     __shared__ __align__(8) uint8_t key_bits[4][16];  // by tile & 3: which of its 128 keys are there
     __shared__ uint8_t raw_keys[kRaw][8];             // keys of each chunk that are there
-    __shared__ __align__(8) uint8_t odd_tile[4][2][kFillWarps];  // by tile & 3, key or value, filling warp
+    __shared__ __align__(4) uint8_t odd_tile[4][2][kFillWarps];  // by tile & 3, key or value, filling warp
     __shared__ int32_t row_at[2][128];        // stream, row: node << 16 | head, -1 behind the unit's last row
     __shared__ float2 q_scale[2][128];        // what a row's query and its scores are multiplied by
     __shared__ float half_max[2][2][2][128];  // stream, exchange & 1, half, row
@@ -223,9 +315,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
             mbar_init(&bar.v_full[i], kFillWarps);
             mbar_init(&bar.k_empty[i], 1);
             mbar_init(&bar.v_empty[i], 1);
-            mbar_init(&bar.q_full[i], 256);
+            mbar_init(&bar.q_full[i], 8);
             mbar_init(&bar.s_full[i], 1);
-            mbar_init(&bar.p_full[i], 256);
+            mbar_init(&bar.p_full[i], 8);  // by warps: 256 arrivals take their turns on the barrier's word
             mbar_init(&bar.o_done[i], 1);
         }
         for (int i = 0; i < kRaw; ++i) {
@@ -258,101 +350,112 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
     auto rows_of = [&]() { return min(kKv4TcRows, k.Mq - w.qt * kKv4TcRows); };  // rows of the unit
 
     if (warp >= 16 && warp < 24) {
-        // ---------------- the tiles ----------------
-        const int32_t fw = warp - 16;
-        uint32_t gt = 0, raw = 0;  // tiles and halves of cached tiles so far
+        // ---------------- the tiles: four warps for the keys, four for the values ----------------
+        const int32_t half = (warp - 16) >> 2, fw = warp & 3;
+        uint64_t *const full = half ? bar.v_full : bar.k_full, *const empty = half ? bar.v_empty : bar.k_empty;
+        uint8_t *const stages = base + (half ? S::kV : S::kK);
+        uint32_t gt = 0, raw = 0;  // tiles and cached tiles so far
         do {
-            for (int32_t s = w.s0; s < w.s1; ++s, ++gt) {
-                const uint32_t st = gt & 1u;
-#pragma unroll 1
-                for (int32_t half = 0; half < 2; ++half) {
-                    uint8_t *dst = base + (half ? S::kV : S::kK) + st * S::kTileBytes;
-                    bool odd = false;
-                    if (s >= w.nt) {
-                        const uint32_t rs = raw % kRaw;
-                        wait(&bar.raw_full[rs], raw / kRaw);
-                        if (gt >= 2) wait(half ? &bar.v_empty[st] : &bar.k_empty[st], (gt >> 1) - 1);
-                        __syncwarp();
-                        const uint8_t *src = base + S::kCodes + rs * 8 * S::kPart;
-                        // lanes: four pieces of 8 dims of rows t and t + 4: the stores of eight
-                        // lanes touch all banks
-                        const int32_t m = lane >> 2, q = lane & 3;
-                        const int32_t t8 = (m >> 1) | ((m & 1) << 2);          // token among the 8
-                        const int32_t slot8 = half ? t8 : m;                   // its row
-                        const int32_t qq = half && G == 4 ? q ^ (t8 & 2) : q;  // value rows' halves change places
-                        // group i of 8 rows: 1024 bytes on; dims 32 g + 8 q: chunk 4 g + q
-                        uint8_t *to = dst + fw * 1024 + t8 * 128 + ((qq ^ t8) << 4);
-                        const int32_t odd_g = ((((4 + qq) ^ t8) - (qq ^ t8)) << 4);
-#pragma unroll 2
-                        for (int32_t i = 0; i < 2; ++i) {
-                            const int32_t group = kFillWarps * i + fw;
-                            const uint8_t *part = src + (group >> 1) * S::kPart;
-                            const int32_t slot = (group & 1) * 8 + slot8;
-                            const int32_t here = max(0, min(8, static_cast<int32_t>(raw_keys[rs][group >> 1]) - 8 * (group & 1)));
-                            uint32_t c[G], sm[G];
-                            if constexpr (G == 4) {
-                                const uint4 cv = *reinterpret_cast<const uint4 *>(part + slot * 64 + q * 16);
-                                const uint4 mv = *reinterpret_cast<const uint4 *>(part + 1024 + slot * 16);
-                                c[0] = cv.x, c[1] = cv.y, c[2] = cv.z, c[3] = cv.w;
-                                sm[0] = mv.x, sm[1] = mv.y, sm[2] = mv.z, sm[3] = mv.w;
-                            } else {
-                                const uint2 cv = *reinterpret_cast<const uint2 *>(part + slot * 32 + q * 8);
-                                const uint2 mv = *reinterpret_cast<const uint2 *>(part + 512 + slot * 8);
-                                c[0] = cv.x, c[1] = cv.y;
-                                sm[0] = mv.x, sm[1] = mv.y;
-                            }
-                            if (half) {  // two 16-bit words of four dims each to the keys' words of eight
-                                uint32_t x[G];
+            int32_t s = w.s0;
+            if (s < w.nt) {  // new keys or values, the next ones' loads under way
+                constexpr int kPer = D / 8, kRowsWarp = 32 / kPer, kBatch = 8;  // pieces a row; rows a warp takes at once
+                constexpr int kBatches = kKeys / (4 * kRowsWarp * kBatch);
+                const int32_t ch = lane % kPer, first = fw * kRowsWarp + lane / kPer;
+                const __nv_bfloat16 *src = (half ? a.vn : a.kn) + static_cast<int64_t>(w.b) * a.n * a.ldkv + static_cast<int64_t>(w.hk) * D + ch * 8;
+                uint4 v[kBatch];
+                auto load = [&](int32_t row0) {
 #pragma unroll
-                                for (int g = 0; g < G; ++g) x[g] = __byte_perm(c[g / 2], c[G / 2 + g / 2], g & 1 ? 0x7632 : 0x5410);
-#pragma unroll
-                                for (int g = 0; g < G; ++g) c[g] = x[g];
-                            } else if (lane == 0) {
-                                key_bits[gt & 3][group] = static_cast<uint8_t>((1u << here) - 1u);
-                            }
-                            if (here < 8) {  // rows that are not there hold 0
-#pragma unroll
-                                for (int g = 0; g < G; ++g)
-                                    if (t8 >= here) c[g] = sm[g] = 0u;
-                            }
-#pragma unroll
-                            for (int g = 0; g < G; ++g)
-                                *reinterpret_cast<uint4 *>(to + i * (kFillWarps * 1024) + (g >> 1) * (kKeys * 128) + (g & 1 ? odd_g : 0)) = dequant8(c[g], sm[g]);
-                        }
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&bar.raw_empty[rs]);
-                        ++raw;
-                    } else {
-                        constexpr int kPer = D / 8, kRowsWarp = 32 / kPer;  // pieces a row; rows a warp takes at once
-                        const int32_t ch = lane % kPer, first = fw * kRowsWarp + lane / kPer;
-                        const __nv_bfloat16 *src = (half ? a.vn : a.kn) + (static_cast<int64_t>(w.b) * a.n + s * kKeys) * a.ldkv +
-                                                   static_cast<int64_t>(w.hk) * D + ch * 8;
-                        const int32_t rows = min(a.n - s * kKeys, kKeys);
-#pragma unroll 1
-                        for (int32_t sub = 0; sub < D / 64; ++sub) {
-                            uint4 v[4];
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const int32_t row = (sub * 4 + i) * kFillWarps * kRowsWarp + first;
-                                v[i] = row < rows ? *reinterpret_cast<const uint4 *>(src + row * a.ldkv) : make_uint4(0, 0, 0, 0);
-                            }
-                            if (sub == 0) {
-                                if (gt >= 2) wait(half ? &bar.v_empty[st] : &bar.k_empty[st], (gt >> 1) - 1);
-                                __syncwarp();
-                            }
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const int32_t row = (sub * 4 + i) * kFillWarps * kRowsWarp + first;
-                                *reinterpret_cast<uint4 *>(dst + (ch >> 3) * (kKeys * 128) + sw128(row, ch & 7)) = convert8(v[i], odd);
-                            }
-                        }
+                    for (int i = 0; i < kBatch; ++i) {
+                        const int32_t row = row0 + i * 4 * kRowsWarp + first;
+                        v[i] = row < a.n ? *reinterpret_cast<const uint4 *>(src + row * a.ldkv) : make_uint4(0, 0, 0, 0);
                     }
-                    const bool any = __any_sync(kFull, odd);
-                    if (lane == 0) odd_tile[gt & 3][half][fw] = any;
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(half ? &bar.v_full[st] : &bar.k_full[st]);
+                };
+                load(s * kKeys);
+                const int32_t last = min(w.s1, w.nt);
+                bool odd = false;
+#pragma unroll 1
+                for (int32_t at = s * kBatches; at < last * kBatches; ++at) {
+                    const uint32_t st = gt & 1u;
+                    const int32_t sub = at % kBatches;
+                    if (sub == 0) {
+                        odd = false;
+                        if (gt >= 2) wait(&empty[st], (gt >> 1) - 1);
+                        __syncwarp();
+                    }
+                    uint8_t *dst = stages + st * S::kTileBytes + (ch >> 3) * (kKeys * 128);
+#pragma unroll
+                    for (int i = 0; i < kBatch; ++i)
+                        *reinterpret_cast<uint4 *>(dst + sw128((sub * kBatch + i) * 4 * kRowsWarp + first, ch & 7)) = convert8(v[i], odd);
+                    if (at + 1 < last * kBatches) load((at + 1) * (kKeys / kBatches));
+                    if (sub == kBatches - 1) {
+                        const bool any = __any_sync(kFull, odd);
+                        if (lane == 0) odd_tile[gt & 3][half][fw] = any;
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&full[st]);
+                        ++gt;
+                    }
                 }
+                s = last;
+            }
+#pragma unroll 1
+            for (; s < w.s1; ++s, ++gt, ++raw) {
+                const uint32_t st = gt & 1u;
+                wait(&bar.raw_full[half], raw);
+                const uint8_t *src = base + S::kCodes + half * 8 * S::kPart;
+                // lanes: four pieces of 8 dims of rows t and t + 4: the stores of eight lanes touch
+                // all banks
+                const int32_t m = lane >> 2, q = lane & 3;
+                const int32_t t8 = (m >> 1) | ((m & 1) << 2);          // token among the 8
+                const int32_t slot8 = half ? t8 : m;                   // its row
+                const int32_t qq = half && G == 4 ? q ^ (t8 & 2) : q;  // value rows' halves change places
+                // group i of 8 rows: 1024 bytes on; dims 32 g + 8 q: chunk 4 g + q
+                uint8_t *to = stages + st * S::kTileBytes + fw * 1024 + t8 * 128 + ((qq ^ t8) << 4);
+                const int32_t odd_g = ((((4 + qq) ^ t8) - (qq ^ t8)) << 4);
+                uint32_t c[4][G], sm[4][G];
+#pragma unroll
+                for (int32_t i = 0; i < 4; ++i) {
+                    const int32_t group = 4 * i + fw;
+                    const uint8_t *part = src + (group >> 1) * S::kPart;
+                    const int32_t slot = (group & 1) * 8 + slot8;
+                    const int32_t here = max(0, min(8, static_cast<int32_t>(raw_keys[half][group >> 1]) - 8 * (group & 1)));
+                    if constexpr (G == 4) {
+                        const uint4 cv = *reinterpret_cast<const uint4 *>(part + slot * 64 + q * 16);
+                        const uint4 mv = *reinterpret_cast<const uint4 *>(part + 1024 + slot * 16);
+                        c[i][0] = cv.x, c[i][1] = cv.y, c[i][2] = cv.z, c[i][3] = cv.w;
+                        sm[i][0] = mv.x, sm[i][1] = mv.y, sm[i][2] = mv.z, sm[i][3] = mv.w;
+                    } else {
+                        const uint2 cv = *reinterpret_cast<const uint2 *>(part + slot * 32 + q * 8);
+                        const uint2 mv = *reinterpret_cast<const uint2 *>(part + 512 + slot * 8);
+                        c[i][0] = cv.x, c[i][1] = cv.y;
+                        sm[i][0] = mv.x, sm[i][1] = mv.y;
+                    }
+                    if (!half && lane == 0) key_bits[gt & 3][group] = static_cast<uint8_t>((1u << here) - 1u);
+                    if (t8 >= here) {  // rows that are not there hold 0
+#pragma unroll
+                        for (int g = 0; g < G; ++g) c[i][g] = sm[i][g] = 0u;
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.raw_empty[half]);
+                if (gt >= 2) wait(&empty[st], (gt >> 1) - 1);
+                __syncwarp();
+#pragma unroll
+                for (int32_t i = 0; i < 4; ++i) {
+                    if (half) {  // two 16-bit words of four dims each to the keys' words of eight
+                        uint32_t x[G];
+#pragma unroll
+                        for (int g = 0; g < G; ++g) x[g] = __byte_perm(c[i][g / 2], c[i][G / 2 + g / 2], g & 1 ? 0x7632 : 0x5410);
+#pragma unroll
+                        for (int g = 0; g < G; ++g) c[i][g] = x[g];
+                    }
+#pragma unroll
+                    for (int g = 0; g < G; ++g)
+                        *reinterpret_cast<uint4 *>(to + i * 4096 + (g >> 1) * (kKeys * 128) + (g & 1 ? odd_g : 0)) = dequant8(c[i][g], sm[i][g]);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&full[st]);
             }
         } while (w.next(k, p));
     } else if (warp == 25) {
@@ -461,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
             const int32_t unit_rows = rows_of();
             const bool both = unit_rows > 128;
             const int32_t ur = both ? j * 128 + r : r, row = w.qt * kKv4TcRows + ur;
-            const bool live = ur < unit_rows;
+            const bool live = ur < unit_rows, used = ur - lane < unit_rows;  // the row; any of the warp's
             const int32_t node = live ? row / k.group : 0;
             if (h == 0) row_at[j][r] = live ? (node << 16) | (w.hk * k.group + row - node * k.group) : -1;
             named_barrier_sync(1 + j, 256);
@@ -498,7 +601,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
                 }
             }
             fence_proxy_async_smem();
-            mbar_arrive(&bar.q_full[j]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.q_full[j]);
             {
                 uint32_t z[16];
 #pragma unroll
@@ -542,33 +646,28 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
                     // the tile's values have come too: whether it holds what fp16 does not
                     wait(&bar.v_full[t & 1], t >> 1);
                     __syncwarp();
-                    odd_k = *reinterpret_cast<const volatile unsigned long long *>(odd_tile[t & 3][0]) != 0;
-                    odd_v = *reinterpret_cast<const volatile unsigned long long *>(odd_tile[t & 3][1]) != 0;
+                    odd_k = *reinterpret_cast<const volatile uint32_t *>(odd_tile[t & 3][0]) != 0;
+                    odd_v = *reinterpret_cast<const volatile uint32_t *>(odd_tile[t & 3][1]) != 0;
                 }
                 if (!live) see0 = see1 = 0u;
-                const bool all = __all_sync(kFull, (see0 & see1) == kFull);
                 const int64_t new_row = (static_cast<int64_t>(w.b) * a.n + s * kKeys) * a.ldkv + static_cast<int64_t>(w.hk) * D;
                 const int32_t new_rows = min(a.n - s * kKeys, kKeys);
-                if (odd_k) {
+                if (odd_k && used) {
                     const int32_t head = live ? row_at[j][r] & 0xffff : 0;  // rows that are not there read a query that is
                     add_odd_keys<D>(a.kn + new_row, a.ldkv, 64 * h, min(new_rows, 64 * h + 64),
                                     a.q + (static_cast<int64_t>(w.b) * a.n + node) * a.ldq + static_cast<int64_t>(head) * D, f, t_s);
                 }
-                float mx;
-                {
+                float mx = -INFINITY;
+                if (used) {
+                    if (!__all_sync(kFull, (see0 & see1) == kFull)) hide_keys(t_h, see0, see1);
                     float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
                     for (int c = 0; c < 2; ++c) {
                         uint32_t v[32];
                         tmem_ld_32(t_h + 32 * c, v);
                         tmem_wait_ld();
-                        if (!all) {
-                            const uint32_t bits = c ? see1 : see0;
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) v[i] = (bits >> i) & 1u ? v[i] : __float_as_uint(-INFINITY);
-                        }
-#pragma unroll
-                        for (int i = 0; i < 32; i += 2) m4[(i >> 1) & 3] = fmaxf(fmaxf(m4[(i >> 1) & 3], __uint_as_float(v[i])), __uint_as_float(v[i + 1]));
+                        for (int i = 0; i < 32; i += 2) m4[(i >> 1) & 3] = max_3(m4[(i >> 1) & 3], v[i], v[i + 1]);
                     }
                     mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
                 }
@@ -587,7 +686,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
                     ref = nr;
                 }
                 const float sub = ref == -INFINITY ? 0.0f : -ref;
-                if (done > 0 && __any_sync(kFull, corr != 1.0f)) {
+                if (used && done > 0 && __any_sync(kFull, corr != 1.0f)) {
                     // the scores' arrival says that the stream's earlier products are complete
 #pragma unroll 1
                     for (int c = 0; c < D / 32; ++c) {
@@ -604,42 +703,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
                     const int32_t key0 = s * kKeys;
                     uint4 see = make_uint4(0u, 0u, 0u, 0u);
                     if (live) see = make_uint4(new_seen(key0), new_seen(key0 + 32), new_seen(key0 + 64), new_seen(key0 + 96));
-                    add_odd_values(a.vn + new_row, a.ldkv, new_rows, see, mul, sub, t_s, t_o, h * (D / 2), (h + 1) * (D / 2));
+                    if (used)
+                        add_odd_values(a.vn + new_row, a.ldkv, new_rows, see, mul, sub, t_s, t_o, h * (D / 2), (h + 1) * (D / 2));
                     named_barrier_sync(1 + j, 256);  // both halves have read the scores that p overwrites
                 }
-                // One product and difference; scores so large that the product's rounding matters next
-                // to their differences (and could pass for a score above the maximum) in two steps,
-                // as the maximum was formed.
-                auto exponentials = [&](auto exponent, auto masked) {
-#pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t v[16], pk[8];
-                        tmem_ld_16(t_h + 16 * c, v);
-                        tmem_wait_ld();
-                        const uint32_t bits = (c < 2 ? see0 : see1) >> (16 * (c & 1));
-                        float sum[2] = {0.0f, 0.0f};
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            float p0 = ex2_approx(exponent(__uint_as_float(v[2 * i])));
-                            float p1 = ex2_approx(exponent(__uint_as_float(v[2 * i + 1])));
-                            if constexpr (decltype(masked)::value) {
-                                p0 = (bits >> (2 * i)) & 1u ? p0 : 0.0f;
-                                p1 = (bits >> (2 * i + 1)) & 1u ? p1 : 0.0f;
-                            }
-                            sum[i & 1] += p0 + p1;
-                            pk[i] = pack_f16(p0, p1);
-                        }
-                        l += sum[0] + sum[1];
-                        tmem_st_8(t_h + 8 * c, pk);
-                    }
-                };
-                if (all && !__any_sync(kFull, fabsf(sub) > 1048576.0f))
-                    exponentials([&](float x) { return fmaf(x, mul, sub); }, std::false_type{});
-                else
-                    exponentials([&](float x) { return __fadd_rn(__fmul_rn(x, mul), sub); }, std::true_type{});
+                if (used) l += __any_sync(kFull, fabsf(sub) > 1048576.0f) ? probabilities_in_steps(t_h, mul, sub) : probabilities(t_h, mul, sub);
                 tmem_wait_st();
                 tc_fence_before();
-                mbar_arrive(&bar.p_full[j]);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.p_full[j]);
             }
             gt += tiles;
             // ---------------- the segment's output ----------------
