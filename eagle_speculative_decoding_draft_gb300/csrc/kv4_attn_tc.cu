@@ -252,7 +252,7 @@ static __device__ __noinline__ void hide_keys(uint32_t t, uint32_t see0, uint32_
 __device__ __forceinline__ float probabilities(uint32_t t, float mul, float sub) {
     const uint64_t mul2 = pack_2(__float_as_uint(mul), __float_as_uint(mul)), sub2 = pack_2(__float_as_uint(sub), __float_as_uint(sub));
     uint64_t sum = 0;
-#pragma unroll 1
+#pragma unroll 2
     for (int c = 0; c < 4; ++c) {
         uint32_t v[16], pk[8];
         tmem_ld_16(t + 16 * c, v);
@@ -306,6 +306,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
     __shared__ float2 half_ml[2][2][128];     // stream, half, row: references and sums of a segment
     __shared__ int32_t red[kThreads / 32];
     __shared__ Spot spots[2];
+    __shared__ Place place;
+    __shared__ Walk walks[kThreads / 32];  // each warp's: in registers they would be spilled, and L1 is all shared memory here
     const int32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     volatile int32_t *abort_flag = &abort_mark;
     const Kv4Attention &a = k.a;
@@ -329,11 +331,22 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
         fence_barrier_init();
     }
     pdl_wait();  // and no early launch of dependents (kv4_attn.cu)
-    Place p;
-    const bool busy = find_place(k, &p, red, spots);
-    if (!busy) {
-        if (threadIdx.x == 0) k.share[blockIdx.x].kind = 0;
-        return;
+    {
+        Place p;
+        const bool busy = find_place(k, &p, red, spots);
+        if (!busy) {
+            if (threadIdx.x == 0) k.share[blockIdx.x].kind = 0;
+            return;
+        }
+        if (lane == 0) {
+            Walk first;
+            first.start(k, p);
+            walks[warp] = first;
+            if (warp == 0) {
+                place = p;
+                k.share[blockIdx.x] = share_of(first);
+            }
+        }
     }
     if (warp == 24) {
         tmem_alloc(&tmem_base, kTmemCols);
@@ -343,9 +356,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(kFull, tmem_base, 0);
-    Walk w;
-    w.start(k, p);
-    if (threadIdx.x == 0) k.share[blockIdx.x] = share_of(w);
+    const Walk &w = walks[warp];
+    auto next_unit = [&]() -> bool {
+        __syncwarp();  // every lane is through with the last
+        int more = 0;
+        if (lane == 0) {
+            Walk n = walks[warp];
+            more = n.next(k, place);
+            walks[warp] = n;
+        }
+        more = __shfl_sync(kFull, more, 0);
+        __syncwarp();
+        return more != 0;
+    };
     auto wait = [&](uint64_t *b, uint32_t parity) -> bool { return kv4_wait(b, parity, abort_flag); };
     auto rows_of = [&]() { return min(kKv4TcRows, k.Mq - w.qt * kKv4TcRows); };  // rows of the unit
 
@@ -457,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&full[st]);
             }
-        } while (w.next(k, p));
+        } while (next_unit());
     } else if (warp == 25) {
         // ---------------- copies of codes: a stage is the keys or the values of a cached tile -------
         uint32_t raw = 0;
@@ -492,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
                                   &bar.raw_full[rs]);
                 }
             }
-        } while (!dead && w.next(k, p));
+        } while (!dead && next_unit());
         // every copy has landed before the block's memory is handed on
         if (lane == 0)
             for (uint32_t i = raw > kRaw ? raw - kRaw : 0; i < raw; ++i) mbar_wait(&bar.raw_full[i % kRaw], (i / kRaw) & 1u, nullptr);
@@ -547,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
             }
             gt += tiles;
             ++seg;
-        } while (ok && w.next(k, p));
+        } while (ok && next_unit());
         // what was issued lands before the block's memory is handed on
         commit_to(&bar.drain, leader);
         mbar_wait(&bar.drain, 0, nullptr);
@@ -559,14 +582,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t t_s = tmem + lanes + j * 128u, t_h = t_s + 64 * h, t_o = tmem + lanes + 256u + j * 128u;
         uint32_t gt = 0, n_s = 0, n_o = 0;  // tiles, scores and outputs of this stream so far
-        uint32_t buf = 0;                   // of half_max: another one at every exchange
         do {
-            const int32_t unit_rows = rows_of();
-            const bool both = unit_rows > 128;
-            const int32_t ur = both ? j * 128 + r : r, row = w.qt * kKv4TcRows + ur;
-            const bool live = ur < unit_rows, used = ur - lane < unit_rows;  // the row; any of the warp's
-            const int32_t node = live ? row / k.group : 0;
-            if (h == 0) row_at[j][r] = live ? (node << 16) | (w.hk * k.group + row - node * k.group) : -1;
+            const bool both = rows_of() > 128;
+            bool live, used;  // the thread's row, any of the warp's
+            {
+                const int32_t unit_rows = rows_of(), ur = both ? j * 128 + r : r, row = w.qt * kKv4TcRows + ur;
+                live = ur < unit_rows;
+                used = ur - lane < unit_rows;
+                const int32_t node = row / k.group;
+                if (h == 0) row_at[j][r] = live ? (node << 16) | (w.hk * k.group + row - node * k.group) : -1;
+            }
             named_barrier_sync(1 + j, 256);
             // the stream's queries, whole rows at a time: scaled, to fp16, and what turns a row's
             // scores to base 2
@@ -612,24 +637,26 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
                 tmem_wait_st();
             }
             named_barrier_sync(1 + j, 256);
-            const float f = q_scale[j][r].x, mul = q_scale[j][r].y;
-            const uint32_t *mrow = a.mask ? a.mask + (static_cast<int64_t>(w.b) * a.n + node) * k.W : nullptr;
+            const float mul = q_scale[j][r].y;
             // which of new keys k0 .. k0 + 31 the row sees
             auto new_seen = [&](int32_t k0) {
+                const int32_t node = max(row_at[j][r], 0) >> 16;
+                const uint32_t *mrow = a.mask ? a.mask + (static_cast<int64_t>(w.b) * a.n + node) * k.W : nullptr;
                 const int32_t left = a.n - k0, own = node - k0;  // causal: nodes 0..node
                 uint32_t v = own >= 31 ? kFull : (own >= 0 ? (2u << own) - 1u : 0u);
                 if (mrow) v = left > 0 ? mrow[k0 >> 5] : 0u;
                 return v & (left >= 32 ? kFull : (left > 0 ? (1u << left) - 1u : 0u));
             };
+            // the first of new tile s's keys or values
+            auto new_row = [&](int32_t s) {
+                return (static_cast<int64_t>(w.b) * a.n + s * kKeys) * a.ldkv + static_cast<int64_t>(w.hk) * D;
+            };
             float ref = -INFINITY, l = 0.0f;
-            const int32_t tiles = w.s1 - w.s0;
-            int32_t done = 0;  // tiles of this segment that this stream took
-            for (int32_t ti = both ? 0 : j; ti < tiles; ti += both ? 1 : 2, ++done) {
-                const int32_t s = w.s0 + ti;
-                const uint32_t t = gt + ti;
+            const int32_t first_tile = both ? 0 : j, s1 = w.s1;
+            for (int32_t s = w.s0 + first_tile; s < s1; s += both ? 1 : 2) {
+                const uint32_t t = gt + (s - w.s0);
                 // which of this half's keys the row sees
                 uint32_t see0 = 0u, see1 = 0u;
-                bool odd_k = false, odd_v = false;
                 if (s < w.nt) {
                     const int32_t key0 = s * kKeys + 64 * h;
                     see0 = new_seen(key0);
@@ -642,21 +669,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
                     const uint2 b = *reinterpret_cast<const uint2 *>(key_bits[t & 3] + 8 * h);
                     see0 = b.x;
                     see1 = b.y;
-                } else {
-                    // the tile's values have come too: whether it holds what fp16 does not
-                    wait(&bar.v_full[t & 1], t >> 1);
-                    __syncwarp();
-                    odd_k = *reinterpret_cast<const volatile uint32_t *>(odd_tile[t & 3][0]) != 0;
-                    odd_v = *reinterpret_cast<const volatile uint32_t *>(odd_tile[t & 3][1]) != 0;
+                } else if (used && *reinterpret_cast<const volatile uint32_t *>(odd_tile[t & 3][0]) != 0) {
+                    const int32_t at = max(row_at[j][r], 0);  // rows that are not there read a query that is
+                    add_odd_keys<D>(a.kn + new_row(s), a.ldkv, 64 * h, min(a.n - s * kKeys, 64 * h + 64),
+                                    a.q + (static_cast<int64_t>(w.b) * a.n + (at >> 16)) * a.ldq + static_cast<int64_t>(at & 0xffff) * D, q_scale[j][r].x, t_s);
                 }
                 if (!live) see0 = see1 = 0u;
-                const int64_t new_row = (static_cast<int64_t>(w.b) * a.n + s * kKeys) * a.ldkv + static_cast<int64_t>(w.hk) * D;
-                const int32_t new_rows = min(a.n - s * kKeys, kKeys);
-                if (odd_k && used) {
-                    const int32_t head = live ? row_at[j][r] & 0xffff : 0;  // rows that are not there read a query that is
-                    add_odd_keys<D>(a.kn + new_row, a.ldkv, 64 * h, min(new_rows, 64 * h + 64),
-                                    a.q + (static_cast<int64_t>(w.b) * a.n + node) * a.ldq + static_cast<int64_t>(head) * D, f, t_s);
-                }
                 float mx = -INFINITY;
                 if (used) {
                     if (!__all_sync(kFull, (see0 & see1) == kFull)) hide_keys(t_h, see0, see1);
@@ -672,10 +690,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
                     mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
                 }
                 // the row's maximum over both halves
-                half_max[j][buf][h][r] = mx;
+                half_max[j][n_s & 1u][h][r] = mx;  // the other one at every second tile
                 named_barrier_sync(1 + j, 256);
-                mx = fmaxf(mx, half_max[j][buf][h ^ 1][r]);
-                buf ^= 1;
+                mx = fmaxf(mx, half_max[j][n_s & 1u][h ^ 1][r]);
                 ++n_s;
                 mx = mx == -INFINITY ? mx : mx * mul;  // mul may underflow to 0
                 float corr = 1.0f;
@@ -686,7 +703,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
                     ref = nr;
                 }
                 const float sub = ref == -INFINITY ? 0.0f : -ref;
-                if (used && done > 0 && __any_sync(kFull, corr != 1.0f)) {
+                if (used && s > w.s0 + first_tile && __any_sync(kFull, corr != 1.0f)) {
                     // the scores' arrival says that the stream's earlier products are complete
 #pragma unroll 1
                     for (int c = 0; c < D / 32; ++c) {
@@ -699,13 +716,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
                     }
                     tmem_wait_st();
                 }
-                if (odd_v) {
-                    const int32_t key0 = s * kKeys;
-                    uint4 see = make_uint4(0u, 0u, 0u, 0u);
-                    if (live) see = make_uint4(new_seen(key0), new_seen(key0 + 32), new_seen(key0 + 64), new_seen(key0 + 96));
-                    if (used)
-                        add_odd_values(a.vn + new_row, a.ldkv, new_rows, see, mul, sub, t_s, t_o, h * (D / 2), (h + 1) * (D / 2));
-                    named_barrier_sync(1 + j, 256);  // both halves have read the scores that p overwrites
+                if (s < w.nt) {
+                    // whether the tile's values hold what fp16 does not
+                    wait(&bar.v_full[t & 1], t >> 1);
+                    __syncwarp();
+                    if (*reinterpret_cast<const volatile uint32_t *>(odd_tile[t & 3][1]) != 0) {
+                        const int32_t key0 = s * kKeys;
+                        uint4 see = make_uint4(0u, 0u, 0u, 0u);
+                        if (live) see = make_uint4(new_seen(key0), new_seen(key0 + 32), new_seen(key0 + 64), new_seen(key0 + 96));
+                        if (used)
+                            add_odd_values(a.vn + new_row(s), a.ldkv, min(a.n - s * kKeys, kKeys), see, mul, sub, t_s, t_o, h * (D / 2), (h + 1) * (D / 2));
+                        named_barrier_sync(1 + j, 256);  // both halves have read the scores that p overwrites
+                    }
                 }
                 if (used) l += __any_sync(kFull, fabsf(sub) > 1048576.0f) ? probabilities_in_steps(t_h, mul, sub) : probabilities(t_h, mul, sub);
                 tmem_wait_st();
@@ -713,9 +735,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.p_full[j]);
             }
-            gt += tiles;
+            gt += s1 - w.s0;
             // ---------------- the segment's output ----------------
-            if (done > 0) {
+            if (w.s0 + first_tile < s1) {
                 wait(&bar.o_done[j], n_o);
                 ++n_o;
             }
@@ -727,6 +749,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
             else named_barrier_sync(3, 512);
             tc_fence_after();
             const bool whole = w.s0 == 0 && w.s1 == w.unit;
+            const int32_t ur = both ? j * 128 + r : r;
             const int64_t slot = slot_of(w);
             const uint32_t o_first = tmem + lanes + 256u;
             float M, L, w0 = 1.0f, w1 = 0.0f;
@@ -805,7 +828,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
                 if (both) named_barrier_sync(1 + j, 256);
                 else named_barrier_sync(3, 512);
             }
-        } while (w.next(k, p));
+        } while (next_unit());
     }
 
     // ---------------- teardown ----------------
