@@ -535,10 +535,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
             const int32_t tiles = __shfl_sync(kFull, w.s1 - w.s0, 0);
             const uint32_t both = __shfl_sync(kFull, rows_of() > 128 ? 1 : 0, 0);
             const int32_t n = tiles << both;
-            auto issue_s = [&](int32_t q) -> bool {
+            auto key_tile = [&](int32_t q) -> bool {  // the first of a tile's jobs waits for both
+                const uint32_t t = gt + (q >> both);
+                return (both && (q & 1)) || wait_all(&bar.k_full[t & 1u], t >> 1);
+            };
+            auto issue_s = [&](int32_t q) {
                 const uint32_t t = gt + (q >> both), st = t & 1u, j = q & 1;
-                if (!wait_all(&bar.k_full[st], t >> 1)) return false;
-                tc_fence_after();
                 const uint64_t qd = q_desc + j * kStep, kd = k_desc + st * kStep;
                 const uint32_t d = tmem + j * 128u;
 #pragma unroll
@@ -548,13 +550,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
                 }
                 commit_to(&bar.s_full[j], leader);
                 if (!both || j) commit_to(&bar.k_empty[st], leader);  // the tile's last reader
-                return true;
             };
-            ok = wait_all(&bar.q_full[0], seg) && issue_s(0);
-            ok = ok && wait_all(&bar.q_full[1], seg) && (n < 2 || issue_s(1));
+            ok = wait_all(&bar.q_full[0], seg) && key_tile(0);
+            tc_fence_after();
+            if (ok) issue_s(0);
+            ok = ok && wait_all(&bar.q_full[1], seg) && (n < 2 || key_tile(1));
+            tc_fence_after();
+            if (ok && n >= 2) issue_s(1);
             for (int32_t q = 0; q < n && ok; ++q) {
                 const uint32_t t = gt + (q >> both), st = t & 1u, j = q & 1;
-                ok = wait_all(&bar.v_full[st], t >> 1) && wait_all(&bar.p_full[j], j ? jobs1 : jobs0);
+                // everything but p is waited for ahead of it: from its arrival the products of the
+                // job and the scores of the stream's next one follow each other
+                ok = ((both && j) || wait_all(&bar.v_full[st], t >> 1)) && (q + 2 >= n || key_tile(q + 2)) &&
+                     wait_all(&bar.p_full[j], j ? jobs1 : jobs0);
                 if (!ok) break;
                 if (j) ++jobs1;
                 else ++jobs0;
@@ -564,9 +572,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
 #pragma unroll
                 for (int kk = 0; kk < kKeys / 16; ++kk)  // keys 64 .. 127 lie 64 columns on
                     mma_ts(d, pa + (kk & 3) * 8u + (kk >> 2) * 64u, vd + kk * 128u, idesc_o, leader);
-                if (q + 2 >= n) commit_to(&bar.o_done[j], leader);
                 if (!both || j) commit_to(&bar.v_empty[st], leader);
-                if (q + 2 < n) ok = issue_s(q + 2);
+                if (q + 2 < n) issue_s(q + 2);
+                else commit_to(&bar.o_done[j], leader);
             }
             gt += tiles;
             ++seg;
@@ -652,25 +660,27 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
                 return (static_cast<int64_t>(w.b) * a.n + s * kKeys) * a.ldkv + static_cast<int64_t>(w.hk) * D;
             };
             float ref = -INFINITY, l = 0.0f;
-            const int32_t first_tile = both ? 0 : j, s1 = w.s1;
-            for (int32_t s = w.s0 + first_tile; s < s1; s += both ? 1 : 2) {
-                const uint32_t t = gt + (s - w.s0);
+            // the segment's tiles, those of new keys among them, and the stream's first and step
+            const int32_t tiles = w.s1 - w.s0, fresh = max(w.nt - w.s0, 0), from = both ? 0 : j, step = both ? 1 : 2;
+            for (int32_t i = from; i < tiles; i += step) {
+                const uint32_t t = gt + i;
                 // which of this half's keys the row sees
                 uint32_t see0 = 0u, see1 = 0u;
-                if (s < w.nt) {
-                    const int32_t key0 = s * kKeys + 64 * h;
+                if (i < fresh) {
+                    const int32_t key0 = (w.s0 + i) * kKeys + 64 * h;
                     see0 = new_seen(key0);
                     see1 = new_seen(key0 + 32);
                 }
                 wait(&bar.s_full[j], n_s);
                 __syncwarp();
                 tc_fence_after();
-                if (s >= w.nt) {
+                if (i >= fresh) {
                     const uint2 b = *reinterpret_cast<const uint2 *>(key_bits[t & 3] + 8 * h);
                     see0 = b.x;
                     see1 = b.y;
                 } else if (used && *reinterpret_cast<const volatile uint32_t *>(odd_tile[t & 3][0]) != 0) {
                     const int32_t at = max(row_at[j][r], 0);  // rows that are not there read a query that is
+                    const int32_t s = w.s0 + i;
                     add_odd_keys<D>(a.kn + new_row(s), a.ldkv, 64 * h, min(a.n - s * kKeys, 64 * h + 64),
                                     a.q + (static_cast<int64_t>(w.b) * a.n + (at >> 16)) * a.ldq + static_cast<int64_t>(at & 0xffff) * D, q_scale[j][r].x, t_s);
                 }
@@ -679,7 +689,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
                 if (used) {
                     if (!__all_sync(kFull, (see0 & see1) == kFull)) hide_keys(t_h, see0, see1);
                     float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll 1
+#pragma unroll
                     for (int c = 0; c < 2; ++c) {
                         uint32_t v[32];
                         tmem_ld_32(t_h + 32 * c, v);
@@ -703,7 +713,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
                     ref = nr;
                 }
                 const float sub = ref == -INFINITY ? 0.0f : -ref;
-                if (used && s > w.s0 + first_tile && __any_sync(kFull, corr != 1.0f)) {
+                if (used && i > from && __any_sync(kFull, corr != 1.0f)) {
                     // the scores' arrival says that the stream's earlier products are complete
 #pragma unroll 1
                     for (int c = 0; c < D / 32; ++c) {
@@ -716,12 +726,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
                     }
                     tmem_wait_st();
                 }
-                if (s < w.nt) {
+                if (i < fresh) {
                     // whether the tile's values hold what fp16 does not
                     wait(&bar.v_full[t & 1], t >> 1);
                     __syncwarp();
                     if (*reinterpret_cast<const volatile uint32_t *>(odd_tile[t & 3][1]) != 0) {
-                        const int32_t key0 = s * kKeys;
+                        const int32_t s = w.s0 + i, key0 = s * kKeys;
                         uint4 see = make_uint4(0u, 0u, 0u, 0u);
                         if (live) see = make_uint4(new_seen(key0), new_seen(key0 + 32), new_seen(key0 + 64), new_seen(key0 + 96));
                         if (used)
@@ -735,9 +745,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.p_full[j]);
             }
-            gt += s1 - w.s0;
+            gt += tiles;
             // ---------------- the segment's output ----------------
-            if (w.s0 + first_tile < s1) {
+            if (from < tiles) {
                 wait(&bar.o_done[j], n_o);
                 ++n_o;
             }
