@@ -155,15 +155,8 @@ static __device__ __noinline__ uint4 without_odd(uint4 v) {
     }
     return v;
 }
-// Eight bf16 to fp16 in the order of the tiles; what fp16 cannot hold becomes 0 and sets `odd`.
-__device__ __forceinline__ uint4 convert8(uint4 v, bool &odd) {
-    auto abs2 = [](uint32_t x) { return x & 0x7fff7fffu; };
-    auto b2 = [](uint32_t x) { return *reinterpret_cast<const __nv_bfloat162 *>(&x); };
-    const __nv_bfloat162 big = __hmax2_nan(__hmax2_nan(b2(abs2(v.x)), b2(abs2(v.y))), __hmax2_nan(b2(abs2(v.z)), b2(abs2(v.w))));
-    if (!(__low2float(big) <= 65504.0f && __high2float(big) <= 65504.0f)) {
-        odd = true;
-        v = without_odd(v);
-    }
+// Eight bf16 to fp16 in the order of the tiles.
+__device__ __forceinline__ uint4 convert8(uint4 v) {
     return make_uint4(pack_f16(bf_lo(v.x), bf_lo(v.z)), pack_f16(bf_hi(v.x), bf_hi(v.z)), pack_f16(bf_lo(v.y), bf_lo(v.w)),
                       pack_f16(bf_hi(v.y), bf_hi(v.w)));
 }
@@ -406,9 +399,23 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
                         __syncwarp();
                     }
                     uint8_t *dst = stages + st * S::kTileBytes + (ch >> 3) * (kKeys * 128);
+                    auto store = [&](int32_t i, uint4 x) {
+                        *reinterpret_cast<uint4 *>(dst + sw128((sub * kBatch + i) * 4 * kRowsWarp + first, ch & 7)) = x;
+                    };
+                    // the largest magnitude of the results is infinite or NaN where fp16 does not hold an element
+                    __half2 big = as_h2(0u);
 #pragma unroll
-                    for (int i = 0; i < kBatch; ++i)
-                        *reinterpret_cast<uint4 *>(dst + sw128((sub * kBatch + i) * 4 * kRowsWarp + first, ch & 7)) = convert8(v[i], odd);
+                    for (int i = 0; i < kBatch; ++i) {
+                        const uint4 x = convert8(v[i]);
+                        big = __hmax2_nan(__hmax2_nan(__hmax2_nan(big, __habs2(as_h2(x.x))), __habs2(as_h2(x.y))),
+                                          __hmax2_nan(__habs2(as_h2(x.z)), __habs2(as_h2(x.w))));
+                        store(i, x);
+                    }
+                    if (!(__low2float(big) <= 65504.0f && __high2float(big) <= 65504.0f)) {
+                        odd = true;
+#pragma unroll
+                        for (int i = 0; i < kBatch; ++i) store(i, convert8(without_odd(v[i])));
+                    }
                     if (at + 1 < last * kBatches) load((at + 1) * (kKeys / kBatches));
                     if (sub == kBatches - 1) {
                         const bool any = __any_sync(kFull, odd);
