@@ -350,18 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(kFull, tmem_base, 0);
     const Walk &w = walks[warp];
-    auto next_unit = [&]() -> bool {
-        __syncwarp();  // every lane is through with the last
-        int more = 0;
-        if (lane == 0) {
-            Walk n = walks[warp];
-            more = n.next(k, place);
-            walks[warp] = n;
-        }
-        more = __shfl_sync(kFull, more, 0);
-        __syncwarp();
-        return more != 0;
-    };
+    auto next_unit = [&]() { return kv4_next(k, place, walks[warp]); };
     auto wait = [&](uint64_t *b, uint32_t parity) -> bool { return kv4_wait(b, parity, abort_flag); };
     auto rows_of = [&]() { return min(kKv4TcRows, k.Mq - w.qt * kKv4TcRows); };  // rows of the unit
 

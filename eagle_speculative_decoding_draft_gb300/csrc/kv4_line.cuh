@@ -316,6 +316,20 @@ struct Walk {
     }
 };
 
+// On to the next unit of a walk in shared memory that the warp's lanes read; false behind the last.
+__device__ __forceinline__ bool kv4_next(const Kv4Args &k, const Place &p, Walk &walk) {
+    __syncwarp();  // every lane is through with the last
+    int more = 0;
+    if ((threadIdx.x & 31) == 0) {
+        Walk w = walk;
+        more = w.next(k, p);
+        walk = w;
+    }
+    more = __shfl_sync(kFull, more, 0);
+    __syncwarp();
+    return more != 0;
+}
+
 // What CTA blockIdx.x leaves for the merge.
 __device__ __forceinline__ Kv4Share share_of(const Walk &w) {
     return Kv4Share{w.s0 == 0 ? 0 : (w.s1 == w.unit ? 1 : 2), w.b, w.hk, w.qt};
