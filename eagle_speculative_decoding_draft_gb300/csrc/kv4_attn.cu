@@ -25,6 +25,12 @@
 // Scores are formed transposed (16 keys on the MMA's M side, 8 query rows on N), so few query rows
 // waste no MMA rows, and the accumulators turn into the value product's operand by movmatrix.
 //
+// Measured: 64 trees of 8 nodes, 32 heads of 128 over 1024 tokens each (352 MB) in 115 us, 0.45 of the
+// measured copy rate; 16 requests of 1 .. 65536 tokens under groups of 8 heads in 170 us, 0.58 of it.
+// Three CTAs of 128 registers a thread stay on an SM; it issues in 41 % of the cycles, waiting for
+// memory in the new keys' part and for fixed latencies in the rest.  Slower, measured: warps that copy
+// their own chunks, with four CTAs an SM or tiles of 32 keys (127 and 118 us against 115).
+//
 // kv4_line.cuh: how the work is split.  kv4_attn_tc.cu: the kernel for many query rows.
 #include <algorithm>
 #include <mutex>
@@ -39,7 +45,7 @@ constexpr int kTile = 64;       // keys of a tile: a chunk of 16 for each of the
 constexpr int kWarps = 4;       // warps that multiply
 constexpr int kThreads = kWarps * 32 + 32;  // and one that copies
 constexpr int kStages = 5;
-constexpr int kMinTiles = 2;    // tiles a CTA takes at least
+constexpr int kMinTiles = 2;    // tiles a CTA takes at least: a single tile's CTA is merging more than work
 constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -660,7 +666,8 @@ __global__ void __launch_bounds__(kThreads, Shape<G, NQ>::kBlocks) kv4_attention
 
 // Units that several CTAs worked on: block (c, .) merges the unit that CTA c is the second to work on.
 // o = sum_i w_i O_i / sum_i w_i l_i, w_i = 2^(m_i - max m), over its CTAs in order.  A warp a row: a lane
-// a part for the weights, then four dims a lane over all parts.
+// a part for the weights, then four dims a lane over all parts.  Bound by latency (two dependent
+// reads from L2): about 4 us.
 constexpr int kMergeRows = 4;
 __global__ void __launch_bounds__(kMergeRows * 32) kv4_merge_kernel(const __grid_constant__ Kv4Args k) {
     pdl_wait();
@@ -730,7 +737,10 @@ struct Variant {
 
 template <int G>
 Variant variant_of(int32_t mq) {
-    // query rows a unit takes: 8, 16 or 32
+    // Query rows a unit takes: 8, 16 or, with head_dim 32 or 96, 32.  From 17 rows on the tensor
+    // cores of tcgen05 take over where its layouts allow it (head_dim 64 and 128).  32 requests, 8 kv
+    // heads of 128: 16 rows take 40 us over 1024 tokens and 149 over 8192 here, 49 and 213 there; 32
+    // rows 96 us over 1024 tokens here, 47 there.
     if (mq <= 8) return Variant{8, kThreads, Shape<G, 1>::kTotal, kv4_attention_kernel<G, 1>};
     if (mq <= 16) return Variant{16, kThreads, Shape<G, 2>::kTotal, kv4_attention_kernel<G, 2>};
     if constexpr (G == 2 || G == 4) return Variant{kKv4TcRows, 0, 0, nullptr};
@@ -809,6 +819,9 @@ cudaError_t launch_kv4_attention(const Kv4Attention &a, cudaStream_t st) {
     const int64_t tile = v.kernel ? kTile : kKv4TcTile;
     k.tile_shift = v.kernel ? 6 : 7;
     k.min_tiles = v.kernel ? kMinTiles : 1;
+    // cuts move to a unit's end from so many tiles: a unit cut in two writes and reads partial sums of
+    // all its rows.  32 requests of 64 nodes on tcgen05: 89 us with 0, 82 with 2, 66 with 5 and 8;
+    // the 2047-token piece 696, 696, 688 and 697
     k.snap = v.kernel ? 1 : 5;
     k.scale2 = kLog2e / sqrtf(static_cast<float>(G * kKv4Group));
     const int32_t full = grid_of(*d, G, v);

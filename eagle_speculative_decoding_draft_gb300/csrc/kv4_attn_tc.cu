@@ -11,15 +11,29 @@
 //                    TMEM over the scores it came from, the running maximum and sum in fp32.  p is
 //                    held below 2^15 and its reference only moved (and O rescaled) when a tile's
 //                    maximum passes that; the halves agree on the maximum through shared memory.
-//   warps 16-23      fill the tiles: codes become fp16 values m + s c (one fused multiply-add: half
-//                    an fp16 step, 2^-11 relative); new keys and values are converted from bf16
-//                    (exact but for magnitudes below 2^-14).
+//                    Warps whose 32 rows lie behind the unit's last skip the softmax.
+//   warps 16-19, 20-23  fill the key and the value tiles: codes become fp16 values m + s c (one fused
+//                    multiply-add: half an fp16 step, 2^-11 relative); new keys and values are
+//                    converted from bf16 (exact but for magnitudes below 2^-14).
 //   warp 24          issues the MMAs: S = Q K^T (128 x 128 x D, operands in shared memory) and
 //                    O += P V (P from TMEM, V as stored: the MN-major B operand).  The order S0 S1
-//                    [P0] O0 S0' [P1] O1 S1' ... keeps one stream's MMAs under the other's softmax.
-//                    The warp stays whole and one lane's instructions count, so that descriptors
-//                    are in uniform registers (moving them there cost 100 cycles an MMA).
-//   warp 25          copies the codes of cached tiles into a ring of two halves of tiles
+//                    [P0] O0 S0' [P1] O1 S1' ... keeps one stream's MMAs under the other's softmax,
+//                    and from a p's arrival on nothing else is waited for.  The warp stays whole and
+//                    one lane's instructions count, so that descriptors are in uniform registers
+//                    (moving them there cost 100 cycles an MMA).
+//   warp 25          copies the codes of cached tiles, one tile's keys and one tile's values at a time
+//
+// What bounds it: instruction issue and the chain of one stream's tile (scores, two passes, p, product):
+// the next 2047 tokens of two requests over 4096 cached ones (64 heads, 8 kv heads of 128)
+// take 688 us, 0.53 of the measured bf16 matrix rate; 32 requests of 65 nodes (260 rows,
+// a full unit and one of 4 rows each) over 1024 tokens 108 us.  Registers are what it is short of:
+// 26 warps leave 72 a thread, and what is spilled goes to L2, as shared memory takes all of L1: with
+// 112 bytes spilled the first took 822 us, with the walk over the units in shared memory and 16
+// bytes 784.  So the masks and the elements that fp16 does not hold have functions of their own.
+// Slower, measured: scores kept in registers from the first pass to the second with registers moved
+// from the other warps (setmaxnreg; 855 us against 739), a second issuing warp (895 against 822:
+// the streams then work in step), a second copying warp and an L2 prefetch (708 against 688).
+//
 // Queries are scaled by a power of two so that a row's largest element is 2^9..2^10 (exact, as in
 // kv4_attn.cu).  Within 8 neighbouring dims the tiles hold them in the order 0 4 1 5 2 6 3 7, in
 // which masking a word of codes leaves them; queries are stored in the same order and the output's
@@ -312,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
             mbar_init(&bar.v_empty[i], 1);
             mbar_init(&bar.q_full[i], 8);
             mbar_init(&bar.s_full[i], 1);
-            mbar_init(&bar.p_full[i], 8);  // by warps: 256 arrivals take their turns on the barrier's word
+            mbar_init(&bar.p_full[i], 8);
             mbar_init(&bar.o_done[i], 1);
         }
         for (int i = 0; i < kRaw; ++i) {

@@ -81,7 +81,7 @@ class KV4Cache:
         self._c = _lib.KV4CacheStruct(kv_heads, head_dim, page_size, num_pages, max_pages, None, None, None)
         self._ref = ctypes.byref(self._c)
         nbytes = self._lib.eagle_kv4_pages_bytes(self._ref)
-        if nbytes == 0 or batch < 0:
+        if nbytes == 0 or batch < 1:
             raise ValueError("unusable 4-bit cache sizes")
         if pages is None:
             pages = torch.empty(nbytes, dtype=torch.uint8, device=self.device)

@@ -554,10 +554,10 @@ EAGLE_API size_t eagle_kv4_pages_bytes(const eagle_kv4_cache *cache);
  *              EAGLE_ERR_DEVICE_BOUNDS and leaves the request as it is.
  * lengths[b] becomes start[b] plus the last written slot's number plus one (start[b] if there is
  * none), at most the capacity; slots beyond the capacity latch EAGLE_ERR_DEVICE_BOUNDS.  Positions
- * other than those written keep what they hold.  A request's slots are written by one launch; a
- * second, small one sets the lengths when they are also the starts and a request needs several
- * blocks.  d_start must not overlap cache->lengths other than being it.
- * Errors: INVALID_ARG, CUDA.
+ * other than those written keep what they hold.  The slots are written by one launch; where the
+ * lengths are also the starts, a second, small one sets them.  d_start must not overlap
+ * cache->lengths other than being it.  Calls that write the same request must not overlap.
+ * Errors: INVALID_ARG, CUDA; UNSUPPORTED where batch * kv_heads * chunks of 16 slots passes 2^31.
  */
 EAGLE_API eagle_status eagle_kv4_append(const eagle_kv4_cache *cache, int32_t batch, int32_t src_rows,
                                         int32_t slots, const void *d_k, const void *d_v, int64_t ld,
@@ -570,7 +570,8 @@ EAGLE_API eagle_status eagle_kv4_append(const eagle_kv4_cache *cache, int32_t ba
  * its codes stand for, rounded to `dtype` (EAGLE_F32 or EAGLE_BF16) from fp32.
  *   d_k, d_v   [batch][rows][kv_heads][head_dim], 16-byte aligned.  Rows at or behind the request's
  *              length are left as they are.
- * Errors: INVALID_ARG, CUDA; a negative start latches EAGLE_ERR_DEVICE_BOUNDS and reads nothing.
+ * Errors: INVALID_ARG, CUDA; UNSUPPORTED where batch * kv_heads * chunks of 16 rows passes 2^31; a
+ * negative start latches EAGLE_ERR_DEVICE_BOUNDS and reads nothing.
  */
 EAGLE_API eagle_status eagle_kv4_read(const eagle_kv4_cache *cache, int32_t batch, int32_t rows,
                                       const int32_t *d_start, void *d_k, void *d_v, eagle_dtype dtype,
@@ -596,7 +597,8 @@ EAGLE_API eagle_status eagle_kv4_read(const eagle_kv4_cache *cache, int32_t batc
  * run at the same time (other streams, graphs replayed side by side) need workspaces of their own.
  * The size depends on the current device, not on the batch or the lengths.  Results do not depend on
  * what else runs, and are the same in every call with the same lengths.
- * Errors: INVALID_ARG, CUDA.
+ * Errors: INVALID_ARG, CUDA; UNSUPPORTED where batch * kv_heads * tiles of query rows (8 to 256) *
+ * tiles of keys (64 or 128) of a full cache passes 2^31.
  */
 EAGLE_API size_t eagle_kv4_attention_workspace_bytes(const eagle_kv4_cache *cache, int32_t nodes,
                                                      int32_t heads);

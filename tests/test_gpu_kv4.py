@@ -277,6 +277,15 @@ ATTENTION = [
     (1, 1, 8, 8, 128, 64, [50000], "causal"),
     (1, 70, 32, 4, 128, 64, [9000], "tree"),         # 560 rows, split units of many rows
     (300, 1, 2, 1, 64, 16, [i % 37 for i in range(300)], "causal"),  # more requests than threads
+    (40, 8, 8, 2, 128, 16, [i * 131 % 700 for i in range(40)], "tree"),     # 32 rows of more than 32 requests
+    (35, 80, 8, 2, 64, 32, [i * 53 % 300 for i in range(35)], "causal"),    # and 320 rows: units of different lengths
+    (900, 17, 1, 1, 64, 16, [i % 21 for i in range(900)], "causal"),        # 17 rows, more requests than threads
+    (2, 128, 1, 1, 128, 64, [128, 127], "causal"),   # rows and keys that fill their tiles
+    (3, 129, 1, 1, 128, 16, [0, 255, 257], "tree"),  # one row and one key more
+    (1, 256, 1, 1, 64, 1024, [1025], "causal"),
+    (1, 300, 16, 2, 128, 64, [100], "tree"),         # ten tiles of query rows
+    (1, 4097, 1, 1, 64, 16, [5], "causal"),          # the most nodes
+    (1, 4097, 1, 1, 32, 16, [5], "causal"),
 ]
 
 
@@ -464,6 +473,80 @@ def test_two_graphs_side_by_side(dev):
     assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1])
 
 
+@pytest.mark.parametrize("n,H,D", [(3, 8, 128), (7, 6, 96), (30, 8, 128), (130, 4, 64)])
+def test_calls_write_their_outputs_and_workspace_only(dev, n, H, D):
+    case = (3, n, H, 2, D, 32, [900, 0, 77], "tree")
+    c, kc, vc, q, kn, vn, mask = build(case, 13)
+    want = c.attention(q, kn, vn, mask=mask)
+    size, nbytes = q.numel(), c.attention_workspace_bytes(n, H)
+    out = torch.full((size + 512,), 7.0, dtype=torch.bfloat16, device="cuda")
+    ws = torch.full((nbytes + 512,), 0xA5, dtype=torch.uint8, device="cuda")
+    pages, table, lengths = c.pages.clone(), c.table.clone(), c.lengths.clone()
+    got = c.attention(q, kn, vn, mask=mask, out=out[256:256 + size].view(q.shape), workspace=ws[256:256 + nbytes])
+    assert torch.equal(got, want)
+    assert torch.all(out[:256] == 7.0) and torch.all(out[256 + size:] == 7.0)
+    assert torch.all(ws[:256] == 0xA5) and torch.all(ws[256 + nbytes:] == 0xA5)
+    assert torch.equal(c.pages, pages) and torch.equal(c.table, table) and torch.equal(c.lengths, lengths)
+    row = 2 * D
+    back = torch.full((2, 3 * 901 * row + 512), 7.0, dtype=torch.bfloat16, device="cuda")
+    k, v = (back[i, 256:256 + 3 * 901 * row].view(3, 901, 2, D) for i in range(2))
+    c.read(out=(k, v))
+    assert torch.all(back[:, :256] == 7.0) and torch.all(back[:, 256 + 3 * 901 * row:] == 7.0)
+    for b, t in enumerate(case[6]):
+        assert torch.all(k[b, t:] == 7.0) and torch.all(v[b, t:] == 7.0)
+    assert torch.equal(c.pages, pages)
+
+
+def test_refusals(dev):
+    from eagle_speculative_decoding_draft_gb300 import KV4Cache
+    for kw in (dict(batch=0), dict(head_dim=80), dict(page_size=24), dict(num_pages=0), dict(device="cpu"),
+               dict(pages=torch.zeros(64, dtype=torch.uint8, device="cuda"))):
+        with pytest.raises(ValueError):
+            KV4Cache(**dict(dict(batch=2, kv_heads=2, head_dim=64, num_pages=4, max_pages=2, page_size=16), **kw))
+    c = make_cache(2, 2, 64, 32, 16)
+    g = gen(1)
+    k, v, q = rows(g, 2, 3, 2, 64), rows(g, 2, 3, 2, 64), rows(g, 2, 3, 4, 64)
+    mask, one = i32([[[1], [3], [7]]] * 2), i32([3, 3])
+    cases = [
+        (ValueError, lambda: c.append(k[:1], v[:1])), (ValueError, lambda: c.append(k, v[:, :2])),
+        (ValueError, lambda: c.append(k[..., :32], v[..., :32])), (TypeError, lambda: c.append(k.float(), v.float())),
+        (ValueError, lambda: c.append(k.cpu(), v.cpu())), (ValueError, lambda: c.append(k.transpose(2, 3), v.transpose(2, 3))),
+        (TypeError, lambda: c.append(k, v, count=one.long())), (ValueError, lambda: c.append(k, v, count=one[:1])),
+        (ValueError, lambda: c.append(k, v, start=one.cpu())), (ValueError, lambda: c.append(k, v, select=one)),
+        (ValueError, lambda: c.append(k, v, select=i32([[0, 1]] * 4)[::2])),
+        (ValueError, lambda: c.read(out=(k, v[:, :2]))), (ValueError, lambda: c.read(out=(k.half(), v.half()))),
+        (ValueError, lambda: c.read(rows=4, out=(k, v))), (ValueError, lambda: c.read(start=one[:1])),
+        (ValueError, lambda: c.attention(q[:1], k, v)), (ValueError, lambda: c.attention(q[:, :, :3], k, v)),
+        (ValueError, lambda: c.attention(q[:, :0], k[:, :0], v[:, :0])), (TypeError, lambda: c.attention(q.float(), k, v)),
+        (ValueError, lambda: c.attention(q, k)), (ValueError, lambda: c.attention(q, mask=mask)),
+        (ValueError, lambda: c.attention(q, k[:, :2], v[:, :2])), (ValueError, lambda: c.attention(q, k, v, mask=mask[:1])),
+        (TypeError, lambda: c.attention(q, k.float(), v.float())), (TypeError, lambda: c.attention(q, k, v, mask=mask.long())),
+        (ValueError, lambda: c.attention(q, k, v, out=q[:, :2])),
+        (ValueError, lambda: c.attention(q, k, v, workspace=torch.zeros(16, dtype=torch.uint8, device="cuda"))),
+    ]
+    for i, (error, call) in enumerate(cases):
+        with pytest.raises(error):
+            call()
+            pytest.fail(f"call {i} was not refused")
+    c.status()
+    assert c.lengths.tolist() == [0, 0]
+    c.append(k, v)
+    assert torch.equal(c.attention(q, k, v), c.attention(q, k, v, mask=mask))  # the same cache still works
+
+
+def test_work_beyond_32_bits_is_refused(dev):
+    """Before anything is launched: the sizes alone, whatever the pointers hold."""
+    import ctypes
+    from eagle_speculative_decoding_draft_gb300 import _lib
+    lib, P = _lib.load(), ctypes.c_void_p
+    c = _lib.KV4CacheStruct(1024, 128, 16, 16, 1 << 20, 256, 256, 256)
+    assert lib.eagle_kv4_append(ctypes.byref(c), 1 << 22, 1, 1, P(256), P(256), 1 << 17, None, None, None, None, None) == 2
+    assert lib.eagle_kv4_read(ctypes.byref(c), 1 << 22, 1, None, P(256), P(256), 1, None, None) == 2
+    need = lib.eagle_kv4_attention_workspace_bytes(ctypes.byref(c), 1, 1024)
+    assert lib.eagle_kv4_attention(ctypes.byref(c), 1 << 6, 1, 1024, P(256), 1 << 17, None, None, 0, None, P(256), P(256), need,
+                                   None, None) == 2
+
+
 # ------------------------------------------------------------------------------------------------
 # the decoder layer and a round of drafting
 # ------------------------------------------------------------------------------------------------
@@ -501,6 +584,21 @@ def test_decoder_layer_over_the_cache(dev, case):
     _, kb, vb = lay(g(w["x"]), g(w["k_cache"]) if P else None, g(w["v_cache"]) if P else None, pos_d, mask_d, new_kv=True)
     assert torch.equal(kn, kb) and torch.equal(vn, vb)
     assert torch.equal(lay.kv4(g(w["x"]), c, pos_d, mask_d), out)
+
+
+def test_decoder_layer_without_a_mask_is_the_next_piece_of_a_prompt(dev):
+    from eagle_speculative_decoding_draft_gb300.engine import DecoderLayer
+    B, n, P, h, H, Hk, D, I = 2, 37, 50, 256, 8, 2, 64, 512
+    w, d = layer(B=B, n=n, P=P, h=h, H=H, Hk=Hk, D=D, I=I, seed=4)
+    g = lambda t: t.to(dev).contiguous()
+    lay = DecoderLayer(g(w["w_qkv"]), g(w["w_o"]), g(w["w_norm"]), g(w["w_gu"]), g(w["w_d"]), H, Hk)
+    c = make_cache(B, Hk, D, P, 16)
+    c.append(g(w["k_cache"]), g(w["v_cache"]))
+    pos = i32([[P + i for i in range(n)]] * B)
+    chain = tree_mask(np.arange(n) - 1)  # every node's parent is the one before it
+    chain = torch.from_numpy(np.broadcast_to(chain, (B, n, 2)).copy().view(np.int32)).to(dev)
+    assert torch.equal(lay.kv4(g(w["x"]), c, pos), lay.kv4(g(w["x"]), c, pos, chain))
+    c.status()
 
 
 def test_rounds_of_drafting_over_the_cache(dev):
