@@ -97,7 +97,7 @@ struct Shape {
     static constexpr uint32_t kMerge = kRing + kStages * kStageBytes;
     static constexpr uint32_t kMl = kMerge + kWarps * kRows * kMergeStride * 4;
     static constexpr uint32_t kTotal = kMl + kWarps * kRows * 8;
-    static constexpr int kBlocks = NQ == 1 ? 3 : (NQ == 2 ? 2 : 1);
+    static constexpr int kBlocks = NQ == 1 ? 3 : 2;
 };
 
 template <int G, int NQ>
@@ -737,14 +737,12 @@ struct Variant {
 
 template <int G>
 Variant variant_of(int32_t mq) {
-    // Query rows a unit takes: 8, 16 or, with head_dim 32 or 96, 32.  From 17 rows on the tensor
-    // cores of tcgen05 take over where its layouts allow it (head_dim 64 and 128).  32 requests, 8 kv
-    // heads of 128: 16 rows take 40 us over 1024 tokens and 149 over 8192 here, 49 and 213 there; 32
-    // rows 96 us over 1024 tokens here, 47 there.
+    // Query rows a unit takes: 8 or 16; from 17 rows on tcgen05 takes over.  32 requests, 8 kv heads of
+    // 128: 16 rows take 40 us over 1024 tokens and 149 over 8192 here, 49 and 213 there; 32 rows 96 us
+    // over 1024 tokens here (with 32 rows a unit), 47 there.
     if (mq <= 8) return Variant{8, kThreads, Shape<G, 1>::kTotal, kv4_attention_kernel<G, 1>};
     if (mq <= 16) return Variant{16, kThreads, Shape<G, 2>::kTotal, kv4_attention_kernel<G, 2>};
-    if constexpr (G == 2 || G == 4) return Variant{kKv4TcRows, 0, 0, nullptr};
-    else return Variant{32, kThreads, Shape<G, 4>::kTotal, kv4_attention_kernel<G, 4>};
+    return Variant{kKv4TcRows, 0, 0, nullptr};
 }
 Variant variant(int32_t G, int32_t mq) {
     switch (G) {
@@ -757,7 +755,7 @@ Variant variant(int32_t G, int32_t mq) {
 
 struct Device {
     int32_t sms = 0;
-    int32_t blocks[5][3] = {};  // CTAs an SM holds, by groups and rows
+    int32_t blocks[5][2] = {};  // CTAs an SM holds, by groups and rows
 };
 std::mutex g_mu;
 Device g_dev[64];
@@ -772,9 +770,8 @@ const Device *device_now() {
     int sms = 0;
     if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1) return nullptr;
     for (int g = 1; g <= 4; ++g)
-        for (int i = 0; i < 3; ++i) {
+        for (int i = 0; i < 2; ++i) {
             const Variant v = variant(g, 8 << i);
-            if (!v.kernel) continue;
             int n = 0;
             if (cudaFuncSetAttribute(v.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(v.smem)) != cudaSuccess ||
                 cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, v.kernel, v.threads, v.smem) != cudaSuccess || n < 1)
@@ -788,7 +785,7 @@ const Device *device_now() {
 
 int32_t grid_of(const Device &d, int32_t G, const Variant &v) {
     if (!v.kernel) return d.sms;
-    return d.sms * d.blocks[G][v.rows == 8 ? 0 : (v.rows == 16 ? 1 : 2)];
+    return d.sms * d.blocks[G][v.rows == 8 ? 0 : 1];
 }
 
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }

@@ -40,6 +40,9 @@
 // columns are put right as they leave.
 // New keys or values that fp16 cannot hold (above 65504, infinite, NaN) count as 0 in the tiles, and
 // the rows that see them add their terms one by one: nothing hidden reaches a row, whatever it is.
+// Tiles are made of blocks of 64 dims; with head_dim 32 and 96 half of the last one lies idle and the
+// MMAs stop before it (1000 tokens of two prompts over 4096 cached ones, 32 heads of 96: 179 us, where
+// the register kernel with 32 rows a unit took 1935).
 // TMEM: S0 S1 O0 O1, 128 columns each (O uses D).  Every wait is bounded.
 #include <type_traits>
 
@@ -59,7 +62,10 @@ constexpr uint32_t kTmemCols = 512;
 template <int G>
 struct Tc {
     static constexpr int D = G * kKv4Group;
-    static constexpr uint32_t kTileBytes = kKeys * D * 2;  // D / 64 blocks of [128 rows][128 bytes]
+    // a tile: blocks of [128 rows][128 bytes], 64 dims each (half of the last one idle with an odd G)
+    static constexpr uint32_t kTileBytes = (D + 63) / 64 * (kKeys * 128u);
+    // lanes that take a bf16 row's 16-byte pieces: kPer, of which the first kPieces have one
+    static constexpr int kPieces = D / 8, kPer = G == 3 ? 16 : kPieces, kRowsWarp = 32 / kPer;
     static constexpr uint32_t kQ = 0;                      // two streams
     static constexpr uint32_t kK = kQ + 2 * kTileBytes;    // two stages
     static constexpr uint32_t kV = kK + 2 * kTileBytes;    // two stages
@@ -377,16 +383,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
         do {
             int32_t s = w.s0;
             if (s < w.nt) {  // new keys or values, the next ones' loads under way
-                constexpr int kPer = D / 8, kRowsWarp = 32 / kPer, kBatch = 8;  // pieces a row; rows a warp takes at once
+                constexpr int kPer = S::kPer, kRowsWarp = S::kRowsWarp;
+                constexpr int kBatch = kKeys / (4 * kRowsWarp) < 8 ? kKeys / (4 * kRowsWarp) : 8;
                 constexpr int kBatches = kKeys / (4 * kRowsWarp * kBatch);
                 const int32_t ch = lane % kPer, first = fw * kRowsWarp + lane / kPer;
+                const bool mine = S::kPieces == kPer || ch < S::kPieces;
                 const __nv_bfloat16 *src = (half ? a.vn : a.kn) + static_cast<int64_t>(w.b) * a.n * a.ldkv + static_cast<int64_t>(w.hk) * D + ch * 8;
                 uint4 v[kBatch];
                 auto load = [&](int32_t row0) {
 #pragma unroll
                     for (int i = 0; i < kBatch; ++i) {
                         const int32_t row = row0 + i * 4 * kRowsWarp + first;
-                        v[i] = row < a.n ? *reinterpret_cast<const uint4 *>(src + row * a.ldkv) : make_uint4(0, 0, 0, 0);
+                        v[i] = mine && row < a.n ? *reinterpret_cast<const uint4 *>(src + row * a.ldkv) : make_uint4(0, 0, 0, 0);
                     }
                 };
                 load(s * kKeys);
@@ -403,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
                     }
                     uint8_t *dst = stages + st * S::kTileBytes + (ch >> 3) * (kKeys * 128);
                     auto store = [&](int32_t i, uint4 x) {
-                        *reinterpret_cast<uint4 *>(dst + sw128((sub * kBatch + i) * 4 * kRowsWarp + first, ch & 7)) = x;
+                        if (mine) *reinterpret_cast<uint4 *>(dst + sw128((sub * kBatch + i) * 4 * kRowsWarp + first, ch & 7)) = x;
                     };
                     // the largest magnitude of the results is infinite or NaN where fp16 does not hold an element
                     __half2 big = as_h2(0u);
@@ -452,17 +460,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
                     const uint8_t *part = src + (group >> 1) * S::kPart;
                     const int32_t slot = (group & 1) * 8 + slot8;
                     const int32_t here = max(0, min(8, static_cast<int32_t>(raw_keys[half][group >> 1]) - 8 * (group & 1)));
-                    if constexpr (G == 4) {
-                        const uint4 cv = *reinterpret_cast<const uint4 *>(part + slot * 64 + q * 16);
-                        const uint4 mv = *reinterpret_cast<const uint4 *>(part + 1024 + slot * 16);
-                        c[i][0] = cv.x, c[i][1] = cv.y, c[i][2] = cv.z, c[i][3] = cv.w;
-                        sm[i][0] = mv.x, sm[i][1] = mv.y, sm[i][2] = mv.z, sm[i][3] = mv.w;
-                    } else {
-                        const uint2 cv = *reinterpret_cast<const uint2 *>(part + slot * 32 + q * 8);
-                        const uint2 mv = *reinterpret_cast<const uint2 *>(part + 512 + slot * 8);
-                        c[i][0] = cv.x, c[i][1] = cv.y;
-                        sm[i][0] = mv.x, sm[i][1] = mv.y;
-                    }
+                    load_words<G>(part + slot * 16 * G + q * 4 * G, c[i]);
+                    load_words<G>(part + 256 * G + slot * 4 * G, sm[i]);
                     if (!half && lane == 0) key_bits[gt & 3][group] = static_cast<uint8_t>((1u << here) - 1u);
                     if (t8 >= here) {  // rows that are not there hold 0
 #pragma unroll
@@ -475,10 +474,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
                 __syncwarp();
 #pragma unroll
                 for (int32_t i = 0; i < 4; ++i) {
-                    if (half) {  // two 16-bit words of four dims each to the keys' words of eight
+                    if (half) {  // two 16-bit words of four dims each, G apart, to the keys' words of eight
                         uint32_t x[G];
 #pragma unroll
-                        for (int g = 0; g < G; ++g) x[g] = __byte_perm(c[i][g / 2], c[i][G / 2 + g / 2], g & 1 ? 0x7632 : 0x5410);
+                        for (int g = 0; g < G; ++g)
+                            x[g] = __byte_perm(c[i][g / 2], c[i][(G + g) / 2], (g & 1 ? 0x32 : 0x10) | ((G + g) & 1 ? 0x7600 : 0x5400));
 #pragma unroll
                         for (int g = 0; g < G; ++g) c[i][g] = x[g];
                     }
@@ -613,21 +613,22 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
             named_barrier_sync(1 + j, 256);
             // the stream's queries, whole rows at a time: scaled, to fp16, and what turns a row's
             // scores to base 2
-            constexpr int kPer = D / 8, kRowsLoad = 32 / kPer;  // 16-byte pieces a row; rows a warp takes at once
+            constexpr int kPer = S::kPer, kRowsLoad = S::kRowsWarp, kBatch = 16 / kRowsLoad < 4 ? 16 / kRowsLoad : 4;
             const int32_t w8 = warp & 7, piece = lane % kPer;
+            const bool mine = S::kPieces == kPer || piece < S::kPieces;
 #pragma unroll 1
-            for (int32_t i0 = 0; i0 < 16 / kRowsLoad; i0 += 4) {
-                uint4 v[4];
+            for (int32_t i0 = 0; i0 < 16 / kRowsLoad; i0 += kBatch) {
+                uint4 v[kBatch];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < kBatch; ++i) {
                     const int32_t at = row_at[j][(i0 + i) * kRowsLoad + w8 * 16 + lane / kPer];
                     v[i] = make_uint4(0, 0, 0, 0);
-                    if (at >= 0)
+                    if (mine && at >= 0)
                         v[i] = *reinterpret_cast<const uint4 *>(a.q + (static_cast<int64_t>(w.b) * a.n + (at >> 16)) * a.ldq +
                                                                  static_cast<int64_t>(at & 0xffff) * D + 8 * piece);
                 }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < kBatch; ++i) {
                     const int32_t qr = (i0 + i) * kRowsLoad + w8 * 16 + lane / kPer;
                     const uint32_t vw[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
                     uint32_t big = 0;  // magnitudes compare as whole numbers, NaN above all
@@ -637,8 +638,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
                     for (int off = 1; off < kPer; off <<= 1) big = max(big, __shfl_xor_sync(kFull, big, off));
                     const int32_t e = max(static_cast<int32_t>(big >> 23), 10);
                     const float f = __uint_as_float(static_cast<uint32_t>(263 - e) << 23);
-                    *reinterpret_cast<uint4 *>(base + S::kQ + j * S::kTileBytes + (piece >> 3) * (kKeys * 128) + sw128(qr, piece & 7)) =
-                        make_uint4(pack_f16(bf_lo(v[i].x) * f, bf_lo(v[i].z) * f), pack_f16(bf_hi(v[i].x) * f, bf_hi(v[i].z) * f),
+                    if (mine)
+                        *reinterpret_cast<uint4 *>(base + S::kQ + j * S::kTileBytes + (piece >> 3) * (kKeys * 128) + sw128(qr, piece & 7)) =
+                            make_uint4(pack_f16(bf_lo(v[i].x) * f, bf_lo(v[i].z) * f), pack_f16(bf_hi(v[i].x) * f, bf_hi(v[i].z) * f),
                                    pack_f16(bf_lo(v[i].y) * f, bf_lo(v[i].w) * f), pack_f16(bf_hi(v[i].y) * f, bf_hi(v[i].w) * f));
                     if (piece == 0) q_scale[j][qr] = make_float2(f, __uint_as_float(static_cast<uint32_t>(e - 9) << 23) * k.scale2);
                 }
@@ -787,10 +789,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
             }
             const float inv = L == 0.0f ? 0.0f : 1.0f / L;
             const bool ok = !*abort_flag;
-            // 16 columns at a time: a half of the stream's, or a quarter of both streams' sum
-            const int32_t first = both ? h * (D / 2) : (2 * j + h) * (D / 4), cols = both ? D / 2 : D / 4;
+            // 16 columns at a time: a half of the stream's, or every fourth of both streams' sum
+            const int32_t first = both ? h * (D / 2) : (2 * j + h) * 16, end = both ? first + D / 2 : D, stride = both ? 16 : 64;
 #pragma unroll 1
-            for (int32_t c = first; c < first + cols; c += 16) {
+            for (int32_t c = first; c < end; c += stride) {
                 float x[16];
                 {
                     uint32_t v[16];
@@ -841,7 +843,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
 #pragma unroll 4
                 for (int32_t r0 = wi * kRowsLoad; r0 < 128; r0 += warps * kRowsLoad) {
                     const int32_t orow = r0 + lane / kPer, at = row_at[both ? j : 0][orow];
-                    if (at >= 0 && ok)
+                    if (mine && at >= 0 && ok)
                         *reinterpret_cast<uint4 *>(a.o + ((static_cast<int64_t>(w.b) * a.n + (at >> 16)) * a.H + (at & 0xffff)) * D + 8 * piece) =
                             *reinterpret_cast<const uint4 *>(src + (piece >> 3) * (kKeys * 128) + sw128(orow, piece & 7));
                 }
@@ -865,15 +867,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
 }  // namespace
 
 cudaError_t prepare_kv4_attention_tc() {
-    cudaError_t e = cudaFuncSetAttribute(kv4_attention_tc_kernel<4>, cudaFuncAttributeMaxDynamicSharedMemorySize, Tc<4>::kTotal);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(kv4_attention_tc_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, Tc<2>::kTotal);
+    auto set = [](auto *kernel, uint32_t bytes) { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)); };
+    cudaError_t e = set(kv4_attention_tc_kernel<1>, Tc<1>::kTotal);
+    if (e == cudaSuccess) e = set(kv4_attention_tc_kernel<2>, Tc<2>::kTotal);
+    if (e == cudaSuccess) e = set(kv4_attention_tc_kernel<3>, Tc<3>::kTotal);
+    if (e == cudaSuccess) e = set(kv4_attention_tc_kernel<4>, Tc<4>::kTotal);
     return e;
 }
 
 cudaError_t launch_kv4_attention_tc(const Kv4Args &k, int32_t grid, cudaStream_t st) {
-    if (k.a.cache.G == 4) return launch_pdl(kv4_attention_tc_kernel<4>, dim3(grid), dim3(kThreads), Tc<4>::kTotal, st, k);
-    return launch_pdl(kv4_attention_tc_kernel<2>, dim3(grid), dim3(kThreads), Tc<2>::kTotal, st, k);
+    switch (k.a.cache.G) {
+        case 1: return launch_pdl(kv4_attention_tc_kernel<1>, dim3(grid), dim3(kThreads), Tc<1>::kTotal, st, k);
+        case 2: return launch_pdl(kv4_attention_tc_kernel<2>, dim3(grid), dim3(kThreads), Tc<2>::kTotal, st, k);
+        case 3: return launch_pdl(kv4_attention_tc_kernel<3>, dim3(grid), dim3(kThreads), Tc<3>::kTotal, st, k);
+        default: return launch_pdl(kv4_attention_tc_kernel<4>, dim3(grid), dim3(kThreads), Tc<4>::kTotal, st, k);
+    }
 }
 
 }  // namespace eagle

@@ -337,7 +337,7 @@ __device__ __forceinline__ Kv4Share share_of(const Walk &w) {
 // Where a segment's partial sums go: slot 0 of its CTA for a unit that an earlier CTA began, else 1.
 __device__ __forceinline__ int64_t slot_of(const Walk &w) { return 2 * static_cast<int64_t>(blockIdx.x) + (w.s0 > 0 ? 0 : 1); }
 
-// The tcgen05 kernel (kv4_attn_tc.cu): head_dim 64 or 128, units of 256 query rows, tiles of 128 keys.
+// The tcgen05 kernel (kv4_attn_tc.cu): units of 256 query rows, tiles of 128 keys.
 constexpr int32_t kKv4TcRows = 256;
 constexpr int32_t kKv4TcTile = 128;
 cudaError_t prepare_kv4_attention_tc();

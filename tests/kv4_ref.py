@@ -58,7 +58,7 @@ def attend(q, kc, vc, kn, vn, see):
       exponentials               2^-21 relative each
       fp16 range                 products below 2^-14 lose at most 2^-25 of a scale where the largest
                                  p is 2^9 or more (2^0 where some s is 16 or more): 15 N 2^-34 or 2^-25
-    More than 16 query rows a kv head of 64 or 128 dims go through tiles of fp16 values instead:
+    More than 16 query rows a kv head go through tiles of fp16 values instead:
       cached k, v to fp16        2^-11 of their size and 2^-25: the exponent is off by 2^-11 A +
                                  2^-25 sum |q| / sqrt(D) more, v by 2^-11 |v| + 2^-25
       new k, v to fp16           exact but for 2^-25 below 2^-14: the same 2^-25 terms
@@ -68,7 +68,7 @@ def attend(q, kc, vc, kn, vn, see):
     """
     n, H, D = q.shape
     Hk = kc.shape[1]
-    tiles = n * H // Hk > 16 and D in (64, 128)
+    tiles = n * H // Hk > 16
     k, v, size, ksize = stands_for(kc), stands_for(vc), size_of(vc), size_of(kc)
     steep = bool((parts(vc)[1] >= 16).any()) if vc.numel() else False
     if kn is not None:

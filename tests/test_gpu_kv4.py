@@ -286,6 +286,11 @@ ATTENTION = [
     (1, 300, 16, 2, 128, 64, [100], "tree"),         # ten tiles of query rows
     (1, 4097, 1, 1, 64, 16, [5], "causal"),          # the most nodes
     (1, 4097, 1, 1, 32, 16, [5], "causal"),
+    (2, 65, 8, 2, 96, 64, [1024, 77], "tree"),
+    (3, 150, 4, 2, 32, 32, [900, 0, 131], "causal"),
+    (20, 17, 3, 3, 96, 16, [i * 97 % 1500 for i in range(20)], "tree"),
+    (2, 40, 8, 1, 96, 128, [3000, 5], "cache"),
+    (2, 90, 8, 1, 32, 128, [3000, 5], "cache"),
 ]
 
 
@@ -322,7 +327,9 @@ def test_attention_over_values_of_other_sizes(dev, case, kscale, vscale, qscale)
 
 
 @pytest.mark.parametrize("case", [(2, 9, 4, 4, 128, 32, [70, 0], "tree"), (1, 65, 8, 2, 64, 64, [100], "tree"),
-                                  (2, 40, 8, 1, 128, 16, [0, 257], "tree")], ids=["9rows", "260rows", "320rows"])
+                                  (2, 40, 8, 1, 128, 16, [0, 257], "tree"), (1, 50, 4, 1, 96, 16, [40], "tree"),
+                                  (2, 50, 2, 1, 32, 16, [40, 300], "tree")],
+                         ids=["9rows", "260rows", "320rows", "200rows96", "100rows32"])
 @pytest.mark.parametrize("what", [math.nan, math.inf, -math.inf, 3e38])
 def test_what_hidden_keys_hold_has_no_influence(dev, case, what):
     """A leaf that no other node sees: its key and value may hold anything."""
