@@ -1214,8 +1214,14 @@ namespace {
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 struct DecoderLayout {
-    size_t qkv, o, y, h1, r, gu, act, counters, partials, part_o, part_ml, kv4, total;
+    size_t qkv, o, y, h1, r, gu, act, counters, ticket_bytes, partials, part_o, part_ml, kv4, total;
 };
+
+__global__ void __launch_bounds__(256) zero_tickets_kernel(int32_t *tickets, int32_t n) {
+    pdl_launch_dependents();
+    pdl_wait();
+    for (int32_t i = threadIdx.x; i < n; i += 256) tickets[i] = 0;
+}
 
 constexpr int32_t kAttnMaxSplits = 32;
 
@@ -1280,7 +1286,8 @@ DecoderLayout decoder_layout(const eagle_decoder_layer_weights *w, int32_t batch
     };
     const int32_t chunk = static_cast<int32_t>(std::min<int64_t>(rows, kLinearMaxRows));
     const int32_t widest = static_cast<int32_t>(std::max<int64_t>(std::max(nqkv, h), 2 * I));
-    L.counters = take(linear_counters_bytes(widest, static_cast<int32_t>(rows)));
+    L.ticket_bytes = linear_counters_bytes(widest, static_cast<int32_t>(rows));
+    L.counters = take(L.ticket_bytes);
     L.partials = take(linear_partials_bytes(sms, linear_n_tile(chunk)));
     L.qkv = take(static_cast<size_t>(rows) * nqkv * 2);
     L.o = take(static_cast<size_t>(rows) * nq * 2);
@@ -1398,6 +1405,7 @@ eagle_status run_layer(const eagle_decoder_layer_weights *w, int32_t batch, int3
     int32_t *counters = reinterpret_cast<int32_t *>(at(L.counters));
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const int32_t h = w->hidden, H = w->heads, Hk = w->kv_heads, D = w->head_dim, I = w->inter;
+    if (kv4 && !kv4_attention_fits(*kv4, batch, nodes, H, true)) return EAGLE_ERR_UNSUPPORTED;
     const int32_t nq = H * D, nk = Hk * D, nqkv = nq + 2 * nk;
     auto *qkv = reinterpret_cast<__nv_bfloat16 *>(at(L.qkv));
     auto *o = reinterpret_cast<__nv_bfloat16 *>(at(L.o));
@@ -1412,6 +1420,8 @@ eagle_status run_layer(const eagle_decoder_layer_weights *w, int32_t batch, int3
     do {                                            \
         if ((expr) != cudaSuccess) return EAGLE_ERR_CUDA; \
     } while (0)
+    if (kv4)  // a workspace of any content: the layer is called with changing sizes, at which the tickets lie elsewhere
+        DEC_CUDA(launch_pdl(zero_tickets_kernel, dim3(1), dim3(256), 0, st, counters, static_cast<int32_t>(L.ticket_bytes / 4)));
     // projections of every node, rotated
     DEC_CUDA(gemm_rows(w->w_qkv, nqkv, h, d_x, rows, qkv, 1, partials, counters, sms, st));
     // rotation (one block per row, heads split over more blocks when rows are few); the tree's

@@ -89,6 +89,8 @@ struct Kv4Attention {
     void *ws;
     int32_t *status;
 };
+// False: more key tiles over all units than 32 bits count (launch_kv4_attention then refuses).
+bool kv4_attention_fits(const Kv4View &cache, int32_t B, int32_t n, int32_t H, bool new_keys);
 size_t kv4_attention_workspace(int32_t Hk, int32_t G, int32_t H, int32_t n);
 cudaError_t launch_kv4_attention(const Kv4Attention &a, cudaStream_t st);
 

@@ -788,6 +788,15 @@ int32_t grid_of(const Device &d, int32_t G, const Variant &v) {
     return d.sms * d.blocks[G][v.rows == 8 ? 0 : 1];
 }
 
+// Key tiles of all units where every request fills its pages.
+int64_t longest_line(const Kv4View &cache, int32_t B, int32_t n, int32_t H, bool new_keys) {
+    const int64_t mq = static_cast<int64_t>(n) * (H / cache.Hk);
+    const Variant v = variant(cache.G, static_cast<int32_t>(mq));
+    const int64_t tile = v.kernel ? kTile : kKv4TcTile, units = static_cast<int64_t>(B) * cache.Hk * ((mq + v.rows - 1) / v.rows);
+    const int64_t tiles = (cache.cap + tile - 1) / tile + (new_keys ? (n + tile - 1) / tile : 0);
+    return units >= (int64_t{1} << 31) ? units : units * tiles;
+}
+
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 }  // namespace
@@ -800,9 +809,14 @@ size_t kv4_attention_workspace(int32_t Hk, int32_t G, int32_t H, int32_t n) {
     return align256(grid * sizeof(Kv4Share)) + align256(grid * 2 * v.rows * sizeof(float2)) + grid * 2 * v.rows * G * kKv4Group * 4;
 }
 
+bool kv4_attention_fits(const Kv4View &cache, int32_t B, int32_t n, int32_t H, bool new_keys) {
+    return longest_line(cache, B, n, H, new_keys) < (int64_t{1} << 31);
+}
+
 cudaError_t launch_kv4_attention(const Kv4Attention &a, cudaStream_t st) {
     const Device *d = device_now();
     if (!d) return cudaErrorInvalidDevice;
+    if (!kv4_attention_fits(a.cache, a.B, a.n, a.H, a.kn != nullptr)) return cudaErrorNotSupported;
     const int32_t G = a.cache.G;
     Kv4Args k;
     k.a = a;
@@ -813,7 +827,6 @@ cudaError_t launch_kv4_attention(const Kv4Attention &a, cudaStream_t st) {
     k.QT = (k.Mq + v.rows - 1) / v.rows;
     k.W = (a.n + 31) / 32;
     static_assert(kTile == 1 << 6 && kKv4TcTile == 1 << 7, "tile_shift");
-    const int64_t tile = v.kernel ? kTile : kKv4TcTile;
     k.tile_shift = v.kernel ? 6 : 7;
     k.min_tiles = v.kernel ? kMinTiles : 1;
     // cuts move to a unit's end from so many tiles: a unit cut in two writes and reads partial sums of
@@ -829,10 +842,7 @@ cudaError_t launch_kv4_attention(const Kv4Attention &a, cudaStream_t st) {
     ws += align256(static_cast<size_t>(full) * 2 * v.rows * sizeof(float2));
     k.part_o = reinterpret_cast<float *>(ws);
     // no more CTAs than the longest possible line gives work to
-    const int64_t units = static_cast<int64_t>(a.B) * a.cache.Hk * k.QT;
-    const int64_t tiles = (a.cache.cap + tile - 1) / tile + (a.kn ? (a.n + tile - 1) / tile : 0);
-    if (units >= (int64_t{1} << 31) || units * tiles >= (int64_t{1} << 31)) return cudaErrorNotSupported;
-    const int64_t most = (units * tiles + k.min_tiles - 1) / k.min_tiles;
+    const int64_t most = (longest_line(a.cache, a.B, a.n, a.H, a.kn != nullptr) + k.min_tiles - 1) / k.min_tiles;
     const unsigned grid = static_cast<unsigned>(std::min<int64_t>(full, std::max<int64_t>(most, 1)));
     const cudaError_t e = v.kernel ? launch_pdl(v.kernel, dim3(grid), dim3(v.threads), v.smem, st, k)
                                    : launch_kv4_attention_tc(k, static_cast<int32_t>(grid), st);

@@ -69,7 +69,7 @@ __device__ __forceinline__ int32_t length_after(const AppendArgs &a, int32_t b, 
     if (a.select) {
         last = 0;
         for (int32_t j = threadIdx.x & 31; j < cnt; j += 32)
-            if (a.select[static_cast<int64_t>(b) * a.slots + j] >= 0) last = j + 1;
+            if (static_cast<uint32_t>(a.select[static_cast<int64_t>(b) * a.slots + j]) < static_cast<uint32_t>(a.src_rows)) last = j + 1;
         last = __reduce_max_sync(kFull, last);
     }
     return static_cast<int32_t>(min(start + last, a.v.cap));

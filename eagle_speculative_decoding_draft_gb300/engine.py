@@ -437,7 +437,6 @@ class DecoderLayer:
         self.hidden, self.heads, self.kv_heads, self.head_dim, self.inter = h, heads, kv_heads, D, inter
         self.device = w_qkv.device
         self._ws = None
-        self._ws4 = {}
 
     def workspace(self, batch: int, nodes: int):
         nbytes = self._lib.eagle_decoder_layer_workspace_bytes(ctypes.byref(self.w), batch, nodes)
@@ -483,8 +482,7 @@ class DecoderLayer:
         """The layer over a 4-bit cache (a ``KV4Cache`` of the layer's kv heads and head_dim; each
         request at its own length).  x, positions, mask and the results are those of the call above
         (mask None: node i sees nodes 0..i); ``cache.append`` takes k_new and v_new.  workspace: a
-        zero-filled uint8 tensor, used for these sizes alone, instead of the layer's own (one for each
-        batch and n); calls that may overlap need one each."""
+        uint8 tensor to use instead of a fresh one; calls that may overlap need one each."""
         _need(x, "x", torch.bfloat16)
         B, n, h = x.shape
         if h != self.hidden or B != cache.batch:
@@ -509,11 +507,7 @@ class DecoderLayer:
             if nbytes == 0:
                 raise ValueError(f"unusable decoder layer sizes (batch={B}, nodes={n}) or a cache of other heads")
             if workspace is None:
-                # one a shape, kept: regions lie elsewhere at other sizes, and the tile tickets
-                # must find the zeros that the last call of the same sizes left
-                workspace = self._ws4.get((B, n))
-                if workspace is None or workspace.numel() < nbytes:
-                    workspace = self._ws4[(B, n)] = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
+                workspace = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
             elif _need(workspace, "workspace", torch.uint8).numel() < nbytes:
                 raise ValueError(f"workspace must hold at least {nbytes} bytes")
             check(self._lib.eagle_decoder_layer_kv4(

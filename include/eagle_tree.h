@@ -612,8 +612,9 @@ EAGLE_API eagle_status eagle_kv4_attention(const eagle_kv4_cache *cache, int32_t
  * The draft decoder layer over a 4-bit cache: eagle_decoder_layer with the cached keys and values
  * read by eagle_kv4_attention, each request with its own length.  cache->kv_heads and head_dim must be
  * the layer's; the other arguments, limits and rounding points are those of eagle_decoder_layer
- * (d_mask NULL: node i sees nodes 0..i).  d_k_new / d_v_new are what eagle_kv4_append takes after the
- * verify.  The layer does not write to the cache.
+ * (d_mask NULL: node i sees nodes 0..i), but that d_ws may hold anything and the errors are also those
+ * of eagle_kv4_attention.  d_k_new / d_v_new are what eagle_kv4_append takes after the verify.  The
+ * layer does not write to the cache.
  */
 EAGLE_API size_t eagle_decoder_layer_kv4_workspace_bytes(const eagle_decoder_layer_weights *w,
                                                          const eagle_kv4_cache *cache, int32_t batch,

@@ -552,6 +552,12 @@ def test_work_beyond_32_bits_is_refused(dev):
     need = lib.eagle_kv4_attention_workspace_bytes(ctypes.byref(c), 1, 1024)
     assert lib.eagle_kv4_attention(ctypes.byref(c), 1 << 6, 1, 1024, P(256), 1 << 17, None, None, 0, None, P(256), P(256), need,
                                    None, None) == 2
+    w = _lib.DecoderLayerWeights(256, 4, 2, 64, 256, 1e4, 1e-5, *[256] * 5)
+    c = _lib.KV4CacheStruct(2, 64, 1024, 16, 1 << 20, 256, 256, 256)
+    need = lib.eagle_decoder_layer_kv4_workspace_bytes(ctypes.byref(w), ctypes.byref(c), 128, 1)
+    assert need > 0
+    assert lib.eagle_decoder_layer_kv4(ctypes.byref(w), ctypes.byref(c), 128, 1, P(256), P(256), None, P(256), None, None, P(256),
+                                       need, None, None) == 2
 
 
 # ------------------------------------------------------------------------------------------------
@@ -605,6 +611,41 @@ def test_decoder_layer_without_a_mask_is_the_next_piece_of_a_prompt(dev):
     chain = tree_mask(np.arange(n) - 1)  # every node's parent is the one before it
     chain = torch.from_numpy(np.broadcast_to(chain, (B, n, 2)).copy().view(np.int32)).to(dev)
     assert torch.equal(lay.kv4(g(w["x"]), c, pos), lay.kv4(g(w["x"]), c, pos, chain))
+    c.status()
+
+
+def test_decoder_layer_captured_with_changing_sizes(dev):
+    """Workspaces hold anything: eager calls of other sizes between a graph's replays, one workspace of
+    0xFF for several sizes, and two graphs replayed side by side."""
+    from eagle_speculative_decoding_draft_gb300.engine import DecoderLayer
+    B, h, H, Hk, D, I = 2, 256, 4, 2, 64, 512
+    w, d = layer(B=B, n=70, P=30, h=h, H=H, Hk=Hk, D=D, I=I, seed=6)
+    g = lambda t: t.to(dev).contiguous()
+    lay = DecoderLayer(g(w["w_qkv"]), g(w["w_o"]), g(w["w_norm"]), g(w["w_gu"]), g(w["w_d"]), H, Hk)
+    c = make_cache(B, Hk, D, 30, 16)
+    c.append(g(w["k_cache"]), g(w["v_cache"]))
+    x, pos = g(w["x"]), i32([[30 + i for i in range(70)]] * B)
+    sizes = [70, 1, 9]
+    args = [(x[:, :n].contiguous(), c, pos[:, :n].contiguous()) for n in sizes]
+    graphs, outs = [], []
+    for a in args[:2]:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):  # the first call of these sizes
+            outs.append(lay.kv4(*a))
+        graphs.append(graph)
+    want = [lay.kv4(*a) for a in args]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for graph, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                graph.replay()
+        lay.kv4(*args[2])
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, v) for o, v in zip(outs, want))
+    ws = torch.full((1 << 26,), 0xFF, dtype=torch.uint8, device="cuda")
+    for i in (0, 1, 2, 1, 0):
+        assert torch.equal(lay.kv4(*args[i], workspace=ws), want[i])
     c.status()
 
 
