@@ -30,9 +30,10 @@
 // 26 warps leave 72 a thread, and what is spilled goes to L2, as shared memory takes all of L1: with
 // 112 bytes spilled the first took 822 us, with the walk over the units in shared memory and 16
 // bytes 784.  So the masks and the elements that fp16 does not hold have functions of their own.
-// Slower, measured: scores kept in registers from the first pass to the second with registers moved
-// from the other warps (setmaxnreg; 855 us against 739), a second issuing warp (895 against 822:
-// the streams then work in step), a second copying warp and an L2 prefetch (708 against 688).
+// Slower, measured: scores kept in registers from the first pass to the second, with registers moved from
+// the other warps (setmaxnreg; 855 us against 739); p from one pass with the reference as it is, on trial
+// (833 against 688); a second issuing warp (895 against 822: the streams then work in step); a second
+// copying warp and an L2 prefetch (708 against 688).
 //
 // Queries are scaled by a power of two so that a row's largest element is 2^9..2^10 (exact, as in
 // kv4_attn.cu).  Within 8 neighbouring dims the tiles hold them in the order 0 4 1 5 2 6 3 7, in
@@ -789,8 +790,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
             }
             const float inv = L == 0.0f ? 0.0f : 1.0f / L;
             const bool ok = !*abort_flag;
-            // 16 columns at a time: a half of the stream's, or every fourth of both streams' sum
-            const int32_t first = both ? h * (D / 2) : (2 * j + h) * 16, end = both ? first + D / 2 : D, stride = both ? 16 : 64;
+            // 16 columns at a time: a half of the stream's, or a quarter of both streams' sum, with
+            // head_dim 32 and 96 every fourth 16 of it (for all it took the 2047-token piece 688 -> 722 us)
+            constexpr bool kQuarters = D % 64 == 0;
+            const int32_t first = both ? h * (D / 2) : (2 * j + h) * (kQuarters ? D / 4 : 16);
+            const int32_t end = both ? first + D / 2 : (kQuarters ? first + D / 4 : D), stride = kQuarters || both ? 16 : 64;
 #pragma unroll 1
             for (int32_t c = first; c < end; c += stride) {
                 float x[16];
