@@ -25,8 +25,8 @@
 //
 // What bounds it: instruction issue and the chain of one stream's tile (scores, two passes, p, product):
 // the next 2047 tokens of two requests over 4096 cached ones (64 heads, 8 kv heads of 128)
-// take 688 us, 0.53 of the measured bf16 matrix rate; 32 requests of 65 nodes (260 rows,
-// a full unit and one of 4 rows each) over 1024 tokens 108 us.  Registers are what it is short of:
+// take 690 us, 0.53 of the measured bf16 matrix rate; 32 requests of 65 nodes (260 rows,
+// a full unit and one of 4 rows each) over 1024 tokens 105 us.  Registers are what it is short of:
 // 26 warps leave 72 a thread, and what is spilled goes to L2, as shared memory takes all of L1: with
 // 112 bytes spilled the first took 822 us, with the walk over the units in shared memory and 16
 // bytes 784.  So the masks and the elements that fp16 does not hold have functions of their own.
@@ -311,7 +311,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
     __shared__ TcBars bar;
     __shared__ uint32_t tmem_base;
     __shared__ int32_t abort_mark;
-    __shared__ __align__(8) uint8_t key_bits[4][16];  // by tile & 3: which of its 128 keys are there
+    // By tile & 7: which of its 128 keys are there.  Written ahead of the tile itself, when the scores of
+    // the tile three before are there: the other stream may not have looked at the tile four before yet.
+    __shared__ __align__(8) uint8_t key_bits[8][16];
     __shared__ uint8_t raw_keys[kRaw][8];             // keys of each chunk that are there
     __shared__ __align__(4) uint8_t odd_tile[4][2][kFillWarps];  // by tile & 3, key or value, filling warp
     __shared__ int32_t row_at[2][128];        // stream, row: node << 16 | head, -1 behind the unit's last row
@@ -385,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
             int32_t s = w.s0;
             if (s < w.nt) {  // new keys or values, the next ones' loads under way
                 constexpr int kPer = S::kPer, kRowsWarp = S::kRowsWarp;
-                constexpr int kBatch = kKeys / (4 * kRowsWarp) < 8 ? kKeys / (4 * kRowsWarp) : 8;
+                constexpr int kBatch = 4;  // with 8 at once the loops miss the instruction cache more: 65-node trees 108 us, not 105
                 constexpr int kBatches = kKeys / (4 * kRowsWarp * kBatch);
                 const int32_t ch = lane % kPer, first = fw * kRowsWarp + lane / kPer;
                 const bool mine = S::kPieces == kPer || ch < S::kPieces;
@@ -463,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
                     const int32_t here = max(0, min(8, static_cast<int32_t>(raw_keys[half][group >> 1]) - 8 * (group & 1)));
                     load_words<G>(part + slot * 16 * G + q * 4 * G, c[i]);
                     load_words<G>(part + 256 * G + slot * 4 * G, sm[i]);
-                    if (!half && lane == 0) key_bits[gt & 3][group] = static_cast<uint8_t>((1u << here) - 1u);
+                    if (!half && lane == 0) key_bits[gt & 7][group] = static_cast<uint8_t>((1u << here) - 1u);
                     if (t8 >= here) {  // rows that are not there hold 0
 #pragma unroll
                         for (int g = 0; g < G; ++g) c[i][g] = sm[i][g] = 0u;
@@ -688,7 +690,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
                 __syncwarp();
                 tc_fence_after();
                 if (i >= fresh) {
-                    const uint2 b = *reinterpret_cast<const uint2 *>(key_bits[t & 3] + 8 * h);
+                    const uint2 b = *reinterpret_cast<const uint2 *>(key_bits[t & 7] + 8 * h);
                     see0 = b.x;
                     see1 = b.y;
                 } else if (used && *reinterpret_cast<const volatile uint32_t *>(odd_tile[t & 3][0]) != 0) {
