@@ -450,16 +450,17 @@ __global__ void __launch_bounds__(kThreads, Shape<G, NQ>::kBlocks) kv4_attention
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     const uint8_t *kp = ch[u] + kv4_key_params(G);
-                    float x[NQ][4];
+                    uint64_t x[NQ][2];  // pairs of columns: key rows gq, gq + 8
                     {
                         const uint32_t ma = qd < G ? *reinterpret_cast<const uint32_t *>(kp + gq * 4 * G + 4 * qd) : 0u;
                         const uint32_t mb = qd < G ? *reinterpret_cast<const uint32_t *>(kp + (gq + 8) * 4 * G + 4 * qd) : 0u;
                         const uint32_t a0 = __byte_perm(ma, ma, 0x3232), a1 = __byte_perm(mb, mb, 0x3232);
 #pragma unroll
                         for (int nq = 0; nq < NQ; ++nq) {
-                            mma_f16_first(x[nq], a0, a1, 0u, 0u, qs[nq], 0u);
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) x[nq][e] *= 0x1p-24f;
+                            float m[4];
+                            mma_f16_first(m, a0, a1, 0u, 0u, qs[nq], 0u);
+                            x[nq][0] = mul_2(pack_2(m[0], m[1]), pack_2(0x1p-24f, 0x1p-24f));
+                            x[nq][1] = mul_2(pack_2(m[2], m[3]), pack_2(0x1p-24f, 0x1p-24f));
                         }
                     }
                     uint32_t wa[G], wb[G], pa[G], pb[G];
@@ -478,16 +479,18 @@ __global__ void __launch_bounds__(kThreads, Shape<G, NQ>::kBlocks) kv4_attention
                                     wb[g] & 0x00f000f0u, qf[2 * g][nq][0], qf[2 * g][nq][1]);
                             mma_f16(acc, xa & 0x000f000fu, xb & 0x000f000fu, xa & 0x00f000f0u, xb & 0x00f000f0u,
                                     qf[2 * g + 1][nq][0], qf[2 * g + 1][nq][1]);
-                            x[nq][0] = fmaf(sa, acc[0], x[nq][0]);
-                            x[nq][1] = fmaf(sa, acc[1], x[nq][1]);
-                            x[nq][2] = fmaf(sb, acc[2], x[nq][2]);
-                            x[nq][3] = fmaf(sb, acc[3], x[nq][3]);
+                            x[nq][0] = fma_2(pack_2(sa, sa), pack_2(acc[0], acc[1]), x[nq][0]);
+                            x[nq][1] = fma_2(pack_2(sb, sb), pack_2(acc[2], acc[3]), x[nq][1]);
                         }
                     }
 #pragma unroll
                     for (int nq = 0; nq < NQ; ++nq)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) sc[nq][4 * u + e] = x[nq][e] * qk[nq][e & 1];
+                        for (int e = 0; e < 2; ++e) {
+                            const float2 y = unpack_2(mul_2(x[nq][e], pack_2(qk[nq][0], qk[nq][1])));
+                            sc[nq][4 * u + 2 * e] = y.x;
+                            sc[nq][4 * u + 2 * e + 1] = y.y;
+                        }
                 }
                 const bool tail = nv[0] + nv[1] < 32;
                 if (tail) {
