@@ -25,8 +25,8 @@
 // Scores are formed transposed (16 keys on the MMA's M side, 8 query rows on N), so few query rows
 // waste no MMA rows, and the accumulators turn into the value product's operand by movmatrix.
 //
-// Measured: 64 trees of 8 nodes, 32 heads of 128 over 1024 tokens each (352 MB) in 115 us, 0.45 of the
-// measured copy rate; 16 requests of 1 .. 65536 tokens under groups of 8 heads in 170 us, 0.58 of it.
+// Measured: 64 trees of 8 nodes, 32 heads of 128 over 1024 tokens each (352 MB) in 113 us, 0.46 of the
+// measured copy rate; 16 requests of 1 .. 65536 tokens under groups of 8 heads in 166 us, 0.60 of it.
 // Three CTAs of 128 registers a thread stay on an SM; it issues in 41 % of the cycles, waiting for
 // memory in the new keys' part and for fixed latencies in the rest.  Slower, measured: warps that copy
 // their own chunks, with four CTAs an SM or tiles of 32 keys (127 and 118 us against 115).
@@ -183,7 +183,8 @@ __global__ void __launch_bounds__(kThreads, Shape<G, NQ>::kBlocks) kv4_attention
     const int32_t gq = lane >> 2, qd = lane & 3;
     float *merge = reinterpret_cast<float *>(smem + S::kMerge);
     float2 *merge_ml = reinterpret_cast<float2 *>(smem + S::kMl);
-    int32_t taken = 0;  // stages
+    int32_t stage = 0;  // the next one, and how often the ring has come round
+    uint32_t turn = 0;
     do {
         uint32_t qf[2 * G][NQ][2];  // fp16 queries, the score MMAs' B operand
         uint32_t qs[NQ];            // fp16 hi + lo of the sum of group qd's elements
@@ -434,14 +435,13 @@ __global__ void __launch_bounds__(kThreads, Shape<G, NQ>::kBlocks) kv4_attention
 #pragma unroll 1
         for (; s < w.s1; s += 2) {
             const int32_t count = min(w.s1 - s, 2);
-            const int32_t st0 = taken % kStages, st1 = (taken + 1) % kStages;
-            kv4_wait(&full[st0], taken / kStages, abort_flag);
-            if (count == 2) kv4_wait(&full[st1], (taken + 1) / kStages, abort_flag);
+            const int32_t st0 = stage, st1 = stage + 1 == kStages ? 0 : stage + 1;
+            const uint32_t turn1 = turn + (st1 == 0 ? 1 : 0);
+            const bool come = kv4_wait(&full[st0], turn, abort_flag) && (count < 2 || kv4_wait(&full[st1], turn1, abort_flag));
             int32_t nv[2];  // keys of the chunks that are there
             nv[0] = valid[st0][warp];
             nv[1] = count == 2 ? valid[st1][warp] : 0;
-            nv[0] = __shfl_sync(kFull, *abort_flag ? 0 : nv[0], 0);
-            nv[1] = __shfl_sync(kFull, *abort_flag ? 0 : nv[1], 0);
+            if (!__all_sync(kFull, come)) nv[0] = nv[1] = 0;
             if (nv[0] + nv[1] > 0) {
                 const uint8_t *ch[2] = {smem + S::kRing + st0 * S::kStageBytes + warp * kv4_chunk_bytes(G),
                                         smem + S::kRing + st1 * S::kStageBytes + warp * kv4_chunk_bytes(G)};
@@ -598,7 +598,8 @@ __global__ void __launch_bounds__(kThreads, Shape<G, NQ>::kBlocks) kv4_attention
                 mbar_arrive(&empty[st0]);
                 if (count == 2) mbar_arrive(&empty[st1]);
             }
-            taken += count;
+            stage = count == 2 ? (st1 + 1 == kStages ? 0 : st1 + 1) : st1;
+            turn = count == 2 ? turn1 + (stage == 0 ? 1 : 0) : turn1;
         }
 
         // ---------------- the warps' shares of the segment meet ----------------
