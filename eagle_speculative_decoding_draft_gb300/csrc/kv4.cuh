@@ -75,6 +75,34 @@ __device__ __forceinline__ int64_t kv4_length(const Kv4View &v, int32_t b) {
 // Host: fills a view from the caller's description.  False when a size or pointer is unusable.
 bool kv4_view(const eagle_kv4_cache *c, Kv4View *out);
 
+// Two fp32 operations by one instruction.
+__device__ __forceinline__ uint64_t pack_2(uint32_t lo, uint32_t hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+    return r;
+}
+__device__ __forceinline__ uint64_t pack_2(float lo, float hi) { return pack_2(__float_as_uint(lo), __float_as_uint(hi)); }
+__device__ __forceinline__ float2 unpack_2(uint64_t x) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma_2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add_2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul_2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
 // ---------------------------------------------------------------------------------------------
 // Attention over the cache and the new keys of each request's nodes (kv4_attn.cu)
 // ---------------------------------------------------------------------------------------------

@@ -102,16 +102,20 @@ __device__ __forceinline__ uint32_t quantise(const uint32_t (&w)[16], uint32_t (
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(sf));  // within 2^-23: 3 units more are above 1 / s
     r = sf > 0.0f ? __int_as_float(__float_as_int(r) + 3) : 0.0f;
     constexpr float kMagic = 12582912.0f;  // bits 0x4b400000: the code adds to them
+    const uint64_t r2 = pack_2(r, r), s2 = pack_2(sf, sf), m2 = pack_2(-mf, -mf), magic2 = pack_2(kMagic, kMagic);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         uint32_t c8 = 0;
 #pragma unroll
-        for (int i = 7; i >= 0; --i) {
-            const uint32_t p = w[4 * k + (i >> 1)];
-            const float a = __uint_as_float(i & 1 ? p & 0xffff0000u : p << 16) - mf;
-            const float t = fmaf(a, r, kMagic), rem = fmaf(kMagic - t, sf, a);
-            uint32_t c = __float_as_uint(t);
-            if (rem <= below && ((c & 1u) || rem < below)) --c;
+        for (int i = 3; i >= 0; --i) {  // two values of a word at a time
+            const uint32_t p = w[4 * k + i];
+            const uint64_t a = add_2(pack_2(p << 16, p & 0xffff0000u), m2), t = fma_2(a, r2, magic2);
+            const float2 code = unpack_2(t), rem = unpack_2(fma_2(fma_2(t, pack_2(-1.0f, -1.0f), magic2), s2, a));
+            uint32_t c = __float_as_uint(code.y);
+            if (rem.y <= below && ((c & 1u) || rem.y < below)) --c;
+            c8 = c8 * 16u + c;
+            c = __float_as_uint(code.x);
+            if (rem.x <= below && ((c & 1u) || rem.x < below)) --c;
             c8 = c8 * 16u + c;
         }
         // without 0x4b400000 (1 + 16 + 256 + ...), of which three terms stay in the word
