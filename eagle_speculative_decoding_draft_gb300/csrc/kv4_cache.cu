@@ -98,6 +98,7 @@ __device__ __forceinline__ uint32_t quantise(const uint32_t (&w)[16], uint32_t (
     const float mf = __half2float(m);
     const __half s = __float2half_ru(__fdiv_rn(hi - mf, 15.0f));
     const float sf = __half2float(s), below = -0.5f * sf;
+    const float below_or_at = __int_as_float(__float_as_int(below) - 1);  // the next one up (NaN for -0: never)
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(sf));  // within 2^-23: 3 units more are above 1 / s
     r = sf > 0.0f ? __int_as_float(__float_as_int(r) + 3) : 0.0f;
@@ -112,10 +113,10 @@ __device__ __forceinline__ uint32_t quantise(const uint32_t (&w)[16], uint32_t (
             const uint64_t a = add_2(pack_2(p << 16, p & 0xffff0000u), m2), t = fma_2(a, r2, magic2);
             const float2 code = unpack_2(t), rem = unpack_2(fma_2(fma_2(t, pack_2(-1.0f, -1.0f), magic2), s2, a));
             uint32_t c = __float_as_uint(code.y);
-            if (rem.y <= below && ((c & 1u) || rem.y < below)) --c;
+            if (rem.y < (c & 1u ? below_or_at : below)) --c;
             c8 = c8 * 16u + c;
             c = __float_as_uint(code.x);
-            if (rem.x <= below && ((c & 1u) || rem.x < below)) --c;
+            if (rem.x < (c & 1u ? below_or_at : below)) --c;
             c8 = c8 * 16u + c;
         }
         // without 0x4b400000 (1 + 16 + 256 + ...), of which three terms stay in the word
@@ -126,8 +127,8 @@ __device__ __forceinline__ uint32_t quantise(const uint32_t (&w)[16], uint32_t (
 
 // A lane takes whole groups (64 bytes): their least and largest value and parameters need no other
 // lane.  The chunk's rows that are written come one behind the other, keys, then values, 32 groups a
-// pass, the next pass on its way.  Bound by instructions, about 13 a value: 33 k tokens of 8 kv heads of
-// 128 (176 MB) in 47 us, 0.55 of the measured copy rate; a lane a 16-byte piece with the least and
+// pass, the next pass on its way.  Bound by instruction issue: 33 k tokens of 8 kv heads of
+// 128 (176 MB) in 45 us, 0.58 of the measured copy rate (47 with single fp32 operations); a lane a 16-byte piece with the least and
 // largest value over four lanes took 82.  The accepted rows of 64 requests: 10 us.
 template <int G>
 __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const AppendArgs a) {

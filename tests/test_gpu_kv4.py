@@ -173,6 +173,21 @@ def test_groups_that_hold_no_numbers_or_only_one(dev):
         assert torch.all(((got.double() - x.double()).abs() <= step / 2 * (1 + 1e-6) + 2.0 ** -24 * want.abs())[~bad])
 
 
+def test_ties_go_to_the_even_code(dev):
+    """Values half way between codes: steps of a power of two, from a least value of 0 and of -8 steps."""
+    halves = torch.cat([torch.tensor([0.0, 15.0]), torch.arange(30) * 0.5]).cuda()
+    x = torch.stack([(halves + low) * 2.0 ** e for low in (0.0, -8.0) for e in (-12, -3, 0, 5, 10)])
+    k = x[:, None, None].to(torch.bfloat16)  # [groups][1][1][32]
+    assert torch.equal(k[:, 0, 0].float(), x)
+    c = make_cache(len(x), 1, 32, 16, 16)
+    c.append(k, -k)
+    got_k, got_v = c.read(rows=1, dtype=torch.float32)
+    c.status()
+    assert torch.equal(got_k, ref.stands_for(k).float()) and torch.equal(got_v, ref.stands_for(-k).float())
+    step = (x.amax(1) - x.amin(1)) / 15
+    assert torch.equal(got_k[:, 0, 0], x.amin(1)[:, None] + torch.round((x - x.amin(1)[:, None]) / step[:, None]) * step[:, None])
+
+
 def test_bad_pages_and_positions_are_skipped_and_reported(dev):
     from eagle_speculative_decoding_draft_gb300._lib import EagleError
     g = gen(5)
