@@ -388,6 +388,7 @@ __global__ void __launch_bounds__(kThreads, Shape<G, NQ>::kBlocks) kv4_attention
                                 }
                         }
                 }
+                __syncwarp();  // lanes whose queries see different keys took different ways; the MMAs take the warp as one
 #pragma unroll
                 for (int g = 0; g < G; ++g)
 #pragma unroll
@@ -665,6 +666,7 @@ __global__ void __launch_bounds__(kThreads, Shape<G, NQ>::kBlocks) kv4_attention
                 }
             }
         }
+        __syncwarp();  // lanes without a row meet the others
     } while (w.next(k, p));
 }
 

@@ -593,6 +593,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
                 const int32_t node = row / k.group;
                 if (h == 0) row_at[j][r] = live ? (node << 16) | (w.hk * k.group + row - node * k.group) : -1;
             }
+            __syncwarp();
             named_barrier_sync(1 + j, 256);
             // the stream's queries, whole rows at a time: scaled, to fp16, and what turns a row's
             // scores to base 2
@@ -631,6 +632,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.q_full[j]);
+            __syncwarp();
             {
                 uint32_t z[16];
 #pragma unroll
@@ -739,6 +741,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.p_full[j]);
+                __syncwarp();
             }
             gt += tiles;
             // ---------------- the segment's output ----------------
@@ -771,7 +774,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
                 L = w0 * l0 + w1 * l1;
             }
             const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-            const bool ok = !*abort_flag;
+            const bool ok = __all_sync(kFull, !*abort_flag);
             // 16 columns at a time: a half of the stream's, or a quarter of both streams' sum, with
             // head_dim 32 and 96 every fourth 16 of it (for all it took the 2047-token piece 688 -> 722 us)
             constexpr bool kQuarters = D % 64 == 0;
@@ -797,9 +800,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
 #pragma unroll
                     for (int i = 0; i < 16; ++i) x[i] = 0.0f;
                 }
-                if (!live || !ok) continue;
                 // columns 8 i + (0 .. 7) are dims 8 i + (0 4 1 5 2 6 3 7)
-                if (whole) {
+                if (live && ok && whole) {
                     // over the stream's queries, which no MMA reads any more; a unit of at most 128
                     // rows over those of stream 0
                     uint8_t *dst = base + S::kQ + (both ? j * S::kTileBytes : 0u);
@@ -808,7 +810,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
                         *reinterpret_cast<uint4 *>(dst + (c >> 6) * (kKeys * 128) + sw128(r, ((c >> 3) & 7) + i)) =
                             make_uint4(pack_b16(x[8 * i] * inv, x[8 * i + 2] * inv), pack_b16(x[8 * i + 4] * inv, x[8 * i + 6] * inv),
                                        pack_b16(x[8 * i + 1] * inv, x[8 * i + 3] * inv), pack_b16(x[8 * i + 5] * inv, x[8 * i + 7] * inv));
-                } else {
+                } else if (live && ok) {
                     float *dst = k.part_o + (slot * k.rows + ur) * D + c;
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
@@ -816,8 +818,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
                         *reinterpret_cast<float4 *>(dst + 8 * i + 4) = make_float4(x[8 * i + 1], x[8 * i + 3], x[8 * i + 5], x[8 * i + 7]);
                     }
                 }
+                __syncwarp();  // lanes behind the unit's last row meet the others: the next columns are loaded by the warp as one
             }
             if (!whole && live && ok && h == 0 && (both || j == 0)) k.part_ml[slot * k.rows + ur] = make_float2(M, L);
+            __syncwarp();
             tc_fence_before();
             // no output column or sum is overwritten before all of its readers have it, and the rows
             // to be written are all there
@@ -833,6 +837,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
                         *reinterpret_cast<uint4 *>(a.o + ((static_cast<int64_t>(w.b) * a.n + (at >> 16)) * a.H + (at & 0xffff)) * D + 8 * piece) =
                             *reinterpret_cast<const uint4 *>(src + (piece >> 3) * (kKeys * 128) + sw128(orow, piece & 7));
                 }
+                __syncwarp();
                 if (both) named_barrier_sync(1 + j, 256);
                 else named_barrier_sync(3, 512);
             }

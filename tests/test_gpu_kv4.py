@@ -326,6 +326,25 @@ def test_attention_matches_the_definition(dev, case):
     assert torch.equal(o, again)  # bit for bit
 
 
+@pytest.mark.parametrize("D", [64, 96, 128])
+@pytest.mark.parametrize("n", [3, 7, 9, 15, 17, 31, 33, 63, 97, 127, 129, 161, 255, 257, 289])
+def test_warps_that_a_unit_fills_in_part(dev, n, D):
+    """Query rows that end inside a warp's 32 (or 8), in units that one CTA finishes and in split ones,
+    with a NaN that some of the warp's queries see and others do not."""
+    case = (3, n, 1, 1, D, 64, [0, 100, 9000], "causal")
+    made = build(case, 14)
+    c, kc, vc, q, kn, vn, mask = made
+    o = c.attention(q, kn, vn)
+    check_attention(case, made, o)
+    vn[:, n // 2, :, 5] = math.nan
+    bad = c.attention(q, kn, vn)
+    c.status()
+    hit = torch.zeros_like(o, dtype=torch.bool)
+    hit[:, n // 2:, :, 5] = True
+    assert torch.equal(torch.isnan(bad), hit)
+    assert torch.equal(bad[~hit], o[~hit])
+
+
 @pytest.mark.parametrize("kscale,vscale,qscale", [(0.8, 60.0, 1.5), (4.0, 1e-3, 4.0), (0.8, 8000.0, 1.5), (1e-3, 1e-5, 1e3),
                                                   (0.8, 0.8, 1e-30), (0.02, 0.8, 1e30)])
 @pytest.mark.parametrize("case", [(2, 8, 4, 4, 128, 32, [700, 33], "tree"), (2, 65, 8, 2, 128, 64, [300, 1], "tree"),
