@@ -109,6 +109,8 @@ _SIGS = {
     "eagle_kv4_attention": (c_int, [POINTER(KV4CacheStruct), c_int32, c_int32, c_int32, c_void_p, c_int64,
                                     c_void_p, c_void_p, c_int64, c_void_p, c_void_p, c_void_p, c_size_t,
                                     c_void_p, c_void_p]),
+    "eagle_test_kv4_stall": (c_int, [POINTER(KV4CacheStruct), c_int32, c_int32, c_int32] + [c_void_p] * 6
+                             + [c_size_t, c_int64, c_int32, c_void_p, c_void_p]),
     "eagle_decoder_layer_kv4_workspace_bytes": (c_size_t, [POINTER(DecoderLayerWeights), POINTER(KV4CacheStruct),
                                                            c_int32, c_int32]),
     "eagle_decoder_layer_kv4": (c_int, [POINTER(DecoderLayerWeights), POINTER(KV4CacheStruct), c_int32, c_int32]

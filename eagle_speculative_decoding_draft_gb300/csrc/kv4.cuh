@@ -116,6 +116,8 @@ struct Kv4Attention {
     __nv_bfloat16 *o;              // [B][n][H * D]
     void *ws;
     int32_t *status;
+    uint64_t limit_ns = kWaitLimitNs;  // of every wait
+    int32_t stall = INT32_MAX;         // (tests) the tile from which a CTA's copying warp sends nothing
 };
 // False: more key tiles over all units than 32 bits count (launch_kv4_attention then refuses).
 bool kv4_attention_fits(const Kv4View &cache, int32_t B, int32_t n, int32_t H, bool new_keys);

@@ -155,8 +155,9 @@ __global__ void __launch_bounds__(kThreads, Shape<G, NQ>::kBlocks) kv4_attention
                 const int32_t tiles = min(k1 - kt, 8);
                 for (int32_t j = 0; j < tiles; ++j, ++issued) {
                     const int32_t st = issued % kStages;
-                    if (issued >= kStages && lane == 0) kv4_wait(&empty[st], issued / kStages - 1, abort_flag);
+                    if (issued >= kStages && lane == 0) kv4_wait(&empty[st], issued / kStages - 1, abort_flag, a.limit_ns);
                     dead = __shfl_sync(kFull, static_cast<int>(*abort_flag), 0) != 0;
+                    dead = dead || issued >= a.stall;
                     if (dead) break;
                     const bool my = (lane >> 2) == j;
                     const uint32_t have = __ballot_sync(kFull, my && src);
@@ -175,7 +176,7 @@ __global__ void __launch_bounds__(kThreads, Shape<G, NQ>::kBlocks) kv4_attention
         if (lane == 0)
             for (int32_t i = max(issued - kStages, 0); i < issued; ++i)
                 mbar_wait(&full[i % kStages], static_cast<uint32_t>(i / kStages) & 1u, nullptr);
-        if (dead && lane == 0) latch(a.status, kDevTimeout);
+        if (lane == 0 && *abort_flag) latch(a.status, kDevTimeout);
         return;
     }
 
@@ -438,7 +439,8 @@ __global__ void __launch_bounds__(kThreads, Shape<G, NQ>::kBlocks) kv4_attention
             const int32_t count = min(w.s1 - s, 2);
             const int32_t st0 = stage, st1 = stage + 1 == kStages ? 0 : stage + 1;
             const uint32_t turn1 = turn + (st1 == 0 ? 1 : 0);
-            const bool come = kv4_wait(&full[st0], turn, abort_flag) && (count < 2 || kv4_wait(&full[st1], turn1, abort_flag));
+            const bool come = kv4_wait(&full[st0], turn, abort_flag, a.limit_ns) &&
+                              (count < 2 || kv4_wait(&full[st1], turn1, abort_flag, a.limit_ns));
             int32_t nv[2];  // keys of the chunks that are there
             nv[0] = valid[st0][warp];
             nv[1] = count == 2 ? valid[st1][warp] : 0;
@@ -856,24 +858,12 @@ cudaError_t launch_kv4_attention(const Kv4Attention &a, cudaStream_t st) {
     return launch_pdl(kv4_merge_kernel, dim3(grid, std::min(k.rows / kMergeRows, 16)), dim3(kMergeRows * 32), 0, st, k);
 }
 
-}  // namespace eagle
+namespace {
 
-extern "C" {
-
-size_t eagle_kv4_attention_workspace_bytes(const eagle_kv4_cache *cache, int32_t nodes, int32_t heads) {
-    eagle::Kv4View v;
-    if (!eagle::kv4_view(cache, &v) || nodes < 1 || nodes > eagle::kMaxCandidates + 1) return 0;
-    if (heads < 1 || heads > 65536 || heads % v.Hk) return 0;
-    return eagle::kv4_attention_workspace(v.Hk, v.G, heads, nodes);
-}
-
-eagle_status eagle_kv4_attention(const eagle_kv4_cache *cache, int32_t batch, int32_t nodes, int32_t heads,
-                                 const void *d_q, int64_t ldq, const void *d_k, const void *d_v, int64_t ldkv,
-                                 const uint32_t *d_mask, void *d_out, void *d_ws, size_t ws_bytes, int32_t *d_status,
-                                 eagle_stream_t stream) {
-    using namespace eagle;
-    NvtxRange nvtx_range("eagle_kv4_attention");
-    Kv4Attention a{};
+// The call on the host: checks, and the launches.  `a` holds what differs from an ordinary call.
+eagle_status attention(Kv4Attention a, const eagle_kv4_cache *cache, int32_t batch, int32_t nodes, int32_t heads, const void *d_q,
+                       int64_t ldq, const void *d_k, const void *d_v, int64_t ldkv, const uint32_t *d_mask, void *d_out,
+                       void *d_ws, size_t ws_bytes, int32_t *d_status, eagle_stream_t stream) {
     if (!kv4_view(cache, &a.cache) || batch < 0 || nodes < 1 || nodes > kMaxCandidates + 1) return EAGLE_ERR_INVALID_ARG;
     if (heads < 1 || heads > 65536 || heads % a.cache.Hk) return EAGLE_ERR_INVALID_ARG;
     if (batch == 0) return EAGLE_OK;
@@ -904,6 +894,39 @@ eagle_status eagle_kv4_attention(const eagle_kv4_cache *cache, int32_t batch, in
     a.status = d_status;
     const cudaError_t e = launch_kv4_attention(a, reinterpret_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? EAGLE_OK : (e == cudaErrorNotSupported ? EAGLE_ERR_UNSUPPORTED : EAGLE_ERR_CUDA);
+}
+
+}  // namespace
+}  // namespace eagle
+
+extern "C" {
+
+size_t eagle_kv4_attention_workspace_bytes(const eagle_kv4_cache *cache, int32_t nodes, int32_t heads) {
+    eagle::Kv4View v;
+    if (!eagle::kv4_view(cache, &v) || nodes < 1 || nodes > eagle::kMaxCandidates + 1) return 0;
+    if (heads < 1 || heads > 65536 || heads % v.Hk) return 0;
+    return eagle::kv4_attention_workspace(v.Hk, v.G, heads, nodes);
+}
+
+eagle_status eagle_kv4_attention(const eagle_kv4_cache *cache, int32_t batch, int32_t nodes, int32_t heads,
+                                 const void *d_q, int64_t ldq, const void *d_k, const void *d_v, int64_t ldkv,
+                                 const uint32_t *d_mask, void *d_out, void *d_ws, size_t ws_bytes, int32_t *d_status,
+                                 eagle_stream_t stream) {
+    eagle::NvtxRange nvtx_range("eagle_kv4_attention");
+    return eagle::attention(eagle::Kv4Attention{}, cache, batch, nodes, heads, d_q, ldq, d_k, d_v, ldkv, d_mask, d_out, d_ws,
+                            ws_bytes, d_status, stream);
+}
+
+eagle_status eagle_test_kv4_stall(const eagle_kv4_cache *cache, int32_t batch, int32_t nodes, int32_t heads, const void *d_q,
+                                  const void *d_k, const void *d_v, const uint32_t *d_mask, void *d_out, void *d_ws,
+                                  size_t ws_bytes, int64_t limit_ns, int32_t tile, int32_t *d_status, eagle_stream_t stream) {
+    if (!cache || limit_ns < 1 || limit_ns > 10000000000ll || tile < 0) return EAGLE_ERR_INVALID_ARG;
+    eagle::Kv4Attention a{};
+    a.limit_ns = static_cast<uint64_t>(limit_ns);
+    a.stall = tile;
+    return eagle::attention(a, cache, batch, nodes, heads, d_q, static_cast<int64_t>(heads) * cache->head_dim, d_k, d_v,
+                            static_cast<int64_t>(cache->kv_heads) * cache->head_dim, d_mask, d_out, d_ws, ws_bytes, d_status,
+                            stream);
 }
 
 }  // extern "C"

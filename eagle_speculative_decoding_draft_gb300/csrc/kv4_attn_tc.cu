@@ -354,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
     const uint32_t tmem = __shfl_sync(kFull, tmem_base, 0);
     const Walk &w = walks[warp];
     auto next_unit = [&]() { return kv4_next(k, place, walks[warp]); };
-    auto wait = [&](uint64_t *b, uint32_t parity) -> bool { return kv4_wait(b, parity, abort_flag); };
+    auto wait = [&](uint64_t *b, uint32_t parity) -> bool { return kv4_wait(b, parity, abort_flag, a.limit_ns); };
     auto rows_of = [&]() { return min(kKv4TcRows, k.Mq - w.qt * kKv4TcRows); };  // rows of the unit
 
     if (warp >= 16 && warp < 24) {
@@ -496,6 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
                     const uint32_t rs = raw % kRaw;
                     if (raw >= kRaw && lane == 0) wait(&bar.raw_empty[rs], raw / kRaw - 1);
                     dead = __shfl_sync(kFull, static_cast<int>(*abort_flag), 0) != 0;
+                    dead = dead || static_cast<int32_t>(raw >> 1) >= a.stall;
                     if (dead) break;
                     const bool my = (lane >> 3) == (hh >> 1);
                     const uint32_t have = __ballot_sync(kFull, my && src);
@@ -698,7 +699,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
                 }
                 // the row's maximum over both halves
                 half_max[j][n_s & 1u][h][r] = mx;  // the other one at every second tile
-                named_barrier_sync(1 + j, 256);
+                bool odd_values = false;  // whether a new tile's values hold what fp16 does not
+                if (i < fresh) {
+                    // one answer for the stream, whose threads all go on to the next barrier or none: where the
+                    // wait has given up, the mark may be changing
+                    const bool come = wait(&bar.v_full[t & 1], t >> 1);
+                    const bool odd = *reinterpret_cast<const volatile uint32_t *>(odd_tile[t & 3][1]) != 0;
+                    __syncwarp();
+                    odd_values = named_barrier_or(1 + j, 256, come && odd);
+                } else {
+                    named_barrier_sync(1 + j, 256);
+                }
                 mx = fmaxf(mx, half_max[j][n_s & 1u][h ^ 1][r]);
                 ++n_s;
                 mx = mx == -INFINITY ? mx : mx * mul;  // mul may underflow to 0
@@ -723,18 +734,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
                     }
                     tmem_wait_st();
                 }
-                if (i < fresh) {
-                    // whether the tile's values hold what fp16 does not
-                    wait(&bar.v_full[t & 1], t >> 1);
+                if (odd_values) {
+                    const int32_t s = w.s0 + i, key0 = s * kKeys;
+                    uint4 see = make_uint4(0u, 0u, 0u, 0u);
+                    if (live) see = make_uint4(new_seen(key0), new_seen(key0 + 32), new_seen(key0 + 64), new_seen(key0 + 96));
                     __syncwarp();
-                    if (*reinterpret_cast<const volatile uint32_t *>(odd_tile[t & 3][1]) != 0) {
-                        const int32_t s = w.s0 + i, key0 = s * kKeys;
-                        uint4 see = make_uint4(0u, 0u, 0u, 0u);
-                        if (live) see = make_uint4(new_seen(key0), new_seen(key0 + 32), new_seen(key0 + 64), new_seen(key0 + 96));
-                        if (used)
-                            add_odd_values(a.vn + new_row(s), a.ldkv, min(a.n - s * kKeys, kKeys), see, mul, sub, t_s, t_o, h * (D / 2), (h + 1) * (D / 2));
-                        named_barrier_sync(1 + j, 256);  // both halves have read the scores that p overwrites
-                    }
+                    if (used)
+                        add_odd_values(a.vn + new_row(s), a.ldkv, min(a.n - s * kKeys, kKeys), see, mul, sub, t_s, t_o, h * (D / 2), (h + 1) * (D / 2));
+                    named_barrier_sync(1 + j, 256);  // both halves have read the scores that p overwrites
                 }
                 if (used) l += __any_sync(kFull, fabsf(sub) > 1048576.0f) ? probabilities_in_steps(t_h, mul, sub) : probabilities(t_h, mul, sub);
                 tmem_wait_st();

@@ -71,9 +71,9 @@ __device__ __forceinline__ bool try_wait_long(uint64_t *bar, uint32_t parity) {
     return ok != 0;
 }
 // Waits for `parity` (its lowest bit) on `bar`.  Gives up when *abort is set, and sets it after
-// kWaitLimitNs.  Small, so that the kernels' loops stay in the instruction cache: the clock is looked
+// limit_ns.  Small, so that the kernels' loops stay in the instruction cache: the clock is looked
 // at once in 64 tries.
-__device__ __forceinline__ bool kv4_wait(uint64_t *bar, uint32_t parity, volatile int32_t *abort) {
+__device__ __forceinline__ bool kv4_wait(uint64_t *bar, uint32_t parity, volatile int32_t *abort, uint64_t limit_ns) {
     uint64_t since = 0;
     for (uint32_t i = 1;; ++i) {
         if (try_wait_long(bar, parity & 1u)) return true;
@@ -82,7 +82,7 @@ __device__ __forceinline__ bool kv4_wait(uint64_t *bar, uint32_t parity, volatil
             const uint64_t now = global_timer_ns();
             if (since == 0) {
                 since = now;
-            } else if (now - since > kWaitLimitNs) {
+            } else if (now - since > limit_ns) {
                 *abort = 1;
                 return false;
             }

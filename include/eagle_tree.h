@@ -609,6 +609,19 @@ EAGLE_API eagle_status eagle_kv4_attention(const eagle_kv4_cache *cache, int32_t
                                            size_t ws_bytes, int32_t *d_status, eagle_stream_t stream);
 
 /*
+ * Test hook (no counterpart on the pages): the attention with limit_ns (1 .. 10^10) in place of its
+ * waits' two seconds, in which each CTA's copying warp stops at its cached tile number `tile`: the other
+ * warps' waits run out and the call latches EAGLE_ERR_DEVICE_TIMEOUT in *d_status; what d_out then
+ * holds is not defined.  q, k and v are contiguous; the other arguments and errors are
+ * eagle_kv4_attention's.
+ */
+EAGLE_API eagle_status eagle_test_kv4_stall(const eagle_kv4_cache *cache, int32_t batch, int32_t nodes,
+                                            int32_t heads, const void *d_q, const void *d_k,
+                                            const void *d_v, const uint32_t *d_mask, void *d_out,
+                                            void *d_ws, size_t ws_bytes, int64_t limit_ns, int32_t tile,
+                                            int32_t *d_status, eagle_stream_t stream);
+
+/*
  * The draft decoder layer over a 4-bit cache: eagle_decoder_layer with the cached keys and values
  * read by eagle_kv4_attention, each request with its own length.  cache->kv_heads and head_dim must be
  * the layer's; the other arguments, limits and rounding points are those of eagle_decoder_layer

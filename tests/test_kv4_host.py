@@ -84,6 +84,15 @@ def test_attention_refuses(lib, kw):
     assert attend(lib, cache(), **kw) == 1
 
 
+@pytest.mark.parametrize("limit,tile", [(0, 0), (-1, 0), (10 ** 10 + 1, 0), (1000, -1)])
+def test_stall_hook_refuses(lib, limit, tile):
+    c = cache()
+    call = lambda cache_ref, limit, tile: lib.eagle_test_kv4_stall(cache_ref, 2, 3, 4, P(256), P(256), P(256), None, P(256), P(256), 1 << 40,
+                                                                   limit, tile, None, None)
+    assert call(ctypes.byref(c), limit, tile) == 1
+    assert call(None, 1000, 0) == 1 and call(ctypes.byref(cache(page_size=24)), 1000, 0) == 1
+
+
 def test_empty_batches_do_nothing(lib):
     c = cache()
     assert append(lib, c, batch=0, k=None, v=None) == 0
