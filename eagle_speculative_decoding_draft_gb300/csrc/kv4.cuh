@@ -66,11 +66,10 @@ __device__ __forceinline__ uint8_t *kv4_chunk(const Kv4View &v, int32_t b, int32
     return v.pages + ((static_cast<int64_t>(page) * v.Hk + hk) * per + in_page) * kv4_chunk_bytes(v.G);
 }
 
-// Cached positions of request b, clamped to what its pages can hold.
-__device__ __forceinline__ int64_t kv4_length(const Kv4View &v, int32_t b) {
-    const int64_t len = v.lengths[b];
-    return len < 0 ? 0 : (len > v.cap ? v.cap : len);
-}
+// A length as lengths[] gives it, clamped to what a request's pages can hold.
+__device__ __forceinline__ int64_t kv4_clamped(const Kv4View &v, int64_t len) { return len < 0 ? 0 : (len > v.cap ? v.cap : len); }
+// Cached positions of request b.
+__device__ __forceinline__ int64_t kv4_length(const Kv4View &v, int32_t b) { return kv4_clamped(v, v.lengths[b]); }
 
 // Host: fills a view from the caller's description.  False when a size or pointer is unusable.
 bool kv4_view(const eagle_kv4_cache *c, Kv4View *out);

@@ -110,6 +110,8 @@ __global__ void __launch_bounds__(kThreads, Shape<G, NQ>::kBlocks) kv4_attention
     __shared__ int32_t abort_mark;
     __shared__ int32_t red[kThreads / 32];
     __shared__ Spot spots[2];
+    __shared__ Place place;
+    __shared__ Lengths lens;
     const int32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
@@ -123,16 +125,18 @@ __global__ void __launch_bounds__(kThreads, Shape<G, NQ>::kBlocks) kv4_attention
     // which all must be resident at once (64 8-node trees back to back: 150 us with it, 115 without)
     pdl_wait();
     const Kv4Attention &a = k.a;
-    Place p;
-    const bool busy = find_place(k, &p, red, spots);
-    __syncthreads();  // the mbarriers too
-    if (!busy) {
+    if (!find_place(k, place, lens, red, spots)) {  // all threads meet there: the mbarriers are ready, too
         if (threadIdx.x == 0) k.share[blockIdx.x].kind = 0;
         return;
     }
+    const Place p = place;
     volatile int32_t *abort_flag = &abort_mark;
     Walk w;
-    w.start(k, p);
+    w.start(k, p, lens);
+    auto next_unit = [&]() {
+        meet(k, p, w, lens, kThreads, warp == kWarps);
+        return w.next(k, p, lens);
+    };
     if (threadIdx.x == 0) k.share[blockIdx.x] = share_of(w);
 
     if (warp == kWarps) {
@@ -140,7 +144,7 @@ __global__ void __launch_bounds__(kThreads, Shape<G, NQ>::kBlocks) kv4_attention
         int32_t issued = 0;
         bool dead = false;
         do {
-            if (lane == 0 && w.len != a.cache.lengths[w.b]) latch(a.status, kDevBounds);  // clamped
+            if (lane == 0 && w.len != lens.of(w.b)) latch(a.status, kDevBounds);  // clamped
             const int32_t k0 = max(w.s0 - w.nt, 0), k1 = w.s1 - w.nt;
             for (int32_t kt = k0; kt < k1 && !dead; kt += 8) {
                 // the chunks of 8 tiles, one a lane
@@ -171,7 +175,7 @@ __global__ void __launch_bounds__(kThreads, Shape<G, NQ>::kBlocks) kv4_attention
                                   kv4_chunk_bytes(G), &full[st]);
                 }
             }
-        } while (!dead && w.next(k, p));
+        } while (next_unit());
         // every copy has landed before the block's memory is handed on
         if (lane == 0)
             for (int32_t i = max(issued - kStages, 0); i < issued; ++i)
@@ -669,7 +673,7 @@ __global__ void __launch_bounds__(kThreads, Shape<G, NQ>::kBlocks) kv4_attention
             }
         }
         __syncwarp();  // lanes without a row meet the others
-    } while (w.next(k, p));
+    } while (next_unit());
 }
 
 // Units that several CTAs worked on: block (c, .) merges the unit that CTA c is the second to work on.

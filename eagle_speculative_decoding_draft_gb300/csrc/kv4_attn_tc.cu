@@ -44,7 +44,8 @@
 // Tiles are made of blocks of 64 dims; with head_dim 32 and 96 half of the last one lies idle and the
 // MMAs stop before it (1000 tokens of two prompts over 4096 cached ones, 32 heads of 96: 179 us, where
 // the register kernel with 32 rows a unit took 1935).
-// TMEM: S0 S1 O0 O1, 128 columns each (O uses D).  Every wait is bounded.
+// TMEM: S0 S1 O0 O1, 128 columns each (O uses D).  Every wait on an mbarrier is bounded; the roles meet at
+// named barriers as often as the units and tiles say, also after a wait has given up.
 #include <type_traits>
 
 #include "kernels.cuh"
@@ -303,6 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
     __shared__ int32_t red[kThreads / 32];
     __shared__ Spot spots[2];
     __shared__ Place place;
+    __shared__ Lengths lens;
     __shared__ Walk walks[kThreads / 32];  // each warp's: in registers they would be spilled, and L1 is all shared memory here
     const int32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     volatile int32_t *abort_flag = &abort_mark;
@@ -327,22 +329,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
         fence_barrier_init();
     }
     pdl_wait();  // and no early launch of dependents (kv4_attn.cu)
-    {
-        Place p;
-        const bool busy = find_place(k, &p, red, spots);
-        if (!busy) {
-            if (threadIdx.x == 0) k.share[blockIdx.x].kind = 0;
-            return;
-        }
-        if (lane == 0) {
-            Walk first;
-            first.start(k, p);
-            walks[warp] = first;
-            if (warp == 0) {
-                place = p;
-                k.share[blockIdx.x] = share_of(first);
-            }
-        }
+    if (!find_place(k, place, lens, red, spots)) {
+        if (threadIdx.x == 0) k.share[blockIdx.x].kind = 0;
+        return;
+    }
+    if (lane == 0) {
+        Walk first;
+        first.start(k, place, lens);
+        walks[warp] = first;
+        if (warp == 0) k.share[blockIdx.x] = share_of(first);
     }
     if (warp == 24) {
         tmem_alloc(&tmem_base, kTmemCols);
@@ -353,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(kFull, tmem_base, 0);
     const Walk &w = walks[warp];
-    auto next_unit = [&]() { return kv4_next(k, place, walks[warp]); };
+    auto next_unit = [&]() { return kv4_next(k, place, walks[warp], lens, kThreads, warp == 25); };
     auto wait = [&](uint64_t *b, uint32_t parity) -> bool { return kv4_wait(b, parity, abort_flag, a.limit_ns); };
     auto rows_of = [&]() { return min(kKv4TcRows, k.Mq - w.qt * kKv4TcRows); };  // rows of the unit
 
@@ -479,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
         uint32_t raw = 0;
         bool dead = false;
         do {
-            if (lane == 0 && w.len != a.cache.lengths[w.b]) latch(a.status, kDevBounds);  // clamped
+            if (lane == 0 && w.len != lens.of(w.b)) latch(a.status, kDevBounds);  // clamped
             const int32_t k0 = max(w.s0 - w.nt, 0), k1 = w.s1 - w.nt;
             for (int32_t kt = k0; kt < k1 && !dead; kt += 4) {
                 // the chunks of four tiles, one a lane
@@ -509,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
                                   &bar.raw_full[rs]);
                 }
             }
-        } while (!dead && next_unit());
+        } while (next_unit());
         // every copy has landed before the block's memory is handed on
         if (lane == 0)
             for (uint32_t i = raw > kRaw ? raw - kRaw : 0; i < raw; ++i) mbar_wait(&bar.raw_full[i % kRaw], (i / kRaw) & 1u, nullptr);
@@ -526,6 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
         auto wait_all = [&](uint64_t *b, uint32_t parity) -> bool { return __all_sync(kFull, wait(b, parity)); };
         bool ok = true;
         do {
+            if (!ok) continue;
             const int32_t tiles = __shfl_sync(kFull, w.s1 - w.s0, 0);
             const uint32_t both = __shfl_sync(kFull, rows_of() > 128 ? 1 : 0, 0);
             const int32_t n = tiles << both;
@@ -572,7 +568,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
             }
             gt += tiles;
             ++seg;
-        } while (ok && next_unit());
+        } while (next_unit());
         // what was issued lands before the block's memory is handed on
         commit_to(&bar.drain, leader);
         mbar_wait(&bar.drain, 0, nullptr);

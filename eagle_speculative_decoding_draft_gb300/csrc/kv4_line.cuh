@@ -108,6 +108,20 @@ __device__ __forceinline__ int32_t cached_tiles(const Kv4Args &k, int32_t len) {
 }
 __device__ __forceinline__ int32_t length_of(const Kv4Args &k, int32_t b) { return static_cast<int32_t>(kv4_length(k.a.cache, b)); }
 
+// The lengths that a CTA goes by, as lengths[] gave them: those of the 32 requests that it is at and of the
+// next 32, in shared memory.  One reading for all of its warps: they meet at barriers, so they have to
+// take the same units and tiles even if the lengths are written to under the call.
+struct Lengths {
+    int32_t raw[2][32];
+    __device__ __forceinline__ int32_t of(int32_t b) const { return raw[(b >> 5) & 1][b & 31]; }
+};
+constexpr uint32_t kLengthsBarrier = 4;
+// The 32 requests from b on, a multiple of 32.  One warp.
+__device__ __forceinline__ void read_lengths(const Kv4Args &k, Lengths &lens, int32_t b) {
+    const int32_t lane = threadIdx.x & 31;
+    lens.raw[(b >> 5) & 1][lane] = b + lane < k.a.B ? k.a.cache.lengths[b + lane] : 0;
+}
+
 // A CTA's tiles [begin, end) of the line, and the unit that the first of them belongs to.
 struct Place {
     int32_t begin, end;
@@ -181,10 +195,10 @@ __device__ __forceinline__ bool place_at(const Kv4Args &k, Place *p, uint32_t to
     return cut0 < cut1;
 }
 
-// At most 32 requests: every warp finds the place by itself (one request a lane), with no barrier.
-__device__ __forceinline__ bool find_place_warp(const Kv4Args &k, Place *p) {
+// At most 32 requests: one warp, a request a lane.
+__device__ __forceinline__ bool find_place_warp(const Kv4Args &k, Place *p, const Lengths &lens) {
     const int32_t lane = threadIdx.x & 31;
-    const int32_t ct = lane < k.a.B ? cached_tiles(k, length_of(k, lane)) : 0;
+    const int32_t ct = lane < k.a.B ? cached_tiles(k, static_cast<int32_t>(kv4_clamped(k.a.cache, lens.of(lane)))) : 0;
     int32_t per;
     if (k.QT == 1 || k.a.mask || !k.a.kn) {
         per = k.QT * new_tiles(k, 0);
@@ -231,6 +245,8 @@ static __device__ __noinline__ int32_t block_sum(int32_t v, int32_t *red) {
 // More: all threads of the block together.
 static __device__ __noinline__ bool find_place_block(const Kv4Args &k, Place *p, int32_t *red, Spot *spots) {
     const int32_t tid = threadIdx.x, nt = blockDim.x, B = k.a.B, Hk = k.a.cache.Hk;
+    // kept where lengths that were written to between the two looks at them put no request behind a cut
+    if (tid < 2) spots[tid] = Spot{B - 1, Hk - 1, k.QT - 1, 0, 1};
     int32_t per = 0;
     if (k.a.mask || !k.a.kn) {
         per = k.QT * new_tiles(k, 0);
@@ -272,10 +288,27 @@ static __device__ __noinline__ bool find_place_block(const Kv4Args &k, Place *p,
         if (cut[1] < base) break;
     }
     __syncthreads();
-    return place_at(k, p, total, ctas, cut[0], cut[1], spots[0], spots[static_cast<uint32_t>(cut[1]) < total]);
+    return place_at(k, p, total, ctas, cut[0], cut[1], spots[0], spots[static_cast<uint32_t>(cut[1]) < total]) && p->b < B;
 }
-__device__ __forceinline__ bool find_place(const Kv4Args &k, Place *p, int32_t *red, Spot *spots) {
-    return k.a.B <= 32 ? find_place_warp(k, p) : find_place_block(k, p, red, spots);
+// The CTA's place and the lengths there, in shared memory; all threads together.  False: nothing to do.
+__device__ __forceinline__ bool find_place(const Kv4Args &k, Place &place, Lengths &lens, int32_t *red, Spot *spots) {
+    const Place none{0, 0, 0, 0, 0, 0};
+    if (k.a.B <= 32) {
+        if (threadIdx.x < 32) {
+            Place p;
+            read_lengths(k, lens, 0);
+            __syncwarp();
+            const bool busy = find_place_warp(k, &p, lens);
+            if (threadIdx.x == 0) place = busy ? p : none;
+        }
+    } else {
+        Place p;
+        const bool busy = find_place_block(k, &p, red, spots);
+        if (busy && threadIdx.x < 64) read_lengths(k, lens, (p.b & ~31) + static_cast<int32_t>(threadIdx.x & 32));
+        if (threadIdx.x == 0) place = busy ? p : none;
+    }
+    __syncthreads();
+    return place.begin < place.end;
 }
 
 // A CTA's run through the line, unit by unit: [s0, s1) of the unit's tiles.
@@ -285,21 +318,27 @@ struct Walk {
     int32_t nt;  // tiles of new keys (the unit's first)
     int32_t len;
 
-    __device__ __forceinline__ void start(const Kv4Args &k, const Place &p) {
+    __device__ __forceinline__ void start(const Kv4Args &k, const Place &p, const Lengths &lens) {
         b = p.b;
         hk = p.hk;
         qt = p.qt;
         t = p.begin;
         s0 = p.off;
-        len = length_of(k, b);
+        len = static_cast<int32_t>(kv4_clamped(k.a.cache, lens.of(b)));
         fill(k, p);
     }
     __device__ __forceinline__ void fill(const Kv4Args &k, const Place &p) {
         nt = new_tiles(k, qt);
         unit = cached_tiles(k, len) + nt;
+        s0 = min(s0, unit - 1);  // the place may come from an earlier length
         s1 = min(unit, s0 + (p.end - t));
     }
-    __device__ __forceinline__ bool next(const Kv4Args &k, const Place &p) {
+    // Whether the next unit is of a request of another 32.
+    __device__ __forceinline__ bool leaves(const Kv4Args &k, const Place &p) const {
+        return ((b + 1) & 31) == 0 && b + 1 < k.a.B && hk + 1 == k.a.cache.Hk && qt + 1 == k.QT && t + s1 - s0 < p.end;
+    }
+    // (meet comes first)
+    __device__ __forceinline__ bool next(const Kv4Args &k, const Place &p, const Lengths &lens) {
         t += s1 - s0;
         if (t >= p.end) return false;
         s0 = 0;
@@ -307,8 +346,8 @@ struct Walk {
             qt = 0;
             if (++hk == k.a.cache.Hk) {
                 hk = 0;
-                if (++b == k.a.B) return false;  // lengths changed under the call
-                len = length_of(k, b);
+                if (++b == k.a.B) return false;  // lengths were written to under the call
+                len = static_cast<int32_t>(kv4_clamped(k.a.cache, lens.of(b)));
             }
         }
         fill(k, p);
@@ -316,13 +355,24 @@ struct Walk {
     }
 };
 
+// Ahead of the next unit: where its request is of another 32, all of the CTA's `threads` meet, after which
+// none needs the 32 before, and the warp with `reads` set brings the lengths of those after.  Every warp
+// comes here for every unit, also once a wait has given up.
+__device__ __forceinline__ void meet(const Kv4Args &k, const Place &p, const Walk &w, Lengths &lens, uint32_t threads, bool reads) {
+    if (!w.leaves(k, p)) return;
+    __syncwarp();
+    named_barrier_sync(kLengthsBarrier, threads);
+    if (reads) read_lengths(k, lens, w.b + 33);
+}
+
 // On to the next unit of a walk in shared memory that the warp's lanes read; false behind the last.
-__device__ __forceinline__ bool kv4_next(const Kv4Args &k, const Place &p, Walk &walk) {
+__device__ __forceinline__ bool kv4_next(const Kv4Args &k, const Place &p, Walk &walk, Lengths &lens, uint32_t threads, bool reads) {
+    meet(k, p, walk, lens, threads, reads);
     __syncwarp();  // every lane is through with the last
     int more = 0;
     if ((threadIdx.x & 31) == 0) {
         Walk w = walk;
-        more = w.next(k, p);
+        more = w.next(k, p, lens);
         walk = w;
     }
     more = __shfl_sync(kFull, more, 0);

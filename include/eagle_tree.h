@@ -596,7 +596,9 @@ EAGLE_API eagle_status eagle_kv4_read(const eagle_kv4_cache *cache, int32_t batc
  * d_ws: eagle_kv4_attention_workspace_bytes bytes, 256-byte aligned, of any content; calls that may
  * run at the same time (other streams, graphs replayed side by side) need workspaces of their own.
  * The size depends on the current device, not on the batch or the lengths.  Results do not depend on
- * what else runs, and are the same in every call with the same lengths.
+ * what else runs, and are the same in every call with the same lengths.  Nothing may write to the pages,
+ * table or lengths of the call's requests while it runs: lengths or a table that change under it make its
+ * outputs undefined (it still ends, and touches nothing but the pool, its outputs and its workspace).
  * Errors: INVALID_ARG, CUDA; UNSUPPORTED where batch * kv_heads * tiles of query rows (8 to 256) *
  * tiles of keys (64 or 128) of a full cache passes 2^31.
  */

@@ -326,6 +326,64 @@ def test_attention_matches_the_definition(dev, case):
     assert torch.equal(o, again)  # bit for bit
 
 
+def many_requests(B, n, kind, D=64, base=50):
+    """B requests that repeat `base` ones (their pages shared): more than 32 for every CTA of the device."""
+    case = (base, n, 1, 1, D, 16, [i * 37 % 101 for i in range(base)], kind)
+    c0, kc, vc, q, kn, vn, mask = made = build(case, 15)
+    from eagle_speculative_decoding_draft_gb300 import KV4Cache
+    again = torch.arange(B, device="cuda") % base
+    c = KV4Cache(B, 1, D, num_pages=c0.num_pages, max_pages=c0.max_pages, page_size=16, pages=c0.pages)
+    c.table.copy_(c0.table[again])
+    c.lengths.copy_(c0.lengths[again])
+    return case, made, again, c, [None if x is None else x[again].contiguous() for x in (q, kn, vn, mask)]
+
+
+MANY = [(20000, 1, "causal"), (9000, 3, "cache"), (8000, 17, "causal"), (6100, 20, "tree")]
+
+
+@pytest.mark.parametrize("B,n,kind", MANY, ids=lambda v: str(v))
+def test_thousands_of_short_requests(dev, B, n, kind):
+    """Runs of a CTA over more than 32 requests, at whose ends the next lengths are read."""
+    case, made, again, c, (q, kn, vn, mask) = many_requests(B, n, kind)
+    o = c.attention(q, kn, vn, mask=mask)
+    c.status()
+    base, lens = case[0], case[6]
+    for b in range(base):  # every copy of the request (the line cuts them at other places)
+        t, (kc, vc, q1, kn, vn, mask1) = lens[b], made[1:]
+        see = ref.sees(n, t, None if mask1 is None else mask1[b], "cuda")[:, :t + (0 if kn is None else n)]
+        want, tol = ref.attend(q1[b], kc[b, :t], vc[b, :t], None if kn is None else kn[b], None if vn is None else vn[b], see)
+        assert torch.all((o[b::base].double() - want).abs() <= tol)
+
+
+@pytest.mark.parametrize("B,n,kind", MANY + [(5, 1, "causal"), (5, 70, "tree"), (40, 8, "tree"), (40, 130, "causal")], ids=lambda v: str(v))
+def test_lengths_that_change_under_a_call(dev, B, n, kind):
+    """Outputs are undefined then, but every call ends, no wait runs out, nothing but the outputs is written, and calls
+    after it are right."""
+    case, made, again, c, (q, kn, vn, mask) = many_requests(B, n, kind)
+    lens = c.lengths.clone()
+    other = [torch.zeros_like(lens), torch.full_like(lens, c.capacity), lens.flip(0), (lens * 7 + 3) % (c.capacity + 1), lens]
+    want = c.attention(q, kn, vn, mask=mask)
+    pages = c.pages.clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    done = torch.cuda.Event()
+    for _ in range(20):
+        for _ in range(5):
+            c.attention(q, kn, vn, mask=mask)
+        done.record()
+        while not done.query():
+            with torch.cuda.stream(side):
+                for x in other:
+                    c.lengths.copy_(x)
+            side.synchronize()
+    torch.cuda.synchronize()
+    c.status()
+    assert torch.equal(c.pages, pages)
+    c.lengths.copy_(lens)
+    assert torch.equal(c.attention(q, kn, vn, mask=mask), want)
+    c.status()
+
+
 @pytest.mark.parametrize("D", [64, 96, 128])
 @pytest.mark.parametrize("n", [3, 7, 9, 15, 17, 31, 33, 63, 97, 127, 129, 161, 255, 257, 289])
 def test_warps_that_a_unit_fills_in_part(dev, n, D):
