@@ -63,16 +63,21 @@ struct AppendArgs {
 __device__ __forceinline__ int32_t slots_of(const AppendArgs &a, int32_t b) {
     return a.count ? min(max(a.count[b], 0), a.slots) : a.slots;
 }
-// The request's length after the write: behind its last written slot.  Whole warp.
+// The request's length after the write: behind its last written slot, which is one that names a row and
+// whose position lies in a page that is there.  Looked for from the end, 32 slots at a time.  Whole warp.
 __device__ __forceinline__ int32_t length_after(const AppendArgs &a, int32_t b, int64_t start, int32_t cnt) {
-    int32_t last = cnt;
-    if (a.select) {
-        last = 0;
-        for (int32_t j = threadIdx.x & 31; j < cnt; j += 32)
-            if (static_cast<uint32_t>(a.select[static_cast<int64_t>(b) * a.slots + j]) < static_cast<uint32_t>(a.src_rows)) last = j + 1;
-        last = __reduce_max_sync(kFull, last);
+    int64_t end = min(static_cast<int64_t>(cnt), a.v.cap - start);  // slots up to the capacity
+    for (; end > 0; end -= 32) {
+        const int64_t j = end - 1 - (threadIdx.x & 31);
+        const bool named = j >= 0 && (!a.select || static_cast<uint32_t>(a.select[static_cast<int64_t>(b) * a.slots + j]) <
+                                                       static_cast<uint32_t>(a.src_rows));
+        const uint32_t written = __ballot_sync(kFull, named && kv4_chunk(a.v, b, 0, start + j));
+        if (written) {
+            end -= __ffs(written) - 1;
+            break;
+        }
     }
-    return static_cast<int32_t>(min(start + last, a.v.cap));
+    return static_cast<int32_t>(min(start + max(end, int64_t{0}), a.v.cap));
 }
 
 __device__ __forceinline__ __nv_bfloat162 as_b2(uint32_t x) { return *reinterpret_cast<const __nv_bfloat162 *>(&x); }

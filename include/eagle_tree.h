@@ -553,8 +553,8 @@ EAGLE_API size_t eagle_kv4_pages_bytes(const eagle_kv4_cache *cache);
  *              replace what was drafted behind an earlier position.  A negative start latches
  *              EAGLE_ERR_DEVICE_BOUNDS and leaves the request as it is.
  * lengths[b] becomes start[b] plus the last written slot's number plus one (start[b] if there is
- * none), at most the capacity; slots beyond the capacity latch EAGLE_ERR_DEVICE_BOUNDS.  Positions
- * other than those written keep what they hold.  The slots are written by one launch; where the
+ * none), at most the capacity; slots beyond the capacity, or whose page the table does not name, are not
+ * written and latch EAGLE_ERR_DEVICE_BOUNDS.  Positions other than those written keep what they hold.  The slots are written by one launch; where the
  * lengths are also the starts, a second, small one sets them.  d_start must not overlap
  * cache->lengths other than being it.  Calls that write the same request must not overlap.
  * Errors: INVALID_ARG, CUDA; UNSUPPORTED where batch * kv_heads * chunks of 16 slots passes 2^31.

@@ -214,6 +214,43 @@ def test_bad_pages_and_positions_are_skipped_and_reported(dev):
     assert torch.equal(c.lengths, before)
 
 
+@pytest.mark.parametrize("own_start", [False, True], ids=["behind", "start"])
+def test_lengths_end_behind_the_last_written_slot(dev, own_start):
+    """Trailing slots that name no row, lie behind the capacity or on no page are not written, and a length that
+    counted them would make old bytes of the pool keys."""
+    from eagle_speculative_decoding_draft_gb300._lib import EagleError
+    g = gen(16)
+    B, rows_n, cap, first = 8, 150, 160, [0, 3, 16, 20, 150, 157, 160, 0]
+    c = make_cache(B, 1, 32, cap, 16)
+    c.table[0, 1:] = -1           # one page: 16 of 150 rows
+    c.table[1, 5:] = c.num_pages  # 80 positions
+    c.table[2, :] = -1            # none
+    c.table[3, 3] = -1            # a gap in front of what is written
+    c.table[7, ::2] = -1          # every second page
+    c.lengths.copy_(i32(first))
+    k = rows(g, B, rows_n, 1, 32)
+    c.append(k, k, start=i32(first) if own_start else None)
+    with pytest.raises(EagleError, match="BOUNDS"):
+        c.status()
+    assert c.lengths.tolist() == [16, 80, 16, 160, 160, 160, 160, 150]
+    # rows by name: -1 and rows that are not there behind the last one, slots behind the capacity
+    c.lengths.copy_(i32(first))
+    sel = torch.full((B, 70), -1, dtype=torch.int32, device="cuda")
+    sel[0, 3] = 5                     # position 3 of the only page
+    sel[0, 20] = 6                    # on no page
+    sel[1, :] = torch.arange(70)      # 3 .. 72
+    sel[1, 60:] = rows_n              # no such rows
+    sel[2, 0] = 1                     # on no page: nothing is written
+    sel[3, 30:34] = 1                 # 50 .. 53: in the gap
+    sel[4, [0, 12]] = 1               # 150; 162 lies behind the capacity
+    sel[5, [0, 2]] = 1                # 157, 159
+    sel[6, 0] = 1                     # 160: behind it
+    c.append(k, k, select=sel, start=i32(first) if own_start else None)
+    with pytest.raises(EagleError, match="BOUNDS"):
+        c.status()
+    assert c.lengths.tolist() == [4, 63, 16, 20, 151, 160, 160, 0]
+
+
 def test_pool_beyond_32_bits(dev):
     """Pages whose byte offsets pass 2^32, written, read and attended to."""
     from eagle_speculative_decoding_draft_gb300 import KV4Cache
