@@ -14,7 +14,7 @@
 //                    Warps whose 32 rows lie behind the unit's last skip the softmax.
 //   warps 16-19, 20-23  fill the key and the value tiles: codes become fp16 values m + s c (one fused
 //                    multiply-add: half an fp16 step, 2^-11 relative); new keys and values are
-//                    converted from bf16 (exact but for magnitudes below 2^-14).
+//                    converted from bf16 (exact but for what is said below).
 //   warp 24          issues the MMAs: S = Q K^T (128 x 128 x D, operands in shared memory) and
 //                    O += P V (P from TMEM, V as stored: the MN-major B operand).  The order S0 S1
 //                    [P0] O0 S0' [P1] O1 S1' ... keeps one stream's MMAs under the other's softmax,
@@ -39,8 +39,13 @@
 // kv4_attn.cu).  Within 8 neighbouring dims the tiles hold them in the order 0 4 1 5 2 6 3 7, in
 // which masking a word of codes leaves them; queries are stored in the same order and the output's
 // columns are put right as they leave.
-// New keys or values that fp16 cannot hold (above 65504, infinite, NaN) count as 0 in the tiles, and
-// the rows that see them add their terms one by one: nothing hidden reaches a row, whatever it is.
+// New keys and values come to the tiles by pieces of 8 dims.  What fp16 does not hold (elements above 65504,
+// infinite or NaN, and those below 2^-17, whose bits go on behind fp16's last of 2^-24) is looked at in pieces
+// with one of the first or with no element of 2^-12 or more: there it counts as 0 in the tiles, and the rows
+// that see it add its terms one by one.  So nothing hidden reaches a row, whatever it is, and sizes may be
+// anything: only next to an element of 2^-12 or more do those below 2^-17 round, by 2^-25 at most (2^-13 of
+// it, next to 2^-11 that p's rounding takes).  Multiplying new tiles in bf16 instead, with the queries in both
+// types one after the other and p as hi + lo, took 866 us where this takes 715 (2047 tokens of two prompts).
 // Tiles are made of blocks of 64 dims; with head_dim 32 and 96 half of the last one lies idle and the
 // MMAs stop before it (1000 tokens of two prompts over 4096 cached ones, 32 heads of 96: 179 us, where
 // the register kernel with 32 rows a unit took 1935).
@@ -125,6 +130,12 @@ __device__ __forceinline__ void tmem_st_8(uint32_t taddr, const uint32_t (&r)[8]
                  "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                  : "memory");
 }
+__device__ __forceinline__ void tmem_ld_8(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr)
+                 : "memory");
+}
 __device__ __forceinline__ void tmem_st_16(uint32_t taddr, const uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
@@ -164,55 +175,86 @@ __device__ __forceinline__ uint4 dequant8(uint32_t w, uint32_t sm) {
     const __half2 c3 = __hfma2(as_h2((w8 & 0x00f000f0u) | 0x64006400u), k16th, k64);
     return make_uint4(as_u32(__hfma2(c0, s, m)), as_u32(__hfma2(c1, s, m)), as_u32(__hfma2(c2, s, m)), as_u32(__hfma2(c3, s, m)));
 }
-// Whether fp16 cannot hold x.
-__device__ __forceinline__ bool is_odd(float x) { return !(fabsf(x) <= 65504.0f); }
-
-// Eight bf16 with 0 in place of what fp16 cannot hold.
+// A piece of 8 bf16 with 0 in place of what the tiles do not hold: nothing, where its largest magnitude is
+// 2^-12 .. 65504; else elements above 65504 or no number, and those below 2^-17 (their fp16 steps are 2^-24).
 static __device__ __noinline__ uint4 without_odd(uint4 v) {
+    constexpr uint32_t kMost = 0x477fu, kSmall = 0x3980u, kExact = 0x3700u;  // bf16 65280, 2^-12, 2^-17
     uint32_t *w = reinterpret_cast<uint32_t *>(&v);
+    uint32_t most = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) most = max(most, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
+    if (most >= kSmall && most <= kMost) return v;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        if (is_odd(bf_lo(w[i]))) w[i] &= 0xffff0000u;
-        if (is_odd(bf_hi(w[i]))) w[i] &= 0x0000ffffu;
+        const uint32_t lo = w[i] & 0x7fffu, hi = (w[i] >> 16) & 0x7fffu;
+        if (lo > kMost || lo < kExact) w[i] &= 0xffff0000u;
+        if (hi > kMost || hi < kExact) w[i] &= 0x0000ffffu;
     }
     return v;
 }
+// The elements that are not 0 there: what the piece holds and the tiles do not.
+__device__ __forceinline__ uint4 odd_of(uint4 v) {
+    const uint4 y = without_odd(v);
+    return make_uint4(v.x ^ y.x, v.y ^ y.y, v.z ^ y.z, v.w ^ y.w);
+}
+__device__ __forceinline__ bool is_any(uint4 v) { return ((v.x | v.y | v.z | v.w) & 0x7fff7fffu) != 0u; }
 // Eight bf16 to fp16 in the order of the tiles.
 __device__ __forceinline__ uint4 convert8(uint4 v) {
     return make_uint4(pack_f16(bf_lo(v.x), bf_lo(v.z)), pack_f16(bf_hi(v.x), bf_hi(v.z)), pack_f16(bf_lo(v.y), bf_lo(v.w)),
                       pack_f16(bf_hi(v.y), bf_hi(v.w)));
 }
 
-// The terms of elements that fp16 cannot hold, which count as 0 in the tiles: for the keys into the
-// row's scores (f: what the query was scaled by; keys first .. last of the tile), for the values into
-// dims first .. last of its output, where the row sees the key.  Warp-wide; `rows`: keys of the tile.
+// The terms of what the tiles do not hold, for the rows of the warp: of the keys into the row's scores
+// (f: what the query was scaled by; keys first .. last of the tile), of the values into dims first ..
+// last of its output, where the row sees the key.  `rows`: keys of the tile.  All lanes look at the same pieces.
 template <int D>
 static __device__ __noinline__ void add_odd_keys(const __nv_bfloat16 *kt, int64_t ld, int32_t first, int32_t last,
                                                  const __nv_bfloat16 *q, float f, uint32_t t_s) {
+#pragma unroll 1
     for (int32_t key = first; key < last; ++key) {
         float add = 0.0f;
         bool any = false;
-        for (int32_t d = 0; d < D; ++d) {
-            const float x = __bfloat162float(kt[key * ld + d]);
-            if (!is_odd(x)) continue;
+#pragma unroll 1
+        for (int32_t d = 0; d < D; d += 8) {
+            const uint4 z = odd_of(*reinterpret_cast<const uint4 *>(kt + key * ld + d));
+            if (!is_any(z)) continue;
             any = true;
-            add += __bfloat162float(q[d]) * f * x;
+            const uint4 x = *reinterpret_cast<const uint4 *>(q + d);
+            const uint32_t zw[4] = {z.x, z.y, z.z, z.w}, xw[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (zw[i] & 0x7fffu) add += bf_lo(xw[i]) * f * bf_lo(zw[i]);
+                if (zw[i] & 0x7fff0000u) add += bf_hi(xw[i]) * f * bf_hi(zw[i]);
+            }
         }
+        __syncwarp();
         if (any) tmem_st_1(t_s + key, tmem_ld_1(t_s + key) + add);
     }
 }
 static __device__ __noinline__ void add_odd_values(const __nv_bfloat16 *vt, int64_t ld, int32_t rows, uint4 see, float mul,
                                                    float sub, uint32_t t_s, uint32_t t_o, int32_t first, int32_t last) {
+#pragma unroll 1
     for (int32_t key = 0; key < rows; ++key) {
         const float pv = ex2_approx(__fadd_rn(__fmul_rn(tmem_ld_1(t_s + key), mul), sub));
         const uint32_t word = key < 64 ? (key < 32 ? see.x : see.y) : (key < 96 ? see.z : see.w);
         const bool mine = (word >> (key & 31)) & 1u;
-        for (int32_t d = first; d < last; ++d) {
-            const float x = __bfloat162float(vt[key * ld + d]);
-            if (!is_odd(x)) continue;
-            const uint32_t col = (d & ~7) + ((d & 3) << 1) + ((d >> 2) & 1);  // the order 0 4 1 5 2 6 3 7
-            const float o = tmem_ld_1(t_o + col);
-            tmem_st_1(t_o + col, mine ? o + pv * x : o);
+#pragma unroll 1
+        for (int32_t d = first; d < last; d += 8) {
+            const uint4 z = odd_of(*reinterpret_cast<const uint4 *>(vt + key * ld + d));
+            if (!is_any(z)) continue;
+            const uint32_t zw[4] = {z.x, z.y, z.z, z.w};
+            uint32_t o[8];  // in the order 0 4 1 5 2 6 3 7
+            tmem_ld_8(t_o + d, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int at = ((i & 3) << 1) | (i >> 2);
+                const float x = i & 1 ? bf_hi(zw[i >> 1]) : bf_lo(zw[i >> 1]);
+                if (mine && x != 0.0f) o[at] = __float_as_uint(__uint_as_float(o[at]) + pv * x);
+            }
+            __syncwarp();
+            tmem_st_8(t_o + d, o);
+            tmem_wait_st();
         }
     }
 }
@@ -391,19 +433,27 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
                     auto store = [&](int32_t i, uint4 x) {
                         if (mine) *reinterpret_cast<uint4 *>(dst + sw128((sub * kBatch + i) * 4 * kRowsWarp + first, ch & 7)) = x;
                     };
-                    // the largest magnitude of the results is infinite or NaN where fp16 does not hold an element
-                    __half2 big = as_h2(0u);
+                    // the largest magnitude of the results is infinite or NaN where an element is above fp16's,
+                    // and that of a small piece is below 2^-12
+                    __half2 big = as_h2(0u), small = as_h2(0x3c003c00u);
 #pragma unroll
                     for (int i = 0; i < kBatch; ++i) {
                         const uint4 x = convert8(v[i]);
-                        big = __hmax2_nan(__hmax2_nan(__hmax2_nan(big, __habs2(as_h2(x.x))), __habs2(as_h2(x.y))),
-                                          __hmax2_nan(__habs2(as_h2(x.z)), __habs2(as_h2(x.w))));
+                        const __half2 most = __hmax2_nan(__hmax2_nan(__habs2(as_h2(x.x)), __habs2(as_h2(x.y))),
+                                                         __hmax2_nan(__habs2(as_h2(x.z)), __habs2(as_h2(x.w))));
+                        big = __hmax2_nan(big, most);
+                        small = __hmin2(small, __hmax2(most, __lowhigh2highlow(most)));
                         store(i, x);
                     }
-                    if (!(__low2float(big) <= 65504.0f && __high2float(big) <= 65504.0f)) {
-                        odd = true;
+                    if (!(__low2float(big) <= 65504.0f && __high2float(big) <= 65504.0f && __low2float(small) >= 0x1p-12f)) {
 #pragma unroll
-                        for (int i = 0; i < kBatch; ++i) store(i, convert8(without_odd(v[i])));
+                        for (int i = 0; i < kBatch; ++i) {
+                            const uint4 x = without_odd(v[i]);
+                            if (((x.x ^ v[i].x) | (x.y ^ v[i].y) | (x.z ^ v[i].z) | (x.w ^ v[i].w)) & 0x7fff7fffu) {
+                                odd = true;
+                                store(i, convert8(x));
+                            }
+                        }
                     }
                     if (at + 1 < last * kBatches) load((at + 1) * (kKeys / kBatches));
                     if (sub == kBatches - 1) {
@@ -695,7 +745,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
                 }
                 // the row's maximum over both halves
                 half_max[j][n_s & 1u][h][r] = mx;  // the other one at every second tile
-                bool odd_values = false;  // whether a new tile's values hold what fp16 does not
+                bool odd_values = false;  // whether a new tile's values are not all held
                 if (i < fresh) {
                     // one answer for the stream, whose threads all go on to the next barrier or none: where the
                     // wait has given up, the mark may be changing

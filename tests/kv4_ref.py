@@ -106,3 +106,53 @@ def attend(q, kc, vc, kn, vn, see):
                        torch.nan_to_num(size.repeat_interleave(rep, 1), posinf=0.0))
     tol = 2.0 ** -8 * torch.nan_to_num(o).abs() * 1.001 + mag + 15 * k.shape[0] * (2.0 ** -25 if steep else 2.0 ** -34)
     return o, tol
+
+
+def rounded_off(x):
+    """What over 16 query rows a new key's or value's elements may lose: 2^-25, half of fp16's last step, where an
+    element below 2^-17 (those above are whole steps: 8 bits of bf16) has one of 2^-12 .. 65504 as the largest of its
+    aligned 8 neighbours."""
+    a = x.double().abs().unflatten(-1, (-1, 8))
+    most = a.amax(-1, keepdim=True)
+    return torch.where((a > 0) & (a < 2.0 ** -17) & (most >= 2.0 ** -12) & (most <= 65504), 2.0 ** -25, 0.0).flatten(-2)
+
+
+def relative_tolerance(q, kc, vc, kn, vn, see, o):
+    """How far the attention of one request may be off where sizes are far from 1: terms that follow the
+    sizes of what a row sees, with none of an absolute size.  Arguments as attend's; o its result.
+      output rounding            2^-8 |o|
+      scores in fp32             delta = (D + 16) 2^-22 of the sum of magnitudes, numerator and denominator;
+                                 over 16 rows cached keys are fp16 values: 2^-11 of their magnitudes more
+      p (and p s) to fp16        2 x 2^-11 of the sum of p (|m| + s c); new keys' p is bf16 hi + lo: less
+      new keys and values        over 16 rows what rounded_off says
+      fp16 range, cached keys    up to 16 rows: a row's largest p is 2^9 or more, the largest s is scaled to 8 or more
+                                 (or by 2^15): 15 codes off by 2^-25 are 15 2^-37 of it (or 15 2^-49); over 16 rows the
+                                 largest p is 2^4 or more: 2^-29 of the largest value
+    """
+    n, H, D = q.shape
+    Hk = kc.shape[1]
+    rep, tiles, t = H // Hk, n * H // Hk > 16, kc.shape[0]
+    k, size, ksize = stands_for(kc), size_of(vc), size_of(kc)
+    if kn is not None:
+        k, size, ksize = torch.cat([k, kn.double()]), torch.cat([size, vn.double().abs()]), torch.cat([ksize, kn.double().abs()])
+    kh, size, ksize = (x.repeat_interleave(rep, 1) for x in (k, size, ksize))
+    z = torch.einsum("nhd,thd->hnt", q.double(), kh) / math.sqrt(D)
+    p = torch.softmax(z.masked_fill(~see, -math.inf), -1).nan_to_num(0.0)
+    A = torch.where(see, torch.einsum("nhd,thd->hnt", q.double().abs(), ksize), 0.0) / math.sqrt(D)
+    delta = (D + 16) * 2.0 ** -22 * A.amax(-1, keepdim=True)
+    if tiles and t:
+        delta = delta + 2.0 ** -11 * A[..., :t].amax(-1, keepdim=True)
+    held = torch.zeros_like(size)  # what the tiles may round off each new value
+    if tiles and kn is not None:
+        lost_k = torch.cat([torch.zeros_like(kc.double()), rounded_off(kn)]).repeat_interleave(rep, 1)
+        held = torch.cat([torch.zeros_like(kc.double()), rounded_off(vn)]).repeat_interleave(rep, 1)
+        B = torch.where(see, torch.einsum("nhd,thd->hnt", q.double().abs(), lost_k), 0.0) / math.sqrt(D)
+        delta = delta + B.amax(-1, keepdim=True)
+    tol = 2.0 ** -8 * 1.001 * o.abs() + torch.einsum("hnt,thd->nhd", p * (2.0 ** -10 + 2.0 ** -19 + 2 * delta), size)
+    tol = tol + torch.einsum("hnt,thd->nhd", p, held)
+    if t and tiles:
+        tol = tol + t * 2.0 ** -29 * size[:t].amax(0)[None]
+    elif t:
+        step = parts(vc)[1].amax((0, 2, 3)).repeat_interleave(rep)[None, :, None]  # of a kv head
+        tol = tol + 15 * t * torch.clamp(2.0 ** -37 * step, min=2.0 ** -49)
+    return tol

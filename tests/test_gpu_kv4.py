@@ -455,6 +455,67 @@ def test_attention_over_values_of_other_sizes(dev, case, kscale, vscale, qscale)
     check_attention(case, made, o)
 
 
+ROWS = [(5, 1), (16, 1), (17, 1), (40, 2), (130, 2), (300, 1)]  # nodes, heads of one kv head
+
+
+def check_sizes(case, made, o):
+    B, n, H, Hk, D, page, lens, kind = case
+    c, kc, vc, q, kn, vn, mask = made
+    for b, t in enumerate(lens):
+        see = ref.sees(n, t, None if mask is None else mask[b], "cuda")[:, :t + (0 if kn is None else n)]
+        args = q[b], kc[b, :t], vc[b, :t], None if kn is None else kn[b], None if vn is None else vn[b], see
+        want = ref.attend(*args)[0]
+        tol = ref.relative_tolerance(*args, want)
+        err = (o[b].double() - want).abs()
+        assert torch.all(err <= tol), (b, float((err / tol.clamp(min=1e-300)).max()))
+
+
+@pytest.mark.parametrize("D", [96, 128])
+@pytest.mark.parametrize("n,H", ROWS, ids=lambda v: str(v))
+@pytest.mark.parametrize("kscale,vscale,qscale", [(0.8, 1e-3, 1.0), (0.8, 1e-5, 1.0), (0.8, 1e-7, 1.0), (0.8, 1e-20, 1.0),
+                                                  (0.8, 2e5, 1.0), (0.8, 1e20, 1.0), (1e-6, 0.8, 1e6), (1e-12, 1e-3, 1e12),
+                                                  (1e15, 0.8, 1e-15)])
+def test_new_keys_and_values_of_any_size(dev, n, H, D, kscale, vscale, qscale):
+    """Nothing cached: the new keys and values alone, as close for small and large ones as for those near 1."""
+    case = (2, n, H, 1, D, 16, [0, 0], "tree")
+    made = build(case, 17, kscale, vscale, qscale)
+    c, _, _, q, kn, vn, mask = made
+    check_sizes(case, made, c.attention(q, kn, vn, mask=mask))
+    c.status()
+
+
+@pytest.mark.parametrize("n,H", ROWS, ids=lambda v: str(v))
+def test_new_values_of_many_sizes_at_once(dev, n, H):
+    """Dims from 2^0 down to 2^-40 and up to 2^40, each as close as its own size says; a hidden node that holds large
+    finite values changes nothing."""
+    case = (1, n, H, 1, 128, 16, [0], "tree")
+    made = build(case, 18)
+    c, _, _, q, kn, vn, mask = made
+    vn *= 2.0 ** (torch.arange(128, device="cuda") % 81 - 40)
+    kn[0, ::3] *= 2.0 ** -20
+    o = c.attention(q, kn, vn, mask=mask)
+    check_sizes(case, made, o)
+    kn[0, n - 1], vn[0, n - 1] = 1e4, -6e4  # the last node: no one's ancestor
+    assert torch.equal(c.attention(q, kn, vn, mask=mask)[0, :n - 1], o[0, :n - 1])
+
+
+@pytest.mark.parametrize("n,H", ROWS, ids=lambda v: str(v))
+def test_largest_and_smallest_sizes(dev, n, H):
+    """The ends of what the contract names, 2^100 and 2^-100, seen and weighted."""
+    case = (1, n, H, 1, 64, 16, [0], "causal")
+    made = build(case, 19)
+    c, _, _, q, kn, vn, mask = made
+    for size in (2.0 ** 100, 2.0 ** -100):
+        vn.copy_(torch.where(vn > 0, size, -size / 2))
+        check_sizes(case, made, c.attention(q, kn, vn))
+        kn.copy_(torch.where(kn > 0, size, -size).to(torch.bfloat16))
+        q.copy_((q.float() / q.float().abs().amax(-1, keepdim=True) / size / 64).to(torch.bfloat16))
+        check_sizes(case, made, c.attention(q, kn, vn))
+        made = build(case, 19)
+        c, _, _, q, kn, vn, mask = made
+    c.status()
+
+
 @pytest.mark.parametrize("case", [(2, 9, 4, 4, 128, 32, [70, 0], "tree"), (1, 65, 8, 2, 64, 64, [100], "tree"),
                                   (2, 40, 8, 1, 128, 16, [0, 257], "tree"), (1, 50, 4, 1, 96, 16, [40], "tree"),
                                   (2, 50, 2, 1, 32, 16, [40, 300], "tree")],
