@@ -21,7 +21,10 @@
 //   * output: o_d = sum_j (p_j s_gj) c_jd + sum_j p_j m_gj.  For each group p s_g is the B operand
 //     (two fp16 products a key pair), the codes again the A operand; the second sum is one MMA whose
 //     rows are the groups.  p and p s are rounded to fp16 (half a step is 2^-11 relative, against
-//     2^-8 of the bf16 output); sums, the running maximum and p's sum are fp32.
+//     2^-8 of the bf16 output); sums, the running maximum and p's sum are fp32.  So that p s keeps its bits
+//     whatever the values' size, s is lifted by the power of two (up to 2^15) that puts the largest one so far
+//     at 8 .. 16, and the first sum carries that power: a p of 2^-26 of the row's largest still has 11 bits
+//     of p s (without it four heavy keys among 65536 that weigh a fifth were off by 3 % at values of 3e-5).
 // Scores are formed transposed (16 keys on the MMA's M side, 8 query rows on N), so few query rows
 // waste no MMA rows, and the accumulators turn into the value product's operand by movmatrix.
 //
@@ -47,6 +50,9 @@ constexpr int kThreads = kWarps * 32 + 32;  // and one that copies
 constexpr int kStages = 5;
 constexpr int kMinTiles = 2;    // tiles a CTA takes at least: a single tile's CTA is merging more than work
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr int32_t kLift = 15;   // the most by which values' scales are lifted: a power of two that fp16 holds
+
+__device__ __forceinline__ float power_of_2(int32_t e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
@@ -200,6 +206,7 @@ __global__ void __launch_bounds__(kThreads, Shape<G, NQ>::kBlocks) kv4_attention
         int32_t node_of[NQ][2];     // the columns' nodes, -1 behind the last row
         // p = 2^(score - ref), at most 2^top; a new ref puts the largest at 2^aim
         float aim = 9.0f, top = 12.0f;
+        int32_t lift = kLift;  // values' scales are multiplied by 2^lift, and so is o
 #pragma unroll
         for (int nq = 0; nq < NQ; ++nq) {
             const int32_t row = w.qt * kRows + nq * 8 + gq;
@@ -429,13 +436,13 @@ __global__ void __launch_bounds__(kThreads, Shape<G, NQ>::kBlocks) kv4_attention
                 }
             }
         }
-        // the cached tiles accumulate c 2^-24 (rows 0-7: even dims) and 16 c 2^-24 (rows 8-15: odd dims)
+        // the cached tiles accumulate c 2^(lift - 24) (rows 0-7: even dims) and 16 c 2^(lift - 24) (rows 8-15: odd dims)
 #pragma unroll
         for (int i = 0; i < 2 * G; ++i)
 #pragma unroll
             for (int nq = 0; nq < NQ; ++nq)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) o[i][nq][e] *= e < 2 ? 0x1p-24f : 0x1p-20f;
+                for (int e = 0; e < 4; ++e) o[i][nq][e] *= e < 2 ? power_of_2(kLift - 24) : power_of_2(kLift - 20);
 
         // ---------------- cached keys: two stages, i.e. two chunks of the warp, at a time ----------
 #pragma unroll 1
@@ -509,20 +516,32 @@ __global__ void __launch_bounds__(kThreads, Shape<G, NQ>::kBlocks) kv4_attention
                         for (int e = 0; e < 8; ++e)
                             if (ta + (e & 2 ? 8 : 0) >= nv[e >> 2]) sc[nq][e] = -INFINITY;
                 }
-                // p s must stay below fp16's largest: with p up to 2^12, s below 16.  Steeper
-                // values (s up to 2^12.1) take p up to 2^3 from here on.  Each lane looks at its
-                // share of the chunks' 16 G scales.
+                // p s must stay below fp16's largest: with p up to 2^12, lifted s below 16, so a larger
+                // one lowers the lift.  Steeper values (s from 16 to 2^12.1) take p up to 2^3 from here on.
+                // Each lane looks at its share of the chunks' 16 G scales.
                 if (aim != 0.0f) {
-                    bool steep = false;
+                    uint32_t most = 0;  // bits of the largest; NaN above all
 #pragma unroll
                     for (int u = 0; u < 2; ++u)
 #pragma unroll
                         for (int i = 0; i < (G + 1) / 2; ++i) {
                             const int32_t at = lane + 32 * i;
-                            if (at < 16 * G && at / G < nv[u])  // s >= 16, or NaN
-                                steep = steep || (reinterpret_cast<const uint32_t *>(ch[u] + kv4_value_params(G))[at] & 0xffffu) >= 0x4c00u;
+                            if (at < 16 * G && at / G < nv[u])
+                                most = max(most, reinterpret_cast<const uint32_t *>(ch[u] + kv4_value_params(G))[at] & 0xffffu);
                         }
-                    if (__any_sync(kFull, steep)) {
+                    if (__any_sync(kFull, most >= static_cast<uint32_t>(19 - lift) << 10)) {  // 2^(4 - lift)
+                        most = __reduce_max_sync(kFull, most);
+                        const int32_t to = max(18 - static_cast<int32_t>(most >> 10), 0);
+                        const float down = power_of_2(to - lift);
+                        lift = to;
+#pragma unroll
+                        for (int i = 0; i < 2 * G; ++i)
+#pragma unroll
+                            for (int nq = 0; nq < NQ; ++nq)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) o[i][nq][e] *= down;
+                    }
+                    if (most >= 0x4c00u && lift == 0) {  // 16
                         aim = 0.0f;
                         top = 3.0f;
 #pragma unroll
@@ -569,6 +588,7 @@ __global__ void __launch_bounds__(kThreads, Shape<G, NQ>::kBlocks) kv4_attention
                         b1[nq] = transpose8(pack_f16(sc[nq][4 * u + 2], sc[nq][4 * u + 3]));
                         mma_f16(om[nq], __byte_perm(mm[0], mm[1], 0x7632), 0u, __byte_perm(mm[2], mm[3], 0x7632), 0u, b0[nq], b1[nq]);
                     }
+                    const uint32_t up = 0x04000400u * static_cast<uint32_t>(15 + lift);  // 2^lift, twice
                     const uint8_t *vc = ch[u] + kv4_value_codes(G);
                     uint32_t vw[4][(G + 1) / 2];  // two groups a word
 #pragma unroll
@@ -590,7 +610,8 @@ __global__ void __launch_bounds__(kThreads, Shape<G, NQ>::kBlocks) kv4_attention
                         const uint32_t sel = g & 1 ? 0x7632 : 0x5410;
                         const uint32_t x = __byte_perm(vw[0][g / 2], vw[1][g / 2], sel), y = __byte_perm(vw[2][g / 2], vw[3][g / 2], sel);
                         const uint32_t x8 = x >> 8, y8 = y >> 8;
-                        const uint32_t s01 = __byte_perm(par[0][g], par[1][g], 0x5410), s23 = __byte_perm(par[2][g], par[3][g], 0x5410);
+                        const uint32_t s01 = mul_f16x2(__byte_perm(par[0][g], par[1][g], 0x5410), up);
+                        const uint32_t s23 = mul_f16x2(__byte_perm(par[2][g], par[3][g], 0x5410), up);
 #pragma unroll
                         for (int nq = 0; nq < NQ; ++nq) {
                             const uint32_t p0 = mul_f16x2(b0[nq], s01), p1 = mul_f16x2(b1[nq], s23);
@@ -611,6 +632,7 @@ __global__ void __launch_bounds__(kThreads, Shape<G, NQ>::kBlocks) kv4_attention
 
         // ---------------- the warps' shares of the segment meet ----------------
         named_barrier_sync(1, kWarps * 32);  // the previous segment's sums have been read
+        const float even = power_of_2(24 - lift), odd = power_of_2(20 - lift);
 #pragma unroll
         for (int nq = 0; nq < NQ; ++nq) {
 #pragma unroll
@@ -623,10 +645,10 @@ __global__ void __launch_bounds__(kThreads, Shape<G, NQ>::kBlocks) kv4_attention
                 for (int c = 0; c < 2; ++c) {
                     const float add = __shfl_sync(kFull, om[nq][c], g * 4 + qd);
                     float4 v;  // dims 32 g + 4 gq .. + 3
-                    v.x = fmaf(o[2 * g][nq][c], 0x1p24f, add);
-                    v.y = fmaf(o[2 * g][nq][2 + c], 0x1p20f, add);
-                    v.z = fmaf(o[2 * g + 1][nq][c], 0x1p24f, add);
-                    v.w = fmaf(o[2 * g + 1][nq][2 + c], 0x1p20f, add);
+                    v.x = fmaf(o[2 * g][nq][c], even, add);
+                    v.y = fmaf(o[2 * g][nq][2 + c], odd, add);
+                    v.z = fmaf(o[2 * g + 1][nq][c], even, add);
+                    v.w = fmaf(o[2 * g + 1][nq][2 + c], odd, add);
                     *reinterpret_cast<float4 *>(merge + (warp * kRows + nq * 8 + 2 * qd + c) * S::kMergeStride + 32 * g + 4 * gq) = v;
                 }
             if (gq < 2) merge_ml[warp * kRows + nq * 8 + 2 * qd + gq] = gq ? make_float2(ref[nq][1], l[nq][1]) : make_float2(ref[nq][0], l[nq][0]);
