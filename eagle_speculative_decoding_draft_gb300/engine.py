@@ -38,6 +38,8 @@ def _need(t, name, dtype=None, device=None):
         raise ValueError(f"{name} must be a contiguous CUDA tensor")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the call on {device}")
     return t
 
 
@@ -489,15 +491,15 @@ class DecoderLayer:
             raise ValueError("x does not match the weights or the cache")
         if cache.device != x.device or self.device != x.device:
             raise ValueError("the weights, the cache and x must be on one device")
-        _need(positions, "positions", torch.int32)
+        _need(positions, "positions", torch.int32, x.device)
         if positions.shape != (B, n):
             raise ValueError("positions shape does not match")
-        if mask is not None and _need(mask, "mask", torch.int32).shape != (B, n, (n + 31) // 32):
+        if mask is not None and _need(mask, "mask", torch.int32, x.device).shape != (B, n, (n + 31) // 32):
             raise ValueError("mask shape does not match")
         with cache._on(stream):
             if out is None:
                 out = torch.empty_like(x)
-            elif _need(out, "out", torch.bfloat16).shape != x.shape:
+            elif _need(out, "out", torch.bfloat16, x.device).shape != x.shape:
                 raise ValueError("out shape does not match")
             kn = vn = None
             if new_kv:
@@ -508,7 +510,7 @@ class DecoderLayer:
                 raise ValueError(f"unusable decoder layer sizes (batch={B}, nodes={n}) or a cache of other heads")
             if workspace is None:
                 workspace = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
-            elif _need(workspace, "workspace", torch.uint8).numel() < nbytes:
+            elif _need(workspace, "workspace", torch.uint8, x.device).numel() < nbytes:
                 raise ValueError(f"workspace must hold at least {nbytes} bytes")
             check(self._lib.eagle_decoder_layer_kv4(
                 ctypes.byref(self.w), cache._ref, B, n, _ptr(x), _ptr(positions), _ptr(mask), _ptr(out), _ptr(kn),

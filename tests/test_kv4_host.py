@@ -119,6 +119,42 @@ def test_decoder_layer_refuses(lib):
     assert call(cache(), heads=3) == 1 and call(cache(), rope_theta=0.0) == 1
 
 
+class Elsewhere:
+    """Looks like a contiguous CUDA tensor; no kernel may get its address."""
+
+    def __init__(self, shape, dtype, index=0):
+        self.shape, self.dtype, self.device, self.is_cuda = shape, dtype, torch.device("cuda", index), True
+
+    def is_contiguous(self):
+        return True
+
+    def numel(self):
+        n = 1
+        for s in self.shape:
+            n *= s
+        return n
+
+    def data_ptr(self):
+        raise AssertionError("the call went on with it")
+
+
+@pytest.mark.parametrize("which", ["positions", "mask", "out", "workspace"])
+def test_decoder_layer_over_the_cache_refuses_tensors_on_another_device(lib, which):
+    import contextlib
+    import types
+    from eagle_speculative_decoding_draft_gb300.engine import DecoderLayer
+    lay = DecoderLayer.__new__(DecoderLayer)
+    lay.hidden, lay.heads, lay.kv_heads, lay.head_dim, lay.device = 256, 4, 2, 64, torch.device("cuda", 0)
+    lay.w = ctypes.c_int(0)
+    lay._lib = types.SimpleNamespace(eagle_decoder_layer_kv4_workspace_bytes=lambda *a: 1024)
+    kv = types.SimpleNamespace(batch=2, device=torch.device("cuda", 0), _on=lambda stream: contextlib.nullcontext(), _ref=None)
+    on = lambda name: 1 if name == which else 0
+    args = dict(positions=Elsewhere((2, 9), torch.int32, on("positions")), mask=Elsewhere((2, 9, 1), torch.int32, on("mask")),
+                out=Elsewhere((2, 9, 256), torch.bfloat16, on("out")), workspace=Elsewhere((1024,), torch.uint8, on("workspace")))
+    with pytest.raises(ValueError, match=f"{which} is on cuda:1"):
+        lay.kv4(Elsewhere((2, 9, 256), torch.bfloat16), kv, **args)
+
+
 @pytest.mark.parametrize("scale", [1.0, 1e-4, 300.0])
 def test_the_definition_holds_its_error_bound(scale):
     """No value is further than half a step from what its code stands for (no code is clamped), and
