@@ -107,6 +107,8 @@ class KV4Cache:
         """Makes the cache's device current, and `stream` where one is given, so that what is
         allocated belongs to the stream that uses it."""
         if stream is not None:
+            if stream.device != self.device:
+                raise ValueError(f"stream is on {stream.device}, the cache on {self.device}")
             return torch.cuda.stream(stream)
         if torch.cuda.current_device() != self._index:
             return torch.cuda.device(self.device)

@@ -155,6 +155,22 @@ def test_decoder_layer_over_the_cache_refuses_tensors_on_another_device(lib, whi
         lay.kv4(Elsewhere((2, 9, 256), torch.bfloat16), kv, **args)
 
 
+def test_a_stream_of_another_device_is_refused():
+    import types
+    from eagle_speculative_decoding_draft_gb300.engine import DecoderLayer
+    from eagle_speculative_decoding_draft_gb300.kv4 import KV4Cache
+    c = KV4Cache.__new__(KV4Cache)
+    c.device, c._index, c.batch, c._tail, c._lib, c._ref = torch.device("cuda", 0), 0, 2, (2, 64), None, None
+    lay = DecoderLayer.__new__(DecoderLayer)
+    lay.hidden, lay.device = 256, c.device
+    stream = types.SimpleNamespace(device=torch.device("cuda", 1), cuda_stream=0)
+    x = Elsewhere((2, 9, 256), torch.bfloat16)
+    for call in (lambda: c.status(stream=stream), lambda: c.read(rows=3, stream=stream),
+                 lambda: lay.kv4(x, c, Elsewhere((2, 9), torch.int32), stream=stream)):
+        with pytest.raises(ValueError, match="stream is on cuda:1"):
+            call()
+
+
 @pytest.mark.parametrize("scale", [1.0, 1e-4, 300.0])
 def test_the_definition_holds_its_error_bound(scale):
     """No value is further than half a step from what its code stands for (no code is clamped), and
