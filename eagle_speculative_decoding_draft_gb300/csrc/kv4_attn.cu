@@ -50,6 +50,7 @@ constexpr int kThreads = kWarps * 32 + 32;  // and one that copies
 constexpr int kStages = 5;
 constexpr int kMinTiles = 2;    // tiles a CTA takes at least: a single tile's CTA is merging more than work
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr int32_t kSegment = 1024;  // tiles summed in one go (kv4_line.cuh)
 constexpr int32_t kLift = 15;   // the most by which values' scales are lifted: a power of two that fp16 holds
 
 __device__ __forceinline__ float power_of_2(int32_t e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
@@ -657,7 +658,7 @@ __global__ void __launch_bounds__(kThreads, Shape<G, NQ>::kBlocks) kv4_attention
         if (*abort_flag) {
             if (threadIdx.x == 0) latch(a.status, kDevTimeout);
         } else {
-            const bool whole = w.s0 == 0 && w.s1 == w.unit;
+            const bool whole = w.from == 0 && w.s1 == w.unit, begun = w.s0 > w.from;
             const int64_t slot = slot_of(w);
             for (int32_t it = threadIdx.x; it < kRows * (D / 4); it += kWarps * 32) {
                 const int32_t r = it / (D / 4), c4 = it - r * (D / 4), row = w.qt * kRows + r;
@@ -669,12 +670,7 @@ __global__ void __launch_bounds__(kThreads, Shape<G, NQ>::kBlocks) kv4_attention
 #pragma unroll
                 for (int i = 0; i < kWarps; ++i) {
                     const float2 ml = merge_ml[i * kRows + r];
-                    if (ml.x == -INFINITY) {
-                        // a warp whose keys are all hidden, or whose scores are all NaN (sum NaN)
-                        wt[i] = ml.y == 0.0f ? 0.0f : ml.y;
-                    } else {
-                        wt[i] = ex2_approx(ml.x - M);
-                    }
+                    wt[i] = weight_of(ml.x, ml.y, M);
                     L += wt[i] * ml.y;
                     if (wt[i] == 0.0f) continue;
                     const float4 x = *reinterpret_cast<const float4 *>(merge + (i * kRows + r) * S::kMergeStride + 4 * c4);
@@ -683,13 +679,25 @@ __global__ void __launch_bounds__(kThreads, Shape<G, NQ>::kBlocks) kv4_attention
                     v.z = fmaf(wt[i], x.z, v.z);
                     v.w = fmaf(wt[i], x.w, v.w);
                 }
+                float2 *carry = k.carry_ml + static_cast<int64_t>(blockIdx.x) * kKv4Carry + it;
+                float4 *part = reinterpret_cast<float4 *>(k.part_o + (slot * kRows + r) * D + 4 * c4);
+                if (begun) {
+                    float now, before;
+                    join(*carry, M, L, now, before);
+                    const float4 was = *part;
+                    if (now == 0.0f) v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    else v = make_float4(now * v.x, now * v.y, now * v.z, now * v.w);
+                    if (before != 0.0f)
+                        v = make_float4(fmaf(before, was.x, v.x), fmaf(before, was.y, v.y), fmaf(before, was.z, v.z), fmaf(before, was.w, v.w));
+                }
                 if (whole) {
                     const int32_t node = row / k.group, head = w.hk * k.group + row - node * k.group;
                     const float inv = L == 0.0f ? 0.0f : 1.0f / L;
                     *reinterpret_cast<uint2 *>(a.o + ((static_cast<int64_t>(w.b) * a.n + node) * a.H + head) * D + 4 * c4) =
                         make_uint2(pack_b16(v.x * inv, v.y * inv), pack_b16(v.z * inv, v.w * inv));
                 } else {
-                    *reinterpret_cast<float4 *>(k.part_o + (slot * kRows + r) * D + 4 * c4) = v;
+                    *part = v;
+                    *carry = make_float2(M, L);
                     if (c4 == 0) k.part_ml[slot * kRows + r] = make_float2(M, L);
                 }
             }
@@ -732,8 +740,7 @@ __global__ void __launch_bounds__(kMergeRows * 32) kv4_merge_kernel(const __grid
             float wt = 0.0f;
             if (i0 + lane < parts) {
                 const float2 ml = k.part_ml[slot(i0 + lane) * k.rows + r];
-                // a part whose scores are all NaN has no maximum and a sum of NaN
-                wt = ml.x == -INFINITY ? (ml.y == 0.0f ? 0.0f : ml.y) : ex2_approx(ml.x - M);
+                wt = weight_of(ml.x, ml.y, M);
                 if (wt != 0.0f) L += wt * ml.y;
             }
             const int32_t n = min(parts - i0, 32);
@@ -840,7 +847,8 @@ size_t kv4_attention_workspace(int32_t Hk, int32_t G, int32_t H, int32_t n) {
     if (!d) return 0;
     const Variant v = variant(G, static_cast<int32_t>(std::min<int64_t>(static_cast<int64_t>(n) * (H / Hk), 1 << 20)));
     const size_t grid = grid_of(*d, G, v);
-    return align256(grid * sizeof(Kv4Share)) + align256(grid * 2 * v.rows * sizeof(float2)) + grid * 2 * v.rows * G * kKv4Group * 4;
+    return align256(grid * sizeof(Kv4Share)) + align256(grid * 2 * v.rows * sizeof(float2)) + grid * 2 * v.rows * G * kKv4Group * 4 +
+           grid * kKv4Carry * sizeof(float2);
 }
 
 bool kv4_attention_fits(const Kv4View &cache, int32_t B, int32_t n, int32_t H, bool new_keys) {
@@ -875,6 +883,9 @@ cudaError_t launch_kv4_attention(const Kv4Attention &a, cudaStream_t st) {
     k.part_ml = reinterpret_cast<float2 *>(ws);
     ws += align256(static_cast<size_t>(full) * 2 * v.rows * sizeof(float2));
     k.part_o = reinterpret_cast<float *>(ws);
+    ws += static_cast<size_t>(full) * 2 * v.rows * G * kKv4Group * 4;
+    k.carry_ml = reinterpret_cast<float2 *>(ws);
+    k.segment = v.kernel ? kSegment : kKv4TcSegment;
     // no more CTAs than the longest possible line gives work to
     const int64_t most = (longest_line(a.cache, a.B, a.n, a.H, a.kn != nullptr) + k.min_tiles - 1) / k.min_tiles;
     const unsigned grid = static_cast<unsigned>(std::min<int64_t>(full, std::max<int64_t>(most, 1)));

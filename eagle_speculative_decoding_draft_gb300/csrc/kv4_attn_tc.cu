@@ -325,6 +325,46 @@ static __device__ __noinline__ float probabilities_in_steps(uint32_t t, float mu
     return sum;
 }
 
+// A unit's sums from segment to segment, at a segment's end: what came before (`begun`), brought to this
+// segment's reference, joins the accumulator, and if the unit goes on the sum moves to memory.  Each thread has
+// its half of its row of the partial sums (stream 1's behind stream 0's) and a (ref, l) of its own, ml.
+template <int D>
+static __device__ __noinline__ void carry_over(const Kv4Args &k, const Walk &w, uint32_t t_o, float2 *ml) {
+    const float ref = ml->x;
+    float l = ml->y;
+    const int32_t row = threadIdx.x >> 8 << 7 | (threadIdx.x & 127), first = (threadIdx.x >> 7 & 1) * (D / 2);
+    const bool begun = w.s0 > w.from, goes_on = w.s1 < w.to;
+    float *part = k.part_o + (slot_of(w) * kKv4TcRows + row) * D + first;
+    float2 *at = k.carry_ml + static_cast<int64_t>(blockIdx.x) * kKv4Carry + threadIdx.x;
+    float f = 0.0f;
+    if (begun) {
+        const float2 was = *at;
+        f = was.x == -INFINITY ? 0.0f : ex2_approx(was.x - ref);
+        l = fmaf(was.y, f, l);
+    }
+    *(goes_on ? at : ml) = make_float2(ref, l);
+    __syncwarp();
+#pragma unroll 1
+    for (int c = 0; c < D / 2; c += 16) {
+        uint32_t v[16];
+        tmem_ld_16(t_o + first + c, v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 16; i += 4) {
+            float4 x = make_float4(__uint_as_float(v[i]), __uint_as_float(v[i + 1]), __uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]));
+            float4 *to = reinterpret_cast<float4 *>(part + c + i);
+            if (begun) {
+                const float4 y = *to;
+                x = make_float4(fmaf(y.x, f, x.x), fmaf(y.y, f, x.y), fmaf(y.z, f, x.z), fmaf(y.w, f, x.w));
+            }
+            if (goes_on) *to = x;
+            v[i] = __float_as_uint(x.x), v[i + 1] = __float_as_uint(x.y), v[i + 2] = __float_as_uint(x.z), v[i + 3] = __float_as_uint(x.w);
+        }
+        if (!goes_on) tmem_st_16(t_o + first + c, v);
+    }
+    tmem_wait_st();
+}
+
 template <int G>
 __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __grid_constant__ Kv4Args k) {
     using S = Tc<G>;
@@ -704,6 +744,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
                 return (static_cast<int64_t>(w.b) * a.n + s * kKeys) * a.ldkv + static_cast<int64_t>(w.hk) * D;
             };
             float ref = -INFINITY, l = 0.0f;
+            if (w.s0 > w.from) ref = half_ml[j][h][r].x;  // the unit goes on
             // the segment's tiles, those of new keys among them, and the stream's first and step
             const int32_t tiles = w.s1 - w.s0, fresh = max(w.nt - w.s0, 0), from = both ? 0 : j, step = both ? 1 : 2;
             for (int32_t i = from; i < tiles; i += step) {
@@ -805,11 +846,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
             __syncwarp();
             // the halves' sums, and of a unit of at most 128 rows both streams' shares
             half_ml[j][h][r] = make_float2(ref, l);
+            if (w.s0 > w.from || w.s1 < w.to) {
+                tc_fence_after();
+                carry_over<D>(k, w, t_o, &half_ml[j][h][r]);
+                if (w.s1 < w.to) continue;
+            }
             tc_fence_before();
             if (both) named_barrier_sync(1 + j, 256);
             else named_barrier_sync(3, 512);
             tc_fence_after();
-            const bool whole = w.s0 == 0 && w.s1 == w.unit;
+            const bool whole = w.from == 0 && w.s1 == w.unit;
             const int32_t ur = both ? j * 128 + r : r;
             const int64_t slot = slot_of(w);
             const uint32_t o_first = tmem + lanes + 256u;
@@ -821,9 +867,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
                 const float m0 = half_ml[0][0][r].x, m1 = half_ml[1][0][r].x;
                 const float l0 = half_ml[0][0][r].y + half_ml[0][1][r].y, l1 = half_ml[1][0][r].y + half_ml[1][1][r].y;
                 M = fmaxf(m0, m1);
-                // a stream whose scores are all NaN has no maximum and a sum of NaN
-                w0 = m0 == -INFINITY ? (l0 == 0.0f ? 0.0f : l0) : ex2_approx(m0 - M);
-                w1 = m1 == -INFINITY ? (l1 == 0.0f ? 0.0f : l1) : ex2_approx(m1 - M);
+                w0 = weight_of(m0, l0, M);
+                w1 = weight_of(m1, l1, M);
                 L = w0 * l0 + w1 * l1;
             }
             const float inv = L == 0.0f ? 0.0f : 1.0f / L;

@@ -30,7 +30,10 @@ struct Kv4Args {
     Kv4Share *share;         // [grid]
     float2 *part_ml;         // [grid * 2][rows]: running maximum (base 2) and sum
     float *part_o;           // [grid * 2][rows][D]
+    float2 *carry_ml;        // [grid][kKv4Carry]: part_ml of a unit's earlier segments, for each thread or item its own
+    int32_t segment;         // tiles summed in one go
 };
+constexpr int32_t kKv4Carry = 512;
 
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
@@ -311,10 +314,14 @@ __device__ __forceinline__ bool find_place(const Kv4Args &k, Place &place, Lengt
     return place.begin < place.end;
 }
 
-// A CTA's run through the line, unit by unit: [s0, s1) of the unit's tiles.
+// A CTA's run through the line, unit by unit: tiles [from, to) of the unit, of which [s0, s1) is a segment.
+// Accumulators of matrix products cut off what lies below their last bit: 2^-24 of themselves or so each time
+// (4 M cached keys in one sum: 2.6 % over 16 query rows, 0.6 % up to 16).  So a segment has k.segment tiles at
+// most, 256 or 1024: under 2^-12.  The segments of a unit join in the CTA's partial sums, in fp32 rounded to
+// the nearest.
 struct Walk {
     int32_t b, hk, qt;
-    int32_t t, s0, s1, unit;
+    int32_t t, from, to, s0, s1, unit;
     int32_t nt;  // tiles of new keys (the unit's first)
     int32_t len;
 
@@ -330,16 +337,22 @@ struct Walk {
     __device__ __forceinline__ void fill(const Kv4Args &k, const Place &p) {
         nt = new_tiles(k, qt);
         unit = cached_tiles(k, len) + nt;
-        s0 = min(s0, unit - 1);  // the place may come from an earlier length
-        s1 = min(unit, s0 + (p.end - t));
+        from = s0 = min(s0, unit - 1);  // the place may come from an earlier length
+        to = min(unit, s0 + (p.end - t));
+        s1 = min(to, s0 + k.segment);
     }
     // Whether the next unit is of a request of another 32.
     __device__ __forceinline__ bool leaves(const Kv4Args &k, const Place &p) const {
-        return ((b + 1) & 31) == 0 && b + 1 < k.a.B && hk + 1 == k.a.cache.Hk && qt + 1 == k.QT && t + s1 - s0 < p.end;
+        return s1 == to && ((b + 1) & 31) == 0 && b + 1 < k.a.B && hk + 1 == k.a.cache.Hk && qt + 1 == k.QT && t + s1 - s0 < p.end;
     }
     // (meet comes first)
     __device__ __forceinline__ bool next(const Kv4Args &k, const Place &p, const Lengths &lens) {
         t += s1 - s0;
+        if (s1 < to) {
+            s0 = s1;
+            s1 = min(to, s0 + k.segment);
+            return true;
+        }
         if (t >= p.end) return false;
         s0 = 0;
         if (++qt == k.QT) {
@@ -382,14 +395,28 @@ __device__ __forceinline__ bool kv4_next(const Kv4Args &k, const Place &p, Walk 
 
 // What CTA blockIdx.x leaves for the merge.
 __device__ __forceinline__ Kv4Share share_of(const Walk &w) {
-    return Kv4Share{w.s0 == 0 ? 0 : (w.s1 == w.unit ? 1 : 2), w.b, w.hk, w.qt};
+    return Kv4Share{w.from == 0 ? 0 : (w.to == w.unit ? 1 : 2), w.b, w.hk, w.qt};
 }
-// Where a segment's partial sums go: slot 0 of its CTA for a unit that an earlier CTA began, else 1.
-__device__ __forceinline__ int64_t slot_of(const Walk &w) { return 2 * static_cast<int64_t>(blockIdx.x) + (w.s0 > 0 ? 0 : 1); }
+// Where a segment's partial sums go: slot 0 of its CTA for a unit that an earlier CTA began, else 1 (which
+// only the CTA's last unit leaves to the merge).
+__device__ __forceinline__ int64_t slot_of(const Walk &w) { return 2 * static_cast<int64_t>(blockIdx.x) + (w.from > 0 ? 0 : 1); }
+
+// What a part with maximum m and sum l counts beside the maximum M of all: one that is all hidden has neither,
+// one whose scores are all NaN has no maximum and a sum of NaN.
+__device__ __forceinline__ float weight_of(float m, float l, float M) { return m == -INFINITY ? (l == 0.0f ? 0.0f : l) : ex2_approx(m - M); }
+// Joins the part `was` of earlier segments to this one's (M, L).  now, before: the two parts' weights.
+__device__ __forceinline__ void join(float2 was, float &M, float &L, float &now, float &before) {
+    const float most = fmaxf(M, was.x);
+    now = weight_of(M, L, most);
+    before = weight_of(was.x, was.y, most);
+    L = (now == 0.0f ? 0.0f : now * L) + (before == 0.0f ? 0.0f : before * was.y);
+    M = most;
+}
 
 // The tcgen05 kernel (kv4_attn_tc.cu): units of 256 query rows, tiles of 128 keys.
 constexpr int32_t kKv4TcRows = 256;
 constexpr int32_t kKv4TcTile = 128;
+constexpr int32_t kKv4TcSegment = 256;
 cudaError_t prepare_kv4_attention_tc();
 cudaError_t launch_kv4_attention_tc(const Kv4Args &k, int32_t grid, cudaStream_t st);
 

@@ -525,6 +525,40 @@ def test_many_light_keys_beside_a_heavy_one(dev, n, vscale):
     assert over <= 1, over
 
 
+@pytest.mark.parametrize("D", [64, 96])
+@pytest.mark.parametrize("n,B,kind", [(1, 1000, "cache"), (16, 700, "cache"), (17, 350, "cache"), (129, 170, "cache"), (129, 170, "causal")],
+                         ids=lambda v: str(v))
+def test_millions_of_cached_keys_in_one_run(dev, n, B, kind, D):
+    """Requests of 4 M tokens each (the same 65536 over and over, and every request the same pages), so many that
+    a CTA sums a whole request: sums of positive values, which accumulators that truncate let shrink.  They may truncate
+    2048 products in a row, 2^-23 each: 2^-12; the sum of p over a tile at a time rounds no more than that."""
+    from eagle_speculative_decoding_draft_gb300 import KV4Cache
+    base, t, page = 1 << 16, 1 << 22, 1024
+    c0 = KV4Cache(1, 1, D, num_pages=base // page, max_pages=base // page, page_size=page)
+    g = gen(21)
+    kc = rows(g, 1, base, 1, D, scale=0.3)
+    vc = (1 + torch.rand(1, base, 1, D, generator=g, device="cuda")).to(torch.bfloat16)
+    c0.append(kc, vc)
+    c = KV4Cache(B, 1, D, num_pages=base // page, max_pages=t // page, page_size=page, pages=c0.pages)
+    c.table.copy_((torch.arange(t // page, device="cuda") % (base // page)).expand(B, -1))
+    c.lengths.fill_(t)
+    q = torch.randn(1, n, 1, D, generator=g, device="cuda").to(torch.bfloat16)
+    kn, vn = (rows(g, 1, n, 1, D, scale=0.3), rows(g, 1, n, 1, D)) if kind == "causal" else (None, None)
+    many = lambda x: None if x is None else x.expand(B, -1, -1, -1).contiguous()
+    o = c.attention(many(q), many(kn), many(vn))
+    c.status()
+    see = torch.ones(n, base, dtype=torch.bool, device="cuda")
+    want, _ = ref.attend(q[0], kc[0], vc[0], None, None, see)
+    tol = ref.relative_tolerance(q[0], kc[0], vc[0], None, None, see, want) + 2.0 ** -11 * want.abs()
+    if kind == "causal":  # the cached keys' weights count 64 times beside the new keys'
+        scores = lambda k: q[0, :, 0].double() @ k[:, 0].T / math.sqrt(D)
+        old = scores(ref.stands_for(kc[0])).exp().sum(1, keepdim=True) * (t // base)
+        new = scores(kn[0].double()).exp().tril()
+        want = ((old * want[:, 0] + new @ vn[0, :, 0].double()) / (old + new.sum(1, keepdim=True)))[:, None]
+    over = float(((o.double() - want).abs() / tol).max())
+    assert over <= 1, over
+
+
 @pytest.mark.parametrize("n,H", ROWS, ids=lambda v: str(v))
 def test_largest_and_smallest_sizes(dev, n, H):
     """The ends of what the contract names, 2^100 and 2^-100, seen and weighted."""
