@@ -24,7 +24,8 @@
 //     2^-8 of the bf16 output); sums, the running maximum and p's sum are fp32.  So that p s keeps its bits
 //     whatever the values' size, s is lifted by the power of two (up to 2^15) that puts the largest one so far
 //     at 8 .. 16, and the first sum carries that power: a p of 2^-26 of the row's largest still has 11 bits
-//     of p s (without it four heavy keys among 65536 that weigh a fifth were off by 3 % at values of 3e-5).
+//     of p s (without it four heavy keys among 65536 that weigh a fifth were off by 3 % at values of 3e-5).  One
+//     lift for all groups: one a group took 123 us where this takes 115 (64 8-node trees).
 // Scores are formed transposed (16 keys on the MMA's M side, 8 query rows on N), so few query rows
 // waste no MMA rows, and the accumulators turn into the value product's operand by movmatrix.
 //

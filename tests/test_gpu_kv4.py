@@ -499,19 +499,22 @@ def test_new_values_of_many_sizes_at_once(dev, n, H):
     assert torch.equal(c.attention(q, kn, vn, mask=mask)[0, :n - 1], o[0, :n - 1])
 
 
-@pytest.mark.parametrize("vscale", [2e-6, 3e-5, 1e-3, 0.8])
+@pytest.mark.parametrize("vscale,other", [(2e-6, 1.0), (3e-5, 1.0), (1e-3, 1.0), (0.8, 1.0), (0.8, 1e-4), (3e-5, 1e4)])
 @pytest.mark.parametrize("n", [1, 16, 17])
-def test_many_light_keys_beside_a_heavy_one(dev, n, vscale):
+def test_many_light_keys_beside_a_heavy_one(dev, n, vscale, other):
     """65536 cached keys, of which four (one for each warp that multiplies) weigh e^11 times as much as the others, which
-    together still are a fifth of the sum: p and p s of the light ones keep their bits however small the values."""
+    together still are a fifth of the sum: p and p s of the light ones keep their bits however small the values, also
+    beside a group of 32 dims of another size."""
     from eagle_speculative_decoding_draft_gb300 import KV4Cache
-    D, t, B = 64, 65536, 600
+    D, t, B = 96, 65536, 600
     case = (1, n, 1, 1, D, 64, [t], "cache")
     made = build(case, 20, 0.05, vscale)
     c0, kc, vc, q, _, _, _ = made
+    vc[..., 32:64] *= other
     q.fill_(1.0)
-    kc[0, :64:16] = 11.0 / 8  # q . k / 8 = 11
+    kc[0, :64:16] = 11.0 / math.sqrt(D)  # q . k / sqrt(D) = 11
     vc[0, :64:16] = -vscale
+    vc[0, :64:16, :, 32:64] *= other
     c0.append(kc, vc, start=i32([0]))
     c = KV4Cache(B, 1, D, num_pages=c0.num_pages, max_pages=c0.max_pages, page_size=64, pages=c0.pages)  # all over the same pages
     c.table.copy_(c0.table.expand(B, -1))
