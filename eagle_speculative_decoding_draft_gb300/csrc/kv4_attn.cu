@@ -29,11 +29,10 @@
 // Scores are formed transposed (16 keys on the MMA's M side, 8 query rows on N), so few query rows
 // waste no MMA rows, and the accumulators turn into the value product's operand by movmatrix.
 //
-// Measured: 64 trees of 8 nodes, 32 heads of 128 over 1024 tokens each (352 MB) in 113 us, 0.46 of the
-// measured copy rate; 16 requests of 1 .. 65536 tokens under groups of 8 heads in 166 us, 0.60 of it.
+// Measured: 64 trees of 8 nodes, 32 heads of 128 over 1024 tokens each (352 MB) in 115 us, 0.45 of the
+// measured copy rate; 16 requests of 1 .. 65536 tokens under groups of 8 heads in 163 us, 0.61 of it.
 // Three CTAs of 128 registers a thread stay on an SM; it issues in 41 % of the cycles, waiting for
-// memory in the new keys' part and for fixed latencies in the rest.  Slower, measured: warps that copy
-// their own chunks, with four CTAs an SM or tiles of 32 keys (127 and 118 us against 115).
+// memory in the new keys' part (95 us without new keys) and for fixed latencies in the rest.
 //
 // kv4_line.cuh: how the work is split.  kv4_attn_tc.cu: the kernel for many query rows.
 #include <algorithm>
@@ -130,7 +129,7 @@ __global__ void __launch_bounds__(kThreads, Shape<G, NQ>::kBlocks) kv4_attention
         fence_barrier_init();
     }
     // no early launch of dependents: their blocks would take the places of the next call's CTAs, of
-    // which all must be resident at once (64 8-node trees back to back: 150 us with it, 115 without)
+    // which all must be resident at once (64 8-node trees back to back took 30 % longer with it)
     pdl_wait();
     const Kv4Attention &a = k.a;
     if (!find_place(k, place, lens, red, spots)) {  // all threads meet there: the mbarriers are ready, too
@@ -710,7 +709,7 @@ __global__ void __launch_bounds__(kThreads, Shape<G, NQ>::kBlocks) kv4_attention
 // Units that several CTAs worked on: block (c, .) merges the unit that CTA c is the second to work on.
 // o = sum_i w_i O_i / sum_i w_i l_i, w_i = 2^(m_i - max m), over its CTAs in order.  A warp a row: a lane
 // a part for the weights, then four dims a lane over all parts.  Bound by latency (two dependent
-// reads from L2): about 4 us.
+// reads from L2): 8 us by itself for 1952 rows of 2 to 3 parts.
 constexpr int kMergeRows = 4;
 __global__ void __launch_bounds__(kMergeRows * 32) kv4_merge_kernel(const __grid_constant__ Kv4Args k) {
     pdl_wait();
@@ -779,9 +778,13 @@ struct Variant {
 
 template <int G>
 Variant variant_of(int32_t mq) {
-    // Query rows a unit takes: 8 or 16; from 17 rows on tcgen05 takes over.  32 requests, 8 kv heads of
-    // 128: 16 rows take 40 us over 1024 tokens and 149 over 8192 here, 49 and 213 there; 32 rows 96 us
-    // over 1024 tokens here (with 32 rows a unit), 47 there.
+    // Query rows a unit takes: 8 or 16; from 17 rows on tcgen05 takes over.  us for 32 requests of 8 kv heads
+    // over 1024 / 8192 tokens each, this kernel (32 rows: with units of 32) and the tcgen05 one:
+    //     head_dim    16 rows here    there       17 here    there       32 here    there
+    //     32             21 /  79    36 / 146     41 / 183   36 / 145    42 / 185   34 / 141
+    //     64             24 /  95    40 / 184     48 / 215   40 / 184    50 / 220   38 / 181
+    //     96             30 / 117    49 / 222     66 / 286   49 / 223    69 / 290   46 / 200
+    //     128            39 / 147    50 / 214     87 / 365   50 / 214    91 / 377   47 / 208
     if (mq <= 8) return Variant{8, kThreads, Shape<G, 1>::kTotal, kv4_attention_kernel<G, 1>};
     if (mq <= 16) return Variant{16, kThreads, Shape<G, 2>::kTotal, kv4_attention_kernel<G, 2>};
     return Variant{kKv4TcRows, 0, 0, nullptr};
@@ -873,8 +876,8 @@ cudaError_t launch_kv4_attention(const Kv4Attention &a, cudaStream_t st) {
     k.tile_shift = v.kernel ? 6 : 7;
     k.min_tiles = v.kernel ? kMinTiles : 1;
     // cuts move to a unit's end from so many tiles: a unit cut in two writes and reads partial sums of
-    // all its rows.  32 requests of 64 nodes on tcgen05: 89 us with 0, 82 with 2, 66 with 5 and 8;
-    // the 2047-token piece 696, 696, 688 and 697
+    // all its rows.  With 0, 2, 5 and 8 on tcgen05: 32 requests of 64 nodes 96, 85, 62 and 62 us, of 65 nodes
+    // 143, 135, 114 and 114, 2047 tokens of two prompts 737, 736, 725 and 732
     k.snap = v.kernel ? 1 : 5;
     k.scale2 = kLog2e / sqrtf(static_cast<float>(G * kKv4Group));
     const int32_t full = grid_of(*d, G, v);

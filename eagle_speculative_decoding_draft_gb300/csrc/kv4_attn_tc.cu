@@ -25,15 +25,12 @@
 //
 // What bounds it: instruction issue and the chain of one stream's tile (scores, two passes, p, product):
 // the next 2047 tokens of two requests over 4096 cached ones (64 heads, 8 kv heads of 128)
-// take 690 us, 0.53 of the measured bf16 matrix rate; 32 requests of 65 nodes (260 rows,
-// a full unit and one of 4 rows each) over 1024 tokens 105 us.  Registers are what it is short of:
-// 26 warps leave 72 a thread, and what is spilled goes to L2, as shared memory takes all of L1: with
-// 112 bytes spilled the first took 822 us, with the walk over the units in shared memory and 16
-// bytes 784.  So the masks and the elements that fp16 does not hold have functions of their own.
-// Slower, measured: scores kept in registers from the first pass to the second, with registers moved from
-// the other warps (setmaxnreg; 855 us against 739); p from one pass with the reference as it is, on trial
-// (833 against 688); a second issuing warp (895 against 822: the streams then work in step); a second
-// copying warp and an L2 prefetch (708 against 688).
+// take 737 us, 0.50 of the measured bf16 matrix rate; 32 requests of 65 nodes (260 rows,
+// a full unit and one of 4 rows each) over 1024 tokens 118 us.  Registers are what it is short of:
+// 26 warps leave 72 a thread, and what is spilled goes to L2, as shared memory takes all of L1.  So is the
+// instruction cache: what the loops of the roles grow by shows in the time (with new keys by batches of 8
+// instead of 4 the first takes 833 us).  So the walk over the units lies in shared memory, and masks
+// and the elements that fp16 does not hold have functions of their own.
 //
 // Queries are scaled by a power of two so that a row's largest element is 2^9..2^10 (exact, as in
 // kv4_attn.cu).  Within 8 neighbouring dims the tiles hold them in the order 0 4 1 5 2 6 3 7, in
@@ -45,10 +42,10 @@
 // that see it add its terms one by one.  So nothing hidden reaches a row, whatever it is, and sizes may be
 // anything: only next to an element of 2^-12 or more do those below 2^-17 round, by 2^-25 at most (2^-13 of
 // it, next to 2^-11 that p's rounding takes).  Multiplying new tiles in bf16 instead, with the queries in both
-// types one after the other and p as hi + lo, took 866 us where this takes 715 (2047 tokens of two prompts).
+// types one after the other and p as hi + lo, took 866 us where this took 715 (2047 tokens of two prompts).
 // Tiles are made of blocks of 64 dims; with head_dim 32 and 96 half of the last one lies idle and the
-// MMAs stop before it (1000 tokens of two prompts over 4096 cached ones, 32 heads of 96: 179 us, where
-// the register kernel with 32 rows a unit took 1935).
+// MMAs stop before it (1000 tokens of two prompts over 4096 cached ones, 32 heads of 96: a tenth of the time
+// that the few-row kernel took with 32 rows a unit).
 // TMEM: S0 S1 O0 O1, 128 columns each (O uses D).  Every wait on an mbarrier is bounded; the roles meet at
 // named barriers as often as the units and tiles say, also after a wait has given up.
 #include <type_traits>
@@ -444,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
             int32_t s = w.s0;
             if (s < w.nt) {  // new keys or values, the next ones' loads under way
                 constexpr int kPer = S::kPer, kRowsWarp = S::kRowsWarp;
-                constexpr int kBatch = 4;  // with 8 at once the loops miss the instruction cache more: 65-node trees 108 us, not 105
+                constexpr int kBatch = 4;  // with 8 the loops miss the instruction cache more: 65-node trees 123 us, not 114
                 constexpr int kBatches = kKeys / (4 * kRowsWarp * kBatch);
                 const int32_t ch = lane % kPer, first = fw * kRowsWarp + lane / kPer;
                 const bool mine = S::kPieces == kPer || ch < S::kPieces;
@@ -874,7 +871,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_attention_tc_kernel(const __g
             const float inv = L == 0.0f ? 0.0f : 1.0f / L;
             const bool ok = __all_sync(kFull, !*abort_flag);
             // 16 columns at a time: a half of the stream's, or a quarter of both streams' sum, with
-            // head_dim 32 and 96 every fourth 16 of it (for all it took the 2047-token piece 688 -> 722 us)
+            // head_dim 32 and 96 every fourth 16 of it (for all it took the 2047-token piece 5 % longer)
             constexpr bool kQuarters = D % 64 == 0;
             const int32_t first = both ? h * (D / 2) : (2 * j + h) * (kQuarters ? D / 4 : 16);
             const int32_t end = both ? first + D / 2 : (kQuarters ? first + D / 4 : D), stride = kQuarters || both ? 16 : 64;

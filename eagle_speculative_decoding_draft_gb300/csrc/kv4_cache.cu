@@ -132,9 +132,10 @@ __device__ __forceinline__ uint32_t quantise(const uint32_t (&w)[16], uint32_t (
 
 // A lane takes whole groups (64 bytes): their least and largest value and parameters need no other
 // lane.  The chunk's rows that are written come one behind the other, keys, then values, 32 groups a
-// pass, the next pass on its way.  Bound by instruction issue: 33 k tokens of 8 kv heads of
-// 128 (176 MB) in 45 us, 0.58 of the measured copy rate (47 with single fp32 operations); a lane a 16-byte piece with the least and
-// largest value over four lanes took 82.  The accepted rows of 64 requests: 10 us.
+// pass, the next pass on its way.  Bound by instruction issue (76 % of the cycles): 33 k tokens of 8 kv heads
+// of 128 (176 MB) in 40 us, 0.65 of the measured copy rate; a lane a 16-byte piece with the least and
+// largest value over four lanes took twice as long.  The accepted rows of 64 requests: 6 us, and 1 more
+// where the lengths are the starts.
 template <int G>
 __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const AppendArgs a) {
     constexpr int kBytes = kv4_chunk_bytes(G);
@@ -273,7 +274,7 @@ __device__ __forceinline__ void values_of(uint32_t codes, uint32_t params, float
 }
 
 // T float: a lane takes 4 dims (16 bytes out), T bf16: 8.  Bound by memory: 65536 tokens of 8 kv heads
-// of 128 to fp32 (621 MB) in 96 us, 0.96 of the measured copy rate; 33 k tokens to bf16 (176 MB) in 31.
+// of 128 to fp32 (621 MB) in 96 us, 0.96 of the measured copy rate; 33 k tokens to bf16 (176 MB) in 29.
 template <int G, typename T>
 __global__ void __launch_bounds__(kThreads) kv4_read_kernel(const ReadArgs a) {
     constexpr int N = 16 / sizeof(T), kPer = 32 * G / N, R = 32 / kPer;  // dims a lane, lanes a row, rows at once

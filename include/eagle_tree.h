@@ -597,8 +597,8 @@ EAGLE_API eagle_status eagle_kv4_read(const eagle_kv4_cache *cache, int32_t batc
  * are, and the product of a key's weight and a group's step rounds to fp16: by 2^-11 of itself, but for
  * products below 2^-26 of the heaviest key's weight times the head's largest step (2^-18 where that step is
  * 16 or more, 2^-14 where it is below 2^-12), which lose bits.  Over 16 rows the matrix products take fp16:
- * what the cache stands for rounds by up to 2^-11 of itself, and an element of a new key or value below
- * 2^-17 by up to 2^-25 where its aligned group of 8 dims holds one of 2^-12 or more.
+ * weights and what the cache stands for round by up to 2^-11 of themselves, and an element of a new key
+ * or value below 2^-17 by up to 2^-25 where its aligned group of 8 dims holds one of 2^-12 or more.
  * nodes in [1, 4097]; heads a multiple of kv_heads, at most 65536, with nodes * heads / kv_heads <= 2^24.
  * Pointers are 16-byte aligned.
  * d_ws: eagle_kv4_attention_workspace_bytes bytes, 256-byte aligned, of any content; calls that may
