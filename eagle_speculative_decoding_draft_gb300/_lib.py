@@ -13,7 +13,7 @@ from pathlib import Path
 
 LIB_PATH = Path(__file__).resolve().parent / "lib" / "libeagle_tree.so"
 
-EAGLE_F32, EAGLE_BF16 = 0, 1
+EAGLE_F32, EAGLE_BF16, EAGLE_E4M3 = 0, 1, 2
 STATUS_NAMES = {
     0: "EAGLE_OK",
     1: "EAGLE_ERR_INVALID_ARG",
@@ -56,6 +56,13 @@ class DecoderLayerWeights(ctypes.Structure):
 class KV4CacheStruct(ctypes.Structure):
     _fields_ = [(n, c_int32) for n in ("kv_heads", "head_dim", "page_size", "num_pages", "max_pages")] + \
                [(n, c_void_p) for n in ("pages", "table", "lengths")]
+
+
+class LinearArgs(ctypes.Structure):
+    _fields_ = [(n, c_int32) for n in ("rows", "out_features", "in_features", "dtype", "y_dtype", "act")] + \
+               [("w", c_void_p), ("x", c_void_p), ("ldw", c_int64), ("ldx", c_int64)] + \
+               [(n, c_void_p) for n in ("w_scale", "x_scale", "bias", "residual")] + \
+               [("ldr", c_int64), ("y", c_void_p), ("ldy", c_int64)]
 
 
 _SIGS = {
@@ -103,6 +110,8 @@ _SIGS = {
     "eagle_kv4_pages_bytes": (c_size_t, [POINTER(KV4CacheStruct)]),
     "eagle_kv4_append": (c_int, [POINTER(KV4CacheStruct), c_int32, c_int32, c_int32, c_void_p, c_void_p, c_int64]
                          + [c_void_p] * 5),
+    "eagle_kv4_append_rotary": (c_int, [POINTER(KV4CacheStruct), c_int32, c_int32, c_int32, c_void_p, c_void_p, c_int64,
+                                        c_void_p, ctypes.c_float, c_int32, c_void_p, c_int64] + [c_void_p] * 6),
     "eagle_kv4_read": (c_int, [POINTER(KV4CacheStruct), c_int32, c_int32, c_void_p, c_void_p, c_void_p, c_int,
                                c_void_p, c_void_p]),
     "eagle_kv4_attention_workspace_bytes": (c_size_t, [POINTER(KV4CacheStruct), c_int32, c_int32]),
@@ -115,6 +124,11 @@ _SIGS = {
                                                            c_int32, c_int32]),
     "eagle_decoder_layer_kv4": (c_int, [POINTER(DecoderLayerWeights), POINTER(KV4CacheStruct), c_int32, c_int32]
                                 + [c_void_p] * 7 + [c_size_t, c_void_p, c_void_p]),
+    "eagle_quantize_rows": (c_int, [c_void_p, c_int64, c_int32, c_int32, c_void_p, c_int64, c_void_p, c_void_p]),
+    "eagle_rms_norm": (c_int, [c_void_p, c_int64, c_void_p, c_int64, c_void_p, ctypes.c_float, c_int32, c_int32,
+                               c_void_p, c_int64, c_int, c_void_p, c_int64, c_void_p, c_void_p]),
+    "eagle_linear_epilogue_workspace_bytes": (c_size_t, [c_int32]),
+    "eagle_linear": (c_int, [POINTER(LinearArgs), c_void_p, c_size_t, c_void_p, c_void_p]),
     "eagle_linear_noalloc_scratch_bytes": (c_size_t, []),
     "eagle_linear_bf16_noalloc": (c_int, [c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int32,
                                           c_int32, c_int32, c_void_p, c_int64, c_int32, c_void_p]),

@@ -5,6 +5,7 @@
 #include <cstdint>
 #include <utility>
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <nvtx3/nvToolsExt.h>
 
@@ -75,10 +76,22 @@ constexpr int kLinearMaxRows = 256;  // MMA N limit: rows of one row chunk
 constexpr int kLinearMaxLaunchRows = 32768;  // rows of one launch (row chunks of kLinearMaxRows)
 constexpr int kLinearMaxFixupRows = 16;  // above this, split tiles are summed by their owner or a second launch
 
+// What follows the sums of products before Y is stored:  act(sum x_scale w_scale + bias) + residual.
+enum : int32_t { kActNone = 0, kActSilu = 1, kActGelu = 2, kActSwiglu = 3 };
+struct LinearEpilogue {
+    const float *x_scale;  // [rows], [M]: 8-bit operands' scales
+    const float *w_scale;
+    const __nv_bfloat16 *residual;  // [rows][ldr] or null
+    int64_t ldr;
+    int32_t act;  // kActSwiglu is a form of its own: W holds M gate rows, then M up rows
+};
+
 struct LinearPlan {
-    CUtensorMap tmap_w;  // W [M][K] bf16, box {64, 128}, 128-byte swizzle
-    CUtensorMap tmap_x;  // X [rows][K] bf16, box {64, n_tile}, 128-byte swizzle
-    CUtensorMap tmap_y;  // Y [rows][ldo], box {128, 32}, no swizzle (valid when y_tma)
+    CUtensorMap tmap_w;  // W [M][K] in boxes of 128 rows x 128 bytes, 128-byte swizzle (gated: 2 x 16 rows)
+    CUtensorMap tmap_x;  // X [rows][K], boxes of n_tile rows (pairs: half) x 128 bytes, the same swizzle
+    CUtensorMap tmap_y;  // Y [rows][ldo], box {128, 32} (gated {64, 32}), no swizzle (valid when y_tma)
+    int32_t form;        // 0: bf16 and a bias; else 1 + (8-bit operands) + 2 (gated), with the epilogue
+    LinearEpilogue ep;
     int32_t M, K, rows, n_tile, num_kb, num_tiles, stages, tmem_cols, grid;
     size_t smem_bytes;
     const void *bias;  // [M] bf16 or null
@@ -118,11 +131,31 @@ bool plan_linear_bf16(LinearPlan *plan, const void *w, int64_t ldw, int32_t M, i
                       int64_t ldo, int32_t out_bf16, float *partials, int32_t *counters,
                       int32_t *status, int32_t num_sms);
 cudaError_t launch_linear_bf16(const LinearPlan &plan, cudaStream_t st);
+// The same product with an epilogue, from bf16 or 8-bit (e4m3) operands; row strides in elements.  With
+// ep.act == kActSwiglu W has 2 M rows.  launch_linear_bf16 launches the plan.
+bool plan_linear(LinearPlan *plan, bool fp8, const LinearEpilogue &ep, const void *w, int64_t ldw, int32_t M, int32_t K,
+                 const void *x, int64_t ldx, int32_t rows, const void *bias, void *out, int64_t ldo, int32_t out_bf16,
+                 float *partials, int32_t *counters, int32_t *status, int32_t num_sms);
+// linear.cu: the kernels of forms 1 .. 4.
+struct LinearArgs;
+cudaError_t launch_linear_form(const LinearPlan &plan, const LinearArgs &args, cudaStream_t st);
+cudaError_t prepare_linear_forms();
+// Their workspace: tickets (one a worker of the split, zero before and after), then partial sums.
+constexpr size_t kLinearTicketBytes = 4096;
+int32_t linear_sms();
+size_t linear_workspace(int32_t rows, int32_t sms);
 // Points a plan's output at another buffer of the same layout (re-encodes the output tensor map
 // of the TMA stores, or falls back to plain stores when the new buffer does not suit it).
 void linear_retarget_out(LinearPlan *plan, void *out);
 // One-time per-device kernel attributes (large dynamic shared memory).
 cudaError_t prepare_kernels();
+
+// norm.cu: rows quantised, and the residual's addition and RMS norm (bf16, or 8-bit rows where scale is given).
+cudaError_t launch_quantize_rows(const void *x, int64_t ldx, int32_t rows, int32_t n, void *y, int64_t ldy, float *scale,
+                                 cudaStream_t st);
+cudaError_t launch_rms_norm(const void *x, int64_t ldx, const void *residual, int64_t ldr, const void *w, float eps,
+                            int32_t rows, int32_t n, void *sum, int64_t lds, void *y, int64_t ldy, float *scale,
+                            cudaStream_t st);
 
 // fp32 path (FMA on the CUDA cores), same contract, no scratch.
 cudaError_t launch_linear_f32(const float *w, int64_t ldw, const float *x, int64_t ldx,

@@ -3,6 +3,8 @@
 // The engine's decoder layer hands out the keys and values of a tree's nodes; after the verify the
 // accepted path's rows join the cache, in 4 bits, at the request's next positions (a prompt's rows
 // in order, a path's rows through the list of its nodes).  kv4.cuh has the format.
+#include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "kernels.cuh"
@@ -58,6 +60,23 @@ struct AppendArgs {
     const int32_t *start;        // [B]
     int32_t *lengths;            // written by this kernel, or null (by kv4_lengths_kernel)
     int32_t *status;
+};
+
+// Keys turned on the way (and the queries of the same rows): pair (j, j + D/2) of a head by position times
+// theta^(-2j/D).  turn[j] is that frequency as a fraction of a whole turn in units of 2^-64, so that a
+// position's angle is their product modulo 2^64: exact whole-number arithmetic whatever the position, and
+// off by 2^-53 of the frequency (theta^(-2j/D) in 64 bits) times the position.
+struct RotaryArgs {
+    AppendArgs a;
+    const int32_t *positions;  // [B][src_rows], or null: start + row
+    const __nv_bfloat16 *q;    // [B][src_rows] rows of ldq elements, or null
+    __nv_bfloat16 *q_out;      // [B][src_rows][H][D]
+    int64_t ldq;
+    int32_t H;
+    int32_t slices;            // blocks of 8 kv heads a chunk
+    int32_t cache_blocks;      // the launch's first blocks write the cache, the others turn queries
+    int32_t q_rows;            // rows of one of those
+    uint64_t turn[64];
 };
 
 __device__ __forceinline__ int32_t slots_of(const AppendArgs &a, int32_t b) {
@@ -130,23 +149,93 @@ __device__ __forceinline__ uint32_t quantise(const uint32_t (&w)[16], uint32_t (
     return ok ? static_cast<uint32_t>(__half_as_ushort(s)) | (static_cast<uint32_t>(__half_as_ushort(m)) << 16) : 0x7fff7fffu;
 }
 
+// The table of cosines and sines: a block of 16 pairs' (cos, sin) is 128 bytes and starts kTurnBlock bytes
+// after the one before it, so that the 16-byte pieces that the lanes of a quarter warp take lie in other banks.
+constexpr int kTurnBlock = 128 + 16;
+__device__ __forceinline__ float2 *turn_entry(uint8_t *table, int32_t G, int32_t row, int32_t j) {
+    return reinterpret_cast<float2 *>(table + (row * G + (j >> 4)) * kTurnBlock) + (j & 15);
+}
+// A warp works out one row's pairs.
+template <int G>
+__device__ __forceinline__ void turn_row(const RotaryArgs &ra, uint8_t *table, int32_t row, int32_t pos) {
+    for (int32_t j = threadIdx.x & 31; j < 16 * G; j += 32) {
+        const uint64_t at = ra.turn[j] * static_cast<uint64_t>(static_cast<int64_t>(pos));
+        // within half a turn of 0; to 2^-25 of itself in fp32
+        const float half_turns = static_cast<float>(static_cast<int32_t>(at >> 32)) * 4.656612873e-10f;  // 2^-31
+        float s, c;
+        sincospif(half_turns, &s, &c);
+        *turn_entry(table, G, row, j) = make_float2(c, s);
+    }
+}
+// Turns two neighbouring values (a bf16 word) of one half of a head by the pairs' cosines and sines, and
+// rounds to bf16: the cache quantises bf16 keys, turned here or by the decoder layer.  `other` is the word
+// of the other half; sign -1 for the first half.
+__device__ __forceinline__ uint32_t turn_word(uint32_t own, uint32_t other, float sign, const float4 &cs) {
+    const float x = __uint_as_float(own << 16), y = __uint_as_float(own & 0xffff0000u);
+    const float p = __uint_as_float(other << 16), q = __uint_as_float(other & 0xffff0000u);
+    const __nv_bfloat162 r = __floats2bfloat162_rn(fmaf(x, cs.x, sign * (p * cs.y)), fmaf(y, cs.z, sign * (q * cs.w)));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+// A key's group g in place; `head` is the key as it came.  Blocks of 16 dims: block i and block i + G (i < G)
+// are each other's halves.
+template <int G>
+__device__ __forceinline__ void turn_group(uint8_t *table, int32_t row, int32_t g, const uint4 *head, uint32_t (&w)[16]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int32_t i = 2 * g + h;
+        const bool first = i < G;
+        const uint4 *other = head + 2 * (first ? i + G : i - G);
+        const uint4 o0 = __ldg(other), o1 = __ldg(other + 1);
+        const uint32_t o[8] = {o0.x, o0.y, o0.z, o0.w, o1.x, o1.y, o1.z, o1.w};
+        const float4 *cs = reinterpret_cast<const float4 *>(turn_entry(table, G, row, 16 * (first ? i : i - G)));
+#pragma unroll
+        for (int k = 0; k < 8; ++k) w[8 * h + k] = turn_word(w[8 * h + k], o[k], first ? -1.0f : 1.0f, cs[k]);
+    }
+}
+// ra.q_rows rows of queries (16 at most): a thread turns 8 pairs of a head at a time.
+template <int G>
+__device__ __forceinline__ void turn_queries(const RotaryArgs &ra, uint8_t *table, int32_t block) {
+    const AppendArgs &a = ra.a;
+    const int64_t all = static_cast<int64_t>(a.B) * a.src_rows, row0 = static_cast<int64_t>(block) * ra.q_rows;
+    const int32_t rows = static_cast<int32_t>(min(all - row0, static_cast<int64_t>(ra.q_rows)));
+    for (int32_t t = threadIdx.x >> 5; t < rows; t += kWarps) {
+        const int64_t r = row0 + t;
+        const int32_t b = static_cast<int32_t>(r / a.src_rows);
+        turn_row<G>(ra, table, t, ra.positions ? ra.positions[r] : a.start[b] + static_cast<int32_t>(r - static_cast<int64_t>(b) * a.src_rows));
+    }
+    __syncthreads();
+    constexpr int kEights = 2 * G;  // of a half head
+    const int32_t per_row = ra.H * kEights;
+    for (int32_t u = threadIdx.x; u < rows * per_row; u += kThreads) {
+        const int32_t t = u / per_row, in = u - t * per_row, head = in / kEights, e = in - head * kEights;
+        const int64_t at = static_cast<int64_t>(head) * 32 * G + 8 * e;
+        const uint4 *src = reinterpret_cast<const uint4 *>(ra.q + (row0 + t) * ra.ldq + at);
+        uint4 *dst = reinterpret_cast<uint4 *>(ra.q_out + (row0 + t) * ra.H * 32 * G + at);
+        const uint4 x = src[0], y = src[2 * G];
+        const float4 *cs = reinterpret_cast<const float4 *>(turn_entry(table, G, t, 8 * e));
+        const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+        uint32_t p[4], q[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            p[k] = turn_word(xw[k], yw[k], -1.0f, cs[k]);
+            q[k] = turn_word(yw[k], xw[k], 1.0f, cs[k]);
+        }
+        dst[0] = make_uint4(p[0], p[1], p[2], p[3]);
+        dst[2 * G] = make_uint4(q[0], q[1], q[2], q[3]);
+    }
+}
+
 // A lane takes whole groups (64 bytes): their least and largest value and parameters need no other
 // lane.  The chunk's rows that are written come one behind the other, keys, then values, 32 groups a
 // pass, the next pass on its way.  Bound by instruction issue (76 % of the cycles): 33 k tokens of 8 kv heads
 // of 128 (176 MB) in 40 us, 0.65 of the measured copy rate; a lane a 16-byte piece with the least and
 // largest value over four lanes took twice as long.  The accepted rows of 64 requests: 6 us, and 1 more
 // where the lengths are the starts.
-template <int G>
-__global__ void __launch_bounds__(kThreads) kv4_append_kernel(const AppendArgs a) {
+template <int G, bool kRotary>
+__device__ __forceinline__ void append_chunk(const AppendArgs &a, uint8_t *st, uint8_t *order, uint8_t *table,
+                                             const RotaryArgs *ra, int32_t b, int32_t rest, int32_t ci, int32_t hk) {
     constexpr int kBytes = kv4_chunk_bytes(G);
-    __shared__ __align__(16) uint8_t stage[kWarps][kBytes];
-    __shared__ uint8_t order[kWarps][16];  // the rows that are written, in order
-    pdl_launch_dependents();
-    pdl_wait();
-    const int32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    int32_t b, rest;
-    if (!unit_request(a.u, static_cast<int32_t>(blockIdx.x) * kWarps + warp, b, rest)) return;
-    const int32_t ci = rest / a.u.Hk, hk = rest - ci * a.u.Hk;
+    const int32_t lane = threadIdx.x & 31;
     const int64_t start = a.start[b];
     const int32_t cnt = slots_of(a, b);
     if (start < 0) {
@@ -173,13 +262,26 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const AppendArgs a
     const uint32_t rows = __ballot_sync(kFull, src >= 0);
     if (rows == 0) return;
     const int32_t live = __popc(rows), items = 2 * live * G;
-    if (src >= 0) order[warp][__popc(rows & ((1u << lane) - 1u))] = static_cast<uint8_t>(lane);
-    __syncwarp();
+    if (src >= 0) order[__popc(rows & ((1u << lane) - 1u))] = static_cast<uint8_t>(lane);
+    if constexpr (kRotary) {
+        // the block's warps share the chunk: each does two of its rows
+        int32_t pos = 0;
+        if (src >= 0)
+            pos = ra->positions ? ra->positions[static_cast<int64_t>(b) * a.src_rows + src] : static_cast<int32_t>(chunk0 + lane);
+        for (int32_t t = threadIdx.x >> 5; t < 16; t += kWarps) {
+            const int32_t p = __shfl_sync(kFull, pos, t);
+            if ((rows >> t) & 1u) turn_row<G>(*ra, table, t, p);
+        }
+        __syncthreads();  // every warp of the block is here: what ended above it is the same for all
+        if (hk >= a.u.Hk) return;
+    } else {
+        __syncwarp();
+    }
     // group `it` of the pass: row, tensor and place in the row
     auto load = [&](int32_t it, uint32_t (&w)[16]) {
         const int32_t n = it / G, g = it - n * G;
         const bool value = n >= live;
-        const int32_t t = order[warp][min(value ? n - live : n, 15)], from = __shfl_sync(kFull, src, t & 15);
+        const int32_t t = order[min(value ? n - live : n, 15)], from = __shfl_sync(kFull, src, t & 15);
         if (it < items) {
             const uint4 *p = reinterpret_cast<const uint4 *>((value ? a.w : a.k) + (static_cast<int64_t>(b) * a.src_rows + from) * a.ld +
                                                              (static_cast<int64_t>(hk) * G + g) * kKv4Group);
@@ -200,22 +302,28 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const AppendArgs a
         if (lane == 0) latch(a.status, kDevBounds);
         return;
     }
-    uint8_t *st = stage[warp];
 #pragma unroll 1
     for (int32_t it0 = 0; it0 < items; it0 += 32) {
         load(it0 + 32 + lane, ahead);
         uint32_t codes[4];
-        const uint32_t params = quantise(now, codes);
         const int32_t it = it0 + lane;
+        if constexpr (kRotary) {
+            const int32_t n = it / G, g = it - n * G;
+            const int32_t t = order[min(n, 15)], from = __shfl_sync(kFull, src, t & 15);
+            if (n < live)
+                turn_group<G>(table, t, g, reinterpret_cast<const uint4 *>(a.k + (static_cast<int64_t>(b) * a.src_rows + from) * a.ld +
+                                                                           static_cast<int64_t>(hk) * G * kKv4Group), now);
+        }
+        const uint32_t params = quantise(now, codes);
         if (it < items) {
             const int32_t n = it / G, g = it - n * G;
             if (n < live) {
-                const int32_t ks = kv4_key_slot(order[warp][n]);
+                const int32_t ks = kv4_key_slot(order[n]);
 #pragma unroll
                 for (int qd = 0; qd < 4; ++qd) *reinterpret_cast<uint32_t *>(st + ks * 16 * G + (qd * G + g) * 4) = codes[qd];
                 *reinterpret_cast<uint32_t *>(st + kv4_key_params(G) + ks * 4 * G + 4 * g) = params;
             } else {
-                const int32_t t = order[warp][n - live];
+                const int32_t t = order[n - live];
                 uint8_t *vrow = st + kv4_value_codes(G) + t * 16 * G;
 #pragma unroll
                 for (int gq = 0; gq < 8; ++gq)
@@ -241,6 +349,40 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const AppendArgs a
         const int32_t t = key ? ((row & 7) >> 1) | ((row & 1) << 2) | (row & 8) : row;
         if ((rows >> t) & 1u) reinterpret_cast<Word *>(chunk)[at] = reinterpret_cast<const Word *>(st)[at];
     }
+}
+
+template <int G>
+__global__ void __launch_bounds__(kThreads) kv4_append_kernel(const AppendArgs a) {
+    __shared__ __align__(16) uint8_t stage[kWarps][kv4_chunk_bytes(G)];
+    __shared__ uint8_t order[kWarps][16];  // the rows that are written, in order
+    pdl_launch_dependents();
+    pdl_wait();
+    const int32_t warp = threadIdx.x >> 5;
+    int32_t b, rest;
+    if (!unit_request(a.u, static_cast<int32_t>(blockIdx.x) * kWarps + warp, b, rest)) return;
+    const int32_t ci = rest / a.u.Hk, hk = rest - ci * a.u.Hk;
+    append_chunk<G, false>(a, stage[warp], order[warp], nullptr, nullptr, b, rest, ci, hk);
+}
+
+// Blocks of one chunk and up to 8 of its kv heads, a warp a head: the chunk's cosines and sines are worked
+// out once a block.  Further blocks turn the queries.
+template <int G>
+__global__ void __launch_bounds__(kThreads) kv4_rotary_kernel(const __grid_constant__ RotaryArgs ra) {
+    __shared__ __align__(16) uint8_t stage[kWarps][kv4_chunk_bytes(G)];
+    __shared__ __align__(16) uint8_t table[16 * G * kTurnBlock];
+    __shared__ uint8_t order[kWarps][16];
+    pdl_launch_dependents();
+    pdl_wait();
+    const AppendArgs &a = ra.a;
+    const int32_t warp = threadIdx.x >> 5, block = blockIdx.x;
+    if (block >= ra.cache_blocks) {
+        turn_queries<G>(ra, table, block - ra.cache_blocks);
+        return;
+    }
+    const int32_t chunks = a.u.per_request / a.u.Hk;  // that a request may touch
+    const int32_t slice = block % ra.slices, unit = block / ra.slices;
+    const int32_t b = unit / chunks, ci = unit - b * chunks, hk = slice * kWarps + warp;
+    append_chunk<G, true>(a, stage[warp], order[warp], table, &ra, b, ci * a.u.Hk + hk, ci, hk);
 }
 
 // The lengths alone, after a write whose blocks all read their starts from them.
@@ -375,6 +517,15 @@ AppendKernel append_kernel(int32_t G) {
         default: return kv4_append_kernel<4>;
     }
 }
+using RotaryKernel = void (*)(const RotaryArgs);
+RotaryKernel rotary_kernel(int32_t G) {
+    switch (G) {
+        case 1: return kv4_rotary_kernel<1>;
+        case 2: return kv4_rotary_kernel<2>;
+        case 3: return kv4_rotary_kernel<3>;
+        default: return kv4_rotary_kernel<4>;
+    }
+}
 using ReadKernel = void (*)(const ReadArgs);
 template <typename T>
 ReadKernel read_kernel(int32_t G) {
@@ -387,6 +538,35 @@ ReadKernel read_kernel(int32_t G) {
 }
 
 bool misaligned(const void *p, uintptr_t by) { return (reinterpret_cast<uintptr_t>(p) & (by - 1)) != 0; }
+
+// What the two writes have in common.
+eagle_status append_args(const eagle_kv4_cache *cache, int32_t batch, int32_t src_rows, int32_t slots, const void *d_k,
+                         const void *d_v, int64_t ld, const int32_t *d_select, const int32_t *d_count,
+                         const int32_t *d_start, int32_t *d_status, AppendArgs *out) {
+    AppendArgs &a = *out;
+    if (!kv4_view(cache, &a.v) || batch < 0 || src_rows < 0 || slots < 0) return EAGLE_ERR_INVALID_ARG;
+    if (!d_select && slots > src_rows) return EAGLE_ERR_INVALID_ARG;
+    if (batch == 0) return EAGLE_OK;
+    const int64_t row = static_cast<int64_t>(a.v.Hk) * a.v.G * kKv4Group;
+    if (slots > 0 && (!d_k || !d_v || ld < row || ld % 8 || misaligned(d_k, 16) || misaligned(d_v, 16)))
+        return EAGLE_ERR_INVALID_ARG;
+    if (misaligned(d_select, 4) || misaligned(d_count, 4) || misaligned(d_start, 4) || misaligned(d_status, 4))
+        return EAGLE_ERR_INVALID_ARG;
+    a.B = batch;
+    a.src_rows = src_rows;
+    a.slots = slots;
+    a.k = static_cast<const __nv_bfloat16 *>(d_k);
+    a.w = static_cast<const __nv_bfloat16 *>(d_v);
+    a.ld = ld;
+    a.select = d_select;
+    a.count = d_count;
+    a.start = d_start ? d_start : cache->lengths;
+    a.status = d_status;
+    if (!units_of(batch, a.v.Hk, slots > 0 ? slots : 1, &a.u)) return EAGLE_ERR_UNSUPPORTED;
+    // starts of their own: the lengths are written in the same launch
+    a.lengths = a.start != cache->lengths ? cache->lengths : nullptr;
+    return EAGLE_OK;
+}
 
 }  // namespace
 }  // namespace eagle
@@ -412,32 +592,61 @@ eagle_status eagle_kv4_append(const eagle_kv4_cache *cache, int32_t batch, int32
     using namespace eagle;
     NvtxRange nvtx_range("eagle_kv4_append");
     AppendArgs a{};
-    if (!kv4_view(cache, &a.v) || batch < 0 || src_rows < 0 || slots < 0) return EAGLE_ERR_INVALID_ARG;
-    if (!d_select && slots > src_rows) return EAGLE_ERR_INVALID_ARG;
-    if (batch == 0) return EAGLE_OK;
-    const int64_t row = static_cast<int64_t>(a.v.Hk) * a.v.G * kKv4Group;
-    if (slots > 0 && (!d_k || !d_v || ld < row || ld % 8 || misaligned(d_k, 16) || misaligned(d_v, 16)))
-        return EAGLE_ERR_INVALID_ARG;
-    if (misaligned(d_select, 4) || misaligned(d_count, 4) || misaligned(d_start, 4) || misaligned(d_status, 4))
-        return EAGLE_ERR_INVALID_ARG;
-    a.B = batch;
-    a.src_rows = src_rows;
-    a.slots = slots;
-    a.k = static_cast<const __nv_bfloat16 *>(d_k);
-    a.w = static_cast<const __nv_bfloat16 *>(d_v);
-    a.ld = ld;
-    a.select = d_select;
-    a.count = d_count;
-    a.start = d_start ? d_start : cache->lengths;
-    a.status = d_status;
-    if (!units_of(batch, a.v.Hk, slots > 0 ? slots : 1, &a.u)) return EAGLE_ERR_UNSUPPORTED;
-    // starts of their own: the lengths are written in the same launch
-    const bool own_lengths = a.start != cache->lengths;
-    a.lengths = own_lengths ? cache->lengths : nullptr;
+    const eagle_status bad = append_args(cache, batch, src_rows, slots, d_k, d_v, ld, d_select, d_count, d_start, d_status, &a);
+    if (bad != EAGLE_OK || batch == 0) return bad;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (launch_pdl(append_kernel(a.v.G), grid_of(a.u), dim3(kThreads), 0, st, a) != cudaSuccess) return EAGLE_ERR_CUDA;
-    if (!own_lengths &&
-        launch_pdl(kv4_lengths_kernel, dim3(batch), dim3(32), 0, st, a, cache->lengths) != cudaSuccess)
+    if (!a.lengths && launch_pdl(kv4_lengths_kernel, dim3(batch), dim3(32), 0, st, a, cache->lengths) != cudaSuccess)
+        return EAGLE_ERR_CUDA;
+    return EAGLE_OK;
+}
+
+eagle_status eagle_kv4_append_rotary(const eagle_kv4_cache *cache, int32_t batch, int32_t src_rows, int32_t slots,
+                                     const void *d_k, const void *d_v, int64_t ld, const int32_t *d_positions,
+                                     float rope_theta, int32_t heads, const void *d_q, int64_t ldq, void *d_q_out,
+                                     const int32_t *d_select, const int32_t *d_count, const int32_t *d_start,
+                                     int32_t *d_status, eagle_stream_t stream) {
+    using namespace eagle;
+    NvtxRange nvtx_range("eagle_kv4_append_rotary");
+    RotaryArgs r{};
+    const eagle_status bad = append_args(cache, batch, src_rows, slots, d_k, d_v, ld, d_select, d_count, d_start, d_status, &r.a);
+    if (bad != EAGLE_OK) return bad;
+    if (!(rope_theta > 0.0f) || (d_select && !d_positions) || misaligned(d_positions, 4)) return EAGLE_ERR_INVALID_ARG;
+    if ((d_q == nullptr) != (d_q_out == nullptr)) return EAGLE_ERR_INVALID_ARG;
+    if (batch == 0) return EAGLE_OK;
+    const int32_t D = r.a.v.G * kKv4Group;
+    if (d_q && (heads < 1 || heads > 65536 || ldq < static_cast<int64_t>(heads) * D || ldq % 8 || misaligned(d_q, 16) ||
+                misaligned(d_q_out, 16)))
+        return EAGLE_ERR_INVALID_ARG;
+    r.positions = d_positions;
+    const int64_t units = r.a.u.total / r.a.u.Hk;  // (request, chunk)
+    r.slices = (r.a.u.Hk + kWarps - 1) / kWarps;
+    int64_t blocks = units * r.slices;
+    r.cache_blocks = static_cast<int32_t>(blocks);
+    if (d_q && src_rows > 0) {
+        int dev = 0, sms = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess ||
+            cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+            return EAGLE_ERR_CUDA;
+        const int64_t rows = static_cast<int64_t>(batch) * src_rows;
+        r.q = static_cast<const __nv_bfloat16 *>(d_q);
+        r.q_out = static_cast<__nv_bfloat16 *>(d_q_out);
+        r.ldq = ldq;
+        r.H = heads;
+        // as many rows a block as leave two blocks an SM, 16 at most (the table's)
+        r.q_rows = static_cast<int32_t>(std::min<int64_t>(16, std::max<int64_t>(1, rows / (2 * sms))));
+        blocks += (rows + r.q_rows - 1) / r.q_rows;
+    }
+    if (blocks > INT32_MAX) return EAGLE_ERR_UNSUPPORTED;
+    constexpr double kTwoPi = 6.283185307179586;
+    for (int32_t j = 0; j < D / 2; ++j) {
+        const double turns = std::pow(static_cast<double>(rope_theta), -2.0 * j / D) / kTwoPi, part = turns - std::floor(turns);
+        r.turn[j] = static_cast<uint64_t>(std::ldexp(part, 64));  // exact: part <= 1 - 2^-53
+    }
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (launch_pdl(rotary_kernel(r.a.v.G), dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, st, r) != cudaSuccess)
+        return EAGLE_ERR_CUDA;
+    if (!r.a.lengths && launch_pdl(kv4_lengths_kernel, dim3(batch), dim3(32), 0, st, r.a, cache->lengths) != cudaSuccess)
         return EAGLE_ERR_CUDA;
     return EAGLE_OK;
 }

@@ -1,0 +1,110 @@
+// linear.cu - the streamed-weight product with an epilogue: the kernels of gemm.cuh's forms for bf16 and for
+// 8-bit (e4m3) operands, plain and gated, and their entry point.
+//
+// A draft layer's products are followed by what is small next to them: the operands' scales, a bias, an
+// activation, the residual's addition.  Done on the accumulator they cost no pass over memory.
+#include <mutex>
+
+#include "../../include/eagle_tree.h"
+#include "gemm.cuh"
+
+namespace eagle {
+namespace {
+
+template <class Op>
+cudaError_t prepare_form() {
+    cudaError_t e = cudaFuncSetAttribute(linear_tc_kernel<0, Op>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(kMaxDynSmem));
+    if (e != cudaSuccess) return e;
+    return cudaFuncSetAttribute(linear_tc_kernel<1, Op>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(kMaxDynSmem));
+}
+
+}  // namespace
+
+// SMs of the current device, 0 where they cannot be read or are more than the tickets count.
+int32_t linear_sms() {
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return 0;
+    return sms <= static_cast<int>(kLinearTicketBytes / 4) ? sms : 0;
+}
+
+size_t linear_workspace(int32_t rows, int32_t sms) {
+    return kLinearTicketBytes + linear_partials_bytes(sms, linear_n_tile(rows < kLinearMaxRows ? rows : kLinearMaxRows));
+}
+
+cudaError_t prepare_linear_forms() {
+    static std::mutex mu;
+    static bool done[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    std::lock_guard<std::mutex> lock(mu);
+    if (done[dev]) return cudaSuccess;
+    e = prepare_kernels();
+    if (e == cudaSuccess) e = prepare_form<EpilogueOp<false, false>>();
+    if (e == cudaSuccess) e = prepare_form<EpilogueOp<true, false>>();
+    if (e == cudaSuccess) e = prepare_form<EpilogueOp<false, true>>();
+    if (e == cudaSuccess) e = prepare_form<EpilogueOp<true, true>>();
+    done[dev] = e == cudaSuccess;
+    return e;
+}
+
+cudaError_t launch_linear_form(const LinearPlan &p, const LinearArgs &a, cudaStream_t st) {
+    switch (p.form) {
+        case 1: return launch_form<EpilogueOp<false, false>>(p, a, st);
+        case 2: return launch_form<EpilogueOp<true, false>>(p, a, st);
+        case 3: return launch_form<EpilogueOp<false, true>>(p, a, st);
+        case 4: return launch_form<EpilogueOp<true, true>>(p, a, st);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace eagle
+
+extern "C" {
+
+size_t eagle_linear_epilogue_workspace_bytes(int32_t rows) {
+    const int32_t sms = eagle::linear_sms();
+    if (rows < 1 || rows > eagle::kLinearMaxLaunchRows || sms < 1) return 0;
+    return eagle::linear_workspace(rows, sms);
+}
+
+eagle_status eagle_linear(const eagle_linear_args *l, void *d_ws, size_t ws_bytes, int32_t *d_status,
+                          eagle_stream_t stream) {
+    using namespace eagle;
+    NvtxRange nvtx_range("eagle_linear");
+    if (!l || l->rows < 0 || l->rows > kLinearMaxLaunchRows || l->in_features < 1 || l->out_features < 1)
+        return EAGLE_ERR_INVALID_ARG;
+    if (l->dtype != EAGLE_BF16 && l->dtype != EAGLE_E4M3) return EAGLE_ERR_INVALID_ARG;
+    if (l->y_dtype != EAGLE_BF16 && l->y_dtype != EAGLE_F32) return EAGLE_ERR_INVALID_ARG;
+    if (l->act < EAGLE_ACT_NONE || l->act > EAGLE_ACT_SWIGLU) return EAGLE_ERR_INVALID_ARG;
+    if (l->rows == 0) return EAGLE_OK;
+    const bool fp8 = l->dtype == EAGLE_E4M3, gated = l->act == EAGLE_ACT_SWIGLU;
+    const int32_t M = l->out_features, K = l->in_features, step = fp8 ? 16 : 8;
+    if (gated && M > INT32_MAX / 2) return EAGLE_ERR_INVALID_ARG;
+    auto off = [](const void *p, uintptr_t by) { return (reinterpret_cast<uintptr_t>(p) & (by - 1)) != 0; };
+    if (!l->w || !l->x || !l->y || !d_ws) return EAGLE_ERR_INVALID_ARG;
+    if (fp8 != (l->w_scale != nullptr) || fp8 != (l->x_scale != nullptr)) return EAGLE_ERR_INVALID_ARG;
+    if (off(l->w, 16) || off(l->x, 16) || off(l->w_scale, 4) || off(l->x_scale, 4) || off(l->bias, 2) || off(l->residual, 2))
+        return EAGLE_ERR_INVALID_ARG;
+    if (off(l->y, l->y_dtype == EAGLE_F32 ? 4 : 2) || off(d_ws, 256) || off(d_status, 4)) return EAGLE_ERR_INVALID_ARG;
+    if (l->ldw < K || l->ldx < K || l->ldw % step || l->ldx % step || l->ldy < M || (l->residual && l->ldr < M))
+        return EAGLE_ERR_INVALID_ARG;
+    const int32_t sms = linear_sms();
+    if (sms < 1) return EAGLE_ERR_CUDA;
+    if (ws_bytes < linear_workspace(l->rows, sms)) return EAGLE_ERR_INVALID_ARG;
+    if (prepare_linear_forms() != cudaSuccess) return EAGLE_ERR_CUDA;
+    const LinearEpilogue ep{l->x_scale, l->w_scale, static_cast<const __nv_bfloat16 *>(l->residual), l->ldr,
+                            static_cast<int32_t>(l->act)};
+    LinearPlan p;
+    if (!plan_linear(&p, fp8, ep, l->w, l->ldw, M, K, l->x, l->ldx, l->rows, l->bias, l->y, l->ldy,
+                     l->y_dtype == EAGLE_BF16, reinterpret_cast<float *>(static_cast<uint8_t *>(d_ws) + kLinearTicketBytes),
+                     static_cast<int32_t *>(d_ws), d_status, sms))
+        return EAGLE_ERR_UNSUPPORTED;
+    return launch_linear_bf16(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? EAGLE_OK : EAGLE_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -152,6 +152,49 @@ class KV4Cache:
             check(self._lib.eagle_kv4_append(self._ref, self.batch, rows, slots, k.data_ptr(), v.data_ptr(), ld, p_select,
                                              p_count, p_start, self._status_ptr, self._raw_stream(stream)), "eagle_kv4_append")
 
+    def append_rotary(self, k, v, q=None, rope_theta: float = 10000.0, positions=None, select=None, count=None,
+                      start=None, out=None, stream=None):
+        """``append`` with the keys turned on the way (RoPE, rotate-half, each row at positions
+        [batch][rows] int32, or without them at its place in the cache: row j of request b at
+        start[b] + j; rows that `select` names need positions).  k and v come as a projection leaves
+        them.  With the queries q [batch][rows][heads][head_dim] of the same rows they are turned too
+        and returned (in out, if given, which may be a contiguous q itself)."""
+        ld = self._kv(k, v)
+        slots = rows = k.shape[1]
+        if select is not None:
+            if select.dim() != 2:
+                raise ValueError("select must be [batch][slots]")
+            if positions is None:
+                raise ValueError("rows that select names need positions")
+            slots = select.shape[1]
+        device = self.device
+        p_positions = _ints(positions, "positions", device, (self.batch, rows))
+        p_select = _ints(select, "select", device, (self.batch, slots))
+        p_count = _ints(count, "count", device, (self.batch,))
+        p_start = _ints(start, "start", device, (self.batch,))
+        heads = ldq = 0
+        p_q = p_out = None
+        if q is not None:
+            if q.dtype is not _BF16 or q.get_device() != self._index:
+                _here(q, "q", device, _BF16)
+            if q.dim() != 4 or q.shape[:2] != k.shape[:2] or q.shape[3] != self.head_dim or q.shape[2] < 1:
+                raise ValueError(f"q must be [{self.batch}][{rows}][heads][{self.head_dim}]")
+            heads, p_q = q.shape[2], q.data_ptr()
+            ldq = _row_step(q, "q") if rows else heads * self.head_dim
+        elif out is not None:
+            raise ValueError("out needs q")
+        with self._on(stream):
+            if q is not None:
+                if out is None:
+                    out = q.new_empty(q.shape)
+                elif not _here(out, "out", device, _BF16).is_contiguous() or out.shape != q.shape:
+                    raise ValueError("out must be contiguous and have the shape of q")
+                p_out = out.data_ptr()
+            check(self._lib.eagle_kv4_append_rotary(
+                self._ref, self.batch, rows, slots, k.data_ptr(), v.data_ptr(), ld, p_positions, rope_theta, heads, p_q, ldq,
+                p_out, p_select, p_count, p_start, self._status_ptr, self._raw_stream(stream)), "eagle_kv4_append_rotary")
+        return out
+
     def read(self, start=None, rows=None, dtype=torch.bfloat16, out=None, stream=None):
         """The values that positions start[b] (default 0) .. + rows - 1 stand for: (k, v), each
         [batch][rows][kv_heads][head_dim] of `dtype` (bf16 or fp32).  out = (k, v) receives them (its

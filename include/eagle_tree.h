@@ -70,7 +70,9 @@ typedef enum {
     EAGLE_ERR_DEVICE_BOUNDS = 6   /* a kernel saw an out-of-range index or a broken tree */
 } eagle_status;
 
-typedef enum { EAGLE_F32 = 0, EAGLE_BF16 = 1 } eagle_dtype;
+/* EAGLE_E4M3 (8 bits: 4 of exponent, 3 of mantissa; largest value 448) is a type of eagle_rms_norm,
+ * eagle_quantize_rows and eagle_linear alone. */
+typedef enum { EAGLE_F32 = 0, EAGLE_BF16 = 1, EAGLE_E4M3 = 2 } eagle_dtype;
 
 /*
  * The engine's configuration.  Knob names follow the SGLang flags quoted on the zdszero page
@@ -566,6 +568,29 @@ EAGLE_API eagle_status eagle_kv4_append(const eagle_kv4_cache *cache, int32_t ba
                                         eagle_stream_t stream);
 
 /*
+ * eagle_kv4_append with the keys turned on the way (Llama's rotate-half RoPE, as eagle_decoder_layer turns
+ * them: pair (j, j + D/2) of a head by position * rope_theta^(-2j/D)) and rounded to bf16 before they are
+ * quantised: keys and values of a projection go to the cache without a pass of their own.  The queries of
+ * the same rows, where given, are turned in the same launch.
+ *   d_positions  [batch][src_rows] int32: the position of each row (any value); NULL: row j of request b is
+ *                at start[b] + j, its place in the cache (then d_select must be NULL)
+ *   d_q, ldq     [batch][src_rows] rows of heads * head_dim bf16, ldq elements apart (a multiple of 8), or NULL
+ *   d_q_out      [batch][src_rows][heads][head_dim] bf16: every row's turned queries, also those of rows that
+ *                are not written to the cache; may be d_q itself where ldq is heads * head_dim
+ * Pointers are 16-byte aligned; the other arguments, what is written and what is latched are those of
+ * eagle_kv4_append.  Angles are whole-number products modulo a turn: exact for any position but for the
+ * frequencies' own rounding in 64 bits; their cosines and sines, and the turned values until they are
+ * rounded, are fp32.  heads at most 65536; rope_theta > 0.
+ * Errors: INVALID_ARG, CUDA; UNSUPPORTED as eagle_kv4_append, or where the launch would pass 2^31 blocks.
+ */
+EAGLE_API eagle_status eagle_kv4_append_rotary(const eagle_kv4_cache *cache, int32_t batch, int32_t src_rows,
+                                               int32_t slots, const void *d_k, const void *d_v, int64_t ld,
+                                               const int32_t *d_positions, float rope_theta, int32_t heads,
+                                               const void *d_q, int64_t ldq, void *d_q_out,
+                                               const int32_t *d_select, const int32_t *d_count,
+                                               const int32_t *d_start, int32_t *d_status, eagle_stream_t stream);
+
+/*
  * Reads the cache back: row j of request b is position start[b] + j (d_start NULL: 0), as the values
  * its codes stand for, rounded to `dtype` (EAGLE_F32 or EAGLE_BF16) from fp32.
  *   d_k, d_v   [batch][rows][kv_heads][head_dim], 16-byte aligned.  Rows at or behind the request's
@@ -649,6 +674,72 @@ EAGLE_API eagle_status eagle_decoder_layer_kv4(const eagle_decoder_layer_weights
                                                void *d_out, void *d_k_new, void *d_v_new, void *d_ws,
                                                size_t ws_bytes, int32_t *d_status,
                                                eagle_stream_t stream);
+
+/*
+ * 8-bit rows (no counterpart on the pages): a row y stands as codes c (EAGLE_E4M3) and one fp32 scale s,
+ *   s = max(max |y| / 448, 2^-100),   c = y / s rounded to the nearest e4m3 value, ties to even,
+ * and its values are s c.  A row that holds a NaN or an infinity has a scale of NaN and codes of NaN.
+ *
+ * eagle_quantize_rows: the rows of d_x [rows] (ldx elements apart) of cols bf16, as they are.
+ * eagle_rms_norm:      h = x + residual (x alone where d_residual is NULL), y = weight h / sqrt(mean(h^2) + eps);
+ *                      y in bf16 (d_scale NULL) or as 8-bit rows.  d_sum, where given, receives h in bf16.
+ * h, the sum of squares and y stay in fp32 until y and the sum are rounded once; the norm takes h before that.
+ *   d_x, d_residual, d_sum, d_y   [rows], ldx, ldr, lds, ldy elements apart (a multiple of 8; of 16 for 8-bit
+ *                      rows, which eagle_linear then takes), 16-byte aligned; what lies between the rows is
+ *                      neither read nor written.  d_sum may be d_x or d_residual, and a bf16 d_y too, with
+ *                      the same row stride.
+ *   d_weight [cols] bf16, 16-byte aligned;  d_scale [rows] fp32
+ * cols at most 32768 (UNSUPPORTED above), eps >= 0; rows == 0 does nothing.  Errors: INVALID_ARG, UNSUPPORTED,
+ * CUDA.
+ */
+EAGLE_API eagle_status eagle_quantize_rows(const void *d_x, int64_t ldx, int32_t rows, int32_t cols, void *d_y,
+                                           int64_t ldy, float *d_scale, eagle_stream_t stream);
+EAGLE_API eagle_status eagle_rms_norm(const void *d_x, int64_t ldx, const void *d_residual, int64_t ldr,
+                                      const void *d_weight, float eps, int32_t rows, int32_t cols, void *d_sum,
+                                      int64_t lds, eagle_dtype y_dtype, void *d_y, int64_t ldy, float *d_scale,
+                                      eagle_stream_t stream);
+
+/*
+ * The streamed-weight GEMM with an epilogue, from bf16 or 8-bit operands:
+ *   z[r][o] = w_scale[o] x_scale[r] sum_i w[o][i] x[r][i] + bias[o]     (bf16 operands: no scales)
+ *   y = act(z) + residual
+ * act: EAGLE_ACT_NONE; EAGLE_ACT_SILU z / (1 + e^-z); EAGLE_ACT_GELU z (1 + erf(z / sqrt 2)) / 2;
+ * EAGLE_ACT_SWIGLU: w holds out_features gate rows, then as many up rows (as w_gu of eagle_decoder_layer;
+ * w_scale and bias have an entry for each of the 2 out_features rows), y = silu(z_gate) z_up + residual.
+ *   dtype     EAGLE_BF16 or EAGLE_E4M3: of w and x
+ *   w, x      [out_features (SWIGLU: twice)][in_features] and [rows][in_features], ldw and ldx elements apart
+ *             (a multiple of 16 bytes), 16-byte aligned
+ *   w_scale, x_scale   fp32, one a row of w and of x (EAGLE_E4M3; else NULL)
+ *   bias      bf16, one a row of w, or NULL
+ *   residual  [rows][out_features] bf16, ldr elements apart, or NULL; may be y where that is bf16 of the same
+ *             row stride
+ *   y         [rows][out_features] of y_dtype (EAGLE_BF16 or EAGLE_F32), ldy elements apart; quickest where it
+ *             is 16-byte aligned with rows a multiple of 16 bytes apart
+ * Sums and the epilogue are fp32; y rounds once.  rows in [0, 32768] per call (0 does nothing).
+ * d_ws: eagle_linear_epilogue_workspace_bytes(rows) bytes (on the current device), 256-byte aligned, of which
+ * the first 4096 are zeroed once; every call leaves them zero, for later calls of any sizes that the workspace
+ * is large enough for.  Calls that may run at the same time need workspaces of their own.  d_status: an int32
+ * of the caller's that latches a wait that ran out (bit 0), or NULL; after one, y is undefined and the 4096
+ * bytes have to be zeroed again.
+ * Results are the same in every call with the same sizes.
+ * Errors: INVALID_ARG, CUDA; UNSUPPORTED where a row stride or size passes what a tensor map holds.
+ */
+typedef enum { EAGLE_ACT_NONE = 0, EAGLE_ACT_SILU = 1, EAGLE_ACT_GELU = 2, EAGLE_ACT_SWIGLU = 3 } eagle_activation;
+typedef struct {
+    int32_t rows, out_features, in_features;
+    eagle_dtype dtype, y_dtype;
+    eagle_activation act;
+    const void *w, *x;
+    int64_t ldw, ldx;
+    const float *w_scale, *x_scale;
+    const void *bias, *residual;
+    int64_t ldr;
+    void *y;
+    int64_t ldy;
+} eagle_linear_args;
+EAGLE_API size_t eagle_linear_epilogue_workspace_bytes(int32_t rows);
+EAGLE_API eagle_status eagle_linear(const eagle_linear_args *args, void *d_ws, size_t ws_bytes, int32_t *d_status,
+                                    eagle_stream_t stream);
 
 /*
  * The streamed-weight GEMM of eagle_linear_bf16 without caller-provided scratch.  The pages have
