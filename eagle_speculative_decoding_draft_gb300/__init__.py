@@ -16,5 +16,5 @@ def __getattr__(name):
         return kv4.KV4Cache
     if name in ("rms_norm", "quantize_rows", "linear", "linear_workspace"):
         from . import fp8
-        return getattr(fp8, name)
+        return globals().setdefault(name, getattr(fp8, name))
     raise AttributeError(name)

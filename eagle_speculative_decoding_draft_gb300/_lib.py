@@ -147,6 +147,8 @@ def load(path: Path | None = None):
     The environment variable EAGLE_TREE_LIB, when set, names another build of the same library
     to load instead (the tests use it for the checking build)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             override = os.environ.get("EAGLE_TREE_LIB")

@@ -67,11 +67,11 @@ EncodeTiledFn encoder() {
     return fn;
 }
 
-// A matrix of bf16 or 8-bit elements in swizzled boxes; elements outside it read as 0.
-bool encode_rows_2d(CUtensorMap *map, bool fp8, const void *ptr, uint64_t inner, uint64_t outer, uint64_t row_stride_elems,
+// A matrix in swizzled boxes, by 64 bytes where a box's rows have 64, else by 128; elements outside it read
+// as 0.
+bool encode_rows_2d(CUtensorMap *map, uint64_t es, const void *ptr, uint64_t inner, uint64_t outer, uint64_t row_stride_elems,
                     uint32_t box_inner, uint32_t box_outer) {
     EncodeTiledFn fn = encoder();
-    const uint64_t es = fp8 ? 1 : 2;
     if (!fn) return false;
     if (reinterpret_cast<uintptr_t>(ptr) % 16 != 0) return false;
     if ((row_stride_elems * es) % 16 != 0) return false;
@@ -79,14 +79,16 @@ bool encode_rows_2d(CUtensorMap *map, bool fp8, const void *ptr, uint64_t inner,
     cuuint64_t strides[1] = {row_stride_elems * es};
     cuuint32_t box[2] = {box_inner, box_outer};
     cuuint32_t estr[2] = {1, 1};
-    return fn(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(ptr),
-              dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+    return fn(map, es == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                           : (es == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32),
+              2, const_cast<void *>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              box_inner * es == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 bool encode_bf16_2d(CUtensorMap *map, const void *ptr, uint64_t inner, uint64_t outer,
                     uint64_t row_stride_elems, uint32_t box_inner, uint32_t box_outer) {
-    return encode_rows_2d(map, false, ptr, inner, outer, row_stride_elems, box_inner, box_outer);
+    return encode_rows_2d(map, 2, ptr, inner, outer, row_stride_elems, box_inner, box_outer);
 }
 
 // Gated weights, M gate rows and behind them M up rows, as [2][M][K]: a box is `box_rows` gates and their
@@ -135,6 +137,12 @@ bool encode_plan_out(LinearPlan *p, const void *out) {
 bool encode_bf16_rows_map(CUtensorMap *map, const void *ptr, uint64_t cols, uint64_t rows, uint64_t ld,
                           uint32_t box_cols, uint32_t box_rows) {
     return encode_bf16_2d(map, ptr, cols, rows, ld, box_cols, box_rows);
+}
+
+bool encode_swizzled_rows(CUtensorMap *map, int32_t es, const void *ptr, int64_t cols, int64_t rows, int64_t ld,
+                          int32_t box_cols, int32_t box_rows) {
+    return encode_rows_2d(map, static_cast<uint64_t>(es), ptr, static_cast<uint64_t>(cols), static_cast<uint64_t>(rows),
+                          static_cast<uint64_t>(ld), static_cast<uint32_t>(box_cols), static_cast<uint32_t>(box_rows));
 }
 
 bool encode_kv_cache_map(CUtensorMap *map, const void *cache, int32_t B, int32_t P, int32_t Hk, int32_t D) {
@@ -239,11 +247,11 @@ bool plan_linear(LinearPlan *p, bool fp8, const LinearEpilogue &ep, const void *
     p->status = status;
     if (gated ? !encode_gated(&p->tmap_w, fp8, w, static_cast<uint64_t>(K), static_cast<uint64_t>(M),
                               static_cast<uint64_t>(ldw), 16)
-              : !encode_rows_2d(&p->tmap_w, fp8, w, static_cast<uint64_t>(K), static_cast<uint64_t>(M),
+              : !encode_rows_2d(&p->tmap_w, fp8 ? 1 : 2, w, static_cast<uint64_t>(K), static_cast<uint64_t>(M),
                                 static_cast<uint64_t>(ldw), BK, BM))
         return false;
     p->y_tma = (want_y_tma && encode_plan_out(p, out)) ? 1 : 0;
-    if (!encode_rows_2d(&p->tmap_x, fp8, x, static_cast<uint64_t>(K), static_cast<uint64_t>(rows),
+    if (!encode_rows_2d(&p->tmap_x, fp8 ? 1 : 2, x, static_cast<uint64_t>(K), static_cast<uint64_t>(rows),
                         static_cast<uint64_t>(ldx), BK, static_cast<uint32_t>(p->n_tile >> p->pair)))
         return false;
     return true;

@@ -39,6 +39,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "epilogue.cuh"
 #include "kernels.cuh"
 
 namespace eagle {
@@ -155,15 +156,6 @@ __device__ __forceinline__ Column column_of(const LinearArgs &a, int32_t tile, i
     c.bias = (a.bias != nullptr && c.ok) ? __bfloat162float(a.bias[row]) : 0.0f;
     if constexpr (Op::kFp8) c.scale = c.ok ? a.ep.w_scale[row] : 0.0f;
     return c;
-}
-
-// z / (1 + e^-z) by the special-function unit: within 2^-20 of itself for |z| up to 10, far below a bf16
-// output's 2^-9 and an fp32 output's sum of products.  0 for z far below 0.
-__device__ __forceinline__ float silu(float z) { return __fdividef(z, 1.0f + __expf(-z)); }
-__device__ __forceinline__ float activation(int32_t act, float z) {
-    if (act == kActSilu) return silu(z);
-    if (act == kActGelu) return 0.5f * z * (1.0f + erff(z * 0.70710678f));
-    return z;
 }
 
 // The outputs of rows r0 .. r0 + N - 1 in this thread's column from the sums of products v, in place, all
@@ -479,7 +471,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tma_load_2d(dst, &tmap_x, &ctl->full[s], kx, y, pol_x);
             };
             // The weights do not depend on the previous kernel: fill the whole ring with weight
-            // tiles first, then wait for the previous kernel and add the activation slices.
+            // tiles first, then wait for the previous kernel and add the activation slices.  (Those of
+            // the forms with an epilogue may: a caller quantises weights and multiplies by them.)
+            if (!Op::kPlain) pdl_wait();
             const int64_t n_pre = min(static_cast<int64_t>(stages), kb_end - kb_begin);
             // units are weight-major: unit u covers weight unit u / nch and row chunk u % nch
             for (int64_t i = 0; i < n_pre; ++i) {

@@ -539,6 +539,26 @@ ReadKernel read_kernel(int32_t G) {
 
 bool misaligned(const void *p, uintptr_t by) { return (reinterpret_cast<uintptr_t>(p) & (by - 1)) != 0; }
 
+// The pairs' frequencies as RotaryArgs has them.  A thread keeps those of its last base and head size: 64
+// powers in 64 bits take longer than the launch.
+void frequencies(float theta, int32_t D, uint64_t (&turn)[64]) {
+    static thread_local struct {
+        float theta;
+        int32_t D;
+        uint64_t turn[64];
+    } last = {};
+    if (last.theta != theta || last.D != D) {
+        constexpr double kTwoPi = 6.283185307179586;
+        for (int32_t j = 0; j < D / 2; ++j) {
+            const double turns = std::pow(static_cast<double>(theta), -2.0 * j / D) / kTwoPi, part = turns - std::floor(turns);
+            last.turn[j] = static_cast<uint64_t>(std::ldexp(part, 64));  // exact: part <= 1 - 2^-53
+        }
+        last.theta = theta;
+        last.D = D;
+    }
+    std::copy(last.turn, last.turn + 64, turn);
+}
+
 // What the two writes have in common.
 eagle_status append_args(const eagle_kv4_cache *cache, int32_t batch, int32_t src_rows, int32_t slots, const void *d_k,
                          const void *d_v, int64_t ld, const int32_t *d_select, const int32_t *d_count,
@@ -638,11 +658,7 @@ eagle_status eagle_kv4_append_rotary(const eagle_kv4_cache *cache, int32_t batch
         blocks += (rows + r.q_rows - 1) / r.q_rows;
     }
     if (blocks > INT32_MAX) return EAGLE_ERR_UNSUPPORTED;
-    constexpr double kTwoPi = 6.283185307179586;
-    for (int32_t j = 0; j < D / 2; ++j) {
-        const double turns = std::pow(static_cast<double>(rope_theta), -2.0 * j / D) / kTwoPi, part = turns - std::floor(turns);
-        r.turn[j] = static_cast<uint64_t>(std::ldexp(part, 64));  // exact: part <= 1 - 2^-53
-    }
+    frequencies(rope_theta, D, r.turn);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (launch_pdl(rotary_kernel(r.a.v.G), dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, st, r) != cudaSuccess)
         return EAGLE_ERR_CUDA;

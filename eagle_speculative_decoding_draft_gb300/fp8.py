@@ -13,30 +13,31 @@ import torch
 
 from . import _lib
 from ._lib import EAGLE_BF16, EAGLE_E4M3, EAGLE_F32, check
-from .kv4 import _AS_IS
 
-_BF16, _E4M3, _F32 = torch.bfloat16, torch.float8_e4m3fn, torch.float32
+_BF16, _E4M3, _F32, _U8 = torch.bfloat16, torch.float8_e4m3fn, torch.float32, torch.uint8
 _ACTS = {None: 0, "none": 0, "silu": 1, "gelu": 2, "swiglu": 3}
+_CODES = {torch.bfloat16: EAGLE_BF16, torch.float8_e4m3fn: EAGLE_E4M3, torch.float32: EAGLE_F32}
 _TICKETS = 4096  # bytes at the start of a workspace that are zero between calls
+_FEW = 16        # rows that need no workspace
 
 
-def _rows(t, name, dtype, index, shape=None):
-    """Elements between the rows of a [rows][cols] matrix on the device, its last axis packed."""
+def _rows(t, name, dtype, index):
+    """(rows, cols, elements between rows) of a matrix on device `index` whose rows are packed."""
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.get_device() != index:
         raise ValueError(f"{name} is on {t.device}, not on cuda:{index}")
-    if t.dim() != 2 or (shape is not None and t.shape != shape):
-        raise ValueError(f"{name} must be a matrix" + ("" if shape is None else f" of shape {tuple(shape)}"))
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be a matrix")
     rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
+    ld, one = t.stride()
+    if one != 1 and cols > 1:
         raise ValueError(f"{name}: a row's elements must be packed")
-    if rows > 1:
-        if t.stride(0) < cols:
-            raise ValueError(f"{name}: rows must not overlap")
-        return t.stride(0)
-    size = 16 // t.element_size()
-    return (cols + size - 1) // size * size  # of one row: whatever the stride
+    if rows < 2:
+        return rows, cols, (cols + 15) // 16 * 16  # whatever the strides of sizes of 1
+    if ld < cols:
+        raise ValueError(f"{name}: rows must not overlap")
+    return rows, cols, ld
 
 
 def _vector(t, name, dtype, index, n):
@@ -44,49 +45,52 @@ def _vector(t, name, dtype, index, n):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.get_device() != index:
         raise ValueError(f"{name} is on {t.device}, not on cuda:{index}")
-    if t.shape != (n,) or not t.is_contiguous():
+    if t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous vector of {n}")
     return t.data_ptr()
 
 
-def _index(t, name):
-    if not t.is_cuda:
+def _device(t, name):
+    index = t.get_device()
+    if index < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
-    return t.get_device()
+    return index
 
 
-def _on(index, stream):
-    """Makes the operands' device current, and `stream` where one is given, so that what is allocated
-    belongs to the stream that uses it."""
+def _elsewhere(index, stream):
+    """None where the operands' device is current and no stream is given; else a context in which they are,
+    so that what is allocated belongs to the stream that uses it."""
     if stream is not None:
         if stream.device.index != index:
             raise ValueError(f"stream is on {stream.device}, the operands on cuda:{index}")
         return torch.cuda.stream(stream)
-    return _AS_IS if torch.cuda.current_device() == index else torch.cuda.device(index)
+    return None if torch._C._cuda_getDevice() == index else torch.cuda.device(index)
 
 
-def _raw(index, stream):
-    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _new_rows(like, rows, cols, dtype, step):
-    """A [rows][cols] matrix whose rows start a multiple of `step` elements apart."""
+    """A [rows][cols] matrix whose rows start a multiple of `step` elements apart, and that multiple."""
     ld = (cols + step - 1) // step * step
-    t = torch.empty((rows, ld), dtype=dtype, device=like.device)
-    return t if ld == cols else t[:, :cols]
+    if ld == cols:
+        return torch.empty((rows, cols), dtype=dtype, device=like.device), ld
+    return torch.empty_strided((rows, cols), (ld, 1), dtype=dtype, device=like.device), ld
 
 
 def quantize_rows(x, stream=None):
     """The rows of x [rows][cols] bf16 as 8-bit rows: (codes [rows][cols] float8_e4m3fn, scale [rows] fp32),
     codes times scale standing for x."""
-    lib, index = _lib.load(), _index(x, "x")
-    ldx = _rows(x, "x", _BF16, index)
-    rows, cols = x.shape
-    with _on(index, stream):
-        y = _new_rows(x, rows, cols, _E4M3, 16)
-        scale = torch.empty(rows, dtype=_F32, device=x.device)
-        check(lib.eagle_quantize_rows(x.data_ptr(), ldx, rows, cols, y.data_ptr(), _rows(y, "y", _E4M3, index),
-                                      scale.data_ptr(), _raw(index, stream)), "eagle_quantize_rows")
+    index = _device(x, "x")
+    rows, cols, ldx = _rows(x, "x", _BF16, index)
+    away = _elsewhere(index, stream)
+    if away is not None:
+        with away:
+            return quantize_rows(x)
+    y, ldy = _new_rows(x, rows, cols, _E4M3, 16)
+    scale = torch.empty(rows, dtype=_F32, device=x.device)
+    check(_lib.load().eagle_quantize_rows(x.data_ptr(), ldx, rows, cols, y.data_ptr(), ldy, scale.data_ptr(), _stream(index)),
+          "eagle_quantize_rows")
     return y, scale
 
 
@@ -95,40 +99,45 @@ def rms_norm(x, weight, eps: float = 1e-6, residual=None, dtype=torch.bfloat16, 
     [rows][cols] bf16, weight [cols] bf16.  Returns (y, scale, h): y in bf16 (scale None), or with
     dtype=torch.float8_e4m3fn as codes with a scale [rows] fp32; h in bf16 where there is a residual, else
     None."""
-    lib, index = _lib.load(), _index(x, "x")
-    ldx = _rows(x, "x", _BF16, index)
-    rows, cols = x.shape
+    index = _device(x, "x")
+    rows, cols, ldx = _rows(x, "x", _BF16, index)
     p_w = _vector(weight, "weight", _BF16, index, cols)
     if dtype is not _BF16 and dtype is not _E4M3:
         raise TypeError(f"rms_norm gives torch.bfloat16 or torch.float8_e4m3fn, not {dtype}")
-    fp8 = dtype is _E4M3
-    p_res, ldr, lds, p_sum, p_scale = None, 0, 0, None, None
+    p_res, ldr, lds, p_sum, p_scale, scale, total = None, 0, 0, None, None, None, None
     if residual is not None:
-        ldr, p_res = _rows(residual, "residual", _BF16, index, x.shape), residual.data_ptr()
-    with _on(index, stream):
-        y = _new_rows(x, rows, cols, dtype, 16 if fp8 else 8)
-        scale = total = None
-        if fp8:
-            scale = torch.empty(rows, dtype=_F32, device=x.device)
-            p_scale = scale.data_ptr()
-        if residual is not None:
-            total = _new_rows(x, rows, cols, _BF16, 8)
-            lds, p_sum = _rows(total, "h", _BF16, index), total.data_ptr()
-        check(lib.eagle_rms_norm(x.data_ptr(), ldx, p_res, ldr, p_w, eps, rows, cols, p_sum, lds,
-                                 EAGLE_E4M3 if fp8 else EAGLE_BF16, y.data_ptr(), _rows(y, "y", dtype, index), p_scale,
-                                 _raw(index, stream)), "eagle_rms_norm")
+        r_rows, r_cols, ldr = _rows(residual, "residual", _BF16, index)
+        if r_rows != rows or r_cols != cols:
+            raise ValueError(f"residual must be [{rows}][{cols}]")
+    away = _elsewhere(index, stream)
+    if away is not None:
+        with away:
+            return rms_norm(x, weight, eps, residual, dtype)
+    if residual is not None:
+        p_res = residual.data_ptr()
+        total, lds = _new_rows(x, rows, cols, _BF16, 8)
+        p_sum = total.data_ptr()
+    y, ldy = _new_rows(x, rows, cols, dtype, 16)
+    if dtype is _E4M3:
+        scale = torch.empty(rows, dtype=_F32, device=x.device)
+        p_scale = scale.data_ptr()
+    check(_lib.load().eagle_rms_norm(x.data_ptr(), ldx, p_res, ldr, p_w, eps, rows, cols, p_sum, lds, _CODES[dtype], y.data_ptr(),
+                                     ldy, p_scale, _stream(index)), "eagle_rms_norm")
     return y, scale, total
 
 
 def linear_workspace(w, rows: int, stream=None):
     """Scratch for ``linear`` calls of up to `rows` rows on w's device, one call at a time."""
-    lib, index = _lib.load(), _index(w, "w")
-    with _on(index, stream):
-        nbytes = lib.eagle_linear_epilogue_workspace_bytes(max(rows, 1))
-        if nbytes == 0:
-            raise ValueError(f"unusable number of rows ({rows})")
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=w.device)
-        ws[:_TICKETS].zero_()
+    index = _device(w, "w")
+    away = _elsewhere(index, stream)
+    if away is not None:
+        with away:
+            return linear_workspace(w, rows)
+    nbytes = _lib.load().eagle_linear_epilogue_workspace_bytes(max(rows, 1))
+    if nbytes == 0:
+        raise ValueError(f"unusable number of rows ({rows})")
+    ws = torch.empty(nbytes, dtype=_U8, device=w.device)
+    ws[:_TICKETS].zero_()
     return ws
 
 
@@ -139,44 +148,60 @@ def linear(w, x, bias=None, act=None, residual=None, w_scale=None, x_scale=None,
     "silu", "gelu" or "swiglu" (w: gate rows, then as many up rows; y = silu(gate) up); residual [rows][out]
     bf16.  Returns y [rows][out] of dtype (bf16 or fp32), or fills out, which may be the residual.  workspace:
     one of ``linear_workspace`` instead of a fresh one; calls that may overlap need one each."""
-    lib, index = _lib.load(), _index(w, "w")
+    index = _device(w, "w")
     kind = w.dtype
-    if kind is not _BF16 and kind is not _E4M3:
-        raise TypeError(f"w must be torch.bfloat16 or torch.float8_e4m3fn, got {kind}")
-    if act not in _ACTS:
-        raise ValueError(f"act must be one of None, 'silu', 'gelu', 'swiglu', got {act!r}")
-    code = _ACTS[act]
-    ldw, ldx = _rows(w, "w", kind, index), _rows(x, "x", kind, index)
-    features, k = w.shape
-    rows = x.shape[0]
-    if x.shape[1] != k:
-        raise ValueError(f"x has {x.shape[1]} columns, w {k}")
-    if code == 3 and features % 2:
-        raise ValueError("swiglu needs as many up rows of w as gate rows")
-    width = features // 2 if code == 3 else features
     fp8 = kind is _E4M3
-    if fp8 != (w_scale is not None) or fp8 != (x_scale is not None):
-        raise ValueError("8-bit operands have w_scale and x_scale, bf16 ones none")
-    p_ws, p_xs = (_vector(w_scale, "w_scale", _F32, index, features), _vector(x_scale, "x_scale", _F32, index, rows)) if fp8 \
-        else (None, None)
-    p_bias = None if bias is None else _vector(bias, "bias", _BF16, index, features)
-    p_res, ldr = None, 0
+    if not fp8 and kind is not _BF16:
+        raise TypeError(f"w must be torch.bfloat16 or torch.float8_e4m3fn, got {kind}")
+    code = _ACTS.get(act)
+    if code is None:
+        raise ValueError(f"act must be one of None, 'silu', 'gelu', 'swiglu', got {act!r}")
+    features, k, ldw = _rows(w, "w", kind, index)
+    rows, xk, ldx = _rows(x, "x", kind, index)
+    if xk != k:
+        raise ValueError(f"x has {xk} columns, w {k}")
+    width = features
+    if code == 3:
+        if features % 2:
+            raise ValueError("swiglu needs as many up rows of w as gate rows")
+        width = features // 2
+    p_ws = p_xs = p_bias = p_res = p_work = None
+    if fp8:
+        if w_scale is None or x_scale is None:
+            raise ValueError("8-bit operands have w_scale and x_scale")
+        p_ws, p_xs = _vector(w_scale, "w_scale", _F32, index, features), _vector(x_scale, "x_scale", _F32, index, rows)
+    elif w_scale is not None or x_scale is not None:
+        raise ValueError("bf16 operands have no scales")
+    if bias is not None:
+        p_bias = _vector(bias, "bias", _BF16, index, features)
+    ldr = nbytes = 0
     if residual is not None:
-        ldr, p_res = _rows(residual, "residual", _BF16, index, (rows, width)), residual.data_ptr()
+        r_rows, r_cols, ldr = _rows(residual, "residual", _BF16, index)
+        if r_rows != rows or r_cols != width:
+            raise ValueError(f"residual must be [{rows}][{width}]")
+        p_res = residual.data_ptr()
     if out is not None:
         dtype = out.dtype
     if dtype is not _BF16 and dtype is not _F32:
         raise TypeError(f"linear gives torch.bfloat16 or torch.float32, not {dtype}")
-    with _on(index, stream):
-        if out is None:
-            out = _new_rows(x, rows, width, dtype, 8 if dtype is _BF16 else 4)
-        ldy = _rows(out, "out", dtype, index, (rows, width))
-        if workspace is None:
-            workspace = linear_workspace(w, rows)
-        elif workspace.dtype is not torch.uint8 or workspace.get_device() != index or not workspace.is_contiguous():
+    if workspace is not None:
+        if workspace.dtype is not _U8 or workspace.get_device() != index or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous uint8 tensor on the operands' device")
-        args = _lib.LinearArgs(rows, width, k, EAGLE_E4M3 if fp8 else EAGLE_BF16, EAGLE_BF16 if dtype is _BF16 else EAGLE_F32,
-                               code, w.data_ptr(), x.data_ptr(), ldw, ldx, p_ws, p_xs, p_bias, p_res, ldr, out.data_ptr(), ldy)
-        check(lib.eagle_linear(ctypes.byref(args), workspace.data_ptr(), workspace.numel(), None, _raw(index, stream)),
-              "eagle_linear")
+        p_work, nbytes = workspace.data_ptr(), workspace.numel()
+    away = _elsewhere(index, stream)
+    if away is not None:
+        with away:
+            return linear(w, x, bias, act, residual, w_scale, x_scale, dtype, out, workspace)
+    if out is None:
+        out, ldy = _new_rows(x, rows, width, dtype, 8)
+    else:
+        o_rows, o_cols, ldy = _rows(out, "out", dtype, index)
+        if o_rows != rows or o_cols != width:
+            raise ValueError(f"out must be [{rows}][{width}]")
+    if workspace is None and rows > _FEW:
+        workspace = linear_workspace(w, rows)
+        p_work, nbytes = workspace.data_ptr(), workspace.numel()
+    args = _lib.LinearArgs(rows, width, k, _CODES[kind], _CODES[dtype], code, w.data_ptr(), x.data_ptr(), ldw, ldx, p_ws, p_xs,
+                           p_bias, p_res, ldr, out.data_ptr(), ldy)
+    check(_lib.load().eagle_linear(ctypes.byref(args), p_work, nbytes, None, _stream(index)), "eagle_linear")
     return out

@@ -58,6 +58,21 @@ def _row_step(t, name):
     return step
 
 
+def _packed(a, b, index):
+    """Elements between the rows of two bf16 tensors [B][n][heads][D] of one shape and layout on the device
+    (rows of a projection, or contiguous), or None."""
+    s = a.stride()
+    if len(s) != 4 or a.dtype is not _BF16 or a.get_device() != index:
+        return None
+    if b is not a and (b.shape != a.shape or b.stride() != s or b.dtype is not _BF16 or b.get_device() != index):
+        return None
+    B, n, heads, D = a.shape
+    step = s[1]
+    if s[3] != 1 or s[2] != D or s[0] != n * step or step < heads * D or step % 8:
+        return None
+    return step
+
+
 class KV4Cache:
     """A paged 4-bit cache of `batch` requests (see eagle_kv4_cache in include/eagle_tree.h).
 
@@ -159,7 +174,10 @@ class KV4Cache:
         start[b] + j; rows that `select` names need positions).  k and v come as a projection leaves
         them.  With the queries q [batch][rows][heads][head_dim] of the same rows they are turned too
         and returned (in out, if given, which may be a contiguous q itself)."""
-        ld = self._kv(k, v)
+        device, index = self.device, self._index
+        ld = _packed(k, v, index)
+        if ld is None or k.shape[0] != self.batch or k.shape[2:] != self._tail:
+            ld = self._kv(k, v)  # other layouts, or what is wrong with them
         slots = rows = k.shape[1]
         if select is not None:
             if select.dim() != 2:
@@ -167,27 +185,29 @@ class KV4Cache:
             if positions is None:
                 raise ValueError("rows that select names need positions")
             slots = select.shape[1]
-        device = self.device
-        p_positions = _ints(positions, "positions", device, (self.batch, rows))
-        p_select = _ints(select, "select", device, (self.batch, slots))
-        p_count = _ints(count, "count", device, (self.batch,))
-        p_start = _ints(start, "start", device, (self.batch,))
+        # addresses beside the tensors, which must live until the call is enqueued
+        p_positions = None if positions is None else _ints(positions, "positions", device, (self.batch, rows))
+        p_select = None if select is None else _ints(select, "select", device, (self.batch, slots))
+        p_count = None if count is None else _ints(count, "count", device, (self.batch,))
+        p_start = None if start is None else _ints(start, "start", device, (self.batch,))
         heads = ldq = 0
         p_q = p_out = None
         if q is not None:
-            if q.dtype is not _BF16 or q.get_device() != self._index:
+            ldq = _packed(q, q, index)
+            shape = q.shape
+            if ldq is None or shape[:2] != k.shape[:2] or shape[3] != self.head_dim or shape[2] < 1:
                 _here(q, "q", device, _BF16)
-            if q.dim() != 4 or q.shape[:2] != k.shape[:2] or q.shape[3] != self.head_dim or q.shape[2] < 1:
-                raise ValueError(f"q must be [{self.batch}][{rows}][heads][{self.head_dim}]")
-            heads, p_q = q.shape[2], q.data_ptr()
-            ldq = _row_step(q, "q") if rows else heads * self.head_dim
+                if q.dim() != 4 or q.shape[:2] != k.shape[:2] or q.shape[3] != self.head_dim or q.shape[2] < 1:
+                    raise ValueError(f"q must be [{self.batch}][{rows}][heads][{self.head_dim}]")
+                ldq = _row_step(q, "q") if rows else q.shape[2] * self.head_dim
+            heads, p_q = shape[2], q.data_ptr()
         elif out is not None:
             raise ValueError("out needs q")
         with self._on(stream):
             if q is not None:
                 if out is None:
-                    out = q.new_empty(q.shape)
-                elif not _here(out, "out", device, _BF16).is_contiguous() or out.shape != q.shape:
+                    out = q.new_empty(shape)
+                elif not _here(out, "out", device, _BF16).is_contiguous() or out.shape != shape:
                     raise ValueError("out must be contiguous and have the shape of q")
                 p_out = out.data_ptr()
             check(self._lib.eagle_kv4_append_rotary(

@@ -46,7 +46,7 @@ def test_rows_limits(lib):
 
 def linear(lib, ws=P(256), nbytes=1 << 40, status=None, **kw):
     from eagle_speculative_decoding_draft_gb300._lib import LinearArgs
-    f = dict(rows=4, out_features=64, in_features=128, dtype=2, y_dtype=1, act=0, w=256, x=256, ldw=128, ldx=128, w_scale=256,
+    f = dict(rows=20, out_features=64, in_features=128, dtype=2, y_dtype=1, act=0, w=256, x=256, ldw=128, ldx=128, w_scale=256,
              x_scale=256, bias=256, residual=256, ldr=64, y=256, ldy=64)
     f.update(kw)
     return lib.eagle_linear(ctypes.byref(LinearArgs(*(f[k] for k, _ in LinearArgs._fields_))), ws, nbytes, status, None)
@@ -57,7 +57,8 @@ def linear(lib, ws=P(256), nbytes=1 << 40, status=None, **kw):
                                  dict(w=264), dict(x=264), dict(w_scale=None), dict(x_scale=None), dict(w_scale=258), dict(x_scale=258),
                                  dict(bias=257), dict(residual=257), dict(y=257), dict(ws=P(128)), dict(status=P(258)), dict(ldw=112),
                                  dict(ldx=136), dict(ldw=136), dict(ldy=63), dict(ldr=63), dict(dtype=1), dict(y_dtype=0, y=258),
-                                 dict(dtype=1, w_scale=None, x_scale=None, ldw=132), dict(out_features=1 << 30, act=3, ldy=1 << 30, residual=None)],
+                                 dict(dtype=1, w_scale=None, x_scale=None, ldw=132), dict(out_features=(1 << 28) + 1, ldy=1 << 30, residual=None),
+                                 dict(in_features=(1 << 28) + 1, ldw=1 << 30, ldx=1 << 30)],
                          ids=str)
 def test_linear_refuses(lib, bad):
     assert linear(lib, **bad) == 1
