@@ -20,8 +20,8 @@ LIB = OUT_DIR / "libeagle_tree.so"
 # (-DEAGLE_CHECKS): a separate build, used by the tests
 CHECKS_DIR = OUT_DIR / "checks"
 CHECKS_LIB = CHECKS_DIR / "libeagle_tree.so"
-SOURCES = ["api.cu", "gemm.cu", "linear.cu", "linear_few.cu", "linear_tiles.cu", "norm.cu", "topk.cu", "tree.cu",
-           "sample.cu", "noalloc.cu", "decoder.cu", "kv4_cache.cu", "kv4_attn.cu", "kv4_attn_tc.cu"]
+SOURCES = ["api.cu", "gemm.cu", "linear.cu", "linear_few.cu", "linear_mid.cu", "linear_tiles.cu", "norm.cu",
+           "topk.cu", "tree.cu", "sample.cu", "noalloc.cu", "decoder.cu", "kv4_cache.cu", "kv4_attn.cu", "kv4_attn_tc.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -145,6 +145,11 @@ bool encode_swizzled_rows(CUtensorMap *map, int32_t es, const void *ptr, int64_t
                           static_cast<uint64_t>(ld), static_cast<uint32_t>(box_cols), static_cast<uint32_t>(box_rows));
 }
 
+bool encode_gated_rows(CUtensorMap *map, int32_t es, const void *ptr, int64_t cols, int64_t rows, int64_t ld, int32_t box_rows) {
+    return encode_gated(map, es == 1, ptr, static_cast<uint64_t>(cols), static_cast<uint64_t>(rows), static_cast<uint64_t>(ld),
+                        static_cast<uint32_t>(box_rows));
+}
+
 bool encode_kv_cache_map(CUtensorMap *map, const void *cache, int32_t B, int32_t P, int32_t Hk, int32_t D) {
     EncodeTiledFn fn = encoder();
     if (!fn || B < 1 || P < 1 || Hk < 1 || (D != 64 && D != 128)) return false;

@@ -124,6 +124,8 @@ bool encode_bf16_rows_map(CUtensorMap *map, const void *ptr, uint64_t cols, uint
 // The same for elements of `es` bytes (1: any 8-bit type, 2: bf16, 4: fp32).
 bool encode_swizzled_rows(CUtensorMap *map, int32_t es, const void *ptr, int64_t cols, int64_t rows, int64_t ld,
                           int32_t box_cols, int32_t box_rows);
+// Gated weights [2 rows][cols] (gates, then ups) in boxes of box_rows gates and their ups x 128 bytes.
+bool encode_gated_rows(CUtensorMap *map, int32_t es, const void *ptr, int64_t cols, int64_t rows, int64_t ld, int32_t box_rows);
 // CTA pairs of the .cta_group::2 mode that fit on the device at once (0: the mode is off).
 int32_t linear_pair_workers(int32_t num_sms);
 
@@ -159,6 +161,12 @@ cudaError_t launch_linear_few(bool fp8, const LinearEpilogue &ep, const void *w,
                               int32_t sms, cudaStream_t st);
 constexpr int kLinearFewRows = 16;
 constexpr int kLinearMidRows = 128;  // above: linear_tiles.cu, between: gemm.cuh's kernels
+// linear_mid.cu: the same product for 17 to 128 rows (more in chunks of 128), without a workspace.  False as
+// launch_linear_tiles.
+bool launch_linear_mid(bool fp8, const LinearEpilogue &ep, const void *w, int64_t ldw, int32_t M, int32_t K, const void *x,
+                       int64_t ldx, int32_t rows, const void *bias, void *out, int64_t ldo, bool out_bf16, int32_t *status,
+                       int32_t sms, cudaStream_t st, cudaError_t *err);
+cudaError_t prepare_linear_mid();
 // linear_tiles.cu: the same product for many rows, on at most `pairs` CTA pairs, without a workspace.  False:
 // not for these arguments (a row stride or an address that a tensor map does not take); else *err.
 bool launch_linear_tiles(bool fp8, const LinearEpilogue &ep, const void *w, int64_t ldw, int32_t M, int32_t K, const void *x,

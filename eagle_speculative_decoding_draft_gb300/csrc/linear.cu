@@ -48,6 +48,7 @@ cudaError_t prepare_linear_forms() {
     if (e == cudaSuccess) e = prepare_form<EpilogueOp<true, false>>();
     if (e == cudaSuccess) e = prepare_form<EpilogueOp<false, true>>();
     if (e == cudaSuccess) e = prepare_form<EpilogueOp<true, true>>();
+    if (e == cudaSuccess) e = prepare_linear_mid();
     if (e == cudaSuccess) e = prepare_linear_tiles();
     done[dev] = e == cudaSuccess;
     return e;
@@ -87,17 +88,18 @@ eagle_status eagle_linear(const eagle_linear_args *l, void *d_ws, size_t ws_byte
     const int32_t M = l->out_features, K = l->in_features, step = fp8 ? 16 : 8;
     if (M > (1 << 28) || K > (1 << 28)) return EAGLE_ERR_INVALID_ARG;
     auto off = [](const void *p, uintptr_t by) { return (reinterpret_cast<uintptr_t>(p) & (by - 1)) != 0; };
-    const bool few = l->rows <= kLinearFewRows;  // works without a workspace
-    if (!l->w || !l->x || !l->y || (!d_ws && !few)) return EAGLE_ERR_INVALID_ARG;
+    const bool few = l->rows <= kLinearFewRows;
+    if (!l->w || !l->x || !l->y) return EAGLE_ERR_INVALID_ARG;
     if (fp8 != (l->w_scale != nullptr) || fp8 != (l->x_scale != nullptr)) return EAGLE_ERR_INVALID_ARG;
     if (off(l->w, 16) || off(l->x, 16) || off(l->w_scale, 4) || off(l->x_scale, 4) || off(l->bias, 2) || off(l->residual, 2))
         return EAGLE_ERR_INVALID_ARG;
     if (off(l->y, l->y_dtype == EAGLE_F32 ? 4 : 2) || off(d_ws, 256) || off(d_status, 4)) return EAGLE_ERR_INVALID_ARG;
     if (l->ldw < K || l->ldx < K || l->ldw % step || l->ldx % step || l->ldy < M || (l->residual && l->ldr < M))
         return EAGLE_ERR_INVALID_ARG;
+    if (d_ws && ws_bytes < kLinearTicketBytes) return EAGLE_ERR_INVALID_ARG;
     const int32_t sms = linear_sms();
     if (sms < 1) return EAGLE_ERR_CUDA;
-    if (!few && ws_bytes < linear_workspace(l->rows, sms)) return EAGLE_ERR_INVALID_ARG;
+    if (d_ws && ws_bytes < linear_workspace(l->rows, sms)) return EAGLE_ERR_INVALID_ARG;
     if (!few && prepare_linear_forms() != cudaSuccess) return EAGLE_ERR_CUDA;
     const LinearEpilogue ep{l->x_scale, l->w_scale, static_cast<const __nv_bfloat16 *>(l->residual), l->ldr,
                             static_cast<int32_t>(l->act)};
@@ -108,14 +110,21 @@ eagle_status eagle_linear(const eagle_linear_args *l, void *d_ws, size_t ws_byte
         err = launch_linear_few(fp8, ep, l->w, l->ldw, M, K, l->x, l->ldx, l->rows, l->bias, l->y, l->ldy, y_bf16, sms, st);
         return err == cudaSuccess ? EAGLE_OK : EAGLE_ERR_CUDA;
     }
-    // Over 128 rows the tensor cores bound the product, or nearly so: whole tiles of both operands (512 rows,
-    // 4096 x 4096 in 8 bits: 14 us, and 30 with the weights streamed past the rows; 128 rows: 12.6 and 15.9,
-    // but 14336 -> 4096 24 and 21)
-    const int32_t pairs = linear_pair_workers(sms);
-    if (pairs > 0 && l->rows > kLinearMidRows &&
-        launch_linear_tiles(fp8, ep, l->w, l->ldw, M, K, l->x, l->ldx, l->rows, l->bias, l->y, l->ldy, y_bf16, d_status, pairs,
-                            st, &err))
+    // Over 128 rows the tensor cores bound the product, or nearly so: whole tiles of both operands (256 rows,
+    // 4096 -> 2 x 11008 in 8 bits: 30 us, and 43 with the weights past 128 rows at a time; 128 rows: 29 and 25).
+    // Outputs that no bulk store takes go through the weights' stream where there is a workspace for it.
+    if (l->rows > kLinearMidRows) {
+        const int32_t pairs = linear_pair_workers(sms);
+        if (pairs > 0 && launch_linear_tiles(fp8, ep, l->w, l->ldw, M, K, l->x, l->ldx, l->rows, l->bias, l->y, l->ldy, y_bf16,
+                                             d_status, pairs, st, &err))
+            return err == cudaSuccess ? EAGLE_OK : EAGLE_ERR_CUDA;
+    }
+    if (l->rows <= kLinearMidRows || !d_ws) {
+        if (!launch_linear_mid(fp8, ep, l->w, l->ldw, M, K, l->x, l->ldx, l->rows, l->bias, l->y, l->ldy, y_bf16, d_status, sms,
+                               st, &err))
+            return EAGLE_ERR_UNSUPPORTED;
         return err == cudaSuccess ? EAGLE_OK : EAGLE_ERR_CUDA;
+    }
     LinearPlan p;
     if (!plan_linear(&p, fp8, ep, l->w, l->ldw, M, K, l->x, l->ldx, l->rows, l->bias, l->y, l->ldy,
                      l->y_dtype == EAGLE_BF16, reinterpret_cast<float *>(static_cast<uint8_t *>(d_ws) + kLinearTicketBytes),

@@ -18,7 +18,6 @@ _BF16, _E4M3, _F32, _U8 = torch.bfloat16, torch.float8_e4m3fn, torch.float32, to
 _ACTS = {None: 0, "none": 0, "silu": 1, "gelu": 2, "swiglu": 3}
 _CODES = {torch.bfloat16: EAGLE_BF16, torch.float8_e4m3fn: EAGLE_E4M3, torch.float32: EAGLE_F32}
 _TICKETS = 4096  # bytes at the start of a workspace that are zero between calls
-_FEW = 16        # rows that need no workspace
 
 
 def _rows(t, name, dtype, index):
@@ -127,7 +126,8 @@ def rms_norm(x, weight, eps: float = 1e-6, residual=None, dtype=torch.bfloat16, 
 
 
 def linear_workspace(w, rows: int, stream=None):
-    """Scratch for ``linear`` calls of up to `rows` rows on w's device, one call at a time."""
+    """Scratch for ``linear`` calls of up to `rows` rows on w's device, one call at a time: what makes those
+    of more than 128 rows quicker whose ``out`` has rows that are not multiples of 16 bytes."""
     index = _device(w, "w")
     away = _elsewhere(index, stream)
     if away is not None:
@@ -147,7 +147,7 @@ def linear(w, x, bias=None, act=None, residual=None, w_scale=None, x_scale=None,
     8-bit rows (float8_e4m3fn) with w_scale [features] and x_scale [rows] fp32; bias [features] bf16; act None,
     "silu", "gelu" or "swiglu" (w: gate rows, then as many up rows; y = silu(gate) up); residual [rows][out]
     bf16.  Returns y [rows][out] of dtype (bf16 or fp32), or fills out, which may be the residual.  workspace:
-    one of ``linear_workspace`` instead of a fresh one; calls that may overlap need one each."""
+    one of ``linear_workspace``, or None; calls that may overlap need one each."""
     index = _device(w, "w")
     kind = w.dtype
     fp8 = kind is _E4M3
@@ -198,9 +198,6 @@ def linear(w, x, bias=None, act=None, residual=None, w_scale=None, x_scale=None,
         o_rows, o_cols, ldy = _rows(out, "out", dtype, index)
         if o_rows != rows or o_cols != width:
             raise ValueError(f"out must be [{rows}][{width}]")
-    if workspace is None and rows > _FEW:
-        workspace = linear_workspace(w, rows)
-        p_work, nbytes = workspace.data_ptr(), workspace.numel()
     args = _lib.LinearArgs(rows, width, k, _CODES[kind], _CODES[dtype], code, w.data_ptr(), x.data_ptr(), ldw, ldx, p_ws, p_xs,
                            p_bias, p_res, ldr, out.data_ptr(), ldy)
     check(_lib.load().eagle_linear(ctypes.byref(args), p_work, nbytes, None, _stream(index)), "eagle_linear")

@@ -713,17 +713,16 @@ EAGLE_API eagle_status eagle_rms_norm(const void *d_x, int64_t ldx, const void *
  *   bias      bf16, one a row of w, or NULL
  *   residual  [rows][out_features] bf16, ldr elements apart, or NULL; may be y where that is bf16 of the same
  *             row stride
- *   y         [rows][out_features] of y_dtype (EAGLE_BF16 or EAGLE_F32), ldy elements apart; quickest where it
- *             is 16-byte aligned with rows a multiple of 16 bytes apart
+ *   y         [rows][out_features] of y_dtype (EAGLE_BF16 or EAGLE_F32), ldy elements apart
  * Sums and the epilogue are fp32; y rounds once.  rows in [0, 32768] per call (0 does nothing); out_features
  * and in_features at most 2^28.
- * d_ws: NULL for up to 16 rows; else eagle_linear_epilogue_workspace_bytes(rows) bytes (on the current
- * device), 256-byte aligned, of which
- * the first 4096 are zeroed once; every call leaves them zero, for later calls of any sizes that the workspace
- * is large enough for.  Calls that may run at the same time need workspaces of their own.  d_status: an int32
- * of the caller's that latches a wait that ran out (bit 0), or NULL; after one, y is undefined and the 4096
- * bytes have to be zeroed again.
- * Results are the same in every call with the same sizes and alignments.
+ * d_ws: NULL, or eagle_linear_epilogue_workspace_bytes(rows) bytes (on the current device), 256-byte aligned,
+ * with which products of more than 128 rows whose y (or bf16 y's residual) is not 16-byte aligned, or has rows
+ * no multiple of 16 bytes apart, are quicker; others do not use it.  Its first 4096 bytes are zeroed once; every
+ * call leaves them zero, for later calls of any sizes that the workspace is large enough for.  Calls that may
+ * run at the same time need workspaces of their own.  d_status: an int32 of the caller's that latches a wait
+ * that ran out (bit 0), or NULL; after one, y is undefined and the 4096 bytes have to be zeroed again.
+ * Results are the same in every call with the same sizes, alignments and presence of d_ws.
  * Errors: INVALID_ARG, CUDA; UNSUPPORTED where a row stride or size passes what a tensor map holds.
  */
 typedef enum { EAGLE_ACT_NONE = 0, EAGLE_ACT_SILU = 1, EAGLE_ACT_GELU = 2, EAGLE_ACT_SWIGLU = 3 } eagle_activation;

@@ -53,7 +53,7 @@ def linear(lib, ws=P(256), nbytes=1 << 40, status=None, **kw):
 
 
 @pytest.mark.parametrize("bad", [dict(rows=-1), dict(rows=32769), dict(out_features=0), dict(in_features=0), dict(dtype=0), dict(dtype=3),
-                                 dict(y_dtype=2), dict(act=-1), dict(act=4), dict(w=None), dict(x=None), dict(y=None), dict(ws=None),
+                                 dict(y_dtype=2), dict(act=-1), dict(act=4), dict(w=None), dict(x=None), dict(y=None), dict(nbytes=4095),
                                  dict(w=264), dict(x=264), dict(w_scale=None), dict(x_scale=None), dict(w_scale=258), dict(x_scale=258),
                                  dict(bias=257), dict(residual=257), dict(y=257), dict(ws=P(128)), dict(status=P(258)), dict(ldw=112),
                                  dict(ldx=136), dict(ldw=136), dict(ldy=63), dict(ldr=63), dict(dtype=1), dict(y_dtype=0, y=258),

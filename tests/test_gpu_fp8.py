@@ -139,17 +139,17 @@ def operands(g, rows, M, K, kind, act, bias, residual, gb, pad=0):
         (x, x_scale), (w, w_scale) = gb.quantize_rows(x), gb.quantize_rows(w)
         if K % step:  # what lies between the rows has no influence
             for t in (x, w):
-                torch.as_strided(t.view(torch.uint8), (t.shape[0], t.stride(0) - K), (t.stride(0), 1), K).fill_(0x7f)
+                torch.as_strided(t.view(torch.uint8), (t.shape[0] - 1, t.stride(0) - K), (t.stride(0), 1), K).fill_(0x7f)
     b = (0.5 * torch.randn(both, generator=g, device="cuda")).to(BF16) if bias else None
     r = wide(g, rows, M, up(M, 8)) if residual else None
     return w, x, b, r, w_scale, x_scale
 
 
 SHAPES = [
-    # rows, M, K: 1-16 rows (tickets), whole tiles, tiles cut between workers, pairs, the second launch, chunks
+    # rows, M, K: up to 16 rows, up to 128 with K in 1 to 8 parts, above with 1, 2 and 4 pairs a tile; odd everything
     (1, 4096, 4096), (1, 128, 64), (2, 1, 8), (7, 777, 1001), (15, 130, 72), (16, 2048, 8192), (16, 40000, 128),
     (17, 128, 4096), (31, 256, 8192), (33, 777, 1000), (61, 1000, 4096), (64, 8192, 512), (77, 777, 1001), (100, 64, 16),
-    (255, 512, 520), (256, 4096, 1024), (257, 384, 2048), (300, 100, 333), (1500, 4096, 256), (600, 2500, 640), (2080, 1024, 4096),
+    (255, 512, 520), (256, 4096, 1024), (257, 384, 2048), (300, 100, 333), (129, 700, 4097), (150, 300, 8192), (1500, 4096, 256), (600, 2500, 640), (2080, 1024, 4096),
 ]
 ACTS = [(None, False, False), ("silu", True, True), ("gelu", True, False), ("swiglu", False, True), (None, True, True), ("swiglu", True, False)]
 
@@ -158,18 +158,15 @@ ACTS = [(None, False, False), ("silu", True, True), ("gelu", True, False), ("swi
 @pytest.mark.parametrize("kind", [BF16, E4M3], ids=["bf16", "e4m3"])
 def test_linear(gb, rows, M, K, kind):
     g = gen(rows * 7 + M + K)
-    ws = gb.linear_workspace(torch.empty(1, 1, device="cuda"), rows)  # of any content but for its first bytes
-    ws[4096:] = 0xff
     for i, (act, bias, residual) in enumerate(ACTS):
         w, x, b, r, w_scale, x_scale = operands(g, rows, M, K, kind, act, bias, residual, gb, pad=i % 2)
         for dtype in (BF16, F32):
             y, tol = ref.linear(w, x, b, act, r, w_scale, x_scale, dtype)
-            got = gb.linear(w, x, bias=b, act=act, residual=r, w_scale=w_scale, x_scale=x_scale, dtype=dtype, workspace=ws)
+            got = gb.linear(w, x, bias=b, act=act, residual=r, w_scale=w_scale, x_scale=x_scale, dtype=dtype)
             assert got.shape == (rows, M) and got.dtype is dtype
             off = (got.double() - y).abs() - tol
             assert (off <= 0).all(), (act, dtype, float(off.max()), int((off > 0).sum()))
-            assert not ws[:4096].any()
-            again = gb.linear(w, x, bias=b, act=act, residual=r, w_scale=w_scale, x_scale=x_scale, dtype=dtype, workspace=ws)
+            again = gb.linear(w, x, bias=b, act=act, residual=r, w_scale=w_scale, x_scale=x_scale, dtype=dtype)
             assert torch.equal(again, got)
 
 
@@ -181,12 +178,13 @@ def test_linear_outputs_of_any_alignment_and_in_place_of_the_residual(gb, rows, 
     M, K, g = 200, 1100, gen(rows)
     w, x, b, r, w_scale, x_scale = operands(g, rows, M, K, kind, act, True, True, gb)
     want = gb.linear(w, x, bias=b, act=act, residual=r, w_scale=w_scale, x_scale=x_scale)
+    ws = gb.linear_workspace(w, rows)
     for dtype in (BF16, F32):
         y, tol = ref.linear(w, x, b, act, r, w_scale, x_scale, dtype)
-        for ld, at in ((M, 0), (M + 1, 1), (M + 8, 8), (208, 3)):
+        for ld, at in ((M, 0), (M + 1, 1), (M + 8, 8), (208, 3), (209, 8)):
             room = torch.full((at + rows * ld + 5,), -7.0, device="cuda").to(dtype)
             out = torch.as_strided(room, (rows, M), (ld, 1), at)
-            gb.linear(w, x, bias=b, act=act, residual=r, w_scale=w_scale, x_scale=x_scale, out=out)
+            gb.linear(w, x, bias=b, act=act, residual=r, w_scale=w_scale, x_scale=x_scale, out=out, workspace=ws if ld % 2 else None)
             assert ((out.double() - y).abs() <= tol).all()
             out.fill_(-7.0)
             assert (room == -7.0).all()
@@ -231,12 +229,24 @@ def test_activations_far_from_zero(gb):
     assert ((got - want).abs()[fine] <= 2.0 ** -18 * want.abs()[fine] + 1e-35).all()
 
 
-def test_linear_workspace_serves_calls_of_changing_sizes(gb):
-    ws = gb.linear_workspace(torch.empty(1, 1, device="cuda"), 600)
-    for rows, M, K in [(600, 4096, 256), (3, 4096, 4096), (70, 256, 8192), (16, 40000, 128), (600, 2500, 640), (1, 129, 5000)] * 2:
-        w, x, b, r, w_scale, x_scale = operands(gen(rows + M), rows, M, K, E4M3, "silu", True, True, gb)
-        got = gb.linear(w, x, bias=b, act="silu", residual=r, w_scale=w_scale, x_scale=x_scale, workspace=ws)
-        assert torch.equal(got, gb.linear(w, x, bias=b, act="silu", residual=r, w_scale=w_scale, x_scale=x_scale))
+@pytest.mark.parametrize("kind", [BF16, E4M3], ids=["bf16", "e4m3"])
+def test_linear_workspace_serves_calls_of_changing_sizes(gb, kind):
+    """Outputs that no bulk store takes, over 128 rows: whole tiles and tiles cut between workers, pairs, the
+    second launch; the workspace of any content but for its first bytes."""
+    ws = gb.linear_workspace(torch.empty(1, 1, device="cuda"), 1500)
+    ws[4096:] = 0xff
+    for i, (rows, M, K) in enumerate([(600, 4095, 256), (1500, 4096, 256), (200, 257, 8192), (257, 777, 1001), (600, 2501, 640), (129, 129, 5000)] * 2):
+        act, bias, residual = ACTS[i % len(ACTS)]
+        w, x, b, r, w_scale, x_scale = operands(gen(rows + M), rows, M, K, kind, act, bias, residual, gb)
+        dtype = (BF16, F32)[i % 2]
+        out = torch.empty(rows, M | 1, device="cuda", dtype=dtype)[:, :M]
+        y, tol = ref.linear(w, x, b, act, r, w_scale, x_scale, dtype)
+        gb.linear(w, x, bias=b, act=act, residual=r, w_scale=w_scale, x_scale=x_scale, workspace=ws, out=out)
+        assert ((out.double() - y).abs() <= tol).all(), (rows, M, K)
+        assert not ws[:4096].any()
+        first = out.clone()
+        gb.linear(w, x, bias=b, act=act, residual=r, w_scale=w_scale, x_scale=x_scale, workspace=ws, out=out)
+        assert torch.equal(first, out)
 
 
 def test_calls_are_captured_and_replayed(gb):
