@@ -160,11 +160,13 @@ template <int G>
 __device__ __forceinline__ void turn_row(const RotaryArgs &ra, uint8_t *table, int32_t row, int32_t pos) {
     for (int32_t j = threadIdx.x & 31; j < 16 * G; j += 32) {
         const uint64_t at = ra.turn[j] * static_cast<uint64_t>(static_cast<int64_t>(pos));
-        // within half a turn of 0; to 2^-25 of itself in fp32
-        const float half_turns = static_cast<float>(static_cast<int32_t>(at >> 32)) * 4.656612873e-10f;  // 2^-31
+        // half turns within 1 of 0 in 32 bits; what fp32 leaves of them, as an angle, turns its sine and cosine
+        const int32_t half_turns = static_cast<int32_t>(at >> 32);
+        const float near = static_cast<float>(half_turns);
+        const float rest = static_cast<float>(static_cast<int64_t>(half_turns) - static_cast<int64_t>(near)) * 1.4629181e-9f;  // pi / 2^31
         float s, c;
-        sincospif(half_turns, &s, &c);
-        *turn_entry(table, G, row, j) = make_float2(c, s);
+        sincospif(near * 4.656612873e-10f, &s, &c);  // 2^-31
+        *turn_entry(table, G, row, j) = make_float2(fmaf(-rest, s, c), fmaf(rest, c, s));
     }
 }
 // Turns two neighbouring values (a bf16 word) of one half of a head by the pairs' cosines and sines, and
@@ -176,20 +178,34 @@ __device__ __forceinline__ uint32_t turn_word(uint32_t own, uint32_t other, floa
     const __nv_bfloat162 r = __floats2bfloat162_rn(fmaf(x, cs.x, sign * (p * cs.y)), fmaf(y, cs.z, sign * (q * cs.w)));
     return *reinterpret_cast<const uint32_t *>(&r);
 }
-// A key's group g in place; `head` is the key as it came.  Blocks of 16 dims: block i and block i + G (i < G)
-// are each other's halves.
+// A key's group g in place, w; `head` is the key as it came.  Blocks of 16 dims: block i and block i + G (i < G)
+// are each other's halves.  Where a row's groups lie in neighbouring lanes of one pass, the other half comes
+// from there (G 1, 2, 4: from the lane itself, or G / 2 lanes apart), else from memory.  Whole warp.
 template <int G>
-__device__ __forceinline__ void turn_group(uint8_t *table, int32_t row, int32_t g, const uint4 *head, uint32_t (&w)[16]) {
+__device__ __forceinline__ void turn_group(uint8_t *table, int32_t row, int32_t g, bool key, const uint4 *head, uint32_t (&w)[16]) {
+    uint32_t o[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+        if constexpr (G == 1)
+            o[k] = w[k ^ 8];
+        else if constexpr (G != 3)
+            o[k] = __shfl_xor_sync(kFull, w[k], G / 2);
+    }
+    if (!key) return;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const int32_t i = 2 * g + h;
         const bool first = i < G;
-        const uint4 *other = head + 2 * (first ? i + G : i - G);
-        const uint4 o0 = __ldg(other), o1 = __ldg(other + 1);
-        const uint32_t o[8] = {o0.x, o0.y, o0.z, o0.w, o1.x, o1.y, o1.z, o1.w};
+        if constexpr (G == 3) {
+            const uint4 *other = head + 2 * (first ? i + G : i - G);
+            const uint4 o0 = __ldg(other), o1 = __ldg(other + 1);
+            const uint32_t p[8] = {o0.x, o0.y, o0.z, o0.w, o1.x, o1.y, o1.z, o1.w};
+#pragma unroll
+            for (int k = 0; k < 8; ++k) o[8 * h + k] = p[k];
+        }
         const float4 *cs = reinterpret_cast<const float4 *>(turn_entry(table, G, row, 16 * (first ? i : i - G)));
 #pragma unroll
-        for (int k = 0; k < 8; ++k) w[8 * h + k] = turn_word(w[8 * h + k], o[k], first ? -1.0f : 1.0f, cs[k]);
+        for (int k = 0; k < 8; ++k) w[8 * h + k] = turn_word(w[8 * h + k], o[8 * h + k], first ? -1.0f : 1.0f, cs[k]);
     }
 }
 // ra.q_rows rows of queries (16 at most): a thread turns 8 pairs of a head at a time.
@@ -206,22 +222,40 @@ __device__ __forceinline__ void turn_queries(const RotaryArgs &ra, uint8_t *tabl
     __syncthreads();
     constexpr int kEights = 2 * G;  // of a half head
     const int32_t per_row = ra.H * kEights;
-    for (int32_t u = threadIdx.x; u < rows * per_row; u += kThreads) {
-        const int32_t t = u / per_row, in = u - t * per_row, head = in / kEights, e = in - head * kEights;
+    // whole rows at once where they are short; a thread keeps its place in the row
+    const int32_t at_once = max(1, kThreads / per_row), mine = per_row < kThreads ? static_cast<int32_t>(threadIdx.x) / per_row : 0;
+    if (mine >= at_once) return;
+    for (int32_t in = static_cast<int32_t>(threadIdx.x) - mine * per_row; in < per_row; in += kThreads) {
+        const int32_t head = in / kEights, e = in - head * kEights;
         const int64_t at = static_cast<int64_t>(head) * 32 * G + 8 * e;
-        const uint4 *src = reinterpret_cast<const uint4 *>(ra.q + (row0 + t) * ra.ldq + at);
-        uint4 *dst = reinterpret_cast<uint4 *>(ra.q_out + (row0 + t) * ra.H * 32 * G + at);
-        const uint4 x = src[0], y = src[2 * G];
-        const float4 *cs = reinterpret_cast<const float4 *>(turn_entry(table, G, t, 8 * e));
-        const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
-        uint32_t p[4], q[4];
+        constexpr int kAhead = 4;  // rows in flight (the outputs may take the queries' place: loads before stores)
+        for (int32_t t0 = mine; t0 < rows; t0 += kAhead * at_once) {
+            uint4 x[kAhead], y[kAhead];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            p[k] = turn_word(xw[k], yw[k], -1.0f, cs[k]);
-            q[k] = turn_word(yw[k], xw[k], 1.0f, cs[k]);
+            for (int i = 0; i < kAhead; ++i) {
+                const int32_t t = t0 + i * at_once;
+                if (t >= rows) break;
+                const uint4 *src = reinterpret_cast<const uint4 *>(ra.q + (row0 + t) * ra.ldq + at);
+                x[i] = src[0];
+                y[i] = src[2 * G];
+            }
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                const int32_t t = t0 + i * at_once;
+                if (t >= rows) break;
+                uint4 *dst = reinterpret_cast<uint4 *>(ra.q_out + (row0 + t) * ra.H * 32 * G + at);
+                const float4 *cs = reinterpret_cast<const float4 *>(turn_entry(table, G, t, 8 * e));
+                const uint32_t xw[4] = {x[i].x, x[i].y, x[i].z, x[i].w}, yw[4] = {y[i].x, y[i].y, y[i].z, y[i].w};
+                uint32_t p[4], q[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    p[k] = turn_word(xw[k], yw[k], -1.0f, cs[k]);
+                    q[k] = turn_word(yw[k], xw[k], 1.0f, cs[k]);
+                }
+                dst[0] = make_uint4(p[0], p[1], p[2], p[3]);
+                dst[2 * G] = make_uint4(q[0], q[1], q[2], q[3]);
+            }
         }
-        dst[0] = make_uint4(p[0], p[1], p[2], p[3]);
-        dst[2 * G] = make_uint4(q[0], q[1], q[2], q[3]);
     }
 }
 
@@ -263,20 +297,7 @@ __device__ __forceinline__ void append_chunk(const AppendArgs &a, uint8_t *st, u
     if (rows == 0) return;
     const int32_t live = __popc(rows), items = 2 * live * G;
     if (src >= 0) order[__popc(rows & ((1u << lane) - 1u))] = static_cast<uint8_t>(lane);
-    if constexpr (kRotary) {
-        // the block's warps share the chunk: each does two of its rows
-        int32_t pos = 0;
-        if (src >= 0)
-            pos = ra->positions ? ra->positions[static_cast<int64_t>(b) * a.src_rows + src] : static_cast<int32_t>(chunk0 + lane);
-        for (int32_t t = threadIdx.x >> 5; t < 16; t += kWarps) {
-            const int32_t p = __shfl_sync(kFull, pos, t);
-            if ((rows >> t) & 1u) turn_row<G>(*ra, table, t, p);
-        }
-        __syncthreads();  // every warp of the block is here: what ended above it is the same for all
-        if (hk >= a.u.Hk) return;
-    } else {
-        __syncwarp();
-    }
+    __syncwarp();
     // group `it` of the pass: row, tensor and place in the row
     auto load = [&](int32_t it, uint32_t (&w)[16]) {
         const int32_t n = it / G, g = it - n * G;
@@ -296,7 +317,19 @@ __device__ __forceinline__ void append_chunk(const AppendArgs &a, uint8_t *st, u
         }
     };
     uint32_t now[16], ahead[16];
-    load(lane, now);
+    if (!kRotary || hk < a.u.Hk) load(lane, now);
+    if constexpr (kRotary) {
+        // the block's warps share the chunk: each does two of its rows
+        int32_t pos = 0;
+        if (src >= 0)
+            pos = ra->positions ? ra->positions[static_cast<int64_t>(b) * a.src_rows + src] : static_cast<int32_t>(chunk0 + lane);
+        for (int32_t t = threadIdx.x >> 5; t < 16; t += kWarps) {
+            const int32_t p = __shfl_sync(kFull, pos, t);
+            if ((rows >> t) & 1u) turn_row<G>(*ra, table, t, p);
+        }
+        __syncthreads();  // every warp of the block is here: what ended above it is the same for all
+        if (hk >= a.u.Hk) return;
+    }
     uint8_t *chunk = kv4_chunk(a.v, b, hk, chunk0);
     if (!chunk) {
         if (lane == 0) latch(a.status, kDevBounds);
@@ -310,9 +343,8 @@ __device__ __forceinline__ void append_chunk(const AppendArgs &a, uint8_t *st, u
         if constexpr (kRotary) {
             const int32_t n = it / G, g = it - n * G;
             const int32_t t = order[min(n, 15)], from = __shfl_sync(kFull, src, t & 15);
-            if (n < live)
-                turn_group<G>(table, t, g, reinterpret_cast<const uint4 *>(a.k + (static_cast<int64_t>(b) * a.src_rows + from) * a.ld +
-                                                                           static_cast<int64_t>(hk) * G * kKv4Group), now);
+            turn_group<G>(table, t, g, n < live, reinterpret_cast<const uint4 *>(a.k + (static_cast<int64_t>(b) * a.src_rows + from) * a.ld +
+                                                                                 static_cast<int64_t>(hk) * G * kKv4Group), now);
         }
         const uint32_t params = quantise(now, codes);
         if (it < items) {
@@ -365,9 +397,11 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const AppendArgs a
 }
 
 // Blocks of one chunk and up to 8 of its kv heads, a warp a head: the chunk's cosines and sines are worked
-// out once a block.  Further blocks turn the queries.
+// out once a block, with the first rows on their way.  Further blocks turn the queries.  Three blocks an SM (80
+// registers): 33 k tokens of 8 kv heads and 32 heads of 128 (0.70 GB) in 132 us, 0.78 of the measured copy rate
+// (two blocks 146); keys and values alone 60 us, 41 as they are.
 template <int G>
-__global__ void __launch_bounds__(kThreads) kv4_rotary_kernel(const __grid_constant__ RotaryArgs ra) {
+__global__ void __launch_bounds__(kThreads, 3) kv4_rotary_kernel(const __grid_constant__ RotaryArgs ra) {
     __shared__ __align__(16) uint8_t stage[kWarps][kv4_chunk_bytes(G)];
     __shared__ __align__(16) uint8_t table[16 * G * kTurnBlock];
     __shared__ uint8_t order[kWarps][16];
