@@ -58,6 +58,10 @@ class KV4CacheStruct(ctypes.Structure):
                [(n, c_void_p) for n in ("pages", "table", "lengths")]
 
 
+class DecoderLayerFP8Weights(ctypes.Structure):
+    _fields_ = DecoderLayerWeights._fields_ + [(n, c_void_p) for n in ("s_qkv", "s_o", "s_gu", "s_d")]
+
+
 class LinearArgs(ctypes.Structure):
     _fields_ = [(n, c_int32) for n in ("rows", "out_features", "in_features", "dtype", "y_dtype", "act")] + \
                [("w", c_void_p), ("x", c_void_p), ("ldw", c_int64), ("ldx", c_int64)] + \
@@ -129,6 +133,10 @@ _SIGS = {
                                c_void_p, c_int64, c_int, c_void_p, c_int64, c_void_p, c_void_p]),
     "eagle_linear_epilogue_workspace_bytes": (c_size_t, [c_int32]),
     "eagle_linear": (c_int, [POINTER(LinearArgs), c_void_p, c_size_t, c_void_p, c_void_p]),
+    "eagle_decoder_layer_fp8_kv4_workspace_bytes": (c_size_t, [POINTER(DecoderLayerFP8Weights), POINTER(KV4CacheStruct),
+                                                               c_int32, c_int32]),
+    "eagle_decoder_layer_fp8_kv4": (c_int, [POINTER(DecoderLayerFP8Weights), POINTER(KV4CacheStruct), c_int32, c_int32]
+                                    + [c_void_p] * 7 + [c_size_t, c_void_p, c_void_p]),
     "eagle_linear_noalloc_scratch_bytes": (c_size_t, []),
     "eagle_linear_bf16_noalloc": (c_int, [c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int32,
                                           c_int32, c_int32, c_void_p, c_int64, c_int32, c_void_p]),

@@ -1372,6 +1372,19 @@ cudaError_t prepare_once(int dev) {
     return e;
 }
 
+// Rotation (one block per row, heads split over more blocks when rows are few); the tree's rotated keys
+// and values go out to k_new / v_new here.
+cudaError_t launch_rope(__nv_bfloat16 *qkv, int32_t rows, int32_t H, int32_t Hk, int32_t D, const int32_t *positions,
+                        float theta, void *k_new, void *v_new, int32_t sms, cudaStream_t st) {
+    const int32_t heads_all = H + Hk + (v_new ? Hk : 0);
+    int32_t hsplit = rows >= 2 * sms ? 1 : std::min((2 * sms + rows - 1) / rows, std::max(1, heads_all / 8));
+    const int32_t heads_per_block = (heads_all + hsplit - 1) / hsplit;
+    hsplit = (heads_all + heads_per_block - 1) / heads_per_block;
+    return launch_pdl(rope_kernel, dim3(rows, hsplit), dim3(256), 0, st, qkv, (H + 2 * Hk) * D, H, Hk, heads_per_block, D,
+                      positions, static_cast<double>(theta), reinterpret_cast<__nv_bfloat16 *>(k_new),
+                      reinterpret_cast<__nv_bfloat16 *>(v_new));
+}
+
 // Both layers: over the bf16 cache (kv4 null) or over a 4-bit one (prefix 0, no cache pointers).
 eagle_status run_layer(const eagle_decoder_layer_weights *w, int32_t batch, int32_t nodes, int32_t prefix,
                        const void *d_x, const void *d_k_cache, const void *d_v_cache, const int32_t *d_positions,
@@ -1424,15 +1437,7 @@ eagle_status run_layer(const eagle_decoder_layer_weights *w, int32_t batch, int3
         DEC_CUDA(launch_pdl(zero_tickets_kernel, dim3(1), dim3(256), 0, st, counters, static_cast<int32_t>(L.ticket_bytes / 4)));
     // projections of every node, rotated
     DEC_CUDA(gemm_rows(w->w_qkv, nqkv, h, d_x, rows, qkv, 1, partials, counters, sms, st));
-    // rotation (one block per row, heads split over more blocks when rows are few); the tree's
-    // rotated keys and values go out to k_new / v_new here
-    const int32_t heads_all = H + Hk + (d_v_new ? Hk : 0);
-    int32_t hsplit = rows >= 2 * sms ? 1 : std::min((2 * sms + rows - 1) / rows, std::max(1, heads_all / 8));
-    const int32_t heads_per_block = (heads_all + hsplit - 1) / hsplit;
-    hsplit = (heads_all + heads_per_block - 1) / heads_per_block;
-    DEC_CUDA(launch_pdl(rope_kernel, dim3(rows, hsplit), dim3(256), 0, st, qkv, nqkv, H, Hk, heads_per_block, D,
-                        d_positions, static_cast<double>(w->rope_theta), reinterpret_cast<__nv_bfloat16 *>(d_k_new),
-                        reinterpret_cast<__nv_bfloat16 *>(d_v_new)));
+    DEC_CUDA(launch_rope(qkv, rows, H, Hk, D, d_positions, w->rope_theta, d_k_new, d_v_new, sms, st));
     // tree attention over the cache and the tree
     if (kv4) {
         Kv4Attention ka{};
@@ -1494,6 +1499,90 @@ eagle_status run_layer(const eagle_decoder_layer_weights *w, int32_t batch, int3
     return EAGLE_OK;
 }
 
+// The layer in 8 bits: what of its workspace is where.
+struct Fp8Layout {
+    size_t codes, scale, qkv, o, h1, act, kv4, total;
+};
+
+bool fp8_dims_ok(const eagle_decoder_layer_fp8_weights *w) {
+    if (!w) return false;
+    const eagle_decoder_layer_weights dims{w->hidden, w->heads, w->kv_heads, w->head_dim, w->inter, w->rope_theta, w->rms_eps,
+                                           nullptr, nullptr, nullptr, nullptr, nullptr};
+    return decoder_dims_ok(&dims) && w->hidden % 16 == 0 && w->inter % 16 == 0 && w->hidden <= 32768 && w->inter <= 32768 &&
+           static_cast<int64_t>(w->heads) * w->head_dim <= 32768;
+}
+
+Fp8Layout fp8_layout(const eagle_decoder_layer_fp8_weights *w, int64_t rows, size_t kv4_bytes) {
+    const int64_t h = w->hidden, nq = static_cast<int64_t>(w->heads) * w->head_dim, nk = static_cast<int64_t>(w->kv_heads) * w->head_dim;
+    Fp8Layout L{};
+    size_t o = 0;
+    auto take = [&](int64_t bytes) {
+        const size_t at = o;
+        o = align256(o + static_cast<size_t>(bytes));
+        return at;
+    };
+    L.codes = take(rows * std::max({h, nq, static_cast<int64_t>(w->inter)}));  // of the next product's rows
+    L.scale = take(rows * 4);
+    L.qkv = take(rows * (nq + 2 * nk) * 2);
+    L.o = take(rows * nq * 2);
+    L.h1 = take(rows * h * 2);
+    L.act = take(rows * w->inter * 2);
+    L.kv4 = take(static_cast<int64_t>(kv4_bytes));
+    L.total = o;
+    return L;
+}
+
+eagle_status run_layer_fp8(const eagle_decoder_layer_fp8_weights *w, const Kv4View &kv4, int32_t batch, int32_t nodes, const void *x,
+                           const int32_t *positions, const uint32_t *mask, void *out, void *k_new, void *v_new, uint8_t *ws,
+                           size_t ws_bytes, int32_t *status, cudaStream_t st) {
+    const int32_t sms = linear_sms(), rows = batch * nodes, h = w->hidden, H = w->heads, Hk = w->kv_heads, D = w->head_dim, I = w->inter;
+    const int32_t nq = H * D, nk = Hk * D, nqkv = nq + 2 * nk;
+    if (sms < 1) return EAGLE_ERR_CUDA;
+    const size_t kv4_bytes = kv4_attention_workspace(Hk, D / kKv4Group, H, nodes);
+    if (kv4_bytes == 0) return EAGLE_ERR_CUDA;
+    const Fp8Layout L = fp8_layout(w, rows, kv4_bytes);
+    if (ws_bytes < L.total) return EAGLE_ERR_INVALID_ARG;
+    if (!kv4_attention_fits(kv4, batch, nodes, H, true)) return EAGLE_ERR_UNSUPPORTED;
+    uint8_t *codes = ws + L.codes;
+    float *scale = reinterpret_cast<float *>(ws + L.scale);
+    auto *qkv = reinterpret_cast<__nv_bfloat16 *>(ws + L.qkv);
+    void *o = ws + L.o, *h1 = ws + L.h1, *act = ws + L.act;
+    // y = act(codes w^T) + residual, in bf16
+    auto product = [&](const void *wt, const float *ws_, int32_t M, int32_t K, int32_t activation, const void *residual, void *y) {
+        const LinearEpilogue ep{scale, ws_, static_cast<const __nv_bfloat16 *>(residual), M, activation};
+        return launch_linear(true, ep, wt, K, M, K, codes, K, rows, nullptr, y, M, true, nullptr, status, sms, st);
+    };
+#define DEC_CUDA(expr)                              \
+    do {                                            \
+        if ((expr) != cudaSuccess) return EAGLE_ERR_CUDA; \
+    } while (0)
+    DEC_CUDA(launch_quantize_rows(x, h, rows, h, codes, h, scale, st));
+    DEC_CUDA(product(w->w_qkv, w->s_qkv, nqkv, h, kActNone, nullptr, qkv));
+    DEC_CUDA(launch_rope(qkv, rows, H, Hk, D, positions, w->rope_theta, k_new, v_new, sms, st));
+    Kv4Attention ka{};
+    ka.cache = kv4;
+    ka.B = batch;
+    ka.n = nodes;
+    ka.H = H;
+    ka.q = qkv;
+    ka.kn = qkv + nq;
+    ka.vn = qkv + nq + nk;
+    ka.ldq = ka.ldkv = nqkv;
+    ka.mask = mask;
+    ka.o = static_cast<__nv_bfloat16 *>(o);
+    ka.ws = ws + L.kv4;
+    ka.status = status;
+    DEC_CUDA(launch_kv4_attention(ka, st));
+    DEC_CUDA(launch_quantize_rows(o, nq, rows, nq, codes, nq, scale, st));
+    DEC_CUDA(product(w->w_o, w->s_o, h, nq, kActNone, x, h1));
+    DEC_CUDA(launch_rms_norm(h1, h, nullptr, 0, w->w_norm, w->rms_eps, rows, h, nullptr, 0, codes, h, scale, st));
+    DEC_CUDA(product(w->w_gu, w->s_gu, I, h, kActSwiglu, nullptr, act));
+    DEC_CUDA(launch_quantize_rows(act, I, rows, I, codes, I, scale, st));
+    DEC_CUDA(product(w->w_d, w->s_d, h, I, kActNone, h1, out));
+#undef DEC_CUDA
+    return EAGLE_OK;
+}
+
 }  // namespace
 }  // namespace eagle
 
@@ -1540,6 +1629,43 @@ eagle_status eagle_decoder_layer_kv4(const eagle_decoder_layer_weights *w, const
     if (reinterpret_cast<uintptr_t>(d_status) & 3u) return EAGLE_ERR_INVALID_ARG;
     return eagle::run_layer(w, batch, nodes, 0, d_x, nullptr, nullptr, d_positions, d_mask, d_out, d_k_new, d_v_new,
                             d_ws, ws_bytes, stream, &v, d_status);
+}
+
+size_t eagle_decoder_layer_fp8_kv4_workspace_bytes(const eagle_decoder_layer_fp8_weights *w, const eagle_kv4_cache *cache,
+                                                   int32_t batch, int32_t nodes) {
+    eagle::Kv4View v;
+    if (!eagle::fp8_dims_ok(w) || !eagle::kv4_view(cache, &v) || batch < 1 || nodes < 1 || nodes > eagle::kMaxCandidates + 1)
+        return 0;
+    if (v.Hk != w->kv_heads || v.G * eagle::kKv4Group != w->head_dim) return 0;
+    if (static_cast<int64_t>(batch) * nodes > eagle::kLinearMaxLaunchRows || eagle::linear_sms() < 1) return 0;
+    const size_t kv4 = eagle::kv4_attention_workspace(v.Hk, v.G, w->heads, nodes);
+    return kv4 ? eagle::fp8_layout(w, static_cast<int64_t>(batch) * nodes, kv4).total : 0;
+}
+
+eagle_status eagle_decoder_layer_fp8_kv4(const eagle_decoder_layer_fp8_weights *w, const eagle_kv4_cache *cache, int32_t batch,
+                                         int32_t nodes, const void *d_x, const int32_t *d_positions, const uint32_t *d_mask,
+                                         void *d_out, void *d_k_new, void *d_v_new, void *d_ws, size_t ws_bytes,
+                                         int32_t *d_status, eagle_stream_t stream) {
+    eagle::NvtxRange nvtx_range("eagle_decoder_layer_fp8_kv4");
+    eagle::Kv4View v;
+    if (!eagle::fp8_dims_ok(w) || !eagle::kv4_view(cache, &v)) return EAGLE_ERR_INVALID_ARG;
+    if (v.Hk != w->kv_heads || v.G * eagle::kKv4Group != w->head_dim) return EAGLE_ERR_INVALID_ARG;
+    if (batch < 0 || nodes < 1 || nodes > eagle::kMaxCandidates + 1) return EAGLE_ERR_INVALID_ARG;
+    if (static_cast<int64_t>(batch) * nodes > eagle::kLinearMaxLaunchRows) return EAGLE_ERR_INVALID_ARG;
+    if (static_cast<int64_t>(nodes) * (w->heads / w->kv_heads) > (1 << 24)) return EAGLE_ERR_INVALID_ARG;
+    if (batch == 0) return EAGLE_OK;
+    const void *needed[] = {w->w_qkv, w->w_o, w->w_norm, w->w_gu, w->w_d, d_x, d_out};
+    for (const void *p : needed)
+        if (!p || (reinterpret_cast<uintptr_t>(p) & 15u)) return EAGLE_ERR_INVALID_ARG;
+    const void *words[] = {w->s_qkv, w->s_o, w->s_gu, w->s_d, d_positions};
+    for (const void *p : words)
+        if (!p || (reinterpret_cast<uintptr_t>(p) & 3u)) return EAGLE_ERR_INVALID_ARG;
+    if ((d_k_new == nullptr) != (d_v_new == nullptr)) return EAGLE_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(d_k_new) | reinterpret_cast<uintptr_t>(d_v_new)) & 15u) return EAGLE_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(d_mask) | reinterpret_cast<uintptr_t>(d_status)) & 3u) return EAGLE_ERR_INVALID_ARG;
+    if (!d_ws || (reinterpret_cast<uintptr_t>(d_ws) & 255u)) return EAGLE_ERR_INVALID_ARG;
+    return eagle::run_layer_fp8(w, v, batch, nodes, d_x, d_positions, d_mask, d_out, d_k_new, d_v_new, static_cast<uint8_t *>(d_ws),
+                                ws_bytes, d_status, reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

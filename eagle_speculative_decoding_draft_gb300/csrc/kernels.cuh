@@ -174,6 +174,12 @@ bool launch_linear_tiles(bool fp8, const LinearEpilogue &ep, const void *w, int6
                          int32_t pairs, cudaStream_t st, cudaError_t *err);
 cudaError_t prepare_linear_tiles();
 
+// linear.cu: the product by whichever of them the sizes ask for (ws may be null; rows >= 1).
+// cudaErrorInvalidValue: a row stride or a size that a tensor map does not hold.
+cudaError_t launch_linear(bool fp8, const LinearEpilogue &ep, const void *w, int64_t ldw, int32_t M, int32_t K, const void *x,
+                          int64_t ldx, int32_t rows, const void *bias, void *y, int64_t ldy, bool y_bf16, void *ws, int32_t *status,
+                          int32_t sms, cudaStream_t st);
+
 // norm.cu: rows quantised, and the residual's addition and RMS norm (bf16, or 8-bit rows where scale is given).
 cudaError_t launch_quantize_rows(const void *x, int64_t ldx, int32_t rows, int32_t n, void *y, int64_t ldy, float *scale,
                                  cudaStream_t st);

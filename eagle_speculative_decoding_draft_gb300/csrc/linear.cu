@@ -64,6 +64,28 @@ cudaError_t launch_linear_form(const LinearPlan &p, const LinearArgs &a, cudaStr
     }
 }
 
+cudaError_t launch_linear(bool fp8, const LinearEpilogue &ep, const void *w, int64_t ldw, int32_t M, int32_t K, const void *x,
+                          int64_t ldx, int32_t rows, const void *bias, void *y, int64_t ldy, bool y_bf16, void *ws, int32_t *status,
+                          int32_t sms, cudaStream_t st) {
+    if (rows <= kLinearFewRows) return launch_linear_few(fp8, ep, w, ldw, M, K, x, ldx, rows, bias, y, ldy, y_bf16, sms, st);
+    cudaError_t e = prepare_linear_forms();
+    if (e != cudaSuccess) return e;
+    // Over 128 rows the tensor cores bound the product, or nearly so: whole tiles of both operands (256 rows,
+    // 4096 -> 2 x 11008 in 8 bits: 30 us, and 43 with the weights past 128 rows at a time; 128 rows: 29 and 25).
+    // Outputs that no bulk store takes go through the weights' stream where there is a workspace for it.
+    if (rows > kLinearMidRows) {
+        const int32_t pairs = linear_pair_workers(sms);
+        if (pairs > 0 && launch_linear_tiles(fp8, ep, w, ldw, M, K, x, ldx, rows, bias, y, ldy, y_bf16, status, pairs, st, &e)) return e;
+    }
+    if (rows <= kLinearMidRows || !ws)
+        return launch_linear_mid(fp8, ep, w, ldw, M, K, x, ldx, rows, bias, y, ldy, y_bf16, status, sms, st, &e) ? e : cudaErrorInvalidValue;
+    LinearPlan p;
+    if (!plan_linear(&p, fp8, ep, w, ldw, M, K, x, ldx, rows, bias, y, ldy, y_bf16,
+                     reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + kLinearTicketBytes), static_cast<int32_t *>(ws), status, sms))
+        return cudaErrorInvalidValue;
+    return launch_linear_bf16(p, st);
+}
+
 }  // namespace eagle
 
 extern "C" {
@@ -88,7 +110,6 @@ eagle_status eagle_linear(const eagle_linear_args *l, void *d_ws, size_t ws_byte
     const int32_t M = l->out_features, K = l->in_features, step = fp8 ? 16 : 8;
     if (M > (1 << 28) || K > (1 << 28)) return EAGLE_ERR_INVALID_ARG;
     auto off = [](const void *p, uintptr_t by) { return (reinterpret_cast<uintptr_t>(p) & (by - 1)) != 0; };
-    const bool few = l->rows <= kLinearFewRows;
     if (!l->w || !l->x || !l->y) return EAGLE_ERR_INVALID_ARG;
     if (fp8 != (l->w_scale != nullptr) || fp8 != (l->x_scale != nullptr)) return EAGLE_ERR_INVALID_ARG;
     if (off(l->w, 16) || off(l->x, 16) || off(l->w_scale, 4) || off(l->x_scale, 4) || off(l->bias, 2) || off(l->residual, 2))
@@ -100,37 +121,12 @@ eagle_status eagle_linear(const eagle_linear_args *l, void *d_ws, size_t ws_byte
     const int32_t sms = linear_sms();
     if (sms < 1) return EAGLE_ERR_CUDA;
     if (d_ws && ws_bytes < linear_workspace(l->rows, sms)) return EAGLE_ERR_INVALID_ARG;
-    if (!few && prepare_linear_forms() != cudaSuccess) return EAGLE_ERR_CUDA;
     const LinearEpilogue ep{l->x_scale, l->w_scale, static_cast<const __nv_bfloat16 *>(l->residual), l->ldr,
                             static_cast<int32_t>(l->act)};
-    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    const bool y_bf16 = l->y_dtype == EAGLE_BF16;
-    cudaError_t err = cudaSuccess;
-    if (few) {
-        err = launch_linear_few(fp8, ep, l->w, l->ldw, M, K, l->x, l->ldx, l->rows, l->bias, l->y, l->ldy, y_bf16, sms, st);
-        return err == cudaSuccess ? EAGLE_OK : EAGLE_ERR_CUDA;
-    }
-    // Over 128 rows the tensor cores bound the product, or nearly so: whole tiles of both operands (256 rows,
-    // 4096 -> 2 x 11008 in 8 bits: 30 us, and 43 with the weights past 128 rows at a time; 128 rows: 29 and 25).
-    // Outputs that no bulk store takes go through the weights' stream where there is a workspace for it.
-    if (l->rows > kLinearMidRows) {
-        const int32_t pairs = linear_pair_workers(sms);
-        if (pairs > 0 && launch_linear_tiles(fp8, ep, l->w, l->ldw, M, K, l->x, l->ldx, l->rows, l->bias, l->y, l->ldy, y_bf16,
-                                             d_status, pairs, st, &err))
-            return err == cudaSuccess ? EAGLE_OK : EAGLE_ERR_CUDA;
-    }
-    if (l->rows <= kLinearMidRows || !d_ws) {
-        if (!launch_linear_mid(fp8, ep, l->w, l->ldw, M, K, l->x, l->ldx, l->rows, l->bias, l->y, l->ldy, y_bf16, d_status, sms,
-                               st, &err))
-            return EAGLE_ERR_UNSUPPORTED;
-        return err == cudaSuccess ? EAGLE_OK : EAGLE_ERR_CUDA;
-    }
-    LinearPlan p;
-    if (!plan_linear(&p, fp8, ep, l->w, l->ldw, M, K, l->x, l->ldx, l->rows, l->bias, l->y, l->ldy,
-                     l->y_dtype == EAGLE_BF16, reinterpret_cast<float *>(static_cast<uint8_t *>(d_ws) + kLinearTicketBytes),
-                     static_cast<int32_t *>(d_ws), d_status, sms))
-        return EAGLE_ERR_UNSUPPORTED;
-    return launch_linear_bf16(p, st) == cudaSuccess ? EAGLE_OK : EAGLE_ERR_CUDA;
+    const cudaError_t e = launch_linear(fp8, ep, l->w, l->ldw, M, K, l->x, l->ldx, l->rows, l->bias, l->y, l->ldy,
+                                        l->y_dtype == EAGLE_BF16, d_ws, d_status, sms, reinterpret_cast<cudaStream_t>(stream));
+    // a row stride or a size that a tensor map does not hold
+    return e == cudaSuccess ? EAGLE_OK : (e == cudaErrorInvalidValue ? EAGLE_ERR_UNSUPPORTED : EAGLE_ERR_CUDA);
 }
 
 }  // extern "C"

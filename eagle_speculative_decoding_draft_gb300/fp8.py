@@ -13,6 +13,7 @@ import torch
 
 from . import _lib
 from ._lib import EAGLE_BF16, EAGLE_E4M3, EAGLE_F32, check
+from .engine import _need
 
 _BF16, _E4M3, _F32, _U8 = torch.bfloat16, torch.float8_e4m3fn, torch.float32, torch.uint8
 _ACTS = {None: 0, "none": 0, "silu": 1, "gelu": 2, "swiglu": 3}
@@ -202,3 +203,72 @@ def linear(w, x, bias=None, act=None, residual=None, w_scale=None, x_scale=None,
                            p_bias, p_res, ldr, out.data_ptr(), ldy)
     check(_lib.load().eagle_linear(ctypes.byref(args), p_work, nbytes, None, _stream(index)), "eagle_linear")
     return out
+
+
+class DecoderLayerFP8:
+    """The draft decoder layer in 8 bits over a 4-bit cache (eagle_decoder_layer_fp8_kv4).  Takes the bf16
+    weights of ``DecoderLayer`` and keeps 8-bit rows of the projections': half the bytes."""
+
+    def __init__(self, w_qkv, w_o, w_norm, w_gu, w_d, heads: int, kv_heads: int, rope_theta: float = 10000.0,
+                 rms_eps: float = 1e-6):
+        self._lib = _lib.load()
+        for t, name in ((w_qkv, "w_qkv"), (w_o, "w_o"), (w_norm, "w_norm"), (w_gu, "w_gu"), (w_d, "w_d")):
+            _need(t, name, _BF16, w_norm.device)
+        h, inter = w_norm.shape[0], w_gu.shape[0] // 2
+        D = w_qkv.shape[0] // (heads + 2 * kv_heads)
+        if w_qkv.shape != (D * (heads + 2 * kv_heads), h) or w_o.shape != (h, heads * D) \
+                or w_gu.shape != (2 * inter, h) or w_d.shape != (h, inter):
+            raise ValueError("decoder layer weight shapes do not agree")
+        if h % 16 or inter % 16:
+            raise ValueError("hidden and inter must be multiples of 16")
+        rows = [quantize_rows(t) for t in (w_qkv, w_o, w_gu, w_d)]
+        self._keep = (rows, w_norm)
+        (qkv, s_qkv), (o, s_o), (gu, s_gu), (d, s_d) = ((c.data_ptr(), s.data_ptr()) for c, s in rows)
+        self.w = _lib.DecoderLayerFP8Weights(h, heads, kv_heads, D, inter, rope_theta, rms_eps, qkv, o, w_norm.data_ptr(), gu, d,
+                                             s_qkv, s_o, s_gu, s_d)
+        self.hidden, self.heads, self.kv_heads, self.head_dim, self.inter = h, heads, kv_heads, D, inter
+        self.device = w_norm.device
+
+    def workspace_bytes(self, cache, batch: int, nodes: int) -> int:
+        """Bytes of scratch that a call with these sizes needs."""
+        with cache._on(None):
+            n = self._lib.eagle_decoder_layer_fp8_kv4_workspace_bytes(ctypes.byref(self.w), cache._ref, max(batch, 1), nodes)
+        if n == 0:
+            raise ValueError(f"unusable decoder layer sizes (batch={batch}, nodes={nodes}) or a cache of other heads")
+        return n
+
+    def kv4(self, x, cache, positions, mask=None, out=None, new_kv: bool = False, workspace=None, stream=None):
+        """The layer over the cache, as ``DecoderLayer.kv4``: x [B][n][h] bf16, positions [B][n] int32, mask
+        [B][n][ceil(n / 32)] int32 (None: node i sees nodes 0..i).  Returns out [B][n][h] bf16, and with new_kv
+        the nodes' turned keys and values for ``cache.append``.  workspace: a uint8 tensor to use instead of a
+        fresh one; calls that may overlap need one each."""
+        _need(x, "x", _BF16)
+        B, n, h = x.shape
+        if h != self.hidden or B != cache.batch:
+            raise ValueError("x does not match the weights or the cache")
+        if cache.device != x.device or self.device != x.device:
+            raise ValueError("the weights, the cache and x must be on one device")
+        if _need(positions, "positions", torch.int32, x.device).shape != (B, n):
+            raise ValueError("positions shape does not match")
+        if mask is not None and _need(mask, "mask", torch.int32, x.device).shape != (B, n, (n + 31) // 32):
+            raise ValueError("mask shape does not match")
+        nbytes = self.workspace_bytes(cache, B, n)
+        with cache._on(stream):
+            if out is None:
+                out = torch.empty_like(x)
+            elif _need(out, "out", _BF16, x.device).shape != x.shape:
+                raise ValueError("out shape does not match")
+            kn = vn = p_kn = p_vn = None
+            if new_kv:
+                kn = torch.empty(B, n, self.kv_heads, self.head_dim, dtype=_BF16, device=x.device)
+                vn = torch.empty_like(kn)
+                p_kn, p_vn = kn.data_ptr(), vn.data_ptr()
+            if workspace is None:
+                workspace = torch.empty(nbytes, dtype=_U8, device=x.device)
+            elif _need(workspace, "workspace", _U8, x.device).numel() < nbytes:
+                raise ValueError(f"workspace must hold at least {nbytes} bytes")
+            check(self._lib.eagle_decoder_layer_fp8_kv4(
+                ctypes.byref(self.w), cache._ref, B, n, x.data_ptr(), positions.data_ptr(), None if mask is None else mask.data_ptr(),
+                out.data_ptr(), p_kn, p_vn, workspace.data_ptr(), nbytes, cache._status.data_ptr(),
+                cache._raw_stream(stream)), "eagle_decoder_layer_fp8_kv4")
+        return (out, kn, vn) if new_kv else out

@@ -743,6 +743,34 @@ EAGLE_API eagle_status eagle_linear(const eagle_linear_args *args, void *d_ws, s
                                     eagle_stream_t stream);
 
 /*
+ * The draft decoder layer in 8 bits over a 4-bit cache: eagle_decoder_layer_kv4 with every projection a
+ * product of 8-bit rows.  Weights are 8-bit rows as eagle_quantize_rows makes them of eagle_decoder_layer's:
+ * codes of contiguous rows and one scale a row (s_qkv [(heads + 2 kv_heads) head_dim], s_o [hidden], s_gu
+ * [2 inter], s_d [hidden], fp32); w_norm [hidden] is bf16.  x, the attention's output, the normed rows and
+ * silu(g) u are quantised a row at a time as they come; the projections' outputs, the attention's output,
+ * h1 = x + Wo o, silu(g) u and the layer's output are bf16, and h1 and the output round once, with the residual
+ * already added.
+ * hidden and inter are multiples of 16; hidden, inter and heads * head_dim at most 32768; batch * nodes at most
+ * 32768.  The other arguments, limits and errors are those of eagle_decoder_layer_kv4; d_ws may hold anything,
+ * and calls that may run at the same time need workspaces of their own.  d_out must not overlap d_x.
+ */
+typedef struct {
+    int32_t hidden, heads, kv_heads, head_dim, inter;
+    float rope_theta, rms_eps;
+    const void *w_qkv, *w_o, *w_norm, *w_gu, *w_d;
+    const float *s_qkv, *s_o, *s_gu, *s_d;
+} eagle_decoder_layer_fp8_weights;
+EAGLE_API size_t eagle_decoder_layer_fp8_kv4_workspace_bytes(const eagle_decoder_layer_fp8_weights *w,
+                                                             const eagle_kv4_cache *cache, int32_t batch,
+                                                             int32_t nodes);
+EAGLE_API eagle_status eagle_decoder_layer_fp8_kv4(const eagle_decoder_layer_fp8_weights *w,
+                                                   const eagle_kv4_cache *cache, int32_t batch, int32_t nodes,
+                                                   const void *d_x, const int32_t *d_positions,
+                                                   const uint32_t *d_mask, void *d_out, void *d_k_new, void *d_v_new,
+                                                   void *d_ws, size_t ws_bytes, int32_t *d_status,
+                                                   eagle_stream_t stream);
+
+/*
  * The streamed-weight GEMM of eagle_linear_bf16 without caller-provided scratch.  The pages have
  * no counterpart: this is an engineering variant for callers that cannot allocate device memory
  * (code where cudaMalloc is not allowed or not wanted because it synchronises the device and can

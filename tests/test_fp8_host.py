@@ -88,3 +88,35 @@ def test_append_rotary_refuses(lib, bad):
 
 def test_append_rotary_of_no_requests(lib):
     assert rotary(lib, batch=0) == 0
+
+
+def fp8_layer(lib, batch=2, nodes=3, x=P(256), positions=P(256), mask=P(256), out=P(256), k_new=P(256), v_new=P(256), ws=P(256), nbytes=1 << 40,
+              status=None, cache=None, **kw):
+    from eagle_speculative_decoding_draft_gb300._lib import DecoderLayerFP8Weights
+    from test_kv4_host import cache as make
+    f = dict(hidden=64, heads=4, kv_heads=2, head_dim=64, inter=48, rope_theta=1e4, rms_eps=1e-6, w_qkv=256, w_o=256, w_norm=256, w_gu=256,
+             w_d=256, s_qkv=256, s_o=256, s_gu=256, s_d=256)
+    f.update(kw)
+    w = DecoderLayerFP8Weights(*(f[k] for k, _ in DecoderLayerFP8Weights._fields_))
+    c = make(**(cache or {}))
+    if nbytes is None:
+        return lib.eagle_decoder_layer_fp8_kv4_workspace_bytes(ctypes.byref(w), ctypes.byref(c), batch, nodes)
+    return lib.eagle_decoder_layer_fp8_kv4(ctypes.byref(w), ctypes.byref(c), batch, nodes, x, positions, mask, out, k_new, v_new, ws, nbytes,
+                                           status, None)
+
+
+@pytest.mark.parametrize("bad", [dict(hidden=72), dict(hidden=0), dict(hidden=32784), dict(inter=40), dict(inter=32784), dict(heads=3),
+                                 dict(heads=1024), dict(head_dim=96), dict(kv_heads=4), dict(rope_theta=0.0), dict(rms_eps=-1.0),
+                                 dict(w_qkv=None), dict(w_o=None), dict(w_norm=None), dict(w_gu=None), dict(w_d=None), dict(s_qkv=None),
+                                 dict(s_o=None), dict(s_gu=None), dict(s_d=None), dict(w_gu=264), dict(s_d=258), dict(batch=-1),
+                                 dict(nodes=0), dict(nodes=4098), dict(batch=11, nodes=3000), dict(x=None), dict(positions=None),
+                                 dict(out=None), dict(x=P(264)), dict(out=P(264)), dict(k_new=None), dict(v_new=P(264)), dict(ws=None),
+                                 dict(ws=P(128)), dict(mask=P(258)), dict(status=P(258)), dict(cache=dict(pages=None))], ids=str)
+def test_fp8_layer_refuses(lib, bad):
+    assert fp8_layer(lib, **bad) == 1
+
+
+def test_fp8_layer_edges(lib):
+    assert fp8_layer(lib, batch=0, x=None, out=None, ws=None) == 0
+    for bad in (dict(batch=0), dict(nodes=0), dict(hidden=72), dict(batch=11, nodes=3000), dict(cache=dict(head_dim=96))):
+        assert fp8_layer(lib, nbytes=None, **bad) == 0
