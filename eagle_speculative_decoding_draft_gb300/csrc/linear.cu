@@ -77,7 +77,7 @@ cudaError_t launch_linear(bool fp8, const LinearEpilogue &ep, const void *w, int
         const int32_t pairs = linear_pair_workers(sms);
         if (pairs > 0 && launch_linear_tiles(fp8, ep, w, ldw, M, K, x, ldx, rows, bias, y, ldy, y_bf16, status, pairs, st, &e)) return e;
     }
-    if (rows <= kLinearMidRows || !ws)
+    if (rows <= kLinearMidRows || !ws || (!fp8 && !y_bf16 && K > 4096))  // (the stream has no parts for long sums)
         return launch_linear_mid(fp8, ep, w, ldw, M, K, x, ldx, rows, bias, y, ldy, y_bf16, status, sms, st, &e) ? e : cudaErrorInvalidValue;
     LinearPlan p;
     if (!plan_linear(&p, fp8, ep, w, ldw, M, K, x, ldx, rows, bias, y, ldy, y_bf16,

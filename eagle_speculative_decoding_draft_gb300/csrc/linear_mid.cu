@@ -31,6 +31,7 @@ struct MidArgs {
     LinearArgs l;      // M, rows, n_tile, num_kb, stages, bias, out, ldo, out_bf16, ep, status
     int32_t split;     // CTAs of a cluster
     int32_t tmem_cols;
+    int32_t halves;    // 2: the second half of a part's sums in an accumulator of its own
 };
 
 __device__ __forceinline__ void tmem_ld_4(uint32_t taddr, uint32_t (&r)[4]) {
@@ -114,6 +115,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     } else if (warp == 1) {
         if (lane == 0) {
             const uint32_t idesc = Op::kFp8 ? idesc_e4m3_f32(BM, static_cast<uint32_t>(n)) : idesc_bf16_f32(BM, static_cast<uint32_t>(n));
+            const int32_t kb_half = m.halves == 2 ? (kb_begin + kb_end) / 2 : kb_end;
             uint32_t stage = 0, phase = 0;
             bool ok = true;
             for (int32_t kb = kb_begin; kb < kb_end; ++kb) {
@@ -131,7 +133,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                     if (Op::kFp8)
                         mma_f8_ss(tmem_base, dw, dx, idesc, kb > kb_begin || kk > 0);
                     else
-                        mma_bf16_ss(tmem_base, dw, dx, idesc, kb > kb_begin || kk > 0);
+                        mma_bf16_ss(tmem_base + (kb >= kb_half ? static_cast<uint32_t>(n) : 0u), dw, dx, idesc,
+                                    (kb > kb_begin && kb != kb_half) || kk > 0);
                 }
                 mma_commit(&ctl->empty[stage]);
                 if (++stage == static_cast<uint32_t>(stages)) {
@@ -165,6 +168,13 @@ __global__ void __launch_bounds__(kThreads, 2)
                 __syncwarp();
                 tmem_ld_32(t_row + static_cast<uint32_t>(c), r);
                 tmem_wait_ld();
+                if (!Op::kFp8 && m.halves == 2) {
+                    uint32_t r2[32];
+                    tmem_ld_32(t_row + static_cast<uint32_t>(n + c), r2);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) + __uint_as_float(r2[i]));
+                }
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {  // a share is a multiple of 4 rows
                     const int32_t to = (c + 4 * i) / share, at = c + 4 * i - to * share;
@@ -187,12 +197,21 @@ __global__ void __launch_bounds__(kThreads, 2)
                 const int32_t n0 = part * share + c;
                 if (n0 >= end) break;
                 uint32_t r[C];
-                __syncwarp();
-                if constexpr (C == 16)
-                    tmem_ld_16(t_row + static_cast<uint32_t>(n0), r);
-                else
-                    tmem_ld_4(t_row + static_cast<uint32_t>(n0), r);
-                tmem_wait_ld();
+                auto sums = [&](int32_t col, uint32_t (&to)[C]) {
+                    __syncwarp();
+                    if constexpr (C == 16)
+                        tmem_ld_16(t_row + static_cast<uint32_t>(col), to);
+                    else
+                        tmem_ld_4(t_row + static_cast<uint32_t>(col), to);
+                    tmem_wait_ld();
+                };
+                sums(n0, r);
+                if (!Op::kFp8 && m.halves == 2) {
+                    uint32_t r2[C];
+                    sums(n + n0, r2);
+#pragma unroll
+                    for (int i = 0; i < C; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) + __uint_as_float(r2[i]));
+                }
                 float v[C];
                 for (int32_t from = 0; from < S; ++from) {  // in their order
                     const float4 *src = reinterpret_cast<const float4 *>(ring + ((from < part ? from : from - 1) * share + c) * 512) + ml;
@@ -277,13 +296,16 @@ bool launch_linear_mid(bool fp8, const LinearEpilogue &ep, const void *w, int64_
     a.out_bf16 = out_bf16;
     a.ep = ep;
     a.status = status;
-    m.tmem_cols = a.n_tile == 96 ? 128 : a.n_tile;
     const int32_t chunks = (rows + a.n_tile - 1) / a.n_tile;
     // as many parts as two CTAs an SM leave room for at once (61 rows, 4096 -> 4096 in 8 bits: 15.7, 11.4, 9.1 and
     // 9.5 us with 1, 2, 4 and 8; 4096 -> 6144: 16.1, 11.7, 10.3 and, in two waves, 16.4; 4096 -> 2 x 11008: 19.9 with
     // one, 26 with two), of at least two k-blocks
     m.split = 1;
     while (m.split < 8 && static_cast<int64_t>(a.num_tiles) * chunks * m.split <= sms && a.num_kb >= 4 * m.split) m.split *= 2;
+    // Long sums of bf16 products in two halves where fp32 goes out: the accumulator truncates (linear_tiles.cu)
+    m.halves = !fp8 && !out_bf16 && a.num_kb / m.split > 64 ? 2 : 1;
+    m.tmem_cols = 32;
+    while (m.tmem_cols < a.n_tile * m.halves) m.tmem_cols *= 2;
     CUtensorMap mw, mx;
     if (gated ? !encode_gated_rows(&mw, es, w, K, M, ldw, 16) : !encode_swizzled_rows(&mw, es, w, K, M, ldw, box, BM)) return false;
     if (!encode_swizzled_rows(&mx, es, x, K, rows, ldx, box, a.n_tile)) return false;

@@ -66,14 +66,19 @@ __device__ __forceinline__ void tile_of(const TileArgs &a, int32_t u, int32_t &r
 
 // kSplit: a cluster of `split` pairs forms one tile, each from its part of K, and each finishes its part of
 // the tile's columns.
-template <bool kFp8, bool kGated, bool kSplit>
+// kLong: the tensor core's accumulator truncates, so a long sum of bf16 products is too small by a part that
+// grows with its length (14336 products 1.7e-5, more than an fp32 output should lose): the sums of kSegment
+// k-blocks at a time are added up, rounded to nearest, in the accumulator's other half (2e-6).
+constexpr int kSegment = 32;
+template <bool kFp8, bool kGated, bool kSplit, bool kLong>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_tiles_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_w,
                         const __grid_constant__ CUtensorMap tmap_y, const __grid_constant__ CUtensorMap tmap_r,
                         const TileArgs a) {
     constexpr int32_t BK = kFp8 ? 128 : 64;
     constexpr int32_t kCols = kGated ? kHalf : kTile;  // outputs of a tile's row
-    constexpr uint32_t kTmemCols = kSplit ? kTile : 2 * kTile;
+    constexpr uint32_t kTmemCols = kSplit && !kLong ? kTile : 2 * kTile;
+    constexpr uint32_t kSums = kLong ? kTile : 0;  // where the epilogue finds the sums, in an accumulator
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_addr = smem_u32(smem_raw);
     uint8_t *ring = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
@@ -164,14 +169,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t idesc = kFp8 ? idesc_e4m3_f32(kTile, kTile) : idesc_bf16_f32(kTile, kTile);
             uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0;
             bool ok = true;
-            for (int32_t u = pair; u < units && ok; u += pairs) {
+            const int32_t segments = kLong ? (kb_end - kb_begin + kSegment - 1) / kSegment : 1;
+            for (int32_t u = pair, seg = 0; u < units && ok; seg = seg + 1 < segments ? seg + 1 : 0, u += seg == 0 ? pairs : 0) {
+                const int32_t kb0 = kb_begin + seg * kSegment, kb1 = kLong ? min(kb_end, kb0 + kSegment) : kb_end;
                 if (!mbar_wait(&ctl->acc_empty[acc], acc_phase ^ 1u, abort_flag)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + acc * kTile;
-                for (int32_t kb = kb_begin; kb < kb_end; ++kb) {
+                for (int32_t kb = kb0; kb < kb1; ++kb) {
                     if (!mbar_wait(&ctl->full[stage], phase, abort_flag)) {
                         ok = false;
                         break;
@@ -182,9 +189,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int kk = 0; kk < 4; ++kk) {  // 32 bytes of the 128 an MMA
                         const uint64_t dx = sw128_kmajor_desc(x0 + kk * 32), dw = sw128_kmajor_desc(w0 + kk * 32);
                         if (kFp8)
-                            mma_f8_ss_pair(d_tmem, dx, dw, idesc, kb > kb_begin || kk > 0);
+                            mma_f8_ss_pair(d_tmem, dx, dw, idesc, kb > kb0 || kk > 0);
                         else
-                            mma_bf16_ss_pair(d_tmem, dx, dw, idesc, kb > kb_begin || kk > 0);
+                            mma_bf16_ss_pair(d_tmem, dx, dw, idesc, kb > kb0 || kk > 0);
                     }
                     mma_commit_pair_mc(&ctl->empty[stage], static_cast<uint16_t>(3u << leader));  // the stage is free in both CTAs
                     if (++stage == kStages) {
@@ -194,7 +201,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (!ok) break;
                 mma_commit_pair_mc(&ctl->acc_full[acc], static_cast<uint16_t>(3u << leader));  // each CTA drains its own 128 rows
-                acc ^= 1u;
+                if (!kLong) acc ^= 1u;
                 if (acc == 0) acc_phase ^= 1u;
             }
             if (!ok) {
@@ -222,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             cluster_sync();  // every CTA's copies and products are over
             if (!__any_sync(kFull, skip)) {
-                const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+                const uint32_t t_row = tmem_base + kSums + (static_cast<uint32_t>(q * 32) << 16);
                 for (int32_t to = 0; to < split; ++to) {
                     if (to == part) continue;
                     const uint32_t at = peer_addr(ring, 2u * to + rank) +
@@ -285,11 +292,42 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             const float rs = kFp8 ? (row < a.rows ? a.ep.x_scale[row] : 0.0f) : 1.0f;
-            const bool got = mbar_wait(&ctl->acc_full[acc], acc_phase, abort_flag);
+            bool got = true;
+            if constexpr (kLong) {
+                named_barrier_sync(1, kEpilogueThreads);  // all are done with the last tile's sums
+                const uint32_t from = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + side * kHalf;
+                for (int32_t kb = kb_begin; kb < kb_end; kb += kSegment) {
+                    got = got && mbar_wait(&ctl->acc_full[0], acc_phase, abort_flag);
+                    got = __all_sync(kFull, got);
+                    if (!got) break;
+                    tc_fence_after();
+                    for (int32_t c = 0; c < kHalf; c += 32) {
+                        uint32_t r[32], s[32];
+                        tmem_ld_32(from + c, r);
+                        if (kb > kb_begin) {
+                            tmem_ld_32(from + kSums + c, s);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) + __uint_as_float(s[j]));
+                        } else {
+                            tmem_wait_ld();
+                        }
+                        tmem_st_32(from + kSums + c, r);
+                    }
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(peer_addr(&ctl->acc_empty[0], leader));
+                    acc_phase ^= 1u;
+                }
+            } else {
+                got = mbar_wait(&ctl->acc_full[acc], acc_phase, abort_flag);
+            }
             if (!got) {
                 *abort_flag = 1;
                 latch(a.status, kDevTimeout);
             }
+            if constexpr (kSplit && kLong) named_barrier_sync(1, kEpilogueThreads);  // sums that other warps send
             if constexpr (kSplit) {
                 tc_fence_after();
                 exchange(!got || *abort_flag);
@@ -304,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ctl->bias[et] = cb;
             named_barrier_sync(1, kEpilogueThreads);
             tc_fence_after();
-            const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * kTile;
+            const uint32_t t_row = tmem_base + kSums + (static_cast<uint32_t>(q * 32) << 16) + acc * kTile;
             for (int32_t c = 0; c < chunks; ++c) {
                 uint8_t *const slot = slot0 + (c & 1) * kSlotBytes, *const mine = slot + lane * row_bytes;
                 if (a.residual_tma) {
@@ -323,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_ld_32(t_row + at, r);
                     if (kGated) tmem_ld_32(t_row + kHalf + at, r2);
                     tmem_wait_ld();
-                    if (c == chunks - 1 && p == chunk_cols / 32 - 1) {  // the sums are out of the accumulator
+                    if (!kLong && c == chunks - 1 && p == chunk_cols / 32 - 1) {  // the sums are out of the accumulator
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive_cluster(peer_addr(&ctl->acc_empty[acc], leader));
@@ -390,8 +428,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) bulk_commit();
             }
             res_phase ^= 1u;
-            acc ^= 1u;
-            if (acc == 0) acc_phase ^= 1u;
+            if (!kLong) {
+                acc ^= 1u;
+                if (acc == 0) acc_phase ^= 1u;
+            }
         }
         if (lane == 0) bulk_wait_all();  // before the slots go away
     }
@@ -437,9 +477,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 using Kernel = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const CUtensorMap, const TileArgs);
 template <bool kSplit>
-Kernel kernel_of(bool fp8, bool gated) {
-    if (fp8) return gated ? linear_tiles_kernel<true, true, kSplit> : linear_tiles_kernel<true, false, kSplit>;
-    return gated ? linear_tiles_kernel<false, true, kSplit> : linear_tiles_kernel<false, false, kSplit>;
+Kernel kernel_of(bool fp8, bool gated, bool lng) {
+    if (fp8) return gated ? linear_tiles_kernel<true, true, kSplit, false> : linear_tiles_kernel<true, false, kSplit, false>;
+    if (lng) return gated ? linear_tiles_kernel<false, true, kSplit, true> : linear_tiles_kernel<false, false, kSplit, true>;
+    return gated ? linear_tiles_kernel<false, true, kSplit, false> : linear_tiles_kernel<false, false, kSplit, false>;
 }
 
 // Clusters of 4 and of 8 CTAs that fit on a device at once.
@@ -459,7 +500,7 @@ cudaError_t count_clusters(int dev) {
         cfg.attrs = attr;
         cfg.numAttrs = 1;
         int n = 0;
-        const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, kernel_of<true>(true, false), &cfg);
+        const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, kernel_of<true>(true, false, false), &cfg);
         if (e != cudaSuccess) return e;
         g_clusters[dev][i] = n;
     }
@@ -469,8 +510,8 @@ cudaError_t count_clusters(int dev) {
 }  // namespace
 
 cudaError_t prepare_linear_tiles() {
-    for (int i = 0; i < 8; ++i) {
-        const Kernel k = i < 4 ? kernel_of<false>(i & 1, i & 2) : kernel_of<true>(i & 1, i & 2);
+    for (int i = 0; i < 16; ++i) {
+        const Kernel k = i < 8 ? kernel_of<false>(i & 1, i & 2, i & 4) : kernel_of<true>(i & 1, i & 2, i & 4);
         const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
         if (e != cudaSuccess) return e;
     }
@@ -518,7 +559,8 @@ bool launch_linear_tiles(bool fp8, const LinearEpilogue &ep, const void *w, int6
     if (a.residual_tma && !encode_swizzled_rows(&mr, 2, ep.residual, M, rows, ep.ldr, chunk, 32)) return false;
     const unsigned cluster = 2u * static_cast<unsigned>(a.split);
     const dim3 grid(a.split > 1 ? cluster * static_cast<unsigned>(units) : 2u * static_cast<unsigned>(units < pairs ? units : pairs));
-    *err = launch_pdl_cluster(a.split > 1 ? kernel_of<true>(fp8, gated) : kernel_of<false>(fp8, gated), grid, dim3(kThreads),
+    const bool lng = !out_bf16 && a.num_kb > 2 * kSegment * a.split;  // 8-bit products are summed exactly enough
+    *err = launch_pdl_cluster(a.split > 1 ? kernel_of<true>(fp8, gated, lng) : kernel_of<false>(fp8, gated, lng), grid, dim3(kThreads),
                               cluster, kSmem, st, mx, mw, my, mr, a);
     return true;
 }

@@ -170,6 +170,21 @@ def test_linear(gb, rows, M, K, kind):
             assert torch.equal(again, got)
 
 
+@pytest.mark.parametrize("rows,M,K", [(300, 520, 16500), (1100, 5000, 4200), (700, 1300, 14336), (100, 300, 40000), (100, 20000, 4200)])
+@pytest.mark.parametrize("act", [None, "swiglu"])
+def test_long_sums_of_bf16_products_for_fp32_outputs(gb, rows, M, K, act):
+    """Over 128 rows 2048 products at a time are summed by the tensor core, which adds 16 to what it has and
+    truncates: 128 additions lose 2^-24 of the sum so far on average, 7.6e-6 of a segment's at most."""
+    w, x, b, r, _, _ = operands(gen(K), rows, M, K, BF16, act, True, True, gb)
+    y, tol = ref.linear(w, x, b, act, r, None, None, F32)
+    got = gb.linear(w, x, bias=b, act=act, residual=r, dtype=F32)
+    assert ((got.double() - y).abs() <= tol).all()
+    if rows > 128 and act is None:
+        z, _ = ref.linear(w, x, None, None, None, None, None, F32)
+        assert (gb.linear(w, x, dtype=F32).double() - z).norm() <= 7.6e-6 * z.norm()
+    assert torch.equal(gb.linear(w, x, bias=b, act=act, residual=r, dtype=F32), got)
+
+
 @pytest.mark.parametrize("rows", [1, 16, 40, 300])
 @pytest.mark.parametrize("kind", [BF16, E4M3], ids=["bf16", "e4m3"])
 @pytest.mark.parametrize("act", ["silu", "swiglu"])
