@@ -174,6 +174,40 @@ def load(path: Path | None = None):
     return _lib
 
 
+def _load_binding():
+    """csrc/binding.cpp's functions, bound to the loaded library, or None where it has not been built."""
+    path = LIB_PATH.parent / "_binding.so"
+    if not path.exists():
+        return None
+    import importlib.machinery
+    import importlib.util
+    loader = importlib.machinery.ExtensionFileLoader("_binding", str(path))
+    module = importlib.util.module_from_spec(importlib.util.spec_from_file_location("_binding", path, loader=loader))
+    loader.exec_module(module)
+    lib = load()
+    module.bind(*(ctypes.cast(getattr(lib, name), c_void_p).value for name in
+                  ("eagle_rms_norm", "eagle_quantize_rows", "eagle_linear", "eagle_kv4_append_rotary",
+                   "eagle_kv4_read")))
+    return module
+
+
+class _Short:
+    """Loads the binding when it is first asked for; without one, its functions decline every call."""
+
+    def __getattr__(self, name):
+        with _lock_binding:
+            if "module" not in self.__dict__:
+                self.__dict__["module"] = _load_binding()
+        module = self.__dict__["module"]
+        fn = getattr(module, name) if module is not None else (lambda *args: NotImplemented)
+        self.__dict__[name] = fn
+        return fn
+
+
+_lock_binding = threading.Lock()
+short = _Short()
+
+
 def check(code: int, where: str) -> None:
     if code != 0:
         raise EagleError(code, where)

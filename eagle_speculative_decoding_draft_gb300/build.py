@@ -25,6 +25,11 @@ SOURCES = ["api.cu", "gemm.cu", "linear.cu", "linear_few.cu", "linear_mid.cu", "
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
+# the short way from tensors to the library's calls (csrc/binding.cpp), a Python extension of this machine's torch
+BINDING = OUT_DIR / "_binding.so"
+BINDING_SRC = CSRC / "binding.cpp"
+
+
 def nvcc() -> str:
     cand = os.environ.get("CUDA_HOME", "/usr/local/cuda")
     p = Path(cand) / "bin" / "nvcc"
@@ -40,6 +45,35 @@ def _stale(lib: Path = LIB) -> bool:
     return any(d.stat().st_mtime > t for d in deps)
 
 
+def build_binding(force: bool = False) -> Path | None:
+    """Compiles the binding unless it is up to date.  A machine without torch's or Python's headers does without
+    it (a warning; the calls then take the long way through ctypes)."""
+    header = ROOT / "include" / "eagle_tree.h"
+    if not force and BINDING.exists() and all(BINDING.stat().st_mtime > p.stat().st_mtime for p in (BINDING_SRC, header, Path(__file__))):
+        return BINDING
+    import sysconfig
+
+    import torch
+    base = Path(torch.__file__).resolve().parent
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    OUT_DIR.mkdir(parents=True, exist_ok=True)
+    tmp = BINDING.with_suffix(f".so.tmp{os.getpid()}")
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f"-I{base / 'include'}", f"-I{base / 'include/torch/csrc/api/include'}", f"-I{cuda}/include",
+           f"-I{sysconfig.get_paths()['include']}", str(BINDING_SRC), "-o", str(tmp), f"-L{base / 'lib'}",
+           "-lc10", "-lc10_cuda", "-ltorch", "-ltorch_cpu", "-ltorch_python", f"-Wl,-rpath,{base / 'lib'}"]
+    try:
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        failed = r.stderr if r.returncode else ""
+    except OSError as e:
+        failed = str(e)
+    if failed:
+        sys.stderr.write("warning: the binding was not built:\n" + failed[-2000:] + "\n")
+        return None
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=(), checks: bool = False) -> Path:
     """Compiles the library (or, with checks, its checking variant) unless it is up to date;
     returns its path."""
@@ -47,6 +81,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), checks: bo
     if checks:
         extra_flags = (*extra_flags, "-DEAGLE_CHECKS")
     if not force and not _stale(lib):
+        build_binding()
         return lib
     out_dir.mkdir(parents=True, exist_ok=True)
     obj_dir = out_dir / "obj"
@@ -64,8 +99,10 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), checks: bo
             raise RuntimeError(f"nvcc failed on {src}")
         return obj
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        binding = ex.submit(build_binding, force)
         objs = list(ex.map(compile_one, SOURCES))
+        binding.result()
     tmp = lib.with_suffix(f".so.tmp{os.getpid()}")
     cmd = [nvcc(), *ARCH, "-shared", "-o", str(tmp), *map(str, objs)]
     r = subprocess.run(cmd, capture_output=True, text=True)

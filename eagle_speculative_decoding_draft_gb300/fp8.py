@@ -12,7 +12,7 @@ import ctypes
 import torch
 
 from . import _lib
-from ._lib import EAGLE_BF16, EAGLE_E4M3, EAGLE_F32, check
+from ._lib import EAGLE_BF16, EAGLE_E4M3, EAGLE_F32, check, short
 from .engine import _need
 
 _BF16, _E4M3, _F32, _U8 = torch.bfloat16, torch.float8_e4m3fn, torch.float32, torch.uint8
@@ -81,6 +81,10 @@ def _new_rows(like, rows, cols, dtype, step):
 def quantize_rows(x, stream=None):
     """The rows of x [rows][cols] bf16 as 8-bit rows: (codes [rows][cols] float8_e4m3fn, scale [rows] fp32),
     codes times scale standing for x."""
+    if stream is None:
+        made = short.quantize_rows(x)
+        if made is not NotImplemented:
+            return made
     index = _device(x, "x")
     rows, cols, ldx = _rows(x, "x", _BF16, index)
     away = _elsewhere(index, stream)
@@ -99,6 +103,10 @@ def rms_norm(x, weight, eps: float = 1e-6, residual=None, dtype=torch.bfloat16, 
     [rows][cols] bf16, weight [cols] bf16.  Returns (y, scale, h): y in bf16 (scale None), or with
     dtype=torch.float8_e4m3fn as codes with a scale [rows] fp32; h in bf16 where there is a residual, else
     None."""
+    if stream is None and (dtype is _E4M3 or dtype is _BF16):
+        made = short.rms_norm(x, weight, eps, residual, dtype is _E4M3)
+        if made is not NotImplemented:
+            return made
     index = _device(x, "x")
     rows, cols, ldx = _rows(x, "x", _BF16, index)
     p_w = _vector(weight, "weight", _BF16, index, cols)
@@ -149,12 +157,18 @@ def linear(w, x, bias=None, act=None, residual=None, w_scale=None, x_scale=None,
     "silu", "gelu" or "swiglu" (w: gate rows, then as many up rows; y = silu(gate) up); residual [rows][out]
     bf16.  Returns y [rows][out] of dtype (bf16 or fp32), or fills out, which may be the residual.  workspace:
     one of ``linear_workspace``, or None; calls that may overlap need one each."""
+    code = _ACTS.get(act)
+    if stream is None and code is not None:
+        to = dtype if out is None else out.dtype
+        if to is _BF16 or to is _F32:
+            made = short.linear(w, x, bias, code, residual, w_scale, x_scale, to is _F32, out, workspace)
+            if made is not NotImplemented:
+                return made
     index = _device(w, "w")
     kind = w.dtype
     fp8 = kind is _E4M3
     if not fp8 and kind is not _BF16:
         raise TypeError(f"w must be torch.bfloat16 or torch.float8_e4m3fn, got {kind}")
-    code = _ACTS.get(act)
     if code is None:
         raise ValueError(f"act must be one of None, 'silu', 'gelu', 'swiglu', got {act!r}")
     features, k, ldw = _rows(w, "w", kind, index)

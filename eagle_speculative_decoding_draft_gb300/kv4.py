@@ -12,7 +12,7 @@ import ctypes
 import torch
 
 from . import _lib
-from ._lib import EAGLE_BF16, EAGLE_F32, check
+from ._lib import EAGLE_BF16, EAGLE_F32, check, short
 from .engine import _need
 
 _BF16, _I32, _U8 = torch.bfloat16, torch.int32, torch.uint8
@@ -112,6 +112,7 @@ class KV4Cache:
         self._c.pages, self._c.table, self._c.lengths = pages.data_ptr(), self._table.data_ptr(), self._lengths.data_ptr()
         self._status_ptr = self._status.data_ptr()
         self._plans = {}
+        self._short = (ctypes.addressof(self._c), batch, kv_heads, head_dim, self._index, self._status_ptr)
 
     pages = property(lambda self: self._pages, doc="The page pool, uint8.")
     table = property(lambda self: self._table, doc="Pages of each request, [batch][max_pages] int32.")
@@ -174,6 +175,10 @@ class KV4Cache:
         start[b] + j; rows that `select` names need positions).  k and v come as a projection leaves
         them.  With the queries q [batch][rows][heads][head_dim] of the same rows they are turned too
         and returned (in out, if given, which may be a contiguous q itself)."""
+        if stream is None and out is None:
+            made = short.append_rotary(self._short, k, v, q, rope_theta, positions, select, count, start)
+            if made is not NotImplemented:
+                return made
         device, index = self.device, self._index
         ld = _packed(k, v, index)
         if ld is None or k.shape[0] != self.batch or k.shape[2:] != self._tail:
@@ -220,6 +225,9 @@ class KV4Cache:
         [batch][rows][kv_heads][head_dim] of `dtype` (bf16 or fp32).  out = (k, v) receives them (its
         shape gives rows); rows behind a request's length are left as they are (0 in fresh
         tensors).  rows defaults to the capacity."""
+        if stream is None and out is not None and len(out) == 2 and (rows is None or out[0].shape[1] == rows):
+            if short.kv4_read(self._short, out[0], out[1], start) is True:
+                return out[0], out[1]
         p_start = _ints(start, "start", self.device, (self.batch,))
         with self._on(stream):
             if out is None:

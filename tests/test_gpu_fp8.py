@@ -342,3 +342,43 @@ def test_refusals_of_the_binding(gb):
         gb.rms_norm(x, torch.ones(32, device="cuda", dtype=BF16), -1.0)
     with pytest.raises(Exception, match="UNSUPPORTED"):
         gb.quantize_rows(torch.zeros(1, 32776, device="cuda", dtype=BF16))
+
+
+def test_the_short_and_the_long_way_are_the_same_call(gb, monkeypatch):
+    """The compiled binding takes what is usual and declines the rest; without it every call goes through
+    ctypes."""
+    from eagle_speculative_decoding_draft_gb300 import _lib, fp8, kv4
+    from test_gpu_kv4 import make_cache
+    g = gen(21)
+    x, r = wide(g, 20, 100, 112), wide(g, 20, 100, 104)
+    weight = torch.ones(100, device="cuda", dtype=BF16)
+    w, w_scale = gb.quantize_rows(wide(g, 64, 100, 104))
+    qkv = torch.randn(2, 5, 8, 64, generator=g, device="cuda").to(BF16)
+
+    def calls():
+        codes, scale = gb.quantize_rows(x)
+        y, ys, total = gb.rms_norm(x, weight, 1e-5, residual=r, dtype=E4M3)
+        y2, none, h = gb.rms_norm(x, weight, 1e-5)
+        assert none is None and h is None
+        z = gb.linear(w, codes, act="swiglu", w_scale=w_scale, x_scale=scale, dtype=F32)
+        out = torch.empty(20, 64, device="cuda", dtype=BF16)
+        assert gb.linear(w, codes, w_scale=w_scale, x_scale=scale, out=out) is out
+        c = make_cache(2, 2, 64, 32, 16, fill=0)
+        q = c.append_rotary(qkv[:, :, 4:6], qkv[:, :, 6:], q=qkv[:, :, :4])
+        assert c.append_rotary(qkv[:, :, 4:6], qkv[:, :, 6:]) is None
+        back = c.read(out=(torch.zeros(2, 32, 2, 64, device="cuda"), torch.zeros(2, 32, 2, 64, device="cuda")))
+        return [*back, codes.view(torch.uint8), scale, y.view(torch.uint8), ys, total, y2, z, out, q, c.pages, c.lengths]
+
+    assert _lib.short.quantize_rows(x) is not NotImplemented
+    one = calls()
+
+    class Declines:
+        def __getattr__(self, name):
+            return lambda *args: NotImplemented
+
+    for module in (fp8, kv4):
+        monkeypatch.setattr(module, "short", Declines())
+    for a, b in zip(one, calls()):
+        assert a.dtype is b.dtype and a.stride() == b.stride() and torch.equal(a, b)
+    for args in [(x.float(),), (x.cpu(),), (x[None],), (x.t(),), (None,)]:
+        assert _lib.short.quantize_rows(*args) is NotImplemented
