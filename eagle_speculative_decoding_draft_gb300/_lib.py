@@ -182,8 +182,11 @@ def _load_binding():
     import importlib.machinery
     import importlib.util
     loader = importlib.machinery.ExtensionFileLoader("_binding", str(path))
-    module = importlib.util.module_from_spec(importlib.util.spec_from_file_location("_binding", path, loader=loader))
-    loader.exec_module(module)
+    try:
+        module = importlib.util.module_from_spec(importlib.util.spec_from_file_location("_binding", path, loader=loader))
+        loader.exec_module(module)
+    except ImportError:  # built for another torch
+        return None
     lib = load()
     module.bind(*(ctypes.cast(getattr(lib, name), c_void_p).value for name in
                   ("eagle_rms_norm", "eagle_quantize_rows", "eagle_linear", "eagle_kv4_append_rotary",

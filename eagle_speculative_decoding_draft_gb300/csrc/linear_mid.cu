@@ -59,7 +59,6 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int32_t row0 = static_cast<int32_t>(blockIdx.y) * n;
     const int32_t kb_begin = a.num_kb * part / S, kb_end = a.num_kb * (part + 1) / S;
 
-    pdl_launch_dependents();
     if (threadIdx.x == 0) {
         prefetch_tensormap(&tmap_w);
         prefetch_tensormap(&tmap_x);
@@ -79,6 +78,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    // behind the allocation: a kernel that begins beside this one and takes all of the SM's tensor memory would
+    // wait for this grid's end, and a CTA that has none yet for that kernel's
+    pdl_launch_dependents();
     const uint32_t tmem_base = ctl->tmem_base;
     uint32_t issued = 0, issued_parity = 0;  // the copying thread's, for unwinding
 
