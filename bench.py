@@ -39,6 +39,7 @@ FALLBACK_HBM_GBS = 6800.0
 FALLBACK_BF16_TFLOPS_SUSTAINED = 1700.0
 TRAFFIC_FILE = ROOT / "profiles" / "gemm_traffic.json"
 KERNEL_SOURCES = ["eagle_speculative_decoding_draft_gb300/csrc/gemm.cu",
+                  "eagle_speculative_decoding_draft_gb300/csrc/gemm.cuh",
                   "eagle_speculative_decoding_draft_gb300/csrc/common.cuh"]
 N_INPUT_SETS = 4
 PROFILE_EVERY = 16
@@ -823,7 +824,7 @@ def measure(args, w, dev, ranks, rank, local, headline):
         "step_frac_of_floor": floor["us"] / (1e3 * ms_max / K),
         "step_floor_us_with_verify_scan": floor["us_with_verify_scan"],
         "roofline": None if gr is None else {
-            "bound": "hbm", "kernel": "linear_bf16_tc_kernel (FC and LM head)",
+            "bound": "hbm", "kernel": "linear_tc_kernel (FC and LM head)",
             "achieved": gr["achieved"], "peak": peak, "unit": "GB/s", "frac": gr["frac"],
             "peak_source": f"{peak_kind} hbm_gbs (of {peak_kind})",
             "traffic": recorded_traffic(w.name),
