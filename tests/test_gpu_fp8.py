@@ -382,3 +382,94 @@ def test_the_short_and_the_long_way_are_the_same_call(gb, monkeypatch):
         assert a.dtype is b.dtype and a.stride() == b.stride() and torch.equal(a, b)
     for args in [(x.float(),), (x.cpu(),), (x[None],), (x.t(),), (None,)]:
         assert _lib.short.quantize_rows(*args) is NotImplemented
+
+
+def test_scales_and_biases_that_start_anywhere(gb):
+    """Vectors that are slices: aligned to their elements alone."""
+    for rows in (5, 60, 300):
+        w, x, b, r, w_scale, x_scale = operands(gen(rows), rows, 260, 512, E4M3, "swiglu", True, True, gb)
+        want = gb.linear(w, x, bias=b, act="swiglu", residual=r, w_scale=w_scale, x_scale=x_scale)
+        b, w_scale, x_scale = (torch.cat([t[:1], t])[1:] for t in (b, w_scale, x_scale))
+        assert w_scale.data_ptr() % 16 == 4 and b.data_ptr() % 16 == 2
+        assert torch.equal(gb.linear(w, x, bias=b, act="swiglu", residual=r, w_scale=w_scale, x_scale=x_scale), want)
+
+
+def test_products_of_two_streams_at_once(gb):
+    """Clusters, pairs and few rows side by side: each stream's results are those of a run by itself."""
+    shapes = [(61, 2048, 4096, "swiglu"), (300, 1024, 8192, "silu"), (8, 4096, 2048, None), (120, 700, 5000, "gelu"), (1500, 2048, 1024, "swiglu")]
+    work = []
+    for i, (rows, M, K, act) in enumerate(shapes):
+        w, x, b, r, ws, xs = operands(gen(i), rows, M, K, E4M3, act, True, True, gb)
+        work.append(dict(w=w, x=x, bias=b, act=act, residual=r, w_scale=ws, x_scale=xs))
+    want = [gb.linear(**c) for c in work]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream(), torch.cuda.Stream()]
+    outs = {}
+    for turn in range(6):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                for j in range(len(work)):
+                    k = (j + i + turn) % len(work)
+                    outs[i, turn, k] = gb.linear(**work[k])
+    torch.cuda.synchronize()
+    for (i, turn, k), out in outs.items():
+        assert torch.equal(out, want[k]), (i, turn, k)
+
+
+def test_offsets_beyond_32_bits(gb):
+    """Rows whose elements lie over 2^31 places from the first."""
+    n = 140000
+    x = torch.zeros(n, 16384, device="cuda", dtype=BF16)
+    x[-3:] = torch.randn(3, 16384, generator=gen(0), device="cuda").to(BF16)
+    x[1] = x[-1]
+    codes, scale = gb.quantize_rows(x)
+    few, few_scale = gb.quantize_rows(x[-3:].clone())
+    assert torch.equal(codes[-3:].view(torch.uint8), few.view(torch.uint8)) and torch.equal(scale[-3:], few_scale)
+    assert not codes[2:-3].view(torch.uint8).any()
+    del codes
+    y, _, h = gb.rms_norm(x, torch.ones(16384, device="cuda", dtype=BF16), 1e-5, residual=x)
+    few_y, _, few_h = gb.rms_norm(x[-3:].clone(), torch.ones(16384, device="cuda", dtype=BF16), 1e-5, residual=x[-3:].clone())
+    assert torch.equal(y[-3:], few_y) and torch.equal(h[-3:], few_h)
+    del x, y, h
+    # a deep product, and a wide one with its residual
+    x = torch.zeros(32768, 66000, device="cuda", dtype=BF16)
+    x[-2:] = torch.randn(2, 66000, generator=gen(1), device="cuda").to(BF16)
+    w = (torch.randn(64, 66000, generator=gen(2), device="cuda") / 256).to(BF16)
+    got = gb.linear(w, x)
+    y, tol = ref.linear(w, x[-2:], None, None, None, None, None, BF16)
+    assert ((got[-2:].double() - y).abs() <= tol).all() and not got[:-2].any()
+    del x
+    w = (torch.randn(66000, 64, generator=gen(3), device="cuda") / 8).to(BF16)
+    x = torch.randn(32768, 64, generator=gen(4), device="cuda").to(BF16)
+    r = torch.zeros(32768, 66000, device="cuda", dtype=BF16)
+    r[-2:] = 3.0
+    for act in (None, "swiglu"):
+        res = r if act is None else r[:, :33000]
+        got = gb.linear(w, x, act=act, residual=res)
+        for at in (slice(0, 2), slice(32766, 32768)):
+            y, tol = ref.linear(w, x[at], None, act, res[at], None, None, BF16)
+            assert ((got[at].double() - y).abs() <= tol).all(), (act, at)
+
+
+@pytest.mark.parametrize("rows", [3, 40, 200])
+def test_graphs_of_products_replayed_by_turns(gb, rows):
+    """Two captured graphs of the same operands, other outputs, replayed on two streams."""
+    w, x, b, r, ws, xs = operands(gen(rows), rows, 512, 2048, E4M3, "silu", True, True, gb)
+    call = lambda: gb.linear(w, x, bias=b, act="silu", residual=r, w_scale=ws, x_scale=xs)  # noqa: E731
+    want = call()
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append([call() for _ in range(3)])
+        graphs.append(g)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(5):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for some in outs:
+        for o in some:
+            assert torch.equal(o, want)
