@@ -41,6 +41,13 @@ __device__ __forceinline__ void tmem_ld_4(uint32_t taddr, uint32_t (&r)[4]) {
                  : "memory");
 }
 
+__device__ __forceinline__ void tmem_ld_8(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr)
+                 : "memory");
+}
+
 // A cluster of a.split CTAs a (tile, chunk of n_tile rows): blockIdx.x / split the tile, blockIdx.y the chunk.
 template <class Op>
 __global__ void __launch_bounds__(kThreads, 2)
@@ -203,6 +210,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                     __syncwarp();
                     if constexpr (C == 16)
                         tmem_ld_16(t_row + static_cast<uint32_t>(col), to);
+                    else if constexpr (C == 8)
+                        tmem_ld_8(t_row + static_cast<uint32_t>(col), to);
                     else
                         tmem_ld_4(t_row + static_cast<uint32_t>(col), to);
                     tmem_wait_ld();
@@ -233,6 +242,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         };
         if (share % 16 == 0)
             rows(std::integral_constant<int, 16>{});
+        else if (share % 8 == 0)
+            rows(std::integral_constant<int, 8>{});
         else
             rows(std::integral_constant<int, 4>{});
     }
@@ -301,9 +312,11 @@ bool launch_linear_mid(bool fp8, const LinearEpilogue &ep, const void *w, int64_
     const int32_t chunks = (rows + a.n_tile - 1) / a.n_tile;
     // as many parts as two CTAs an SM leave room for at once (61 rows, 4096 -> 4096 in 8 bits: 15.7, 11.4, 9.1 and
     // 9.5 us with 1, 2, 4 and 8; 4096 -> 6144: 16.1, 11.7, 10.3 and, in two waves, 16.4; 4096 -> 2 x 11008: 19.9 with
-    // one, 26 with two), of at least two k-blocks
+    // one, 26 with two), of at least two k-blocks, and of eight where eight parts exchange the sums of more than 32 rows
+    // (1024 -> 1024 in bf16, 61 and 128 rows: 5.9 and 8.2 us with four, 6.5 and 9.3 with eight)
+    const int32_t most = a.n_tile > 32 && a.num_kb < 64 ? 4 : 8;
     m.split = 1;
-    while (m.split < 8 && static_cast<int64_t>(a.num_tiles) * chunks * m.split <= sms && a.num_kb >= 4 * m.split) m.split *= 2;
+    while (m.split < most && static_cast<int64_t>(a.num_tiles) * chunks * m.split <= sms && a.num_kb >= 4 * m.split) m.split *= 2;
     // Long sums of bf16 products in two halves where fp32 goes out: the accumulator truncates (linear_tiles.cu)
     m.halves = !fp8 && !out_bf16 && a.num_kb / m.split > 64 ? 2 : 1;
     m.tmem_cols = 32;
