@@ -7,8 +7,9 @@
 // one CTA's beginning and end fall into the other's copies, and the parts' sums meet through the cluster's
 // shared memory, each CTA finishing its share of the rows.  No partial sum goes through memory.  Bound by the
 // memory and, towards 128 rows, by what the SMs take from the L2 (a row of x goes to every tile): 61 rows,
-// 4096 -> 2 x 11008 in 8 bits 19.9 us (0.68 of the measured copy rate; 25.9 through gemm.cuh's stream), 4096 ->
-// 4096 9.5 us (13.8).
+// 4096 -> 2 x 11008 in 8 bits 18.4 us (0.74 of the measured copy rate; 25.9 through gemm.cuh's stream), 4096 ->
+// 4096 8.4 us (13.8).  Two epilogue warps an accumulator quarter: a warp alone on its scheduler takes twice as
+// long over a share (128 rows, 4096 -> 4096: 13.4 -> 11.5 us).
 #include <algorithm>
 #include <type_traits>
 
@@ -20,6 +21,7 @@ namespace {
 
 constexpr int kMidStages = 6;  // at most
 constexpr size_t kMidSmem = 113 * 1024;
+constexpr int kMidThreads = 64 + 256;  // warp 0: copies, warp 1: MMAs, then two warps an accumulator quarter
 
 struct MidCtl {
     uint64_t full[kMidStages], empty[kMidStages], acc_full, drain;
@@ -50,7 +52,7 @@ __device__ __forceinline__ void tmem_ld_8(uint32_t taddr, uint32_t (&r)[8]) {
 
 // A cluster of a.split CTAs a (tile, chunk of n_tile rows): blockIdx.x / split the tile, blockIdx.y the chunk.
 template <class Op>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kMidThreads, 2)
     linear_mid_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_x, const MidArgs m) {
     constexpr int32_t BK = k_block<Op>();
     const LinearArgs &a = m.l;
@@ -166,13 +168,13 @@ __global__ void __launch_bounds__(kThreads, 2)
     // The parts' sums: CTA `to` of the cluster finishes rows to * share .. of the chunk, and finds those that
     // the others send it, from each [rows / 4][128 rows of w][4], where its copies are over.
     const int32_t share = n / S;
-    const int32_t q = warp & 3, ml = q * 32 + lane;
+    const int32_t q = warp & 3, turn = (warp - 2) >> 2, ml = q * 32 + lane;
     const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
     const bool fine = !__any_sync(0xffffffffu, *abort_flag != 0);
     if (S > 1) {
         cluster_sync();
         if (warp >= 2 && fine) {
-            for (int32_t c = 0; c < n; c += 32) {
+            for (int32_t c = 32 * turn; c < n; c += 64) {
                 uint32_t r[32];
                 __syncwarp();
                 tmem_ld_32(t_row + static_cast<uint32_t>(c), r);
@@ -202,7 +204,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         const int32_t end = min(a.rows - row0, n);  // rows of the chunk
         auto rows = [&](auto count) {  // as many at a time
             constexpr int C = decltype(count)::value;
-            for (int32_t c = 0; c < share; c += C) {
+            for (int32_t c = C * turn; c < share; c += 2 * C) {
                 const int32_t n0 = part * share + c;
                 if (n0 >= end) break;
                 uint32_t r[C];
@@ -240,9 +242,9 @@ __global__ void __launch_bounds__(kThreads, 2)
                 store_rows<Op>(a, col, row0, n0, end, v);
             }
         };
-        if (share % 16 == 0)
+        if (share % 32 == 0)
             rows(std::integral_constant<int, 16>{});
-        else if (share % 8 == 0)
+        else if (share % 16 == 0)
             rows(std::integral_constant<int, 8>{});
         else
             rows(std::integral_constant<int, 4>{});
@@ -326,7 +328,7 @@ bool launch_linear_mid(bool fp8, const LinearEpilogue &ep, const void *w, int64_
     if (!encode_swizzled_rows(&mx, es, x, K, rows, ldx, box, a.n_tile)) return false;
     const size_t smem = 1024 + a.stages * stage + sizeof(MidCtl);
     *err = launch_pdl_cluster(kernel_of(fp8, gated), dim3(static_cast<unsigned>(a.num_tiles * m.split), static_cast<unsigned>(chunks)),
-                              dim3(kThreads), static_cast<unsigned>(m.split), smem, st, mw, mx, m);
+                              dim3(kMidThreads), static_cast<unsigned>(m.split), smem, st, mw, mx, m);
     return true;
 }
 
