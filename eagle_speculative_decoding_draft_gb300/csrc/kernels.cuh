@@ -160,7 +160,7 @@ cudaError_t launch_linear_few(bool fp8, const LinearEpilogue &ep, const void *w,
                               int64_t ldx, int32_t rows, const void *bias, void *out, int64_t ldo, bool out_bf16,
                               int32_t sms, cudaStream_t st);
 constexpr int kLinearFewRows = 16;
-constexpr int kLinearMidRows = 128;  // above: linear_tiles.cu, between: gemm.cuh's kernels
+constexpr int kLinearMidRows = 128;  // above: linear_tiles.cu, but where linear_mid.cu has few tiles
 // linear_mid.cu: the same product for 17 to 128 rows (more in chunks of 128), without a workspace.  False as
 // launch_linear_tiles.
 bool launch_linear_mid(bool fp8, const LinearEpilogue &ep, const void *w, int64_t ldw, int32_t M, int32_t K, const void *x,

@@ -71,13 +71,19 @@ cudaError_t launch_linear(bool fp8, const LinearEpilogue &ep, const void *w, int
     cudaError_t e = prepare_linear_forms();
     if (e != cudaSuccess) return e;
     // Over 128 rows the tensor cores bound the product, or nearly so: whole tiles of both operands (256 rows,
-    // 4096 -> 2 x 11008 in 8 bits: 30 us, and 43 with the weights past 128 rows at a time; 128 rows: 29 and 25).
+    // 4096 -> 2 x 11008 in 8 bits: 30 us, and 43 with the weights past 128 rows at a time; 128 rows: 29 and 22).  But
+    // where tiles of 128 rows of either leave room for four parts of K each, those are quicker still (256 rows, 4096
+    // -> 4096 in 8 bits: 12.2 us against 13.1, 14336 -> 4096 21.8 against 25.4, in bf16 34 against 42; 1024 rows,
+    // 14336 -> 1024: 20 against 24; but 384 rows, 4096 -> 4096, three parts' room: 15.5 against 14.2).
     // Outputs that no bulk store takes go through the weights' stream where there is a workspace for it.
-    if (rows > kLinearMidRows) {
+    const int32_t cols = ep.act == kActSwiglu ? 64 : 128;
+    const int64_t small = static_cast<int64_t>((M + cols - 1) / cols) * ((rows + 127) / 128);
+    const bool mid = rows <= kLinearMidRows || (2 * small <= sms && static_cast<int64_t>(K) * (fp8 ? 1 : 2) >= 1024);
+    if (!mid) {
         const int32_t pairs = linear_pair_workers(sms);
         if (pairs > 0 && launch_linear_tiles(fp8, ep, w, ldw, M, K, x, ldx, rows, bias, y, ldy, y_bf16, status, pairs, st, &e)) return e;
     }
-    if (rows <= kLinearMidRows || !ws || (!fp8 && !y_bf16 && K > 4096))  // (the stream has no parts for long sums)
+    if (mid || !ws || (!fp8 && !y_bf16 && K > 4096))  // (the stream has no parts for long sums)
         return launch_linear_mid(fp8, ep, w, ldw, M, K, x, ldx, rows, bias, y, ldy, y_bf16, status, sms, st, &e) ? e : cudaErrorInvalidValue;
     LinearPlan p;
     if (!plan_linear(&p, fp8, ep, w, ldw, M, K, x, ldx, rows, bias, y, ldy, y_bf16,

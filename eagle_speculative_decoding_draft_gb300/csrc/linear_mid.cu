@@ -300,7 +300,8 @@ bool launch_linear_mid(bool fp8, const LinearEpilogue &ep, const void *w, int64_
     a.M = M;
     a.K = K;
     a.rows = rows;
-    a.n_tile = std::min((rows + 31) / 32 * 32, 128);  // shares of 4 rows at least
+    const int32_t chunks = (rows + 127) / 128;
+    a.n_tile = ((rows + chunks - 1) / chunks + 31) / 32 * 32;  // shares of 4 rows at least
     a.num_kb = (K + box - 1) / box;
     a.num_tiles = (M + cols - 1) / cols;
     const size_t stage = kABytes + static_cast<size_t>(a.n_tile) * 128;
@@ -311,7 +312,6 @@ bool launch_linear_mid(bool fp8, const LinearEpilogue &ep, const void *w, int64_
     a.out_bf16 = out_bf16;
     a.ep = ep;
     a.status = status;
-    const int32_t chunks = (rows + a.n_tile - 1) / a.n_tile;
     // as many parts as two CTAs an SM leave room for at once (61 rows, 4096 -> 4096 in 8 bits: 15.7, 11.4, 9.1 and
     // 9.5 us with 1, 2, 4 and 8; 4096 -> 6144: 16.1, 11.7, 10.3 and, in two waves, 16.4; 4096 -> 2 x 11008: 19.9 with
     // one, 26 with two), of at least two k-blocks, and of eight where eight parts exchange the sums of more than 32 rows

@@ -43,7 +43,7 @@ constexpr uint32_t kFull = 0xffffffffu;
 
 struct TileArgs {
     int32_t rows, M, num_kb;
-    int32_t row_tiles, col_tiles, group, split;
+    int32_t row_tiles, col_tiles, group;
     LinearEpilogue ep;
     const __nv_bfloat16 *bias;
     int32_t out_bf16, residual_tma;
@@ -70,8 +70,8 @@ __device__ __forceinline__ void tile_of(const TileArgs &a, int32_t u, int32_t &r
     rt = first + in - ct * gr;
 }
 
-// kSplit: a cluster of `split` pairs forms one tile, each from its part of K, and each finishes its part of
-// the tile's columns.
+// kSplit: a cluster of two pairs forms one tile, each from its half of K, and each finishes half of the tile's
+// columns.
 // kLong: the tensor core's accumulator truncates, so a long sum of bf16 products is too small by a part that
 // grows with its length (14336 products 1.7e-5, more than an fp32 output should lose): the sums of kSegment
 // k-blocks at a time are added up, rounded to nearest, in the accumulator's other half (2e-6).
@@ -94,7 +94,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     const int32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // workers: pairs, or the clusters that share a tile; `part` of the tile's K is this pair's
-    const int32_t split = kSplit ? a.split : 1, rank = blockIdx.x & 1;
+    constexpr int32_t split = kSplit ? 2 : 1;
+    const int32_t rank = blockIdx.x & 1;
     const int32_t pairs = static_cast<int32_t>(gridDim.x >> 1) / split, pair = static_cast<int32_t>(blockIdx.x >> 1) / split;
     const int32_t part = kSplit ? static_cast<int32_t>(blockIdx.x >> 1) - pair * split : 0;
     const uint32_t leader = 2u * part;  // cluster rank of this pair's even CTA
@@ -220,59 +221,46 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---------------- epilogue: warps 2..9, TMEM lane quarter = warp % 4, columns in two halves ----------------
         pdl_wait();
         const int32_t ew = warp - 2, q = warp & 3, side = ew >> 2, et = threadIdx.x - 64;
-        // this CTA's outputs of a row (all of the tile's, or its part), and those of one warp: halves of them, or
-        // where that leaves fewer than 32, all in the first four warps
-        const int32_t slice = kCols / split, span = max(32, slice / 2);
-        const int32_t chunk_cols = a.out_bf16 ? min(span, 64) : 32, chunks = side * span < slice ? span / chunk_cols : 0;
+        // this CTA's outputs of a row (all of the tile's, or its half), and those of one warp
+        constexpr int32_t slice = kCols / split, span = slice / 2;
+        const int32_t chunk_cols = a.out_bf16 ? min(span, 64) : 32, chunks = span / chunk_cols;
         const int32_t row_bytes = a.out_bf16 ? 2 * chunk_cols : 128;
         uint8_t *const slot0 = slots + ew * 2 * kSlotBytes;
         uint32_t acc = 0, acc_phase = 0, res_phase = 0;
         // kSplit: the pairs' sums of a CTA's columns meet in its shared memory, where the copies are over: from
-        // each other pair [accumulator columns of the slice / 4][128 rows][4].  The two cluster barriers are met
+        // the other pair [accumulator columns of the slice / 4][128 rows][4].  The two cluster barriers are met
         // by every thread of the cluster (the other warps', behind their work).
-        const int32_t slice_cols = kTile / split, half_slice = slice_cols / 2;
+        constexpr int32_t half_slice = kTile / split / 2;
         auto exchange = [&](bool skip) {
             __syncwarp();
             cluster_sync();  // every CTA's copies and products are over
             if (!__any_sync(kFull, skip)) {
                 const uint32_t t_row = tmem_base + kSums + (static_cast<uint32_t>(q * 32) << 16);
-                for (int32_t to = 0; to < split; ++to) {
-                    if (to == part) continue;
-                    const uint32_t at = peer_addr(ring, 2u * to + rank) +
-                                        static_cast<uint32_t>(((part < to ? part : part - 1) * slice_cols + side * half_slice) * 512 + (q * 32 + lane) * 16);
-                    const int32_t col = kGated ? side * kHalf + to * half_slice : to * slice_cols + side * half_slice;
-                    for (int32_t c = 0; c < half_slice; c += 32) {
-                        uint32_t r[32];
-                        __syncwarp();
-                        tmem_ld_32(t_row + col + c, r);
-                        tmem_wait_ld();
+                const int32_t to = part ^ 1;
+                const uint32_t at = peer_addr(ring, 2u * to + rank) + static_cast<uint32_t>(side * half_slice * 512 + (q * 32 + lane) * 16);
+                const int32_t col = kGated ? side * kHalf + to * half_slice : (2 * to + side) * half_slice;
+                for (int32_t c = 0; c < half_slice; c += 32) {
+                    uint32_t r[32];
+                    __syncwarp();
+                    tmem_ld_32(t_row + col + c, r);
+                    tmem_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) st_peer_v4(at + static_cast<uint32_t>(c + 4 * i) * 512, r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
-                    }
+                    for (int i = 0; i < 8; ++i) st_peer_v4(at + static_cast<uint32_t>(c + 4 * i) * 512, r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
                 }
             }
             __syncwarp();
             cluster_sync();  // every part is here
         };
-        // the tile's parts of columns c .. c + 31 of the slice, added up in their order
+        // the other pair's sums of columns c .. c + 31 of the slice, added (a sum of two: in either order the same)
         auto add_parts = [&](uint32_t (&r)[32], int32_t c) {
-            float sum[32];
-            for (int32_t from = 0; from < split; ++from) {
-                const float4 *src = reinterpret_cast<const float4 *>(ring + ((from < part ? from : from - 1) * slice_cols + c) * 512) + q * 32 + lane;
+            const float4 *src = reinterpret_cast<const float4 *>(ring + c * 512) + q * 32 + lane;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    float4 x;
-                    if (from == part)
-                        x = make_float4(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1]), __uint_as_float(r[4 * i + 2]), __uint_as_float(r[4 * i + 3]));
-                    else
-                        x = src[i * 128];
-                    const float y[4] = {x.x, x.y, x.z, x.w};
+            for (int i = 0; i < 8; ++i) {
+                const float4 x = src[i * 128];
+                const float y[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) sum[4 * i + k] = from == 0 ? y[k] : sum[4 * i + k] + y[k];
-                }
+                for (int k = 0; k < 4; ++k) r[4 * i + k] = __float_as_uint(__uint_as_float(r[4 * i + k]) + y[k]);
             }
-#pragma unroll
-            for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(sum[j]);
         };
         for (int32_t u = pair; u < units; u += pairs) {
             int32_t rt, ct;
@@ -489,29 +477,25 @@ Kernel kernel_of(bool fp8, bool gated, bool lng) {
     return gated ? linear_tiles_kernel<false, true, kSplit, false> : linear_tiles_kernel<false, false, kSplit, false>;
 }
 
-// Clusters of 4 and of 8 CTAs that fit on a device at once.
+// Clusters of 4 CTAs that fit on a device at once; 0 where that is not known: tiles are not shared then.
 std::mutex g_mu;
-int32_t g_clusters[64][2];
+int32_t g_clusters[64];
 
-void count_clusters(int dev) {
-    for (int i = 0; i < 2; ++i) {
-        cudaLaunchConfig_t cfg = {};
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = 4u << i;
-        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-        cfg.gridDim = dim3((4u << i) * 32);
-        cfg.blockDim = dim3(kThreads);
-        cfg.dynamicSmemBytes = kSmem;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        int n = 0;
-        if (cudaOccupancyMaxActiveClusters(&n, kernel_of<true>(true, false, false), &cfg) != cudaSuccess) {
-            cudaGetLastError();
-            n = 0;  // none: tiles are not shared then
-        }
-        g_clusters[dev][i] = n;
-    }
+int32_t count_clusters() {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 4;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(128);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel_of<true>(true, false, false), &cfg) == cudaSuccess) return n;
+    cudaGetLastError();
+    return 0;
 }
 
 }  // namespace
@@ -527,7 +511,7 @@ cudaError_t prepare_linear_tiles() {
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     std::lock_guard<std::mutex> lock(g_mu);
-    count_clusters(dev);
+    g_clusters[dev] = count_clusters();
     return cudaSuccess;
 }
 
@@ -554,13 +538,10 @@ bool launch_linear_tiles(bool fp8, const LinearEpilogue &ep, const void *w, int6
     *err = cudaGetDevice(&dev);
     if (*err != cudaSuccess) return true;
     const int64_t units = static_cast<int64_t>(a.row_tiles) * a.col_tiles;
-    // Fewer tiles than pairs: two or four pairs to a tile, where the clusters fit on the device at once (36 of 4
-    // CTAs and 15 of 8 on 152 SMs) and each part is long enough (512 rows, 4096 x 4096: 15.3 -> 14.2 us in 8 bits,
-    // 24 -> 19 in bf16; 14336 -> 4096: 38 -> 27, 70 -> 44)
-    a.split = 1;
-    if (units <= g_clusters[dev][0] && a.num_kb >= 8) a.split = 2;
-    if (units <= g_clusters[dev][1] && a.num_kb >= 16) a.split = 4;
-    const int32_t span = std::max(32, cols / a.split / 2), chunk = out_bf16 ? std::min(span, 64) : 32;
+    // Fewer tiles than pairs: two pairs to a tile, where the clusters fit on the device at once (36 of 4 CTAs on 152
+    // SMs) and each half is long enough (512 rows, 4096 x 4096: 15.3 -> 14.2 us in 8 bits, 24 -> 19 in bf16)
+    const int32_t split = units <= g_clusters[dev] && a.num_kb >= 8 ? 2 : 1;
+    const int32_t span = cols / split / 2, chunk = out_bf16 ? std::min(span, 64) : 32;
     CUtensorMap mx, mw, my, mr{};
     if (!encode_swizzled_rows(&mx, es, x, K, rows, ldx, box, kHalf) ||
         !encode_swizzled_rows(&mw, es, w, K, gated ? int64_t{2} * M : M, ldw, box, kHalf))
@@ -568,10 +549,10 @@ bool launch_linear_tiles(bool fp8, const LinearEpilogue &ep, const void *w, int6
     // outputs, or a residual, that a tensor map does not take
     if (!encode_swizzled_rows(&my, out_bf16 ? 2 : 4, out, M, rows, ldo, chunk, 32)) return false;
     if (a.residual_tma && !encode_swizzled_rows(&mr, 2, ep.residual, M, rows, ep.ldr, chunk, 32)) return false;
-    const unsigned cluster = 2u * static_cast<unsigned>(a.split);
-    const dim3 grid(a.split > 1 ? cluster * static_cast<unsigned>(units) : 2u * static_cast<unsigned>(units < pairs ? units : pairs));
-    const bool lng = !out_bf16 && a.num_kb > 2 * kSegment * a.split;  // 8-bit products are summed exactly enough
-    *err = launch_pdl_cluster(a.split > 1 ? kernel_of<true>(fp8, gated, lng) : kernel_of<false>(fp8, gated, lng), grid, dim3(kThreads),
+    const unsigned cluster = 2u * static_cast<unsigned>(split);
+    const dim3 grid(split > 1 ? cluster * static_cast<unsigned>(units) : 2u * static_cast<unsigned>(units < pairs ? units : pairs));
+    const bool lng = !out_bf16 && a.num_kb > 2 * kSegment * split;  // 8-bit products are summed exactly enough
+    *err = launch_pdl_cluster(split > 1 ? kernel_of<true>(fp8, gated, lng) : kernel_of<false>(fp8, gated, lng), grid, dim3(kThreads),
                               cluster, kSmem, st, mx, mw, my, mr, a);
     return true;
 }

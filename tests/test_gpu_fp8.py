@@ -146,10 +146,11 @@ def operands(g, rows, M, K, kind, act, bias, residual, gb, pad=0):
 
 
 SHAPES = [
-    # rows, M, K: up to 16 rows, up to 128 with K in 1 to 8 parts, above with 1, 2 and 4 pairs a tile; odd everything
+    # rows, M, K: up to 16 rows, up to 128 with K in 1 to 8 parts, more in chunks of 128, whole tiles of one pair or two;
+    # odd everything
     (1, 4096, 4096), (1, 128, 64), (2, 1, 8), (7, 777, 1001), (15, 130, 72), (16, 2048, 8192), (16, 40000, 128),
     (17, 128, 4096), (31, 256, 8192), (33, 777, 1000), (61, 1000, 4096), (64, 8192, 512), (77, 777, 1001), (100, 64, 16),
-    (255, 512, 520), (256, 4096, 1024), (257, 384, 2048), (300, 100, 333), (129, 700, 4097), (150, 300, 8192), (1500, 4096, 256), (600, 2500, 640), (2080, 1024, 4096),
+    (255, 512, 520), (256, 4096, 1024), (257, 384, 2048), (300, 100, 333), (129, 700, 4097), (150, 300, 8192), (400, 4100, 1100), (1500, 4096, 256), (600, 2500, 640), (2080, 1024, 4096),
 ]
 ACTS = [(None, False, False), ("silu", True, True), ("gelu", True, False), ("swiglu", False, True), (None, True, True), ("swiglu", True, False)]
 
@@ -170,7 +171,7 @@ def test_linear(gb, rows, M, K, kind):
             assert torch.equal(again, got)
 
 
-@pytest.mark.parametrize("rows,M,K", [(300, 520, 16500), (1100, 5000, 4200), (700, 1300, 14336), (100, 300, 40000), (100, 20000, 4200)])
+@pytest.mark.parametrize("rows,M,K", [(300, 520, 16500), (1100, 5000, 4200), (700, 1300, 14336), (512, 4096, 9000), (512, 2048, 9000), (100, 300, 40000), (100, 20000, 4200)])
 @pytest.mark.parametrize("act", [None, "swiglu"])
 def test_long_sums_of_bf16_products_for_fp32_outputs(gb, rows, M, K, act):
     """Over 128 rows 2048 products at a time are summed by the tensor core, which adds 16 to what it has and
