@@ -227,6 +227,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int32_t row_bytes = a.out_bf16 ? 2 * chunk_cols : 128;
         uint8_t *const slot0 = slots + ew * 2 * kSlotBytes;
         uint32_t acc = 0, acc_phase = 0, res_phase = 0;
+        // chunks of all tiles so far: the slots take turns, also from one tile to the next where a tile is one chunk,
+        // so that a slot's last copy is never the newest
+        int32_t turn = 0;
         // kSplit: the pairs' sums of a CTA's columns meet in its shared memory, where the copies are over: from
         // the other pair [accumulator columns of the slice / 4][128 rows][4].  The two cluster barriers are met
         // by every thread of the cluster (the other warps', behind their work).
@@ -271,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 bulk_wait_read<0>();  // the slots' last outputs are on their way
                 for (int32_t c = 0; c < chunks; ++c) {
                     mbar_arrive_expect_tx(&ctl->res[ew][c], 32 * row_bytes);
-                    tma_load_2d(slot0 + c * kSlotBytes, &tmap_r, &ctl->res[ew][c], col0 + c * chunk_cols, row0, policy_evict_first());
+                    tma_load_2d(slot0 + ((turn + c) & 1) * kSlotBytes, &tmap_r, &ctl->res[ew][c], col0 + c * chunk_cols, row0, policy_evict_first());
                 }
             }
             // the columns' scales and biases: a thread each
@@ -337,8 +340,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             named_barrier_sync(1, kEpilogueThreads);
             tc_fence_after();
             const uint32_t t_row = tmem_base + kSums + (static_cast<uint32_t>(q * 32) << 16) + acc * kTile;
-            for (int32_t c = 0; c < chunks; ++c) {
-                uint8_t *const slot = slot0 + (c & 1) * kSlotBytes, *const mine = slot + lane * row_bytes;
+            for (int32_t c = 0; c < chunks; ++c, ++turn) {
+                uint8_t *const slot = slot0 + (turn & 1) * kSlotBytes, *const mine = slot + lane * row_bytes;
                 if (a.residual_tma) {
                     if (!mbar_wait(&ctl->res[ew][c], res_phase, abort_flag)) {
                         *abort_flag = 1;
