@@ -76,6 +76,7 @@ struct RotaryArgs {
     int32_t slices;            // blocks of 8 kv heads a chunk
     int32_t cache_blocks;      // the launch's first blocks write the cache, the others turn queries
     int32_t q_rows;            // rows of one of those
+    float minus_one;           // turn_word's
     uint64_t turn[64];
 };
 
@@ -149,40 +150,84 @@ __device__ __forceinline__ uint32_t quantise(const uint32_t (&w)[16], uint32_t (
     return ok ? static_cast<uint32_t>(__half_as_ushort(s)) | (static_cast<uint32_t>(__half_as_ushort(m)) << 16) : 0x7fff7fffu;
 }
 
-// The table of cosines and sines: a block of 16 pairs' (cos, sin) is 128 bytes and starts kTurnBlock bytes
-// after the one before it, so that the 16-byte pieces that the lanes of a quarter warp take lie in other banks.
+// Cosine and sine of a fraction of a turn in units of 2^-64, each the nearest fp32 value but for three in ten
+// thousand that lie beside a tie (and but for sines below 2^-21, good to 2^-23 of themselves): a turned key that is
+// one fp32 step off now and then rounds to another bf16 value, and takes another code of the cache.  The
+// angle within an eighth of a turn and its Taylor series to the 14th power, what is left of 1, -1/6 and 1/24 in fp32
+// and these in pairs of fp32 (hi + lo), products and sums by their exact remainders (T. J. Dekker, Numer. Math. 18,
+// 1971).  No fp64: it runs at a 64th of the rate here.
+__device__ __forceinline__ float2 cos_sin(uint64_t at) {
+    const uint32_t quarter = static_cast<uint32_t>((at + (uint64_t{1} << 61)) >> 62);
+    const int64_t rest = static_cast<int64_t>(at - (static_cast<uint64_t>(quarter) << 62));
+    const uint64_t m = static_cast<uint64_t>(rest < 0 ? -rest : rest);
+    const int32_t top = static_cast<int32_t>(m >> 32);
+    const float hi = static_cast<float>(top);
+    const float lo = fmaf(static_cast<float>(top - static_cast<int32_t>(hi)), 4294967296.0f, static_cast<float>(static_cast<uint32_t>(m)));
+    // the angle t + tl: hi and lo times 2 pi / 2^32 and 2^64
+    constexpr double kStep = 6.283185307179586 / 4294967296.0;
+    constexpr float kHi = static_cast<float>(kStep), kLo = static_cast<float>(kStep - static_cast<double>(kHi));
+    const float ph = __fmul_rn(hi, kHi), pl = __fadd_rn(fmaf(hi, kHi, -ph), fmaf(hi, kLo, __fmul_rn(lo, kHi / 4294967296.0f)));
+    const float t = __fadd_rn(ph, pl), tl = __fsub_rn(pl, __fsub_rn(t, ph));
+    const float u = __fmul_rn(t, t), ul = fmaf(__fmul_rn(2.0f, t), tl, fmaf(t, t, -u));  // its square
+    // sine: t (1 + u a), a = -1/6 + u (1/120 - ...)
+    float p = __fmul_rn(u, fmaf(u, fmaf(u, fmaf(u, fmaf(u, 1.0f / 6227020800.0f, -1.0f / 39916800.0f), 1.0f / 362880.0f), -1.0f / 5040.0f), 1.0f / 120.0f));
+    constexpr float kSixth = -1.0f / 6.0f, kSixthLo = static_cast<float>(-1.0 / 6.0 - static_cast<double>(kSixth));
+    float a = __fadd_rn(kSixth, p), al = __fadd_rn(__fsub_rn(p, __fsub_rn(a, kSixth)), kSixthLo);
+    const float w = __fmul_rn(u, a), wl = __fadd_rn(fmaf(u, a, -w), fmaf(u, al, __fmul_rn(ul, a)));
+    const float q = __fmul_rn(t, w), ql = __fadd_rn(fmaf(t, w, -q), fmaf(t, wl, __fmul_rn(tl, w)));
+    const float s0 = __fadd_rn(t, q);
+    const float s = __fadd_rn(s0, __fadd_rn(__fsub_rn(q, __fsub_rn(s0, t)), __fadd_rn(tl, ql)));
+    // cosine: 1 - u / 2 + u^2 a, a = 1/24 - u (1/720 - ...)
+    p = __fmul_rn(u, fmaf(u, fmaf(u, fmaf(u, 1.0f / 479001600.0f, -1.0f / 3628800.0f), 1.0f / 40320.0f), -1.0f / 720.0f));
+    constexpr float k24th = 1.0f / 24.0f, k24thLo = static_cast<float>(1.0 / 24.0 - static_cast<double>(k24th));
+    a = __fadd_rn(k24th, p), al = __fadd_rn(__fsub_rn(p, __fsub_rn(a, k24th)), k24thLo);
+    const float v = __fmul_rn(u, u), vl = fmaf(__fmul_rn(2.0f, u), ul, fmaf(u, u, -v));
+    const float f = __fmul_rn(v, a), fl = __fadd_rn(fmaf(v, a, -f), fmaf(v, al, __fmul_rn(vl, a)));
+    const float c0 = fmaf(-0.5f, u, 1.0f), c0l = fmaf(-0.5f, u, __fsub_rn(1.0f, c0));
+    const float c1 = __fadd_rn(c0, f), c1l = __fsub_rn(f, __fsub_rn(c1, c0));
+    const float c = __fadd_rn(c1, __fadd_rn(c0l, __fadd_rn(c1l, fmaf(-0.5f, ul, fl))));
+    const float sn = rest < 0 ? -s : s;
+    const bool odd = quarter & 1;
+    const float x = odd ? sn : c, y = odd ? c : sn;
+    return make_float2(quarter == 1 || quarter == 2 ? -x : x, quarter & 2 ? -y : y);
+}
+// The table of cosines and sines: a block of 16 pairs is 128 bytes, two pairs' cosines and sines (c, c, s, s) a
+// piece, and starts kTurnBlock bytes after the one before it, so that the 16-byte pieces that the lanes of a
+// quarter warp take lie in other banks.
 constexpr int kTurnBlock = 128 + 16;
-__device__ __forceinline__ float2 *turn_entry(uint8_t *table, int32_t G, int32_t row, int32_t j) {
-    return reinterpret_cast<float2 *>(table + (row * G + (j >> 4)) * kTurnBlock) + (j & 15);
+__device__ __forceinline__ float4 *turn_entry(uint8_t *table, int32_t G, int32_t row, int32_t j) {
+    return reinterpret_cast<float4 *>(table + (row * G + (j >> 4)) * kTurnBlock) + ((j & 15) >> 1);
 }
 // A warp works out one row's pairs.
 template <int G>
 __device__ __forceinline__ void turn_row(const RotaryArgs &ra, uint8_t *table, int32_t row, int32_t pos) {
     for (int32_t j = threadIdx.x & 31; j < 16 * G; j += 32) {
         const uint64_t at = ra.turn[j] * static_cast<uint64_t>(static_cast<int64_t>(pos));
-        // half turns within 1 of 0 in 32 bits; what fp32 leaves of them, as an angle, turns its sine and cosine
-        const int32_t half_turns = static_cast<int32_t>(at >> 32);
-        const float near = static_cast<float>(half_turns);
-        const float rest = static_cast<float>(static_cast<int64_t>(half_turns) - static_cast<int64_t>(near)) * 1.4629181e-9f;  // pi / 2^31
-        float s, c;
-        sincospif(near * 4.656612873e-10f, &s, &c);  // 2^-31
-        *turn_entry(table, G, row, j) = make_float2(fmaf(-rest, s, c), fmaf(rest, c, s));
+        const float2 cs = cos_sin(at);
+        float *entry = reinterpret_cast<float *>(turn_entry(table, G, row, j)) + (j & 1);
+        entry[0] = cs.x;
+        entry[2] = cs.y;
     }
 }
-// Turns two neighbouring values (a bf16 word) of one half of a head by the pairs' cosines and sines, and
-// rounds to bf16: the cache quantises bf16 keys, turned here or by the decoder layer.  `other` is the word
-// of the other half; sign -1 for the first half.
-__device__ __forceinline__ uint32_t turn_word(uint32_t own, uint32_t other, float sign, const float4 &cs) {
-    const float x = __uint_as_float(own << 16), y = __uint_as_float(own & 0xffff0000u);
-    const float p = __uint_as_float(other << 16), q = __uint_as_float(other & 0xffff0000u);
-    const __nv_bfloat162 r = __floats2bfloat162_rn(fmaf(x, cs.x, sign * (p * cs.y)), fmaf(y, cs.z, sign * (q * cs.w)));
+// Turns two neighbouring values (a bf16 word) of one half of a head by the pairs' cosines and sines,
+// own c - other s (the second half's `other` comes with its sign turned: kMinus), and rounds to bf16: the cache
+// quantises bf16 keys, turned here or by the decoder layer.  Both products and their difference are rounded to fp32,
+// as a plain form's are: one rounding less, in a fused sum, gives another bf16 value now and then.  The compiler
+// fuses a product and a sum of packed pairs even where both say .rn, so the sum is a fused one with a factor
+// that it does not know, -1 from the arguments.
+constexpr uint32_t kMinus = 0x80008000u;  // both values' signs
+__device__ __forceinline__ uint32_t turn_word(uint32_t own, uint32_t other, const float4 &cs, float minus_one) {
+    const uint64_t x = pack_2(own << 16, own & 0xffff0000u), p = pack_2(other << 16, other & 0xffff0000u);
+    const float2 y = unpack_2(fma_2(mul_2(p, pack_2(cs.z, cs.w)), pack_2(minus_one, minus_one), mul_2(x, pack_2(cs.x, cs.y))));
+    const __nv_bfloat162 r = __floats2bfloat162_rn(y.x, y.y);
     return *reinterpret_cast<const uint32_t *>(&r);
 }
 // A key's group g in place, w; `head` is the key as it came.  Blocks of 16 dims: block i and block i + G (i < G)
 // are each other's halves.  Where a row's groups lie in neighbouring lanes of one pass, the other half comes
 // from there (G 1, 2, 4: from the lane itself, or G / 2 lanes apart), else from memory.  Whole warp.
 template <int G>
-__device__ __forceinline__ void turn_group(uint8_t *table, int32_t row, int32_t g, bool key, const uint4 *head, uint32_t (&w)[16]) {
+__device__ __forceinline__ void turn_group(uint8_t *table, int32_t row, int32_t g, bool key, const uint4 *head, float minus_one,
+                                           uint32_t (&w)[16]) {
     uint32_t o[16];
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
@@ -196,6 +241,7 @@ __device__ __forceinline__ void turn_group(uint8_t *table, int32_t row, int32_t 
     for (int h = 0; h < 2; ++h) {
         const int32_t i = 2 * g + h;
         const bool first = i < G;
+        const uint32_t sign = first ? 0u : kMinus;
         if constexpr (G == 3) {
             const uint4 *other = head + 2 * (first ? i + G : i - G);
             const uint4 o0 = __ldg(other), o1 = __ldg(other + 1);
@@ -203,9 +249,9 @@ __device__ __forceinline__ void turn_group(uint8_t *table, int32_t row, int32_t 
 #pragma unroll
             for (int k = 0; k < 8; ++k) o[8 * h + k] = p[k];
         }
-        const float4 *cs = reinterpret_cast<const float4 *>(turn_entry(table, G, row, 16 * (first ? i : i - G)));
+        const float4 *cs = turn_entry(table, G, row, 16 * (first ? i : i - G));
 #pragma unroll
-        for (int k = 0; k < 8; ++k) w[8 * h + k] = turn_word(w[8 * h + k], o[8 * h + k], first ? -1.0f : 1.0f, cs[k]);
+        for (int k = 0; k < 8; ++k) w[8 * h + k] = turn_word(w[8 * h + k], o[8 * h + k] ^ sign, cs[k], minus_one);
     }
 }
 // ra.q_rows rows of queries (16 at most): a thread turns 8 pairs of a head at a time.
@@ -244,13 +290,13 @@ __device__ __forceinline__ void turn_queries(const RotaryArgs &ra, uint8_t *tabl
                 const int32_t t = t0 + i * at_once;
                 if (t >= rows) break;
                 uint4 *dst = reinterpret_cast<uint4 *>(ra.q_out + (row0 + t) * ra.H * 32 * G + at);
-                const float4 *cs = reinterpret_cast<const float4 *>(turn_entry(table, G, t, 8 * e));
+                const float4 *cs = turn_entry(table, G, t, 8 * e);
                 const uint32_t xw[4] = {x[i].x, x[i].y, x[i].z, x[i].w}, yw[4] = {y[i].x, y[i].y, y[i].z, y[i].w};
                 uint32_t p[4], q[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    p[k] = turn_word(xw[k], yw[k], -1.0f, cs[k]);
-                    q[k] = turn_word(yw[k], xw[k], 1.0f, cs[k]);
+                    p[k] = turn_word(xw[k], yw[k], cs[k], ra.minus_one);
+                    q[k] = turn_word(yw[k], xw[k] ^ kMinus, cs[k], ra.minus_one);
                 }
                 dst[0] = make_uint4(p[0], p[1], p[2], p[3]);
                 dst[2 * G] = make_uint4(q[0], q[1], q[2], q[3]);
@@ -344,7 +390,7 @@ __device__ __forceinline__ void append_chunk(const AppendArgs &a, uint8_t *st, u
             const int32_t n = it / G, g = it - n * G;
             const int32_t t = order[min(n, 15)], from = __shfl_sync(kFull, src, t & 15);
             turn_group<G>(table, t, g, n < live, reinterpret_cast<const uint4 *>(a.k + (static_cast<int64_t>(b) * a.src_rows + from) * a.ld +
-                                                                                 static_cast<int64_t>(hk) * G * kKv4Group), now);
+                                                                                 static_cast<int64_t>(hk) * G * kKv4Group), ra->minus_one, now);
         }
         const uint32_t params = quantise(now, codes);
         if (it < items) {
@@ -398,8 +444,8 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const AppendArgs a
 
 // Blocks of one chunk and up to 8 of its kv heads, a warp a head: the chunk's cosines and sines are worked
 // out once a block, with the first rows on their way.  Further blocks turn the queries.  Three blocks an SM (80
-// registers): 33 k tokens of 8 kv heads and 32 heads of 128 (0.70 GB) in 132 us, 0.78 of the measured copy rate
-// (two blocks 146); keys and values alone 60 us, 41 as they are.
+// registers): 33 k tokens of 8 kv heads and 32 heads of 128 (0.70 GB) in 135 us, 0.76 of the measured copy rate
+// (132 with cosines and sines an fp32 step off; then two blocks 146); keys and values alone 63 us, 41 as they are.
 template <int G>
 __global__ void __launch_bounds__(kThreads, 3) kv4_rotary_kernel(const __grid_constant__ RotaryArgs ra) {
     __shared__ __align__(16) uint8_t stage[kWarps][kv4_chunk_bytes(G)];
@@ -673,6 +719,7 @@ eagle_status eagle_kv4_append_rotary(const eagle_kv4_cache *cache, int32_t batch
                 misaligned(d_q_out, 16)))
         return EAGLE_ERR_INVALID_ARG;
     r.positions = d_positions;
+    r.minus_one = -1.0f;
     const int64_t units = r.a.u.total / r.a.u.Hk;  // (request, chunk)
     r.slices = (r.a.u.Hk + kWarps - 1) / kWarps;
     int64_t blocks = units * r.slices;

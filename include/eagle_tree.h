@@ -579,8 +579,9 @@ EAGLE_API eagle_status eagle_kv4_append(const eagle_kv4_cache *cache, int32_t ba
  *                are not written to the cache; may be d_q itself where ldq is heads * head_dim
  * Pointers are 16-byte aligned; the other arguments, what is written and what is latched are those of
  * eagle_kv4_append.  Angles are whole-number products modulo a turn: exact for any position but for the
- * frequencies' own rounding in 64 bits; their cosines and sines, and the turned values until they are
- * rounded, are fp32.  heads at most 65536; rope_theta > 0.
+ * frequencies' own rounding in 64 bits.  Their cosines and sines are the nearest fp32 values (but for some three in
+ * ten thousand, one step off), and a turned value is two products and their sum, each rounded to fp32, then
+ * rounded to bf16.  heads at most 65536; rope_theta > 0.
  * Errors: INVALID_ARG, CUDA; UNSUPPORTED as eagle_kv4_append, or where the launch would pass 2^31 blocks.
  */
 EAGLE_API eagle_status eagle_kv4_append_rotary(const eagle_kv4_cache *cache, int32_t batch, int32_t src_rows,

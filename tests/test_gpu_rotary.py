@@ -181,3 +181,29 @@ def test_refusals_of_the_binding():
     with pytest.raises(Exception, match="INVALID_ARG"):
         c.append_rotary(k, v, rope_theta=0.0)
     assert math.isfinite(float(c.attention(q.contiguous()).float().sum()))
+
+
+@pytest.mark.parametrize("H,D,rows,most", [(32, 128, 4096, 8190), (8, 96, 4096, 8190), (16, 64, 4096, 131071), (64, 32, 4096, 1 << 30)])
+def test_turned_values_are_those_of_fp32(H, D, rows, most):
+    """Cosines and sines to the nearest fp32 value, two products and their sum rounded to fp32 each, then bf16:
+    the same bits, but where a cosine or sine lies beside a tie.  The library misses the nearest in 2^-11.8 of
+    them.  Such an entry moves a product by one fp32 step, and so one sum in 2^16 / 4 or less by a bf16 step:
+    2^-25 of the values.  Up to 2^-20 of them may differ here, by one step (with tables and sums an fp32 step off
+    2^-15 do)."""
+    g = gen(H + D)
+    q, k, v = qkv(g, 1, rows, H, 1, D)
+    pos = torch.randint(0, most + 1, (1, rows), generator=g, device="cuda", dtype=torch.int32)
+    c = make_cache(1, 1, D, rows, 64)
+    got = c.append_rotary(k, v, q=q, positions=pos)
+    c.status()
+    # the angle as a fraction of a turn, by whole numbers: frequency in 2^-64 of a turn, as Python's floats have it
+    turns = [math.pow(10000.0, -2.0 * j / D) / (2 * math.pi) for j in range(D // 2)]
+    whole = [int(math.ldexp(t, 64)) % 2 ** 64 for t in turns]
+    f = torch.tensor([w - 2 ** 64 if w >= 2 ** 63 else w for w in whole], dtype=torch.int64, device="cuda")
+    ang = (pos.long()[..., None] * f).double() * (2 * math.pi / 2.0 ** 64)  # modulo a turn
+    cos, sin = torch.cos(ang).float()[:, :, None], torch.sin(ang).float()[:, :, None]
+    a, b = q[..., :D // 2].float(), q[..., D // 2:].float()
+    want = torch.cat([a * cos - b * sin, b * cos + a * sin], -1).to(torch.bfloat16)
+    other = got != want
+    assert int(other.sum()) <= got.numel() * 2.0 ** -20, int(other.sum())
+    assert ((got.double() - want.double()).abs() <= 2 * ref.HALF_BF16 * want.double().abs() + 2.0 ** -23 * 8).all()
