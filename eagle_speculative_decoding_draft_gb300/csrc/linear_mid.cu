@@ -24,7 +24,7 @@ constexpr size_t kMidSmem = 113 * 1024;
 constexpr int kMidThreads = 64 + 256;  // warp 0: copies, warp 1: MMAs, then two warps an accumulator quarter
 
 struct MidCtl {
-    uint64_t full[kMidStages], empty[kMidStages], acc_full, drain;
+    uint64_t full[kMidStages], empty[kMidStages], acc_full, acc_empty, drain;
     uint32_t tmem_base;
     int32_t abort;
 };
@@ -33,7 +33,6 @@ struct MidArgs {
     LinearArgs l;      // M, rows, n_tile, num_kb, stages, bias, out, ldo, out_bf16, ep, status
     int32_t split;     // CTAs of a cluster
     int32_t tmem_cols;
-    int32_t halves;    // 2: the second half of a part's sums in an accumulator of its own
 };
 
 __device__ __forceinline__ void tmem_ld_4(uint32_t taddr, uint32_t (&r)[4]) {
@@ -51,10 +50,13 @@ __device__ __forceinline__ void tmem_ld_8(uint32_t taddr, uint32_t (&r)[8]) {
 }
 
 // A cluster of a.split CTAs a (tile, chunk of n_tile rows): blockIdx.x / split the tile, blockIdx.y the chunk.
-template <class Op>
+// kLong (fp32 out): linear_segment k-blocks are summed at a time, in an accumulator beside the one for their sums
+// (61 rows, 14336 -> 4096 in bf16 24.0 -> 24.2 us; with everything in one accumulator 7.9e-6 lost where a CTA has
+// all 14336 products, 1.0e-6 so).
+template <class Op, bool kLong>
 __global__ void __launch_bounds__(kMidThreads, 2)
     linear_mid_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_x, const MidArgs m) {
-    constexpr int32_t BK = k_block<Op>();
+    constexpr int32_t BK = k_block<Op>(), kSegment = linear_segment(Op::kFp8);
     const LinearArgs &a = m.l;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_addr = smem_u32(smem_raw);
@@ -76,6 +78,7 @@ __global__ void __launch_bounds__(kMidThreads, 2)
             mbar_init(&ctl->empty[s], 1);
         }
         mbar_init(&ctl->acc_full, 1);
+        mbar_init(&ctl->acc_empty, kMidThreads / 32 - 2);  // the epilogue's warps
         mbar_init(&ctl->drain, 1);
         ctl->abort = 0;
         fence_barrier_init();
@@ -126,14 +129,20 @@ __global__ void __launch_bounds__(kMidThreads, 2)
     } else if (warp == 1) {
         if (lane == 0) {
             const uint32_t idesc = Op::kFp8 ? idesc_e4m3_f32(BM, static_cast<uint32_t>(n)) : idesc_bf16_f32(BM, static_cast<uint32_t>(n));
-            const int32_t kb_half = m.halves == 2 ? (kb_begin + kb_end) / 2 : kb_end;
-            uint32_t stage = 0, phase = 0;
+            uint32_t stage = 0, phase = 0, acc_phase = 0;
+            int32_t held = 0;  // k-blocks in the accumulator
             bool ok = true;
-            for (int32_t kb = kb_begin; kb < kb_end; ++kb) {
-                if (!mbar_wait(&ctl->full[stage], phase, abort_flag)) {
+            for (int32_t kb = kb_begin; kb < kb_end; ++kb, ++held) {
+                if (kLong && held == kSegment) {  // they join the sums
+                    mma_commit(&ctl->acc_full);
+                    ok = mbar_wait(&ctl->acc_empty, acc_phase, abort_flag);
+                    acc_phase ^= 1u;
+                    held = 0;
+                }
+                ok = ok && mbar_wait(&ctl->full[stage], phase, abort_flag);
+                if (!ok) {
                     *abort_flag = 1;
                     latch(a.status, kDevTimeout);
-                    ok = false;
                     break;
                 }
                 tc_fence_after();
@@ -142,10 +151,9 @@ __global__ void __launch_bounds__(kMidThreads, 2)
                 for (int kk = 0; kk < 4; ++kk) {
                     const uint64_t dw = sw128_kmajor_desc(w0 + kk * 32), dx = sw128_kmajor_desc(x0 + kk * 32);
                     if (Op::kFp8)
-                        mma_f8_ss(tmem_base, dw, dx, idesc, kb > kb_begin || kk > 0);
+                        mma_f8_ss(tmem_base, dw, dx, idesc, held > 0 || kk > 0);
                     else
-                        mma_bf16_ss(tmem_base + (kb >= kb_half ? static_cast<uint32_t>(n) : 0u), dw, dx, idesc,
-                                    (kb > kb_begin && kb != kb_half) || kk > 0);
+                        mma_bf16_ss(tmem_base, dw, dx, idesc, held > 0 || kk > 0);
                 }
                 mma_commit(&ctl->empty[stage]);
                 if (++stage == static_cast<uint32_t>(stages)) {
@@ -158,18 +166,52 @@ __global__ void __launch_bounds__(kMidThreads, 2)
         __syncwarp();
     } else {
         pdl_wait();
-        if (!mbar_wait(&ctl->acc_full, 0, abort_flag)) {
-            *abort_flag = 1;
-            latch(a.status, kDevTimeout);
+        if constexpr (!kLong) {
+            if (!mbar_wait(&ctl->acc_full, 0, abort_flag)) {
+                *abort_flag = 1;
+                latch(a.status, kDevTimeout);
+            }
+            __syncwarp();
+            tc_fence_after();
+        } else {
+            const uint32_t lanes = tmem_base + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+            uint32_t phase = 0;
+            for (int32_t kb = kb_begin; kb < kb_end; kb += kSegment, phase ^= 1u) {
+                const bool got = mbar_wait(&ctl->acc_full, phase, abort_flag);
+                if (!__all_sync(0xffffffffu, got)) {
+                    *abort_flag = 1;
+                    latch(a.status, kDevTimeout);
+                    break;
+                }
+                tc_fence_after();
+                for (int32_t c = 32 * ((warp - 2) >> 2); c < n; c += 64) {  // this warp's columns, as below
+                    uint32_t r[32];
+                    tmem_ld_32(lanes + static_cast<uint32_t>(c), r);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int h = 0; h < 2 && kb > kb_begin; ++h) {
+                        uint32_t s[16];
+                        tmem_ld_16(lanes + static_cast<uint32_t>(n + c + 16 * h), s);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) r[16 * h + i] = __float_as_uint(__uint_as_float(r[16 * h + i]) + __uint_as_float(s[i]));
+                    }
+                    tmem_st_32(lanes + static_cast<uint32_t>(n + c), r);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl->acc_empty);
+            }
+            named_barrier_sync(1, kMidThreads - 64);  // sums that other warps of the quarter have stored
+            tc_fence_after();
         }
-        __syncwarp();
-        tc_fence_after();
     }
     // The parts' sums: CTA `to` of the cluster finishes rows to * share .. of the chunk, and finds those that
     // the others send it, from each [rows / 4][128 rows of w][4], where its copies are over.
     const int32_t share = n / S;
     const int32_t q = warp & 3, turn = (warp - 2) >> 2, ml = q * 32 + lane;
-    const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+    const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + (kLong ? static_cast<uint32_t>(n) : 0u);
     const bool fine = !__any_sync(0xffffffffu, *abort_flag != 0);
     if (S > 1) {
         cluster_sync();
@@ -179,13 +221,6 @@ __global__ void __launch_bounds__(kMidThreads, 2)
                 __syncwarp();
                 tmem_ld_32(t_row + static_cast<uint32_t>(c), r);
                 tmem_wait_ld();
-                if (!Op::kFp8 && m.halves == 2) {
-                    uint32_t r2[32];
-                    tmem_ld_32(t_row + static_cast<uint32_t>(n + c), r2);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) + __uint_as_float(r2[i]));
-                }
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {  // a share is a multiple of 4 rows
                     const int32_t to = (c + 4 * i) / share, at = c + 4 * i - to * share;
@@ -208,23 +243,14 @@ __global__ void __launch_bounds__(kMidThreads, 2)
                 const int32_t n0 = part * share + c;
                 if (n0 >= end) break;
                 uint32_t r[C];
-                auto sums = [&](int32_t col, uint32_t (&to)[C]) {
-                    __syncwarp();
-                    if constexpr (C == 16)
-                        tmem_ld_16(t_row + static_cast<uint32_t>(col), to);
-                    else if constexpr (C == 8)
-                        tmem_ld_8(t_row + static_cast<uint32_t>(col), to);
-                    else
-                        tmem_ld_4(t_row + static_cast<uint32_t>(col), to);
-                    tmem_wait_ld();
-                };
-                sums(n0, r);
-                if (!Op::kFp8 && m.halves == 2) {
-                    uint32_t r2[C];
-                    sums(n + n0, r2);
-#pragma unroll
-                    for (int i = 0; i < C; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) + __uint_as_float(r2[i]));
-                }
+                __syncwarp();
+                if constexpr (C == 16)
+                    tmem_ld_16(t_row + static_cast<uint32_t>(n0), r);
+                else if constexpr (C == 8)
+                    tmem_ld_8(t_row + static_cast<uint32_t>(n0), r);
+                else
+                    tmem_ld_4(t_row + static_cast<uint32_t>(n0), r);
+                tmem_wait_ld();
                 float v[C];
                 for (int32_t from = 0; from < S; ++from) {  // in their order
                     const float4 *src = reinterpret_cast<const float4 *>(ring + ((from < part ? from : from - 1) * share + c) * 512) + ml;
@@ -274,16 +300,18 @@ __global__ void __launch_bounds__(kMidThreads, 2)
 }
 
 using Kernel = void (*)(const CUtensorMap, const CUtensorMap, const MidArgs);
+template <bool kLong>
 Kernel kernel_of(bool fp8, bool gated) {
-    if (fp8) return gated ? linear_mid_kernel<EpilogueOp<true, true>> : linear_mid_kernel<EpilogueOp<true, false>>;
-    return gated ? linear_mid_kernel<EpilogueOp<false, true>> : linear_mid_kernel<EpilogueOp<false, false>>;
+    if (fp8) return gated ? linear_mid_kernel<EpilogueOp<true, true>, kLong> : linear_mid_kernel<EpilogueOp<true, false>, kLong>;
+    return gated ? linear_mid_kernel<EpilogueOp<false, true>, kLong> : linear_mid_kernel<EpilogueOp<false, false>, kLong>;
 }
 
 }  // namespace
 
 cudaError_t prepare_linear_mid() {
-    for (int i = 0; i < 4; ++i) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel_of(i & 1, i & 2), cudaFuncAttributeMaxDynamicSharedMemorySize,
+    for (int i = 0; i < 8; ++i) {
+        const Kernel k = i < 4 ? kernel_of<false>(i & 1, i & 2) : kernel_of<true>(i & 1, i & 2);
+        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                    static_cast<int>(kMidSmem));
         if (e != cudaSuccess) return e;
     }
@@ -319,16 +347,16 @@ bool launch_linear_mid(bool fp8, const LinearEpilogue &ep, const void *w, int64_
     const int32_t most = a.n_tile > 32 && a.num_kb < 64 ? 4 : 8;
     m.split = 1;
     while (m.split < most && static_cast<int64_t>(a.num_tiles) * chunks * m.split <= sms && a.num_kb >= 4 * m.split) m.split *= 2;
-    // Long sums of bf16 products in two halves where fp32 goes out: the accumulator truncates (linear_tiles.cu)
-    m.halves = !fp8 && !out_bf16 && a.num_kb / m.split > 64 ? 2 : 1;
+    const bool lng = !out_bf16 && (a.num_kb + m.split - 1) / m.split > linear_segment(fp8);
     m.tmem_cols = 32;
-    while (m.tmem_cols < a.n_tile * m.halves) m.tmem_cols *= 2;
+    while (m.tmem_cols < a.n_tile * (lng ? 2 : 1)) m.tmem_cols *= 2;
     CUtensorMap mw, mx;
     if (gated ? !encode_gated_rows(&mw, es, w, K, M, ldw, 16) : !encode_swizzled_rows(&mw, es, w, K, M, ldw, box, BM)) return false;
     if (!encode_swizzled_rows(&mx, es, x, K, rows, ldx, box, a.n_tile)) return false;
     const size_t smem = 1024 + a.stages * stage + sizeof(MidCtl);
-    *err = launch_pdl_cluster(kernel_of(fp8, gated), dim3(static_cast<unsigned>(a.num_tiles * m.split), static_cast<unsigned>(chunks)),
-                              dim3(kMidThreads), static_cast<unsigned>(m.split), smem, st, mw, mx, m);
+    const dim3 grid(static_cast<unsigned>(a.num_tiles * m.split), static_cast<unsigned>(chunks));
+    *err = launch_pdl_cluster(lng ? kernel_of<true>(fp8, gated) : kernel_of<false>(fp8, gated), grid, dim3(kMidThreads),
+                              static_cast<unsigned>(m.split), smem, st, mw, mx, m);
     return true;
 }
 

@@ -56,3 +56,36 @@ def test_gated_products_without_a_residual_beside_others(gb):
         graph.replay()
         for i, out in enumerate(outs):
             assert torch.equal(out, want[i % len(work)]), i
+
+
+# What an fp32 output may lose in a sum of products, norm-wise.  The tensor core truncates: an addition (of 16
+# products, or 32 in 8 bits) loses half a step of the sum so far on average, 2^-24.5 of it, and a sum that grows as a
+# random walk is 2/3 of the last on average.  bf16: 1024 products at a time, 64 additions: 64 x 2/3 x 2^-24.5 =
+# 1.8e-6.  8 bits: 4096 at a time, 128 additions, but rows that reach 448 have products that are mostly multiples of
+# the accumulator's step, which lose nothing: 2.2e-7 was measured of 4096 such products.  On top: the segments' sums,
+# the scales and the output, 2^-24 each.
+LOSS = {BF16: 2.5e-6, E4M3: 3e-7}
+
+
+def check_loss(gb, rows, M, K, kind, odd=False):
+    w, x, _, _, w_scale, x_scale = operands(gen(K + rows), rows, M, K, kind, None, False, False, gb)
+    y, _ = ref.linear(w, x, None, None, None, w_scale, x_scale, F32)
+    out = torch.empty(rows, M | 1, device="cuda")[:, :M] if odd else None
+    got = gb.linear(w, x, w_scale=w_scale, x_scale=x_scale, dtype=F32, out=out)
+    off = float((got.double() - y).norm() / y.norm())
+    assert off <= LOSS[kind], off
+    if odd and rows > 128:  # with a workspace too
+        out.fill_(float("nan"))
+        gb.linear(w, x, w_scale=w_scale, x_scale=x_scale, dtype=F32, out=out, workspace=gb.linear_workspace(w, rows))
+        off = float((out.double() - y).norm() / y.norm())
+        assert off <= LOSS[kind], off
+
+
+@pytest.mark.parametrize("rows,M,K,odd", [(100, 20000, 14336, False), (128, 20001, 28672, True), (100, 20000, 40000, False), (61, 1300, 14336, True),
+                                          (17, 4096, 8192, False), (300, 20000, 14336, True), (700, 1300, 14336, True), (40, 9728, 2100, False)])
+@pytest.mark.parametrize("kind", [BF16, E4M3], ids=["bf16", "e4m3"])
+def test_long_sums_of_17_to_128_rows(gb, rows, M, K, odd, kind):
+    """All of K in a CTA or parts of it in a cluster; over 128 rows outputs that no bulk store takes."""
+    if kind is E4M3 and K > 32768:
+        pytest.skip("rows are quantised up to 32768 columns")
+    check_loss(gb, rows, M, K, kind, odd)
