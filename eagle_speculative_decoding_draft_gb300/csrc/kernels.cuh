@@ -159,12 +159,6 @@ cudaError_t prepare_kernels();
 cudaError_t launch_linear_few(bool fp8, const LinearEpilogue &ep, const void *w, int64_t ldw, int32_t M, int32_t K, const void *x,
                               int64_t ldx, int32_t rows, const void *bias, void *out, int64_t ldo, bool out_bf16,
                               int32_t sms, cudaStream_t st);
-// K-blocks (of 128 bytes: 64 bf16 or 128 8-bit products) that an accumulator sums in one go where fp32 goes out; the
-// segments are added up rounded to nearest.  The tensor core adds 16 products (32 in 8 bits) to what it has and
-// truncates, so a sum is too small by a part that grows with its length: of bf16 products 1.1e-6 (norm-wise,
-// measured) for 1024 of them, 2.1e-6 for 2048, 4.4e-6 for 4096, 1.7e-5 for 14336; of 8-bit ones, mostly multiples
-// of the accumulator's step, 2.2e-7 for 4096 and 1.0e-6 for 14336.
-__host__ __device__ constexpr int32_t linear_segment(bool fp8) { return fp8 ? 32 : 16; }
 constexpr int kLinearFewRows = 16;
 constexpr int kLinearMidRows = 128;  // above: linear_tiles.cu, but where linear_mid.cu has few tiles
 // linear_mid.cu: the same product for 17 to 128 rows (more in chunks of 128), without a workspace.  False as

@@ -83,8 +83,7 @@ cudaError_t launch_linear(bool fp8, const LinearEpilogue &ep, const void *w, int
         const int32_t pairs = linear_pair_workers(sms);
         if (pairs > 0 && launch_linear_tiles(fp8, ep, w, ldw, M, K, x, ldx, rows, bias, y, ldy, y_bf16, status, pairs, st, &e)) return e;
     }
-    // (the stream sums all of K in one go)
-    if (mid || !ws || (!y_bf16 && static_cast<int64_t>(K) * (fp8 ? 1 : 2) > 128 * linear_segment(fp8)))
+    if (mid || !ws || (!fp8 && !y_bf16 && K > 4096))  // (the stream has no parts for long sums)
         return launch_linear_mid(fp8, ep, w, ldw, M, K, x, ldx, rows, bias, y, ldy, y_bf16, status, sms, st, &e) ? e : cudaErrorInvalidValue;
     LinearPlan p;
     if (!plan_linear(&p, fp8, ep, w, ldw, M, K, x, ldx, rows, bias, y, ldy, y_bf16,

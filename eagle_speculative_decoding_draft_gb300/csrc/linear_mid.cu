@@ -21,6 +21,12 @@ namespace {
 
 constexpr int kMidStages = 6;  // at most
 constexpr size_t kMidSmem = 113 * 1024;
+// K-blocks (of 128 bytes: 64 bf16 or 128 8-bit products) that an accumulator sums in one go where fp32 goes out; the
+// segments are added up rounded to nearest.  The tensor core adds 16 products (32 in 8 bits) to what it has and
+// truncates, so a sum is too small by a part that grows with its length: of bf16 products 1.0e-6 (norm-wise,
+// measured) for 1024 of them, 2.1e-6 for 2048, 4.4e-6 for 4096, 1.7e-5 for 14336; of 8-bit ones, mostly multiples
+// of the accumulator's step, 2.2e-7 for 4096 and 1.0e-6 for 14336.
+__host__ __device__ constexpr int32_t segment_of(bool fp8) { return fp8 ? 32 : 16; }
 constexpr int kMidThreads = 64 + 256;  // warp 0: copies, warp 1: MMAs, then two warps an accumulator quarter
 
 struct MidCtl {
@@ -50,13 +56,13 @@ __device__ __forceinline__ void tmem_ld_8(uint32_t taddr, uint32_t (&r)[8]) {
 }
 
 // A cluster of a.split CTAs a (tile, chunk of n_tile rows): blockIdx.x / split the tile, blockIdx.y the chunk.
-// kLong (fp32 out): linear_segment k-blocks are summed at a time, in an accumulator beside the one for their sums
+// kLong (fp32 out): segment_of k-blocks are summed at a time, in an accumulator beside the one for their sums
 // (61 rows, 14336 -> 4096 in bf16 24.0 -> 24.2 us; with everything in one accumulator 7.9e-6 lost where a CTA has
 // all 14336 products, 1.0e-6 so).
 template <class Op, bool kLong>
 __global__ void __launch_bounds__(kMidThreads, 2)
     linear_mid_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_x, const MidArgs m) {
-    constexpr int32_t BK = k_block<Op>(), kSegment = linear_segment(Op::kFp8);
+    constexpr int32_t BK = k_block<Op>(), kSegment = segment_of(Op::kFp8);
     const LinearArgs &a = m.l;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_addr = smem_u32(smem_raw);
@@ -347,7 +353,7 @@ bool launch_linear_mid(bool fp8, const LinearEpilogue &ep, const void *w, int64_
     const int32_t most = a.n_tile > 32 && a.num_kb < 64 ? 4 : 8;
     m.split = 1;
     while (m.split < most && static_cast<int64_t>(a.num_tiles) * chunks * m.split <= sms && a.num_kb >= 4 * m.split) m.split *= 2;
-    const bool lng = !out_bf16 && (a.num_kb + m.split - 1) / m.split > linear_segment(fp8);
+    const bool lng = !out_bf16 && (a.num_kb + m.split - 1) / m.split > segment_of(fp8);
     m.tmem_cols = 32;
     while (m.tmem_cols < a.n_tile * (lng ? 2 : 1)) m.tmem_cols *= 2;
     CUtensorMap mw, mx;

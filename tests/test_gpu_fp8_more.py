@@ -67,18 +67,13 @@ def test_gated_products_without_a_residual_beside_others(gb):
 LOSS = {BF16: 2.5e-6, E4M3: 3e-7}
 
 
-def check_loss(gb, rows, M, K, kind, odd=False):
+def check_loss(gb, rows, M, K, kind, odd=False, most=None):
     w, x, _, _, w_scale, x_scale = operands(gen(K + rows), rows, M, K, kind, None, False, False, gb)
     y, _ = ref.linear(w, x, None, None, None, w_scale, x_scale, F32)
     out = torch.empty(rows, M | 1, device="cuda")[:, :M] if odd else None
     got = gb.linear(w, x, w_scale=w_scale, x_scale=x_scale, dtype=F32, out=out)
     off = float((got.double() - y).norm() / y.norm())
-    assert off <= LOSS[kind], off
-    if odd and rows > 128:  # with a workspace too
-        out.fill_(float("nan"))
-        gb.linear(w, x, w_scale=w_scale, x_scale=x_scale, dtype=F32, out=out, workspace=gb.linear_workspace(w, rows))
-        off = float((out.double() - y).norm() / y.norm())
-        assert off <= LOSS[kind], off
+    assert off <= (most or LOSS[kind]), off
 
 
 @pytest.mark.parametrize("rows,M,K,odd", [(100, 20000, 14336, False), (128, 20001, 28672, True), (100, 20000, 40000, False), (61, 1300, 14336, True),
@@ -89,3 +84,15 @@ def test_long_sums_of_17_to_128_rows(gb, rows, M, K, odd, kind):
     if kind is E4M3 and K > 32768:
         pytest.skip("rows are quantised up to 32768 columns")
     check_loss(gb, rows, M, K, kind, odd)
+
+
+@pytest.mark.parametrize("rows,M,K", [(700, 1300, 14336), (300, 20000, 14336), (2080, 4096, 8192), (1000, 20000, 4000), (512, 4096, 14336), (600, 4096, 40000),
+                                      (400, 2052, 2304)])
+@pytest.mark.parametrize("kind", [BF16, E4M3], ids=["bf16", "e4m3"])
+def test_long_sums_of_many_rows(gb, rows, M, K, kind):
+    """Whole tiles of a pair of CTAs, and of two that share K: up to 4096 bf16 products in one go (256 additions),
+    else 2048 at a time (128); all 8-bit products, of which the losses measured (K 7e-11) are held with half on top."""
+    if kind is E4M3 and K > 32768:
+        pytest.skip("rows are quantised up to 32768 columns")
+    check_loss(gb, rows, M, K, kind, most=(K / 16 if K <= 4096 else 256 if K <= 8192 else 128) * 2 / 3 * 2 ** -24.5 + 3 * 2 ** -24
+               if kind is BF16 else 1e-10 * K + 2 ** -23)
