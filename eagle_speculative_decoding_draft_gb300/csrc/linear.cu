@@ -75,15 +75,20 @@ cudaError_t launch_linear(bool fp8, const LinearEpilogue &ep, const void *w, int
     // where tiles of 128 rows of either leave room for four parts of K each, those are quicker still (256 rows, 4096
     // -> 4096 in 8 bits: 12.2 us against 13.1, 14336 -> 4096 21.8 against 25.4, in bf16 34 against 42; 1024 rows,
     // 14336 -> 1024: 20 against 24; but 384 rows, 4096 -> 4096, three parts' room: 15.5 against 14.2).
-    // Outputs that no bulk store takes go through the weights' stream where there is a workspace for it.
+    // Outputs that no bulk store takes go through linear_mid.cu in chunks of 128 rows, or through the weights' stream
+    // where there is a workspace for it, the weights have more tiles than the device SMs and the rows eight chunks
+    // (2080 and 8192 rows, 4096 -> 31999: 390 and 1430 us in chunks, 290 and 1020 in the stream, in bf16 700 and 2610,
+    // 460 and 1750; but 2080 rows, 4096 -> 4095: 38 and 64, 1024 -> 1001 9 and 23; 600 rows, 4096 -> 31999: 115 and
+    // 112, 4096 -> 2 x 14335: 91 and 105).
     const int32_t cols = ep.act == kActSwiglu ? 64 : 128;
-    const int64_t small = static_cast<int64_t>((M + cols - 1) / cols) * ((rows + 127) / 128);
+    const int64_t w_tiles = (M + cols - 1) / cols, small = w_tiles * ((rows + 127) / 128);
     const bool mid = rows <= kLinearMidRows || (2 * small <= sms && static_cast<int64_t>(K) * (fp8 ? 1 : 2) >= 1024);
     if (!mid) {
         const int32_t pairs = linear_pair_workers(sms);
         if (pairs > 0 && launch_linear_tiles(fp8, ep, w, ldw, M, K, x, ldx, rows, bias, y, ldy, y_bf16, status, pairs, st, &e)) return e;
     }
-    if (mid || !ws || (!fp8 && !y_bf16 && K > 4096))  // (the stream has no parts for long sums)
+    const bool stream = ws && w_tiles > sms && rows > 1024 && (fp8 || y_bf16 || K <= 4096);  // (it has no parts for long sums)
+    if (!stream)
         return launch_linear_mid(fp8, ep, w, ldw, M, K, x, ldx, rows, bias, y, ldy, y_bf16, status, sms, st, &e) ? e : cudaErrorInvalidValue;
     LinearPlan p;
     if (!plan_linear(&p, fp8, ep, w, ldw, M, K, x, ldx, rows, bias, y, ldy, y_bf16,

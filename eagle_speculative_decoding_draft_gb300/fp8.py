@@ -135,8 +135,8 @@ def rms_norm(x, weight, eps: float = 1e-6, residual=None, dtype=torch.bfloat16, 
 
 
 def linear_workspace(w, rows: int, stream=None):
-    """Scratch for ``linear`` calls of up to `rows` rows on w's device, one call at a time: what makes those
-    of more than 128 rows quicker whose ``out`` has rows that are not multiples of 16 bytes."""
+    """Scratch for ``linear`` calls of up to `rows` rows on w's device, one call at a time: what makes large
+    ones (over 1024 rows, some 20000 outputs) quicker whose ``out`` has rows that are not multiples of 16 bytes."""
     index = _device(w, "w")
     away = _elsewhere(index, stream)
     if away is not None:

@@ -718,10 +718,11 @@ EAGLE_API eagle_status eagle_rms_norm(const void *d_x, int64_t ldx, const void *
  * Sums and the epilogue are fp32; y rounds once.  rows in [0, 32768] per call (0 does nothing); out_features
  * and in_features at most 2^28.
  * d_ws: NULL, or eagle_linear_epilogue_workspace_bytes(rows) bytes (on the current device), 256-byte aligned,
- * with which products of more than 128 rows whose y (or bf16 y's residual) is not 16-byte aligned, or has rows
- * no multiple of 16 bytes apart, are quicker; others do not use it.  Its first 4096 bytes are zeroed once; every
- * call leaves them zero, for later calls of any sizes that the workspace is large enough for.  Calls that may
- * run at the same time need workspaces of their own.  d_status: an int32 of the caller's that latches a wait
+ * with which large products (more than 1024 rows, and outputs for more tiles of 128, gated of 64, than the device
+ * has SMs) whose y (or bf16 y's residual) is not 16-byte aligned, or has rows no multiple of 16 bytes apart, are
+ * quicker; others do not use it.  Its first 4096 bytes are zeroed once; every call leaves them zero, for later
+ * calls of any sizes that the workspace is large enough for.  Calls that may run at the same time need
+ * workspaces of their own.  d_status: an int32 of the caller's that latches a wait
  * that ran out (bit 0), or NULL; after one, y is undefined and the 4096 bytes have to be zeroed again.
  * Results are the same in every call with the same sizes, alignments and presence of d_ws.
  * Errors: INVALID_ARG, CUDA; UNSUPPORTED where a row stride or size passes what a tensor map holds.

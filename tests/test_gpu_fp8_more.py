@@ -96,3 +96,29 @@ def test_long_sums_of_many_rows(gb, rows, M, K, kind):
         pytest.skip("rows are quantised up to 32768 columns")
     check_loss(gb, rows, M, K, kind, most=(K / 16 if K <= 4096 else 256 if K <= 8192 else 128) * 2 / 3 * 2 ** -24.5 + 3 * 2 ** -24
                if kind is BF16 else 1e-10 * K + 2 ** -23)
+
+
+@pytest.mark.parametrize("kind", [BF16, E4M3], ids=["bf16", "e4m3"])
+def test_large_products_with_a_workspace(gb, kind):
+    """Over 1024 rows and more tiles of outputs than SMs, in rows that no bulk store takes: whole and cut tiles,
+    one CTA and pairs, an odd number of tiles; the workspace of any content but for its first bytes, which are
+    zero again behind every call, and the rest of the outputs' memory as it was."""
+    ws = gb.linear_workspace(torch.empty(1, 1, device="cuda"), 2080)
+    ws[4096:] = 0xff
+    for i, (rows, M, K, act, residual) in enumerate([(1025, 19999, 256, None, True), (1100, 20001, 520, "silu", False), (2080, 9801, 640, "swiglu", False),
+                                                     (1300, 39999, 128, "gelu", False), (1536, 19841, 4096, None, False)] * 2):
+        w, x, b, r, w_scale, x_scale = operands(gen(rows + M), rows, M, K, kind, act, i % 2 == 0, residual, gb)
+        dtype = (BF16, F32)[(i // 5) % 2]
+        room = torch.full((rows, M + 2 - M % 2 + 1), -7.0, device="cuda").to(dtype)
+        out = room[:, 1:M + 1]
+        y, tol = ref.linear(w, x, b, act, r, w_scale, x_scale, dtype)
+        kw = dict(bias=b, act=act, residual=r, w_scale=w_scale, x_scale=x_scale, workspace=ws, out=out)
+        gb.linear(w, x, **kw)
+        assert ((out.double() - y).abs() <= tol).all(), (rows, M, K)
+        assert not ws[:4096].any()
+        first = out.clone()
+        gb.linear(w, x, **kw)
+        assert torch.equal(first, out)
+        out.fill_(-7.0)
+        assert (room == -7.0).all()
+        del y, tol, room, out, first
