@@ -67,8 +67,11 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
                      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// kBlocks blocks of 8 rows of x.
-template <bool kFp8, bool kGated, int kBlocks, int kWarps>
+// kBlocks blocks of 8 rows of x.  kLong (bf16 operands, fp32 out, more than kSegment products a warp): mma.sync truncates
+// what it adds up, as tcgen05 does (3.8e-6 of 14336 products over 4 warps, norm-wise; 1.1e-5 of 40000), so the sums
+// go to the warp's place in shared memory every kSegment products and are added there, rounded to nearest (1.0e-6).
+constexpr int kSegment = 1024;
+template <bool kFp8, bool kGated, int kBlocks, int kWarps, bool kLong = false>
 __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) linear_few_kernel(const FewArgs a) {
     constexpr int kThreads = 32 * kWarps, kSize = kFp8 ? 1 : 2;
     constexpr int kOut = kGated ? kRows / 2 : kRows;  // the instruction's rows 0-7 and 8-15: gates and their ups
@@ -111,14 +114,29 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) linear_few_kernel(co
                     mma<kFp8>(acc[b], u.z, v.z, u.w, v.w, y.z, y.w);
                 }
     };
+    bool some = false;
+    auto put = [&] {  // every thread has places of its own
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float &s = sums[warp][g + 8 * (i >> 1)][8 * b + 2 * t + (i & 1)];
+                s = kLong && some ? s + acc[b][i] : acc[b][i];
+                if (kLong) acc[b][i] = 0.0f;
+            }
+        some = true;
+    };
     int32_t at = warp * 128;
-    for (; at + (kAhead - 1) * kWarps * 128 + 128 <= a.k_bytes; at += kAhead * kWarps * 128)
+    [[maybe_unused]] int32_t held = 0;  // products a row that acc has
+    for (; at + (kAhead - 1) * kWarps * 128 + 128 <= a.k_bytes; at += kAhead * kWarps * 128) {
         pieces(at, std::integral_constant<int, kAhead>{}, std::false_type{});
+        if (kLong && (held += kAhead * 128 / kSize) >= kSegment) {
+            put();
+            held = 0;
+        }
+    }
     for (; at < a.k_bytes; at += kWarps * 128) pieces(at, std::integral_constant<int, 1>{}, std::true_type{});
-#pragma unroll
-    for (int b = 0; b < kBlocks; ++b)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) sums[warp][g + 8 * (i >> 1)][8 * b + 2 * t + (i & 1)] = acc[b][i];
+    put();
     __syncthreads();
     for (int32_t i = threadIdx.x; i < kOut * 8 * kBlocks; i += kThreads) {
         const int32_t m = i % kOut, n = i / kOut, o = o0 + m;
@@ -160,12 +178,18 @@ cudaError_t launch_linear_few(bool fp8, const LinearEpilogue &ep, const void *w,
         return wide ? launch_pdl(eight, grid, dim3(256), 0, st, a) : launch_pdl(four, grid, dim3(128), 0, st, a);
     };
 #define FEW(F, G, N) go(linear_few_kernel<F, G, N, 8>, linear_few_kernel<F, G, N, 4>)
+#define LONG(G, N) go(linear_few_kernel<false, G, N, 8, true>, linear_few_kernel<false, G, N, 4, true>)
     if (fp8) {
         if (gated) return two ? FEW(true, true, 2) : FEW(true, true, 1);
         return two ? FEW(true, false, 2) : FEW(true, false, 1);
     }
+    if (!out_bf16 && K > (wide ? 8 : 4) * kSegment) {
+        if (gated) return two ? LONG(true, 2) : LONG(true, 1);
+        return two ? LONG(false, 2) : LONG(false, 1);
+    }
     if (gated) return two ? FEW(false, true, 2) : FEW(false, true, 1);
     return two ? FEW(false, false, 2) : FEW(false, false, 1);
+#undef LONG
 #undef FEW
 }
 

@@ -122,3 +122,17 @@ def test_large_products_with_a_workspace(gb, kind):
         out.fill_(-7.0)
         assert (room == -7.0).all()
         del y, tol, room, out, first
+
+
+@pytest.mark.parametrize("rows,M,K", [(1, 1300, 14336), (16, 20000, 14336), (8, 20000, 40000), (9, 1300, 40000), (3, 8192, 4100), (16, 512, 28672), (5, 33000, 28673)])
+@pytest.mark.parametrize("kind", [BF16, E4M3], ids=["bf16", "e4m3"])
+def test_long_sums_of_few_rows(gb, rows, M, K, kind):
+    """A warp's products, an eighth or a quarter of K, in segments where they are more than one."""
+    if kind is E4M3 and K > 32768:
+        pytest.skip("rows are quantised up to 32768 columns")
+    check_loss(gb, rows, M, K, kind)
+    if kind is BF16:  # with an epilogue, gates and their ups
+        w, x, b, r, _, _ = operands(gen(M), rows, M, K, kind, "swiglu", True, True, gb)
+        y, tol = ref.linear(w, x, b, "swiglu", r, None, None, F32)
+        got = gb.linear(w, x, bias=b, act="swiglu", residual=r, dtype=F32)
+        assert ((got.double() - y).abs() <= tol).all() and float((got.double() - y).norm() / y.norm()) <= 4 * LOSS[kind]
