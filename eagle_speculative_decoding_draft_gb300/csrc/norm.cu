@@ -154,7 +154,8 @@ __global__ void __launch_bounds__(max_threads<V>()) norm_kernel(const RowArgs a)
     }
     const float r = rsqrtf(ss / static_cast<float>(a.n) + a.eps);
     if constexpr (kFp8) {
-        const float s = row_scale(__uint_as_float(top) * r), f = r * __frcp_rn(s);
+        // two factors: with an eps near 0, r / s passes fp32 where the row is nothing and s its least value
+        const float s = row_scale(__uint_as_float(top) * r), inv = __frcp_rn(s);
         if (t == 0) a.scale[row] = s;
         uint8_t *y = static_cast<uint8_t *>(a.y) + row * a.ldy;
 #pragma unroll
@@ -163,7 +164,7 @@ __global__ void __launch_bounds__(max_threads<V>()) norm_kernel(const RowArgs a)
             if (e >= a.n) break;
             uint32_t w[2] = {0, 0};
 #pragma unroll
-            for (int k = 0; k < 8; k += 2) w[k >> 2] |= e4m3_pair(h[i][k] * f, h[i][k + 1] * f) << (8 * (k & 3));
+            for (int k = 0; k < 8; k += 2) w[k >> 2] |= e4m3_pair(h[i][k] * r * inv, h[i][k + 1] * r * inv) << (8 * (k & 3));
             store_codes(y, e, a.n, w);
         }
     } else {

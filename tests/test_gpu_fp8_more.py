@@ -136,3 +136,23 @@ def test_long_sums_of_few_rows(gb, rows, M, K, kind):
         y, tol = ref.linear(w, x, b, "swiglu", r, None, None, F32)
         got = gb.linear(w, x, bias=b, act="swiglu", residual=r, dtype=F32)
         assert ((got.double() - y).abs() <= tol).all() and float((got.double() - y).norm() / y.norm()) <= 4 * LOSS[kind]
+
+
+@pytest.mark.parametrize("eps", [1.4e-17, 1e-20, 1e-30, 1e-38, 1e-44])
+@pytest.mark.parametrize("rows,cols", [(3, 64), (600, 4096)])
+def test_norm_with_an_eps_near_nothing(gb, rows, cols, eps):
+    """A row of zeros, or of weights of 0, is 0; tiny rows are what the formula says."""
+    g = gen(cols)
+    x = wide(g, rows, cols, cols)
+    x[0] = 0
+    x[1] *= 2.0 ** -100
+    w = (1 + 0.3 * torch.randn(cols, generator=g, device="cuda")).to(BF16)
+    codes, scale, _ = gb.rms_norm(x, w, eps, dtype=E4M3)
+    y, _ = ref.norm(x, w, float(torch.tensor(eps, dtype=F32)))
+    # rows of 2^-100: their squares vanish in fp32, mean(h^2) of 2^-200 beside any eps but these matters nothing
+    assert (codes[0].float() == 0).all() and float(scale[0]) == ref.LEAST
+    assert torch.isfinite(scale).all() and torch.isfinite(codes.float()).all()
+    ref.check_rows8(codes[2:], scale[2:], y[2:], 40 * 2.0 ** -24)
+    ref.check_rows8(codes[1:2], scale[1:2], y[1:2], 2.0 ** -20)
+    codes, scale, _ = gb.rms_norm(x, torch.zeros_like(w), eps, dtype=E4M3)
+    assert (codes.float() == 0).all() and (scale == ref.LEAST).all()
