@@ -76,6 +76,18 @@ __device__ __forceinline__ float row_scale(float amax) {
 __device__ __forceinline__ uint32_t e4m3_pair(float x, float y) {
     return __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3);
 }
+// The codes of two values: their quotients by the scale, to the nearest fp32 value, then to the nearest code.  A
+// quotient is a product with the reciprocal, corrected once (P. Markstein, IBM J. Res. Dev. 34, 1990), two at a
+// time: bf16 values over a bf16 maximum often lie on a tie between two codes, where the last bit decides.
+struct Quotient {
+    uint64_t inv2, minus2;
+    __device__ __forceinline__ Quotient(float s, float inv) : inv2(pack_2(inv, inv)), minus2(pack_2(-s, -s)) {}
+    __device__ __forceinline__ uint32_t codes(uint64_t v) const {
+        const uint64_t q = mul_2(v, inv2);
+        const float2 c = unpack_2(fma_2(fma_2(q, minus2, v), inv2, q));
+        return e4m3_pair(c.x, c.y);
+    }
+};
 // Codes e .. e + 7 of a row of n.
 __device__ __forceinline__ void store_codes(uint8_t *y, int32_t e, int32_t n, const uint32_t (&w)[2]) {
     if (e + 8 <= n) {
@@ -157,6 +169,8 @@ __global__ void __launch_bounds__(max_threads<V>()) norm_kernel(const RowArgs a)
         // two factors: with an eps near 0, r / s passes fp32 where the row is nothing and s its least value
         const float s = row_scale(__uint_as_float(top) * r), inv = __frcp_rn(s);
         if (t == 0) a.scale[row] = s;
+        const uint64_t r2 = pack_2(r, r);
+        const Quotient by(s, inv);
         uint8_t *y = static_cast<uint8_t *>(a.y) + row * a.ldy;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
@@ -164,7 +178,7 @@ __global__ void __launch_bounds__(max_threads<V>()) norm_kernel(const RowArgs a)
             if (e >= a.n) break;
             uint32_t w[2] = {0, 0};
 #pragma unroll
-            for (int k = 0; k < 8; k += 2) w[k >> 2] |= e4m3_pair(h[i][k] * r * inv, h[i][k + 1] * r * inv) << (8 * (k & 3));
+            for (int k = 0; k < 8; k += 2) w[k >> 2] |= by.codes(mul_2(pack_2(h[i][k], h[i][k + 1]), r2)) << (8 * (k & 3));
             store_codes(y, e, a.n, w);
         }
     } else {
@@ -181,9 +195,7 @@ __global__ void __launch_bounds__(max_threads<V>()) norm_kernel(const RowArgs a)
 }
 
 // Rows as they are, by the same threads.  The magnitudes of bf16 values rank as whole numbers do, two to a
-// word.  The quotient by the scale is a product with its reciprocal, corrected once to the nearest fp32 value
-// (P. Markstein, IBM J. Res. Dev. 34, 1990), two at a time: bf16 values over a bf16 maximum often lie on a tie
-// between two codes, where the last bit decides.
+// word.
 template <int V>
 __global__ void __launch_bounds__(max_threads<V>()) quantize_kernel(const RowArgs a) {
     __shared__ uint32_t s_max[32];
@@ -208,9 +220,9 @@ __global__ void __launch_bounds__(max_threads<V>()) quantize_kernel(const RowArg
         __syncthreads();
         top = __reduce_max_sync(kFull, (t & 31) < (T >> 5) ? s_max[t & 31] : 0u);
     }
-    const float s = row_scale(__uint_as_float(top)), inv = __frcp_rn(s);
+    const float s = row_scale(__uint_as_float(top));
     if (t == 0) a.scale[row] = s;
-    const uint64_t inv2 = pack_2(inv, inv), minus2 = pack_2(-s, -s);
+    const Quotient by(s, __frcp_rn(s));
     uint8_t *y = static_cast<uint8_t *>(a.y) + row * a.ldy;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -219,11 +231,7 @@ __global__ void __launch_bounds__(max_threads<V>()) quantize_kernel(const RowArg
         const uint32_t w[4] = {xq[i].x, xq[i].y, xq[i].z, xq[i].w};
         uint32_t c[2] = {0, 0};
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const uint64_t v = pack_2(w[k] << 16, w[k] & 0xffff0000u), q = mul_2(v, inv2);
-            const float2 code = unpack_2(fma_2(fma_2(q, minus2, v), inv2, q));
-            c[k >> 1] |= e4m3_pair(code.x, code.y) << (16 * (k & 1));
-        }
+        for (int k = 0; k < 4; ++k) c[k >> 1] |= by.codes(pack_2(w[k] << 16, w[k] & 0xffff0000u)) << (16 * (k & 1));
         store_codes(y, e, a.n, c);
     }
 }

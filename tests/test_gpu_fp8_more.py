@@ -156,3 +156,16 @@ def test_norm_with_an_eps_near_nothing(gb, rows, cols, eps):
     ref.check_rows8(codes[1:2], scale[1:2], y[1:2], 2.0 ** -20)
     codes, scale, _ = gb.rms_norm(x, torch.zeros_like(w), eps, dtype=E4M3)
     assert (codes.float() == 0).all() and (scale == ref.LEAST).all()
+
+
+@pytest.mark.parametrize("rows,cols", [(40, 64), (5, 1000), (600, 4096), (2, 16384), (1, 32768)])
+def test_norm_gives_the_codes_of_quantize_rows(gb, rows, cols):
+    """Rows of 1 and -1 have the norm 1, and so y = w h exactly: the codes and scales are those that
+    quantize_rows gives y, ties of bf16 values over a bf16 maximum among them."""
+    g = gen(cols)
+    x = (torch.randint(0, 2, (rows, cols), generator=g, device="cuda") * 2 - 1).to(BF16)
+    for seed in range(6):
+        w = (1 + 0.3 * torch.randn(cols, generator=gen(seed), device="cuda")).to(BF16)
+        codes, scale, _ = gb.rms_norm(x, w, 0.0, dtype=E4M3)
+        want, want_scale = gb.quantize_rows(x * w)
+        assert torch.equal(scale, want_scale) and torch.equal(codes.view(torch.uint8), want.view(torch.uint8))
