@@ -14,7 +14,7 @@ def __getattr__(name):
     if name == "KV4Cache":
         from . import kv4
         return kv4.KV4Cache
-    if name in ("rms_norm", "quantize_rows", "linear", "linear_workspace", "DecoderLayerFP8"):
+    if name in ("rms_norm", "quantize_rows", "linear", "linear_workspace", "linear_status", "DecoderLayerFP8"):
         from . import fp8
         return globals().setdefault(name, getattr(fp8, name))
     raise AttributeError(name)

@@ -133,6 +133,8 @@ _SIGS = {
                                c_void_p, c_int64, c_int, c_void_p, c_int64, c_void_p, c_void_p]),
     "eagle_linear_epilogue_workspace_bytes": (c_size_t, [c_int32]),
     "eagle_linear": (c_int, [POINTER(LinearArgs), c_void_p, c_size_t, c_void_p, c_void_p]),
+    "eagle_linear_status": (c_int, [c_void_p]),
+    "eagle_linear_status_word": (c_void_p, []),
     "eagle_decoder_layer_fp8_kv4_workspace_bytes": (c_size_t, [POINTER(DecoderLayerFP8Weights), POINTER(KV4CacheStruct),
                                                                c_int32, c_int32]),
     "eagle_decoder_layer_fp8_kv4": (c_int, [POINTER(DecoderLayerFP8Weights), POINTER(KV4CacheStruct), c_int32, c_int32]

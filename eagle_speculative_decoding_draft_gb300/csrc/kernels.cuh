@@ -144,7 +144,8 @@ bool plan_linear(LinearPlan *plan, bool fp8, const LinearEpilogue &ep, const voi
 // linear.cu: the kernels of forms 1 .. 4.
 struct LinearArgs;
 cudaError_t launch_linear_form(const LinearPlan &plan, const LinearArgs &args, cudaStream_t st);
-cudaError_t prepare_linear_forms();
+// On the current device, once; *status_word: the device's own, for calls without one.
+cudaError_t prepare_linear_forms(int32_t **status_word);
 // Their workspace: tickets (one a worker of the split, zero before and after), then partial sums.
 constexpr size_t kLinearTicketBytes = 4096;
 int32_t linear_sms();

@@ -11,6 +11,9 @@
 namespace eagle {
 namespace {
 
+// Latches the waits that run out in calls without a status word of the caller's.
+__device__ int32_t g_status;
+
 template <class Op>
 cudaError_t prepare_form() {
     cudaError_t e = cudaFuncSetAttribute(linear_tc_kernel<0, Op>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -34,15 +37,16 @@ size_t linear_workspace(int32_t rows, int32_t sms) {
     return kLinearTicketBytes + linear_partials_bytes(sms, linear_n_tile(rows < kLinearMaxRows ? rows : kLinearMaxRows));
 }
 
-cudaError_t prepare_linear_forms() {
+cudaError_t prepare_linear_forms(int32_t **status_word) {
     static std::mutex mu;
-    static bool done[64] = {};
+    static int32_t *words[64] = {};  // null: not prepared yet
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     std::lock_guard<std::mutex> lock(mu);
-    if (done[dev]) return cudaSuccess;
+    *status_word = words[dev];
+    if (*status_word) return cudaSuccess;
     e = prepare_kernels();
     if (e == cudaSuccess) e = prepare_form<EpilogueOp<false, false>>();
     if (e == cudaSuccess) e = prepare_form<EpilogueOp<true, false>>();
@@ -50,7 +54,9 @@ cudaError_t prepare_linear_forms() {
     if (e == cudaSuccess) e = prepare_form<EpilogueOp<true, true>>();
     if (e == cudaSuccess) e = prepare_linear_mid();
     if (e == cudaSuccess) e = prepare_linear_tiles();
-    done[dev] = e == cudaSuccess;
+    void *word = nullptr;
+    if (e == cudaSuccess) e = cudaGetSymbolAddress(&word, g_status);
+    if (e == cudaSuccess) *status_word = words[dev] = static_cast<int32_t *>(word);
     return e;
 }
 
@@ -68,8 +74,10 @@ cudaError_t launch_linear(bool fp8, const LinearEpilogue &ep, const void *w, int
                           int64_t ldx, int32_t rows, const void *bias, void *y, int64_t ldy, bool y_bf16, void *ws, int32_t *status,
                           int32_t sms, cudaStream_t st) {
     if (rows <= kLinearFewRows) return launch_linear_few(fp8, ep, w, ldw, M, K, x, ldx, rows, bias, y, ldy, y_bf16, sms, st);
-    cudaError_t e = prepare_linear_forms();
+    int32_t *own = nullptr;
+    cudaError_t e = prepare_linear_forms(&own);
     if (e != cudaSuccess) return e;
+    if (!status) status = own;
     // Over 128 rows the tensor cores bound the product, or nearly so: whole tiles of both operands (256 rows,
     // 4096 -> 2 x 11008 in 8 bits: 30 us, and 43 with the weights past 128 rows at a time; 128 rows: 29 and 22).  But
     // where tiles of 128 rows of either leave room for four parts of K each, those are quicker still (256 rows, 4096
@@ -138,6 +146,25 @@ eagle_status eagle_linear(const eagle_linear_args *l, void *d_ws, size_t ws_byte
                                         l->y_dtype == EAGLE_BF16, d_ws, d_status, sms, reinterpret_cast<cudaStream_t>(stream));
     // a row stride or a size that a tensor map does not hold
     return e == cudaSuccess ? EAGLE_OK : (e == cudaErrorInvalidValue ? EAGLE_ERR_UNSUPPORTED : EAGLE_ERR_CUDA);
+}
+
+int32_t *eagle_linear_status_word(void) {
+    int32_t *word = nullptr;
+    return eagle::prepare_linear_forms(&word) == cudaSuccess ? word : nullptr;
+}
+
+eagle_status eagle_linear_status(eagle_stream_t stream) {
+    int32_t *d_word = eagle_linear_status_word();
+    if (!d_word) return EAGLE_ERR_CUDA;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    int32_t word = 0;
+    if (cudaMemcpyAsync(&word, d_word, sizeof(int32_t), cudaMemcpyDeviceToHost, st) != cudaSuccess ||
+        cudaStreamSynchronize(st) != cudaSuccess)
+        return EAGLE_ERR_CUDA;
+    if (word == 0) return EAGLE_OK;
+    if (cudaMemsetAsync(d_word, 0, sizeof(int32_t), st) != cudaSuccess || cudaStreamSynchronize(st) != cudaSuccess)
+        return EAGLE_ERR_CUDA;
+    return (word & eagle::kDevTimeout) ? EAGLE_ERR_DEVICE_TIMEOUT : EAGLE_ERR_DEVICE_BOUNDS;
 }
 
 }  // extern "C"

@@ -7,6 +7,7 @@ activation and residual on the accumulator.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 
 import torch
@@ -18,6 +19,7 @@ from .engine import _need
 _BF16, _E4M3, _F32, _U8 = torch.bfloat16, torch.float8_e4m3fn, torch.float32, torch.uint8
 _ACTS = {None: 0, "none": 0, "silu": 1, "gelu": 2, "swiglu": 3}
 _CODES = {torch.bfloat16: EAGLE_BF16, torch.float8_e4m3fn: EAGLE_E4M3, torch.float32: EAGLE_F32}
+_AS_IS = contextlib.nullcontext()
 _TICKETS = 4096  # bytes at the start of a workspace that are zero between calls
 
 
@@ -156,7 +158,8 @@ def linear(w, x, bias=None, act=None, residual=None, w_scale=None, x_scale=None,
     8-bit rows (float8_e4m3fn) with w_scale [features] and x_scale [rows] fp32; bias [features] bf16; act None,
     "silu", "gelu" or "swiglu" (w: gate rows, then as many up rows; y = silu(gate) up); residual [rows][out]
     bf16.  Returns y [rows][out] of dtype (bf16 or fp32), or fills out, which may be the residual.  workspace:
-    one of ``linear_workspace``, or None; calls that may overlap need one each."""
+    one of ``linear_workspace``, or None; calls that may overlap need one each.  ``linear_status`` raises what a
+    call could not do on the device."""
     code = _ACTS.get(act)
     if stream is None and code is not None:
         to = dtype if out is None else out.dtype
@@ -217,6 +220,28 @@ def linear(w, x, bias=None, act=None, residual=None, w_scale=None, x_scale=None,
                            p_bias, p_res, ldr, out.data_ptr(), ldy)
     check(_lib.load().eagle_linear(ctypes.byref(args), p_work, nbytes, None, _stream(index)), "eagle_linear")
     return out
+
+
+def linear_status(device=None, workspace=None, stream=None):
+    """Waits for `stream` (default: the current one) of `device` (default: the current one, or the stream's), raises
+    the first error that ``linear`` calls there have latched since the last call (a wait that ran out: the outputs
+    of calls since then are undefined) and clears it.  workspace: one that such calls used; with an error it is
+    made fit for use again."""
+    if workspace is not None and workspace.dtype is not _U8:
+        raise ValueError("workspace must be one of linear_workspace")
+    if device is None:
+        place = stream if stream is not None else workspace
+        index = torch.cuda.current_device() if place is None else place.device.index
+    else:
+        index = torch.device("cuda", device).index if isinstance(device, int) else torch.device(device).index
+        index = torch.cuda.current_device() if index is None else index
+    if workspace is not None and workspace.get_device() != index:
+        raise ValueError(f"workspace is on {workspace.device}, not on cuda:{index}")
+    with _elsewhere(index, stream) or _AS_IS:
+        code = _lib.load().eagle_linear_status(_stream(index))
+        if code != 0 and workspace is not None:
+            workspace[:_TICKETS].zero_()
+    check(code, "linear_status")
 
 
 class DecoderLayerFP8:

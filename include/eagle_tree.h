@@ -722,8 +722,9 @@ EAGLE_API eagle_status eagle_rms_norm(const void *d_x, int64_t ldx, const void *
  * has SMs) whose y (or bf16 y's residual) is not 16-byte aligned, or has rows no multiple of 16 bytes apart, are
  * quicker; others do not use it.  Its first 4096 bytes are zeroed once; every call leaves them zero, for later
  * calls of any sizes that the workspace is large enough for.  Calls that may run at the same time need
- * workspaces of their own.  d_status: an int32 of the caller's that latches a wait
- * that ran out (bit 0), or NULL; after one, y is undefined and the 4096 bytes have to be zeroed again.
+ * workspaces of their own.
+ * d_status: an int32 of the caller's that latches a wait that ran out (bit 0); NULL: the device's own word does,
+ * which eagle_linear_status reads.  After one, y is undefined and the 4096 bytes have to be zeroed again.
  * Results are the same in every call with the same sizes, alignments and presence of d_ws.
  * Errors: INVALID_ARG, CUDA; UNSUPPORTED where a row stride or size passes what a tensor map holds.
  */
@@ -743,6 +744,15 @@ typedef struct {
 EAGLE_API size_t eagle_linear_epilogue_workspace_bytes(int32_t rows);
 EAGLE_API eagle_status eagle_linear(const eagle_linear_args *args, void *d_ws, size_t ws_bytes, int32_t *d_status,
                                     eagle_stream_t stream);
+
+/*
+ * Waits for the stream and returns the first device error that calls without a d_status (eagle_linear's, and the
+ * products of the layer below) have latched on the current device since the last call, from whatever stream:
+ * DEVICE_TIMEOUT, or OK; it is then cleared.  eagle_linear_status_word: the address of that word, for callers that
+ * read it in their own way, or NULL where there is no device.
+ */
+EAGLE_API eagle_status eagle_linear_status(eagle_stream_t stream);
+EAGLE_API int32_t *eagle_linear_status_word(void);
 
 /*
  * The draft decoder layer in 8 bits over a 4-bit cache: eagle_decoder_layer_kv4 with every projection a

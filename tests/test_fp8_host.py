@@ -120,3 +120,11 @@ def test_fp8_layer_edges(lib):
     assert fp8_layer(lib, batch=0, x=None, out=None, ws=None) == 0
     for bad in (dict(batch=0), dict(nodes=0), dict(hidden=72), dict(batch=11, nodes=3000), dict(cache=dict(head_dim=96))):
         assert fp8_layer(lib, nbytes=None, **bad) == 0
+
+
+def test_status_of_products_without_a_device(lib):
+    """The word is the device's: without one there is none to read."""
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("there is a device")
+    assert not lib.eagle_linear_status_word() and lib.eagle_linear_status(None) == 4

@@ -169,3 +169,37 @@ def test_norm_gives_the_codes_of_quantize_rows(gb, rows, cols):
         codes, scale, _ = gb.rms_norm(x, w, 0.0, dtype=E4M3)
         want, want_scale = gb.quantize_rows(x * w)
         assert torch.equal(scale, want_scale) and torch.equal(codes.view(torch.uint8), want.view(torch.uint8))
+
+
+def test_a_wait_that_ran_out_is_reported(gb):
+    """Calls without a status word latch into the device's own.  Here a stalled attention call does it in their
+    place: no product is made to fail."""
+    from eagle_speculative_decoding_draft_gb300 import KV4Cache, _lib
+    lib = _lib.load()
+    w, x, _, _, ws, xs = operands(gen(1), 300, 256, 512, E4M3, None, False, False, gb)
+    want = gb.linear(w, x, w_scale=ws, x_scale=xs)
+    gb.linear_status()
+    word = lib.eagle_linear_status_word()
+    assert word
+    work = gb.linear_workspace(w, 300)
+    work[:4096] = 3  # tickets that a product given up in the middle has left
+    c = KV4Cache(1, 2, 64, num_pages=4, max_pages=4, page_size=32)
+    g = gen(3)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda").to(BF16)  # noqa: E731
+    c.append(r(1, 100, 2, 64), r(1, 100, 2, 64))
+    q, k, v = r(1, 65, 8, 64), r(1, 65, 2, 64), r(1, 65, 2, 64)
+    out, nbytes = torch.empty_like(q), c.attention_workspace_bytes(65, 8)
+    scratch = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+    assert lib.eagle_test_kv4_stall(c._ref, 1, 65, 8, q.data_ptr(), k.data_ptr(), v.data_ptr(), None, out.data_ptr(), scratch.data_ptr(), nbytes,
+                                    5_000_000, 0, word, torch.cuda.current_stream().cuda_stream) == 0
+    with pytest.raises(_lib.EagleError, match="TIMEOUT"):
+        gb.linear_status(workspace=work)
+    assert not work[:4096].any()
+    side = torch.cuda.Stream()
+    gb.linear_status(stream=side), gb.linear_status(device=0), gb.linear_status(device="cuda", workspace=work)
+    assert torch.equal(gb.linear(w, x, w_scale=ws, x_scale=xs, workspace=work), want)
+    gb.linear_status()
+    with pytest.raises(ValueError):
+        gb.linear_status(workspace=torch.zeros(4, device="cuda"))
+    with pytest.raises(ValueError):
+        gb.linear_status(workspace=torch.zeros(4096, dtype=torch.uint8))
