@@ -246,7 +246,8 @@ def linear_status(device=None, workspace=None, stream=None):
 
 class DecoderLayerFP8:
     """The draft decoder layer in 8 bits over a 4-bit cache (eagle_decoder_layer_fp8_kv4).  Takes the bf16
-    weights of ``DecoderLayer`` and keeps 8-bit rows of the projections': half the bytes."""
+    weights of ``DecoderLayer`` and keeps 8-bit rows of the projections': half the bytes.  They are ready when the
+    constructor returns, for calls on any stream; the layer must live until its calls have ended."""
 
     def __init__(self, w_qkv, w_o, w_norm, w_gu, w_d, heads: int, kv_heads: int, rope_theta: float = 10000.0,
                  rms_eps: float = 1e-6):
@@ -261,6 +262,9 @@ class DecoderLayerFP8:
         if h % 16 or inter % 16:
             raise ValueError("hidden and inter must be multiples of 16")
         rows = [quantize_rows(t) for t in (w_qkv, w_o, w_gu, w_d)]
+        with torch.cuda.device(w_norm.device):
+            if not torch.cuda.is_current_stream_capturing():  # a graph's weights are ready when it has run
+                torch.cuda.current_stream().synchronize()
         self._keep = (rows, w_norm)
         (qkv, s_qkv), (o, s_o), (gu, s_gu), (d, s_d) = ((c.data_ptr(), s.data_ptr()) for c, s in rows)
         self.w = _lib.DecoderLayerFP8Weights(h, heads, kv_heads, D, inter, rope_theta, rms_eps, qkv, o, w_norm.data_ptr(), gu, d,

@@ -148,3 +148,25 @@ def test_refusals_of_the_binding(gb):
             lay.kv4(**{**dict(x=w["x"], cache=c, positions=pos), **kw})
     with pytest.raises(ValueError):
         gb.DecoderLayerFP8(w["w_qkv"], w["w_o"], w["w_norm"], w["w_gu"][:80], w["w_d"][:, :40].contiguous(), heads=4, kv_heads=2)
+
+
+def test_a_new_layer_is_ready_on_any_stream(gb):
+    """Constructed behind a queue of other work and called at once on another stream."""
+    B, n, h, H, Hk, D, I = 2, 9, 256, 4, 2, 64, 512
+    w, want_layer = build(gb, B, n, h, H, Hk, D, I, 20, 3)
+    c = filled(gb, w, B, Hk, D, 20, n, 3)
+    pos = c.lengths[:, None] + torch.arange(n, device="cuda", dtype=torch.int32)
+    want = want_layer.kv4(w["x"], c, pos)
+    names = ("w_qkv", "w_o", "w_norm", "w_gu", "w_d")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        trash = [torch.full((1 << 20,), 0x7f, dtype=torch.uint8, device="cuda") for _ in range(8)]  # what the codes' memory holds
+        del trash
+        torch.cuda._sleep(100_000_000)
+        made = gb.DecoderLayerFP8(*(w[k] for k in names), heads=H, kv_heads=Hk)
+        got = made.kv4(w["x"], c, pos, stream=side)
+        side.synchronize()
+        assert torch.equal(got, want)
+        torch.cuda.synchronize()
+    c.status()
