@@ -893,8 +893,10 @@ cudaError_t launch_form(const LinearPlan &p, const LinearArgs &a, cudaStream_t s
         e = launch_pdl(linear_tc_kernel<0, Op>, dim3(p.grid), dim3(kThreads), p.smem_bytes, st, p.tmap_w, p.tmap_x,
                        p.tmap_y, a);
     if (e != cudaSuccess || !p.defer) return e;
-    return launch_pdl(linear_reduce_kernel<Op>, dim3(p.num_tiles * p.num_chunks, (p.n_tile + kReduceRows - 1) / kReduceRows),
-                      dim3(256), 0, st, a, p.grid >> p.pair);
+    if constexpr (Op::kPlain)
+        return launch_pdl(linear_reduce_kernel<Op>, dim3(p.num_tiles * p.num_chunks, (p.n_tile + kReduceRows - 1) / kReduceRows),
+                          dim3(256), 0, st, a, p.grid >> p.pair);
+    return cudaErrorInvalidValue;  // the other forms come here with more tiles than workers (linear.cu)
 }
 
 }  // namespace

@@ -125,7 +125,7 @@ eagle_status eagle_linear(const eagle_linear_args *l, void *d_ws, size_t ws_byte
     if (l->y_dtype != EAGLE_BF16 && l->y_dtype != EAGLE_F32) return EAGLE_ERR_INVALID_ARG;
     if (l->act < EAGLE_ACT_NONE || l->act > EAGLE_ACT_SWIGLU) return EAGLE_ERR_INVALID_ARG;
     if (l->rows == 0) return EAGLE_OK;
-    const bool fp8 = l->dtype == EAGLE_E4M3, gated = l->act == EAGLE_ACT_SWIGLU;
+    const bool fp8 = l->dtype == EAGLE_E4M3;
     const int32_t M = l->out_features, K = l->in_features, step = fp8 ? 16 : 8;
     if (M > (1 << 28) || K > (1 << 28)) return EAGLE_ERR_INVALID_ARG;
     auto off = [](const void *p, uintptr_t by) { return (reinterpret_cast<uintptr_t>(p) & (by - 1)) != 0; };
