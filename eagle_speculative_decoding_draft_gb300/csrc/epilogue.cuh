@@ -6,7 +6,7 @@
 namespace eagle {
 
 // z / (1 + e^-z) by the special-function unit: within 2^-20 of itself for |z| up to 10, far below a bf16
-// output's 2^-9 and an fp32 output's sum of products.  0 for z far below 0.
+// output's 2^-9 and about what an fp32 output's sum of products loses.  0 for z far below 0.
 __device__ __forceinline__ float silu(float z) { return __fdividef(z, 1.0f + __expf(-z)); }
 __device__ __forceinline__ float activation(int32_t act, float z) {
     if (act == kActSilu) return silu(z);

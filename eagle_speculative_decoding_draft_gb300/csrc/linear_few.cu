@@ -9,7 +9,7 @@
 // not matter as long as it is the same one in w and in x: 16 neighbouring bytes a lane are two instructions'
 // operands.  The warps' sums meet in shared memory, where the epilogue takes them; nothing is cut between
 // blocks.  Bound by the memory: one row, 4096 -> 2 x 14336 in bf16 34 us, 1.0 of the measured copy rate, in
-// 8 bits 19.8 us (0.87); 4096 -> 4096 in 8 bits 3.8 us (0.65: the call's own latency), against 10.6 through the
+// 8 bits 20.2 us (0.86); 4096 -> 4096 in 8 bits 4.4 us (0.56: the call's own latency), against 10.6 through the
 // ring of gemm.cuh.
 #include <type_traits>
 

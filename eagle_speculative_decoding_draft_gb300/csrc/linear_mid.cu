@@ -7,9 +7,9 @@
 // one CTA's beginning and end fall into the other's copies, and the parts' sums meet through the cluster's
 // shared memory, each CTA finishing its share of the rows.  No partial sum goes through memory.  Bound by the
 // memory and, towards 128 rows, by what the SMs take from the L2 (a row of x goes to every tile): 61 rows,
-// 4096 -> 2 x 11008 in 8 bits 18.4 us (0.74 of the measured copy rate; 25.9 through gemm.cuh's stream), 4096 ->
-// 4096 8.4 us (13.8).  Two epilogue warps an accumulator quarter: a warp alone on its scheduler takes twice as
-// long over a share (128 rows, 4096 -> 4096: 13.4 -> 11.5 us).
+// 4096 -> 2 x 11008 in 8 bits 19.8 us (0.68 of the measured copy rate; 25.9 through gemm.cuh's stream), 4096 ->
+// 4096 8.7 us, 9.2 with a residual (13.8).  Two epilogue warps an accumulator quarter: a warp alone on its scheduler
+// takes twice as long over a share (128 rows, 4096 -> 4096: 13.4 -> 11.4 us).
 #include <algorithm>
 #include <type_traits>
 

@@ -17,9 +17,9 @@
 //               through the same swizzled 4 KB of shared memory a warp and 32 x 128 bytes of outputs.
 //
 // Bound by the tensor cores and, over many calls, by the board's power: 2080 rows 4096 -> 2 x 14336 in 8 bits
-// 163 us at first (3.0 PFLOP/s, 80 % of the tensor pipe's cycles; the ninth row tile has 32 rows of 256) and 176
-// call after call; 8192 rows 14336 -> 4096 319 us (3.02 PFLOP/s).  Tiles of 128 columns take 1.75 times as long
-// (the pair's operands then cost the shared memory more than the tensor core's time).
+// 164 us at first (3.0 PFLOP/s, 80 % of the tensor pipe's cycles; the ninth row tile has 32 rows of 256) and 177
+// to 181 call after call; 8192 rows 14336 -> 4096 324 to 328 us (2.9 to 3.0 PFLOP/s).  Tiles of 128 columns take 1.75
+// times as long (the pair's operands then cost the shared memory more than the tensor core's time).
 #include <algorithm>
 #include <mutex>
 
@@ -74,7 +74,10 @@ __device__ __forceinline__ void tile_of(const TileArgs &a, int32_t u, int32_t &r
 // columns.
 // kLong: the tensor core's accumulator truncates, so a long sum of bf16 products is too small by a part that
 // grows with its length (14336 products 1.7e-5, more than an fp32 output should lose): the sums of kSegment
-// k-blocks at a time are added up, rounded to nearest, in the accumulator's other half (2e-6).
+// k-blocks at a time are added up, rounded to nearest, in the accumulator's other half (2.1e-6; up to 4096 products in
+// one go 4.4e-6).  The products wait meanwhile: 2080 rows 14336 -> 4096 in bf16 157 us, 142 with bf16 out.  Segments of
+// half the length lose half as much and cost as much again; the sums in registers do not fit beside 10 warps.
+// 8-bit products, mostly multiples of the accumulator's step, lose 1.0e-6 of 14336 and are left whole.
 constexpr int kSegment = 32;
 template <bool kFp8, bool kGated, bool kSplit, bool kLong>
 __global__ void __launch_bounds__(kThreads, 1)

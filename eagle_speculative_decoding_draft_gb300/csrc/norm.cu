@@ -6,8 +6,9 @@
 //
 // A row is read once and stays in registers.  Its norm is one factor r = 1 / sqrt(...), so the largest |y| is
 // r max |w h|, and one reduction over the row finds the sum of squares and that maximum together.  Bound by the
-// memory: 16382 rows of 8192 with their residual (1.07 GB) in 153 us, 1.03 of the measured copy rate; 2080 rows
-// of 14336 quantised (89 MB) in 15.7 us, 0.84, with the quotients two at a time (one at a time 19.3).
+// memory: 16382 rows of 8192 with their residual (1.07 GB) in 152 us, 1.04 of the measured copy rate; 2080 rows
+// of 14336 quantised (89 MB) in 15.1 us, 0.87, with the quotients two at a time (one at a time 19.3); 512 rows of 4096
+// with their residual to 8 bits 4.1 us (0.53: a launch's beginning and end).
 #include <cuda_fp8.h>
 
 #include "../../include/eagle_tree.h"

@@ -233,8 +233,10 @@ def linear_status(device=None, workspace=None, stream=None):
         place = stream if stream is not None else workspace
         index = torch.cuda.current_device() if place is None else place.device.index
     else:
-        index = torch.device("cuda", device).index if isinstance(device, int) else torch.device(device).index
-        index = torch.cuda.current_device() if index is None else index
+        device = torch.device("cuda", device) if isinstance(device, int) else torch.device(device)
+        if device.type != "cuda":
+            raise ValueError(f"device must be a CUDA device, got {device}")
+        index = torch.cuda.current_device() if device.index is None else device.index
     if workspace is not None and workspace.get_device() != index:
         raise ValueError(f"workspace is on {workspace.device}, not on cuda:{index}")
     with _elsewhere(index, stream) or _AS_IS:

@@ -685,6 +685,8 @@ EAGLE_API eagle_status eagle_decoder_layer_kv4(const eagle_decoder_layer_weights
  * eagle_rms_norm:      h = x + residual (x alone where d_residual is NULL), y = weight h / sqrt(mean(h^2) + eps);
  *                      y in bf16 (d_scale NULL) or as 8-bit rows.  d_sum, where given, receives h in bf16.
  * h, the sum of squares and y stay in fp32 until y and the sum are rounded once; the norm takes h before that.
+ * (Squares that fp32 does not hold: rows of some 2^64 and more come out as 0; with eps 0 rows of nothing as NaN, rows
+ * under some 2^-75 as infinities.)
  *   d_x, d_residual, d_sum, d_y   [rows], ldx, ldr, lds, ldy elements apart (a multiple of 8; of 16 for 8-bit
  *                      rows, which eagle_linear then takes), 16-byte aligned; what lies between the rows is
  *                      neither read nor written.  d_sum may be d_x or d_residual, and a bf16 d_y too, with
