@@ -203,3 +203,26 @@ def test_a_wait_that_ran_out_is_reported(gb):
         gb.linear_status(workspace=torch.zeros(4, device="cuda"))
     with pytest.raises(ValueError):
         gb.linear_status(workspace=torch.zeros(4096, dtype=torch.uint8))
+
+
+@pytest.mark.parametrize("rows", [1, 61, 300, 2080])
+def test_the_first_call_of_a_process_may_be_captured(gb, rows):
+    """What a call prepares once a device (attributes, occupancy, its status word) is allowed in a capture."""
+    import subprocess
+    import sys
+    from pathlib import Path
+    code = f"""
+import torch
+import eagle_speculative_decoding_draft_gb300 as gb
+w, x = torch.randn(700, 512, device="cuda").bfloat16(), torch.randn({rows}, 512, device="cuda").bfloat16()
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    y = gb.linear(w, x, dtype=torch.float32)
+graph.replay()
+gb.linear_status()
+want = x.double() @ w.double().T
+assert (y.double() - want).norm() <= 1e-5 * want.norm()
+"""
+    done = subprocess.run([sys.executable, "-c", code], cwd=Path(__file__).resolve().parent.parent, capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0, done.stderr[-2000:]
